@@ -322,7 +322,8 @@ int32_t aq_decode_max_m(void);
  * aq_path value other than AQ_PATH_AUTO; 0 if none). */
 int32_t aq_last_path(void);
 
-/* Number of kernel launches the last successful aq_* call on this thread enqueued. */
+/* Number of kernel launches the last successful linear, MLP or precompute call on this thread
+ * enqueued. */
 int32_t aq_last_launch_count(void);
 
 /* ---------------------------------------------------------------------------------
@@ -363,6 +364,166 @@ size_t aq_randomized_svd_workspace_bytes(int32_t m, int32_t n, int32_t k, int32_
 aq_status aq_randomized_svd(const double* A, int64_t lda, int32_t m, int32_t n, int32_t r, const double* omega,
                             int64_t ld_omega, int32_t k, int32_t power_iters, void* U, int64_t ld_u, void* V,
                             int64_t ld_v, void* workspace, size_t workspace_bytes, void* stream);
+
+/* ---------------------------------------------------------------------------------
+ * What a decode layer runs between aq_linear_qkv and the o projection, and a model after its
+ * last layer: rotary positions, a paged key/value cache, attention of drafted tokens over that
+ * cache, and the verification of the drafts. The pages have no counterpart: they leave these to
+ * the serving stack. The conventions above hold (device pointers, bf16 activations, explicit
+ * strides in elements, 16-byte alignment, stream order, programmatic dependent launch), and:
+ * - activations are [T, heads, head_dim] with a stride from token to token and one from head to
+ *   head (both multiples of 8): column slices of one stacked [q | k | v] projection output, or
+ *   tensors with heads outermost;
+ * - index arrays live on the device and are not seen by the host. What they name outside its
+ *   range (a slot, a page, a token) is left out, as stated at each: no call reads or writes
+ *   beyond the buffers whose sizes it was given;
+ * - these calls leave aq_last_launch_count() and aq_last_path() alone.
+ * --------------------------------------------------------------------------------- */
+
+/* Rotary positions: the pair (a, b) of a head at position pos turns by the angle pos * f_i,
+ *   (a cos - b sin, b cos + a sin) * magnitude,
+ * for the first rotary_dim elements of a head (a multiple of 16); the rest passes through.
+ *   AQ_ROPE_HALF         pair i is elements i and i + rotary_dim / 2
+ *   AQ_ROPE_INTERLEAVED  pair i is elements 2 i and 2 i + 1
+ * freq: device array [rotary_dim / 2], f_i / (2 pi) as a 64-bit binary fraction of a turn (2^64 is
+ * one turn). The product with the position wraps where the angle does, so the angle is exact at
+ * every 32-bit position. aq_rope_frequencies fills a host array with it. */
+typedef enum aq_rope_layout { AQ_ROPE_HALF = 0, AQ_ROPE_INTERLEAVED = 1 } aq_rope_layout;
+typedef struct aq_rope_spec {
+  const uint64_t* freq;
+  int32_t rotary_dim;
+  int32_t layout;     /* aq_rope_layout */
+  float magnitude;    /* factor on cos and sin; 1 unless the frequencies were scaled that way */
+} aq_rope_spec;
+
+/* f_i = base^(-2 i / rotary_dim), scaled for contexts longer than the trained one:
+ *   AQ_ROPE_SCALE_LINEAR      f / factor
+ *   AQ_ROPE_SCALE_NTK         base * factor^(rotary_dim / (rotary_dim - 2)) in place of base
+ *   AQ_ROPE_SCALE_YARN        pairs that turn more than `fast` times over original_len positions keep
+ *                             f, those below `slow` turns take f / factor, a ramp over the pair index
+ *                             between; magnitude 0.1 ln(factor) + 1
+ *   AQ_ROPE_SCALE_WAVELENGTH  the same two limits, the ramp over the number of turns; magnitude 1
+ * Host function, no device work. freq: host array [rotary_dim / 2]; rotary_dim even, up to 256. */
+typedef enum aq_rope_scale {
+  AQ_ROPE_SCALE_NONE = 0,
+  AQ_ROPE_SCALE_LINEAR = 1,
+  AQ_ROPE_SCALE_NTK = 2,
+  AQ_ROPE_SCALE_YARN = 3,
+  AQ_ROPE_SCALE_WAVELENGTH = 4
+} aq_rope_scale;
+typedef struct aq_rope_scaling {
+  double factor;        /* >= 1 */
+  double original_len;  /* YARN and WAVELENGTH */
+  double fast, slow;    /* YARN and WAVELENGTH, in turns: fast > slow > 0 */
+} aq_rope_scaling;
+aq_status aq_rope_frequencies(int32_t rotary_dim, double base, int32_t scaling, const aq_rope_scaling* params,
+                              uint64_t* freq, float* magnitude);
+
+/* y[t, h] = rotated x[t, h] at position pos[t], each element rounded to bf16 once. inverse != 0
+ * turns the other way: the transpose of the rotation, which is its gradient. y may be x (same
+ * pointer and strides); otherwise they must not overlap. pos: device int32 [T]. head_dim: a
+ * multiple of 16 up to 256. T == 0 is a no-op. */
+aq_status aq_rope(const aq_rope_spec* rope, const int32_t* pos, int64_t T, int32_t heads, int32_t head_dim,
+                  const void* x, int64_t x_tok, int64_t x_head, void* y, int64_t y_tok, int64_t y_head,
+                  int32_t inverse, void* stream);
+
+/* A paged key/value cache of one layer. Token slot n is offset n % page_size of page n / page_size.
+ *   k, v              [pages, kv_heads, page_size, head_dim], bf16 or E4M3 codes
+ *   k_scale, v_scale  [pages, kv_heads, page_size] fp32 with AQ_KV_E4M3 (one scale for each token
+ *                     and head: the value is code * scale), NULL with AQ_KV_BF16
+ * page_size: 16, 32, 64, 128 or 256. head_dim: a multiple of 16 up to 256. Contents need no
+ * initialisation: a token that was never written is read by no one who does not name it. */
+typedef enum aq_kv_type { AQ_KV_BF16 = 0, AQ_KV_E4M3 = 1 } aq_kv_type;
+typedef struct aq_kv_cache {
+  void* k;
+  void* v;
+  float* k_scale;
+  float* v_scale;
+  int32_t pages, page_size, kv_heads, head_dim;
+  int32_t type;  /* aq_kv_type */
+} aq_kv_cache;
+
+/* Writes the keys and values of T tokens into their slots (device int64 [T]; a slot outside the
+ * cache, -1 for one, writes nothing; a slot named twice holds either token). With rope, keys are
+ * rotated at pos[t] on the way; with q and q_out too, the queries are rotated in the same launch
+ * (q_out may be q). E4M3: scale = max(max|x| / 448, 2^-100) over a token's head, taken after the
+ * rotation and before any rounding, code = nearest E4M3 of x / scale, by the reciprocals of 448 and of
+ * the scale; a vector with an infinity or a NaN is stored so that it reads back as NaN. */
+aq_status aq_kv_write(const aq_kv_cache* cache, const int64_t* slots, int64_t T, const void* k, int64_t k_tok,
+                      int64_t k_head, const void* v, int64_t v_tok, int64_t v_head, const aq_rope_spec* rope,
+                      const int32_t* pos, const void* q, int32_t q_heads, int64_t q_tok, int64_t q_head, void* q_out,
+                      int64_t qo_tok, int64_t qo_head, void* stream);
+
+/* Reads T slots back as bf16 (code * scale rounded once); a slot outside the cache reads as zeros.
+ * k or v may be NULL (not both). */
+aq_status aq_kv_read(const aq_kv_cache* cache, const int64_t* slots, int64_t T, void* k, int64_t k_tok, int64_t k_head,
+                     void* v, int64_t v_tok, int64_t v_head, void* stream);
+
+/* Attention of the newest tokens of each sequence over its cache. Sequence b brings the rows
+ * cu_q[b] .. cu_q[b+1]-1 of q, its T_b drafted tokens; their keys and values are already in the cache,
+ * behind the ctx[b] tokens of its context. Key j of a sequence, j < ctx[b] + T_b, lies in the page
+ * page_table[b, j / page_size] at offset j % page_size.
+ *   o[i, h] = sum_j p_j v_j,  p = softmax over the keys j that row i sees of scale * (q[i, h] . k_j)
+ * Query head h reads key/value head h / (q_heads / kv_heads).
+ * Row i sees every context token, and of the drafted ones
+ *   mask given   those j whose bit j % 64 of mask[row, j / 64] is set (its ancestors and itself), the
+ *                rows' positions being ctx[b] + depth[row] (depth NULL: the drafted index itself)
+ *   mask NULL    those with j <= i (a chain; one token is the plain decode step, many a prefill chunk)
+ * window > 0 leaves out keys whose position lies `window` or more before the row's.
+ * A row that sees nothing (or whose scores are all minus infinity) gives zeros and lse = -inf. Masked
+ * keys and values take no part, whatever they hold. Softmax and sums are held in fp32; bf16 weights
+ * with a bf16 cache; with E4M3, queries and weights as two E4M3 terms each (8 bits, and nothing below 2^-18
+ * of the largest of a head's elements or of a tile's weights).
+ *   lse  fp32 [total_q, q_heads], log of the sum of exp(score), or NULL
+ * Left out: keys past pages_per_seq pages, keys in pages outside the cache, rows past max_q of a
+ * sequence or outside [0, total_q). Needs head_dim 64, 128 or 256 (AQ_ERR_UNSUPPORTED otherwise).
+ * workspace: aq_tree_attention_workspace_bytes(...) bytes, 256-byte aligned, no initial contents. */
+typedef struct aq_draft_batch {
+  int32_t batch;
+  int32_t max_q;           /* at least the largest T_b */
+  int64_t total_q;         /* rows of q */
+  const int32_t* cu_q;     /* [batch + 1] */
+  const int32_t* ctx;      /* [batch] */
+  const int32_t* page_table; /* [batch, pages_per_seq], row stride ld_table */
+  int32_t pages_per_seq;
+  int64_t ld_table;
+  const uint64_t* mask;    /* [total_q, ceil(max_q / 64)], row stride ld_mask, or NULL */
+  int64_t ld_mask;
+  const int32_t* depth;    /* [total_q], or NULL; used with mask */
+  int32_t window;          /* 0: none */
+} aq_draft_batch;
+size_t aq_tree_attention_workspace_bytes(const aq_kv_cache* cache, const aq_draft_batch* batch, int32_t q_heads);
+aq_status aq_tree_attention(const aq_kv_cache* cache, const aq_draft_batch* batch, const void* q, int32_t q_heads,
+                            int64_t q_tok, int64_t q_head, float scale, void* o, int64_t o_tok, int64_t o_head,
+                            float* lse, void* workspace, size_t workspace_bytes, void* stream);
+
+/* Verification of drafted tokens against the target's probabilities, from given random numbers.
+ * Sequence b drafted the nodes cu[b] .. cu[b+1]-1 (tokens int32); parent[node] is the index within the
+ * sequence of the node it follows, less than its own, or -1 for the context (parent NULL: a chain). p
+ * holds, for each sequence, one row of probabilities after the context and one after each node: row
+ * cu[b] + b, then cu[b] + b + 1 + i for node i. Walking from the context, with r = p of the row:
+ *   children c in index order: accepted when u[c] * q(x_c) < r(x_c), and the walk moves to c;
+ *   a child refused makes r the normalised max(r - q, 0)
+ * where q is the row (of the same index as r's) that the children were drawn from; q NULL says that
+ * each draft was taken for certain, so that a refused token's r becomes 0. At the end of the walk, the
+ * next token is the v with the largest r(v) / noise[b, v], the lowest of equal ones; where r has no mass
+ * left, r = p. With u uniform in [0, 1) and noise exponential with mean 1, the tokens are distributed as
+ * the target's own.
+ *   p_type     AQ_PROB_F32 or AQ_PROB_BF16, of p and q; rows of `vocab`, row strides ld_p and ld_q; rows:
+ *              number of rows of p and of q
+ *   u [nodes], noise [batch, vocab] (row stride ld_noise): fp32
+ *   n_accepted int32 [batch]; path int32 [batch, path_cap] (row stride ld_path): the accepted nodes' indices
+ *              in order, then -1; the walk ends after path_cap of them; token int32 [batch]
+ * max_nodes: at least the most nodes of a sequence (at most 1024). A node whose token lies outside the
+ * vocabulary, or whose parent or row is out of range, is never accepted. Sums over the vocabulary are taken
+ * in a fixed order. */
+typedef enum aq_prob_type { AQ_PROB_F32 = 0, AQ_PROB_BF16 = 1 } aq_prob_type;
+#define AQ_MAX_DRAFT_NODES 1024
+aq_status aq_verify_drafts(int32_t batch, int32_t vocab, const int32_t* cu, const int32_t* tokens,
+                           const int32_t* parent, int64_t nodes, int32_t max_nodes, const void* p, int64_t ld_p,
+                           const void* q, int64_t ld_q, int64_t rows, int32_t p_type, const float* u,
+                           const float* noise, int64_t ld_noise, int32_t* n_accepted, int32_t* path, int64_t ld_path,
+                           int32_t path_cap, int32_t* token, void* stream);
 
 const char* aq_status_string(aq_status status);
 /* Thread-local description of the last error returned on this thread ("" if none). */

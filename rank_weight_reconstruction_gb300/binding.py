@@ -36,6 +36,18 @@ AQ_SF_LINEAR = 0
 AQ_SF_128X4 = 1
 AQ_NVFP4_SCALE_FROM_AMAX = 0
 AQ_NVFP4_SCALE_GIVEN = 1
+AQ_ROPE_HALF = 0
+AQ_ROPE_INTERLEAVED = 1
+AQ_ROPE_SCALE_NONE = 0
+AQ_ROPE_SCALE_LINEAR = 1
+AQ_ROPE_SCALE_NTK = 2
+AQ_ROPE_SCALE_YARN = 3
+AQ_ROPE_SCALE_WAVELENGTH = 4
+AQ_KV_BF16 = 0
+AQ_KV_E4M3 = 1
+AQ_PROB_F32 = 0
+AQ_PROB_BF16 = 1
+AQ_MAX_DRAFT_NODES = 1024
 
 EXPORTED_SYMBOLS = [
     "aq_linear_workspace_bytes", "aq_linear", "aq_linear_qkv", "aq_precompute",
@@ -45,6 +57,8 @@ EXPORTED_SYMBOLS = [
     "aq_band_mean", "aq_ls_residual", "aq_randomized_svd_workspace_bytes", "aq_randomized_svd",
     "aq_mlp_workspace_bytes", "aq_mlp", "aq_precompute_nvfp4_workspace_bytes", "aq_precompute_nvfp4",
     "aq_selftest_prefill_timeout", "aq_checked_build", "aq_selftest_bounds_check",
+    "aq_rope_frequencies", "aq_rope", "aq_kv_write", "aq_kv_read", "aq_tree_attention_workspace_bytes",
+    "aq_tree_attention", "aq_verify_drafts",
 ]
 AQ_MAX_FAMILIES = 3
 AQ_NOALLOC_WORKSPACE_BYTES = 8 * 1024 * 1024
@@ -65,6 +79,29 @@ class c_theta(ctypes.Structure):
         ("V", ctypes.c_void_p), ("ld_v", ctypes.c_int64),
         ("out", ctypes.c_int32), ("in_", ctypes.c_int32), ("r", ctypes.c_int32),
     ]
+
+
+class c_rope(ctypes.Structure):
+    _fields_ = [("freq", ctypes.c_void_p), ("rotary_dim", ctypes.c_int32), ("layout", ctypes.c_int32),
+                ("magnitude", ctypes.c_float)]
+
+
+class c_rope_scaling(ctypes.Structure):
+    _fields_ = [("factor", ctypes.c_double), ("original_len", ctypes.c_double), ("fast", ctypes.c_double),
+                ("slow", ctypes.c_double)]
+
+
+class c_kv_cache(ctypes.Structure):
+    _fields_ = [("k", ctypes.c_void_p), ("v", ctypes.c_void_p), ("k_scale", ctypes.c_void_p),
+                ("v_scale", ctypes.c_void_p), ("pages", ctypes.c_int32), ("page_size", ctypes.c_int32),
+                ("kv_heads", ctypes.c_int32), ("head_dim", ctypes.c_int32), ("type", ctypes.c_int32)]
+
+
+class c_draft_batch(ctypes.Structure):
+    _fields_ = [("batch", ctypes.c_int32), ("max_q", ctypes.c_int32), ("total_q", ctypes.c_int64),
+                ("cu_q", ctypes.c_void_p), ("ctx", ctypes.c_void_p), ("page_table", ctypes.c_void_p),
+                ("pages_per_seq", ctypes.c_int32), ("ld_table", ctypes.c_int64), ("mask", ctypes.c_void_p),
+                ("ld_mask", ctypes.c_int64), ("depth", ctypes.c_void_p), ("window", ctypes.c_int32)]
 
 
 _lib = None
@@ -129,6 +166,25 @@ def load(path: str | None = None) -> ctypes.CDLL:
     lib.aq_selftest_bounds_check.restype = ctypes.c_int
     lib.aq_set_path.argtypes = [ctypes.c_int]
     lib.aq_set_path.restype = ctypes.c_int
+    rope_p, cache_p = ctypes.POINTER(c_rope), ctypes.POINTER(c_kv_cache)
+    batch_p, f32 = ctypes.POINTER(c_draft_batch), ctypes.c_float
+    lib.aq_rope_frequencies.argtypes = [i32, ctypes.c_double, i32, ctypes.POINTER(c_rope_scaling), vp,
+                                        ctypes.POINTER(f32)]
+    lib.aq_rope_frequencies.restype = ctypes.c_int
+    lib.aq_rope.argtypes = [rope_p, vp, i64, i32, i32, vp, i64, i64, vp, i64, i64, i32, vp]
+    lib.aq_rope.restype = ctypes.c_int
+    lib.aq_kv_write.argtypes = [cache_p, vp, i64, vp, i64, i64, vp, i64, i64, rope_p, vp, vp, i32, i64, i64, vp, i64,
+                                i64, vp]
+    lib.aq_kv_write.restype = ctypes.c_int
+    lib.aq_kv_read.argtypes = [cache_p, vp, i64, vp, i64, i64, vp, i64, i64, vp]
+    lib.aq_kv_read.restype = ctypes.c_int
+    lib.aq_tree_attention_workspace_bytes.argtypes = [cache_p, batch_p, i32]
+    lib.aq_tree_attention_workspace_bytes.restype = sz
+    lib.aq_tree_attention.argtypes = [cache_p, batch_p, vp, i32, i64, i64, f32, vp, i64, i64, vp, vp, sz, vp]
+    lib.aq_tree_attention.restype = ctypes.c_int
+    lib.aq_verify_drafts.argtypes = [i32, i32, vp, vp, vp, i64, i32, vp, i64, vp, i64, i64, i32, vp, vp, i64, vp, vp,
+                                     i64, i32, vp, vp]
+    lib.aq_verify_drafts.restype = ctypes.c_int
     for name in ("aq_decode_max_m", "aq_last_path", "aq_last_launch_count", "aq_abi_version"):
         getattr(lib, name).argtypes = []
         getattr(lib, name).restype = i32
@@ -480,3 +536,246 @@ def aq_mlp(gate: Theta, up: Theta, down: Theta, x, act=AQ_ACT_GELU_TANH, y=None,
     _check(load().aq_mlp(ctypes.byref(g), ctypes.byref(u), ctypes.byref(d), int(act), _ptr(x), M, _ld(x), _ptr(y),
                          _ld(y), _ptr(workspace), workspace.numel() * workspace.element_size(), _stream(stream)))
     return y
+
+
+# ----------------------------------------------------------------------------------
+# serving: rotary positions, the paged key/value cache, drafted-token attention, verification
+# ----------------------------------------------------------------------------------
+def _want(t, dtype, name, dim=None):
+    """A tensor argument's type (and number of dimensions), checked before its pointer is taken."""
+    if t is not None and (t.dtype != dtype or (dim is not None and t.dim() != dim)):
+        raise TypeError(f"{name}: expected a {dtype} tensor" + (f" of {dim} dimensions" if dim else "")
+                        + f", got {t.dtype} of {t.dim()}")
+    return t
+
+
+def _flat(t, dtype, name, n=None):
+    """Pointer of a contiguous 1-D tensor of the given type, holding n elements where n is given."""
+    if t is None:
+        return 0
+    _want(t, dtype, name, 1)
+    if t.numel() > 1 and t.stride(0) != 1:
+        raise ValueError(f"{name}: expected a contiguous tensor")
+    if n is not None and t.numel() != n:
+        raise ValueError(f"{name}: expected {n} elements, got {t.numel()}")
+    return _ptr(t)
+
+
+def _heads(t, name, tokens=None, heads=None, dim=None):
+    """(pointer, token stride, head stride) of a bf16 [tokens, heads, head_dim] tensor or view."""
+    import torch
+    _want(t, torch.bfloat16, name, 3)
+    if t.size(2) > 1 and t.stride(2) != 1:
+        raise ValueError(f"{name}: expected unit stride along the head")
+    for want, got, what in ((tokens, t.size(0), "tokens"), (heads, t.size(1), "heads"), (dim, t.size(2), "head_dim")):
+        if want is not None and got != want:
+            raise ValueError(f"{name}: expected {want} {what}, got {got}")
+    h, d = int(t.size(1)), int(t.size(2))
+    head = int(t.stride(1)) if h > 1 else d
+    return _ptr(t), int(t.stride(0)) if t.size(0) > 1 else h * head, head
+
+
+@dataclass
+class Rope:
+    """Rotary positions: ``freq`` is an int64 (or uint64) device tensor [rotary_dim / 2] of turns per
+    position in units of 2^-64 (``rope_frequencies``); ``layout`` AQ_ROPE_HALF or AQ_ROPE_INTERLEAVED."""
+    freq: object
+    layout: int = AQ_ROPE_HALF
+    magnitude: float = 1.0
+
+    def c(self) -> c_rope:
+        import torch
+        if self.freq.dtype not in (torch.int64, torch.uint64):
+            raise TypeError(f"Rope.freq: expected an int64 tensor, got {self.freq.dtype}")
+        return c_rope(freq=_flat(self.freq, self.freq.dtype, "Rope.freq"), rotary_dim=2 * int(self.freq.numel()),
+                      layout=int(self.layout), magnitude=float(self.magnitude))
+
+
+def rope_frequencies(rotary_dim: int, base: float = 10000.0, scaling: int = AQ_ROPE_SCALE_NONE, factor: float = 1.0,
+                     original_len: float = 0.0, fast: float = 32.0, slow: float = 1.0, layout: int = AQ_ROPE_HALF,
+                     device="cuda") -> Rope:
+    """A ``Rope`` with the frequencies base^(-2i / rotary_dim), scaled for long contexts by one of the
+    AQ_ROPE_SCALE_* rules (the table is made on the host and copied to ``device`` once)."""
+    import torch
+    host = (ctypes.c_uint64 * max(1, int(rotary_dim) // 2))()
+    mag = ctypes.c_float()
+    par = c_rope_scaling(float(factor), float(original_len), float(fast), float(slow))
+    _check(load().aq_rope_frequencies(int(rotary_dim), float(base), int(scaling), ctypes.byref(par),
+                                      ctypes.cast(host, ctypes.c_void_p), ctypes.byref(mag)))
+    table = torch.tensor([v if v < 2 ** 63 else v - 2 ** 64 for v in host], dtype=torch.int64, device=device)
+    return Rope(table, layout=layout, magnitude=float(mag.value))
+
+
+def aq_rope(rope: Rope, pos, x, inverse: bool = False, y=None, stream=None):
+    """x [T, heads, head_dim] (bf16, any token and head strides) rotated at positions pos (int32 [T]);
+    ``inverse`` turns back, which is the gradient of the rotation. y may be x."""
+    import torch
+    T, heads, dim = (int(n) for n in x.shape)
+    if y is None:
+        y = torch.empty_like(x)
+    xp, xt, xh = _heads(x, "x")
+    yp, yt, yh = _heads(y, "y", T, heads, dim)
+    r = rope.c()
+    _check(load().aq_rope(ctypes.byref(r), _flat(pos, torch.int32, "pos", T), T, heads, dim, xp, xt, xh, yp, yt, yh,
+                          int(bool(inverse)), _stream(stream)))
+    return y
+
+
+@dataclass
+class KvCache:
+    """One layer's paged cache: k and v [pages, kv_heads, page_size, head_dim], bf16, or uint8 (E4M3
+    codes) with the fp32 scales k_scale and v_scale [pages, kv_heads, page_size]."""
+    k: object
+    v: object
+    k_scale: object = None
+    v_scale: object = None
+
+    @classmethod
+    def empty(cls, pages: int, page_size: int, kv_heads: int, head_dim: int, type: int = AQ_KV_BF16, device="cuda"):
+        import torch
+        shape = (pages, kv_heads, page_size, head_dim)
+        if type == AQ_KV_BF16:
+            return cls(*(torch.empty(shape, dtype=torch.bfloat16, device=device) for _ in range(2)))
+        return cls(*(torch.empty(shape, dtype=torch.uint8, device=device) for _ in range(2)),
+                   *(torch.empty(shape[:3], dtype=torch.float32, device=device) for _ in range(2)))
+
+    @property
+    def type(self) -> int:
+        return AQ_KV_BF16 if self.k_scale is None else AQ_KV_E4M3
+
+    @property
+    def page_size(self) -> int:
+        return int(self.k.size(2))
+
+    @property
+    def kv_heads(self) -> int:
+        return int(self.k.size(1))
+
+    @property
+    def head_dim(self) -> int:
+        return int(self.k.size(3))
+
+    def c(self) -> c_kv_cache:
+        import torch
+        code = torch.bfloat16 if self.k_scale is None else torch.uint8
+        for t, dtype, shape, name in ((self.k, code, self.k.shape, "k"), (self.v, code, self.k.shape, "v"),
+                                      (self.k_scale, torch.float32, self.k.shape[:3], "k_scale"),
+                                      (self.v_scale, torch.float32, self.k.shape[:3], "v_scale")):
+            if t is None:
+                continue
+            _want(t, dtype, f"KvCache.{name}")
+            if t.shape != shape or not t.is_contiguous():
+                raise ValueError(f"KvCache.{name}: expected a contiguous tensor of shape {tuple(shape)}")
+        if self.k.dim() != 4:
+            raise ValueError("KvCache.k: expected [pages, kv_heads, page_size, head_dim]")
+        return c_kv_cache(k=_ptr(self.k), v=_ptr(self.v), k_scale=_ptr(self.k_scale), v_scale=_ptr(self.v_scale),
+                          pages=int(self.k.size(0)), page_size=self.page_size, kv_heads=self.kv_heads,
+                          head_dim=self.head_dim, type=self.type)
+
+
+def aq_kv_write(cache: KvCache, k, v, slots, rope: Rope | None = None, pos=None, q=None, q_out=None, stream=None):
+    """Writes k and v [T, kv_heads, head_dim] into the cache's slots (int64 [T]), rotating k with
+    ``rope`` at ``pos``. With q [T, q_heads, head_dim] the rotated queries are returned too (into q_out,
+    which may be q)."""
+    import torch
+    T = int(k.size(0))
+    c = cache.c()
+    kp, kt, kh = _heads(k, "k", T, cache.kv_heads, cache.head_dim)
+    vp, vt, vh = _heads(v, "v", T, cache.kv_heads, cache.head_dim)
+    qp = qt = qh = op = ot = oh = heads = 0
+    if q is not None:
+        heads = int(q.size(1))
+        if q_out is None:
+            q_out = torch.empty(q.shape, dtype=q.dtype, device=q.device)
+        qp, qt, qh = _heads(q, "q", T, None, cache.head_dim)
+        op, ot, oh = _heads(q_out, "q_out", T, heads, cache.head_dim)
+    r = None if rope is None else rope.c()
+    _check(load().aq_kv_write(ctypes.byref(c), _flat(slots, torch.int64, "slots", T), T, kp, kt, kh, vp, vt, vh,
+                              None if r is None else ctypes.byref(r),
+                              0 if pos is None else _flat(pos, torch.int32, "pos", T), qp, heads, qt, qh, op, ot, oh,
+                              _stream(stream)))
+    return q_out
+
+
+def aq_kv_read(cache: KvCache, slots, k=None, v=None, stream=None):
+    """The tokens in the cache's slots (int64 [T]) as bf16: (k, v), each [T, kv_heads, head_dim]."""
+    import torch
+    T = int(slots.numel())
+    shape = (T, cache.kv_heads, cache.head_dim)
+    k = torch.empty(shape, dtype=torch.bfloat16, device=cache.k.device) if k is None else k
+    v = torch.empty(shape, dtype=torch.bfloat16, device=cache.k.device) if v is None else v
+    c = cache.c()
+    _check(load().aq_kv_read(ctypes.byref(c), _flat(slots, torch.int64, "slots"), T, *_heads(k, "k", *shape),
+                             *_heads(v, "v", *shape), _stream(stream)))
+    return k, v
+
+
+def aq_tree_attention(cache: KvCache, q, cu_q, ctx, page_table, max_q: int, mask=None, depth=None, window: int = 0,
+                      scale: float | None = None, out=None, lse=None, return_lse: bool = False, workspace=None,
+                      stream=None):
+    """Attention of drafted tokens q [total_q, q_heads, head_dim] over their sequences' caches: cu_q
+    int32 [batch + 1], ctx int32 [batch], page_table int32 [batch, pages_per_seq], mask int64 [total_q,
+    ceil(max_q / 64)] (bit j of a row: drafted token j of its sequence is seen; None: a chain), depth int32
+    [total_q]. Returns out, or (out, lse [total_q, q_heads] fp32) with ``return_lse``."""
+    import torch
+    total, heads, dim = (int(n) for n in q.shape)
+    if out is None:
+        out = torch.empty(q.shape, dtype=q.dtype, device=q.device)
+    if lse is None and return_lse:
+        lse = torch.empty(total, heads, dtype=torch.float32, device=q.device)
+    if lse is not None and (_want(lse, torch.float32, "lse", 2).shape != (total, heads) or not lse.is_contiguous()):
+        raise ValueError(f"lse: expected a contiguous [{total}, {heads}] tensor")
+    _want(page_table, torch.int32, "page_table", 2)
+    batch = int(page_table.size(0))
+    if mask is not None and (_want(mask, torch.int64, "mask", 2).size(0) != total or mask.size(1) * 64 < max_q):
+        raise ValueError(f"mask: expected [{total}, >= {-(-max_q // 64)}] words")
+    for t, name in ((page_table, "page_table"), (mask, "mask")):
+        if t is not None and t.size(1) > 1 and t.stride(1) != 1:
+            raise ValueError(f"{name}: expected unit column stride")
+    qp, qt, qh = _heads(q, "q", None, None, cache.head_dim)
+    op, ot, oh = _heads(out, "out", total, heads, dim)
+    c = cache.c()
+    d = c_draft_batch(batch=batch, max_q=int(max_q), total_q=total, cu_q=_flat(cu_q, torch.int32, "cu_q", batch + 1),
+                      ctx=_flat(ctx, torch.int32, "ctx", batch), page_table=_ptr(page_table),
+                      pages_per_seq=int(page_table.size(1)), ld_table=_ld_any(page_table), mask=_ptr(mask),
+                      ld_mask=0 if mask is None else _ld_any(mask),
+                      depth=0 if depth is None else _flat(depth, torch.int32, "depth", total), window=int(window))
+    lib = load()
+    if workspace is None:
+        need = lib.aq_tree_attention_workspace_bytes(ctypes.byref(c), ctypes.byref(d), heads)
+        if need == ctypes.c_size_t(-1).value:
+            raise AqError(AQ_ERR_INVALID_ARG, aq_last_error())
+        workspace = torch.empty(int(need), dtype=torch.uint8, device=q.device) if need else None
+    _check(lib.aq_tree_attention(ctypes.byref(c), ctypes.byref(d), qp, heads, qt, qh,
+                                 float(dim ** -0.5 if scale is None else scale), op, ot, oh, _ptr(lse), _ptr(workspace),
+                                 0 if workspace is None else workspace.numel() * workspace.element_size(),
+                                 _stream(stream)))
+    return (out, lse) if return_lse else out
+
+
+def aq_verify_drafts(p, tokens, cu, u, noise, q=None, parent=None, path_cap: int | None = None,
+                     max_nodes: int | None = None, stream=None):
+    """Accepted drafts and the next token of each sequence: (n_accepted [batch], path [batch, path_cap],
+    token [batch]), all int32. p (and q): [nodes + batch, vocab] fp32 or bf16; tokens, parent int32 [nodes]; cu
+    int32 [batch + 1]; u fp32 [nodes]; noise fp32 [batch, vocab]. path_cap and max_nodes default to nodes."""
+    import torch
+    nodes, batch = int(tokens.numel()), int(cu.numel()) - 1
+    for t, name in ((p, "p"), (q, "q")):
+        if t is not None and (t.dtype not in (torch.float32, torch.bfloat16) or t.dtype != p.dtype or t.dim() != 2):
+            raise TypeError(f"{name}: expected a 2-D float32 or bfloat16 tensor (p and q alike)")
+    rows, vocab = int(p.size(0)), int(p.size(1))
+    if q is not None and q.shape != p.shape:
+        raise ValueError(f"q: expected shape {tuple(p.shape)}, got {tuple(q.shape)}")
+    if _want(noise, torch.float32, "noise", 2).shape != (batch, vocab):
+        raise ValueError(f"noise: expected [{batch}, {vocab}]")
+    path_cap = min(nodes, AQ_MAX_DRAFT_NODES) if path_cap is None else int(path_cap)
+    max_nodes = min(nodes, AQ_MAX_DRAFT_NODES) if max_nodes is None else int(max_nodes)
+    n_accepted, token = (torch.empty(batch, dtype=torch.int32, device=p.device) for _ in range(2))
+    path = torch.empty(batch, path_cap, dtype=torch.int32, device=p.device)
+    _check(load().aq_verify_drafts(
+        batch, vocab, _flat(cu, torch.int32, "cu"), _flat(tokens, torch.int32, "tokens"),
+        0 if parent is None else _flat(parent, torch.int32, "parent", nodes), nodes, max_nodes, _ptr(p), _ld_any(p),
+        _ptr(q), 0 if q is None else _ld_any(q), rows, AQ_PROB_F32 if p.dtype == torch.float32 else AQ_PROB_BF16,
+        _flat(u, torch.float32, "u", nodes), _ptr(noise), _ld_any(noise), _ptr(n_accepted), _ptr(path),
+        max(path_cap, 1), path_cap, _ptr(token), _stream(stream)))
+    return n_accepted, path, token

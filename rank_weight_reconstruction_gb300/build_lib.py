@@ -20,8 +20,9 @@ LIB_PATH = os.path.join(PKG_DIR, "libaq_gb300.so")
 # extent and records a violation as AQ_ERR_BOUNDS in the device status word.
 DEBUG_BUILD_DIR = os.path.join(PKG_DIR, "_build_debug")
 DEBUG_LIB_PATH = os.path.join(PKG_DIR, "libaq_gb300_debug.so")
-SOURCES = ["aq_kernels.cu", "aq_decode.cu", "aq_decode2.cu", "aq_decompose.cu", "aq_host.cu", "aq_noalloc.cu"]
-HEADERS = ["aq_ptx.cuh", "aq_internal.h"]
+SOURCES = ["aq_kernels.cu", "aq_decode.cu", "aq_decode2.cu", "aq_decompose.cu", "aq_host.cu", "aq_noalloc.cu",
+           "aq_positions.cu", "aq_attention.cu", "aq_verify.cu"]
+HEADERS = ["aq_ptx.cuh", "aq_internal.h", "aq_serve.h"]
 
 ARCH_FLAGS = ["-gencode", "arch=compute_103a,code=sm_103a"]
 NVCC_FLAGS = ["-O3", "-lineinfo", "-std=c++17", "-Xcompiler", "-fPIC", "-Xcompiler", "-O2",
