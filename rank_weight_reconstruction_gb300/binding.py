@@ -9,6 +9,7 @@ from __future__ import annotations
 
 import ctypes
 import os
+import struct
 from dataclasses import dataclass
 
 from . import build_lib
@@ -166,8 +167,8 @@ def load(path: str | None = None) -> ctypes.CDLL:
     lib.aq_selftest_bounds_check.restype = ctypes.c_int
     lib.aq_set_path.argtypes = [ctypes.c_int]
     lib.aq_set_path.restype = ctypes.c_int
-    rope_p, cache_p = ctypes.POINTER(c_rope), ctypes.POINTER(c_kv_cache)
-    batch_p, f32 = ctypes.POINTER(c_draft_batch), ctypes.c_float
+    rope_p = cache_p = batch_p = vp   # struct pointers: byref() of a c_* struct, or its packed bytes
+    f32 = ctypes.c_float
     lib.aq_rope_frequencies.argtypes = [i32, ctypes.c_double, i32, ctypes.POINTER(c_rope_scaling), vp,
                                         ctypes.POINTER(f32)]
     lib.aq_rope_frequencies.restype = ctypes.c_int
@@ -540,39 +541,61 @@ def aq_mlp(gate: Theta, up: Theta, down: Theta, x, act=AQ_ACT_GELU_TANH, y=None,
 
 # ----------------------------------------------------------------------------------
 # serving: rotary positions, the paged key/value cache, drafted-token attention, verification
+#
+# A decode step makes these calls one after another on a few tokens, so the time of a call is the
+# marshalling below as much as the kernel: shapes and strides are taken once per tensor, dtypes compared
+# by identity, and the argument structs packed as bytes (native alignment, the layout of the c_* structs)
+# instead of filled field by field (measured on one host core: aq_rope 18 -> 7 us a call).
 # ----------------------------------------------------------------------------------
-def _want(t, dtype, name, dim=None):
-    """A tensor argument's type (and number of dimensions), checked before its pointer is taken."""
-    if t is not None and (t.dtype != dtype or (dim is not None and t.dim() != dim)):
-        raise TypeError(f"{name}: expected a {dtype} tensor" + (f" of {dim} dimensions" if dim else "")
-                        + f", got {t.dtype} of {t.dim()}")
-    return t
+_pack_rope = struct.Struct("@Piif4x").pack
+_pack_cache = struct.Struct("@PPPPiiiii4x").pack
+_pack_batch = struct.Struct("@iiqPPPiqPqPi4x").pack
 
 
-def _flat(t, dtype, name, n=None):
-    """Pointer of a contiguous 1-D tensor of the given type, holding n elements where n is given."""
-    if t is None:
-        return 0
-    _want(t, dtype, name, 1)
-    if t.numel() > 1 and t.stride(0) != 1:
-        raise ValueError(f"{name}: expected a contiguous tensor")
-    if n is not None and t.numel() != n:
-        raise ValueError(f"{name}: expected {n} elements, got {t.numel()}")
-    return _ptr(t)
+def _raw_stream(stream, t) -> int:
+    if stream is None:
+        import torch
+        return torch._C._cuda_getCurrentRawStream(t.get_device()) if t.is_cuda else 0
+    return int(stream.cuda_stream) if hasattr(stream, "cuda_stream") else int(stream)
 
 
-def _heads(t, name, tokens=None, heads=None, dim=None):
+def _flat(t, dtype, name, n) -> int:
+    """Pointer of a contiguous 1-D tensor of the given type with n elements (None: any number)."""
+    if t.dtype is not dtype:
+        raise TypeError(f"{name}: expected a {dtype} tensor, got {t.dtype}")
+    shape = t.shape
+    if len(shape) != 1 or (n is not None and shape[0] != n) or not t.is_contiguous():
+        raise ValueError(f"{name}: expected a contiguous 1-D tensor" + ("" if n is None else f" of {n} elements")
+                         + f", got {tuple(shape)} with strides {t.stride()}")
+    return t.data_ptr()
+
+
+def _heads(t, name, tokens, heads, dim):
     """(pointer, token stride, head stride) of a bf16 [tokens, heads, head_dim] tensor or view."""
     import torch
-    _want(t, torch.bfloat16, name, 3)
-    if t.size(2) > 1 and t.stride(2) != 1:
+    if t.dtype is not torch.bfloat16:
+        raise TypeError(f"{name}: expected a bfloat16 tensor, got {t.dtype}")
+    if t.shape != (tokens, heads, dim):
+        raise ValueError(f"{name}: expected shape {(tokens, heads, dim)}, got {tuple(t.shape)}")
+    tok, head, one = t.stride()
+    if one != 1 and dim > 1:
         raise ValueError(f"{name}: expected unit stride along the head")
-    for want, got, what in ((tokens, t.size(0), "tokens"), (heads, t.size(1), "heads"), (dim, t.size(2), "head_dim")):
-        if want is not None and got != want:
-            raise ValueError(f"{name}: expected {want} {what}, got {got}")
-    h, d = int(t.size(1)), int(t.size(2))
-    head = int(t.stride(1)) if h > 1 else d
-    return _ptr(t), int(t.stride(0)) if t.size(0) > 1 else h * head, head
+    if heads == 1:
+        head = dim
+    return t.data_ptr(), tok if tokens > 1 else heads * head, head
+
+
+def _rows(t, dtype, name, rows, cols):
+    """(pointer, row stride) of a 2-D tensor with unit column stride and at least `cols` columns."""
+    if t.dtype is not dtype:
+        raise TypeError(f"{name}: expected a {dtype} tensor, got {t.dtype}")
+    shape = t.shape
+    if len(shape) != 2 or shape[0] != rows or shape[1] < cols:
+        raise ValueError(f"{name}: expected [{rows}, {cols}], got {tuple(shape)}")
+    ld, one = t.stride()
+    if one != 1 and shape[1] > 1:
+        raise ValueError(f"{name}: expected unit column stride")
+    return t.data_ptr(), ld if rows > 1 else max(ld, shape[1])
 
 
 @dataclass
@@ -583,12 +606,12 @@ class Rope:
     layout: int = AQ_ROPE_HALF
     magnitude: float = 1.0
 
-    def c(self) -> c_rope:
+    def packed(self) -> bytes:
         import torch
-        if self.freq.dtype not in (torch.int64, torch.uint64):
-            raise TypeError(f"Rope.freq: expected an int64 tensor, got {self.freq.dtype}")
-        return c_rope(freq=_flat(self.freq, self.freq.dtype, "Rope.freq"), rotary_dim=2 * int(self.freq.numel()),
-                      layout=int(self.layout), magnitude=float(self.magnitude))
+        f = self.freq
+        if f.dtype is not torch.int64 and f.dtype is not torch.uint64:
+            raise TypeError(f"Rope.freq: expected an int64 tensor, got {f.dtype}")
+        return _pack_rope(_flat(f, f.dtype, "Rope.freq", None), 2 * f.shape[0], self.layout, self.magnitude)
 
 
 def rope_frequencies(rotary_dim: int, base: float = 10000.0, scaling: int = AQ_ROPE_SCALE_NONE, factor: float = 1.0,
@@ -610,14 +633,12 @@ def aq_rope(rope: Rope, pos, x, inverse: bool = False, y=None, stream=None):
     """x [T, heads, head_dim] (bf16, any token and head strides) rotated at positions pos (int32 [T]);
     ``inverse`` turns back, which is the gradient of the rotation. y may be x."""
     import torch
-    T, heads, dim = (int(n) for n in x.shape)
+    T, heads, dim = x.shape
     if y is None:
         y = torch.empty_like(x)
-    xp, xt, xh = _heads(x, "x")
-    yp, yt, yh = _heads(y, "y", T, heads, dim)
-    r = rope.c()
-    _check(load().aq_rope(ctypes.byref(r), _flat(pos, torch.int32, "pos", T), T, heads, dim, xp, xt, xh, yp, yt, yh,
-                          int(bool(inverse)), _stream(stream)))
+    _check(load().aq_rope(rope.packed(), _flat(pos, torch.int32, "pos", T), T, heads, dim,
+                          *_heads(x, "x", T, heads, dim), *_heads(y, "y", T, heads, dim), 1 if inverse else 0,
+                          _raw_stream(stream, x)))
     return y
 
 
@@ -643,34 +664,25 @@ class KvCache:
     def type(self) -> int:
         return AQ_KV_BF16 if self.k_scale is None else AQ_KV_E4M3
 
-    @property
-    def page_size(self) -> int:
-        return int(self.k.size(2))
-
-    @property
-    def kv_heads(self) -> int:
-        return int(self.k.size(1))
-
-    @property
-    def head_dim(self) -> int:
-        return int(self.k.size(3))
-
-    def c(self) -> c_kv_cache:
+    def packed(self) -> bytes:
         import torch
-        code = torch.bfloat16 if self.k_scale is None else torch.uint8
-        for t, dtype, shape, name in ((self.k, code, self.k.shape, "k"), (self.v, code, self.k.shape, "v"),
-                                      (self.k_scale, torch.float32, self.k.shape[:3], "k_scale"),
-                                      (self.v_scale, torch.float32, self.k.shape[:3], "v_scale")):
-            if t is None:
-                continue
-            _want(t, dtype, f"KvCache.{name}")
-            if t.shape != shape or not t.is_contiguous():
-                raise ValueError(f"KvCache.{name}: expected a contiguous tensor of shape {tuple(shape)}")
-        if self.k.dim() != 4:
-            raise ValueError("KvCache.k: expected [pages, kv_heads, page_size, head_dim]")
-        return c_kv_cache(k=_ptr(self.k), v=_ptr(self.v), k_scale=_ptr(self.k_scale), v_scale=_ptr(self.v_scale),
-                          pages=int(self.k.size(0)), page_size=self.page_size, kv_heads=self.kv_heads,
-                          head_dim=self.head_dim, type=self.type)
+        k, v, ks, vs = self.k, self.v, self.k_scale, self.v_scale
+        shape = k.shape
+        code = torch.bfloat16 if ks is None else torch.uint8
+        if len(shape) != 4 or v.shape != shape or not k.is_contiguous() or not v.is_contiguous():
+            raise ValueError("KvCache: expected contiguous k and v of one shape [pages, kv_heads, page_size, head_dim]")
+        if k.dtype is not code or v.dtype is not code:
+            raise TypeError(f"KvCache: expected {code} tensors k and v, got {k.dtype} and {v.dtype}")
+        if ks is None or vs is None:
+            if ks is not vs:
+                raise ValueError("KvCache: k_scale and v_scale go together")
+            return _pack_cache(k.data_ptr(), v.data_ptr(), 0, 0, shape[0], shape[2], shape[1], shape[3], AQ_KV_BF16)
+        if ks.dtype is not torch.float32 or vs.dtype is not torch.float32:
+            raise TypeError("KvCache: expected float32 scales")
+        if ks.shape != shape[:3] or vs.shape != shape[:3] or not ks.is_contiguous() or not vs.is_contiguous():
+            raise ValueError(f"KvCache: expected contiguous scales of shape {tuple(shape[:3])}")
+        return _pack_cache(k.data_ptr(), v.data_ptr(), ks.data_ptr(), vs.data_ptr(), shape[0], shape[2], shape[1],
+                           shape[3], AQ_KV_E4M3)
 
 
 def aq_kv_write(cache: KvCache, k, v, slots, rope: Rope | None = None, pos=None, q=None, q_out=None, stream=None):
@@ -678,35 +690,31 @@ def aq_kv_write(cache: KvCache, k, v, slots, rope: Rope | None = None, pos=None,
     ``rope`` at ``pos``. With q [T, q_heads, head_dim] the rotated queries are returned too (into q_out,
     which may be q)."""
     import torch
-    T = int(k.size(0))
-    c = cache.c()
-    kp, kt, kh = _heads(k, "k", T, cache.kv_heads, cache.head_dim)
-    vp, vt, vh = _heads(v, "v", T, cache.kv_heads, cache.head_dim)
-    qp = qt = qh = op = ot = oh = heads = 0
+    c = cache.packed()
+    _, hk, _, dim = cache.k.shape
+    T = k.shape[0]
+    heads, qs, os = 0, (0, 0, 0), (0, 0, 0)
     if q is not None:
-        heads = int(q.size(1))
+        heads = q.shape[1]
         if q_out is None:
             q_out = torch.empty(q.shape, dtype=q.dtype, device=q.device)
-        qp, qt, qh = _heads(q, "q", T, None, cache.head_dim)
-        op, ot, oh = _heads(q_out, "q_out", T, heads, cache.head_dim)
-    r = None if rope is None else rope.c()
-    _check(load().aq_kv_write(ctypes.byref(c), _flat(slots, torch.int64, "slots", T), T, kp, kt, kh, vp, vt, vh,
-                              None if r is None else ctypes.byref(r),
-                              0 if pos is None else _flat(pos, torch.int32, "pos", T), qp, heads, qt, qh, op, ot, oh,
-                              _stream(stream)))
+        qs, os = _heads(q, "q", T, heads, dim), _heads(q_out, "q_out", T, heads, dim)
+    _check(load().aq_kv_write(c, _flat(slots, torch.int64, "slots", T), T, *_heads(k, "k", T, hk, dim),
+                              *_heads(v, "v", T, hk, dim), None if rope is None else rope.packed(),
+                              0 if pos is None else _flat(pos, torch.int32, "pos", T), qs[0], heads, qs[1], qs[2], *os,
+                              _raw_stream(stream, k)))
     return q_out
 
 
 def aq_kv_read(cache: KvCache, slots, k=None, v=None, stream=None):
     """The tokens in the cache's slots (int64 [T]) as bf16: (k, v), each [T, kv_heads, head_dim]."""
     import torch
-    T = int(slots.numel())
-    shape = (T, cache.kv_heads, cache.head_dim)
-    k = torch.empty(shape, dtype=torch.bfloat16, device=cache.k.device) if k is None else k
-    v = torch.empty(shape, dtype=torch.bfloat16, device=cache.k.device) if v is None else v
-    c = cache.c()
-    _check(load().aq_kv_read(ctypes.byref(c), _flat(slots, torch.int64, "slots"), T, *_heads(k, "k", *shape),
-                             *_heads(v, "v", *shape), _stream(stream)))
+    c = cache.packed()
+    sp = _flat(slots, torch.int64, "slots", None)
+    T, (_, hk, _, dim) = slots.shape[0], cache.k.shape
+    k = torch.empty((T, hk, dim), dtype=torch.bfloat16, device=slots.device) if k is None else k
+    v = torch.empty_like(k, memory_format=torch.contiguous_format) if v is None else v
+    _check(load().aq_kv_read(c, sp, T, *_heads(k, "k", T, hk, dim), *_heads(v, "v", T, hk, dim), _raw_stream(stream, k)))
     return k, v
 
 
@@ -716,41 +724,49 @@ def aq_tree_attention(cache: KvCache, q, cu_q, ctx, page_table, max_q: int, mask
     """Attention of drafted tokens q [total_q, q_heads, head_dim] over their sequences' caches: cu_q
     int32 [batch + 1], ctx int32 [batch], page_table int32 [batch, pages_per_seq], mask int64 [total_q,
     ceil(max_q / 64)] (bit j of a row: drafted token j of its sequence is seen; None: a chain), depth int32
-    [total_q]. Returns out, or (out, lse [total_q, q_heads] fp32) with ``return_lse``."""
+    [total_q]. Returns out, or (out, lse [total_q, q_heads] fp32) with ``return_lse``. A workspace that is
+    not given is allocated (its size: ``aq_tree_attention_workspace_bytes``)."""
     import torch
-    total, heads, dim = (int(n) for n in q.shape)
+    i32 = torch.int32
+    c = cache.packed()
+    total, heads, dim = q.shape
     if out is None:
         out = torch.empty(q.shape, dtype=q.dtype, device=q.device)
     if lse is None and return_lse:
-        lse = torch.empty(total, heads, dtype=torch.float32, device=q.device)
-    if lse is not None and (_want(lse, torch.float32, "lse", 2).shape != (total, heads) or not lse.is_contiguous()):
-        raise ValueError(f"lse: expected a contiguous [{total}, {heads}] tensor")
-    _want(page_table, torch.int32, "page_table", 2)
-    batch = int(page_table.size(0))
-    if mask is not None and (_want(mask, torch.int64, "mask", 2).size(0) != total or mask.size(1) * 64 < max_q):
-        raise ValueError(f"mask: expected [{total}, >= {-(-max_q // 64)}] words")
-    for t, name in ((page_table, "page_table"), (mask, "mask")):
-        if t is not None and t.size(1) > 1 and t.stride(1) != 1:
-            raise ValueError(f"{name}: expected unit column stride")
-    qp, qt, qh = _heads(q, "q", None, None, cache.head_dim)
-    op, ot, oh = _heads(out, "out", total, heads, dim)
-    c = cache.c()
-    d = c_draft_batch(batch=batch, max_q=int(max_q), total_q=total, cu_q=_flat(cu_q, torch.int32, "cu_q", batch + 1),
-                      ctx=_flat(ctx, torch.int32, "ctx", batch), page_table=_ptr(page_table),
-                      pages_per_seq=int(page_table.size(1)), ld_table=_ld_any(page_table), mask=_ptr(mask),
-                      ld_mask=0 if mask is None else _ld_any(mask),
-                      depth=0 if depth is None else _flat(depth, torch.int32, "depth", total), window=int(window))
+        lse = torch.empty((total, heads), dtype=torch.float32, device=q.device)
+    if lse is not None and (lse.dtype is not torch.float32 or lse.shape != (total, heads) or not lse.is_contiguous()):
+        raise ValueError(f"lse: expected a contiguous float32 [{total}, {heads}] tensor")
+    batch, pages = page_table.shape
+    table, ld_table = _rows(page_table, i32, "page_table", batch, pages)
+    mp, ld_mask = (0, 0) if mask is None else _rows(mask, torch.int64, "mask", total, -(-max_q // 64))
+    d = _pack_batch(batch, max_q, total, _flat(cu_q, i32, "cu_q", batch + 1), _flat(ctx, i32, "ctx", batch), table, pages,
+                    ld_table, mp, ld_mask, 0 if depth is None else _flat(depth, i32, "depth", total), window)
+    qp, op = _heads(q, "q", total, heads, dim), _heads(out, "out", total, heads, dim)
     lib = load()
+    if dim != cache.k.shape[3]:
+        raise ValueError(f"q: expected head_dim {cache.k.shape[3]}, got {dim}")
     if workspace is None:
-        need = lib.aq_tree_attention_workspace_bytes(ctypes.byref(c), ctypes.byref(d), heads)
-        if need == ctypes.c_size_t(-1).value:
+        need = lib.aq_tree_attention_workspace_bytes(c, d, heads)
+        if need == _NO_SIZE:
             raise AqError(AQ_ERR_INVALID_ARG, aq_last_error())
-        workspace = torch.empty(int(need), dtype=torch.uint8, device=q.device) if need else None
-    _check(lib.aq_tree_attention(ctypes.byref(c), ctypes.byref(d), qp, heads, qt, qh,
-                                 float(dim ** -0.5 if scale is None else scale), op, ot, oh, _ptr(lse), _ptr(workspace),
-                                 0 if workspace is None else workspace.numel() * workspace.element_size(),
-                                 _stream(stream)))
+        workspace = torch.empty(need, dtype=torch.uint8, device=q.device) if need else None
+    wp, wn = (0, 0) if workspace is None else (workspace.data_ptr(), workspace.nbytes)
+    _check(lib.aq_tree_attention(c, d, qp[0], heads, qp[1], qp[2], dim ** -0.5 if scale is None else scale, *op,
+                                 0 if lse is None else lse.data_ptr(), wp, wn, _raw_stream(stream, q)))
     return (out, lse) if return_lse else out
+
+
+_NO_SIZE = ctypes.c_size_t(-1).value
+
+
+def aq_tree_attention_workspace_bytes(cache: KvCache, q_heads: int, batch: int, max_q: int, total_q: int) -> int:
+    """Bytes of device workspace of aq_tree_attention for `batch` sequences that bring at most max_q rows
+    each and total_q in all."""
+    d = _pack_batch(batch, max_q, total_q, 0, 0, 0, 0, 0, 0, 0, 0, 0)
+    need = load().aq_tree_attention_workspace_bytes(cache.packed(), d, q_heads)
+    if need == _NO_SIZE:
+        raise AqError(AQ_ERR_INVALID_ARG, aq_last_error())
+    return int(need)
 
 
 def aq_verify_drafts(p, tokens, cu, u, noise, q=None, parent=None, path_cap: int | None = None,
@@ -759,23 +775,24 @@ def aq_verify_drafts(p, tokens, cu, u, noise, q=None, parent=None, path_cap: int
     token [batch]), all int32. p (and q): [nodes + batch, vocab] fp32 or bf16; tokens, parent int32 [nodes]; cu
     int32 [batch + 1]; u fp32 [nodes]; noise fp32 [batch, vocab]. path_cap and max_nodes default to nodes."""
     import torch
-    nodes, batch = int(tokens.numel()), int(cu.numel()) - 1
-    for t, name in ((p, "p"), (q, "q")):
-        if t is not None and (t.dtype not in (torch.float32, torch.bfloat16) or t.dtype != p.dtype or t.dim() != 2):
-            raise TypeError(f"{name}: expected a 2-D float32 or bfloat16 tensor (p and q alike)")
-    rows, vocab = int(p.size(0)), int(p.size(1))
-    if q is not None and q.shape != p.shape:
-        raise ValueError(f"q: expected shape {tuple(p.shape)}, got {tuple(q.shape)}")
-    if _want(noise, torch.float32, "noise", 2).shape != (batch, vocab):
-        raise ValueError(f"noise: expected [{batch}, {vocab}]")
-    path_cap = min(nodes, AQ_MAX_DRAFT_NODES) if path_cap is None else int(path_cap)
-    max_nodes = min(nodes, AQ_MAX_DRAFT_NODES) if max_nodes is None else int(max_nodes)
-    n_accepted, token = (torch.empty(batch, dtype=torch.int32, device=p.device) for _ in range(2))
-    path = torch.empty(batch, path_cap, dtype=torch.int32, device=p.device)
+    i32, f32 = torch.int32, torch.float32
+    nodes, batch = tokens.shape[0], cu.shape[0] - 1
+    rows, vocab = p.shape
+    if p.dtype is not f32 and p.dtype is not torch.bfloat16:
+        raise TypeError(f"p: expected a float32 or bfloat16 tensor, got {p.dtype}")
+    pp = _rows(p, p.dtype, "p", rows, vocab)
+    qq = (0, 0) if q is None else _rows(q, p.dtype, "q", rows, vocab)
+    nn = _rows(noise, f32, "noise", batch, vocab)
+    if noise.shape[1] != vocab or (q is not None and q.shape[1] != vocab):
+        raise ValueError(f"noise and q: expected {vocab} columns")
+    path_cap = min(nodes, AQ_MAX_DRAFT_NODES) if path_cap is None else path_cap
+    max_nodes = min(nodes, AQ_MAX_DRAFT_NODES) if max_nodes is None else max_nodes
+    both = torch.empty((2, batch), dtype=i32, device=p.device)
+    n_accepted, token = both[0], both[1]
+    path = torch.empty((batch, path_cap), dtype=i32, device=p.device)
     _check(load().aq_verify_drafts(
-        batch, vocab, _flat(cu, torch.int32, "cu"), _flat(tokens, torch.int32, "tokens"),
-        0 if parent is None else _flat(parent, torch.int32, "parent", nodes), nodes, max_nodes, _ptr(p), _ld_any(p),
-        _ptr(q), 0 if q is None else _ld_any(q), rows, AQ_PROB_F32 if p.dtype == torch.float32 else AQ_PROB_BF16,
-        _flat(u, torch.float32, "u", nodes), _ptr(noise), _ld_any(noise), _ptr(n_accepted), _ptr(path),
-        max(path_cap, 1), path_cap, _ptr(token), _stream(stream)))
+        batch, vocab, _flat(cu, i32, "cu", None), _flat(tokens, i32, "tokens", None),
+        0 if parent is None else _flat(parent, i32, "parent", nodes), nodes, max_nodes, *pp, *qq, rows,
+        AQ_PROB_F32 if p.dtype is f32 else AQ_PROB_BF16, _flat(u, f32, "u", nodes), *nn, n_accepted.data_ptr(),
+        path.data_ptr(), max(path_cap, 1), path_cap, token.data_ptr(), _raw_stream(stream, p)))
     return n_accepted, path, token

@@ -1,11 +1,32 @@
 // aq_attention.cu -- aq_tree_attention: attention of each sequence's newest (drafted) tokens over its
 // paged cache.
 //   o_i = sum_j p_ij v_j,  p_i = softmax over the visible j of scale * (q_i . k_j)
-// One pass over the keys with the running maximum m and sum l of the softmax: on a larger maximum the
-// sums so far are scaled by exp(m_old - m_new).
+//
+// Work. The rows of one sequence that read one key/value head (drafted tokens x group of query heads) form
+// row tiles; a tile against its visible keys is an item, its keys cut into tiles of KS. The items' key
+// tiles, laid end to end, are shared out evenly over a persistent grid, so that every CTA streams the same
+// number of keys whatever the sequences' lengths; an item that ends up in several CTAs leaves fp32
+// partial sums (at most two a CTA) that a second launch adds in order.
+//
+// One pass over the keys with the running maximum and sum of the softmax. A producer warp streams K and V
+// pages through a ring of shared-memory stages with TMA (128-byte swizzle); consumer warps split a stage by
+// keys (KG ways) and the tile by rows (RG ways), 16 rows a warp. With keys split over the warps each cache
+// byte is read from shared memory once per 16 rows, no warp waits for another, and their softmax states meet
+// once per item. The products are mma.sync: at 1 to 64 rows a byte of cache meets few rows, the kernel is
+// bound by HBM, and the rows would fill a small part of a 128-lane tcgen05 accumulator.
+//
+// E4M3 caches stay E4M3 down to the matrix instruction (measured here: mma.sync e4m3 2286 TFLOP/s against 607
+// for bf16, both with fp32 sums exact to 24 bits; converting codes to bf16 first costs more than the
+// products). A bf16 query has 8 significant bits, an E4M3 code 4: with a row scaled by a power of two to
+// [128, 256), q = q1 + q2 in E4M3, exact down to 2^-18 of the row's largest element, and q . k takes two
+// products. The weights go the same way: per 32 or 64 keys, w_j = p_j * vscale_j is scaled by a power of two
+// against the row's largest and split in two codes, the product starts from zero and joins the running sum
+// with its factor in fp32, so what a weight loses is 2^-9 of itself or 2^-18 of the largest beside it.
+// With a bf16 cache the weights are rounded to bf16 (2^-9) against the running maximum.
 #include <math.h>
 
 #include <algorithm>
+#include <atomic>
 
 #include "aq_serve.h"
 
@@ -13,8 +34,7 @@ namespace aq {
 namespace {
 
 struct AttnParams {
-  const uint8_t* kc;
-  const uint8_t* vc;
+  CUtensorMap tm_k, tm_v;
   const float* ks;
   const float* vs;
   int32_t pages, page_shift, hk, group;
@@ -34,89 +54,910 @@ struct AttnParams {
   int32_t batch, max_q, window;
   int64_t total_q;
   float scale;
+  int32_t rows_per_tile, row_tiles;   // rows of a tile, tiles of a sequence
+  int32_t main_grid, stages;
+  int64_t* prefix;                    // [batch * row_tiles + 1] first tile of each entry
+  float2* part_ml;                    // [CTA][2][rows of a tile] maximum (base 2) and sum of a partial item
+  float* part_o;                      // [CTA][2][rows of a tile][D]
+  int32_t* status;
+  uint64_t timeout_ns;
+};
+static_assert(sizeof(AttnParams) <= 4096, "kernel parameters are limited to 4 KB");
+
+// ---------------------------------------------------------------------------------
+// instructions
+// ---------------------------------------------------------------------------------
+__device__ __forceinline__ void ldsm4(uint32_t (&r)[4], uint32_t addr) {
+  asm volatile("ldmatrix.sync.aligned.m8n8.x4.shared.b16 {%0, %1, %2, %3}, [%4];"
+               : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3])
+               : "r"(addr)
+               : "memory");
+}
+__device__ __forceinline__ void ldsm4_t(uint32_t (&r)[4], uint32_t addr) {
+  asm volatile("ldmatrix.sync.aligned.m8n8.x4.trans.shared.b16 {%0, %1, %2, %3}, [%4];"
+               : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3])
+               : "r"(addr)
+               : "memory");
+}
+__device__ __forceinline__ void mma_bf16(float (&d)[4], const uint32_t (&a)[4], uint32_t b0, uint32_t b1) {
+  asm volatile("mma.sync.aligned.m16n8k16.row.col.f32.bf16.bf16.f32 {%0, %1, %2, %3}, {%4, %5, %6, %7}, {%8, %9}, "
+               "{%0, %1, %2, %3};"
+               : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3])
+               : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
+}
+__device__ __forceinline__ void mma_e4m3(float (&d)[4], const uint32_t (&a)[4], uint32_t b0, uint32_t b1) {
+  asm volatile("mma.sync.aligned.m16n8k32.row.col.f32.e4m3.e4m3.f32 {%0, %1, %2, %3}, {%4, %5, %6, %7}, {%8, %9}, "
+               "{%0, %1, %2, %3};"
+               : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3])
+               : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
+}
+__device__ __forceinline__ float ex2(float x) {
+  float r;
+  asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(x));
+  return r;
+}
+__device__ __forceinline__ void bulk_load(void* dst, const void* src, uint32_t bytes, uint64_t* bar) {
+  asm volatile("cp.async.bulk.shared::cluster.global.mbarrier::complete_tx::bytes [%0], [%1], %2, [%3];" ::"r"(
+                   smem_u32(dst)),
+               "l"(src), "r"(bytes), "r"(smem_u32(bar))
+               : "memory");
+}
+// Two fp32 values as two E4M3 terms each: hi, then what it leaves (|x| <= 448).
+__device__ __forceinline__ void split_e4m3(float x, float y, uint16_t& hi, uint16_t& lo) {
+  hi = e4m3x2_from_f32(x, y);
+  const uint32_t back = f16x2_from_e4m3x2(hi);
+  const float2 b = __half22float2(*reinterpret_cast<const __half2*>(&back));
+  lo = e4m3x2_from_f32(x - b.x, y - b.y);
+}
+// 2^e for e in [-126, 127].
+__device__ __forceinline__ float pow2(int e) { return __int_as_float((e + 127) << 23); }
+// Exponent of the largest magnitude, for scaling to [128, 256); zero and subnormals count as 2^-119.
+__device__ __forceinline__ int top_exponent(float x) { return max(static_cast<int>(__float_as_uint(x) >> 23) - 127, -119); }
+
+constexpr int kAttnStages = 6;          // most stages of the ring
+constexpr int kAttnWarps = 4;           // consumer warps
+constexpr int kAttnThreads = (kAttnWarps + 1) * 32;
+constexpr int kAttnSmsBound = 192;      // SMs (of any sm_103 part) and CTAs an SM, for sizing the
+constexpr int kAttnMaxPerSm = 2;        // workspace without a device
+
+// ---------------------------------------------------------------------------------
+// shapes: D elements a head, RG row groups of 16 rows, KG key groups, CK keys a warp takes at a time
+// ---------------------------------------------------------------------------------
+template <int D_, bool E4M3_, int RG_>
+struct Shape {
+  static constexpr int D = D_;
+  static constexpr bool E4M3 = E4M3_;
+  static constexpr int RG = RG_, KG = kAttnWarps / RG_;
+  static constexpr int M = 16 * RG;
+  static constexpr int ES = E4M3 ? 1 : 2;
+  // E4M3 products take 32 keys at once; more keys a step mean fewer joins of the partial product, as far
+  // as registers go. A stage holds 16 to 64 KB.
+  static constexpr int CK = E4M3 ? (RG == 1 || D == 256 ? 32 : 64) : (RG == 1 && D >= 128 ? 16 : 32);
+  static constexpr int NI = (E4M3 && D == 64 && RG != 2) || (RG == 4 && D * ES < 512) ? 2 : 1;
+  static constexpr int KS = CK * KG * NI;
+  static constexpr int RB = D * ES < 128 ? D * ES : 128;   // bytes of a row of one column block
+  static constexpr int NC = D * ES / RB;
+  static constexpr int kCode = KS * D * ES;                // bytes of K (or V) in a stage
+  static constexpr int kStage = 2 * kCode;
+  static constexpr int kScale = E4M3 ? KS * 4 : 0;         // bytes of K's (or V's) scales in a stage
+  // two CTAs an SM where the registers and three stages in half its shared memory allow
+  static constexpr bool kTwo = D < 256 && kStage <= 32 * 1024;
+  static constexpr int kCols = 64;                         // columns joined at a time
+  static constexpr int kJoinLd = kCols + 4;
+  static constexpr int kJoin = kAttnWarps * 16 * kJoinLd * 4;
 };
 
-// One block per row and query head; each of four warps takes every fourth key, its lanes the elements.
-template <int D, bool E4M3>
-__global__ void __launch_bounds__(128) aq_tree_attention_kernel(const __grid_constant__ AttnParams p) {
-  constexpr int N = D / 32;
-  __shared__ float sm[4], sl[4], so[4][D];
-  pdl_wait_prior_grid();
-  pdl_launch_dependents();
-  const int lane = threadIdx.x & 31, w = threadIdx.x >> 5;
-  const int64_t row = blockIdx.x;
-  const int h = blockIdx.y, kh = h / p.group;
-  int b = 0;
-  while (b < p.batch && !(p.cu[b] <= row && row < p.cu[b + 1])) ++b;
-  if (b == p.batch) return;
-  const int64_t first = p.cu[b];
-  const int i = static_cast<int>(row - first);
-  if (first < 0 || i >= p.max_q) return;
-  const int T = static_cast<int>(min(static_cast<int64_t>(min(p.cu[b + 1], static_cast<int32_t>(p.total_q))) - first, static_cast<int64_t>(p.max_q)));
-  const int ctx = max(p.ctx[b], 0);
-  const bool dep = p.mask && p.depth;
-  const int64_t pos = static_cast<int64_t>(ctx) + (dep ? p.depth[row] : i);
-  float q[N], o[N], m = -INFINITY, l = 0.0f;
-  for (int e = 0; e < N; ++e) {
-    q[e] = bf16_to_f32(p.q[row * p.q_tok + h * p.q_head + lane * N + e]);
-    o[e] = 0.0f;
-  }
-  for (int64_t j = w; j < static_cast<int64_t>(ctx) + T; j += 4) {
-    const int t = static_cast<int>(j - ctx);
-    bool seen = true;
-    if (t >= 0) seen = p.mask ? (p.mask[row * p.ld_mask + t / 64] >> (t & 63)) & 1 : t <= i;
-    if (p.window > 0) {
-      const int64_t at = t < 0 ? j : static_cast<int64_t>(ctx) + (dep ? p.depth[first + t] : t);
-      seen = seen && pos - at < p.window;
-    }
-    const int64_t pg = j >> p.page_shift;
-    if (!seen || pg >= p.pages_per_seq) continue;
-    const int page = p.table[b * p.ld_table + pg];
-    if (page < 0 || page >= p.pages) continue;
-    const int64_t cell = ((static_cast<int64_t>(page) * p.hk + kh) << p.page_shift) + (j & ((1 << p.page_shift) - 1));
-    float k[N], v[N], s = 0.0f;
-    for (int e = 0; e < N; ++e) {
-      const int64_t at = cell * D + lane * N + e;
-      if (E4M3) {
-        const uint32_t kk = f16x2_from_e4m3x2(p.kc[at]), vv = f16x2_from_e4m3x2(p.vc[at]);
-        k[e] = __low2float(*reinterpret_cast<const __half2*>(&kk)) * p.ks[cell];
-        v[e] = __low2float(*reinterpret_cast<const __half2*>(&vv)) * p.vs[cell];
-      } else {
-        k[e] = bf16_to_f32(reinterpret_cast<const uint16_t*>(p.kc)[at]);
-        v[e] = bf16_to_f32(reinterpret_cast<const uint16_t*>(p.vc)[at]);
-      }
-      s = fmaf(q[e], k[e], s);
-    }
-    for (int off = 16; off; off >>= 1) s += __shfl_xor_sync(0xffffffffu, s, off);
-    s *= p.scale;
-    if (s == -INFINITY) continue;
-    const float mn = fmaxf(m, s), f = m == -INFINITY ? 0.0f : expf(m - mn), x = expf(s - mn);
-    for (int e = 0; e < N; ++e) o[e] = o[e] * f + x * v[e];
-    l = l * f + x;
-    m = mn;
-    if (isnan(s)) l = s;
-  }
-  for (int e = 0; e < N; ++e) so[w][lane * N + e] = o[e];
-  if (lane == 0) {
-    sm[w] = m;
-    sl[w] = l;
-  }
-  __syncthreads();
-  float mt = -INFINITY, lt = 0.0f;
-  for (int k = 0; k < 4; ++k) mt = fmaxf(mt, sm[k]);
-  for (int k = 0; k < 4; ++k) lt += sm[k] == -INFINITY ? 0.0f : sl[k] * expf(sm[k] - mt);
-  for (int d = threadIdx.x; d < D; d += 128) {
-    float x = 0.0f;
-    for (int k = 0; k < 4; ++k) x += sm[k] == -INFINITY ? 0.0f : so[k][d] * expf(sm[k] - mt);
-    p.o[row * p.o_tok + h * p.o_head + d] = f32_to_bf16_rn(mt == -INFINITY ? 0.0f : x / lt);
-  }
-  if (p.lse && threadIdx.x == 0) p.lse[row * (p.hk * p.group) + h] = mt == -INFINITY ? -INFINITY : mt + logf(lt);
+struct AttnShared {
+  uint64_t full[kAttnStages], empty[kAttnStages];
+  uint32_t valid[kAttnStages];
+  int32_t abort;
+  int64_t start_entry, start_tile;      // where this CTA begins: entry, tile within it
+  int64_t part[kAttnThreads];
+  float m[kAttnWarps][16], l[kAttnWarps][16];
+};
+
+// Keys [lo, hi) and tiles [t0, t1) that the rows of entry (sequence b, row tile rt) can see.
+struct Span {
+  int64_t lo, hi;
+  int32_t t0, t1;
+  int32_t first, T, ctx;    // first row in q, rows, context
+};
+
+template <int M, int KS>
+__device__ __forceinline__ Span entry_span(const AttnParams& p, int b, int rt) {
+  Span s;
+  const int c0 = p.cu[b], c1 = p.cu[b + 1];
+  s.first = c0;
+  s.ctx = max(p.ctx[b], 0);
+  s.T = c0 >= 0 && c1 > c0 && c0 < p.total_q ? static_cast<int>(min(static_cast<int64_t>(min(c1 - c0, p.max_q)), p.total_q - c0)) : 0;
+  const int64_t rows = static_cast<int64_t>(s.T) * p.group, r0 = static_cast<int64_t>(rt) * M;
+  s.t0 = s.t1 = 0;
+  s.lo = s.hi = 0;
+  if (r0 >= rows) return s;
+  const int i0 = static_cast<int>(r0 / p.group), i1 = static_cast<int>((min(r0 + M, rows) - 1) / p.group);
+  s.hi = min(static_cast<int64_t>(s.ctx) + (p.mask ? s.T : i1 + 1), static_cast<int64_t>(p.pages_per_seq) << p.page_shift);
+  if (p.window > 0) s.lo = max(static_cast<int64_t>(s.ctx) + (p.mask ? 0 : i0) - p.window + 1, static_cast<int64_t>(0));
+  s.lo = min(s.lo, s.hi);
+  s.t0 = static_cast<int32_t>(s.lo / KS);
+  s.t1 = max(static_cast<int32_t>((s.hi + KS - 1) / KS), s.t0 + 1);   // a row that can see nothing is written too
+  return s;
 }
 
+// Where tile number `at` of the whole call lies; called by every thread, the answer in sh. CTA 0 also leaves
+// the entries' first tiles for the joining launch.
+template <int M, int KS>
+__device__ __forceinline__ void locate(const AttnParams& p, AttnShared& sh, int64_t* prefix, bool write,
+                                          int64_t (&range)[2]) {
+  const int n = p.batch * p.row_tiles, tid = threadIdx.x;
+  const int per = (n + kAttnThreads - 1) / kAttnThreads;
+  const int e0 = min(tid * per, n), e1 = min(e0 + per, n);
+  int64_t sum = 0;
+  for (int e = e0; e < e1; ++e) {
+    const Span s = entry_span<M, KS>(p, e / p.row_tiles, e % p.row_tiles);
+    sum += static_cast<int64_t>(s.t1 - s.t0) * p.hk;
+  }
+  sh.part[tid] = sum;
+  __syncthreads();
+  int64_t before = 0, total = 0;
+  for (int i = 0; i < kAttnThreads; ++i) {
+    const int64_t v = sh.part[i];
+    before += i < tid ? v : 0;
+    total += v;
+  }
+  const int64_t share = (total + gridDim.x - 1) / gridDim.x;
+  range[0] = min(share * blockIdx.x, total);
+  range[1] = min(range[0] + share, total);
+  if (write || (range[0] >= before && range[0] < before + sum)) {
+    int64_t at = before;
+    for (int e = e0; e < e1; ++e) {
+      const Span s = entry_span<M, KS>(p, e / p.row_tiles, e % p.row_tiles);
+      const int64_t len = static_cast<int64_t>(s.t1 - s.t0) * p.hk;
+      if (range[0] >= at && range[0] < at + len) {
+        sh.start_entry = e;
+        sh.start_tile = range[0] - at;
+      }
+      if (write) prefix[e] = at;
+      at += len;
+    }
+    if (write && e1 == n && e0 < n) prefix[n] = at;
+  }
+  if (write && n == 0 && tid == 0) prefix[0] = 0;
+  __syncthreads();
+}
+
+// Walks the segments of a CTA's range: consecutive tiles of one item.
+template <int M, int KS>
+struct Walk {
+  int64_t left;          // tiles of the CTA's range still to come
+  int entry, head;
+  int tile0, n;          // this segment: first tile (within the sequence) and how many
+  int len;               // tiles of the whole item
+  int offset;            // of them before this segment
+  Span s;
+  __device__ __forceinline__ Walk(const AttnParams& p, const AttnShared& sh, const int64_t (&range)[2]) {
+    left = range[1] - range[0];
+    if (left <= 0) return;
+    entry = static_cast<int>(sh.start_entry);
+    s = entry_span<M, KS>(p, entry / p.row_tiles, entry % p.row_tiles);
+    len = s.t1 - s.t0;
+    head = static_cast<int>(sh.start_tile / len);
+    offset = static_cast<int>(sh.start_tile - static_cast<int64_t>(head) * len);
+    cut();
+  }
+  __device__ __forceinline__ void cut() {
+    tile0 = s.t0 + offset;
+    n = static_cast<int>(min(static_cast<int64_t>(len - offset), left));
+  }
+  __device__ __forceinline__ void next(const AttnParams& p) {
+    left -= n;
+    if (left <= 0) return;
+    offset = 0;
+    if (++head == p.hk) {
+      head = 0;
+      do {
+        ++entry;
+        s = entry_span<M, KS>(p, entry / p.row_tiles, entry % p.row_tiles);
+        len = s.t1 - s.t0;
+      } while (len == 0);
+    }
+    cut();
+  }
+};
+
+template <class S>
+__device__ __forceinline__ void produce(const AttnParams& p, AttnShared& sh, uint8_t* stage0, uint8_t* scale0,
+                                        const int64_t (&range)[2], int stages, const AbortCtl& ctl) {
+  const int lane = threadIdx.x & 31;
+  const int page = 1 << p.page_shift;
+  const int box = min(page, S::KS), np = S::KS / box;   // rows of a page in a tile; pages a tile touches
+  int st = 0, issued = 0;
+  uint32_t parity = 1;
+  Walk<S::M, S::KS> w(p, sh, range);
+  bool ok = true;
+  while (ok && w.left > 0) {
+    const int b = w.entry / p.row_tiles;
+    const int32_t* table = p.table + b * p.ld_table;
+    auto page_id = [&](int64_t i) {   // -1: left out
+      if (i >= p.pages_per_seq || (i << p.page_shift) >= w.s.hi || ((i + 1) << p.page_shift) <= w.s.lo) return -1;
+      const int id = table[i];
+      return id >= 0 && id < p.pages ? id : -1;
+    };
+    // page numbers of this sequence, 32 at a time and 32 ahead
+    int64_t base = (static_cast<int64_t>(w.tile0) * S::KS) >> p.page_shift;
+    int cur = page_id(base + lane), ahead = page_id(base + 32 + lane);
+    for (int i = 0; i < w.n; ++i) {
+      const int64_t key = static_cast<int64_t>(w.tile0 + i) * S::KS;
+      const int64_t first = key >> p.page_shift;
+      if (first >= base + 32) {
+        base += 32;
+        cur = ahead;
+        ahead = page_id(base + 32 + lane);
+      }
+      const int id = __shfl_sync(0xffffffffu, cur, static_cast<int>(first - base) + (lane < np ? lane : 0));
+      const bool valid = lane < np && id >= 0 && key + static_cast<int64_t>(lane) * box < w.s.hi;
+      const uint32_t mask = __ballot_sync(0xffffffffu, valid);
+      ok = mbar_wait(&sh.empty[st], parity, ctl);
+      if (!__all_sync(0xffffffffu, ok)) {
+        ok = false;
+        break;
+      }
+      if (lane == 0) {
+        sh.valid[st] = mask;
+        mbar_arrive_expect_tx(&sh.full[st], __popc(mask) * box * (2 * S::D * S::ES + (S::E4M3 ? 8 : 0)));
+      }
+      __syncwarp();
+      if (valid) {
+        uint8_t* kd = stage0 + st * S::kStage + lane * box * S::RB;
+        const int off = static_cast<int>(key & (page - 1));
+        const int row = id * p.hk + w.head;
+#pragma unroll
+        for (int c = 0; c < S::NC; ++c) {
+          tma_load_3d(kd + c * S::KS * S::RB, &p.tm_k, c * (S::RB / S::ES), off, row, &sh.full[st]);
+          tma_load_3d(kd + S::kCode + c * S::KS * S::RB, &p.tm_v, c * (S::RB / S::ES), off, row, &sh.full[st]);
+        }
+        if (S::E4M3) {
+          const int64_t cell = (static_cast<int64_t>(row) << p.page_shift) + off;
+          uint8_t* sd = scale0 + st * 2 * S::kScale + lane * box * 4;
+          bulk_load(sd, p.ks + cell, box * 4, &sh.full[st]);
+          bulk_load(sd + S::kScale, p.vs + cell, box * 4, &sh.full[st]);
+        }
+      }
+      ++issued;
+      if (++st == stages) {
+        st = 0;
+        parity ^= 1;
+      }
+    }
+    if (ok) w.next(p);
+  }
+  if (!ok) {   // a wait ran out: let the copies already issued land before the CTA may end
+    for (int i = 0; i < min(issued, stages); ++i) {
+      st = st == 0 ? stages - 1 : st - 1;
+      const uint32_t use = (issued - 1 - i) / stages;
+      const uint64_t t0 = global_timer_ns();
+      while (!mbar_try_wait(&sh.full[st], use & 1))
+        if (global_timer_ns() - t0 > ctl.timeout_ns) break;
+    }
+  }
+}
+
+// What a thread holds of its warp's 16 rows: rows g and g + 8 (g = lane / 4).
+template <class S>
+struct Rows {
+  static constexpr int NK = S::D * S::ES / 32;            // 32-byte steps of a row
+  static constexpr int NQ = S::E4M3 ? 2 : 1;
+  uint32_t q[NQ][NK][4];
+  float fac[2];                                           // of the raw products, to base-2 logits
+  int64_t pos[2];
+  int64_t top;                                            // largest position of the warp's rows
+  const uint64_t* mask[2];
+  int i[2];
+  __device__ __forceinline__ void load(const AttnParams& p, const Span& s, int head, int rt, int rg) {
+    const int lane = threadIdx.x & 31, g = lane >> 2, t = lane & 3;
+    const float scale2 = p.scale * 1.4426950408889634f;
+    const bool dep = p.mask && p.depth;
+#pragma unroll
+    for (int h = 0; h < 2; ++h) {
+      const int64_t r = static_cast<int64_t>(rt) * S::M + rg * 16 + g + 8 * h;
+      const bool live = r < static_cast<int64_t>(s.T) * p.group;
+      const int64_t rr = live ? r : 0;
+      i[h] = static_cast<int>(rr / p.group);
+      const int64_t row = s.first + i[h];
+      const uint16_t* src = p.q + row * p.q_tok + (head * p.group + static_cast<int>(rr - static_cast<int64_t>(i[h]) * p.group)) * p.q_head;
+      pos[h] = static_cast<int64_t>(s.ctx) + (dep ? max(p.depth[row], 0) : i[h]);
+      mask[h] = p.mask ? p.mask + row * p.ld_mask : nullptr;
+      if (S::E4M3) {
+        float amax = 0.0f;
+        bool finite = true;
+#pragma unroll
+        for (int k = 0; k < NK; ++k)
+#pragma unroll
+          for (int c = 0; c < 2; ++c) {
+            const uint2 v = live ? *reinterpret_cast<const uint2*>(src + k * 32 + c * 16 + t * 4) : make_uint2(0, 0);
+            const float x[4] = {__uint_as_float(v.x << 16), __uint_as_float(v.x & 0xffff0000u),
+                                __uint_as_float(v.y << 16), __uint_as_float(v.y & 0xffff0000u)};
+#pragma unroll
+            for (int e = 0; e < 4; ++e) {
+              amax = fmaxf(amax, fabsf(x[e]));
+              finite = finite && isfinite(x[e]);
+            }
+            q[0][k][h + 2 * c] = v.x;
+            q[NQ - 1][k][h + 2 * c] = v.y;
+          }
+        amax = fmaxf(amax, __shfl_xor_sync(0xffffffffu, amax, 1));
+        amax = fmaxf(amax, __shfl_xor_sync(0xffffffffu, amax, 2));
+        const unsigned bad = __ballot_sync(0xffffffffu, !finite);
+        finite = ((bad >> (lane & ~3)) & 15u) == 0;
+        const int e = finite ? top_exponent(amax) : 0;
+        const float f = pow2(7 - e);
+        // a row that holds an infinity or a NaN has no finite score
+        fac[h] = finite ? pow2(e - 7) * scale2 : __uint_as_float(0x7fc00000u);
+#pragma unroll
+        for (int k = 0; k < NK; ++k)
+#pragma unroll
+          for (int c = 0; c < 2; ++c) {
+            const uint32_t a = finite ? q[0][k][h + 2 * c] : 0u, b = finite ? q[NQ - 1][k][h + 2 * c] : 0u;
+            uint16_t h0, l0, h1, l1;
+            split_e4m3(__uint_as_float(a << 16) * f, __uint_as_float(a & 0xffff0000u) * f, h0, l0);
+            split_e4m3(__uint_as_float(b << 16) * f, __uint_as_float(b & 0xffff0000u) * f, h1, l1);
+            q[0][k][h + 2 * c] = h0 | (static_cast<uint32_t>(h1) << 16);
+            q[NQ - 1][k][h + 2 * c] = l0 | (static_cast<uint32_t>(l1) << 16);
+          }
+      } else {
+        fac[h] = scale2;
+#pragma unroll
+        for (int k = 0; k < NK; ++k)
+#pragma unroll
+          for (int c = 0; c < 2; ++c)
+            q[0][k][h + 2 * c] = live ? *reinterpret_cast<const uint32_t*>(src + k * 16 + c * 8 + t * 2) : 0u;
+      }
+    }
+    top = max(pos[0], pos[1]);
+#pragma unroll
+    for (int o = 16; o > 0; o >>= 1) top = max(top, __shfl_xor_sync(0xffffffffu, top, o));
+  }
+};
+
+// Shared-memory address of 16 bytes of a key: column block x / (RB / 16), swizzled as TMA writes it.
+template <class S>
+__device__ __forceinline__ uint32_t cell_addr(uint32_t base, int key, int x) {
+  constexpr int XB = S::RB / 16;
+  const int c = x / XB, xi = x % XB;
+  const int sw = S::RB == 128 ? (key & 7) : ((key >> 1) & 3);
+  return base + c * S::KS * S::RB + key * S::RB + ((xi ^ sw) << 4);
+}
+
+template <class S>
+__device__ __forceinline__ bool visible(const AttnParams& p, const Span& s, const Rows<S>& rw, int h, int64_t key,
+                                        uint32_t pages, int box_shift, int in_tile) {
+  if (key >= s.hi || !((pages >> (in_tile >> box_shift)) & 1)) return false;
+  const int64_t t = key - s.ctx;
+  int64_t at = key;
+  if (t >= 0) {
+    if (rw.mask[h]) {
+      if (!((rw.mask[h][t >> 6] >> (t & 63)) & 1)) return false;
+      if (p.window > 0 && p.depth) at = static_cast<int64_t>(s.ctx) + max(p.depth[s.first + t], 0);
+    } else if (t > rw.i[h]) {
+      return false;
+    }
+  }
+  return p.window <= 0 || rw.pos[h] - at < p.window;
+}
+
+template <class S>
+__device__ __forceinline__ void consume(const AttnParams& p, AttnShared& sh, const uint8_t* stage0, const uint8_t* scale0,
+                                        float* join, const int64_t (&range)[2], int stages,
+                                        const AbortCtl& ctl) {
+  constexpr int D = S::D, NT = S::CK / 8;      // key tiles of 8 in a step
+  constexpr int NX = D / 16;                   // 16-column groups of the output
+  const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+  const int g = lane >> 2, t = lane & 3;
+  const int rg = warp / S::KG, kg = warp % S::KG;
+  const int box_shift = min(p.page_shift, 31 - __clz(S::KS));
+  int st = 0;
+  uint32_t parity = 0;
+  Walk<S::M, S::KS> w(p, sh, range);
+  float* mine = join + warp * 16 * S::kJoinLd;
+  bool ok = true;
+  while (w.left > 0) {
+    Rows<S> rw;
+    const int rt = w.entry % p.row_tiles;
+    rw.load(p, w.s, w.head, rt, rg);
+    float o[NX][2][4];     // E4M3: [row half][4 consecutive columns]; bf16: [8-column tile][fragment]
+#pragma unroll
+    for (int x = 0; x < NX; ++x)
+#pragma unroll
+      for (int a = 0; a < 2; ++a)
+#pragma unroll
+        for (int c = 0; c < 4; ++c) o[x][a][c] = 0.0f;
+    float m[2] = {-INFINITY, -INFINITY}, l[2] = {0.0f, 0.0f};
+
+    for (int it = 0; it < w.n; ++it) {
+      ok = ok && mbar_wait(&sh.full[st], parity, ctl);
+      ok = __all_sync(0xffffffffu, ok);
+      if (!ok) break;
+      const uint32_t pages = sh.valid[st];
+      const uint32_t kb = smem_u32(stage0 + st * S::kStage), vb = kb + S::kCode;
+      const float* ksc = reinterpret_cast<const float*>(scale0 + st * 2 * S::kScale);
+      const float* vsc = reinterpret_cast<const float*>(scale0 + st * 2 * S::kScale + S::kScale);
+      const int64_t key0 = static_cast<int64_t>(w.tile0 + it) * S::KS;
+      const uint32_t all_pages = S::KS >> box_shift >= 32 ? 0xffffffffu : (1u << (S::KS >> box_shift)) - 1;
+      for (int ni = 0; ni < S::NI; ++ni) {
+        const int k0 = (kg * S::NI + ni) * S::CK;            // the step's first key within the tile
+        const int64_t ka = key0 + k0;
+        if (ka >= w.s.hi || ka + S::CK <= w.s.lo) continue;
+        const bool whole = ka + S::CK <= min(static_cast<int64_t>(w.s.ctx), w.s.hi) && pages == all_pages &&
+                           (p.window <= 0 || rw.top - ka < p.window);
+        // scores
+        float sc[NT][4];
+#pragma unroll
+        for (int n = 0; n < NT; ++n) {
+          sc[n][0] = sc[n][1] = sc[n][2] = sc[n][3] = 0.0f;
+#pragma unroll
+          for (int k2 = 0; k2 < Rows<S>::NK / 2; ++k2) {
+            uint32_t r[4];
+            ldsm4(r, cell_addr<S>(kb, k0 + n * 8 + (lane & 7), 4 * k2 + (lane >> 3)));
+            if (S::E4M3) {
+              mma_e4m3(sc[n], rw.q[0][2 * k2], r[0], r[1]);
+              mma_e4m3(sc[n], rw.q[Rows<S>::NQ - 1][2 * k2], r[0], r[1]);
+              mma_e4m3(sc[n], rw.q[0][2 * k2 + 1], r[2], r[3]);
+              mma_e4m3(sc[n], rw.q[Rows<S>::NQ - 1][2 * k2 + 1], r[2], r[3]);
+            } else {
+              mma_bf16(sc[n], rw.q[0][2 * k2], r[0], r[1]);
+              mma_bf16(sc[n], rw.q[0][2 * k2 + 1], r[2], r[3]);
+            }
+          }
+        }
+        float mt[2] = {-INFINITY, -INFINITY};
+#pragma unroll
+        for (int n = 0; n < NT; ++n) {
+          float2 ks = make_float2(1.0f, 1.0f);
+          if (S::E4M3) ks = *reinterpret_cast<const float2*>(ksc + k0 + n * 8 + 2 * t);
+#pragma unroll
+          for (int c = 0; c < 4; ++c) {
+            float v = sc[n][c] * rw.fac[c >> 1];
+            if (S::E4M3) v *= (c & 1) ? ks.y : ks.x;
+            if (!whole) {
+              const int in_tile = k0 + n * 8 + 2 * t + (c & 1);
+              if (!visible<S>(p, w.s, rw, c >> 1, key0 + in_tile, pages, box_shift, in_tile)) v = -INFINITY;
+            }
+            sc[n][c] = v;
+            mt[c >> 1] = fmaxf(mt[c >> 1], v);
+          }
+        }
+#pragma unroll
+        for (int h = 0; h < 2; ++h) {
+          mt[h] = fmaxf(mt[h], __shfl_xor_sync(0xffffffffu, mt[h], 1));
+          mt[h] = fmaxf(mt[h], __shfl_xor_sync(0xffffffffu, mt[h], 2));
+        }
+        float keep[2], mn[2];      // factor of the sums so far; the new maximum (0 where nothing was seen)
+        bool same = true;
+#pragma unroll
+        for (int h = 0; h < 2; ++h) {
+          const float mx = fmaxf(m[h], mt[h]);
+          mn[h] = mx == -INFINITY ? 0.0f : mx;
+          keep[h] = ex2(m[h] - mn[h]);
+          same = same && mx == m[h];
+          m[h] = mx;
+        }
+        same = __all_sync(0xffffffffu, same);
+        if constexpr (S::E4M3) {
+          // weights against the step's own maximum, times the values' scales
+          float ms[2], lt[2] = {0.0f, 0.0f}, wm[2] = {0.0f, 0.0f};
+          ms[0] = mt[0] == -INFINITY ? 0.0f : mt[0];
+          ms[1] = mt[1] == -INFINITY ? 0.0f : mt[1];
+#pragma unroll
+          for (int n = 0; n < NT; ++n) {
+            const float2 vs = *reinterpret_cast<const float2*>(vsc + k0 + n * 8 + 2 * t);
+#pragma unroll
+            for (int c = 0; c < 4; ++c) {
+              const float e = ex2(sc[n][c] - ms[c >> 1]);
+              lt[c >> 1] += e;
+              float v = e * ((c & 1) ? vs.y : vs.x);
+              if (!whole && sc[n][c] == -INFINITY) v = 0.0f;   // whatever scale lies there
+              sc[n][c] = v;
+              wm[c >> 1] = fmaxf(wm[c >> 1], v);
+            }
+          }
+          float f[2], back[2];
+#pragma unroll
+          for (int h = 0; h < 2; ++h) {
+            wm[h] = fmaxf(wm[h], __shfl_xor_sync(0xffffffffu, wm[h], 1));
+            wm[h] = fmaxf(wm[h], __shfl_xor_sync(0xffffffffu, wm[h], 2));
+            const int e = min(top_exponent(wm[h]), 120);
+            const float in = ex2(ms[h] - mn[h]);
+            f[h] = pow2(7 - e);
+            back[h] = mt[h] == -INFINITY ? 0.0f : in * pow2(e - 7);
+            l[h] = l[h] * keep[h] + (mt[h] == -INFINITY && lt[h] == 0.0f ? 0.0f : lt[h] * in);
+          }
+          constexpr int NP = S::CK / 32;
+          uint32_t hi[NP][4], lo[NP][4];
+#pragma unroll
+          for (int k = 0; k < NP; ++k)
+#pragma unroll
+            for (int h = 0; h < 2; ++h)
+#pragma unroll
+              for (int c = 0; c < 2; ++c) {
+                uint16_t h0, l0, h1, l1;
+                const float(&a)[4] = sc[4 * k + 2 * c];
+                const float(&b)[4] = sc[4 * k + 2 * c + 1];
+                split_e4m3(a[2 * h] * f[h], a[2 * h + 1] * f[h], h0, l0);
+                split_e4m3(b[2 * h] * f[h], b[2 * h + 1] * f[h], h1, l1);
+                hi[k][h + 2 * c] = h0 | (static_cast<uint32_t>(h1) << 16);
+                lo[k][h + 2 * c] = l0 | (static_cast<uint32_t>(l1) << 16);
+              }
+#pragma unroll
+          for (int x = 0; x < NX; ++x) {
+            float ev[4] = {0.0f, 0.0f, 0.0f, 0.0f}, od[4] = {0.0f, 0.0f, 0.0f, 0.0f};
+#pragma unroll
+            for (int k = 0; k < NP; ++k) {
+              uint32_t r[4];
+              ldsm4_t(r, cell_addr<S>(vb, k0 + k * 32 + lane, x));
+              if (!whole) {   // codes of NaN in cells that nobody wrote
+#pragma unroll
+                for (int i = 0; i < 4; ++i) {
+                  const uint32_t nan = ((r[i] & 0x7f7f7f7fu) + 0x01010101u) & 0x80808080u;
+                  r[i] &= ~((nan >> 7) * 255u);
+                }
+              }
+              const uint32_t e0 = __byte_perm(r[0], r[1], 0x6420), e1 = __byte_perm(r[2], r[3], 0x6420);
+              const uint32_t d0 = __byte_perm(r[0], r[1], 0x7531), d1 = __byte_perm(r[2], r[3], 0x7531);
+              mma_e4m3(ev, hi[k], e0, e1);
+              mma_e4m3(od, hi[k], d0, d1);
+              mma_e4m3(ev, lo[k], e0, e1);
+              mma_e4m3(od, lo[k], d0, d1);
+            }
+#pragma unroll
+            for (int h = 0; h < 2; ++h) {
+              const float v[4] = {ev[2 * h], od[2 * h], ev[2 * h + 1], od[2 * h + 1]};
+#pragma unroll
+              for (int c = 0; c < 4; ++c)
+                o[x][h][c] = same ? fmaf(v[c], back[h], o[x][h][c]) : fmaf(v[c], back[h], o[x][h][c] * keep[h]);
+            }
+          }
+        } else {
+          float lt[2] = {0.0f, 0.0f};
+          uint32_t pw[NT / 2][4];
+          const bool slow_rows = !whole;
+          if (slow_rows)
+            for (int n = 0; n < NT; ++n)
+              for (int c = 0; c < 4; ++c)
+                mine[(g + 8 * (c >> 1)) * S::kJoinLd + n * 8 + 2 * t + (c & 1)] = sc[n][c] == -INFINITY ? -1.0f : ex2(sc[n][c] - mn[c >> 1]);
+#pragma unroll
+          for (int n = 0; n < NT; ++n) {
+#pragma unroll
+            for (int c = 0; c < 4; ++c) {
+              sc[n][c] = ex2(sc[n][c] - mn[c >> 1]);
+              lt[c >> 1] += sc[n][c];
+            }
+            pw[n / 2][2 * (n & 1)] = pack_bf16x2_cvt(sc[n][0], sc[n][1]);
+            pw[n / 2][2 * (n & 1) + 1] = pack_bf16x2_cvt(sc[n][2], sc[n][3]);
+          }
+          l[0] = l[0] * keep[0] + lt[0];
+          l[1] = l[1] * keep[1] + lt[1];
+          if (!same) {
+#pragma unroll
+            for (int x = 0; x < NX; ++x)
+#pragma unroll
+              for (int a = 0; a < 2; ++a)
+#pragma unroll
+                for (int c = 0; c < 4; ++c) o[x][a][c] *= keep[c >> 1];
+          }
+          uint32_t bad = 0;
+#pragma unroll
+          for (int k = 0; k < NT / 2; ++k)
+#pragma unroll
+            for (int x = 0; x < NX; ++x) {
+              uint32_t r[4];
+              ldsm4_t(r, cell_addr<S>(vb, k0 + k * 16 + (lane & 15), 2 * x + (lane >> 4)));
+              if (!whole) {   // infinities and NaN take no part in the product; see below
+#pragma unroll
+                for (int i = 0; i < 4; ++i) {
+                  const uint32_t off = __vcmpeq2(r[i] & 0x7f807f80u, 0x7f807f80u);
+                  bad |= off;
+                  r[i] &= ~off;
+                }
+              }
+              mma_bf16(o[x][0], pw[k], r[0], r[1]);
+              mma_bf16(o[x][1], pw[k], r[2], r[3]);
+            }
+          if (slow_rows && __any_sync(0xffffffffu, bad != 0)) {
+            // they reach the rows that see them, and no others
+            __syncwarp();
+            for (int k = 0; k < S::CK; ++k) {
+              const float w0 = mine[g * S::kJoinLd + k], w1 = mine[(g + 8) * S::kJoinLd + k];
+#pragma unroll
+              for (int x = 0; x < NX; ++x)
+#pragma unroll
+                for (int a = 0; a < 2; ++a) {
+                  const uint32_t addr = cell_addr<S>(vb, k0 + k, 2 * x + a) + 4 * t;
+                  uint32_t v;
+                  asm volatile("ld.shared.u32 %0, [%1];" : "=r"(v) : "r"(addr) : "memory");
+                  const float v0 = __uint_as_float(v << 16), v1 = __uint_as_float(v & 0xffff0000u);
+                  if (!isfinite(v0)) {
+                    if (w0 >= 0.0f) o[x][a][0] += w0 * v0;
+                    if (w1 >= 0.0f) o[x][a][2] += w1 * v0;
+                  }
+                  if (!isfinite(v1)) {
+                    if (w0 >= 0.0f) o[x][a][1] += w0 * v1;
+                    if (w1 >= 0.0f) o[x][a][3] += w1 * v1;
+                  }
+                }
+            }
+          }
+          __syncwarp();
+        }
+      }
+      __syncwarp();
+      if (lane == 0) mbar_arrive(&sh.empty[st]);
+      if (++st == stages) {
+        st = 0;
+        parity ^= 1;
+      }
+    }
+    // the item's rows: the warps of a row group put their sums together
+#pragma unroll
+    for (int h = 0; h < 2; ++h) {
+      l[h] += __shfl_xor_sync(0xffffffffu, l[h], 1);
+      l[h] += __shfl_xor_sync(0xffffffffu, l[h], 2);
+      if (t == 0) {
+        sh.m[warp][g + 8 * h] = m[h];
+        sh.l[warp][g + 8 * h] = l[h];
+      }
+    }
+    named_bar_sync(1, kAttnWarps * 32);
+    const bool complete = w.n == w.len;
+    const int slot = w.offset > 0 ? 0 : 1;   // partial sums: an item begun elsewhere, or one that goes on elsewhere
+    float fold[2];
+#pragma unroll
+    for (int h = 0; h < 2; ++h) {
+      float mx = -INFINITY;
+      for (int k = 0; k < S::KG; ++k) mx = fmaxf(mx, sh.m[rg * S::KG + k][g + 8 * h]);
+      fold[h] = ex2(m[h] - (mx == -INFINITY ? 0.0f : mx));
+    }
+    for (int c0 = 0; c0 < D; c0 += S::kCols) {
+#pragma unroll
+      for (int x = 0; x < NX; ++x) {
+        if (x * 16 < c0 || x * 16 >= c0 + S::kCols) continue;
+        if (S::E4M3) {
+#pragma unroll
+          for (int h = 0; h < 2; ++h)
+            *reinterpret_cast<float4*>(mine + (g + 8 * h) * S::kJoinLd + x * 16 - c0 + 4 * t) =
+                make_float4(o[x][h][0] * fold[h], o[x][h][1] * fold[h], o[x][h][2] * fold[h], o[x][h][3] * fold[h]);
+        } else {
+#pragma unroll
+          for (int a = 0; a < 2; ++a)
+#pragma unroll
+            for (int h = 0; h < 2; ++h)
+              *reinterpret_cast<float2*>(mine + (g + 8 * h) * S::kJoinLd + x * 16 + 8 * a - c0 + 2 * t) =
+                  make_float2(o[x][a][2 * h] * fold[h], o[x][a][2 * h + 1] * fold[h]);
+        }
+      }
+      named_bar_sync(1, kAttnWarps * 32);
+      for (int u = tid; u < S::M * (S::kCols / 4); u += kAttnWarps * 32) {
+        const int r = u / (S::kCols / 4), c = u % (S::kCols / 4) * 4;
+        const int g0 = r / 16 * S::KG, rr = r % 16;
+        float mx = -INFINITY, lt = 0.0f;
+        float4 v = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+#pragma unroll
+        for (int k = 0; k < S::KG; ++k) mx = fmaxf(mx, sh.m[g0 + k][rr]);
+        const float mz = mx == -INFINITY ? 0.0f : mx;
+#pragma unroll
+        for (int k = 0; k < S::KG; ++k) {
+          lt += sh.l[g0 + k][rr] * ex2(sh.m[g0 + k][rr] - mz);
+          const float4 a = *reinterpret_cast<const float4*>(join + ((g0 + k) * 16 + rr) * S::kJoinLd + c);
+          v.x += a.x;
+          v.y += a.y;
+          v.z += a.z;
+          v.w += a.w;
+        }
+        const int64_t row = static_cast<int64_t>(rt) * S::M + r;
+        if (row >= static_cast<int64_t>(w.s.T) * p.group || !ok) continue;
+        if (complete) {
+          const int i = static_cast<int>(row / p.group);
+          const int head = w.head * p.group + static_cast<int>(row - static_cast<int64_t>(i) * p.group);
+          const bool none = mx == -INFINITY && lt == 0.0f;
+          const float inv = none ? 0.0f : 1.0f / lt;
+          uint16_t* dst = p.o + (static_cast<int64_t>(w.s.first) + i) * p.o_tok + head * p.o_head + c0 + c;
+          *reinterpret_cast<uint2*>(dst) = none ? make_uint2(0, 0)
+                                                : make_uint2(pack_bf16x2_cvt(v.x * inv, v.y * inv), pack_bf16x2_cvt(v.z * inv, v.w * inv));
+          if (p.lse && c0 == 0 && c == 0)
+            p.lse[(static_cast<int64_t>(w.s.first) + i) * (p.hk * p.group) + head] = none ? -INFINITY : (mz + log2f(lt)) * 0.6931471805599453f;
+        } else {
+          const int64_t at = (static_cast<int64_t>(blockIdx.x) * 2 + slot) * S::M + r;
+          *reinterpret_cast<float4*>(p.part_o + at * D + c0 + c) = v;
+          if (c0 == 0 && c == 0) p.part_ml[at] = make_float2(mx, lt);
+        }
+      }
+      named_bar_sync(1, kAttnWarps * 32);
+    }
+    w.next(p);
+  }
+}
+
+template <class S>
+__global__ void __launch_bounds__(kAttnThreads, S::kTwo ? 2 : 1)
+aq_tree_attention_kernel(const __grid_constant__ AttnParams p) {
+  extern __shared__ uint8_t raw[];
+  __shared__ AttnShared sh;
+  uint8_t* stage0 = raw + ((1024 - (smem_u32(raw) & 1023)) & 1023);
+  uint8_t* scale0 = stage0 + p.stages * S::kStage;
+  float* join = reinterpret_cast<float*>(scale0 + p.stages * 2 * S::kScale);
+  if (threadIdx.x == 0) {
+    for (int i = 0; i < p.stages; ++i) {
+      mbar_init(&sh.full[i], 1);
+      mbar_init(&sh.empty[i], kAttnWarps);
+    }
+    sh.abort = 0;
+    fence_barrier_init();
+    tma_prefetch_desc(&p.tm_k);
+    tma_prefetch_desc(&p.tm_v);
+  }
+  pdl_wait_prior_grid();
+  int64_t range[2];
+  locate<S::M, S::KS>(p, sh, p.prefix, blockIdx.x == 0, range);
+  const AbortCtl ctl = {&sh.abort, p.status, p.timeout_ns};
+  if (threadIdx.x >= kAttnWarps * 32)
+    produce<S>(p, sh, stage0, scale0, range, p.stages, ctl);
+  else
+    consume<S>(p, sh, stage0, scale0, join, range, p.stages, ctl);
+  pdl_launch_dependents();
+}
+
+// Adds the partial sums of the items that were shared between CTAs, in the CTAs' order. One block per row and
+// query head: its four warps take every fourth part.
 template <int D>
-cudaError_t launch_attention(const AttnParams& p, bool e4m3, dim3 grid, cudaStream_t st) {
-  return e4m3 ? launch_serve(aq_tree_attention_kernel<D, true>, p, grid, 128, 0, st)
-              : launch_serve(aq_tree_attention_kernel<D, false>, p, grid, 128, 0, st);
+__global__ void __launch_bounds__(128) aq_attention_join_kernel(const __grid_constant__ AttnParams p) {
+  constexpr int N = D / 32;
+  __shared__ int b_of;
+  __shared__ float sm[4], sl[4], so[4][D];
+  const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+  const int heads = p.hk * p.group;
+  const int64_t row = blockIdx.x / heads;
+  const int head = static_cast<int>(blockIdx.x - row * heads);
+  if (tid == 0) b_of = -1;
+  __syncthreads();
+  pdl_wait_prior_grid();
+  pdl_launch_dependents();
+  for (int b = tid; b < p.batch; b += 128) {
+    const int c0 = p.cu[b], c1 = p.cu[b + 1];
+    if (c0 >= 0 && c0 <= row && row < c1 && row - c0 < p.max_q) b_of = b;
+  }
+  const int64_t total = p.prefix[p.batch * p.row_tiles];
+  __syncthreads();
+  const int b = b_of;
+  if (b < 0) return;
+  const int64_t r = (row - p.cu[b]) * p.group + head % p.group;
+  const int entry = b * p.row_tiles + static_cast<int>(r / p.rows_per_tile);
+  const int rr = static_cast<int>(r % p.rows_per_tile);
+  const int64_t first = p.prefix[entry], len = (p.prefix[entry + 1] - first) / p.hk;
+  const int64_t t0 = first + (head / p.group) * len, t1 = t0 + len;
+  const int64_t share = (total + p.main_grid - 1) / p.main_grid;
+  const int c0 = static_cast<int>(t0 / share), c1 = static_cast<int>((t1 - 1) / share);
+  if (c0 == c1) return;   // one CTA had it all
+  float m = -INFINITY, l = 0.0f, o[N];
+#pragma unroll
+  for (int e = 0; e < N; ++e) o[e] = 0.0f;
+  for (int c = c0 + warp; c <= c1; c += 4) {
+    const int64_t at = (static_cast<int64_t>(c) * 2 + (c > c0 ? 0 : 1)) * p.rows_per_tile + rr;
+    const float2 ml = p.part_ml[at];
+    const float mx = fmaxf(m, ml.x), mz = mx == -INFINITY ? 0.0f : mx;
+    const float a = ex2(m - mz), f = ex2(ml.x - mz);
+    const float* src = p.part_o + at * D + lane * N;
+#pragma unroll
+    for (int e = 0; e < N; ++e) o[e] = o[e] * a + src[e] * f;
+    l = l * a + ml.y * f;
+    m = mx;
+  }
+#pragma unroll
+  for (int e = 0; e < N; ++e) so[warp][lane * N + e] = o[e];
+  if (lane == 0) {
+    sm[warp] = m;
+    sl[warp] = l;
+  }
+  __syncthreads();
+  float mt = -INFINITY, lt = 0.0f, f[4];
+#pragma unroll
+  for (int k = 0; k < 4; ++k) mt = fmaxf(mt, sm[k]);
+  const float mz = mt == -INFINITY ? 0.0f : mt;
+#pragma unroll
+  for (int k = 0; k < 4; ++k) {
+    f[k] = ex2(sm[k] - mz);
+    lt += sl[k] * f[k];
+  }
+  const bool none = mt == -INFINITY && lt == 0.0f;
+  const float inv = none ? 0.0f : 1.0f / lt;
+  for (int d = tid; d < D; d += 128) {
+    float x = 0.0f;
+#pragma unroll
+    for (int k = 0; k < 4; ++k) x += so[k][d] * f[k];
+    p.o[row * p.o_tok + head * p.o_head + d] = f32_to_bf16_rn(none ? 0.0f : x * inv);
+  }
+  if (p.lse && tid == 0) p.lse[row * heads + head] = none ? -INFINITY : (mz + log2f(lt)) * 0.6931471805599453f;
+}
+
+// ---------------------------------------------------------------------------------
+// host
+// ---------------------------------------------------------------------------------
+// Rows of a tile: the fewest of 16, 32, 64 that hold a sequence's rows of one key/value head.
+int rows_per_tile(int64_t rows) { return rows <= 16 ? 16 : rows <= 32 ? 32 : 64; }
+
+struct AttnLayout {
+  int rows = 0, row_tiles = 0;
+  size_t part_o = 0, part_ml = 0, total = 0;   // prefix at 0
+};
+// Entries (sequences x row tiles) beyond this are refused: the prefix is scanned by every CTA.
+constexpr int64_t kAttnMaxEntries = 1 << 22;
+
+bool attn_layout(const aq_kv_cache* c, const aq_draft_batch* d, int32_t q_heads, AttnLayout* out) {
+  const int64_t rows = static_cast<int64_t>(d->max_q) * (q_heads / c->kv_heads);
+  AttnLayout l;
+  l.rows = rows_per_tile(rows);
+  const int64_t tiles = std::max<int64_t>((rows + l.rows - 1) / l.rows, 1);
+  if (tiles * d->batch > kAttnMaxEntries) return false;
+  l.row_tiles = static_cast<int>(tiles);
+  const int64_t ctas = kAttnSmsBound * kAttnMaxPerSm;
+  auto up = [](size_t v) { return (v + 255) / 256 * 256; };
+  l.part_ml = up((tiles * d->batch + 1) * 8);
+  l.part_o = up(l.part_ml + ctas * 2 * l.rows * 8);
+  l.total = up(l.part_o + static_cast<size_t>(ctas) * 2 * l.rows * c->head_dim * 4);
+  *out = l;
+  return true;
+}
+
+// Cache codes as {D, page, pages * heads}: boxes of one column block (128 bytes at most) of up to KS rows.
+aq_status cache_map(CUtensorMap* m, const void* base, const aq_kv_cache* c, int box_cols, int box_rows, const char* who) {
+  const bool e4m3 = c->type == AQ_KV_E4M3;
+  const cuuint64_t es = e4m3 ? 1 : 2, row = c->head_dim * es;
+  const cuuint64_t dims[3] = {static_cast<cuuint64_t>(c->head_dim), static_cast<cuuint64_t>(c->page_size),
+                              static_cast<cuuint64_t>(c->pages) * c->kv_heads};
+  const cuuint64_t strides[2] = {row, row * c->page_size};
+  const cuuint32_t box[3] = {static_cast<cuuint32_t>(box_cols), static_cast<cuuint32_t>(box_rows), 1};
+  const cuuint32_t unit[3] = {1, 1, 1};
+  const serve_encode_fn fn = serve_encode();
+  if (!fn) return serve_fail(AQ_ERR_CUDA, "%s: cuTensorMapEncodeTiled is not available from the driver", who);
+  const CUresult r = fn(m, e4m3 ? CU_TENSOR_MAP_DATA_TYPE_UINT8 : CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 3, const_cast<void*>(base),
+                        dims, strides, box, unit, CU_TENSOR_MAP_INTERLEAVE_NONE,
+                        box_cols * es == 128 ? CU_TENSOR_MAP_SWIZZLE_128B : CU_TENSOR_MAP_SWIZZLE_64B,
+                        CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
+  if (r != CUDA_SUCCESS) return serve_fail(AQ_ERR_CUDA, "%s: cuTensorMapEncodeTiled failed (%d)", who, static_cast<int>(r));
+  return AQ_OK;
+}
+
+template <class S>
+aq_status launch_attention(AttnParams& p, const aq_kv_cache* c, const ServeDev& dev, cudaStream_t st, const char* who) {
+  aq_status s;
+  const int box = std::min(c->page_size, S::KS);
+  if ((s = cache_map(&p.tm_k, c->k, c, S::RB / S::ES, box, who)) != AQ_OK) return s;
+  if ((s = cache_map(&p.tm_v, c->v, c, S::RB / S::ES, box, who)) != AQ_OK) return s;
+  constexpr size_t kStatic = (sizeof(AttnShared) + 127) / 128 * 128;
+  constexpr size_t kUnit = S::kStage + 2 * S::kScale;
+  constexpr bool two = S::kTwo;
+  const size_t room = (two ? (dev.smem_optin + 1024) / 2 - 1024 : dev.smem_optin) - kStatic - 1024 - S::kJoin;
+  p.stages = static_cast<int>(std::min<size_t>(room / kUnit, kAttnStages));
+  if (p.stages < 2) return serve_fail(AQ_ERR_UNSUPPORTED, "%s: the device has too little shared memory", who);
+  const size_t smem = 1024 + p.stages * kUnit + S::kJoin;
+  static std::atomic<uint64_t> ready{0};   // devices on which the kernel may use that much
+  const uint64_t bit = 1ull << dev.index;
+  if (!(ready.load() & bit)) {
+    const cudaError_t e = cudaFuncSetAttribute(aq_tree_attention_kernel<S>, cudaFuncAttributeMaxDynamicSharedMemorySize, static_cast<int>(smem));
+    if (e != cudaSuccess) return serve_launched(e, who);
+    ready.fetch_or(bit);
+  }
+  p.main_grid = std::min(dev.sms, kAttnSmsBound) * (two ? 2 : 1);
+  cudaError_t e = launch_serve(aq_tree_attention_kernel<S>, p, dim3(p.main_grid), kAttnThreads, smem, st);
+  if (e == cudaSuccess)
+    e = launch_serve(aq_attention_join_kernel<S::D>, p, dim3(static_cast<unsigned>(p.total_q * p.hk * p.group)), 128, 0, st);
+  return serve_launched(e, who);
+}
+
+template <int D, bool E4M3>
+aq_status launch_rows(AttnParams& p, const aq_kv_cache* c, const ServeDev& dev, cudaStream_t st, const char* who) {
+  switch (p.rows_per_tile) {
+    case 16: return launch_attention<Shape<D, E4M3, 1>>(p, c, dev, st, who);
+    case 32: return launch_attention<Shape<D, E4M3, 2>>(p, c, dev, st, who);
+    default: return launch_attention<Shape<D, E4M3, 4>>(p, c, dev, st, who);
+  }
 }
 
 aq_status check_batch(const aq_kv_cache* c, const aq_draft_batch* d, int32_t q_heads, const char* who) {
@@ -141,7 +982,13 @@ using namespace aq;
 
 extern "C" size_t aq_tree_attention_workspace_bytes(const aq_kv_cache* cache, const aq_draft_batch* batch, int32_t q_heads) {
   if (check_batch(cache, batch, q_heads, "aq_tree_attention_workspace_bytes") != AQ_OK) return static_cast<size_t>(-1);
-  return 0;
+  AttnLayout l;
+  if (batch->batch == 0 || batch->total_q == 0 || batch->max_q == 0) return 0;
+  if (!attn_layout(cache, batch, q_heads, &l)) {
+    serve_fail(AQ_ERR_SHAPE, "aq_tree_attention_workspace_bytes: batch * max_q is too large for one call");
+    return static_cast<size_t>(-1);
+  }
+  return l.total;
 }
 
 extern "C" aq_status aq_tree_attention(const aq_kv_cache* cache, const aq_draft_batch* batch, const void* q,
@@ -190,13 +1037,20 @@ extern "C" aq_status aq_tree_attention(const aq_kv_cache* cache, const aq_draft_
     for (const ByteSpan& in : ins)
       if (byte_overlap(outs[i], in)) return serve_fail(AQ_ERR_OVERLAP, "%s: an output overlaps an input", who);
   if (byte_overlap(outs[0], outs[1])) return serve_fail(AQ_ERR_OVERLAP, "%s: o and lse overlap", who);
-  (void)workspace;
-  (void)workspace_bytes;
+  AttnLayout l;
+  if (!attn_layout(cache, batch, q_heads, &l) || nq * q_heads > 0x7fffffffLL)
+    return serve_fail(AQ_ERR_SHAPE, "%s: batch * max_q is too large for one call", who);
+  if (!workspace || workspace_bytes < l.total || !serve_aligned(workspace, 256))
+    return serve_fail(AQ_ERR_WORKSPACE, "%s: workspace of %zu bytes (256-byte aligned) required, got %zu", who, l.total,
+                      workspace_bytes);
+  const ByteSpan ws = byte_span(workspace, 1, 0, static_cast<int64_t>(l.total), 1);
+  for (const ByteSpan& x : ins)
+    if (byte_overlap(ws, x)) return serve_fail(AQ_ERR_OVERLAP, "%s: workspace overlaps an input", who);
+  if (byte_overlap(ws, outs[0]) || byte_overlap(ws, outs[1]))
+    return serve_fail(AQ_ERR_OVERLAP, "%s: workspace overlaps an output", who);
   ServeDev dev;
   if ((st = serve_device(&dev)) != AQ_OK) return st;
   AttnParams p = {};
-  p.kc = static_cast<const uint8_t*>(cache->k);
-  p.vc = static_cast<const uint8_t*>(cache->v);
   p.ks = cache->k_scale;
   p.vs = cache->v_scale;
   p.pages = cache->pages;
@@ -223,11 +1077,17 @@ extern "C" aq_status aq_tree_attention(const aq_kv_cache* cache, const aq_draft_
   p.window = d.window;
   p.total_q = nq;
   p.scale = scale;
-  const dim3 grid(static_cast<unsigned>(nq), q_heads);
+  uint8_t* base = static_cast<uint8_t*>(workspace);
+  p.rows_per_tile = l.rows;
+  p.row_tiles = l.row_tiles;
+  p.prefix = reinterpret_cast<int64_t*>(base);
+  p.part_ml = reinterpret_cast<float2*>(base + l.part_ml);
+  p.part_o = reinterpret_cast<float*>(base + l.part_o);
+  p.status = dev.status;
+  p.timeout_ns = kServeTimeoutNs;
   const bool e4m3 = cache->type == AQ_KV_E4M3;
   const cudaStream_t cs = static_cast<cudaStream_t>(stream);
-  const cudaError_t e = D == 64    ? launch_attention<64>(p, e4m3, grid, cs)
-                        : D == 128 ? launch_attention<128>(p, e4m3, grid, cs)
-                                   : launch_attention<256>(p, e4m3, grid, cs);
-  return serve_launched(e, who);
+  if (D == 64) return e4m3 ? launch_rows<64, true>(p, cache, dev, cs, who) : launch_rows<64, false>(p, cache, dev, cs, who);
+  if (D == 128) return e4m3 ? launch_rows<128, true>(p, cache, dev, cs, who) : launch_rows<128, false>(p, cache, dev, cs, who);
+  return e4m3 ? launch_rows<256, true>(p, cache, dev, cs, who) : launch_rows<256, false>(p, cache, dev, cs, who);
 }

@@ -47,11 +47,28 @@ aq_status serve_device(ServeDev* out) {
     if (major != 10 || minor != 3)
       return serve_fail(AQ_ERR_UNSUPPORTED, "device %d is sm_%d%d; this library is built for sm_103a (GB300)", dev,
                         major, minor);
+    int32_t* status = device_status_ptr(dev, &e);
+    if (e != cudaSuccess) return serve_launched(e, "cudaGetSymbolAddress(status)");
+    d.index = dev;
+    d.status = status;
     d.smem_optin = static_cast<size_t>(smem);
     d.sms = sms;
   }
   *out = d;
   return AQ_OK;
+}
+
+serve_encode_fn serve_encode() {
+  static serve_encode_fn fn = nullptr;
+  static std::once_flag once;
+  std::call_once(once, [] {
+    void* p = nullptr;
+    cudaDriverEntryPointQueryResult q;
+    if (cudaGetDriverEntryPointByVersion("cuTensorMapEncodeTiled", &p, 12000, cudaEnableDefault, &q) == cudaSuccess &&
+        q == cudaDriverEntryPointSuccess)
+      fn = reinterpret_cast<serve_encode_fn>(p);
+  });
+  return fn;
 }
 
 aq_status check_kv_cache(const aq_kv_cache* c, const char* who) {

@@ -20,12 +20,20 @@ constexpr float kE4m3Max = 448.0f;
 // needs no case of its own (codes 0).
 constexpr float kKvScaleFloor = 0x1p-100f;
 
+constexpr uint64_t kServeTimeoutNs = 1000ull * 1000 * 1000;   // limit of one in-kernel wait: 1 s
+
 struct ServeDev {
-  int sms = 0;
+  int index = 0, sms = 0;
   size_t smem_optin = 0;
+  int32_t* status = nullptr;   // device status word
 };
 // Facts of the current device, queried once; refuses any device but sm_103.
 aq_status serve_device(ServeDev* out);
+// The driver's tensor-map encoder, or NULL.
+typedef CUresult (*serve_encode_fn)(CUtensorMap*, CUtensorMapDataType, cuuint32_t, void*, const cuuint64_t*,
+                                    const cuuint64_t*, const cuuint32_t*, const cuuint32_t*, CUtensorMapInterleave,
+                                    CUtensorMapSwizzle, CUtensorMapL2promotion, CUtensorMapFloatOOBfill);
+serve_encode_fn serve_encode();
 
 inline aq_status serve_fail(aq_status st, const char* fmt, ...) {
   char buf[512];

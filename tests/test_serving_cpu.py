@@ -195,4 +195,4 @@ def test_binding_checks_types_before_pointers():
     with pytest.raises(ValueError):
         b.aq_kv_write(kv, x[:, :1].bfloat16(), x.bfloat16(), torch.zeros(3, dtype=torch.int64))
     with pytest.raises(ValueError):
-        b.KvCache(kv.k[:, :1], kv.v, kv.k_scale, kv.v_scale).c()
+        b.KvCache(kv.k[:, :1], kv.v, kv.k_scale, kv.v_scale).packed()
