@@ -471,9 +471,9 @@ aq_status aq_kv_read(const aq_kv_cache* cache, const int64_t* slots, int64_t T, 
  *   mask NULL    those with j <= i (a chain; one token is the plain decode step, many a prefill chunk)
  * window > 0 leaves out keys whose position lies `window` or more before the row's.
  * A row that sees nothing (or whose scores are all minus infinity) gives zeros and lse = -inf. Masked
- * keys and values take no part, whatever they hold. Softmax and sums are held in fp32; bf16 weights
- * with a bf16 cache; with E4M3, queries and weights as two E4M3 terms each (8 bits, and nothing below 2^-18
- * of the largest of a head's elements or of a tile's weights).
+ * keys and values take no part, whatever they hold. Softmax and sums are held in fp32. With a bf16 cache
+ * the weights enter the second product in bf16; with E4M3 they and the queries enter as f16, scaled by
+ * powers of two (query elements below 2^-28 of their head's largest, and weights below 2^-38, lose bits).
  *   lse  fp32 [total_q, q_heads], log of the sum of exp(score), or NULL
  * Left out: keys past pages_per_seq pages, keys in pages outside the cache, rows past max_q of a
  * sequence or outside [0, total_q). Needs head_dim 64, 128 or 256 (AQ_ERR_UNSUPPORTED otherwise).

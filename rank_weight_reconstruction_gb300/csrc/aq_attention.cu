@@ -15,18 +15,18 @@
 // once per item. The products are mma.sync: at 1 to 64 rows a byte of cache meets few rows, the kernel is
 // bound by HBM, and the rows would fill a small part of a 128-lane tcgen05 accumulator.
 //
-// E4M3 caches stay E4M3 down to the matrix instruction (measured here: mma.sync e4m3 2286 TFLOP/s against 607
-// for bf16, both with fp32 sums exact to 24 bits; converting codes to bf16 first costs more than the
-// products). A bf16 query has 8 significant bits, an E4M3 code 4: with a row scaled by a power of two to
-// [128, 256), q = q1 + q2 in E4M3, exact down to 2^-18 of the row's largest element, and q . k takes two
-// products. The weights go the same way: per 32 or 64 keys, w_j = p_j * vscale_j is scaled by a power of two
-// against the row's largest and split in two codes, the product starts from zero and joins the running sum
-// with its factor in fp32, so what a weight loses is 2^-9 of itself or 2^-18 of the largest beside it.
-// With a bf16 cache the weights are rounded to bf16 (2^-9) against the running maximum.
+// E4M3 codes become halves on their way into the registers (exact; mma.sync on E4M3 operands is no
+// shortcut: it is carried out as the same conversions and f16 products, repeated for every use of a
+// fragment). A query row is scaled by a power of two to [2^14, 2^15), so that its bf16 elements are exact in f16 down to
+// 2^-28 of the largest; keys' scales multiply the scores. The weights against the running maximum, times the
+// values' scales against the largest of them so far (a power of two), fill the range of f16 from 2^15 down to
+// 2^-24: 11 bits each, and nothing below 2^-38 of the largest is kept. With a bf16 cache the weights are
+// rounded to bf16 (2^-9).
 #include <math.h>
 
 #include <algorithm>
 #include <atomic>
+#include <type_traits>
 
 #include "aq_serve.h"
 
@@ -85,11 +85,28 @@ __device__ __forceinline__ void mma_bf16(float (&d)[4], const uint32_t (&a)[4], 
                : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3])
                : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
 }
-__device__ __forceinline__ void mma_e4m3(float (&d)[4], const uint32_t (&a)[4], uint32_t b0, uint32_t b1) {
-  asm volatile("mma.sync.aligned.m16n8k32.row.col.f32.e4m3.e4m3.f32 {%0, %1, %2, %3}, {%4, %5, %6, %7}, {%8, %9}, "
+__device__ __forceinline__ void mma_f16(float (&d)[4], const uint32_t (&a)[4], uint32_t b0, uint32_t b1) {
+  asm volatile("mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0, %1, %2, %3}, {%4, %5, %6, %7}, {%8, %9}, "
                "{%0, %1, %2, %3};"
                : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3])
                : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
+}
+// Four E4M3 codes to two pairs of halves.
+__device__ __forceinline__ void widen(uint32_t c, uint32_t& lo, uint32_t& hi) {
+  asm("{\n .reg .b16 l, h;\n mov.b32 {l, h}, %2;\n cvt.rn.f16x2.e4m3x2 %0, l;\n cvt.rn.f16x2.e4m3x2 %1, h;\n}"
+      : "=r"(lo), "=r"(hi)
+      : "r"(c));
+}
+__device__ __forceinline__ uint32_t pack_f16x2(float lo, float hi) {
+  uint32_t r;
+  asm("cvt.rn.f16x2.f32 %0, %1, %2;" : "=r"(r) : "f"(hi), "f"(lo));
+  return r;
+}
+// Transposes an 8 x 8 matrix of 16-bit elements held one row pair a lane.
+__device__ __forceinline__ uint32_t transpose8(uint32_t x) {
+  uint32_t r;
+  asm volatile("movmatrix.sync.aligned.m8n8.trans.b16 %0, %1;" : "=r"(r) : "r"(x));
+  return r;
 }
 __device__ __forceinline__ float ex2(float x) {
   float r;
@@ -102,49 +119,54 @@ __device__ __forceinline__ void bulk_load(void* dst, const void* src, uint32_t b
                "l"(src), "r"(bytes), "r"(smem_u32(bar))
                : "memory");
 }
-// Two fp32 values as two E4M3 terms each: hi, then what it leaves (|x| <= 448).
-__device__ __forceinline__ void split_e4m3(float x, float y, uint16_t& hi, uint16_t& lo) {
-  hi = e4m3x2_from_f32(x, y);
-  const uint32_t back = f16x2_from_e4m3x2(hi);
-  const float2 b = __half22float2(*reinterpret_cast<const __half2*>(&back));
-  lo = e4m3x2_from_f32(x - b.x, y - b.y);
-}
 // 2^e for e in [-126, 127].
 __device__ __forceinline__ float pow2(int e) { return __int_as_float((e + 127) << 23); }
-// Exponent of the largest magnitude, for scaling to [128, 256); zero and subnormals count as 2^-119.
-__device__ __forceinline__ int top_exponent(float x) { return max(static_cast<int>(__float_as_uint(x) >> 23) - 127, -119); }
+// Exponent of a non-negative value, kept where 2^(14 - e) and 2^(e - 14) are finite; zero counts as 2^-112.
+__device__ __forceinline__ int top_exponent(float x) { return min(max(static_cast<int>(__float_as_uint(x) >> 23) - 127, -112), 126); }
 
 constexpr int kAttnStages = 6;          // most stages of the ring
-constexpr int kAttnWarps = 4;           // consumer warps
-constexpr int kAttnThreads = (kAttnWarps + 1) * 32;
+constexpr int kAttnMaxWarps = 8;        // most consumer warps
+constexpr int kAttnMaxRows = 64;        // rows of the largest tile
 constexpr int kAttnSmsBound = 192;      // SMs (of any sm_103 part) and CTAs an SM, for sizing the
 constexpr int kAttnMaxPerSm = 2;        // workspace without a device
+// The maximum that weights are taken against may lag by this power of two before the sums are scaled over.
+constexpr float kLag = 6.0f;
+// Weights times values' scales in f16 stay below 2^(kLag + 1 + kTop) <= 2^15.
+constexpr int kTop = 8;
 
 // ---------------------------------------------------------------------------------
-// shapes: D elements a head, RG row groups of 16 rows, KG key groups, CK keys a warp takes at a time
+// shapes: D elements a head; a warp takes 8 NR rows against CK keys at a time; NW warps are RG row groups by
+// KG key groups. Keys are the matrix instruction's 16 lanes and rows its 8 columns, in both products: S^T = K Q^T
+// and O^T = V^T P^T. So 1 to 8 rows (a single token's group of query heads) cost half of what they would as the
+// 16 lanes, and a fragment of the cache, converted once, meets all rows of the warp.
 // ---------------------------------------------------------------------------------
-template <int D_, bool E4M3_, int RG_>
+template <int D_, bool E4M3_, int NR_, int RG_, int NW_, int PER_SM_>
 struct Shape {
   static constexpr int D = D_;
   static constexpr bool E4M3 = E4M3_;
-  static constexpr int RG = RG_, KG = kAttnWarps / RG_;
-  static constexpr int M = 16 * RG;
+  static constexpr int NR = NR_, RG = RG_, NW = NW_, KG = NW_ / RG_;
+  static constexpr int kPerSm = PER_SM_;
+  // eight consumer warps take the registers of the producer's warpgroup, of which one warp works
+  static constexpr bool kSplitRegs = NW == 8;
+  static constexpr int kThreads = (NW + (kSplitRegs ? 4 : 1)) * 32;
+  static constexpr int M = 8 * NR * RG;                    // rows of a tile
   static constexpr int ES = E4M3 ? 1 : 2;
-  // E4M3 products take 32 keys at once; more keys a step mean fewer joins of the partial product, as far
-  // as registers go. A stage holds 16 to 64 KB.
-  static constexpr int CK = E4M3 ? (RG == 1 || D == 256 ? 32 : 64) : (RG == 1 && D >= 128 ? 16 : 32);
-  static constexpr int NI = (E4M3 && D == 64 && RG != 2) || (RG == 4 && D * ES < 512) ? 2 : 1;
-  static constexpr int KS = CK * KG * NI;
+  // 16 KB to 64 KB a stage, so that three fit a CTA's share of shared memory
+  static constexpr int CK = (E4M3 ? D * KG * kPerSm >= 2048 : D * KG >= 512) ? 16 : 32;
+  static constexpr int KT = CK / 16;
+  static constexpr int NI = CK * KG * D * ES >= 16384 || CK * KG >= 128 ? 1 : 2;
+  static constexpr int KS = CK * KG * NI;                  // keys of a stage
   static constexpr int RB = D * ES < 128 ? D * ES : 128;   // bytes of a row of one column block
-  static constexpr int NC = D * ES / RB;
   static constexpr int kCode = KS * D * ES;                // bytes of K (or V) in a stage
+  static constexpr int NC = D * ES / RB;
   static constexpr int kStage = 2 * kCode;
   static constexpr int kScale = E4M3 ? KS * 4 : 0;         // bytes of K's (or V's) scales in a stage
-  // two CTAs an SM where the registers and three stages in half its shared memory allow
-  static constexpr bool kTwo = D < 256 && kStage <= 32 * 1024;
-  static constexpr int kCols = 64;                         // columns joined at a time
+  static constexpr int kQ = M * D * 2;                     // queries, in the order of fragments
+  static constexpr bool kQRegs = NR * D <= 256;            // ... and in registers
+  static constexpr int kCols = 32;   // columns joined at a time
   static constexpr int kJoinLd = kCols + 4;
-  static constexpr int kJoin = kAttnWarps * 16 * kJoinLd * 4;
+  static constexpr int kJoin = NW * 8 * NR * kJoinLd * 4;
+  static_assert(kJoin >= kThreads * 8 && M <= kAttnMaxRows && 8 * NR <= 32, "shared arrays");
 };
 
 struct AttnShared {
@@ -152,8 +174,10 @@ struct AttnShared {
   uint32_t valid[kAttnStages];
   int32_t abort;
   int64_t start_entry, start_tile;      // where this CTA begins: entry, tile within it
-  int64_t part[kAttnThreads];
-  float m[kAttnWarps][16], l[kAttnWarps][16];
+  float m[kAttnMaxWarps][32], l[kAttnMaxWarps][32];
+  float fac[kAttnMaxRows];                       // of a row's raw products, to base-2 logits; not negative
+  int64_t pos[kAttnMaxRows];                  // of a row
+  int32_t i[kAttnMaxRows];                     // its drafted index
 };
 
 // Keys [lo, hi) and tiles [t0, t1) that the rows of entry (sequence b, row tile rt) can see.
@@ -183,24 +207,26 @@ __device__ __forceinline__ Span entry_span(const AttnParams& p, int b, int rt) {
   return s;
 }
 
-// Where tile number `at` of the whole call lies; called by every thread, the answer in sh. CTA 0 also leaves
+// Where tile number `at` of the whole call lies; called by every thread, the answer in sh; `part` holds
+// a number for each thread. CTA 0 also leaves
 // the entries' first tiles for the joining launch.
 template <int M, int KS>
-__device__ __forceinline__ void locate(const AttnParams& p, AttnShared& sh, int64_t* prefix, bool write,
+__device__ __forceinline__ void locate(const AttnParams& p, AttnShared& sh, int64_t* part, int64_t* prefix, bool write,
                                           int64_t (&range)[2]) {
   const int n = p.batch * p.row_tiles, tid = threadIdx.x;
-  const int per = (n + kAttnThreads - 1) / kAttnThreads;
+  const int threads = blockDim.x;
+  const int per = (n + threads - 1) / threads;
   const int e0 = min(tid * per, n), e1 = min(e0 + per, n);
   int64_t sum = 0;
   for (int e = e0; e < e1; ++e) {
     const Span s = entry_span<M, KS>(p, e / p.row_tiles, e % p.row_tiles);
     sum += static_cast<int64_t>(s.t1 - s.t0) * p.hk;
   }
-  sh.part[tid] = sum;
+  part[tid] = sum;
   __syncthreads();
   int64_t before = 0, total = 0;
-  for (int i = 0; i < kAttnThreads; ++i) {
-    const int64_t v = sh.part[i];
+  for (int i = 0; i < threads; ++i) {
+    const int64_t v = part[i];
     before += i < tid ? v : 0;
     total += v;
   }
@@ -341,83 +367,6 @@ __device__ __forceinline__ void produce(const AttnParams& p, AttnShared& sh, uin
   }
 }
 
-// What a thread holds of its warp's 16 rows: rows g and g + 8 (g = lane / 4).
-template <class S>
-struct Rows {
-  static constexpr int NK = S::D * S::ES / 32;            // 32-byte steps of a row
-  static constexpr int NQ = S::E4M3 ? 2 : 1;
-  uint32_t q[NQ][NK][4];
-  float fac[2];                                           // of the raw products, to base-2 logits
-  int64_t pos[2];
-  int64_t top;                                            // largest position of the warp's rows
-  const uint64_t* mask[2];
-  int i[2];
-  __device__ __forceinline__ void load(const AttnParams& p, const Span& s, int head, int rt, int rg) {
-    const int lane = threadIdx.x & 31, g = lane >> 2, t = lane & 3;
-    const float scale2 = p.scale * 1.4426950408889634f;
-    const bool dep = p.mask && p.depth;
-#pragma unroll
-    for (int h = 0; h < 2; ++h) {
-      const int64_t r = static_cast<int64_t>(rt) * S::M + rg * 16 + g + 8 * h;
-      const bool live = r < static_cast<int64_t>(s.T) * p.group;
-      const int64_t rr = live ? r : 0;
-      i[h] = static_cast<int>(rr / p.group);
-      const int64_t row = s.first + i[h];
-      const uint16_t* src = p.q + row * p.q_tok + (head * p.group + static_cast<int>(rr - static_cast<int64_t>(i[h]) * p.group)) * p.q_head;
-      pos[h] = static_cast<int64_t>(s.ctx) + (dep ? max(p.depth[row], 0) : i[h]);
-      mask[h] = p.mask ? p.mask + row * p.ld_mask : nullptr;
-      if (S::E4M3) {
-        float amax = 0.0f;
-        bool finite = true;
-#pragma unroll
-        for (int k = 0; k < NK; ++k)
-#pragma unroll
-          for (int c = 0; c < 2; ++c) {
-            const uint2 v = live ? *reinterpret_cast<const uint2*>(src + k * 32 + c * 16 + t * 4) : make_uint2(0, 0);
-            const float x[4] = {__uint_as_float(v.x << 16), __uint_as_float(v.x & 0xffff0000u),
-                                __uint_as_float(v.y << 16), __uint_as_float(v.y & 0xffff0000u)};
-#pragma unroll
-            for (int e = 0; e < 4; ++e) {
-              amax = fmaxf(amax, fabsf(x[e]));
-              finite = finite && isfinite(x[e]);
-            }
-            q[0][k][h + 2 * c] = v.x;
-            q[NQ - 1][k][h + 2 * c] = v.y;
-          }
-        amax = fmaxf(amax, __shfl_xor_sync(0xffffffffu, amax, 1));
-        amax = fmaxf(amax, __shfl_xor_sync(0xffffffffu, amax, 2));
-        const unsigned bad = __ballot_sync(0xffffffffu, !finite);
-        finite = ((bad >> (lane & ~3)) & 15u) == 0;
-        const int e = finite ? top_exponent(amax) : 0;
-        const float f = pow2(7 - e);
-        // a row that holds an infinity or a NaN has no finite score
-        fac[h] = finite ? pow2(e - 7) * scale2 : __uint_as_float(0x7fc00000u);
-#pragma unroll
-        for (int k = 0; k < NK; ++k)
-#pragma unroll
-          for (int c = 0; c < 2; ++c) {
-            const uint32_t a = finite ? q[0][k][h + 2 * c] : 0u, b = finite ? q[NQ - 1][k][h + 2 * c] : 0u;
-            uint16_t h0, l0, h1, l1;
-            split_e4m3(__uint_as_float(a << 16) * f, __uint_as_float(a & 0xffff0000u) * f, h0, l0);
-            split_e4m3(__uint_as_float(b << 16) * f, __uint_as_float(b & 0xffff0000u) * f, h1, l1);
-            q[0][k][h + 2 * c] = h0 | (static_cast<uint32_t>(h1) << 16);
-            q[NQ - 1][k][h + 2 * c] = l0 | (static_cast<uint32_t>(l1) << 16);
-          }
-      } else {
-        fac[h] = scale2;
-#pragma unroll
-        for (int k = 0; k < NK; ++k)
-#pragma unroll
-          for (int c = 0; c < 2; ++c)
-            q[0][k][h + 2 * c] = live ? *reinterpret_cast<const uint32_t*>(src + k * 16 + c * 8 + t * 2) : 0u;
-      }
-    }
-    top = max(pos[0], pos[1]);
-#pragma unroll
-    for (int o = 16; o > 0; o >>= 1) top = max(top, __shfl_xor_sync(0xffffffffu, top, o));
-  }
-};
-
 // Shared-memory address of 16 bytes of a key: column block x / (RB / 16), swizzled as TMA writes it.
 template <class S>
 __device__ __forceinline__ uint32_t cell_addr(uint32_t base, int key, int x) {
@@ -427,266 +376,397 @@ __device__ __forceinline__ uint32_t cell_addr(uint32_t base, int key, int x) {
   return base + c * S::KS * S::RB + key * S::RB + ((xi ^ sw) << 4);
 }
 
+// Loads the item's queries into shared memory in the order of B fragments, uint2 [D / 16][M][4]: bf16 elements
+// 16 k + 2 t + {0, 1} and 8 more; for E4M3 keys f16 elements 16 k + 4 t + {0, 1, 2, 3} (the order in which a key's
+// codes are loaded), scaled by the row's power of two. The sign of the logits' scale goes into them.
 template <class S>
-__device__ __forceinline__ bool visible(const AttnParams& p, const Span& s, const Rows<S>& rw, int h, int64_t key,
+__device__ __forceinline__ void load_queries(const AttnParams& p, AttnShared& sh, uint2* qs, const Span& s, int head, int rt) {
+  const int tid = threadIdx.x, lane = tid & 31;
+  const float scale2 = p.scale * 1.4426950408889634f;
+  const uint32_t sign = scale2 < 0.0f ? 0x80008000u : 0u;
+  const bool dep = p.mask && p.depth;
+  constexpr int L = S::D / 8;                  // lanes a row, 16 bytes each: 8, 16 or 32
+  constexpr int RPW = 32 / L;
+  for (int r = (tid >> 5) * RPW + lane / L; r < S::M; r += S::NW * RPW) {   // M is a multiple of NW * RPW or less than it
+    const int64_t rr = static_cast<int64_t>(rt) * S::M + r;
+    const bool live = rr < static_cast<int64_t>(s.T) * p.group;
+    const int i = live ? static_cast<int>(rr / p.group) : 0;
+    const int64_t row = static_cast<int64_t>(s.first) + i;
+    const int c = lane % L;                    // elements 8 c .. 8 c + 7
+    uint4 v = make_uint4(0, 0, 0, 0);
+    if (live)
+      v = *reinterpret_cast<const uint4*>(p.q + row * p.q_tok + (head * p.group + static_cast<int>(rr - static_cast<int64_t>(i) * p.group)) * p.q_head + c * 8);
+    float fac = fabsf(scale2);
+    uint32_t x[4] = {v.x ^ sign, v.y ^ sign, v.z ^ sign, v.w ^ sign};
+    if constexpr (S::E4M3) {
+      uint32_t top = 0;
+#pragma unroll
+      for (int e = 0; e < 4; ++e) top = max(top, max((x[e] << 16) & 0x7fff0000u, x[e] & 0x7fff0000u));
+      const uint32_t group = (L == 32 ? 0xffffffffu : (1u << L) - 1) << (lane & ~(L - 1));
+#pragma unroll
+      for (int o = L / 2; o > 0; o >>= 1) top = max(top, __shfl_xor_sync(group, top, o));
+      const bool finite = top < 0x7f800000u;
+      const int e = finite ? top_exponent(__uint_as_float(top)) : 0;
+      const float f = pow2(14 - e);
+      fac = finite ? pow2(e - 14) * fac : __uint_as_float(0x7fc00000u);   // a row with an infinity or a NaN has no finite score
+#pragma unroll
+      for (int k = 0; k < 4; ++k)
+        x[k] = finite ? pack_f16x2(__uint_as_float(x[k] << 16) * f, __uint_as_float(x[k] & 0xffff0000u) * f) : 0u;
+      uint2* dst = qs + ((c >> 1) * S::M + r) * 4 + (c & 1) * 2;
+      dst[0] = make_uint2(x[0], x[1]);
+      dst[1] = make_uint2(x[2], x[3]);
+    } else {
+      uint32_t* dst = reinterpret_cast<uint32_t*>(qs + ((c >> 1) * S::M + r) * 4) + (c & 1);
+#pragma unroll
+      for (int k = 0; k < 4; ++k) dst[2 * k] = x[k];
+    }
+    if (c == 0) {
+      sh.fac[r] = fac;
+      sh.i[r] = i;
+      sh.pos[r] = static_cast<int64_t>(s.ctx) + (dep ? max(p.depth[row], 0) : i);
+    }
+  }
+}
+
+// Whether row r of the tile sees a key.
+template <class S>
+__device__ __forceinline__ bool visible(const AttnParams& p, const AttnShared& sh, const Span& s, int r, int64_t key,
                                         uint32_t pages, int box_shift, int in_tile) {
   if (key >= s.hi || !((pages >> (in_tile >> box_shift)) & 1)) return false;
   const int64_t t = key - s.ctx;
   int64_t at = key;
   if (t >= 0) {
-    if (rw.mask[h]) {
-      if (!((rw.mask[h][t >> 6] >> (t & 63)) & 1)) return false;
+    const int i = sh.i[r];
+    if (p.mask) {
+      if (!((p.mask[(static_cast<int64_t>(s.first) + i) * p.ld_mask + (t >> 6)] >> (t & 63)) & 1)) return false;
       if (p.window > 0 && p.depth) at = static_cast<int64_t>(s.ctx) + max(p.depth[s.first + t], 0);
-    } else if (t > rw.i[h]) {
+    } else if (t > i) {
       return false;
     }
   }
-  return p.window <= 0 || rw.pos[h] - at < p.window;
+  return p.window <= 0 || sh.pos[r] - at < p.window;
+}
+
+// A warp's sums for its rows 2 t + {0, 1} of each of NR groups of eight.
+template <class S>
+struct Sums {
+  // o[x][n]: O^T fragment, lanes the columns: E4M3 16 x + 2 g + {0: first half, 1: second}, bf16 16 x + g + {0, 8}
+  float o[S::D / 16][S::NR][4];
+  float m[S::NR][2], l[S::NR][2];
+  int ve;   // E4M3: o holds sums of w 2^(kTop - ve)
+};
+
+// Adds the infinities and NaN among a step's values to the rows that see them (weights in w [row][key], -1: masked).
+template <class S>
+__device__ __forceinline__ void reach_rows(Sums<S>& a, const float* w, uint32_t vb, int k0) {
+  const int lane = threadIdx.x & 31, g = lane >> 2, t = lane & 3;
+#pragma unroll 1
+  for (int k = 0; k < S::CK; ++k) {
+#pragma unroll
+    for (int x = 0; x < S::D / 16; ++x)
+#pragma unroll
+      for (int h = 0; h < 2; ++h) {
+        const int d = S::E4M3 ? 16 * x + 2 * g + h : 16 * x + g + 8 * h;
+        const uint32_t addr = cell_addr<S>(vb, k0 + k, d * S::ES / 16) + d * S::ES % 16;
+        uint32_t v;
+        bool special;
+        if (S::E4M3) {
+          asm volatile("ld.shared.u8 %0, [%1];" : "=r"(v) : "r"(addr) : "memory");
+          special = (v & 0x7f) == 0x7f;
+          v = 0x7fc00000u;
+        } else {
+          asm volatile("ld.shared.u16 %0, [%1];" : "=r"(v) : "r"(addr) : "memory");
+          special = (v & 0x7f80) == 0x7f80;
+          v <<= 16;
+        }
+        if (special) {
+#pragma unroll
+          for (int n = 0; n < S::NR; ++n)
+#pragma unroll
+            for (int c = 0; c < 2; ++c) {
+              const float q = w[(8 * n + 2 * t + c) * S::kJoinLd + k];
+              if (q >= 0.0f) a.o[x][n][2 * h + c] += q * __uint_as_float(v);
+            }
+        }
+      }
+  }
+}
+
+struct StepInfo {          // what a step that not every row sees in full needs besides
+  uint32_t pages;
+  int box_shift;
+  int64_t key0;            // first key of the tile
+  int rg;
+};
+
+// CK keys, the first being key k0 of the stage, against the warp's rows. WHOLE: every row sees every key.
+template <class S, bool WHOLE>
+__device__ __forceinline__ void step(const AttnParams& p, const AttnShared& sh, const Span& span, const StepInfo& info, Sums<S>& a,
+                                     const uint2* qs, const uint2 (&qr)[S::kQRegs ? S::D / 16 : 1][S::NR], uint32_t kb,
+                                     uint32_t vb, const float* ksc, const float* vsc, float* mine, int k0,
+                                     const float (&fac)[S::NR][2]) {
+  constexpr int D = S::D, NR = S::NR, KT = S::KT;
+  const int lane = threadIdx.x & 31, g = lane >> 2, t = lane & 3;
+  // scores, in the units of fac: sc[j][n]: keys 16 j + g + {0, 8}, rows 8 n + 2 t + {0, 1}
+  float sc[KT][NR][4];
+#pragma unroll
+  for (int j = 0; j < KT; ++j)
+#pragma unroll
+    for (int n = 0; n < NR; ++n) sc[j][n][0] = sc[j][n][1] = sc[j][n][2] = sc[j][n][3] = 0.0f;
+  auto query = [&](int k, int n) { return S::kQRegs ? qr[S::kQRegs ? k : 0][n] : qs[(k * S::M + 8 * n + g) * 4 + t]; };
+  if constexpr (S::E4M3) {
+#pragma unroll
+    for (int k = 0; k < D / 16; k += 2)
+#pragma unroll
+      for (int j = 0; j < KT; ++j) {
+        uint32_t r[4];   // keys 0-7 and 8-15 of columns k, then of columns k + 1
+        ldsm4(r, cell_addr<S>(kb, k0 + 16 * j + (lane & 15), k + (lane >> 4)));
+#pragma unroll
+        for (int i = 0; i < 2; ++i) {
+          uint32_t f[4];
+          widen(r[2 * i], f[0], f[2]);
+          widen(r[2 * i + 1], f[1], f[3]);
+#pragma unroll
+          for (int n = 0; n < NR; ++n) {
+            const uint2 b = query(k + i, n);
+            mma_f16(sc[j][n], f, b.x, b.y);
+          }
+        }
+      }
+  } else {
+#pragma unroll
+    for (int k = 0; k < D / 16; ++k)
+#pragma unroll
+      for (int j = 0; j < KT; ++j) {
+        uint32_t f[4];
+        ldsm4(f, cell_addr<S>(kb, k0 + 16 * j + (lane & 15), 2 * k + (lane >> 4)));
+#pragma unroll
+        for (int n = 0; n < NR; ++n) {
+          const uint2 b = query(k, n);
+          mma_bf16(sc[j][n], f, b.x, b.y);
+        }
+      }
+  }
+  float vs[KT][2], vmax = 0.0f;
+  if constexpr (S::E4M3) {
+#pragma unroll
+    for (int j = 0; j < KT; ++j)
+#pragma unroll
+      for (int h = 0; h < 2; ++h) {
+        const float ks = ksc[k0 + 16 * j + 8 * h + g];
+        vs[j][h] = vsc[k0 + 16 * j + 8 * h + g];
+        if (WHOLE) vmax = fmaxf(vmax, vs[j][h]);
+#pragma unroll
+        for (int n = 0; n < NR; ++n) {
+          sc[j][n][2 * h] *= ks;
+          sc[j][n][2 * h + 1] *= ks;
+        }
+      }
+  }
+  if constexpr (!WHOLE) {
+#pragma unroll
+    for (int j = 0; j < KT; ++j)
+#pragma unroll
+      for (int n = 0; n < NR; ++n)
+#pragma unroll
+        for (int c = 0; c < 4; ++c) {
+          const int in_tile = k0 + 16 * j + 8 * (c >> 1) + g;
+          const bool see = visible<S>(p, sh, span, info.rg * 8 * NR + 8 * n + 2 * t + (c & 1), info.key0 + in_tile, info.pages,
+                                      info.box_shift, in_tile);
+          if (!see) sc[j][n][c] = -INFINITY;
+          else if (S::E4M3) vmax = fmaxf(vmax, vs[j][c >> 1]);
+        }
+  }
+  // the maxima: looked at by each lane for itself, put together only where one is passed
+  float mt[NR][2];
+  bool grown = false;
+#pragma unroll
+  for (int n = 0; n < NR; ++n)
+#pragma unroll
+    for (int c = 0; c < 2; ++c) {
+      float x = fmaxf(sc[0][n][c], sc[0][n][2 + c]);
+#pragma unroll
+      for (int j = 1; j < KT; ++j) x = fmaxf(x, fmaxf(sc[j][n][c], sc[j][n][2 + c]));
+      mt[n][c] = x == -INFINITY ? x : x * fac[n][c];
+      grown = grown || mt[n][c] > a.m[n][c] + kLag;
+    }
+  if (S::E4M3) grown = grown || top_exponent(vmax) > a.ve;
+  if (__any_sync(0xffffffffu, grown)) {
+    float turn = 1.0f;
+    if constexpr (S::E4M3) {
+#pragma unroll
+      for (int off = 1; off < 32; off *= 2) vmax = fmaxf(vmax, __shfl_xor_sync(0xffffffffu, vmax, off));
+      const int e = max(a.ve, top_exponent(vmax));
+      turn = ex2(static_cast<float>(a.ve - e));
+      a.ve = e;
+    }
+#pragma unroll
+    for (int n = 0; n < NR; ++n)
+#pragma unroll
+      for (int c = 0; c < 2; ++c) {
+#pragma unroll
+        for (int off = 4; off < 32; off *= 2) mt[n][c] = fmaxf(mt[n][c], __shfl_xor_sync(0xffffffffu, mt[n][c], off));
+        const float mx = fmaxf(a.m[n][c], mt[n][c]);
+        const float keep = ex2(a.m[n][c] - (mx == -INFINITY ? 0.0f : mx));
+        a.m[n][c] = mx;
+        a.l[n][c] *= keep;
+#pragma unroll
+        for (int x = 0; x < D / 16; ++x) {
+          a.o[x][n][c] *= keep * turn;
+          a.o[x][n][2 + c] *= keep * turn;
+        }
+      }
+  }
+  // weights
+  const float vf = S::E4M3 ? pow2(kTop - a.ve) : 1.0f;
+  uint32_t pw[KT][NR][2];
+#pragma unroll
+  for (int j = 0; j < KT; ++j) {
+    float f[2] = {1.0f, 1.0f};
+    if (S::E4M3) {
+      f[0] = vs[j][0] * vf;
+      f[1] = vs[j][1] * vf;
+    }
+#pragma unroll
+    for (int n = 0; n < NR; ++n) {
+#pragma unroll
+      for (int c = 0; c < 4; ++c) {
+        const bool off = !WHOLE && sc[j][n][c] == -INFINITY;
+        const float mz = !WHOLE && a.m[n][c & 1] == -INFINITY ? 0.0f : a.m[n][c & 1];
+        float e = ex2(fmaf(sc[j][n][c], fac[n][c & 1], -mz));
+        if (off) e = 0.0f;
+        a.l[n][c & 1] += e;
+        if (S::E4M3) e *= f[c >> 1];
+        if (S::E4M3 && off) e = 0.0f;   // whatever scale lies there
+        if (!WHOLE) mine[(8 * n + 2 * t + (c & 1)) * S::kJoinLd + 16 * j + 8 * (c >> 1) + g] = off ? -1.0f : e;
+        sc[j][n][c] = e;
+      }
+#pragma unroll
+      for (int h = 0; h < 2; ++h)
+        pw[j][n][h] = transpose8(S::E4M3 ? pack_f16x2(sc[j][n][2 * h], sc[j][n][2 * h + 1])
+                                         : pack_bf16x2_cvt(sc[j][n][2 * h], sc[j][n][2 * h + 1]));
+    }
+  }
+  // values
+  uint32_t bad = 0;   // infinities and NaN where not every row sees every key: they take no part in the product
+  if constexpr (S::E4M3) {
+    // 32 keys by 16 columns, or 16 keys by 32 columns at a time
+#pragma unroll
+    for (int y = 0; y < D / 16; y += 3 - KT) {
+      uint32_t r[4];
+      ldsm4_t(r, KT == 2 ? cell_addr<S>(vb, k0 + lane, y) : cell_addr<S>(vb, k0 + (lane & 15), y + (lane >> 4)));
+#pragma unroll
+      for (int u = 0; u < 2; ++u) {
+        const int x = KT == 2 ? y : y + u, j = KT == 2 ? u : 0;
+        uint32_t f[4];
+#pragma unroll
+        for (int i = 0; i < 2; ++i) {
+          uint32_t& c = r[2 * u + i];
+          if (!WHOLE) {
+            const uint32_t nan = ((((c & 0x7f7f7f7fu) + 0x01010101u) & 0x80808080u) >> 7) * 255u;
+            bad |= nan;
+            c &= ~nan;
+          }
+          widen(__byte_perm(c, 0, 0x3120), f[2 * i], f[2 * i + 1]);   // keys 2 t, 2 t + 1: column 2 g, then 2 g + 1
+        }
+#pragma unroll
+        for (int n = 0; n < NR; ++n) mma_f16(a.o[x][n], f, pw[j][n][0], pw[j][n][1]);
+      }
+    }
+  } else {
+#pragma unroll
+    for (int j = 0; j < KT; ++j)
+#pragma unroll
+      for (int x = 0; x < D / 16; ++x) {
+        uint32_t f[4];
+        ldsm4_t(f, cell_addr<S>(vb, k0 + 16 * j + (lane & 7) + 8 * (lane >> 4), 2 * x + ((lane >> 3) & 1)));
+        if (!WHOLE) {
+#pragma unroll
+          for (int i = 0; i < 4; ++i) {
+            const uint32_t off = __vcmpeq2(f[i] & 0x7f807f80u, 0x7f807f80u);
+            bad |= off;
+            f[i] &= ~off;
+          }
+        }
+#pragma unroll
+        for (int n = 0; n < NR; ++n) mma_bf16(a.o[x][n], f, pw[j][n][0], pw[j][n][1]);
+      }
+  }
+  if (!WHOLE) {
+    __syncwarp();
+    if (__any_sync(0xffffffffu, bad != 0)) reach_rows<S>(a, mine, vb, k0);
+    __syncwarp();
+  }
 }
 
 template <class S>
 __device__ __forceinline__ void consume(const AttnParams& p, AttnShared& sh, const uint8_t* stage0, const uint8_t* scale0,
-                                        float* join, const int64_t (&range)[2], int stages,
-                                        const AbortCtl& ctl) {
-  constexpr int D = S::D, NT = S::CK / 8;      // key tiles of 8 in a step
-  constexpr int NX = D / 16;                   // 16-column groups of the output
+                                        uint2* qs, float* join, const int64_t (&range)[2], int stages, const AbortCtl& ctl) {
+  constexpr int D = S::D, NR = S::NR;
+  constexpr int kConsumers = S::NW * 32;
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
   const int g = lane >> 2, t = lane & 3;
   const int rg = warp / S::KG, kg = warp % S::KG;
-  const int box_shift = min(p.page_shift, 31 - __clz(S::KS));
+  StepInfo info;
+  info.box_shift = min(p.page_shift, 31 - __clz(S::KS));
+  info.rg = rg;
+  const uint32_t all_pages = S::KS >> info.box_shift >= 32 ? 0xffffffffu : (1u << (S::KS >> info.box_shift)) - 1;
   int st = 0;
   uint32_t parity = 0;
   Walk<S::M, S::KS> w(p, sh, range);
-  float* mine = join + warp * 16 * S::kJoinLd;
+  float* mine = join + warp * 8 * NR * S::kJoinLd;
   bool ok = true;
   while (w.left > 0) {
-    Rows<S> rw;
     const int rt = w.entry % p.row_tiles;
-    rw.load(p, w.s, w.head, rt, rg);
-    float o[NX][2][4];     // E4M3: [row half][4 consecutive columns]; bf16: [8-column tile][fragment]
+    load_queries<S>(p, sh, qs, w.s, w.head, rt);
+    named_bar_sync(1, kConsumers);
+    const uint2* qw = qs + rg * 8 * NR * 4;
+    uint2 qr[S::kQRegs ? D / 16 : 1][NR];
+    if constexpr (S::kQRegs) {
 #pragma unroll
-    for (int x = 0; x < NX; ++x)
+      for (int k = 0; k < D / 16; ++k)
 #pragma unroll
-      for (int a = 0; a < 2; ++a)
+        for (int n = 0; n < NR; ++n) qr[k][n] = qw[(k * S::M + 8 * n + g) * 4 + t];
+    }
+    float fac[NR][2];
+    Sums<S> a;
+    a.ve = -112;
+    int64_t top = 0;         // largest position of the warp's rows
 #pragma unroll
-        for (int c = 0; c < 4; ++c) o[x][a][c] = 0.0f;
-    float m[2] = {-INFINITY, -INFINITY}, l[2] = {0.0f, 0.0f};
+    for (int n = 0; n < NR; ++n)
+#pragma unroll
+      for (int c = 0; c < 2; ++c) {
+        const int r = rg * 8 * NR + 8 * n + 2 * t + c;
+        fac[n][c] = sh.fac[r];
+        top = max(top, sh.pos[r]);
+        a.m[n][c] = -INFINITY;
+        a.l[n][c] = 0.0f;
+#pragma unroll
+        for (int x = 0; x < D / 16; ++x) a.o[x][n][c] = a.o[x][n][2 + c] = 0.0f;
+      }
+#pragma unroll
+    for (int off = 1; off < 4; off *= 2) top = max(top, __shfl_xor_sync(0xffffffffu, top, off));
+    // keys [whole0, whole1) are seen by every row
+    const int64_t whole1 = min(static_cast<int64_t>(w.s.ctx), w.s.hi), whole0 = p.window > 0 ? top - p.window + 1 : 0;
 
     for (int it = 0; it < w.n; ++it) {
       ok = ok && mbar_wait(&sh.full[st], parity, ctl);
       ok = __all_sync(0xffffffffu, ok);
       if (!ok) break;
-      const uint32_t pages = sh.valid[st];
+      info.pages = sh.valid[st];
       const uint32_t kb = smem_u32(stage0 + st * S::kStage), vb = kb + S::kCode;
       const float* ksc = reinterpret_cast<const float*>(scale0 + st * 2 * S::kScale);
       const float* vsc = reinterpret_cast<const float*>(scale0 + st * 2 * S::kScale + S::kScale);
-      const int64_t key0 = static_cast<int64_t>(w.tile0 + it) * S::KS;
-      const uint32_t all_pages = S::KS >> box_shift >= 32 ? 0xffffffffu : (1u << (S::KS >> box_shift)) - 1;
+      info.key0 = static_cast<int64_t>(w.tile0 + it) * S::KS;
+#pragma unroll 1
       for (int ni = 0; ni < S::NI; ++ni) {
         const int k0 = (kg * S::NI + ni) * S::CK;            // the step's first key within the tile
-        const int64_t ka = key0 + k0;
+        const int64_t ka = info.key0 + k0;
         if (ka >= w.s.hi || ka + S::CK <= w.s.lo) continue;
-        const bool whole = ka + S::CK <= min(static_cast<int64_t>(w.s.ctx), w.s.hi) && pages == all_pages &&
-                           (p.window <= 0 || rw.top - ka < p.window);
-        // scores
-        float sc[NT][4];
-#pragma unroll
-        for (int n = 0; n < NT; ++n) {
-          sc[n][0] = sc[n][1] = sc[n][2] = sc[n][3] = 0.0f;
-#pragma unroll
-          for (int k2 = 0; k2 < Rows<S>::NK / 2; ++k2) {
-            uint32_t r[4];
-            ldsm4(r, cell_addr<S>(kb, k0 + n * 8 + (lane & 7), 4 * k2 + (lane >> 3)));
-            if (S::E4M3) {
-              mma_e4m3(sc[n], rw.q[0][2 * k2], r[0], r[1]);
-              mma_e4m3(sc[n], rw.q[Rows<S>::NQ - 1][2 * k2], r[0], r[1]);
-              mma_e4m3(sc[n], rw.q[0][2 * k2 + 1], r[2], r[3]);
-              mma_e4m3(sc[n], rw.q[Rows<S>::NQ - 1][2 * k2 + 1], r[2], r[3]);
-            } else {
-              mma_bf16(sc[n], rw.q[0][2 * k2], r[0], r[1]);
-              mma_bf16(sc[n], rw.q[0][2 * k2 + 1], r[2], r[3]);
-            }
-          }
-        }
-        float mt[2] = {-INFINITY, -INFINITY};
-#pragma unroll
-        for (int n = 0; n < NT; ++n) {
-          float2 ks = make_float2(1.0f, 1.0f);
-          if (S::E4M3) ks = *reinterpret_cast<const float2*>(ksc + k0 + n * 8 + 2 * t);
-#pragma unroll
-          for (int c = 0; c < 4; ++c) {
-            float v = sc[n][c] * rw.fac[c >> 1];
-            if (S::E4M3) v *= (c & 1) ? ks.y : ks.x;
-            if (!whole) {
-              const int in_tile = k0 + n * 8 + 2 * t + (c & 1);
-              if (!visible<S>(p, w.s, rw, c >> 1, key0 + in_tile, pages, box_shift, in_tile)) v = -INFINITY;
-            }
-            sc[n][c] = v;
-            mt[c >> 1] = fmaxf(mt[c >> 1], v);
-          }
-        }
-#pragma unroll
-        for (int h = 0; h < 2; ++h) {
-          mt[h] = fmaxf(mt[h], __shfl_xor_sync(0xffffffffu, mt[h], 1));
-          mt[h] = fmaxf(mt[h], __shfl_xor_sync(0xffffffffu, mt[h], 2));
-        }
-        float keep[2], mn[2];      // factor of the sums so far; the new maximum (0 where nothing was seen)
-        bool same = true;
-#pragma unroll
-        for (int h = 0; h < 2; ++h) {
-          const float mx = fmaxf(m[h], mt[h]);
-          mn[h] = mx == -INFINITY ? 0.0f : mx;
-          keep[h] = ex2(m[h] - mn[h]);
-          same = same && mx == m[h];
-          m[h] = mx;
-        }
-        same = __all_sync(0xffffffffu, same);
-        if constexpr (S::E4M3) {
-          // weights against the step's own maximum, times the values' scales
-          float ms[2], lt[2] = {0.0f, 0.0f}, wm[2] = {0.0f, 0.0f};
-          ms[0] = mt[0] == -INFINITY ? 0.0f : mt[0];
-          ms[1] = mt[1] == -INFINITY ? 0.0f : mt[1];
-#pragma unroll
-          for (int n = 0; n < NT; ++n) {
-            const float2 vs = *reinterpret_cast<const float2*>(vsc + k0 + n * 8 + 2 * t);
-#pragma unroll
-            for (int c = 0; c < 4; ++c) {
-              const float e = ex2(sc[n][c] - ms[c >> 1]);
-              lt[c >> 1] += e;
-              float v = e * ((c & 1) ? vs.y : vs.x);
-              if (!whole && sc[n][c] == -INFINITY) v = 0.0f;   // whatever scale lies there
-              sc[n][c] = v;
-              wm[c >> 1] = fmaxf(wm[c >> 1], v);
-            }
-          }
-          float f[2], back[2];
-#pragma unroll
-          for (int h = 0; h < 2; ++h) {
-            wm[h] = fmaxf(wm[h], __shfl_xor_sync(0xffffffffu, wm[h], 1));
-            wm[h] = fmaxf(wm[h], __shfl_xor_sync(0xffffffffu, wm[h], 2));
-            const int e = min(top_exponent(wm[h]), 120);
-            const float in = ex2(ms[h] - mn[h]);
-            f[h] = pow2(7 - e);
-            back[h] = mt[h] == -INFINITY ? 0.0f : in * pow2(e - 7);
-            l[h] = l[h] * keep[h] + (mt[h] == -INFINITY && lt[h] == 0.0f ? 0.0f : lt[h] * in);
-          }
-          constexpr int NP = S::CK / 32;
-          uint32_t hi[NP][4], lo[NP][4];
-#pragma unroll
-          for (int k = 0; k < NP; ++k)
-#pragma unroll
-            for (int h = 0; h < 2; ++h)
-#pragma unroll
-              for (int c = 0; c < 2; ++c) {
-                uint16_t h0, l0, h1, l1;
-                const float(&a)[4] = sc[4 * k + 2 * c];
-                const float(&b)[4] = sc[4 * k + 2 * c + 1];
-                split_e4m3(a[2 * h] * f[h], a[2 * h + 1] * f[h], h0, l0);
-                split_e4m3(b[2 * h] * f[h], b[2 * h + 1] * f[h], h1, l1);
-                hi[k][h + 2 * c] = h0 | (static_cast<uint32_t>(h1) << 16);
-                lo[k][h + 2 * c] = l0 | (static_cast<uint32_t>(l1) << 16);
-              }
-#pragma unroll
-          for (int x = 0; x < NX; ++x) {
-            float ev[4] = {0.0f, 0.0f, 0.0f, 0.0f}, od[4] = {0.0f, 0.0f, 0.0f, 0.0f};
-#pragma unroll
-            for (int k = 0; k < NP; ++k) {
-              uint32_t r[4];
-              ldsm4_t(r, cell_addr<S>(vb, k0 + k * 32 + lane, x));
-              if (!whole) {   // codes of NaN in cells that nobody wrote
-#pragma unroll
-                for (int i = 0; i < 4; ++i) {
-                  const uint32_t nan = ((r[i] & 0x7f7f7f7fu) + 0x01010101u) & 0x80808080u;
-                  r[i] &= ~((nan >> 7) * 255u);
-                }
-              }
-              const uint32_t e0 = __byte_perm(r[0], r[1], 0x6420), e1 = __byte_perm(r[2], r[3], 0x6420);
-              const uint32_t d0 = __byte_perm(r[0], r[1], 0x7531), d1 = __byte_perm(r[2], r[3], 0x7531);
-              mma_e4m3(ev, hi[k], e0, e1);
-              mma_e4m3(od, hi[k], d0, d1);
-              mma_e4m3(ev, lo[k], e0, e1);
-              mma_e4m3(od, lo[k], d0, d1);
-            }
-#pragma unroll
-            for (int h = 0; h < 2; ++h) {
-              const float v[4] = {ev[2 * h], od[2 * h], ev[2 * h + 1], od[2 * h + 1]};
-#pragma unroll
-              for (int c = 0; c < 4; ++c)
-                o[x][h][c] = same ? fmaf(v[c], back[h], o[x][h][c]) : fmaf(v[c], back[h], o[x][h][c] * keep[h]);
-            }
-          }
-        } else {
-          float lt[2] = {0.0f, 0.0f};
-          uint32_t pw[NT / 2][4];
-          const bool slow_rows = !whole;
-          if (slow_rows)
-            for (int n = 0; n < NT; ++n)
-              for (int c = 0; c < 4; ++c)
-                mine[(g + 8 * (c >> 1)) * S::kJoinLd + n * 8 + 2 * t + (c & 1)] = sc[n][c] == -INFINITY ? -1.0f : ex2(sc[n][c] - mn[c >> 1]);
-#pragma unroll
-          for (int n = 0; n < NT; ++n) {
-#pragma unroll
-            for (int c = 0; c < 4; ++c) {
-              sc[n][c] = ex2(sc[n][c] - mn[c >> 1]);
-              lt[c >> 1] += sc[n][c];
-            }
-            pw[n / 2][2 * (n & 1)] = pack_bf16x2_cvt(sc[n][0], sc[n][1]);
-            pw[n / 2][2 * (n & 1) + 1] = pack_bf16x2_cvt(sc[n][2], sc[n][3]);
-          }
-          l[0] = l[0] * keep[0] + lt[0];
-          l[1] = l[1] * keep[1] + lt[1];
-          if (!same) {
-#pragma unroll
-            for (int x = 0; x < NX; ++x)
-#pragma unroll
-              for (int a = 0; a < 2; ++a)
-#pragma unroll
-                for (int c = 0; c < 4; ++c) o[x][a][c] *= keep[c >> 1];
-          }
-          uint32_t bad = 0;
-#pragma unroll
-          for (int k = 0; k < NT / 2; ++k)
-#pragma unroll
-            for (int x = 0; x < NX; ++x) {
-              uint32_t r[4];
-              ldsm4_t(r, cell_addr<S>(vb, k0 + k * 16 + (lane & 15), 2 * x + (lane >> 4)));
-              if (!whole) {   // infinities and NaN take no part in the product; see below
-#pragma unroll
-                for (int i = 0; i < 4; ++i) {
-                  const uint32_t off = __vcmpeq2(r[i] & 0x7f807f80u, 0x7f807f80u);
-                  bad |= off;
-                  r[i] &= ~off;
-                }
-              }
-              mma_bf16(o[x][0], pw[k], r[0], r[1]);
-              mma_bf16(o[x][1], pw[k], r[2], r[3]);
-            }
-          if (slow_rows && __any_sync(0xffffffffu, bad != 0)) {
-            // they reach the rows that see them, and no others
-            __syncwarp();
-            for (int k = 0; k < S::CK; ++k) {
-              const float w0 = mine[g * S::kJoinLd + k], w1 = mine[(g + 8) * S::kJoinLd + k];
-#pragma unroll
-              for (int x = 0; x < NX; ++x)
-#pragma unroll
-                for (int a = 0; a < 2; ++a) {
-                  const uint32_t addr = cell_addr<S>(vb, k0 + k, 2 * x + a) + 4 * t;
-                  uint32_t v;
-                  asm volatile("ld.shared.u32 %0, [%1];" : "=r"(v) : "r"(addr) : "memory");
-                  const float v0 = __uint_as_float(v << 16), v1 = __uint_as_float(v & 0xffff0000u);
-                  if (!isfinite(v0)) {
-                    if (w0 >= 0.0f) o[x][a][0] += w0 * v0;
-                    if (w1 >= 0.0f) o[x][a][2] += w1 * v0;
-                  }
-                  if (!isfinite(v1)) {
-                    if (w0 >= 0.0f) o[x][a][1] += w0 * v1;
-                    if (w1 >= 0.0f) o[x][a][3] += w1 * v1;
-                  }
-                }
-            }
-          }
-          __syncwarp();
-        }
+        if (ka >= whole0 && ka + S::CK <= whole1 && info.pages == all_pages)
+          step<S, true>(p, sh, w.s, info, a, qw, qr, kb, vb, ksc, vsc, mine, k0, fac);
+        else
+          step<S, false>(p, sh, w.s, info, a, qw, qr, kb, vb, ksc, vsc, mine, k0, fac);
       }
       __syncwarp();
       if (lane == 0) mbar_arrive(&sh.empty[st]);
@@ -697,46 +777,52 @@ __device__ __forceinline__ void consume(const AttnParams& p, AttnShared& sh, con
     }
     // the item's rows: the warps of a row group put their sums together
 #pragma unroll
-    for (int h = 0; h < 2; ++h) {
-      l[h] += __shfl_xor_sync(0xffffffffu, l[h], 1);
-      l[h] += __shfl_xor_sync(0xffffffffu, l[h], 2);
-      if (t == 0) {
-        sh.m[warp][g + 8 * h] = m[h];
-        sh.l[warp][g + 8 * h] = l[h];
-      }
-    }
-    named_bar_sync(1, kAttnWarps * 32);
-    const bool complete = w.n == w.len;
-    const int slot = w.offset > 0 ? 0 : 1;   // partial sums: an item begun elsewhere, or one that goes on elsewhere
-    float fold[2];
+    for (int n = 0; n < NR; ++n)
 #pragma unroll
-    for (int h = 0; h < 2; ++h) {
-      float mx = -INFINITY;
-      for (int k = 0; k < S::KG; ++k) mx = fmaxf(mx, sh.m[rg * S::KG + k][g + 8 * h]);
-      fold[h] = ex2(m[h] - (mx == -INFINITY ? 0.0f : mx));
-    }
-    for (int c0 = 0; c0 < D; c0 += S::kCols) {
+      for (int c = 0; c < 2; ++c) {
 #pragma unroll
-      for (int x = 0; x < NX; ++x) {
-        if (x * 16 < c0 || x * 16 >= c0 + S::kCols) continue;
-        if (S::E4M3) {
-#pragma unroll
-          for (int h = 0; h < 2; ++h)
-            *reinterpret_cast<float4*>(mine + (g + 8 * h) * S::kJoinLd + x * 16 - c0 + 4 * t) =
-                make_float4(o[x][h][0] * fold[h], o[x][h][1] * fold[h], o[x][h][2] * fold[h], o[x][h][3] * fold[h]);
-        } else {
-#pragma unroll
-          for (int a = 0; a < 2; ++a)
-#pragma unroll
-            for (int h = 0; h < 2; ++h)
-              *reinterpret_cast<float2*>(mine + (g + 8 * h) * S::kJoinLd + x * 16 + 8 * a - c0 + 2 * t) =
-                  make_float2(o[x][a][2 * h] * fold[h], o[x][a][2 * h + 1] * fold[h]);
+        for (int off = 4; off < 32; off *= 2) a.l[n][c] += __shfl_xor_sync(0xffffffffu, a.l[n][c], off);
+        if (g == 0) {
+          sh.m[warp][8 * n + 2 * t + c] = a.m[n][c];
+          sh.l[warp][8 * n + 2 * t + c] = a.l[n][c];
         }
       }
-      named_bar_sync(1, kAttnWarps * 32);
-      for (int u = tid; u < S::M * (S::kCols / 4); u += kAttnWarps * 32) {
+    named_bar_sync(1, kConsumers);
+    const bool complete = w.n == w.len;
+    const int slot = w.offset > 0 ? 0 : 1;   // partial sums: an item begun elsewhere, or one that goes on elsewhere
+    float fold[NR][2];
+#pragma unroll
+    for (int n = 0; n < NR; ++n)
+#pragma unroll
+      for (int c = 0; c < 2; ++c) {
+        float mx = -INFINITY;
+        for (int k = 0; k < S::KG; ++k) mx = fmaxf(mx, sh.m[rg * S::KG + k][8 * n + 2 * t + c]);
+        fold[n][c] = ex2(a.m[n][c] - (mx == -INFINITY ? 0.0f : mx)) * (S::E4M3 ? pow2(a.ve - kTop) : 1.0f);
+      }
+    for (int c0 = 0; c0 < D; c0 += S::kCols) {
+#pragma unroll
+      for (int x = 0; x < D / 16; ++x) {
+        if (x * 16 < c0 || x * 16 >= c0 + S::kCols) continue;
+#pragma unroll
+        for (int n = 0; n < NR; ++n)
+#pragma unroll
+          for (int c = 0; c < 2; ++c) {
+            float* dst = mine + (8 * n + 2 * t + c) * S::kJoinLd + x * 16 - c0;
+            const float v0 = a.o[x][n][c] * fold[n][c], v1 = a.o[x][n][2 + c] * fold[n][c];
+            if (S::E4M3) {
+              *reinterpret_cast<float2*>(dst + 2 * g) = make_float2(v0, v1);
+            } else {
+              dst[g] = v0;
+              dst[g + 8] = v1;
+            }
+          }
+      }
+      named_bar_sync(1, kConsumers);
+      for (int u = tid; u < S::M * (S::kCols / 4); u += kConsumers) {
         const int r = u / (S::kCols / 4), c = u % (S::kCols / 4) * 4;
-        const int g0 = r / 16 * S::KG, rr = r % 16;
+        const int g0 = r / (8 * NR) * S::KG, rr = r % (8 * NR);
+        const int64_t row = static_cast<int64_t>(rt) * S::M + r;
+        if (row >= static_cast<int64_t>(w.s.T) * p.group || !ok) continue;
         float mx = -INFINITY, lt = 0.0f;
         float4 v = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
 #pragma unroll
@@ -745,14 +831,12 @@ __device__ __forceinline__ void consume(const AttnParams& p, AttnShared& sh, con
 #pragma unroll
         for (int k = 0; k < S::KG; ++k) {
           lt += sh.l[g0 + k][rr] * ex2(sh.m[g0 + k][rr] - mz);
-          const float4 a = *reinterpret_cast<const float4*>(join + ((g0 + k) * 16 + rr) * S::kJoinLd + c);
-          v.x += a.x;
-          v.y += a.y;
-          v.z += a.z;
-          v.w += a.w;
+          const float4 y = *reinterpret_cast<const float4*>(join + ((g0 + k) * 8 * NR + rr) * S::kJoinLd + c);
+          v.x += y.x;
+          v.y += y.y;
+          v.z += y.z;
+          v.w += y.w;
         }
-        const int64_t row = static_cast<int64_t>(rt) * S::M + r;
-        if (row >= static_cast<int64_t>(w.s.T) * p.group || !ok) continue;
         if (complete) {
           const int i = static_cast<int>(row / p.group);
           const int head = w.head * p.group + static_cast<int>(row - static_cast<int64_t>(i) * p.group);
@@ -769,24 +853,24 @@ __device__ __forceinline__ void consume(const AttnParams& p, AttnShared& sh, con
           if (c0 == 0 && c == 0) p.part_ml[at] = make_float2(mx, lt);
         }
       }
-      named_bar_sync(1, kAttnWarps * 32);
+      named_bar_sync(1, kConsumers);
     }
     w.next(p);
   }
 }
 
 template <class S>
-__global__ void __launch_bounds__(kAttnThreads, S::kTwo ? 2 : 1)
-aq_tree_attention_kernel(const __grid_constant__ AttnParams p) {
+__global__ void __launch_bounds__(S::kThreads, S::kPerSm) aq_tree_attention_kernel(const __grid_constant__ AttnParams p) {
   extern __shared__ uint8_t raw[];
   __shared__ AttnShared sh;
   uint8_t* stage0 = raw + ((1024 - (smem_u32(raw) & 1023)) & 1023);
   uint8_t* scale0 = stage0 + p.stages * S::kStage;
-  float* join = reinterpret_cast<float*>(scale0 + p.stages * 2 * S::kScale);
+  uint2* qs = reinterpret_cast<uint2*>(scale0 + p.stages * 2 * S::kScale);
+  float* join = reinterpret_cast<float*>(qs) + S::kQ / 4;
   if (threadIdx.x == 0) {
     for (int i = 0; i < p.stages; ++i) {
       mbar_init(&sh.full[i], 1);
-      mbar_init(&sh.empty[i], kAttnWarps);
+      mbar_init(&sh.empty[i], S::NW);
     }
     sh.abort = 0;
     fence_barrier_init();
@@ -795,12 +879,16 @@ aq_tree_attention_kernel(const __grid_constant__ AttnParams p) {
   }
   pdl_wait_prior_grid();
   int64_t range[2];
-  locate<S::M, S::KS>(p, sh, p.prefix, blockIdx.x == 0, range);
+  locate<S::M, S::KS>(p, sh, reinterpret_cast<int64_t*>(join), p.prefix, blockIdx.x == 0, range);
   const AbortCtl ctl = {&sh.abort, p.status, p.timeout_ns};
-  if (threadIdx.x >= kAttnWarps * 32)
-    produce<S>(p, sh, stage0, scale0, range, p.stages, ctl);
-  else
-    consume<S>(p, sh, stage0, scale0, join, range, p.stages, ctl);
+  if (threadIdx.x >= S::NW * 32) {
+    // 384 threads at 168 registers: 256 at 232 and 128 at 40
+    if (S::kSplitRegs) asm volatile("setmaxnreg.dec.sync.aligned.u32 40;");
+    if (threadIdx.x < S::NW * 32 + 32) produce<S>(p, sh, stage0, scale0, range, p.stages, ctl);
+  } else {
+    if (S::kSplitRegs) asm volatile("setmaxnreg.inc.sync.aligned.u32 232;");
+    consume<S>(p, sh, stage0, scale0, qs, join, range, p.stages, ctl);
+  }
   pdl_launch_dependents();
 }
 
@@ -879,8 +967,8 @@ __global__ void __launch_bounds__(128) aq_attention_join_kernel(const __grid_con
 // ---------------------------------------------------------------------------------
 // host
 // ---------------------------------------------------------------------------------
-// Rows of a tile: the fewest of 16, 32, 64 that hold a sequence's rows of one key/value head.
-int rows_per_tile(int64_t rows) { return rows <= 16 ? 16 : rows <= 32 ? 32 : 64; }
+// Rows of a tile: the fewest of 8, 16, 32, 64 that hold a sequence's rows of one key/value head.
+int rows_per_tile(int64_t rows) { return rows <= 8 ? 8 : rows <= 16 ? 16 : rows <= 32 ? 32 : 64; }
 
 struct AttnLayout {
   int rows = 0, row_tiles = 0;
@@ -931,12 +1019,11 @@ aq_status launch_attention(AttnParams& p, const aq_kv_cache* c, const ServeDev& 
   if ((s = cache_map(&p.tm_k, c->k, c, S::RB / S::ES, box, who)) != AQ_OK) return s;
   if ((s = cache_map(&p.tm_v, c->v, c, S::RB / S::ES, box, who)) != AQ_OK) return s;
   constexpr size_t kStatic = (sizeof(AttnShared) + 127) / 128 * 128;
-  constexpr size_t kUnit = S::kStage + 2 * S::kScale;
-  constexpr bool two = S::kTwo;
-  const size_t room = (two ? (dev.smem_optin + 1024) / 2 - 1024 : dev.smem_optin) - kStatic - 1024 - S::kJoin;
+  constexpr size_t kUnit = S::kStage + 2 * S::kScale, kFixed = 1024 + S::kQ + S::kJoin;
+  const size_t room = (dev.smem_optin + 1024) / S::kPerSm - 1024 - kStatic - kFixed;   // 1 KB a CTA is the system's
   p.stages = static_cast<int>(std::min<size_t>(room / kUnit, kAttnStages));
   if (p.stages < 2) return serve_fail(AQ_ERR_UNSUPPORTED, "%s: the device has too little shared memory", who);
-  const size_t smem = 1024 + p.stages * kUnit + S::kJoin;
+  const size_t smem = kFixed + p.stages * kUnit;
   static std::atomic<uint64_t> ready{0};   // devices on which the kernel may use that much
   const uint64_t bit = 1ull << dev.index;
   if (!(ready.load() & bit)) {
@@ -944,19 +1031,22 @@ aq_status launch_attention(AttnParams& p, const aq_kv_cache* c, const ServeDev& 
     if (e != cudaSuccess) return serve_launched(e, who);
     ready.fetch_or(bit);
   }
-  p.main_grid = std::min(dev.sms, kAttnSmsBound) * (two ? 2 : 1);
-  cudaError_t e = launch_serve(aq_tree_attention_kernel<S>, p, dim3(p.main_grid), kAttnThreads, smem, st);
+  p.main_grid = std::min(dev.sms, kAttnSmsBound) * S::kPerSm;
+  cudaError_t e = launch_serve(aq_tree_attention_kernel<S>, p, dim3(p.main_grid), S::kThreads, smem, st);
   if (e == cudaSuccess)
     e = launch_serve(aq_attention_join_kernel<S::D>, p, dim3(static_cast<unsigned>(p.total_q * p.hk * p.group)), 128, 0, st);
   return serve_launched(e, who);
 }
 
+// Registers (O^T takes D NR / 4 a thread) and shared memory decide how many CTAs share an SM.
 template <int D, bool E4M3>
 aq_status launch_rows(AttnParams& p, const aq_kv_cache* c, const ServeDev& dev, cudaStream_t st, const char* who) {
+  constexpr int per1 = D == 256 && !E4M3 ? 1 : 2, per2 = D == 256 ? 1 : 2;
   switch (p.rows_per_tile) {
-    case 16: return launch_attention<Shape<D, E4M3, 1>>(p, c, dev, st, who);
-    case 32: return launch_attention<Shape<D, E4M3, 2>>(p, c, dev, st, who);
-    default: return launch_attention<Shape<D, E4M3, 4>>(p, c, dev, st, who);
+    case 8: return launch_attention<Shape<D, E4M3, 1, 1, 4, per1>>(p, c, dev, st, who);
+    case 16: return launch_attention<Shape<D, E4M3, 2, 1, 4, per2>>(p, c, dev, st, who);
+    case 32: return launch_attention<std::conditional_t<D == 256, Shape<D, E4M3, 2, 2, 8, 1>, Shape<D, E4M3, 4, 1, 8, 1>>>(p, c, dev, st, who);
+    default: return launch_attention<std::conditional_t<D == 256, Shape<D, E4M3, 2, 4, 8, 1>, Shape<D, E4M3, 4, 2, 8, 1>>>(p, c, dev, st, who);
   }
 }
 
