@@ -509,7 +509,7 @@ aq_status aq_tree_attention(const aq_kv_cache* cache, const aq_draft_batch* batc
  * next token is the v with the largest r(v) / noise[b, v], the lowest of equal ones; where r has no mass
  * left, r = p. With u uniform in [0, 1) and noise exponential with mean 1, the tokens are distributed as
  * the target's own.
- *   p_type     AQ_PROB_F32 or AQ_PROB_BF16, of p and q; rows of `vocab`, row strides ld_p and ld_q; rows:
+ *   p_type     AQ_PROB_F32 or AQ_PROB_BF16, of p and q; rows of `vocab` (up to 2^30), row strides ld_p and ld_q; rows:
  *              number of rows of p and of q
  *   u [nodes], noise [batch, vocab] (row stride ld_noise): fp32
  *   n_accepted int32 [batch]; path int32 [batch, path_cap] (row stride ld_path): the accepted nodes' indices

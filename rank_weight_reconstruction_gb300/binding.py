@@ -9,7 +9,6 @@ from __future__ import annotations
 
 import ctypes
 import os
-import struct
 from dataclasses import dataclass
 
 from . import build_lib
@@ -167,8 +166,8 @@ def load(path: str | None = None) -> ctypes.CDLL:
     lib.aq_selftest_bounds_check.restype = ctypes.c_int
     lib.aq_set_path.argtypes = [ctypes.c_int]
     lib.aq_set_path.restype = ctypes.c_int
-    rope_p = cache_p = batch_p = vp   # struct pointers: byref() of a c_* struct, or its packed bytes
-    f32 = ctypes.c_float
+    rope_p, cache_p = ctypes.POINTER(c_rope), ctypes.POINTER(c_kv_cache)
+    batch_p, f32 = ctypes.POINTER(c_draft_batch), ctypes.c_float
     lib.aq_rope_frequencies.argtypes = [i32, ctypes.c_double, i32, ctypes.POINTER(c_rope_scaling), vp,
                                         ctypes.POINTER(f32)]
     lib.aq_rope_frequencies.restype = ctypes.c_int
@@ -540,16 +539,33 @@ def aq_mlp(gate: Theta, up: Theta, down: Theta, x, act=AQ_ACT_GELU_TANH, y=None,
 
 
 # ----------------------------------------------------------------------------------
-# serving: rotary positions, the paged key/value cache, drafted-token attention, verification
-#
-# A decode step makes these calls one after another on a few tokens, so the time of a call is the
-# marshalling below as much as the kernel: shapes and strides are taken once per tensor, dtypes compared
-# by identity, and the argument structs packed as bytes (native alignment, the layout of the c_* structs)
-# instead of filled field by field (measured on one host core: aq_rope 18 -> 7 us a call).
+# serving: rotary positions, the paged key/value cache, drafted-token attention, verification. Their
+# tensors are marshalled by the compiled module _marshal (csrc/aq_python.c), which checks types, shapes and
+# strides, calls the entry point and returns its status.
 # ----------------------------------------------------------------------------------
-_pack_rope = struct.Struct("@Piif4x").pack
-_pack_cache = struct.Struct("@PPPPiiiii4x").pack
-_pack_batch = struct.Struct("@iiqPPPiqPqPi4x").pack
+_marshal = None
+
+
+def _serve():
+    """The marshalling module, bound to the loaded library."""
+    global _marshal
+    if _marshal is None:
+        import importlib.util
+
+        import torch
+        lib = load()
+        if not os.path.exists(build_lib.MARSHAL_PATH):
+            raise RuntimeError(f"{build_lib.MARSHAL_PATH} is missing: build it with "
+                               "rank_weight_reconstruction_gb300.build_lib.build()")
+        spec = importlib.util.spec_from_file_location("_marshal", build_lib.MARSHAL_PATH)
+        module = importlib.util.module_from_spec(spec)
+        spec.loader.exec_module(module)
+        names = ("aq_rope", "aq_kv_write", "aq_kv_read", "aq_tree_attention_workspace_bytes", "aq_tree_attention",
+                 "aq_verify_drafts")
+        module.bind(tuple(ctypes.cast(getattr(lib, n), ctypes.c_void_p).value for n in names),
+                    (torch.bfloat16, torch.float32, torch.int32, torch.int64, torch.uint64, torch.uint8))
+        _marshal = module
+    return _marshal
 
 
 def _raw_stream(stream, t) -> int:
@@ -559,45 +575,6 @@ def _raw_stream(stream, t) -> int:
     return int(stream.cuda_stream) if hasattr(stream, "cuda_stream") else int(stream)
 
 
-def _flat(t, dtype, name, n) -> int:
-    """Pointer of a contiguous 1-D tensor of the given type with n elements (None: any number)."""
-    if t.dtype is not dtype:
-        raise TypeError(f"{name}: expected a {dtype} tensor, got {t.dtype}")
-    shape = t.shape
-    if len(shape) != 1 or (n is not None and shape[0] != n) or not t.is_contiguous():
-        raise ValueError(f"{name}: expected a contiguous 1-D tensor" + ("" if n is None else f" of {n} elements")
-                         + f", got {tuple(shape)} with strides {t.stride()}")
-    return t.data_ptr()
-
-
-def _heads(t, name, tokens, heads, dim):
-    """(pointer, token stride, head stride) of a bf16 [tokens, heads, head_dim] tensor or view."""
-    import torch
-    if t.dtype is not torch.bfloat16:
-        raise TypeError(f"{name}: expected a bfloat16 tensor, got {t.dtype}")
-    if t.shape != (tokens, heads, dim):
-        raise ValueError(f"{name}: expected shape {(tokens, heads, dim)}, got {tuple(t.shape)}")
-    tok, head, one = t.stride()
-    if one != 1 and dim > 1:
-        raise ValueError(f"{name}: expected unit stride along the head")
-    if heads == 1:
-        head = dim
-    return t.data_ptr(), tok if tokens > 1 else heads * head, head
-
-
-def _rows(t, dtype, name, rows, cols):
-    """(pointer, row stride) of a 2-D tensor with unit column stride and at least `cols` columns."""
-    if t.dtype is not dtype:
-        raise TypeError(f"{name}: expected a {dtype} tensor, got {t.dtype}")
-    shape = t.shape
-    if len(shape) != 2 or shape[0] != rows or shape[1] < cols:
-        raise ValueError(f"{name}: expected [{rows}, {cols}], got {tuple(shape)}")
-    ld, one = t.stride()
-    if one != 1 and shape[1] > 1:
-        raise ValueError(f"{name}: expected unit column stride")
-    return t.data_ptr(), ld if rows > 1 else max(ld, shape[1])
-
-
 @dataclass
 class Rope:
     """Rotary positions: ``freq`` is an int64 (or uint64) device tensor [rotary_dim / 2] of turns per
@@ -605,13 +582,6 @@ class Rope:
     freq: object
     layout: int = AQ_ROPE_HALF
     magnitude: float = 1.0
-
-    def packed(self) -> bytes:
-        import torch
-        f = self.freq
-        if f.dtype is not torch.int64 and f.dtype is not torch.uint64:
-            raise TypeError(f"Rope.freq: expected an int64 tensor, got {f.dtype}")
-        return _pack_rope(_flat(f, f.dtype, "Rope.freq", None), 2 * f.shape[0], self.layout, self.magnitude)
 
 
 def rope_frequencies(rotary_dim: int, base: float = 10000.0, scaling: int = AQ_ROPE_SCALE_NONE, factor: float = 1.0,
@@ -632,13 +602,12 @@ def rope_frequencies(rotary_dim: int, base: float = 10000.0, scaling: int = AQ_R
 def aq_rope(rope: Rope, pos, x, inverse: bool = False, y=None, stream=None):
     """x [T, heads, head_dim] (bf16, any token and head strides) rotated at positions pos (int32 [T]);
     ``inverse`` turns back, which is the gradient of the rotation. y may be x."""
-    import torch
-    T, heads, dim = x.shape
     if y is None:
+        import torch
         y = torch.empty_like(x)
-    _check(load().aq_rope(rope.packed(), _flat(pos, torch.int32, "pos", T), T, heads, dim,
-                          *_heads(x, "x", T, heads, dim), *_heads(y, "y", T, heads, dim), 1 if inverse else 0,
-                          _raw_stream(stream, x)))
+    st = _serve().rope(rope, pos, x, y, inverse, _raw_stream(stream, x))
+    if st:
+        _check(st)
     return y
 
 
@@ -664,58 +633,42 @@ class KvCache:
     def type(self) -> int:
         return AQ_KV_BF16 if self.k_scale is None else AQ_KV_E4M3
 
-    def packed(self) -> bytes:
-        import torch
-        k, v, ks, vs = self.k, self.v, self.k_scale, self.v_scale
-        shape = k.shape
-        code = torch.bfloat16 if ks is None else torch.uint8
-        if len(shape) != 4 or v.shape != shape or not k.is_contiguous() or not v.is_contiguous():
-            raise ValueError("KvCache: expected contiguous k and v of one shape [pages, kv_heads, page_size, head_dim]")
-        if k.dtype is not code or v.dtype is not code:
-            raise TypeError(f"KvCache: expected {code} tensors k and v, got {k.dtype} and {v.dtype}")
-        if ks is None or vs is None:
-            if ks is not vs:
-                raise ValueError("KvCache: k_scale and v_scale go together")
-            return _pack_cache(k.data_ptr(), v.data_ptr(), 0, 0, shape[0], shape[2], shape[1], shape[3], AQ_KV_BF16)
-        if ks.dtype is not torch.float32 or vs.dtype is not torch.float32:
-            raise TypeError("KvCache: expected float32 scales")
-        if ks.shape != shape[:3] or vs.shape != shape[:3] or not ks.is_contiguous() or not vs.is_contiguous():
-            raise ValueError(f"KvCache: expected contiguous scales of shape {tuple(shape[:3])}")
-        return _pack_cache(k.data_ptr(), v.data_ptr(), ks.data_ptr(), vs.data_ptr(), shape[0], shape[2], shape[1],
-                           shape[3], AQ_KV_E4M3)
-
 
 def aq_kv_write(cache: KvCache, k, v, slots, rope: Rope | None = None, pos=None, q=None, q_out=None, stream=None):
     """Writes k and v [T, kv_heads, head_dim] into the cache's slots (int64 [T]), rotating k with
     ``rope`` at ``pos``. With q [T, q_heads, head_dim] the rotated queries are returned too (into q_out,
     which may be q)."""
-    import torch
-    c = cache.packed()
-    _, hk, _, dim = cache.k.shape
-    T = k.shape[0]
-    heads, qs, os = 0, (0, 0, 0), (0, 0, 0)
-    if q is not None:
-        heads = q.shape[1]
-        if q_out is None:
-            q_out = torch.empty(q.shape, dtype=q.dtype, device=q.device)
-        qs, os = _heads(q, "q", T, heads, dim), _heads(q_out, "q_out", T, heads, dim)
-    _check(load().aq_kv_write(c, _flat(slots, torch.int64, "slots", T), T, *_heads(k, "k", T, hk, dim),
-                              *_heads(v, "v", T, hk, dim), None if rope is None else rope.packed(),
-                              0 if pos is None else _flat(pos, torch.int32, "pos", T), qs[0], heads, qs[1], qs[2], *os,
-                              _raw_stream(stream, k)))
+    if q is not None and q_out is None:
+        import torch
+        q_out = torch.empty_like(q)
+    st = _serve().kv_write(cache, k, v, slots, rope, pos, q, q_out, _raw_stream(stream, k))
+    if st:
+        _check(st)
     return q_out
 
 
 def aq_kv_read(cache: KvCache, slots, k=None, v=None, stream=None):
     """The tokens in the cache's slots (int64 [T]) as bf16: (k, v), each [T, kv_heads, head_dim]."""
-    import torch
-    c = cache.packed()
-    sp = _flat(slots, torch.int64, "slots", None)
-    T, (_, hk, _, dim) = slots.shape[0], cache.k.shape
-    k = torch.empty((T, hk, dim), dtype=torch.bfloat16, device=slots.device) if k is None else k
-    v = torch.empty_like(k, memory_format=torch.contiguous_format) if v is None else v
-    _check(load().aq_kv_read(c, sp, T, *_heads(k, "k", T, hk, dim), *_heads(v, "v", T, hk, dim), _raw_stream(stream, k)))
+    if k is None or v is None:
+        import torch
+        if k is None:
+            _, heads, _, dim = cache.k.shape
+            k = torch.empty(slots.shape[0], heads, dim, dtype=torch.bfloat16, device=slots.device)
+        if v is None:
+            v = torch.empty_like(k)
+    st = _serve().kv_read(cache, slots, k, v, _raw_stream(stream, k))
+    if st:
+        _check(st)
     return k, v
+
+
+def aq_tree_attention_workspace_bytes(cache: KvCache, q_heads: int, batch: int, max_q: int, total_q: int) -> int:
+    """Bytes of device workspace of aq_tree_attention for `batch` sequences that bring at most max_q rows
+    each and total_q in all."""
+    need = _serve().attention_bytes(cache, q_heads, batch, max_q, total_q)
+    if need < 0:
+        raise AqError(AQ_ERR_INVALID_ARG, aq_last_error())
+    return need
 
 
 def aq_tree_attention(cache: KvCache, q, cu_q, ctx, page_table, max_q: int, mask=None, depth=None, window: int = 0,
@@ -727,46 +680,19 @@ def aq_tree_attention(cache: KvCache, q, cu_q, ctx, page_table, max_q: int, mask
     [total_q]. Returns out, or (out, lse [total_q, q_heads] fp32) with ``return_lse``. A workspace that is
     not given is allocated (its size: ``aq_tree_attention_workspace_bytes``)."""
     import torch
-    i32 = torch.int32
-    c = cache.packed()
     total, heads, dim = q.shape
     if out is None:
-        out = torch.empty(q.shape, dtype=q.dtype, device=q.device)
+        out = torch.empty_like(q)
     if lse is None and return_lse:
-        lse = torch.empty((total, heads), dtype=torch.float32, device=q.device)
-    if lse is not None and (lse.dtype is not torch.float32 or lse.shape != (total, heads) or not lse.is_contiguous()):
-        raise ValueError(f"lse: expected a contiguous float32 [{total}, {heads}] tensor")
-    batch, pages = page_table.shape
-    table, ld_table = _rows(page_table, i32, "page_table", batch, pages)
-    mp, ld_mask = (0, 0) if mask is None else _rows(mask, torch.int64, "mask", total, -(-max_q // 64))
-    d = _pack_batch(batch, max_q, total, _flat(cu_q, i32, "cu_q", batch + 1), _flat(ctx, i32, "ctx", batch), table, pages,
-                    ld_table, mp, ld_mask, 0 if depth is None else _flat(depth, i32, "depth", total), window)
-    qp, op = _heads(q, "q", total, heads, dim), _heads(out, "out", total, heads, dim)
-    lib = load()
-    if dim != cache.k.shape[3]:
-        raise ValueError(f"q: expected head_dim {cache.k.shape[3]}, got {dim}")
+        lse = torch.empty(total, heads, dtype=torch.float32, device=q.device)
     if workspace is None:
-        need = lib.aq_tree_attention_workspace_bytes(c, d, heads)
-        if need == _NO_SIZE:
-            raise AqError(AQ_ERR_INVALID_ARG, aq_last_error())
+        need = aq_tree_attention_workspace_bytes(cache, heads, page_table.shape[0], max_q, total)
         workspace = torch.empty(need, dtype=torch.uint8, device=q.device) if need else None
-    wp, wn = (0, 0) if workspace is None else (workspace.data_ptr(), workspace.nbytes)
-    _check(lib.aq_tree_attention(c, d, qp[0], heads, qp[1], qp[2], dim ** -0.5 if scale is None else scale, *op,
-                                 0 if lse is None else lse.data_ptr(), wp, wn, _raw_stream(stream, q)))
+    st = _serve().attention(cache, q, cu_q, ctx, page_table, max_q, mask, depth, window, dim ** -0.5 if scale is None else scale,
+                            out, lse, workspace, _raw_stream(stream, q))
+    if st:
+        _check(st)
     return (out, lse) if return_lse else out
-
-
-_NO_SIZE = ctypes.c_size_t(-1).value
-
-
-def aq_tree_attention_workspace_bytes(cache: KvCache, q_heads: int, batch: int, max_q: int, total_q: int) -> int:
-    """Bytes of device workspace of aq_tree_attention for `batch` sequences that bring at most max_q rows
-    each and total_q in all."""
-    d = _pack_batch(batch, max_q, total_q, 0, 0, 0, 0, 0, 0, 0, 0, 0)
-    need = load().aq_tree_attention_workspace_bytes(cache.packed(), d, q_heads)
-    if need == _NO_SIZE:
-        raise AqError(AQ_ERR_INVALID_ARG, aq_last_error())
-    return int(need)
 
 
 def aq_verify_drafts(p, tokens, cu, u, noise, q=None, parent=None, path_cap: int | None = None,
@@ -775,24 +701,13 @@ def aq_verify_drafts(p, tokens, cu, u, noise, q=None, parent=None, path_cap: int
     token [batch]), all int32. p (and q): [nodes + batch, vocab] fp32 or bf16; tokens, parent int32 [nodes]; cu
     int32 [batch + 1]; u fp32 [nodes]; noise fp32 [batch, vocab]. path_cap and max_nodes default to nodes."""
     import torch
-    i32, f32 = torch.int32, torch.float32
     nodes, batch = tokens.shape[0], cu.shape[0] - 1
-    rows, vocab = p.shape
-    if p.dtype is not f32 and p.dtype is not torch.bfloat16:
-        raise TypeError(f"p: expected a float32 or bfloat16 tensor, got {p.dtype}")
-    pp = _rows(p, p.dtype, "p", rows, vocab)
-    qq = (0, 0) if q is None else _rows(q, p.dtype, "q", rows, vocab)
-    nn = _rows(noise, f32, "noise", batch, vocab)
-    if noise.shape[1] != vocab or (q is not None and q.shape[1] != vocab):
-        raise ValueError(f"noise and q: expected {vocab} columns")
     path_cap = min(nodes, AQ_MAX_DRAFT_NODES) if path_cap is None else path_cap
     max_nodes = min(nodes, AQ_MAX_DRAFT_NODES) if max_nodes is None else max_nodes
-    both = torch.empty((2, batch), dtype=i32, device=p.device)
-    n_accepted, token = both[0], both[1]
-    path = torch.empty((batch, path_cap), dtype=i32, device=p.device)
-    _check(load().aq_verify_drafts(
-        batch, vocab, _flat(cu, i32, "cu", None), _flat(tokens, i32, "tokens", None),
-        0 if parent is None else _flat(parent, i32, "parent", nodes), nodes, max_nodes, *pp, *qq, rows,
-        AQ_PROB_F32 if p.dtype is f32 else AQ_PROB_BF16, _flat(u, f32, "u", nodes), *nn, n_accepted.data_ptr(),
-        path.data_ptr(), max(path_cap, 1), path_cap, token.data_ptr(), _raw_stream(stream, p)))
+    path = torch.empty(batch, path_cap, dtype=torch.int32, device=p.device)
+    n_accepted = torch.empty(batch, dtype=torch.int32, device=p.device)
+    token = torch.empty_like(n_accepted)
+    st = _serve().verify(p, tokens, cu, u, noise, q, parent, path_cap, max_nodes, n_accepted, path, token, _raw_stream(stream, p))
+    if st:
+        _check(st)
     return n_accepted, path, token

@@ -1,7 +1,8 @@
 """Builds the sm_103a shared library ``libaq_gb300.so`` in-tree with nvcc.
 
 The translation units are compiled in parallel and linked with the static CUDA runtime;
-the driver's tensor-map encoder is resolved at run time, so nothing else is linked.
+the driver's tensor-map encoder is resolved at run time, so nothing else is linked. The
+serving calls' marshalling module is compiled beside them by the host compiler.
 """
 from __future__ import annotations
 
@@ -9,6 +10,7 @@ import os
 import shutil
 import subprocess
 import sys
+import sysconfig
 
 PKG_DIR = os.path.dirname(os.path.abspath(__file__))
 ROOT = os.path.dirname(PKG_DIR)
@@ -24,6 +26,10 @@ SOURCES = ["aq_kernels.cu", "aq_decode.cu", "aq_decode2.cu", "aq_decompose.cu", 
            "aq_positions.cu", "aq_attention.cu", "aq_verify.cu"]
 HEADERS = ["aq_ptx.cuh", "aq_internal.h", "aq_serve.h"]
 
+# The serving calls' marshalling, a CPython module of host code (see csrc/aq_python.c).
+MARSHAL_SOURCE = "aq_python.c"
+MARSHAL_PATH = os.path.join(PKG_DIR, "_marshal.so")
+
 ARCH_FLAGS = ["-gencode", "arch=compute_103a,code=sm_103a"]
 NVCC_FLAGS = ["-O3", "-lineinfo", "-std=c++17", "-Xcompiler", "-fPIC", "-Xcompiler", "-O2",
               "--expt-relaxed-constexpr", f"-I{INCLUDE}", f"-I{CSRC}"]
@@ -37,17 +43,34 @@ def nvcc_path() -> str:
 
 
 def _inputs():
-    files = [os.path.join(CSRC, f) for f in SOURCES + HEADERS]
+    files = [os.path.join(CSRC, f) for f in SOURCES + HEADERS + [MARSHAL_SOURCE]]
     files.append(os.path.join(INCLUDE, "aq.h"))
     files.append(os.path.abspath(__file__))
     return files
 
 
 def up_to_date(lib: str = LIB_PATH) -> bool:
-    if not os.path.exists(lib):
+    if not os.path.exists(lib) or not os.path.exists(MARSHAL_PATH):
         return False
-    t = os.path.getmtime(lib)
+    t = min(os.path.getmtime(lib), os.path.getmtime(MARSHAL_PATH))
     return all(os.path.getmtime(f) <= t for f in _inputs())
+
+
+def build_marshal(verbose: bool = False) -> str:
+    """Compile the marshalling module with the host compiler (needs Python.h)."""
+    include = sysconfig.get_paths()["include"]
+    if not os.path.exists(os.path.join(include, "Python.h")):
+        raise RuntimeError(f"{include}/Python.h not found: the Python headers are required to build {MARSHAL_PATH}")
+    tmp = MARSHAL_PATH + f".{os.getpid()}.tmp"
+    cmd = [os.environ.get("CC") or shutil.which("gcc") or "cc", "-O2", "-shared", "-fPIC", "-fvisibility=hidden", f"-I{include}",
+           f"-I{INCLUDE}", os.path.join(CSRC, MARSHAL_SOURCE), "-o", tmp]
+    if verbose:
+        print(" ".join(cmd), file=sys.stderr)
+    r = subprocess.run(cmd, stdout=subprocess.PIPE, stderr=subprocess.STDOUT)
+    if r.returncode != 0:
+        raise RuntimeError(f"{cmd[0]} failed on {MARSHAL_SOURCE}:\n{r.stdout.decode(errors='replace')}")
+    os.replace(tmp, MARSHAL_PATH)
+    return MARSHAL_PATH
 
 
 def build(force: bool = False, verbose: bool = False, debug: bool = False) -> str:
@@ -67,6 +90,7 @@ def build(force: bool = False, verbose: bool = False, debug: bool = False) -> st
         if verbose:
             print(" ".join(cmd), file=sys.stderr)
         procs.append((src, obj, subprocess.Popen(cmd, stdout=subprocess.PIPE, stderr=subprocess.STDOUT)))
+    build_marshal(verbose)
     objs = []
     for src, obj, p in procs:
         out, _ = p.communicate()

@@ -166,7 +166,7 @@ struct Shape {
   static constexpr int kCols = 32;   // columns joined at a time
   static constexpr int kJoinLd = kCols + 4;
   static constexpr int kJoin = NW * 8 * NR * kJoinLd * 4;
-  static_assert(kJoin >= kThreads * 8 && M <= kAttnMaxRows && 8 * NR <= 32, "shared arrays");
+  static_assert(M <= kAttnMaxRows && 8 * NR <= 32, "shared arrays");
 };
 
 struct AttnShared {
@@ -174,6 +174,7 @@ struct AttnShared {
   uint32_t valid[kAttnStages];
   int32_t abort;
   int64_t start_entry, start_tile;      // where this CTA begins: entry, tile within it
+  int64_t part[kAttnMaxWarps + 4];
   float m[kAttnMaxWarps][32], l[kAttnMaxWarps][32];
   float fac[kAttnMaxRows];                       // of a row's raw products, to base-2 logits; not negative
   int64_t pos[kAttnMaxRows];                  // of a row
@@ -207,12 +208,11 @@ __device__ __forceinline__ Span entry_span(const AttnParams& p, int b, int rt) {
   return s;
 }
 
-// Where tile number `at` of the whole call lies; called by every thread, the answer in sh; `part` holds
-// a number for each thread. CTA 0 also leaves
+// Where tile number `at` of the whole call lies; called by every thread, the answer in sh. CTA 0 also leaves
 // the entries' first tiles for the joining launch.
 template <int M, int KS>
-__device__ __forceinline__ void locate(const AttnParams& p, AttnShared& sh, int64_t* part, int64_t* prefix, bool write,
-                                          int64_t (&range)[2]) {
+__device__ __forceinline__ void locate(const AttnParams& p, AttnShared& sh, int64_t* prefix, bool write,
+                                       int64_t (&range)[2]) {
   const int n = p.batch * p.row_tiles, tid = threadIdx.x;
   const int threads = blockDim.x;
   const int per = (n + threads - 1) / threads;
@@ -222,13 +222,18 @@ __device__ __forceinline__ void locate(const AttnParams& p, AttnShared& sh, int6
     const Span s = entry_span<M, KS>(p, e / p.row_tiles, e % p.row_tiles);
     sum += static_cast<int64_t>(s.t1 - s.t0) * p.hk;
   }
-  part[tid] = sum;
+  int64_t upto = sum;   // within the warp, this thread's own among them
+#pragma unroll
+  for (int off = 1; off < 32; off *= 2) {
+    const int64_t v = __shfl_up_sync(0xffffffffu, upto, off);
+    if ((tid & 31) >= off) upto += v;
+  }
+  if ((tid & 31) == 31) sh.part[tid >> 5] = upto;
   __syncthreads();
-  int64_t before = 0, total = 0;
-  for (int i = 0; i < threads; ++i) {
-    const int64_t v = part[i];
-    before += i < tid ? v : 0;
-    total += v;
+  int64_t before = upto - sum, total = 0;
+  for (int i = 0; i < threads / 32; ++i) {
+    if (i < (tid >> 5)) before += sh.part[i];
+    total += sh.part[i];
   }
   const int64_t share = (total + gridDim.x - 1) / gridDim.x;
   range[0] = min(share * blockIdx.x, total);
@@ -428,23 +433,52 @@ __device__ __forceinline__ void load_queries(const AttnParams& p, AttnShared& sh
   }
 }
 
-// Whether row r of the tile sees a key.
+// The step's keys that each of a warp's rows sees, as bits: lane r answers for row r (rows 8 NR, keys CK <= 32;
+// ka: the first key, k0: its place in the tile). One round of loads, whatever the mask.
 template <class S>
-__device__ __forceinline__ bool visible(const AttnParams& p, const AttnShared& sh, const Span& s, int r, int64_t key,
-                                        uint32_t pages, int box_shift, int in_tile) {
-  if (key >= s.hi || !((pages >> (in_tile >> box_shift)) & 1)) return false;
-  const int64_t t = key - s.ctx;
-  int64_t at = key;
-  if (t >= 0) {
-    const int i = sh.i[r];
+__device__ __forceinline__ uint32_t seen_bits(const AttnParams& p, const AttnShared& sh, const Span& s, int rg, int64_t ka,
+                                              int k0, uint32_t pages, int box_shift) {
+  const int lane = threadIdx.x & 31;
+  constexpr uint32_t kAll = S::CK == 32 ? 0xffffffffu : (1u << S::CK) - 1;
+  auto below = [](int64_t n) { return n <= 0 ? 0u : n >= 32 ? 0xffffffffu : (1u << n) - 1; };   // bits [0, n)
+  const int r = rg * 8 * S::NR + min(lane, 8 * S::NR - 1);
+  const int i = sh.i[r];
+  const int64_t pos = sh.pos[r];
+  uint32_t bits = below(s.hi - ka) & kAll;
+  for (int k = 0; k < S::CK; k += 1 << min(box_shift, 5))
+    if (!((pages >> ((k0 + k) >> box_shift)) & 1)) bits &= ~(below(1 << min(box_shift, 5)) << k);
+  const int64_t t0 = ka - s.ctx;                  // drafted index of the first key (negative: context)
+  uint32_t drafted = ~below(-t0);                 // which keys are drafted ones
+  if (drafted) {
+    uint32_t see;
     if (p.mask) {
-      if (!((p.mask[(static_cast<int64_t>(s.first) + i) * p.ld_mask + (t >> 6)] >> (t & 63)) & 1)) return false;
-      if (p.window > 0 && p.depth) at = static_cast<int64_t>(s.ctx) + max(p.depth[s.first + t], 0);
-    } else if (t > i) {
-      return false;
+      const uint64_t* m = p.mask + (static_cast<int64_t>(s.first) + i) * p.ld_mask;
+      const int64_t at = max(t0, static_cast<int64_t>(0));
+      const int last = (s.T - 1) >> 6, w0 = min(static_cast<int>(at >> 6), last), w1 = min(w0 + 1, last);
+      const uint64_t lo = m[w0], hi = m[w1];
+      const int sh0 = static_cast<int>(at & 63);
+      const uint64_t v = sh0 ? (lo >> sh0) | (hi << (64 - sh0)) : lo;
+      see = t0 < 0 ? static_cast<uint32_t>(v) << static_cast<int>(-t0) : static_cast<uint32_t>(v);
+    } else {
+      see = below(i - t0 + 1);
+    }
+    bits &= ~drafted | see;
+  }
+  if (p.window > 0) {
+    // context (and a chain's) keys lie at their index; a tree's drafted ones at their depth
+    const bool tree = p.mask && p.depth;
+    const uint32_t indexed = tree ? ~drafted : 0xffffffffu;
+    bits &= ~indexed | ~below(pos - p.window + 1 - ka);
+    if (tree && drafted) {
+      const int64_t t = t0 + lane;
+      const int d = t >= 0 && t < s.T ? max(p.depth[s.first + t], 0) : 0;
+      for (int k = 0; k < S::CK; ++k) {
+        const int dk = __shfl_sync(0xffffffffu, d, k);
+        if (((drafted >> k) & 1) && pos - (static_cast<int64_t>(s.ctx) + dk) >= p.window) bits &= ~(1u << k);
+      }
     }
   }
-  return p.window <= 0 || sh.pos[r] - at < p.window;
+  return bits;
 }
 
 // A warp's sums for its rows 2 t + {0, 1} of each of NR groups of eight.
@@ -564,18 +598,20 @@ __device__ __forceinline__ void step(const AttnParams& p, const AttnShared& sh, 
       }
   }
   if constexpr (!WHOLE) {
+    const uint32_t bits = seen_bits<S>(p, sh, span, info.rg, info.key0 + k0, k0, info.pages, info.box_shift);
 #pragma unroll
-    for (int j = 0; j < KT; ++j)
+    for (int n = 0; n < NR; ++n)
 #pragma unroll
-      for (int n = 0; n < NR; ++n)
+      for (int c = 0; c < 2; ++c) {
+        const uint32_t mine_bits = __shfl_sync(0xffffffffu, bits, 8 * n + 2 * t + c) >> g;
 #pragma unroll
-        for (int c = 0; c < 4; ++c) {
-          const int in_tile = k0 + 16 * j + 8 * (c >> 1) + g;
-          const bool see = visible<S>(p, sh, span, info.rg * 8 * NR + 8 * n + 2 * t + (c & 1), info.key0 + in_tile, info.pages,
-                                      info.box_shift, in_tile);
-          if (!see) sc[j][n][c] = -INFINITY;
-          else if (S::E4M3) vmax = fmaxf(vmax, vs[j][c >> 1]);
-        }
+        for (int j = 0; j < KT; ++j)
+#pragma unroll
+          for (int h = 0; h < 2; ++h) {
+            if (!((mine_bits >> (16 * j + 8 * h)) & 1)) sc[j][n][2 * h + c] = -INFINITY;
+            else if (S::E4M3) vmax = fmaxf(vmax, vs[j][h]);
+          }
+      }
   }
   // the maxima: looked at by each lane for itself, put together only where one is passed
   float mt[NR][2];
@@ -879,7 +915,7 @@ __global__ void __launch_bounds__(S::kThreads, S::kPerSm) aq_tree_attention_kern
   }
   pdl_wait_prior_grid();
   int64_t range[2];
-  locate<S::M, S::KS>(p, sh, reinterpret_cast<int64_t*>(join), p.prefix, blockIdx.x == 0, range);
+  locate<S::M, S::KS>(p, sh, p.prefix, blockIdx.x == 0, range);
   const AbortCtl ctl = {&sh.abort, p.status, p.timeout_ns};
   if (threadIdx.x >= S::NW * 32) {
     // 384 threads at 168 registers: 256 at 232 and 128 at 40

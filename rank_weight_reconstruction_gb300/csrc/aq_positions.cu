@@ -17,8 +17,8 @@
 // Both are bound by memory: every element is read once and written once. A group of lanes owns one
 // token's vector, each lane two 16-byte chunks of it (in the half layout the two that rotate against
 // each other), so a vector is loaded in whole 128-byte lines and its maximum is a few shuffles. The
-// eight sines and cosines of a lane depend on the token alone, so a group walks `hb` heads of its token
-// with them in registers; hb is 1 while the call is too small to fill the GPU.
+// eight sines and cosines of a lane depend on the token alone, so a group walks several heads of its token
+// with them in registers, two heads' loads in flight.
 #include <math.h>
 
 #include <algorithm>
@@ -137,8 +137,7 @@ struct PosParams {
   int32_t rot16;          // rotary_dim / 16
   float magnitude, sin_sign;
   int32_t page_shift;
-  int32_t hb;             // heads one group walks
-  int32_t head_blocks;
+  int32_t hl_shift;       // log2 of the groups that share a token, each taking every hl-th head
 };
 
 // Not through the read-only path: in place, the same lane writes the chunk back.
@@ -163,21 +162,26 @@ __device__ __forceinline__ uint4 pack8(const float (&x)[8]) {
                     pack_bf16x2_cvt(x[6], x[7]));
 }
 
-// Two chunks of eight elements of a vector per lane: which ones, and how they rotate.
+// The two chunks of eight elements that lane u of a vector holds: load 0 of the lanes covers one stretch of
+// memory, load 1 another. In the half layout a rotating lane's chunks rotate against each other.
 template <bool HALF>
 struct Chunks {
-  int c0, c1;      // chunk indices (element / 8); c1 may lie past the vector
-  bool rotates;
-  __device__ __forceinline__ Chunks(int u, int rot16) {
-    rotates = u < rot16;
+  int c0, c1;        // chunk indices (element / 8)
+  bool turns0, turns1;
+  __device__ __forceinline__ Chunks(int u, int rot16, int d16) {
     if (HALF) {
-      c0 = rotates ? u : 2 * u;
-      c1 = rotates ? u + rot16 : 2 * u + 1;
+      c0 = u < rot16 ? u : u + rot16;
+      c1 = u < rot16 ? u + rot16 : u + d16;
+      turns0 = turns1 = u < rot16;
     } else {
-      c0 = 2 * u;
-      c1 = 2 * u + 1;
+      c0 = u;
+      c1 = u + d16;
+      turns0 = c0 < 2 * rot16;
+      turns1 = c1 < 2 * rot16;
     }
   }
+  // index of pair i (of eight) among the frequencies
+  __device__ __forceinline__ int pair(int u, int i) const { return HALF ? u * 8 + i : (i < 4 ? c0 * 4 + i : c1 * 4 + i - 4); }
 };
 
 template <bool HALF>
@@ -203,32 +207,47 @@ __device__ __forceinline__ void rotate16(float (&a)[8], float (&b)[8], const flo
 }
 
 // GW lanes per vector (a power of two, >= D / 16).
-template <bool HALF, int GW, bool E4M3>
-__global__ void __launch_bounds__(256) aq_positions_kernel(const __grid_constant__ PosParams p) {
+// SPLIT: the groups of a warp are at one token.
+template <bool HALF, int GW, bool E4M3, bool SPLIT>
+__global__ void __launch_bounds__(256, 4) aq_positions_kernel(const __grid_constant__ PosParams p) {
   pdl_wait_prior_grid();
   pdl_launch_dependents();
   const int u = threadIdx.x % GW;
   const int64_t item = static_cast<int64_t>(blockIdx.x) * (256 / GW) + threadIdx.x / GW;
-  const int64_t t = item / p.head_blocks;
-  const int h0 = static_cast<int>(item - t * p.head_blocks) * p.hb;
+  const int64_t t = item >> p.hl_shift;
+  const int hl = 1 << p.hl_shift, h0 = static_cast<int>(item & (hl - 1));
   const int heads = p.hq + 2 * p.hk;
-  const bool live = t < p.T;
+  const bool live = t < p.T && u * 16 < p.D;
   const int64_t tt = live ? t : 0;
-  const Chunks<HALF> ch(u, p.rot16);
-  const bool has0 = live && ch.c0 * 8 < p.D, has1 = live && ch.c1 * 8 < p.D;
+  const Chunks<HALF> ch(u, p.rot16, p.D / 16);
 
-  // this token's sines and cosines, for the eight pairs the lane rotates
+  // This token's sines and cosines, for the eight pairs the lane rotates. Where the warp's groups share the token,
+  // each works out its part of the eight and passes it round.
+  constexpr int kShare = SPLIT ? (32 / GW < 8 ? 32 / GW : 8) : 1;
   float c[8], s[8];
-  const bool turn = p.freq != nullptr && ch.rotates && live && h0 < p.hq + p.hk;
-  if (turn) {
-    const int64_t pos = p.pos[tt];
+  const bool turn = p.freq != nullptr && (ch.turns0 || ch.turns1) && live && h0 < p.hq + p.hk;
+  {
+    const int64_t pos = p.freq && live ? p.pos[tt] : 0;
+    const int lane = threadIdx.x & 31, part = SPLIT ? (lane / GW) % kShare : 0;
+    float cm[8 / kShare], sm[8 / kShare];
+#pragma unroll
+    for (int k = 0; k < 8 / kShare; ++k) {
+      const int i = k * kShare + part;
+      cm[k] = 1.0f;
+      sm[k] = 0.0f;
+      if (p.freq && (i < 4 ? ch.turns0 : ch.turns1)) {   // half layout: both or neither
+        const uint64_t phase = static_cast<uint64_t>(pos) * p.freq[ch.pair(u, i)];
+        float sn, cs;
+        sincospif(static_cast<float>(static_cast<int32_t>(phase >> 32)) * 0x1p-31f, &sn, &cs);
+        cm[k] = cs * p.magnitude;
+        sm[k] = sn * p.sin_sign;
+      }
+    }
 #pragma unroll
     for (int i = 0; i < 8; ++i) {
-      const uint64_t phase = static_cast<uint64_t>(pos) * p.freq[u * 8 + i];
-      float sn, cs;
-      sincospif(static_cast<float>(static_cast<int32_t>(phase >> 32)) * 0x1p-31f, &sn, &cs);
-      c[i] = cs * p.magnitude;
-      s[i] = sn * p.sin_sign;
+      const int from = (lane & ~(GW * kShare - 1)) + (i % kShare) * GW + u;
+      c[i] = SPLIT ? __shfl_sync(0xffffffffu, cm[i / kShare], from) : cm[i / kShare];
+      s[i] = SPLIT ? __shfl_sync(0xffffffffu, sm[i / kShare], from) : sm[i / kShare];
     }
   }
   int64_t cell0 = -1;
@@ -240,43 +259,40 @@ __global__ void __launch_bounds__(256) aq_positions_kernel(const __grid_constant
 
   // groups of one warp may be at different kinds of heads, so each shuffles by itself
   const uint32_t group = (GW == 32 ? 0xffffffffu : (1u << GW) - 1) << ((threadIdx.x & 31) & ~(GW - 1));
-  const int h1 = min(h0 + p.hb, heads);
-  for (int h = h0; h < h1; ++h) {
-    const uint16_t* src;
-    if (h < p.hq) src = p.q + tt * p.q_tok + h * p.q_head;
-    else if (h < p.hq + p.hk) src = p.k + tt * p.k_tok + (h - p.hq) * p.k_head;
-    else src = p.v + tt * p.v_tok + (h - p.hq - p.hk) * p.v_head;
-    const uint4 zero = make_uint4(0, 0, 0, 0);
-    const uint4 r0 = has0 ? ld_stream(src + ch.c0 * 8) : zero;
-    const uint4 r1 = has1 ? ld_stream(src + ch.c1 * 8) : zero;
+  const uint4 zero = make_uint4(0, 0, 0, 0);
+  auto source = [&](int h) {
+    if (h < p.hq) return p.q + tt * p.q_tok + h * p.q_head;
+    if (h < p.hq + p.hk) return p.k + tt * p.k_tok + (h - p.hq) * p.k_head;
+    return p.v + tt * p.v_tok + (h - p.hq - p.hk) * p.v_head;
+  };
+  auto finish = [&](int h, const uint4& r0, const uint4& r1) {
     const bool is_v = h >= p.hq + p.hk;
-    if (!turn || is_v) {
-      if (h < p.hq) {   // nothing rotates in this lane's part
-        uint16_t* dst = p.qo + tt * p.qo_tok + h * p.qo_head;
-        if (has0) *reinterpret_cast<uint4*>(dst + ch.c0 * 8) = r0;
-        if (has1) *reinterpret_cast<uint4*>(dst + ch.c1 * 8) = r1;
-        continue;
-      }
+    const bool turns = turn && !is_v;
+    if (h < p.hq && !turns) {   // nothing rotates in this lane's part
+      uint16_t* dst = p.qo + tt * p.qo_tok + h * p.qo_head;
+      if (live) *reinterpret_cast<uint4*>(dst + ch.c0 * 8) = r0;
+      if (live) *reinterpret_cast<uint4*>(dst + ch.c1 * 8) = r1;
+      return;
     }
     float a[8], b[8];
     unpack8(r0, a);
     unpack8(r1, b);
-    if (turn && !is_v) rotate16<HALF>(a, b, c, s);
+    if (turns) rotate16<HALF>(a, b, c, s);
     if (h < p.hq) {
       uint16_t* dst = p.qo + tt * p.qo_tok + h * p.qo_head;
-      if (has0) *reinterpret_cast<uint4*>(dst + ch.c0 * 8) = pack8(a);
-      if (has1) *reinterpret_cast<uint4*>(dst + ch.c1 * 8) = pack8(b);
-      continue;
+      if (live) *reinterpret_cast<uint4*>(dst + ch.c0 * 8) = pack8(a);
+      if (live) *reinterpret_cast<uint4*>(dst + ch.c1 * 8) = pack8(b);
+      return;
     }
     const int hh = h - p.hq - (is_v ? p.hk : 0);
     const int64_t cell = cell0 + (static_cast<int64_t>(hh) << p.page_shift);
     uint8_t* base = is_v ? p.vc : p.kc;
     if (!E4M3) {
-      if (cell0 < 0) continue;
+      if (cell0 < 0) return;
       uint16_t* dst = reinterpret_cast<uint16_t*>(base) + cell * p.D;
-      if (has0) *reinterpret_cast<uint4*>(dst + ch.c0 * 8) = pack8(a);
-      if (has1) *reinterpret_cast<uint4*>(dst + ch.c1 * 8) = pack8(b);
-      continue;
+      if (live) *reinterpret_cast<uint4*>(dst + ch.c0 * 8) = pack8(a);
+      if (live) *reinterpret_cast<uint4*>(dst + ch.c1 * 8) = pack8(b);
+      return;
     }
     // max|x| on the bit patterns: a NaN or infinity stays the largest
     uint32_t top = 0;
@@ -285,28 +301,29 @@ __global__ void __launch_bounds__(256) aq_positions_kernel(const __grid_constant
       top = max(top, max(__float_as_uint(a[i]) & 0x7fffffffu, __float_as_uint(b[i]) & 0x7fffffffu));
 #pragma unroll
     for (int o = GW / 2; o > 0; o >>= 1) top = max(top, __shfl_xor_sync(group, top, o));
-    if (cell0 < 0) continue;
+    if (cell0 < 0) return;
     const bool finite = top < 0x7f800000u;
     const float scale = finite ? fmaxf(__uint_as_float(top) * (1.0f / kE4m3Max), kKvScaleFloor) : __uint_as_float(0x7fc00000u);
     const float inv = finite ? __frcp_rn(scale) : 0.0f;
     uint8_t* dst = base + cell * p.D;
-    if (has0) {
-      uint2 w = make_uint2(0, 0);
-      if (finite) {
-        w.x = e4m3x2_from_f32(a[0] * inv, a[1] * inv) | (static_cast<uint32_t>(e4m3x2_from_f32(a[2] * inv, a[3] * inv)) << 16);
-        w.y = e4m3x2_from_f32(a[4] * inv, a[5] * inv) | (static_cast<uint32_t>(e4m3x2_from_f32(a[6] * inv, a[7] * inv)) << 16);
-      }
-      *reinterpret_cast<uint2*>(dst + ch.c0 * 8) = w;
-    }
-    if (has1) {
-      uint2 w = make_uint2(0, 0);
-      if (finite) {
-        w.x = e4m3x2_from_f32(b[0] * inv, b[1] * inv) | (static_cast<uint32_t>(e4m3x2_from_f32(b[2] * inv, b[3] * inv)) << 16);
-        w.y = e4m3x2_from_f32(b[4] * inv, b[5] * inv) | (static_cast<uint32_t>(e4m3x2_from_f32(b[6] * inv, b[7] * inv)) << 16);
-      }
-      *reinterpret_cast<uint2*>(dst + ch.c1 * 8) = w;
-    }
+    auto codes = [&](const float (&x)[8]) {
+      if (!finite) return make_uint2(0, 0);
+      return make_uint2(e4m3x2_from_f32(x[0] * inv, x[1] * inv) | (static_cast<uint32_t>(e4m3x2_from_f32(x[2] * inv, x[3] * inv)) << 16),
+                        e4m3x2_from_f32(x[4] * inv, x[5] * inv) | (static_cast<uint32_t>(e4m3x2_from_f32(x[6] * inv, x[7] * inv)) << 16));
+    };
+    if (live) *reinterpret_cast<uint2*>(dst + ch.c0 * 8) = codes(a);
+    if (live) *reinterpret_cast<uint2*>(dst + ch.c1 * 8) = codes(b);
     if (u == 0) (is_v ? p.vs : p.ks)[cell] = scale;
+  };
+  // two heads' loads in flight
+  for (int h = h0; h < heads; h += 2 * hl) {
+    const bool two = h + hl < heads;
+    const uint16_t* s0 = source(h);
+    const uint16_t* s1 = source(two ? h + hl : h);
+    const uint4 r0 = live ? ld_stream(s0 + ch.c0 * 8) : zero, r1 = live ? ld_stream(s0 + ch.c1 * 8) : zero;
+    const uint4 r2 = live && two ? ld_stream(s1 + ch.c0 * 8) : zero, r3 = live && two ? ld_stream(s1 + ch.c1 * 8) : zero;
+    finish(h, r0, r1);
+    if (two) finish(h + hl, r2, r3);
   }
 }
 
@@ -320,8 +337,8 @@ struct ReadParams {
   int32_t hk, D, page_shift;
 };
 
-// One group of GW lanes per vector; blockIdx.y 0: keys, 1: values. A slot outside the cache reads
-// as zeros.
+// One group of GW lanes per token and head, two chunks of eight elements of its key and of its value a lane (chunk u
+// and chunk D / 16 + u: each load and store of the group covers one stretch), all four loads in flight. A slot outside the cache reads as zeros.
 template <int GW, bool E4M3>
 __global__ void __launch_bounds__(256) aq_kv_read_kernel(const __grid_constant__ ReadParams p) {
   pdl_wait_prior_grid();
@@ -329,51 +346,68 @@ __global__ void __launch_bounds__(256) aq_kv_read_kernel(const __grid_constant__
   const int u = threadIdx.x % GW;
   const int64_t item = static_cast<int64_t>(blockIdx.x) * (256 / GW) + threadIdx.x / GW;
   const int64_t t = item / p.hk;
-  if (t >= p.T) return;
+  if (t >= p.T || u * 16 >= p.D) return;
   const int h = static_cast<int>(item - t * p.hk);
-  const int w = blockIdx.y;
-  if (!p.o[w] || u * 16 >= p.D) return;
-  uint16_t* dst = p.o[w] + t * p.o_tok[w] + h * p.o_head[w] + u * 16;
   const int64_t slot = p.slots[t];
-  uint4 lo = make_uint4(0, 0, 0, 0), hi = lo;
-  if (slot >= 0 && slot < p.n_slots) {
-    const int64_t cell = ((((slot >> p.page_shift) * p.hk) + h) << p.page_shift) + (slot & ((1 << p.page_shift) - 1));
+  const bool held = slot >= 0 && slot < p.n_slots;
+  const int64_t cell = ((((slot >> p.page_shift) * p.hk) + h) << p.page_shift) + (slot & ((1 << p.page_shift) - 1));
+  uint4 r[2][2];
+  float s[2];
+#pragma unroll
+  for (int w = 0; w < 2; ++w) {
+    r[w][0] = r[w][1] = make_uint4(0, 0, 0, 0);
+    s[w] = 0.0f;
+    if (!p.o[w] || !held) continue;
+    const uint8_t* src = p.c[w] + (cell * p.D + u * 8) * (E4M3 ? 1 : 2);
     if (E4M3) {
-      const float s = p.s[w][cell];
-      const uint4 r = *reinterpret_cast<const uint4*>(p.c[w] + cell * p.D + u * 16);
-      const uint32_t q[4] = {r.x, r.y, r.z, r.w};
+      s[w] = p.s[w][cell];
+      const uint2 lo = *reinterpret_cast<const uint2*>(src), hi = *reinterpret_cast<const uint2*>(src + p.D / 2);
+      r[w][0] = make_uint4(lo.x, lo.y, hi.x, hi.y);
+    } else {
+      r[w][0] = *reinterpret_cast<const uint4*>(src);
+      r[w][1] = *reinterpret_cast<const uint4*>(src + p.D);
+    }
+  }
+#pragma unroll
+  for (int w = 0; w < 2; ++w) {
+    if (!p.o[w]) continue;
+    uint16_t* dst = p.o[w] + t * p.o_tok[w] + h * p.o_head[w] + u * 8;
+    if (E4M3) {
+      const uint32_t q[4] = {r[w][0].x, r[w][0].y, r[w][0].z, r[w][0].w};
       uint32_t o[8];
 #pragma unroll
       for (int i = 0; i < 8; ++i) {
         const uint32_t f = f16x2_from_e4m3x2(static_cast<uint16_t>(q[i / 2] >> (16 * (i & 1))));
         const float2 v = __half22float2(*reinterpret_cast<const __half2*>(&f));
-        o[i] = pack_bf16x2_cvt(v.x * s, v.y * s);
+        o[i] = pack_bf16x2_cvt(v.x * s[w], v.y * s[w]);
       }
-      lo = make_uint4(o[0], o[1], o[2], o[3]);
-      hi = make_uint4(o[4], o[5], o[6], o[7]);
-    } else {
-      const uint4* src = reinterpret_cast<const uint4*>(p.c[w] + (cell * p.D + u * 16) * 2);
-      lo = src[0];
-      hi = src[1];
+      r[w][0] = make_uint4(o[0], o[1], o[2], o[3]);
+      r[w][1] = make_uint4(o[4], o[5], o[6], o[7]);
     }
+    *reinterpret_cast<uint4*>(dst) = r[w][0];
+    *reinterpret_cast<uint4*>(dst + p.D / 2) = r[w][1];
   }
-  reinterpret_cast<uint4*>(dst)[0] = lo;
-  reinterpret_cast<uint4*>(dst)[1] = hi;
 }
 
+template <bool HALF, int GW, bool E4M3>
+cudaError_t launch_positions(const PosParams& p, unsigned blocks, cudaStream_t st) {
+  if (GW < 32 && (GW << p.hl_shift) >= 32)
+    return launch_serve(aq_positions_kernel<HALF, GW, E4M3, true>, p, blocks, 256, 0, st);
+  return launch_serve(aq_positions_kernel<HALF, GW, E4M3, false>, p, blocks, 256, 0, st);
+}
 template <bool HALF, bool E4M3>
 cudaError_t launch_positions(const PosParams& p, unsigned blocks, int gw, cudaStream_t st) {
   switch (gw) {
-    case 1: return launch_serve(aq_positions_kernel<HALF, 1, E4M3>, p, blocks, 256, 0, st);
-    case 2: return launch_serve(aq_positions_kernel<HALF, 2, E4M3>, p, blocks, 256, 0, st);
-    case 4: return launch_serve(aq_positions_kernel<HALF, 4, E4M3>, p, blocks, 256, 0, st);
-    case 8: return launch_serve(aq_positions_kernel<HALF, 8, E4M3>, p, blocks, 256, 0, st);
-    default: return launch_serve(aq_positions_kernel<HALF, 16, E4M3>, p, blocks, 256, 0, st);
+    case 1: return launch_positions<HALF, 1, E4M3>(p, blocks, st);
+    case 2: return launch_positions<HALF, 2, E4M3>(p, blocks, st);
+    case 4: return launch_positions<HALF, 4, E4M3>(p, blocks, st);
+    case 8: return launch_positions<HALF, 8, E4M3>(p, blocks, st);
+    default: return launch_positions<HALF, 16, E4M3>(p, blocks, st);
   }
 }
 
 template <bool E4M3>
-cudaError_t launch_read(const ReadParams& p, dim3 grid, int gw, cudaStream_t st) {
+cudaError_t launch_read(const ReadParams& p, unsigned grid, int gw, cudaStream_t st) {
   switch (gw) {
     case 1: return launch_serve(aq_kv_read_kernel<1, E4M3>, p, grid, 256, 0, st);
     case 2: return launch_serve(aq_kv_read_kernel<2, E4M3>, p, grid, 256, 0, st);
@@ -394,19 +428,21 @@ int log2_of(int v) {
   return s;
 }
 
-// Grid of a positions launch: heads per group grow while the groups still fill the GPU four times
-// over, up to eight (the sines then cost an eighth of a head's time).
+// Grid of a positions launch. The groups that share a token take neighbouring heads and each walks the rest of
+// them with its angles: as many as a warp holds, so that the angles are worked out once a warp (and 512 bytes to
+// 2 KB read in one stretch where heads are the inner dimension), more while the call does not fill half the GPU.
 aq_status run_positions(PosParams& p, bool half, bool e4m3, cudaStream_t st, const char* who) {
   ServeDev dev;
   aq_status s = serve_device(&dev);
   if (s != AQ_OK) return s;
   const int heads = p.hq + 2 * p.hk;
   const int gw = group_width(p.D);
-  const int64_t fill = static_cast<int64_t>(dev.sms) * 2048 / gw * 4;
-  p.hb = 1;
-  while (p.hb < 8 && p.hb < heads && p.T * ((heads + 2 * p.hb - 1) / (2 * p.hb)) >= fill) p.hb *= 2;
-  p.head_blocks = (heads + p.hb - 1) / p.hb;
-  const int64_t blocks = (p.T * p.head_blocks + 256 / gw - 1) / (256 / gw);
+  const int64_t fill = static_cast<int64_t>(dev.sms) * 1024 / gw;
+  int most = 0;   // no more groups than heads, and a block's at most
+  while ((2 << most) <= heads && (2 << most) <= 256 / gw) ++most;
+  p.hl_shift = std::min(log2_of(32 / gw), most);
+  while (p.hl_shift < most && (p.T << p.hl_shift) < fill) ++p.hl_shift;
+  const int64_t blocks = ((p.T << p.hl_shift) + 256 / gw - 1) / (256 / gw);
   if (blocks > 0x7fffffffLL) return serve_fail(AQ_ERR_SHAPE, "%s: %lld tokens are too many for one call", who, (long long)p.T);
   const unsigned g = static_cast<unsigned>(blocks);
   cudaError_t e = half ? (e4m3 ? launch_positions<true, true>(p, g, gw, st) : launch_positions<true, false>(p, g, gw, st))
@@ -679,7 +715,7 @@ extern "C" aq_status aq_kv_read(const aq_kv_cache* cache, const int64_t* slots, 
   const int gw = group_width(D);
   const int64_t blocks = (T * hk + 256 / gw - 1) / (256 / gw);
   if (blocks > 0x7fffffffLL) return serve_fail(AQ_ERR_SHAPE, "%s: %lld tokens are too many for one call", who, (long long)T);
-  const dim3 grid(static_cast<unsigned>(blocks), 2);
+  const unsigned grid = static_cast<unsigned>(blocks);
   const cudaStream_t cs = static_cast<cudaStream_t>(stream);
   return serve_launched(cache->type == AQ_KV_E4M3 ? launch_read<true>(p, grid, gw, cs) : launch_read<false>(p, grid, gw, cs), who);
 }

@@ -14,12 +14,16 @@
 // their maxima (packed value and index, so the order does not matter and the lowest index wins) through
 // distributed shared memory: one launch, no workspace. Only a refused child that has siblings left, with
 // q given, needs a normaliser in between: one more pass, its partial sums added in rank order by every CTA.
+#include <atomic>
+
 #include "aq_serve.h"
 
 namespace aq {
 namespace {
 
-constexpr int kVerThreads = 512;
+// Threads of a CTA: 1024 where the clusters of a call leave SMs to spare (one sequence then loads its rows
+// in one or two rounds), else 256, four CTAs an SM.
+constexpr int kVerWide = 1024, kVerNarrow = 256;
 constexpr int kVerMaxCluster = 16;
 
 struct VerifyParams {
@@ -35,7 +39,7 @@ struct VerifyParams {
   int32_t* n_accepted;
   int32_t* path;
   int32_t* token;
-  int32_t vocab, max_nodes, path_cap, cluster;
+  int32_t vocab, max_nodes, path_cap, cluster, device;
 };
 
 __device__ __forceinline__ float prob(const float* p, int64_t i) { return p[i]; }
@@ -61,12 +65,25 @@ struct Vec<float, 4> {
   }
 };
 template <>
-struct Vec<uint16_t, 4> {
-  float x[4];
+struct Vec<uint16_t, 8> {
+  float x[8];
   __device__ __forceinline__ void load(const uint16_t* p) {
-    const uint2 r = __ldg(reinterpret_cast<const uint2*>(p));
-    x[0] = __uint_as_float(r.x << 16); x[1] = __uint_as_float(r.x & 0xffff0000u);
-    x[2] = __uint_as_float(r.y << 16); x[3] = __uint_as_float(r.y & 0xffff0000u);
+    const uint4 r = __ldg(reinterpret_cast<const uint4*>(p));
+    const uint32_t w[4] = {r.x, r.y, r.z, r.w};
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      x[2 * i] = __uint_as_float(w[i] << 16);
+      x[2 * i + 1] = __uint_as_float(w[i] & 0xffff0000u);
+    }
+  }
+};
+template <>
+struct Vec<float, 8> {
+  float x[8];
+  __device__ __forceinline__ void load(const float* p) {
+    const float4 r = __ldg(reinterpret_cast<const float4*>(p)), s = __ldg(reinterpret_cast<const float4*>(p) + 1);
+    x[0] = r.x; x[1] = r.y; x[2] = r.z; x[3] = r.w;
+    x[4] = s.x; x[5] = s.y; x[6] = s.z; x[7] = s.w;
   }
 };
 template <>
@@ -85,17 +102,21 @@ struct VerShared {
   int32_t parent[AQ_MAX_DRAFT_NODES], tok[AQ_MAX_DRAFT_NODES], gone[AQ_MAX_DRAFT_NODES];
   unsigned long long best[2][kVerMaxCluster];
   float sum[2][kVerMaxCluster];
-  unsigned long long wbest[kVerThreads / 32];
-  float wsum[kVerThreads / 32];
+  unsigned long long wbest[kVerWide / 32];
+  float wsum[kVerWide / 32];
   int32_t cur, refused, next, count, done;
 };
 
 // Largest r(v) / E(v) of this CTA's share of the vocabulary, N words at a time.
-template <typename T, bool HASQ, int N>
+template <typename T, bool HASQ, int N, int kVerThreads>
 __device__ __forceinline__ void race(const T* pr, const T* qr, const float* er, int vocab, int k, const VerShared& sh,
                                      int rank, int cluster, float& best, int& at) {
-  auto offer = [&](float w, float q, float e, int v) {
-    if (HASQ) w = residual(w, q, k, k - 1, sh.zinv);
+  // A quotient can pass the warp's best so far only if w > best e (1 - 2^-21), rounding included: one product and
+  // one comparison a word, and the divisions only where some word of a thread's batch gets that far. Words equal to
+  // the best pass too, and the lowest index is sorted out when the threads' bests meet.
+  float bar = 0.0f;
+  auto weigh = [&](float w, float q) { return HASQ ? residual(w, q, k, k - 1, sh.zinv) : w; };
+  auto offer = [&](float w, float e, int v) {
     const float s = __fdiv_rn(w, e);
     if (s > best) {
       if (!HASQ)
@@ -107,8 +128,9 @@ __device__ __forceinline__ void race(const T* pr, const T* qr, const float* er, 
   };
   const int step = cluster * kVerThreads * N;
   int v = (rank * kVerThreads + threadIdx.x) * N;
-  constexpr int U = N == 1 ? 8 : 4;
-  for (; v + (U - 1) * step + N <= vocab; v += U * step) {
+  constexpr int U = N == 1 ? 8 : N == 4 ? 4 : 2;   // loads in flight: 32 to 64 bytes a thread of each operand
+  // warps leave this loop together: a warp's words of a round are neighbours
+  for (; (v - (static_cast<int>(threadIdx.x) & 31) * N) + (U - 1) * step + 32 * N <= vocab; v += U * step) {
     Vec<T, N> w[U], q[U];
     Vec<float, N> e[U];
 #pragma unroll
@@ -117,18 +139,34 @@ __device__ __forceinline__ void race(const T* pr, const T* qr, const float* er, 
       if (HASQ && k > 0) q[j].load(qr + v + j * step);
       e[j].load(er + v + j * step);
     }
+    bool hit = false;
 #pragma unroll
     for (int j = 0; j < U; ++j)
 #pragma unroll
-      for (int i = 0; i < N; ++i) offer(w[j].x[i], HASQ && k > 0 ? q[j].x[i] : 0.0f, e[j].x[i], v + j * step + i);
+      for (int i = 0; i < N; ++i) {
+        if (HASQ && k > 0) w[j].x[i] = weigh(w[j].x[i], q[j].x[i]);
+        hit = hit || w[j].x[i] > bar * e[j].x[i];
+      }
+    if (__any_sync(0xffffffffu, hit)) {
+      if (hit) {
+#pragma unroll
+        for (int j = 0; j < U; ++j)
+#pragma unroll
+          for (int i = 0; i < N; ++i)
+            if (w[j].x[i] > bar * e[j].x[i]) offer(w[j].x[i], e[j].x[i], v + j * step + i);
+      }
+      bar = __uint_as_float(__reduce_max_sync(0xffffffffu, __float_as_uint(best))) * (1.0f - 0x1p-21f);
+    }
   }
   for (; v < vocab; v += step)
-    for (int i = 0; i < N && v + i < vocab; ++i)
-      offer(prob(pr, v + i), HASQ && k > 0 ? prob(qr, v + i) : 0.0f, er[v + i], v + i);
+    for (int i = 0; i < N && v + i < vocab; ++i) {
+      const float w = weigh(prob(pr, v + i), HASQ && k > 0 ? prob(qr, v + i) : 0.0f), e = er[v + i];
+      if (w > bar * e) offer(w, e, v + i);
+    }
 }
 
-template <typename T, bool HASQ>
-__global__ void __launch_bounds__(kVerThreads) aq_verify_kernel(const __grid_constant__ VerifyParams p) {
+template <typename T, bool HASQ, int kVerThreads>
+__global__ void __launch_bounds__(kVerThreads, 1024 / kVerThreads) aq_verify_kernel(const __grid_constant__ VerifyParams p) {
   __shared__ VerShared sh;
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
   const int C = p.cluster;
@@ -266,10 +304,11 @@ __global__ void __launch_bounds__(kVerThreads) aq_verify_kernel(const __grid_con
     const T* qr = HASQ ? Q + row * p.ld_q : pr;
     const float* er = p.noise + b * p.ld_noise;
     const uintptr_t low = reinterpret_cast<uintptr_t>(pr) | reinterpret_cast<uintptr_t>(qr);
-    if ((low & (sizeof(T) * 4 - 1)) == 0 && (reinterpret_cast<uintptr_t>(er) & 15) == 0)
-      race<T, HASQ, 4>(pr, qr, er, p.vocab, k, sh, rank, C, best, at);
+    constexpr int kVec = 16 / sizeof(T);
+    if (((low | reinterpret_cast<uintptr_t>(er)) & 15) == 0)
+      race<T, HASQ, kVec, kVerThreads>(pr, qr, er, p.vocab, k, sh, rank, C, best, at);
     else
-      race<T, HASQ, 1>(pr, qr, er, p.vocab, k, sh, rank, C, best, at);
+      race<T, HASQ, 1, kVerThreads>(pr, qr, er, p.vocab, k, sh, rank, C, best, at);
     unsigned long long key = (static_cast<unsigned long long>(__float_as_uint(best)) << 32) | (0xffffffffu - static_cast<uint32_t>(at));
 #pragma unroll
     for (int o = 16; o > 0; o >>= 1) {
@@ -301,13 +340,19 @@ __global__ void __launch_bounds__(kVerThreads) aq_verify_kernel(const __grid_con
   }
 }
 
-template <typename T, bool HASQ>
+template <typename T, bool HASQ, int THREADS>
 cudaError_t launch_verify(const VerifyParams& p, unsigned grid, cudaStream_t st) {
-  if (p.cluster > 8) {
-    cudaError_t e = cudaFuncSetAttribute(aq_verify_kernel<T, HASQ>, cudaFuncAttributeNonPortableClusterSizeAllowed, 1);
+  static std::atomic<uint64_t> ready{0};   // devices on which the kernel may use clusters of 16
+  if (p.cluster > 8 && !(ready.load() >> p.device & 1)) {
+    const cudaError_t e = cudaFuncSetAttribute(aq_verify_kernel<T, HASQ, THREADS>, cudaFuncAttributeNonPortableClusterSizeAllowed, 1);
     if (e != cudaSuccess) return e;
+    ready.fetch_or(1ull << p.device);
   }
-  return launch_serve(aq_verify_kernel<T, HASQ>, p, grid, kVerThreads, 0, st, p.cluster);
+  return launch_serve(aq_verify_kernel<T, HASQ, THREADS>, p, grid, THREADS, 0, st, p.cluster);
+}
+template <typename T, bool HASQ>
+cudaError_t launch_verify(const VerifyParams& p, unsigned grid, bool wide, cudaStream_t st) {
+  return wide ? launch_verify<T, HASQ, kVerWide>(p, grid, st) : launch_verify<T, HASQ, kVerNarrow>(p, grid, st);
 }
 
 }  // namespace
@@ -324,7 +369,7 @@ extern "C" aq_status aq_verify_drafts(int32_t batch, int32_t vocab, const int32_
   if (batch < 0 || nodes < 0 || rows < 0 || path_cap < 0)
     return serve_fail(AQ_ERR_SHAPE, "%s: batch=%d nodes=%lld rows=%lld path_cap=%d must not be negative", who, batch,
                       (long long)nodes, (long long)rows, path_cap);
-  if (vocab < 1) return serve_fail(AQ_ERR_SHAPE, "%s: vocab=%d must be >= 1", who, vocab);
+  if (vocab < 1 || vocab > (1 << 30)) return serve_fail(AQ_ERR_SHAPE, "%s: vocab=%d outside [1, 2^30]", who, vocab);
   if (max_nodes < 0 || max_nodes > AQ_MAX_DRAFT_NODES)
     return serve_fail(AQ_ERR_UNSUPPORTED, "%s: max_nodes=%d outside [0, %d]", who, max_nodes, AQ_MAX_DRAFT_NODES);
   if (p_type != AQ_PROB_F32 && p_type != AQ_PROB_BF16)
@@ -376,18 +421,21 @@ extern "C" aq_status aq_verify_drafts(int32_t batch, int32_t vocab, const int32_
   v.vocab = vocab;
   v.max_nodes = max_nodes;
   v.path_cap = path_cap;
-  // the largest cluster that keeps the launch within four CTAs an SM (all resident at once) and gives
-  // every CTA at least one round of its threads
+  // the largest cluster that keeps the launch within the CTAs that are resident at once and gives every CTA at
+  // least one round of its threads
+  const bool wide = static_cast<int64_t>(batch) * kVerMaxCluster <= dev.sms;
+  const int threads = wide ? kVerWide : kVerNarrow;
   int c = kVerMaxCluster;
-  while (c > 1 && (static_cast<int64_t>(batch) * c > 4 * dev.sms || vocab < c * kVerThreads)) c /= 2;
+  while (c > 1 && (static_cast<int64_t>(batch) * c > (wide ? 1 : 4) * dev.sms || vocab < c * threads)) c /= 2;
   v.cluster = c;
+  v.device = dev.index;
   if (static_cast<int64_t>(batch) * c > 0x7fffffffLL) return serve_fail(AQ_ERR_SHAPE, "%s: batch=%d is too large", who, batch);
   const unsigned grid = static_cast<unsigned>(batch) * c;
   const cudaStream_t cs = static_cast<cudaStream_t>(stream);
   cudaError_t e;
   if (p_type == AQ_PROB_F32)
-    e = q ? launch_verify<float, true>(v, grid, cs) : launch_verify<float, false>(v, grid, cs);
+    e = q ? launch_verify<float, true>(v, grid, wide, cs) : launch_verify<float, false>(v, grid, wide, cs);
   else
-    e = q ? launch_verify<uint16_t, true>(v, grid, cs) : launch_verify<uint16_t, false>(v, grid, cs);
+    e = q ? launch_verify<uint16_t, true>(v, grid, wide, cs) : launch_verify<uint16_t, false>(v, grid, wide, cs);
   return serve_launched(e, who);
 }

@@ -150,7 +150,9 @@ def call_attention(lib, d=None, c=None, q=C, heads=4, qt=256, qh=64, o=D_, ot=25
     (dict(d=dict(mask=0x5000, ld_mask=0)), b.AQ_ERR_SHAPE), (dict(d=dict(mask=0x5004, ld_mask=1)), b.AQ_ERR_ALIGNMENT),
     (dict(q=0), b.AQ_ERR_INVALID_ARG), (dict(o=0), b.AQ_ERR_INVALID_ARG), (dict(q=C + 8), b.AQ_ERR_ALIGNMENT),
     (dict(qt=252), b.AQ_ERR_ALIGNMENT), (dict(ot=128), b.AQ_ERR_SHAPE), (dict(o=C), b.AQ_ERR_OVERLAP), (dict(o=A), b.AQ_ERR_OVERLAP),
-    (dict(lse=D_ + 16), b.AQ_ERR_OVERLAP), (dict(lse=2), b.AQ_ERR_ALIGNMENT),
+    (dict(lse=D_ + 16), b.AQ_ERR_OVERLAP), (dict(lse=2), b.AQ_ERR_ALIGNMENT), (dict(ws=0), b.AQ_ERR_WORKSPACE),
+    (dict(ws=0x80000010), b.AQ_ERR_WORKSPACE), (dict(ws_bytes=4096), b.AQ_ERR_WORKSPACE), (dict(ws=A), b.AQ_ERR_OVERLAP),
+    (dict(ws=D_), b.AQ_ERR_OVERLAP), (dict(d=dict(batch=1 << 22, max_q=64)), b.AQ_ERR_SHAPE),
 ])
 def test_attention_refusals(lib, kw, status):
     assert call_attention(lib, **kw) == status, b.aq_last_error()
@@ -195,4 +197,15 @@ def test_binding_checks_types_before_pointers():
     with pytest.raises(ValueError):
         b.aq_kv_write(kv, x[:, :1].bfloat16(), x.bfloat16(), torch.zeros(3, dtype=torch.int64))
     with pytest.raises(ValueError):
-        b.KvCache(kv.k[:, :1], kv.v, kv.k_scale, kv.v_scale).packed()
+        b.aq_kv_read(b.KvCache(kv.k[:, :1], kv.v, kv.k_scale, kv.v_scale), torch.zeros(3, dtype=torch.int64))
+    with pytest.raises(TypeError):
+        b.aq_kv_read(b.KvCache(kv.k, kv.v), torch.zeros(3, dtype=torch.int64))
+    with pytest.raises(TypeError):
+        b.aq_verify_drafts(torch.zeros(4, 8, dtype=torch.float64), torch.zeros(3, dtype=torch.int32),
+                           torch.tensor([0, 3], dtype=torch.int32), torch.zeros(3), torch.ones(1, 8))
+    with pytest.raises(ValueError):
+        b.aq_tree_attention(kv, torch.zeros(2, 2, 64, dtype=torch.bfloat16), torch.tensor([0, 2], dtype=torch.int32),
+                            torch.tensor([1, 2], dtype=torch.int32), torch.zeros(1, 2, dtype=torch.int32), max_q=2)
+    with pytest.raises(b.AqError):   # well-formed tensors on the host: refused by the library, not read
+        b.aq_tree_attention(kv, torch.zeros(2, 3, 64, dtype=torch.bfloat16), torch.tensor([0, 2], dtype=torch.int32),
+                            torch.tensor([1], dtype=torch.int32), torch.zeros(1, 2, dtype=torch.int32), max_q=2)
