@@ -119,6 +119,12 @@ __device__ __forceinline__ void bulk_load(void* dst, const void* src, uint32_t b
                "l"(src), "r"(bytes), "r"(smem_u32(bar))
                : "memory");
 }
+// Quotient of non-negative numbers, by a 32-bit division where they fit (a 64-bit one costs ten times as much, and
+// these stand between a call's dependent loads).
+__device__ __forceinline__ int64_t quot(int64_t a, int64_t b) {
+  if (((a | b) >> 32) == 0) return static_cast<uint32_t>(a) / static_cast<uint32_t>(b);
+  return a / b;
+}
 // 2^e for e in [-126, 127].
 __device__ __forceinline__ float pow2(int e) { return __int_as_float((e + 127) << 23); }
 // Exponent of a non-negative value, kept where 2^(14 - e) and 2^(e - 14) are finite; zero counts as 2^-112.
@@ -163,7 +169,7 @@ struct Shape {
   static constexpr int kScale = E4M3 ? KS * 4 : 0;         // bytes of K's (or V's) scales in a stage
   static constexpr int kQ = M * D * 2;                     // queries, in the order of fragments
   static constexpr bool kQRegs = NR * D <= 256;            // ... and in registers
-  static constexpr int kCols = 32;   // columns joined at a time
+  static constexpr int kCols = D == 256 && NW == 8 ? 64 : 32;   // columns joined at a time
   static constexpr int kJoinLd = kCols + 4;
   static constexpr int kJoin = NW * 8 * NR * kJoinLd * 4;
   static_assert(M <= kAttnMaxRows && 8 * NR <= 32, "shared arrays");
@@ -195,11 +201,11 @@ __device__ __forceinline__ Span entry_span(const AttnParams& p, int b, int rt) {
   s.first = c0;
   s.ctx = max(p.ctx[b], 0);
   s.T = c0 >= 0 && c1 > c0 && c0 < p.total_q ? static_cast<int>(min(static_cast<int64_t>(min(c1 - c0, p.max_q)), p.total_q - c0)) : 0;
-  const int64_t rows = static_cast<int64_t>(s.T) * p.group, r0 = static_cast<int64_t>(rt) * M;
+  const uint32_t rows = static_cast<uint32_t>(s.T) * p.group, r0 = static_cast<uint32_t>(rt) * M;   // below 2^31: see the host
   s.t0 = s.t1 = 0;
   s.lo = s.hi = 0;
   if (r0 >= rows) return s;
-  const int i0 = static_cast<int>(r0 / p.group), i1 = static_cast<int>((min(r0 + M, rows) - 1) / p.group);
+  const int i0 = r0 / static_cast<uint32_t>(p.group), i1 = (min(r0 + M, rows) - 1) / static_cast<uint32_t>(p.group);
   s.hi = min(static_cast<int64_t>(s.ctx) + (p.mask ? s.T : i1 + 1), static_cast<int64_t>(p.pages_per_seq) << p.page_shift);
   if (p.window > 0) s.lo = max(static_cast<int64_t>(s.ctx) + (p.mask ? 0 : i0) - p.window + 1, static_cast<int64_t>(0));
   s.lo = min(s.lo, s.hi);
@@ -235,7 +241,7 @@ __device__ __forceinline__ void locate(const AttnParams& p, AttnShared& sh, int6
     if (i < (tid >> 5)) before += sh.part[i];
     total += sh.part[i];
   }
-  const int64_t share = (total + gridDim.x - 1) / gridDim.x;
+  const int64_t share = quot(total + gridDim.x - 1, gridDim.x);
   range[0] = min(share * blockIdx.x, total);
   range[1] = min(range[0] + share, total);
   if (write || (range[0] >= before && range[0] < before + sum)) {
@@ -271,7 +277,7 @@ struct Walk {
     entry = static_cast<int>(sh.start_entry);
     s = entry_span<M, KS>(p, entry / p.row_tiles, entry % p.row_tiles);
     len = s.t1 - s.t0;
-    head = static_cast<int>(sh.start_tile / len);
+    head = static_cast<int>(quot(sh.start_tile, len));
     offset = static_cast<int>(sh.start_tile - static_cast<int64_t>(head) * len);
     cut();
   }
@@ -389,47 +395,57 @@ __device__ __forceinline__ void load_queries(const AttnParams& p, AttnShared& sh
   const int tid = threadIdx.x, lane = tid & 31;
   const float scale2 = p.scale * 1.4426950408889634f;
   const uint32_t sign = scale2 < 0.0f ? 0x80008000u : 0u;
-  const bool dep = p.mask && p.depth;
   constexpr int L = S::D / 8;                  // lanes a row, 16 bytes each: 8, 16 or 32
-  constexpr int RPW = 32 / L;
-  for (int r = (tid >> 5) * RPW + lane / L; r < S::M; r += S::NW * RPW) {   // M is a multiple of NW * RPW or less than it
-    const int64_t rr = static_cast<int64_t>(rt) * S::M + r;
-    const bool live = rr < static_cast<int64_t>(s.T) * p.group;
-    const int i = live ? static_cast<int>(rr / p.group) : 0;
-    const int64_t row = static_cast<int64_t>(s.first) + i;
-    const int c = lane % L;                    // elements 8 c .. 8 c + 7
-    uint4 v = make_uint4(0, 0, 0, 0);
-    if (live)
-      v = *reinterpret_cast<const uint4*>(p.q + row * p.q_tok + (head * p.group + static_cast<int>(rr - static_cast<int64_t>(i) * p.group)) * p.q_head + c * 8);
+  constexpr int kStep = S::NW * (32 / L);      // rows the warps take at once
+  constexpr int kRounds = (S::M + kStep - 1) / kStep;
+  const int c = lane % L;                      // elements 8 c .. 8 c + 7
+  const uint32_t rows = static_cast<uint32_t>(s.T) * p.group, group = p.group;
+  if (tid < S::M) {
+    const uint32_t rr = static_cast<uint32_t>(rt) * S::M + tid;
+    const int i = rr < rows ? rr / group : 0;
+    sh.i[tid] = i;
+    sh.pos[tid] = static_cast<int64_t>(s.ctx) + (p.mask && p.depth ? max(p.depth[s.first + i], 0) : i);
+  }
+  uint4 v[kRounds];                            // every round's load in flight
+#pragma unroll
+  for (int k = 0; k < kRounds; ++k) {
+    const int r = (tid >> 5) * (32 / L) + lane / L + k * kStep;
+    const uint32_t rr = static_cast<uint32_t>(rt) * S::M + r;
+    v[k] = make_uint4(0, 0, 0, 0);
+    if (r < S::M && rr < rows) {
+      const uint32_t i = rr / group;
+      v[k] = *reinterpret_cast<const uint4*>(p.q + (static_cast<int64_t>(s.first) + i) * p.q_tok + (head * group + (rr - i * group)) * p.q_head + c * 8);
+    }
+  }
+#pragma unroll
+  for (int k = 0; k < kRounds; ++k) {
+    const int r = (tid >> 5) * (32 / L) + lane / L + k * kStep;
+    if (r >= S::M) break;                      // whole groups of L lanes
     float fac = fabsf(scale2);
-    uint32_t x[4] = {v.x ^ sign, v.y ^ sign, v.z ^ sign, v.w ^ sign};
+    uint32_t x[4] = {v[k].x ^ sign, v[k].y ^ sign, v[k].z ^ sign, v[k].w ^ sign};
     if constexpr (S::E4M3) {
       uint32_t top = 0;
 #pragma unroll
       for (int e = 0; e < 4; ++e) top = max(top, max((x[e] << 16) & 0x7fff0000u, x[e] & 0x7fff0000u));
-      const uint32_t group = (L == 32 ? 0xffffffffu : (1u << L) - 1) << (lane & ~(L - 1));
+      const uint32_t lanes = (L == 32 ? 0xffffffffu : (1u << L) - 1) << (lane & ~(L - 1));
 #pragma unroll
-      for (int o = L / 2; o > 0; o >>= 1) top = max(top, __shfl_xor_sync(group, top, o));
+      for (int o = L / 2; o > 0; o >>= 1) top = max(top, __shfl_xor_sync(lanes, top, o));
       const bool finite = top < 0x7f800000u;
       const int e = finite ? top_exponent(__uint_as_float(top)) : 0;
       const float f = pow2(14 - e);
       fac = finite ? pow2(e - 14) * fac : __uint_as_float(0x7fc00000u);   // a row with an infinity or a NaN has no finite score
 #pragma unroll
-      for (int k = 0; k < 4; ++k)
-        x[k] = finite ? pack_f16x2(__uint_as_float(x[k] << 16) * f, __uint_as_float(x[k] & 0xffff0000u) * f) : 0u;
+      for (int y = 0; y < 4; ++y)
+        x[y] = finite ? pack_f16x2(__uint_as_float(x[y] << 16) * f, __uint_as_float(x[y] & 0xffff0000u) * f) : 0u;
       uint2* dst = qs + ((c >> 1) * S::M + r) * 4 + (c & 1) * 2;
       dst[0] = make_uint2(x[0], x[1]);
       dst[1] = make_uint2(x[2], x[3]);
     } else {
       uint32_t* dst = reinterpret_cast<uint32_t*>(qs + ((c >> 1) * S::M + r) * 4) + (c & 1);
 #pragma unroll
-      for (int k = 0; k < 4; ++k) dst[2 * k] = x[k];
+      for (int y = 0; y < 4; ++y) dst[2 * y] = x[y];
     }
-    if (c == 0) {
-      sh.fac[r] = fac;
-      sh.i[r] = i;
-      sh.pos[r] = static_cast<int64_t>(s.ctx) + (dep ? max(p.depth[row], 0) : i);
-    }
+    if (c == 0) sh.fac[r] = fac;
   }
 }
 
@@ -857,8 +873,8 @@ __device__ __forceinline__ void consume(const AttnParams& p, AttnShared& sh, con
       for (int u = tid; u < S::M * (S::kCols / 4); u += kConsumers) {
         const int r = u / (S::kCols / 4), c = u % (S::kCols / 4) * 4;
         const int g0 = r / (8 * NR) * S::KG, rr = r % (8 * NR);
-        const int64_t row = static_cast<int64_t>(rt) * S::M + r;
-        if (row >= static_cast<int64_t>(w.s.T) * p.group || !ok) continue;
+        const uint32_t row = static_cast<uint32_t>(rt) * S::M + r;
+        if (row >= static_cast<uint32_t>(w.s.T) * p.group || !ok) continue;
         float mx = -INFINITY, lt = 0.0f;
         float4 v = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
 #pragma unroll
@@ -874,8 +890,8 @@ __device__ __forceinline__ void consume(const AttnParams& p, AttnShared& sh, con
           v.w += y.w;
         }
         if (complete) {
-          const int i = static_cast<int>(row / p.group);
-          const int head = w.head * p.group + static_cast<int>(row - static_cast<int64_t>(i) * p.group);
+          const int i = sh.i[r];
+          const int head = w.head * p.group + static_cast<int>(row - static_cast<uint32_t>(i) * p.group);
           const bool none = mx == -INFINITY && lt == 0.0f;
           const float inv = none ? 0.0f : 1.0f / lt;
           uint16_t* dst = p.o + (static_cast<int64_t>(w.s.first) + i) * p.o_tok + head * p.o_head + c0 + c;
@@ -937,8 +953,7 @@ __global__ void __launch_bounds__(128) aq_attention_join_kernel(const __grid_con
   __shared__ float sm[4], sl[4], so[4][D];
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
   const int heads = p.hk * p.group;
-  const int64_t row = blockIdx.x / heads;
-  const int head = static_cast<int>(blockIdx.x - row * heads);
+  const int row = blockIdx.x / static_cast<uint32_t>(heads), head = blockIdx.x - row * heads;
   if (tid == 0) b_of = -1;
   __syncthreads();
   pdl_wait_prior_grid();
@@ -951,26 +966,44 @@ __global__ void __launch_bounds__(128) aq_attention_join_kernel(const __grid_con
   __syncthreads();
   const int b = b_of;
   if (b < 0) return;
-  const int64_t r = (row - p.cu[b]) * p.group + head % p.group;
-  const int entry = b * p.row_tiles + static_cast<int>(r / p.rows_per_tile);
-  const int rr = static_cast<int>(r % p.rows_per_tile);
-  const int64_t first = p.prefix[entry], len = (p.prefix[entry + 1] - first) / p.hk;
-  const int64_t t0 = first + (head / p.group) * len, t1 = t0 + len;
-  const int64_t share = (total + p.main_grid - 1) / p.main_grid;
-  const int c0 = static_cast<int>(t0 / share), c1 = static_cast<int>((t1 - 1) / share);
+  const uint32_t r = static_cast<uint32_t>(row - p.cu[b]) * p.group + head % static_cast<uint32_t>(p.group);
+  const int entry = b * p.row_tiles + r / static_cast<uint32_t>(p.rows_per_tile);
+  const int rr = r % static_cast<uint32_t>(p.rows_per_tile);
+  const int64_t first = p.prefix[entry], len = quot(p.prefix[entry + 1] - first, p.hk);
+  const int64_t t0 = first + head / p.group * len, t1 = t0 + len;
+  const int64_t share = quot(total + p.main_grid - 1, p.main_grid);
+  const int c0 = static_cast<int>(quot(t0, share)), c1 = static_cast<int>(quot(t1 - 1, share));
   if (c0 == c1) return;   // one CTA had it all
   float m = -INFINITY, l = 0.0f, o[N];
 #pragma unroll
   for (int e = 0; e < N; ++e) o[e] = 0.0f;
-  for (int c = c0 + warp; c <= c1; c += 4) {
-    const int64_t at = (static_cast<int64_t>(c) * 2 + (c > c0 ? 0 : 1)) * p.rows_per_tile + rr;
-    const float2 ml = p.part_ml[at];
-    const float mx = fmaxf(m, ml.x), mz = mx == -INFINITY ? 0.0f : mx;
-    const float a = ex2(m - mz), f = ex2(ml.x - mz);
-    const float* src = p.part_o + at * D + lane * N;
+  constexpr int kParts = 4;   // of each warp in flight at once
+  for (int c = c0 + warp; c <= c1; c += 4 * kParts) {
+    float2 ml[kParts];
+    float v[kParts][N];
 #pragma unroll
-    for (int e = 0; e < N; ++e) o[e] = o[e] * a + src[e] * f;
-    l = l * a + ml.y * f;
+    for (int k = 0; k < kParts; ++k) {
+      const int cc = c + 4 * k;
+      const int64_t at = (static_cast<int64_t>(cc) * 2 + (cc > c0 ? 0 : 1)) * p.rows_per_tile + rr;
+      ml[k] = cc <= c1 ? p.part_ml[at] : make_float2(-INFINITY, 0.0f);
+      const float* src = p.part_o + at * D + lane * N;
+#pragma unroll
+      for (int e = 0; e < N; ++e) v[k][e] = cc <= c1 ? src[e] : 0.0f;
+    }
+    float mx = m;
+#pragma unroll
+    for (int k = 0; k < kParts; ++k) mx = fmaxf(mx, ml[k].x);
+    const float mz = mx == -INFINITY ? 0.0f : mx, a = ex2(m - mz);
+    l *= a;
+#pragma unroll
+    for (int e = 0; e < N; ++e) o[e] *= a;
+#pragma unroll
+    for (int k = 0; k < kParts; ++k) {
+      const float f = ex2(ml[k].x - mz);
+      l += ml[k].y * f;
+#pragma unroll
+      for (int e = 0; e < N; ++e) o[e] += v[k][e] * f;
+    }
     m = mx;
   }
 #pragma unroll
@@ -995,9 +1028,9 @@ __global__ void __launch_bounds__(128) aq_attention_join_kernel(const __grid_con
     float x = 0.0f;
 #pragma unroll
     for (int k = 0; k < 4; ++k) x += so[k][d] * f[k];
-    p.o[row * p.o_tok + head * p.o_head + d] = f32_to_bf16_rn(none ? 0.0f : x * inv);
+    p.o[static_cast<int64_t>(row) * p.o_tok + head * p.o_head + d] = f32_to_bf16_rn(none ? 0.0f : x * inv);
   }
-  if (p.lse && tid == 0) p.lse[row * heads + head] = none ? -INFINITY : (mz + log2f(lt)) * 0.6931471805599453f;
+  if (p.lse && tid == 0) p.lse[static_cast<int64_t>(row) * heads + head] = none ? -INFINITY : (mz + log2f(lt)) * 0.6931471805599453f;
 }
 
 // ---------------------------------------------------------------------------------
