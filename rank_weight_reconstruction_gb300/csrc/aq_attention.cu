@@ -28,41 +28,29 @@
 #include <atomic>
 #include <type_traits>
 
-#include "aq_serve.h"
+#include "aq_attention.cuh"
 
 namespace aq {
-namespace {
 
-struct AttnParams {
-  CUtensorMap tm_k, tm_v;
-  const float* ks;
-  const float* vs;
-  int32_t pages, page_shift, hk, group;
-  const uint16_t* q;
-  int64_t q_tok, q_head;
-  uint16_t* o;
-  int64_t o_tok, o_head;
-  float* lse;
-  const int32_t* cu;
-  const int32_t* ctx;
-  const int32_t* table;
-  int64_t ld_table;
-  int32_t pages_per_seq;
-  const uint64_t* mask;
-  int64_t ld_mask;
-  const int32_t* depth;
-  int32_t batch, max_q, window;
-  int64_t total_q;
-  float scale;
-  int32_t rows_per_tile, row_tiles;   // rows of a tile, tiles of a sequence
-  int32_t main_grid, stages;
-  int64_t* prefix;                    // [batch * row_tiles + 1] first tile of each entry
-  float2* part_ml;                    // [CTA][2][rows of a tile] maximum (base 2) and sum of a partial item
-  float* part_o;                      // [CTA][2][rows of a tile][D]
-  int32_t* status;
-  uint64_t timeout_ns;
-};
-static_assert(sizeof(AttnParams) <= 4096, "kernel parameters are limited to 4 KB");
+aq_status attention_cache_map(CUtensorMap* m, const void* base, const aq_kv_cache* c, int box_cols, int box_rows, const char* who) {
+  const bool e4m3 = c->type == AQ_KV_E4M3;
+  const cuuint64_t es = e4m3 ? 1 : 2, row = c->head_dim * es;
+  const cuuint64_t dims[3] = {static_cast<cuuint64_t>(c->head_dim), static_cast<cuuint64_t>(c->page_size),
+                              static_cast<cuuint64_t>(c->pages) * c->kv_heads};
+  const cuuint64_t strides[2] = {row, row * c->page_size};
+  const cuuint32_t box[3] = {static_cast<cuuint32_t>(box_cols), static_cast<cuuint32_t>(box_rows), 1};
+  const cuuint32_t unit[3] = {1, 1, 1};
+  const serve_encode_fn fn = serve_encode();
+  if (!fn) return serve_fail(AQ_ERR_CUDA, "%s: cuTensorMapEncodeTiled is not available from the driver", who);
+  const CUresult r = fn(m, e4m3 ? CU_TENSOR_MAP_DATA_TYPE_UINT8 : CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 3, const_cast<void*>(base),
+                        dims, strides, box, unit, CU_TENSOR_MAP_INTERLEAVE_NONE,
+                        box_cols * es == 128 ? CU_TENSOR_MAP_SWIZZLE_128B : CU_TENSOR_MAP_SWIZZLE_64B,
+                        CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
+  if (r != CUDA_SUCCESS) return serve_fail(AQ_ERR_CUDA, "%s: cuTensorMapEncodeTiled failed (%d)", who, static_cast<int>(r));
+  return AQ_OK;
+}
+
+namespace {
 
 // ---------------------------------------------------------------------------------
 // instructions
@@ -91,55 +79,15 @@ __device__ __forceinline__ void mma_f16(float (&d)[4], const uint32_t (&a)[4], u
                : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3])
                : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
 }
-// Four E4M3 codes to two pairs of halves.
-__device__ __forceinline__ void widen(uint32_t c, uint32_t& lo, uint32_t& hi) {
-  asm("{\n .reg .b16 l, h;\n mov.b32 {l, h}, %2;\n cvt.rn.f16x2.e4m3x2 %0, l;\n cvt.rn.f16x2.e4m3x2 %1, h;\n}"
-      : "=r"(lo), "=r"(hi)
-      : "r"(c));
-}
-__device__ __forceinline__ uint32_t pack_f16x2(float lo, float hi) {
-  uint32_t r;
-  asm("cvt.rn.f16x2.f32 %0, %1, %2;" : "=r"(r) : "f"(hi), "f"(lo));
-  return r;
-}
 // Transposes an 8 x 8 matrix of 16-bit elements held one row pair a lane.
 __device__ __forceinline__ uint32_t transpose8(uint32_t x) {
   uint32_t r;
   asm volatile("movmatrix.sync.aligned.m8n8.trans.b16 %0, %1;" : "=r"(r) : "r"(x));
   return r;
 }
-__device__ __forceinline__ float ex2(float x) {
-  float r;
-  asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(x));
-  return r;
-}
-__device__ __forceinline__ void bulk_load(void* dst, const void* src, uint32_t bytes, uint64_t* bar) {
-  asm volatile("cp.async.bulk.shared::cluster.global.mbarrier::complete_tx::bytes [%0], [%1], %2, [%3];" ::"r"(
-                   smem_u32(dst)),
-               "l"(src), "r"(bytes), "r"(smem_u32(bar))
-               : "memory");
-}
-// Quotient of non-negative numbers, by a 32-bit division where they fit (a 64-bit one costs ten times as much, and
-// these stand between a call's dependent loads).
-__device__ __forceinline__ int64_t quot(int64_t a, int64_t b) {
-  if (((a | b) >> 32) == 0) return static_cast<uint32_t>(a) / static_cast<uint32_t>(b);
-  return a / b;
-}
-// 2^e for e in [-126, 127].
-__device__ __forceinline__ float pow2(int e) { return __int_as_float((e + 127) << 23); }
-// Exponent of a non-negative value, kept where 2^(14 - e) and 2^(e - 14) are finite; zero counts as 2^-112.
-__device__ __forceinline__ int top_exponent(float x) { return min(max(static_cast<int>(__float_as_uint(x) >> 23) - 127, -112), 126); }
-
 constexpr int kAttnStages = 6;          // most stages of the ring
 constexpr int kAttnMaxWarps = 8;        // most consumer warps
 constexpr int kAttnMaxRows = 64;        // rows of the largest tile
-constexpr int kAttnSmsBound = 192;      // SMs (of any sm_103 part) and CTAs an SM, for sizing the
-constexpr int kAttnMaxPerSm = 2;        // workspace without a device
-// The maximum that weights are taken against may lag by this power of two before the sums are scaled over.
-constexpr float kLag = 6.0f;
-// Weights times values' scales in f16 stay below 2^(kLag + 1 + kTop) <= 2^15.
-constexpr int kTop = 8;
-
 // ---------------------------------------------------------------------------------
 // shapes: D elements a head; a warp takes 8 NR rows against CK keys at a time; NW warps are RG row groups by
 // KG key groups. Keys are the matrix instruction's 16 lanes and rows its 8 columns, in both products: S^T = K Q^T
@@ -179,126 +127,11 @@ struct AttnShared {
   uint64_t full[kAttnStages], empty[kAttnStages];
   uint32_t valid[kAttnStages];
   int32_t abort;
-  int64_t start_entry, start_tile;      // where this CTA begins: entry, tile within it
-  int64_t part[kAttnMaxWarps + 4];
+  AttnWork work;
   float m[kAttnMaxWarps][32], l[kAttnMaxWarps][32];
   float fac[kAttnMaxRows];                       // of a row's raw products, to base-2 logits; not negative
   int64_t pos[kAttnMaxRows];                  // of a row
   int32_t i[kAttnMaxRows];                     // its drafted index
-};
-
-// Keys [lo, hi) and tiles [t0, t1) that the rows of entry (sequence b, row tile rt) can see.
-struct Span {
-  int64_t lo, hi;
-  int32_t t0, t1;
-  int32_t first, T, ctx;    // first row in q, rows, context
-};
-
-template <int M, int KS>
-__device__ __forceinline__ Span entry_span(const AttnParams& p, int b, int rt) {
-  Span s;
-  const int c0 = p.cu[b], c1 = p.cu[b + 1];
-  s.first = c0;
-  s.ctx = max(p.ctx[b], 0);
-  s.T = c0 >= 0 && c1 > c0 && c0 < p.total_q ? static_cast<int>(min(static_cast<int64_t>(min(c1 - c0, p.max_q)), p.total_q - c0)) : 0;
-  const uint32_t rows = static_cast<uint32_t>(s.T) * p.group, r0 = static_cast<uint32_t>(rt) * M;   // below 2^31: see the host
-  s.t0 = s.t1 = 0;
-  s.lo = s.hi = 0;
-  if (r0 >= rows) return s;
-  const int i0 = r0 / static_cast<uint32_t>(p.group), i1 = (min(r0 + M, rows) - 1) / static_cast<uint32_t>(p.group);
-  s.hi = min(static_cast<int64_t>(s.ctx) + (p.mask ? s.T : i1 + 1), static_cast<int64_t>(p.pages_per_seq) << p.page_shift);
-  if (p.window > 0) s.lo = max(static_cast<int64_t>(s.ctx) + (p.mask ? 0 : i0) - p.window + 1, static_cast<int64_t>(0));
-  s.lo = min(s.lo, s.hi);
-  s.t0 = static_cast<int32_t>(s.lo / KS);
-  s.t1 = max(static_cast<int32_t>((s.hi + KS - 1) / KS), s.t0 + 1);   // a row that can see nothing is written too
-  return s;
-}
-
-// Where tile number `at` of the whole call lies; called by every thread, the answer in sh. CTA 0 also leaves
-// the entries' first tiles for the joining launch.
-template <int M, int KS>
-__device__ __forceinline__ void locate(const AttnParams& p, AttnShared& sh, int64_t* prefix, bool write,
-                                       int64_t (&range)[2]) {
-  const int n = p.batch * p.row_tiles, tid = threadIdx.x;
-  const int threads = blockDim.x;
-  const int per = (n + threads - 1) / threads;
-  const int e0 = min(tid * per, n), e1 = min(e0 + per, n);
-  int64_t sum = 0;
-  for (int e = e0; e < e1; ++e) {
-    const Span s = entry_span<M, KS>(p, e / p.row_tiles, e % p.row_tiles);
-    sum += static_cast<int64_t>(s.t1 - s.t0) * p.hk;
-  }
-  int64_t upto = sum;   // within the warp, this thread's own among them
-#pragma unroll
-  for (int off = 1; off < 32; off *= 2) {
-    const int64_t v = __shfl_up_sync(0xffffffffu, upto, off);
-    if ((tid & 31) >= off) upto += v;
-  }
-  if ((tid & 31) == 31) sh.part[tid >> 5] = upto;
-  __syncthreads();
-  int64_t before = upto - sum, total = 0;
-  for (int i = 0; i < threads / 32; ++i) {
-    if (i < (tid >> 5)) before += sh.part[i];
-    total += sh.part[i];
-  }
-  const int64_t share = quot(total + gridDim.x - 1, gridDim.x);
-  range[0] = min(share * blockIdx.x, total);
-  range[1] = min(range[0] + share, total);
-  if (write || (range[0] >= before && range[0] < before + sum)) {
-    int64_t at = before;
-    for (int e = e0; e < e1; ++e) {
-      const Span s = entry_span<M, KS>(p, e / p.row_tiles, e % p.row_tiles);
-      const int64_t len = static_cast<int64_t>(s.t1 - s.t0) * p.hk;
-      if (range[0] >= at && range[0] < at + len) {
-        sh.start_entry = e;
-        sh.start_tile = range[0] - at;
-      }
-      if (write) prefix[e] = at;
-      at += len;
-    }
-    if (write && e1 == n && e0 < n) prefix[n] = at;
-  }
-  if (write && n == 0 && tid == 0) prefix[0] = 0;
-  __syncthreads();
-}
-
-// Walks the segments of a CTA's range: consecutive tiles of one item.
-template <int M, int KS>
-struct Walk {
-  int64_t left;          // tiles of the CTA's range still to come
-  int entry, head;
-  int tile0, n;          // this segment: first tile (within the sequence) and how many
-  int len;               // tiles of the whole item
-  int offset;            // of them before this segment
-  Span s;
-  __device__ __forceinline__ Walk(const AttnParams& p, const AttnShared& sh, const int64_t (&range)[2]) {
-    left = range[1] - range[0];
-    if (left <= 0) return;
-    entry = static_cast<int>(sh.start_entry);
-    s = entry_span<M, KS>(p, entry / p.row_tiles, entry % p.row_tiles);
-    len = s.t1 - s.t0;
-    head = static_cast<int>(quot(sh.start_tile, len));
-    offset = static_cast<int>(sh.start_tile - static_cast<int64_t>(head) * len);
-    cut();
-  }
-  __device__ __forceinline__ void cut() {
-    tile0 = s.t0 + offset;
-    n = static_cast<int>(min(static_cast<int64_t>(len - offset), left));
-  }
-  __device__ __forceinline__ void next(const AttnParams& p) {
-    left -= n;
-    if (left <= 0) return;
-    offset = 0;
-    if (++head == p.hk) {
-      head = 0;
-      do {
-        ++entry;
-        s = entry_span<M, KS>(p, entry / p.row_tiles, entry % p.row_tiles);
-        len = s.t1 - s.t0;
-      } while (len == 0);
-    }
-    cut();
-  }
 };
 
 template <class S>
@@ -309,7 +142,7 @@ __device__ __forceinline__ void produce(const AttnParams& p, AttnShared& sh, uin
   const int box = min(page, S::KS), np = S::KS / box;   // rows of a page in a tile; pages a tile touches
   int st = 0, issued = 0;
   uint32_t parity = 1;
-  Walk<S::M, S::KS> w(p, sh, range);
+  Walk<S::M, S::KS> w(p, sh.work, range);
   bool ok = true;
   while (ok && w.left > 0) {
     const int b = w.entry / p.row_tiles;
@@ -391,7 +224,7 @@ __device__ __forceinline__ uint32_t cell_addr(uint32_t base, int key, int x) {
 // 16 k + 2 t + {0, 1} and 8 more; for E4M3 keys f16 elements 16 k + 4 t + {0, 1, 2, 3} (the order in which a key's
 // codes are loaded), scaled by the row's power of two. The sign of the logits' scale goes into them.
 template <class S>
-__device__ __forceinline__ void load_queries(const AttnParams& p, AttnShared& sh, uint2* qs, const Span& s, int head, int rt) {
+__device__ __forceinline__ void load_queries(const AttnParams& p, AttnShared& sh, uint2* qs, const KeySpan& s, int head, int rt) {
   const int tid = threadIdx.x, lane = tid & 31;
   const float scale2 = p.scale * 1.4426950408889634f;
   const uint32_t sign = scale2 < 0.0f ? 0x80008000u : 0u;
@@ -449,61 +282,12 @@ __device__ __forceinline__ void load_queries(const AttnParams& p, AttnShared& sh
   }
 }
 
-// The step's keys that each of a warp's rows sees, as bits: lane r answers for row r (rows 8 NR, keys CK <= 32;
-// ka: the first key, k0: its place in the tile). One round of loads, whatever the mask.
-template <class S>
-__device__ __forceinline__ uint32_t seen_bits(const AttnParams& p, const AttnShared& sh, const Span& s, int rg, int64_t ka,
-                                              int k0, uint32_t pages, int box_shift) {
-  const int lane = threadIdx.x & 31;
-  constexpr uint32_t kAll = S::CK == 32 ? 0xffffffffu : (1u << S::CK) - 1;
-  auto below = [](int64_t n) { return n <= 0 ? 0u : n >= 32 ? 0xffffffffu : (1u << n) - 1; };   // bits [0, n)
-  const int r = rg * 8 * S::NR + min(lane, 8 * S::NR - 1);
-  const int i = sh.i[r];
-  const int64_t pos = sh.pos[r];
-  uint32_t bits = below(s.hi - ka) & kAll;
-  for (int k = 0; k < S::CK; k += 1 << min(box_shift, 5))
-    if (!((pages >> ((k0 + k) >> box_shift)) & 1)) bits &= ~(below(1 << min(box_shift, 5)) << k);
-  const int64_t t0 = ka - s.ctx;                  // drafted index of the first key (negative: context)
-  uint32_t drafted = ~below(-t0);                 // which keys are drafted ones
-  if (drafted) {
-    uint32_t see;
-    if (p.mask) {
-      const uint64_t* m = p.mask + (static_cast<int64_t>(s.first) + i) * p.ld_mask;
-      const int64_t at = max(t0, static_cast<int64_t>(0));
-      const int last = (s.T - 1) >> 6, w0 = min(static_cast<int>(at >> 6), last), w1 = min(w0 + 1, last);
-      const uint64_t lo = m[w0], hi = m[w1];
-      const int sh0 = static_cast<int>(at & 63);
-      const uint64_t v = sh0 ? (lo >> sh0) | (hi << (64 - sh0)) : lo;
-      see = t0 < 0 ? static_cast<uint32_t>(v) << static_cast<int>(-t0) : static_cast<uint32_t>(v);
-    } else {
-      see = below(i - t0 + 1);
-    }
-    bits &= ~drafted | see;
-  }
-  if (p.window > 0) {
-    // context (and a chain's) keys lie at their index; a tree's drafted ones at their depth
-    const bool tree = p.mask && p.depth;
-    const uint32_t indexed = tree ? ~drafted : 0xffffffffu;
-    bits &= ~indexed | ~below(pos - p.window + 1 - ka);
-    if (tree && drafted) {
-      const int64_t t = t0 + lane;
-      const int d = t >= 0 && t < s.T ? max(p.depth[s.first + t], 0) : 0;
-      for (int k = 0; k < S::CK; ++k) {
-        const int dk = __shfl_sync(0xffffffffu, d, k);
-        if (((drafted >> k) & 1) && pos - (static_cast<int64_t>(s.ctx) + dk) >= p.window) bits &= ~(1u << k);
-      }
-    }
-  }
-  return bits;
-}
-
 // A warp's sums for its rows 2 t + {0, 1} of each of NR groups of eight.
 template <class S>
 struct Sums {
   // o[x][n]: O^T fragment, lanes the columns: E4M3 16 x + 2 g + {0: first half, 1: second}, bf16 16 x + g + {0, 8}
   float o[S::D / 16][S::NR][4];
-  float m[S::NR][2], l[S::NR][2];
-  int ve;   // E4M3: o holds sums of w 2^(kTop - ve)
+  float m[S::NR][2], l[S::NR][2];   // the reference (base 2), the sum of the weights against it
 };
 
 // Adds the infinities and NaN among a step's values to the rows that see them (weights in w [row][key], -1: masked).
@@ -551,7 +335,7 @@ struct StepInfo {          // what a step that not every row sees in full needs 
 
 // CK keys, the first being key k0 of the stage, against the warp's rows. WHOLE: every row sees every key.
 template <class S, bool WHOLE>
-__device__ __forceinline__ void step(const AttnParams& p, const AttnShared& sh, const Span& span, const StepInfo& info, Sums<S>& a,
+__device__ __forceinline__ void step(const AttnParams& p, const AttnShared& sh, const KeySpan& span, const StepInfo& info, Sums<S>& a,
                                      const uint2* qs, const uint2 (&qr)[S::kQRegs ? S::D / 16 : 1][S::NR], uint32_t kb,
                                      uint32_t vb, const float* ksc, const float* vsc, float* mine, int k0,
                                      const float (&fac)[S::NR][2]) {
@@ -597,61 +381,65 @@ __device__ __forceinline__ void step(const AttnParams& p, const AttnShared& sh, 
         }
       }
   }
-  float vs[KT][2], vmax = 0.0f;
-  if constexpr (S::E4M3) {
+  float vs[KT][2], ve[KT][2], vtop = 0.0f;   // values' scales, their exponents, the lane's largest
 #pragma unroll
-    for (int j = 0; j < KT; ++j)
+  for (int j = 0; j < KT; ++j)
 #pragma unroll
-      for (int h = 0; h < 2; ++h) {
+    for (int h = 0; h < 2; ++h) {
+      vs[j][h] = 1.0f;
+      ve[j][h] = 0.0f;
+      if constexpr (S::E4M3) {
         const float ks = ksc[k0 + 16 * j + 8 * h + g];
         vs[j][h] = vsc[k0 + 16 * j + 8 * h + g];
-        if (WHOLE) vmax = fmaxf(vmax, vs[j][h]);
+        vtop = fmaxf(vtop, vs[j][h]);
+        if (!WHOLE) ve[j][h] = scale_exponent(vs[j][h]);
 #pragma unroll
         for (int n = 0; n < NR; ++n) {
           sc[j][n][2 * h] *= ks;
           sc[j][n][2 * h + 1] *= ks;
         }
       }
-  }
-  if constexpr (!WHOLE) {
-    const uint32_t bits = seen_bits<S>(p, sh, span, info.rg, info.key0 + k0, k0, info.pages, info.box_shift);
+    }
+  // What the reference has to cover: the logits, and with E4M3 the exponents of the values' scales on them. Looked
+  // at by each lane for itself (where all is seen by its largest logit and its largest scale), put together only
+  // where one lane's passes the reference.
+  float mt[NR][2];
+  if constexpr (WHOLE) {
+    const float e = S::E4M3 ? scale_exponent(vtop) - kTop : 0.0f;
+#pragma unroll
+    for (int n = 0; n < NR; ++n)
+#pragma unroll
+      for (int c = 0; c < 2; ++c) {
+        float x = fmaxf(sc[0][n][c], sc[0][n][2 + c]);
+#pragma unroll
+        for (int j = 1; j < KT; ++j) x = fmaxf(x, fmaxf(sc[j][n][c], sc[j][n][2 + c]));
+        mt[n][c] = x == -INFINITY ? x : fmaf(x, fac[n][c], e);
+      }
+  } else {
+    const uint32_t bits = seen_bits(p, span, sh.i[info.rg * 8 * NR + min(lane, 8 * NR - 1)], sh.pos[info.rg * 8 * NR + min(lane, 8 * NR - 1)],
+                                    info.key0 + k0, k0, S::CK, info.pages, info.box_shift);
 #pragma unroll
     for (int n = 0; n < NR; ++n)
 #pragma unroll
       for (int c = 0; c < 2; ++c) {
         const uint32_t mine_bits = __shfl_sync(0xffffffffu, bits, 8 * n + 2 * t + c) >> g;
+        mt[n][c] = -INFINITY;
 #pragma unroll
         for (int j = 0; j < KT; ++j)
 #pragma unroll
           for (int h = 0; h < 2; ++h) {
-            if (!((mine_bits >> (16 * j + 8 * h)) & 1)) sc[j][n][2 * h + c] = -INFINITY;
-            else if (S::E4M3) vmax = fmaxf(vmax, vs[j][h]);
+            float& x = sc[j][n][2 * h + c];
+            if (!((mine_bits >> (16 * j + 8 * h)) & 1)) x = -INFINITY;
+            if (x != -INFINITY) mt[n][c] = fmaxf(mt[n][c], fmaf(x, fac[n][c], S::E4M3 ? ve[j][h] - kTop : 0.0f));
           }
       }
   }
-  // the maxima: looked at by each lane for itself, put together only where one is passed
-  float mt[NR][2];
   bool grown = false;
 #pragma unroll
   for (int n = 0; n < NR; ++n)
 #pragma unroll
-    for (int c = 0; c < 2; ++c) {
-      float x = fmaxf(sc[0][n][c], sc[0][n][2 + c]);
-#pragma unroll
-      for (int j = 1; j < KT; ++j) x = fmaxf(x, fmaxf(sc[j][n][c], sc[j][n][2 + c]));
-      mt[n][c] = x == -INFINITY ? x : x * fac[n][c];
-      grown = grown || mt[n][c] > a.m[n][c] + kLag;
-    }
-  if (S::E4M3) grown = grown || top_exponent(vmax) > a.ve;
+    for (int c = 0; c < 2; ++c) grown = grown || mt[n][c] > a.m[n][c] + kLag;
   if (__any_sync(0xffffffffu, grown)) {
-    float turn = 1.0f;
-    if constexpr (S::E4M3) {
-#pragma unroll
-      for (int off = 1; off < 32; off *= 2) vmax = fmaxf(vmax, __shfl_xor_sync(0xffffffffu, vmax, off));
-      const int e = max(a.ve, top_exponent(vmax));
-      turn = ex2(static_cast<float>(a.ve - e));
-      a.ve = e;
-    }
 #pragma unroll
     for (int n = 0; n < NR; ++n)
 #pragma unroll
@@ -664,31 +452,29 @@ __device__ __forceinline__ void step(const AttnParams& p, const AttnShared& sh, 
         a.l[n][c] *= keep;
 #pragma unroll
         for (int x = 0; x < D / 16; ++x) {
-          a.o[x][n][c] *= keep * turn;
-          a.o[x][n][2 + c] *= keep * turn;
+          a.o[x][n][c] *= keep;
+          a.o[x][n][2 + c] *= keep;
         }
       }
   }
+  float mz[NR][2];   // the reference, 0 while every score was minus infinity
+#pragma unroll
+  for (int n = 0; n < NR; ++n)
+#pragma unroll
+    for (int c = 0; c < 2; ++c) mz[n][c] = a.m[n][c] == -INFINITY ? 0.0f : a.m[n][c];
   // weights
-  const float vf = S::E4M3 ? pow2(kTop - a.ve) : 1.0f;
   uint32_t pw[KT][NR][2];
 #pragma unroll
-  for (int j = 0; j < KT; ++j) {
-    float f[2] = {1.0f, 1.0f};
-    if (S::E4M3) {
-      f[0] = vs[j][0] * vf;
-      f[1] = vs[j][1] * vf;
-    }
+  for (int j = 0; j < KT; ++j)
 #pragma unroll
     for (int n = 0; n < NR; ++n) {
 #pragma unroll
       for (int c = 0; c < 4; ++c) {
         const bool off = !WHOLE && sc[j][n][c] == -INFINITY;
-        const float mz = !WHOLE && a.m[n][c & 1] == -INFINITY ? 0.0f : a.m[n][c & 1];
-        float e = ex2(fmaf(sc[j][n][c], fac[n][c & 1], -mz));
+        float e = ex2(fmaf(sc[j][n][c], fac[n][c & 1], -mz[n][c & 1]));
         if (off) e = 0.0f;
         a.l[n][c & 1] += e;
-        if (S::E4M3) e *= f[c >> 1];
+        if (S::E4M3) e *= vs[j][c >> 1];
         if (S::E4M3 && off) e = 0.0f;   // whatever scale lies there
         if (!WHOLE) mine[(8 * n + 2 * t + (c & 1)) * S::kJoinLd + 16 * j + 8 * (c >> 1) + g] = off ? -1.0f : e;
         sc[j][n][c] = e;
@@ -698,7 +484,6 @@ __device__ __forceinline__ void step(const AttnParams& p, const AttnShared& sh, 
         pw[j][n][h] = transpose8(S::E4M3 ? pack_f16x2(sc[j][n][2 * h], sc[j][n][2 * h + 1])
                                          : pack_bf16x2_cvt(sc[j][n][2 * h], sc[j][n][2 * h + 1]));
     }
-  }
   // values
   uint32_t bad = 0;   // infinities and NaN where not every row sees every key: they take no part in the product
   if constexpr (S::E4M3) {
@@ -765,7 +550,7 @@ __device__ __forceinline__ void consume(const AttnParams& p, AttnShared& sh, con
   const uint32_t all_pages = S::KS >> info.box_shift >= 32 ? 0xffffffffu : (1u << (S::KS >> info.box_shift)) - 1;
   int st = 0;
   uint32_t parity = 0;
-  Walk<S::M, S::KS> w(p, sh, range);
+  Walk<S::M, S::KS> w(p, sh.work, range);
   float* mine = join + warp * 8 * NR * S::kJoinLd;
   bool ok = true;
   while (w.left > 0) {
@@ -782,7 +567,6 @@ __device__ __forceinline__ void consume(const AttnParams& p, AttnShared& sh, con
     }
     float fac[NR][2];
     Sums<S> a;
-    a.ve = -112;
     int64_t top = 0;         // largest position of the warp's rows
 #pragma unroll
     for (int n = 0; n < NR; ++n)
@@ -849,7 +633,7 @@ __device__ __forceinline__ void consume(const AttnParams& p, AttnShared& sh, con
       for (int c = 0; c < 2; ++c) {
         float mx = -INFINITY;
         for (int k = 0; k < S::KG; ++k) mx = fmaxf(mx, sh.m[rg * S::KG + k][8 * n + 2 * t + c]);
-        fold[n][c] = ex2(a.m[n][c] - (mx == -INFINITY ? 0.0f : mx)) * (S::E4M3 ? pow2(a.ve - kTop) : 1.0f);
+        fold[n][c] = ex2(a.m[n][c] - (mx == -INFINITY ? 0.0f : mx));
       }
     for (int c0 = 0; c0 < D; c0 += S::kCols) {
 #pragma unroll
@@ -931,7 +715,7 @@ __global__ void __launch_bounds__(S::kThreads, S::kPerSm) aq_tree_attention_kern
   }
   pdl_wait_prior_grid();
   int64_t range[2];
-  locate<S::M, S::KS>(p, sh, p.prefix, blockIdx.x == 0, range);
+  locate<S::M, S::KS>(p, sh.work, p.prefix, blockIdx.x == 0, range);
   const AbortCtl ctl = {&sh.abort, p.status, p.timeout_ns};
   if (threadIdx.x >= S::NW * 32) {
     // 384 threads at 168 registers: 256 at 232 and 128 at 40
@@ -1062,31 +846,12 @@ bool attn_layout(const aq_kv_cache* c, const aq_draft_batch* d, int32_t q_heads,
   return true;
 }
 
-// Cache codes as {D, page, pages * heads}: boxes of one column block (128 bytes at most) of up to KS rows.
-aq_status cache_map(CUtensorMap* m, const void* base, const aq_kv_cache* c, int box_cols, int box_rows, const char* who) {
-  const bool e4m3 = c->type == AQ_KV_E4M3;
-  const cuuint64_t es = e4m3 ? 1 : 2, row = c->head_dim * es;
-  const cuuint64_t dims[3] = {static_cast<cuuint64_t>(c->head_dim), static_cast<cuuint64_t>(c->page_size),
-                              static_cast<cuuint64_t>(c->pages) * c->kv_heads};
-  const cuuint64_t strides[2] = {row, row * c->page_size};
-  const cuuint32_t box[3] = {static_cast<cuuint32_t>(box_cols), static_cast<cuuint32_t>(box_rows), 1};
-  const cuuint32_t unit[3] = {1, 1, 1};
-  const serve_encode_fn fn = serve_encode();
-  if (!fn) return serve_fail(AQ_ERR_CUDA, "%s: cuTensorMapEncodeTiled is not available from the driver", who);
-  const CUresult r = fn(m, e4m3 ? CU_TENSOR_MAP_DATA_TYPE_UINT8 : CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 3, const_cast<void*>(base),
-                        dims, strides, box, unit, CU_TENSOR_MAP_INTERLEAVE_NONE,
-                        box_cols * es == 128 ? CU_TENSOR_MAP_SWIZZLE_128B : CU_TENSOR_MAP_SWIZZLE_64B,
-                        CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
-  if (r != CUDA_SUCCESS) return serve_fail(AQ_ERR_CUDA, "%s: cuTensorMapEncodeTiled failed (%d)", who, static_cast<int>(r));
-  return AQ_OK;
-}
-
 template <class S>
 aq_status launch_attention(AttnParams& p, const aq_kv_cache* c, const ServeDev& dev, cudaStream_t st, const char* who) {
   aq_status s;
   const int box = std::min(c->page_size, S::KS);
-  if ((s = cache_map(&p.tm_k, c->k, c, S::RB / S::ES, box, who)) != AQ_OK) return s;
-  if ((s = cache_map(&p.tm_v, c->v, c, S::RB / S::ES, box, who)) != AQ_OK) return s;
+  if ((s = attention_cache_map(&p.tm_k, c->k, c, S::RB / S::ES, box, who)) != AQ_OK) return s;
+  if ((s = attention_cache_map(&p.tm_v, c->v, c, S::RB / S::ES, box, who)) != AQ_OK) return s;
   constexpr size_t kStatic = (sizeof(AttnShared) + 127) / 128 * 128;
   constexpr size_t kUnit = S::kStage + 2 * S::kScale, kFixed = 1024 + S::kQ + S::kJoin;
   const size_t room = (dev.smem_optin + 1024) / S::kPerSm - 1024 - kStatic - kFixed;   // 1 KB a CTA is the system's

@@ -405,6 +405,44 @@ def test_attention_masked_infinities(kind):
 
 
 @KINDS
+def test_attention_scores_of_minus_infinity_and_negative_scale(kind):
+    """Keys of minus infinity under positive queries (bf16; an E4M3 cache reads such a key as NaN): rows of zeros
+    where no other key is seen, no weight where one is. A negative scale turns the order of the weights round."""
+    c = Case(15, kind, 64, 1, 1, 16, [100], [2], "chain")
+    if kind == "bf16":
+        c.q = c.q.abs() + 0.5
+        clean, _ = c.run()
+        c.cache.k[..., 0] = torch.where(torch.isnan(c.cache.k[..., 0]), c.cache.k[..., 0], -float("inf"))
+        out, lse = c.run()
+        assert not out.any() and bool((lse == -float("inf")).all())
+        page, off = divmod(int(c.slots[70]), 16)
+        c.cache.k[page, 0, off, 0] = 1.0
+        out, lse = c.run()
+        assert torch.equal(out, c.cache.v[page, 0, off].expand(2, 1, 64)) and bool(torch.isfinite(lse).all())
+    d = Case(16, kind, 128, 2, 2, 32, [70], [3], "tree")
+    flipped = aq.aq_tree_attention(d.cache, d.q, d.cu, d.ctx_t, d.table, max_q=3, mask=d.mask, depth=d.depth_t, scale=-128 ** -0.5)
+    d.q = -d.q
+    assert torch.equal(d.run()[0], flipped)
+
+
+@KINDS
+def test_attention_values_of_masked_keys_set_no_scale(kind):
+    """A drafted token with values of 1e30 leaves the rows that do not see it as they were."""
+    c = Case(17, kind, 128, 1, 2, 16, [40], [8], "tree")
+    clean, _ = c.run()
+    x = torch.full((1, 1, 128), 1e30, dtype=torch.bfloat16, device="cuda")
+    k = torch.zeros_like(x)
+    aq.aq_kv_write(c.cache, k, x, c.slots[43:44])
+    out, lse = c.run()
+    for i in range(8):
+        if c.bits[0][i, 3]:
+            assert bool((out[i].float().abs() > 1e20).all())
+        else:
+            assert torch.equal(out[i], clean[i]), i
+    c.check(out, lse)
+
+
+@KINDS
 def test_attention_left_out_pages_and_rows(kind):
     """Pages outside the cache and past the table are not read; rows past max_q are not written."""
     c = Case(7, kind, 64, 2, 2, 16, [100], [4], "chain")
