@@ -23,7 +23,8 @@ LIB_PATH = os.path.join(PKG_DIR, "libaq_gb300.so")
 DEBUG_BUILD_DIR = os.path.join(PKG_DIR, "_build_debug")
 DEBUG_LIB_PATH = os.path.join(PKG_DIR, "libaq_gb300_debug.so")
 SOURCES = ["aq_kernels.cu", "aq_decode.cu", "aq_decode2.cu", "aq_decompose.cu", "aq_host.cu", "aq_noalloc.cu",
-           "aq_positions.cu", "aq_attention.cu", "aq_verify.cu"]
+           "aq_positions.cu", "aq_attention.cu", "aq_attention_tc.cu",
+           "aq_verify.cu"]
 HEADERS = ["aq_ptx.cuh", "aq_internal.h", "aq_serve.h", "aq_attention.cuh"]
 
 # The serving calls' marshalling, a CPython module of host code (see csrc/aq_python.c).

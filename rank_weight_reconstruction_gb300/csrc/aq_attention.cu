@@ -820,8 +820,11 @@ __global__ void __launch_bounds__(128) aq_attention_join_kernel(const __grid_con
 // ---------------------------------------------------------------------------------
 // host
 // ---------------------------------------------------------------------------------
-// Rows of a tile: the fewest of 8, 16, 32, 64 that hold a sequence's rows of one key/value head.
-int rows_per_tile(int64_t rows) { return rows <= 8 ? 8 : rows <= 16 ? 16 : rows <= 32 ? 32 : 64; }
+// Rows of a tile: the fewest of 8, 16, 32, 64 (mma.sync), 128, 256 (tcgen05; 256 sums of D = 256 do not fit tensor
+// memory) that hold a sequence's rows of one key/value head.
+int rows_per_tile(int64_t rows, int D) {
+  return rows <= 8 ? 8 : rows <= 16 ? 16 : rows <= 32 ? 32 : rows <= 64 ? 64 : rows <= 128 || D == 256 ? 128 : 256;
+}
 
 struct AttnLayout {
   int rows = 0, row_tiles = 0;
@@ -833,11 +836,11 @@ constexpr int64_t kAttnMaxEntries = 1 << 22;
 bool attn_layout(const aq_kv_cache* c, const aq_draft_batch* d, int32_t q_heads, AttnLayout* out) {
   const int64_t rows = static_cast<int64_t>(d->max_q) * (q_heads / c->kv_heads);
   AttnLayout l;
-  l.rows = rows_per_tile(rows);
+  l.rows = rows_per_tile(rows, c->head_dim);
   const int64_t tiles = std::max<int64_t>((rows + l.rows - 1) / l.rows, 1);
   if (tiles * d->batch > kAttnMaxEntries) return false;
   l.row_tiles = static_cast<int>(tiles);
-  const int64_t ctas = kAttnSmsBound * kAttnMaxPerSm;
+  const int64_t ctas = kAttnSmsBound * (l.rows >= 128 ? 1 : kAttnMaxPerSm);
   auto up = [](size_t v) { return (v + 255) / 256 * 256; };
   l.part_ml = up((tiles * d->batch + 1) * 8);
   l.part_o = up(l.part_ml + ctas * 2 * l.rows * 8);
@@ -866,22 +869,23 @@ aq_status launch_attention(AttnParams& p, const aq_kv_cache* c, const ServeDev& 
     ready.fetch_or(bit);
   }
   p.main_grid = std::min(dev.sms, kAttnSmsBound) * S::kPerSm;
-  cudaError_t e = launch_serve(aq_tree_attention_kernel<S>, p, dim3(p.main_grid), S::kThreads, smem, st);
-  if (e == cudaSuccess)
-    e = launch_serve(aq_attention_join_kernel<S::D>, p, dim3(static_cast<unsigned>(p.total_q * p.hk * p.group)), 128, 0, st);
-  return serve_launched(e, who);
+  return serve_launched(launch_serve(aq_tree_attention_kernel<S>, p, dim3(p.main_grid), S::kThreads, smem, st), who);
 }
 
 // Registers (O^T takes D NR / 4 a thread) and shared memory decide how many CTAs share an SM.
 template <int D, bool E4M3>
 aq_status launch_rows(AttnParams& p, const aq_kv_cache* c, const ServeDev& dev, cudaStream_t st, const char* who) {
   constexpr int per1 = D == 256 && !E4M3 ? 1 : 2, per2 = D == 256 ? 1 : 2;
+  aq_status s;
   switch (p.rows_per_tile) {
-    case 8: return launch_attention<Shape<D, E4M3, 1, 1, 4, per1>>(p, c, dev, st, who);
-    case 16: return launch_attention<Shape<D, E4M3, 2, 1, 4, per2>>(p, c, dev, st, who);
-    case 32: return launch_attention<std::conditional_t<D == 256, Shape<D, E4M3, 2, 2, 8, 1>, Shape<D, E4M3, 4, 1, 8, 1>>>(p, c, dev, st, who);
-    default: return launch_attention<std::conditional_t<D == 256, Shape<D, E4M3, 2, 4, 8, 1>, Shape<D, E4M3, 4, 2, 8, 1>>>(p, c, dev, st, who);
+    case 8: s = launch_attention<Shape<D, E4M3, 1, 1, 4, per1>>(p, c, dev, st, who); break;
+    case 16: s = launch_attention<Shape<D, E4M3, 2, 1, 4, per2>>(p, c, dev, st, who); break;
+    case 32: s = launch_attention<std::conditional_t<D == 256, Shape<D, E4M3, 2, 2, 8, 1>, Shape<D, E4M3, 4, 1, 8, 1>>>(p, c, dev, st, who); break;
+    case 64: s = launch_attention<std::conditional_t<D == 256, Shape<D, E4M3, 2, 4, 8, 1>, Shape<D, E4M3, 4, 2, 8, 1>>>(p, c, dev, st, who); break;
+    default: s = launch_attention_tc(p, c, dev, st, who);
   }
+  if (s != AQ_OK) return s;
+  return serve_launched(launch_serve(aq_attention_join_kernel<D>, p, dim3(static_cast<unsigned>(p.total_q * p.hk * p.group)), 128, 0, st), who);
 }
 
 aq_status check_batch(const aq_kv_cache* c, const aq_draft_batch* d, int32_t q_heads, const char* who) {

@@ -1,0 +1,777 @@
+// aq_attention_tc.cu -- aq_tree_attention for many rows: S = Q K^T and O = P V on tcgen05, accumulators in tensor
+// memory.
+//
+// From about 128 rows a key/value head (64 drafted tokens of a group of four, a chunk of a prefill) a byte of cache
+// meets enough rows for the products to weigh as much as the loads, and mma.sync (607 TFLOP/s measured here) falls
+// behind HBM. A CTA takes one or two tiles of 128 rows of one item against key tiles of BN: a producer warp streams
+// pages with TMA, one thread issues the MMAs, and each row tile has a group of four warps, a thread to a row, that
+// turns its scores into weights (no exchange between threads: the row's maximum and sum are the thread's own).
+// With two row tiles the groups take turns, so that one's products run under the other's exponentials; with one,
+// two score buffers let the next scores form under the weights of this tile. The weights go back to tensor memory
+// over the scores they came from and enter P V from there; V is read as stored, [key][column], as the MN-major
+// operand. The sums O stay in tensor memory for the item; they are scaled over only when a row's reference is
+// passed by 2^kLag.
+//
+// E4M3 codes are widened to f16 tiles in shared memory by four warps in between (exact), once for all rows; scales
+// and f16 scaling as in the mma.sync kernel.
+#include <math.h>
+
+#include <algorithm>
+#include <atomic>
+
+#include "aq_attention.cuh"
+
+namespace aq {
+namespace {
+
+constexpr int kInfo = 8;      // tiles whose scales and page masks are kept
+constexpr int kMaxRing = 8;   // most tile buffers
+constexpr int kGroup = 128;   // threads (rows) of a row tile
+
+template <int D_, bool E4M3_, int TILES_>
+struct TcShape {
+  static constexpr int D = D_, TILES = TILES_;
+  static constexpr bool E4M3 = E4M3_;
+  static constexpr int M = 128 * TILES;
+  static constexpr int BN = D == 256 ? 64 : 128;           // keys of a tile
+  static constexpr int kTile = BN * D * 2;                 // bytes of a 16-bit K or V tile
+  static constexpr int kQ = M * D * 2;
+  static constexpr int CB = D < 128 ? D : 128;             // bytes of a row of one column block of codes
+  static constexpr int kCode = BN * D;                     // bytes of a tile of codes
+  static constexpr int kScale = E4M3 ? kInfo * 2 * BN * 4 : 0;
+  static constexpr int kSoftWarps = 4 * TILES;
+  static constexpr int kConvWarp = kSoftWarps;             // first of four converting warps (E4M3)
+  static constexpr int kTmaWarp = kSoftWarps + (E4M3 ? 4 : 0), kMmaWarp = kTmaWarp + 1;
+  static constexpr int kThreads = (kMmaWarp + 1) * 32;
+  // tensor memory: two score buffers, one a row tile or two of one tile (the weights over them), then the sums
+  static constexpr int kS(int x) { return x * 128; }
+  static constexpr int kO(int t) { return 256 + t * D; }
+  static_assert(256 + TILES * D <= 512, "tensor memory");
+  static constexpr int NF = E4M3 ? 3 : 0;                  // f16 buffers of an E4M3 cache
+};
+
+struct TcShared {
+  uint64_t full[kMaxRing], empty[kMaxRing];     // 16-bit tiles: K of tile n is buffer use 2 n, V use 2 n + 1
+  uint64_t cfull[kMaxRing], cempty[kMaxRing];   // codes
+  uint64_t info[kInfo];                         // page mask and scales of a tile
+  uint64_t q_ready, s_full[2], p_ready[2], o_done[2], together[2], drain;
+  uint32_t valid[kInfo];
+  int32_t skip[2];                              // the product P V of this score buffer is done by the threads
+  int32_t special[2][2];                        // [row tile][tile & 1]
+  uint32_t tmem;
+  int32_t abort;
+  int64_t top[2][4];
+  float fac[256];
+  AttnWork work;
+};
+
+__device__ __forceinline__ void tmem_ld32(uint32_t addr, float (&v)[32]) {
+  // one statement: the values exist only past the wait
+  asm volatile(
+      "tcgen05.ld.sync.aligned.32x32b.x32.b32 "
+      "{%0, %1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, %15, "
+      "%16, %17, %18, %19, %20, %21, %22, %23, %24, %25, %26, %27, %28, %29, %30, %31}, [%32];\n\t"
+      "tcgen05.wait::ld.sync.aligned;"
+      : "=f"(v[0]), "=f"(v[1]), "=f"(v[2]), "=f"(v[3]), "=f"(v[4]), "=f"(v[5]), "=f"(v[6]), "=f"(v[7]), "=f"(v[8]), "=f"(v[9]),
+        "=f"(v[10]), "=f"(v[11]), "=f"(v[12]), "=f"(v[13]), "=f"(v[14]), "=f"(v[15]), "=f"(v[16]), "=f"(v[17]), "=f"(v[18]),
+        "=f"(v[19]), "=f"(v[20]), "=f"(v[21]), "=f"(v[22]), "=f"(v[23]), "=f"(v[24]), "=f"(v[25]), "=f"(v[26]), "=f"(v[27]),
+        "=f"(v[28]), "=f"(v[29]), "=f"(v[30]), "=f"(v[31])
+      : "r"(addr)
+      : "memory");
+}
+__device__ __forceinline__ void tmem_ld16u(uint32_t addr, uint32_t (&v)[16]) {
+  asm volatile(
+      "tcgen05.ld.sync.aligned.32x32b.x16.b32 "
+      "{%0, %1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, %15}, [%16];\n\t"
+      "tcgen05.wait::ld.sync.aligned;"
+      : "=r"(v[0]), "=r"(v[1]), "=r"(v[2]), "=r"(v[3]), "=r"(v[4]), "=r"(v[5]), "=r"(v[6]), "=r"(v[7]), "=r"(v[8]), "=r"(v[9]),
+        "=r"(v[10]), "=r"(v[11]), "=r"(v[12]), "=r"(v[13]), "=r"(v[14]), "=r"(v[15])
+      : "r"(addr)
+      : "memory");
+}
+__device__ __forceinline__ void tmem_st32(uint32_t addr, const float (&v)[32]) {
+  asm volatile(
+      "tcgen05.st.sync.aligned.32x32b.x32.b32 [%0], "
+      "{%1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, %15, %16, "
+      "%17, %18, %19, %20, %21, %22, %23, %24, %25, %26, %27, %28, %29, %30, %31, %32};" ::"r"(addr),
+      "f"(v[0]), "f"(v[1]), "f"(v[2]), "f"(v[3]), "f"(v[4]), "f"(v[5]), "f"(v[6]), "f"(v[7]), "f"(v[8]), "f"(v[9]), "f"(v[10]),
+      "f"(v[11]), "f"(v[12]), "f"(v[13]), "f"(v[14]), "f"(v[15]), "f"(v[16]), "f"(v[17]), "f"(v[18]), "f"(v[19]), "f"(v[20]),
+      "f"(v[21]), "f"(v[22]), "f"(v[23]), "f"(v[24]), "f"(v[25]), "f"(v[26]), "f"(v[27]), "f"(v[28]), "f"(v[29]), "f"(v[30]),
+      "f"(v[31])
+      : "memory");
+}
+__device__ __forceinline__ void tmem_st16u(uint32_t addr, const uint32_t (&v)[16]) {
+  asm volatile(
+      "tcgen05.st.sync.aligned.32x32b.x16.b32 [%0], "
+      "{%1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, %15, %16};" ::"r"(addr),
+      "r"(v[0]), "r"(v[1]), "r"(v[2]), "r"(v[3]), "r"(v[4]), "r"(v[5]), "r"(v[6]), "r"(v[7]), "r"(v[8]), "r"(v[9]), "r"(v[10]),
+      "r"(v[11]), "r"(v[12]), "r"(v[13]), "r"(v[14]), "r"(v[15])
+      : "memory");
+}
+// D (+)= A B^T with A from tensor memory (rows the lanes, two 16-bit elements a column), B from shared memory.
+__device__ __forceinline__ void tc_mma_ts(uint32_t d, uint32_t a, uint64_t b_desc, uint32_t idesc, uint32_t accumulate) {
+  asm volatile(
+      "{\n\t.reg .pred p;\n\t"
+      "setp.ne.b32 p, %4, 0;\n\t"
+      "tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], %2, %3, p;\n\t}" ::"r"(d),
+      "r"(a), "l"(b_desc), "r"(idesc), "r"(accumulate)
+      : "memory");
+}
+// MN-major operand with 128-byte swizzle: 64 elements of the M/N dimension to a 128-byte row, rows along K, eight
+// rows (1024 bytes) repeating along K, blocks of 64 elements `block` bytes apart.
+__device__ __forceinline__ uint64_t smem_desc_mn128(uint32_t addr, uint32_t block) {
+  uint64_t d = 0;
+  d |= static_cast<uint64_t>((addr & 0x3FFFFu) >> 4);
+  d |= static_cast<uint64_t>(block >> 4) << 16;      // leading byte offset: next block of 64 elements
+  d |= static_cast<uint64_t>(1024 >> 4) << 32;       // stride byte offset: next eight rows along K
+  d |= static_cast<uint64_t>(1) << 46;
+  d |= static_cast<uint64_t>(2) << 61;
+  return d;
+}
+// kind::f16, f16 or bf16 operands, fp32 sums; b_mn: B is MN-major.
+constexpr uint32_t tc_idesc(bool f16, bool b_mn, int n) {
+  return (1u << 4) | ((f16 ? 0u : 1u) << 7) | ((f16 ? 0u : 1u) << 10) | ((b_mn ? 1u : 0u) << 16) | (static_cast<uint32_t>(n >> 3) << 17) |
+         (static_cast<uint32_t>(128 >> 4) << 24);
+}
+
+// Address of 16 bytes (eight elements from 8 c on) of a row of a 16-bit tile: column blocks of 64 elements, each
+// `rows` rows of 128 swizzled bytes.
+__device__ __forceinline__ uint32_t tile_addr(uint32_t base, int rows, int row, int c) {
+  return base + (c >> 3) * rows * 128 + row * 128 + (((c & 7) ^ (row & 7)) << 4);
+}
+
+// ---------------------------------------------------------------------------------
+// producer
+// ---------------------------------------------------------------------------------
+template <class S>
+__device__ __forceinline__ void tc_produce(const AttnParams& p, TcShared& sh, uint8_t* ring, uint8_t* scales, int nring,
+                                           const int64_t (&range)[2], const AbortCtl& ctl) {
+  constexpr int ES = S::E4M3 ? 1 : 2;
+  constexpr int kBytes = S::BN * S::D * ES;
+  constexpr int RB = S::E4M3 ? S::CB : 128, NC = S::D * ES / RB;
+  uint64_t* full = S::E4M3 ? sh.cfull : sh.full;
+  uint64_t* empty = S::E4M3 ? sh.cempty : sh.empty;
+  const int lane = threadIdx.x & 31;
+  const int page = 1 << p.page_shift;
+  const int box = min(page, S::BN), np = S::BN / box;
+  int b_of = 0, uses = 0, tile = 0;
+  uint32_t parity = 1;
+  Walk<S::M, S::BN> w(p, sh.work, range);
+  bool ok = true;
+  while (ok && w.left > 0) {
+    const int32_t* table = p.table + static_cast<int64_t>(w.entry / p.row_tiles) * p.ld_table;
+    auto page_id = [&](int64_t i) {   // -1: left out
+      if (i >= p.pages_per_seq || (i << p.page_shift) >= w.s.hi || ((i + 1) << p.page_shift) <= w.s.lo) return -1;
+      const int id = table[i];
+      return id >= 0 && id < p.pages ? id : -1;
+    };
+    int64_t base = (static_cast<int64_t>(w.tile0) * S::BN) >> p.page_shift;   // page numbers, 32 at a time and 32 ahead
+    int cur = page_id(base + lane), ahead = page_id(base + 32 + lane);
+    for (int i = 0; ok && i < w.n; ++i, ++tile) {
+      const int64_t key = static_cast<int64_t>(w.tile0 + i) * S::BN;
+      const int64_t first = key >> p.page_shift;
+      if (first >= base + 32) {
+        base += 32;
+        cur = ahead;
+        ahead = page_id(base + 32 + lane);
+      }
+      const int id = __shfl_sync(0xffffffffu, cur, static_cast<int>(first - base) + (lane < np ? lane : 0));
+      const bool valid = lane < np && id >= 0 && key + static_cast<int64_t>(lane) * box < w.s.hi;
+      const uint32_t mask = __ballot_sync(0xffffffffu, valid);
+      const int off = static_cast<int>(key & (page - 1));
+      const int row = id * p.hk + w.head;
+#pragma unroll 1
+      for (int kv = 0; kv < 2; ++kv) {
+        ok = __all_sync(0xffffffffu, mbar_wait(&empty[b_of], parity, ctl));
+        if (!ok) break;
+        const int slot = tile % kInfo;
+        if (lane == 0) {
+          if (kv == 0) {
+            sh.valid[slot] = mask;
+            mbar_arrive_expect_tx(&sh.info[slot], S::E4M3 ? __popc(mask) * box * 8 : 0);
+          }
+          mbar_arrive_expect_tx(&full[b_of], __popc(mask) * box * S::D * ES);
+        }
+        __syncwarp();
+        if (valid) {
+          uint8_t* dst = ring + b_of * kBytes + lane * box * RB;
+#pragma unroll
+          for (int c = 0; c < NC; ++c)
+            tma_load_3d(dst + c * S::BN * RB, kv ? &p.tm_v : &p.tm_k, c * (RB / ES), off, row, &full[b_of]);
+          if (S::E4M3 && kv == 0) {
+            const int64_t cell = (static_cast<int64_t>(row) << p.page_shift) + off;
+            uint8_t* sd = scales + slot * 2 * S::BN * 4 + lane * box * 4;
+            bulk_load(sd, p.ks + cell, box * 4, &sh.info[slot]);
+            bulk_load(sd + S::BN * 4, p.vs + cell, box * 4, &sh.info[slot]);
+          }
+        }
+        ++uses;
+        if (++b_of == nring) {
+          b_of = 0;
+          parity ^= 1;
+        }
+      }
+    }
+    if (ok) w.next(p);
+  }
+  if (!ok) {   // a wait ran out: let the copies already issued land before the CTA may end
+    for (int i = 0; i < min(uses, nring); ++i) {
+      const int u = uses - 1 - i;
+      const uint64_t t0 = global_timer_ns();
+      while (!mbar_try_wait(&full[u % nring], (u / nring) & 1))
+        if (global_timer_ns() - t0 > ctl.timeout_ns) break;
+    }
+    if (S::E4M3)
+      for (int i = 0; i < min(tile + 1, kInfo); ++i) {
+        const int u = tile - i;
+        const uint64_t t0 = global_timer_ns();
+        while (u >= 0 && 2 * u < uses && !mbar_try_wait(&sh.info[u % kInfo], (u / kInfo) & 1))
+          if (global_timer_ns() - t0 > ctl.timeout_ns) break;
+      }
+  }
+}
+
+// ---------------------------------------------------------------------------------
+// converting warps (E4M3): a tile of codes to a tile of halves
+// ---------------------------------------------------------------------------------
+template <class S>
+__device__ __forceinline__ void tc_convert(TcShared& sh, const uint8_t* codes, const uint8_t* tiles, int ncode, int64_t count,
+                                           const AbortCtl& ctl) {
+  constexpr int XC = S::D / 16;                // 16-byte chunks of a key's codes
+  constexpr int NF = S::E4M3 ? S::NF : 1;
+  const int tid = threadIdx.x - S::kConvWarp * 32, lane = tid & 31;
+  for (int64_t u = 0; u < 2 * count; ++u) {
+    const int c = static_cast<int>(u % ncode), f = static_cast<int>(u % NF);
+    if (!__all_sync(0xffffffffu, mbar_wait(&sh.cfull[c], static_cast<uint32_t>(u / ncode) & 1, ctl))) return;
+    if (!__all_sync(0xffffffffu, mbar_wait(&sh.empty[f], (static_cast<uint32_t>(u / NF) & 1) ^ 1, ctl))) return;
+    const uint32_t src = smem_u32(codes + c * S::kCode), dst = smem_u32(tiles + f * S::kTile);
+#pragma unroll 4
+    for (int i = tid; i < S::BN * XC; i += 128) {
+      const int key = i / XC, x = i % XC;
+      constexpr int XB = S::CB / 16;
+      const uint32_t from = src + (x / XB) * S::BN * S::CB + key * S::CB + (((x % XB) ^ (S::CB == 128 ? key & 7 : (key >> 1) & 3)) << 4);
+      uint32_t q[4], h[8];
+      asm volatile("ld.shared.v4.u32 {%0, %1, %2, %3}, [%4];" : "=r"(q[0]), "=r"(q[1]), "=r"(q[2]), "=r"(q[3]) : "r"(from) : "memory");
+#pragma unroll
+      for (int e = 0; e < 4; ++e) widen(q[e], h[2 * e], h[2 * e + 1]);
+#pragma unroll
+      for (int e = 0; e < 2; ++e)
+        asm volatile("st.shared.v4.u32 [%0], {%1, %2, %3, %4};" ::"r"(tile_addr(dst, S::BN, key, 2 * x + e)), "r"(h[4 * e]),
+                     "r"(h[4 * e + 1]), "r"(h[4 * e + 2]), "r"(h[4 * e + 3])
+                     : "memory");
+    }
+    fence_proxy_async_smem();
+    __syncwarp();
+    if (lane == 0) {
+      mbar_arrive(&sh.full[f]);
+      mbar_arrive(&sh.cempty[c]);
+    }
+  }
+}
+
+// ---------------------------------------------------------------------------------
+// MMA issue, one thread
+// ---------------------------------------------------------------------------------
+template <class S>
+__device__ __forceinline__ bool tc_issue(const AttnParams& p, TcShared& sh, const uint8_t* qbuf, const uint8_t* tiles, int nring,
+                                         uint32_t tmem, const int64_t (&range)[2], const AbortCtl& ctl) {
+  constexpr uint32_t kIdS = tc_idesc(S::E4M3, false, S::BN), kIdO = tc_idesc(S::E4M3, true, S::D);
+  Walk<S::M, S::BN> w(p, sh.work, range);
+  int64_t tile = 0;          // tiles so far, of all segments
+  uint32_t seg = 0;
+  auto x_of = [](int t, int64_t n) { return S::TILES == 2 ? t : static_cast<int>(n & 1); };
+  auto x_parity = [](int64_t n) { return static_cast<uint32_t>(S::TILES == 2 ? n & 1 : (n >> 1) & 1); };
+  auto scores = [&](int t, int64_t n) {
+    const int64_t u = 2 * n;
+    const uint32_t q = smem_u32(qbuf) + t * 128 * S::D * 2, k = smem_u32(tiles) + static_cast<uint32_t>(u % nring) * S::kTile;
+    const int x = x_of(t, n);
+#pragma unroll
+    for (int i = 0; i < S::D / 16; ++i)
+      tc_mma_bf16(tmem + S::kS(x), smem_desc_k128(q + (i >> 2) * 128 * 128 + (i & 3) * 32),
+                  smem_desc_k128(k + (i >> 2) * S::BN * 128 + (i & 3) * 32), kIdS, i > 0);
+    tc_commit(&sh.s_full[x]);
+    if (t == S::TILES - 1) tc_commit(&sh.empty[u % nring]);
+  };
+  auto sums = [&](int t, int64_t n, bool first) {
+    const int64_t u = 2 * n + 1;
+    const uint32_t v = smem_u32(tiles) + static_cast<uint32_t>(u % nring) * S::kTile;
+    const int x = x_of(t, n);
+    if (!*reinterpret_cast<volatile int32_t*>(&sh.skip[x])) {
+#pragma unroll
+      for (int i = 0; i < S::BN / 16; ++i)
+        tc_mma_ts(tmem + S::kO(t), tmem + S::kS(x) + 8 * i, smem_desc_mn128(v + i * 2048, S::BN * 128), kIdO, !(first && i == 0));
+    }
+    tc_commit(&sh.o_done[t]);
+    if (t == S::TILES - 1) tc_commit(&sh.empty[u % nring]);
+  };
+  auto arrived = [&](int64_t u) { return mbar_wait(&sh.full[u % nring], static_cast<uint32_t>(u / nring) & 1, ctl); };
+  for (; w.left > 0; w.next(p), ++seg) {
+    if (!mbar_wait(&sh.q_ready, seg & 1, ctl) || !arrived(2 * tile)) return false;
+    tc_fence_after();
+    for (int t = 0; t < S::TILES; ++t) scores(t, tile);
+    for (int i = 0; i < w.n; ++i, ++tile) {
+      const bool more = i + 1 < w.n;
+      if (S::TILES == 1 && more) {
+        if (!arrived(2 * tile + 2)) return false;
+        tc_fence_after();
+        scores(0, tile + 1);
+      }
+      for (int t = 0; t < S::TILES; ++t) {
+        if (!mbar_wait(&sh.p_ready[x_of(t, tile)], x_parity(tile), ctl) || !arrived(2 * tile + 1)) return false;
+        tc_fence_after();
+        sums(t, tile, i == 0);
+        if (S::TILES == 2 && more) {
+          if (!arrived(2 * tile + 2)) return false;
+          tc_fence_after();
+          scores(t, tile + 1);
+        }
+      }
+    }
+  }
+  return true;
+}
+
+// ---------------------------------------------------------------------------------
+// weights: a thread to a row
+// ---------------------------------------------------------------------------------
+// P V of one tile by the threads: taken where V holds infinities or NaN that some row does not see (0 times them would
+// reach every row). The weights are read back from tensor memory, masked keys by their bits.
+template <class S>
+__device__ __noinline__ void sums_by_hand(const AttnParams& p, const KeySpan& s, int i, int64_t pos, int64_t key0, uint32_t pages,
+                                          int box_shift, uint32_t p_addr, uint32_t o_addr, uint32_t v, bool first) {
+#pragma unroll 1
+  for (int d0 = 0; d0 < S::D; d0 += 32) {
+    float o[32];
+    tmem_ld32(o_addr + d0, o);
+    if (first)
+      for (int d = 0; d < 32; ++d) o[d] = 0.0f;
+#pragma unroll 1
+    for (int c = 0; c < S::BN / 32; ++c) {
+      const uint32_t bits = seen_bits(p, s, i, pos, key0 + 32 * c, 32 * c, 32, pages, box_shift);
+      uint32_t w[16];
+      tmem_ld16u(p_addr + 16 * c, w);
+#pragma unroll
+      for (int k = 0; k < 32; ++k) {
+        const uint16_t half = static_cast<uint16_t>(k & 1 ? w[k / 2] >> 16 : w[k / 2]);
+        const float wk = S::E4M3 ? __half2float(__ushort_as_half(half)) : bf16_to_f32(half);
+        if ((bits >> k) & 1) {
+#pragma unroll
+          for (int q = 0; q < 4; ++q) {
+            uint32_t r[4];
+            asm volatile("ld.shared.v4.u32 {%0, %1, %2, %3}, [%4];"
+                         : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3])
+                         : "r"(tile_addr(v, S::BN, 32 * c + k, d0 / 8 + q))
+                         : "memory");
+#pragma unroll
+            for (int e = 0; e < 4; ++e) {
+              float lo, hi;
+              if (S::E4M3) {
+                const float2 f = __half22float2(*reinterpret_cast<const __half2*>(&r[e]));
+                lo = f.x;
+                hi = f.y;
+              } else {
+                lo = __uint_as_float(r[e] << 16);
+                hi = __uint_as_float(r[e] & 0xffff0000u);
+              }
+              o[8 * q + 2 * e] = fmaf(wk, lo, o[8 * q + 2 * e]);
+              o[8 * q + 2 * e + 1] = fmaf(wk, hi, o[8 * q + 2 * e + 1]);
+            }
+          }
+        }
+      }
+    }
+    tmem_st32(o_addr + d0, o);
+  }
+  tmem_st_wait();
+}
+
+template <class S>
+__device__ __forceinline__ void tc_weigh(const AttnParams& p, TcShared& sh, uint8_t* qbuf, const uint8_t* tiles, const uint8_t* scales,
+                                         int nring, uint32_t tmem, const int64_t (&range)[2], const AbortCtl& ctl) {
+  constexpr int D = S::D, BN = S::BN;
+  const int tid = threadIdx.x, lane = tid & 31, t = tid / kGroup, r = tid % kGroup, wq = r >> 5;
+  const uint32_t lanes = static_cast<uint32_t>(wq * 32) << 16;   // this warp's quarter of the tensor memory lanes
+  const int box_shift = min(p.page_shift, 31 - __clz(BN));
+  const uint32_t all_pages = BN >> box_shift >= 32 ? 0xffffffffu : (1u << (BN >> box_shift)) - 1;
+  const float scale2 = p.scale * 1.4426950408889634f;
+  const uint32_t sign = scale2 < 0.0f ? 0x80008000u : 0u;
+  const uint32_t group = p.group;
+  int64_t tile = 0;
+  uint32_t together = 0;     // uses of the group's own barrier
+  bool ok = true;
+  auto wait = [&](uint64_t* bar, uint32_t parity) {
+    ok = ok && mbar_wait(bar, parity, ctl);
+    ok = __all_sync(0xffffffffu, ok);
+    return ok;
+  };
+  auto meet = [&]() {        // the group's 128 threads
+    __syncwarp();
+    if (lane == 0) mbar_arrive(&sh.together[t]);
+    return wait(&sh.together[t], together++ & 1);
+  };
+  Walk<S::M, BN> w(p, sh.work, range);
+  for (; w.left > 0; w.next(p)) {
+    const int rt = w.entry % p.row_tiles;
+    const uint32_t rows = static_cast<uint32_t>(w.s.T) * group, row0 = static_cast<uint32_t>(rt) * S::M + t * 128;
+    const uint32_t row = row0 + r;
+    const bool live_warp = row0 + wq * 32 < rows;
+    const int i_row = row < rows ? row / group : 0;
+    const int64_t pos = static_cast<int64_t>(w.s.ctx) + (p.mask && p.depth ? max(p.depth[w.s.first + i_row], 0) : i_row);
+    // queries of the warp's 32 rows, as the MMA reads them
+    constexpr int L = D / 8, RPW = 32 / L;       // lanes a row, rows at once
+    const int c = lane % L;
+    constexpr int kBatch = 8;
+#pragma unroll 1
+    for (int k0 = 0; k0 < 32 / RPW; k0 += kBatch) {
+      uint4 v[kBatch];
+#pragma unroll
+      for (int k = 0; k < kBatch; ++k) {
+        const uint32_t rr = row0 + wq * 32 + (k0 + k) * RPW + lane / L;
+        v[k] = make_uint4(0, 0, 0, 0);
+        if (rr < rows) {
+          const uint32_t i = rr / group;
+          v[k] = *reinterpret_cast<const uint4*>(p.q + (static_cast<int64_t>(w.s.first) + i) * p.q_tok + (w.head * group + (rr - i * group)) * p.q_head + c * 8);
+        }
+      }
+#pragma unroll
+      for (int k = 0; k < kBatch; ++k) {
+        const int lr = wq * 32 + (k0 + k) * RPW + lane / L;   // row within the tile
+        float fac = fabsf(scale2);
+        uint32_t x[4] = {v[k].x ^ sign, v[k].y ^ sign, v[k].z ^ sign, v[k].w ^ sign};
+        if constexpr (S::E4M3) {
+          uint32_t top = 0;
+#pragma unroll
+          for (int e = 0; e < 4; ++e) top = max(top, max((x[e] << 16) & 0x7fff0000u, x[e] & 0x7fff0000u));
+          const uint32_t who = (L == 32 ? 0xffffffffu : (1u << L) - 1) << (lane & ~(L - 1));
+#pragma unroll
+          for (int off = L / 2; off > 0; off >>= 1) top = max(top, __shfl_xor_sync(who, top, off));
+          const bool finite = top < 0x7f800000u;
+          const int e = finite ? top_exponent(__uint_as_float(top)) : 0;
+          const float f = pow2(14 - e);
+          fac = finite ? pow2(e - 14) * fac : __uint_as_float(0x7fc00000u);   // no finite score
+#pragma unroll
+          for (int y = 0; y < 4; ++y)
+            x[y] = finite ? pack_f16x2(__uint_as_float(x[y] << 16) * f, __uint_as_float(x[y] & 0xffff0000u) * f) : 0u;
+        }
+        if (c == 0) sh.fac[t * 128 + lr] = fac;
+        asm volatile("st.shared.v4.u32 [%0], {%1, %2, %3, %4};" ::"r"(tile_addr(smem_u32(qbuf) + t * 128 * D * 2, 128, lr, c)), "r"(x[0]),
+                     "r"(x[1]), "r"(x[2]), "r"(x[3])
+                     : "memory");
+      }
+    }
+    int64_t top = pos;
+#pragma unroll
+    for (int off = 16; off > 0; off >>= 1) top = max(top, __shfl_xor_sync(0xffffffffu, top, off));
+    if (lane == 0) sh.top[t][wq] = top;
+    fence_proxy_async_smem();
+    tc_fence_before();       // the last item's sums have been read
+    __syncwarp();
+    if (lane == 0) mbar_arrive(&sh.q_ready);
+    if (!meet()) return;
+    const float fac = sh.fac[t * 128 + r];
+#pragma unroll
+    for (int k = 0; k < 4; ++k) top = max(top, sh.top[t][k]);
+    // keys [whole0, whole1) are seen by every row of the tile
+    const int64_t whole1 = min(static_cast<int64_t>(w.s.ctx), w.s.hi), whole0 = p.window > 0 ? top - p.window + 1 : 0;
+
+    float m = -INFINITY, l = 0.0f;
+    for (int it = 0; it < w.n; ++it, ++tile) {
+      const int x = S::TILES == 2 ? t : static_cast<int>(tile & 1);
+      const uint32_t x_parity = static_cast<uint32_t>(S::TILES == 2 ? tile & 1 : (tile >> 1) & 1);
+      const int slot = static_cast<int>(tile % kInfo);
+      const uint32_t s_addr = tmem + lanes + S::kS(x), o_addr = tmem + lanes + S::kO(t);
+      if (!wait(&sh.info[slot], static_cast<uint32_t>(tile / kInfo) & 1) || !wait(&sh.s_full[x], x_parity)) return;
+      tc_fence_after();
+      const uint32_t pages = *reinterpret_cast<volatile uint32_t*>(&sh.valid[slot]);
+      const int64_t ka = static_cast<int64_t>(w.tile0 + it) * BN;
+      const bool whole = ka >= whole0 && ka + BN <= whole1 && pages == all_pages;
+      const float4* ks = reinterpret_cast<const float4*>(scales + slot * 2 * BN * 4);
+      const float4* vs = ks + BN / 4;
+      if (live_warp) {
+        // the row's largest logit, and what the reference has to cover
+        float want = -INFINITY;
+        if (whole) {
+          float mx = -INFINITY;
+#pragma unroll 1
+          for (int c = 0; c < BN / 32; ++c) {
+            float v[32];
+            tmem_ld32(s_addr + 32 * c, v);
+            if constexpr (S::E4M3) {
+#pragma unroll
+              for (int e = 0; e < 8; ++e) {
+                const float4 f = ks[8 * c + e];
+                mx = fmaxf(fmaxf(fmaxf(mx, v[4 * e] * f.x), fmaxf(v[4 * e + 1] * f.y, v[4 * e + 2] * f.z)), v[4 * e + 3] * f.w);
+              }
+            } else {
+#pragma unroll
+              for (int e = 0; e < 32; e += 2) mx = fmaxf(mx, fmaxf(v[e], v[e + 1]));
+            }
+          }
+          float e = 0.0f;
+          if constexpr (S::E4M3) {
+            const float* f = reinterpret_cast<const float*>(vs);
+            uint32_t big = 0;   // a NaN counts as the largest: every row sees it and is NaN
+#pragma unroll
+            for (int k = 0; k < BN / 32; ++k) big = max(big, __float_as_uint(f[32 * k + lane]));
+            e = scale_exponent(__uint_as_float(__reduce_max_sync(0xffffffffu, big))) - kTop;
+          }
+          want = mx == -INFINITY ? mx : fmaf(mx, fac, e);
+        } else {
+#pragma unroll 1
+          for (int c = 0; c < BN / 32; ++c) {
+            const uint32_t bits = seen_bits(p, w.s, i_row, pos, ka + 32 * c, 32 * c, 32, pages, box_shift);
+            float v[32];
+            tmem_ld32(s_addr + 32 * c, v);
+            const float* kf = reinterpret_cast<const float*>(ks) + 32 * c;
+            const float* vf = reinterpret_cast<const float*>(vs) + 32 * c;
+#pragma unroll
+            for (int e = 0; e < 32; ++e) {
+              const float y = S::E4M3 ? v[e] * kf[e] : v[e];
+              if (((bits >> e) & 1) && y != -INFINITY) want = fmaxf(want, fmaf(y, fac, S::E4M3 ? scale_exponent(vf[e]) - kTop : 0.0f));
+            }
+          }
+        }
+        const bool grown = want > m + kLag;
+        if (__any_sync(0xffffffffu, grown)) {
+          const float mx = fmaxf(m, want), keep = ex2(m - (mx == -INFINITY ? 0.0f : mx));
+          m = mx;
+          l *= keep;
+          if (it > 0) {   // the sums of the item so far
+            if (!wait(&sh.o_done[t], static_cast<uint32_t>(tile - 1) & 1)) return;
+            tc_fence_after();
+#pragma unroll 1
+            for (int d = 0; d < D; d += 32) {
+              float v[32];
+              tmem_ld32(o_addr + d, v);
+#pragma unroll
+              for (int e = 0; e < 32; ++e) v[e] *= keep;
+              tmem_st32(o_addr + d, v);
+            }
+            tmem_st_wait();
+          }
+        }
+        const float mz = m == -INFINITY ? 0.0f : m;
+#pragma unroll 1
+        for (int c = 0; c < BN / 32; ++c) {
+          const uint32_t bits = whole ? 0xffffffffu : seen_bits(p, w.s, i_row, pos, ka + 32 * c, 32 * c, 32, pages, box_shift);
+          float v[32];
+          tmem_ld32(s_addr + 32 * c, v);
+          uint32_t pk[16];
+#pragma unroll
+          for (int e = 0; e < 8; ++e) {
+            float4 kf = make_float4(1.0f, 1.0f, 1.0f, 1.0f), vf = kf;
+            if (S::E4M3) {
+              kf = ks[8 * c + e];
+              vf = vs[8 * c + e];
+            }
+            const float k4[4] = {kf.x, kf.y, kf.z, kf.w}, v4[4] = {vf.x, vf.y, vf.z, vf.w};
+#pragma unroll
+            for (int k = 0; k < 4; ++k) {
+              const float y = S::E4M3 ? v[4 * e + k] * k4[k] : v[4 * e + k];
+              float u = ex2(fmaf(y, fac, -mz));
+              if (!whole && (!((bits >> (4 * e + k)) & 1) || y == -INFINITY)) u = 0.0f;
+              l += u;
+              if (S::E4M3) {
+                u *= v4[k];
+                if (!whole && !((bits >> (4 * e + k)) & 1)) u = 0.0f;   // whatever scale lies there
+              }
+              v[4 * e + k] = u;
+            }
+            pk[2 * e] = S::E4M3 ? pack_f16x2(v[4 * e], v[4 * e + 1]) : pack_bf16x2_cvt(v[4 * e], v[4 * e + 1]);
+            pk[2 * e + 1] = S::E4M3 ? pack_f16x2(v[4 * e + 2], v[4 * e + 3]) : pack_bf16x2_cvt(v[4 * e + 2], v[4 * e + 3]);
+          }
+          tmem_st16u(s_addr + 16 * c, pk);   // over scores already read
+        }
+        tmem_st_wait();
+      }
+      if (!whole) {
+        // Values behind the last key and in pages left out may hold anything: zeros in their place. Infinities and NaN in
+        // keys that some row sees: the product is done by hand.
+        const int64_t u = 2 * tile + 1;
+        if (!wait(&sh.full[u % nring], static_cast<uint32_t>(u / nring) & 1)) return;
+        const uint32_t vb = smem_u32(tiles) + static_cast<uint32_t>(u % nring) * S::kTile;
+        if (r == 0) sh.special[t][tile & 1] = 0;
+        if (!meet()) return;
+        bool special = false;
+#pragma unroll 1
+        for (int e = r; e < BN * D / 8; e += kGroup) {
+          const int key = e / (D / 8), c = e % (D / 8);
+          const uint32_t at = tile_addr(vb, BN, key, c);
+          uint32_t q[4];
+          asm volatile("ld.shared.v4.u32 {%0, %1, %2, %3}, [%4];" : "=r"(q[0]), "=r"(q[1]), "=r"(q[2]), "=r"(q[3]) : "r"(at) : "memory");
+          const uint32_t exp = S::E4M3 ? 0x7c007c00u : 0x7f807f80u;
+          uint32_t odd = 0;
+#pragma unroll
+          for (int k = 0; k < 4; ++k) odd |= __vcmpeq2(q[k] & exp, exp);
+          if (odd) {
+            const int64_t kk = ka + key;
+            if (kk < w.s.lo || kk >= w.s.hi || !((pages >> (key >> box_shift)) & 1))
+              asm volatile("st.shared.v4.u32 [%0], {%1, %1, %1, %1};" ::"r"(at), "r"(0) : "memory");
+            else
+              special = true;
+          }
+        }
+        if (special) sh.special[t][tile & 1] = 1;
+        fence_proxy_async_smem();
+        if (!meet()) return;
+        const bool by_hand = *reinterpret_cast<volatile int32_t*>(&sh.special[t][tile & 1]) != 0;
+        if (by_hand) {
+          if (it > 0 && !wait(&sh.o_done[t], static_cast<uint32_t>(tile - 1) & 1)) return;
+          tc_fence_after();
+          if (live_warp) sums_by_hand<S>(p, w.s, i_row, pos, ka, pages, box_shift, s_addr, o_addr, vb, it == 0);
+        }
+        if (r == 0) sh.skip[x] = by_hand;
+      } else if (r == 0) {
+        sh.skip[x] = 0;
+      }
+      tc_fence_before();
+      __syncwarp();
+      if (lane == 0) mbar_arrive(&sh.p_ready[x]);
+    }
+    // the item's rows
+    if (!wait(&sh.o_done[t], static_cast<uint32_t>(tile - 1) & 1)) return;
+    tc_fence_after();
+    if (live_warp) {
+      const bool complete = w.n == w.len;
+      const int slot = w.offset > 0 ? 0 : 1;   // partial sums: an item begun elsewhere, or one that goes on elsewhere
+      const bool none = m == -INFINITY && l == 0.0f;
+      const float inv = complete ? (none ? 0.0f : 1.0f / l) : 1.0f;
+      const int head = w.head * group + static_cast<int>(row - static_cast<uint32_t>(i_row) * group);
+      const int64_t out_row = static_cast<int64_t>(w.s.first) + i_row;
+      const int64_t at = (static_cast<int64_t>(blockIdx.x) * 2 + slot) * S::M + t * 128 + r;
+#pragma unroll 1
+      for (int d = 0; d < D; d += 32) {
+        float v[32];
+        tmem_ld32(tmem + lanes + S::kO(t) + d, v);
+        if (row >= rows) continue;
+        if (complete) {
+          uint4* dst = reinterpret_cast<uint4*>(p.o + out_row * p.o_tok + head * p.o_head + d);
+#pragma unroll
+          for (int q = 0; q < 4; ++q) {
+            const float* f = v + 8 * q;
+            dst[q] = none ? make_uint4(0, 0, 0, 0)
+                          : make_uint4(pack_bf16x2_cvt(f[0] * inv, f[1] * inv), pack_bf16x2_cvt(f[2] * inv, f[3] * inv),
+                                       pack_bf16x2_cvt(f[4] * inv, f[5] * inv), pack_bf16x2_cvt(f[6] * inv, f[7] * inv));
+          }
+        } else {
+          float4* dst = reinterpret_cast<float4*>(p.part_o + at * D + d);
+#pragma unroll
+          for (int q = 0; q < 8; ++q) dst[q] = make_float4(v[4 * q], v[4 * q + 1], v[4 * q + 2], v[4 * q + 3]);
+        }
+      }
+      if (row < rows) {
+        if (!complete) p.part_ml[at] = make_float2(m, l);
+        else if (p.lse) p.lse[out_row * (p.hk * p.group) + head] = none ? -INFINITY : ((m == -INFINITY ? 0.0f : m) + log2f(l)) * 0.6931471805599453f;
+      }
+    }
+  }
+}
+
+template <class S>
+__global__ void __launch_bounds__(S::kThreads, 1) aq_tree_attention_tc_kernel(const __grid_constant__ AttnParams p) {
+  extern __shared__ uint8_t raw[];
+  __shared__ TcShared sh;
+  uint8_t* qbuf = raw + ((1024 - (smem_u32(raw) & 1023)) & 1023);
+  uint8_t* tiles = qbuf + S::kQ;                                     // 16-bit K and V tiles
+  const int nring = S::E4M3 ? S::NF : p.stages;
+  uint8_t* codes = tiles + nring * S::kTile;                         // E4M3: p.stages tiles of codes
+  uint8_t* scales = codes + (S::E4M3 ? p.stages * S::kCode : 0);
+  const int warp = threadIdx.x >> 5;
+  if (threadIdx.x == 0) {
+    for (int i = 0; i < kMaxRing; ++i) {
+      mbar_init(&sh.full[i], S::E4M3 ? 4 : 1);
+      mbar_init(&sh.empty[i], 1);
+      mbar_init(&sh.cfull[i], 1);
+      mbar_init(&sh.cempty[i], 4);
+    }
+    for (int i = 0; i < kInfo; ++i) mbar_init(&sh.info[i], 1);
+    mbar_init(&sh.q_ready, S::kSoftWarps);
+    for (int i = 0; i < 2; ++i) {
+      mbar_init(&sh.s_full[i], 1);
+      mbar_init(&sh.p_ready[i], 4);
+      mbar_init(&sh.o_done[i], 1);
+      mbar_init(&sh.together[i], 4);
+      sh.skip[i] = 0;
+    }
+    mbar_init(&sh.drain, 1);
+    sh.abort = 0;
+    fence_barrier_init();
+    tma_prefetch_desc(&p.tm_k);
+    tma_prefetch_desc(&p.tm_v);
+  }
+  if (warp == S::kMmaWarp) {
+    tmem_alloc(&sh.tmem, 512);
+    tmem_relinquish();
+  }
+  tc_fence_before();
+  __syncthreads();
+  tc_fence_after();
+  const uint32_t tmem = sh.tmem;
+  pdl_wait_prior_grid();
+  int64_t range[2];
+  locate<S::M, S::BN>(p, sh.work, p.prefix, blockIdx.x == 0, range);
+  const AbortCtl ctl = {&sh.abort, p.status, p.timeout_ns};
+  if (warp < S::kSoftWarps) {
+    tc_weigh<S>(p, sh, qbuf, tiles, scales, nring, tmem, range, ctl);
+  } else if (warp == S::kTmaWarp) {
+    tc_produce<S>(p, sh, S::E4M3 ? codes : tiles, scales, p.stages, range, ctl);
+  } else if (warp == S::kMmaWarp) {
+    if ((threadIdx.x & 31) == 0 && range[1] > range[0]) {
+      tc_issue<S>(p, sh, qbuf, tiles, nring, tmem, range, ctl);
+      tc_commit(&sh.drain);   // nothing is in flight when tensor memory is freed
+      const uint64_t t0 = global_timer_ns();
+      while (!mbar_try_wait(&sh.drain, 0))
+        if (global_timer_ns() - t0 > p.timeout_ns) break;
+    }
+    __syncwarp();
+  } else if (S::E4M3) {
+    tc_convert<S>(sh, codes, tiles, p.stages, range[1] - range[0], ctl);
+  }
+  tc_fence_before();
+  __syncthreads();
+  if (warp == S::kMmaWarp) {
+    tc_fence_after();
+    tmem_dealloc(tmem, 512);
+  }
+  pdl_launch_dependents();
+}
+
+template <class S>
+aq_status launch_tc(AttnParams& p, const aq_kv_cache* c, const ServeDev& dev, cudaStream_t st, const char* who) {
+  aq_status s;
+  const int box = std::min(c->page_size, S::BN), cols = S::E4M3 ? S::CB : 64;
+  if ((s = attention_cache_map(&p.tm_k, c->k, c, cols, box, who)) != AQ_OK) return s;
+  if ((s = attention_cache_map(&p.tm_v, c->v, c, cols, box, who)) != AQ_OK) return s;
+  constexpr size_t kStatic = (sizeof(TcShared) + 127) / 128 * 128, kFixed = 1024 + S::kQ + S::kScale + S::NF * S::kTile;
+  constexpr size_t kUnit = S::E4M3 ? S::kCode : S::kTile;
+  if (dev.smem_optin < kStatic + kFixed + 2 * kUnit) return serve_fail(AQ_ERR_UNSUPPORTED, "%s: the device has too little shared memory", who);
+  p.stages = static_cast<int>(std::min<size_t>((dev.smem_optin - kStatic - kFixed) / kUnit, S::E4M3 ? 6 : kMaxRing));
+  const size_t smem = kFixed + p.stages * kUnit;
+  static std::atomic<uint64_t> ready{0};   // devices on which the kernel may use that much
+  const uint64_t bit = 1ull << dev.index;
+  if (!(ready.load() & bit)) {
+    const cudaError_t e = cudaFuncSetAttribute(aq_tree_attention_tc_kernel<S>, cudaFuncAttributeMaxDynamicSharedMemorySize, static_cast<int>(smem));
+    if (e != cudaSuccess) return serve_launched(e, who);
+    ready.fetch_or(bit);
+  }
+  p.main_grid = std::min(dev.sms, kAttnSmsBound);
+  return serve_launched(launch_serve(aq_tree_attention_tc_kernel<S>, p, dim3(p.main_grid), S::kThreads, smem, st), who);
+}
+
+}  // namespace
+
+aq_status launch_attention_tc(AttnParams& p, const aq_kv_cache* c, const ServeDev& dev, cudaStream_t st, const char* who) {
+  const bool e4m3 = c->type == AQ_KV_E4M3, two = p.rows_per_tile == 256;
+  switch (c->head_dim) {
+    case 64:
+      if (two) return e4m3 ? launch_tc<TcShape<64, true, 2>>(p, c, dev, st, who) : launch_tc<TcShape<64, false, 2>>(p, c, dev, st, who);
+      return e4m3 ? launch_tc<TcShape<64, true, 1>>(p, c, dev, st, who) : launch_tc<TcShape<64, false, 1>>(p, c, dev, st, who);
+    case 128:
+      if (two) return e4m3 ? launch_tc<TcShape<128, true, 2>>(p, c, dev, st, who) : launch_tc<TcShape<128, false, 2>>(p, c, dev, st, who);
+      return e4m3 ? launch_tc<TcShape<128, true, 1>>(p, c, dev, st, who) : launch_tc<TcShape<128, false, 1>>(p, c, dev, st, who);
+    default:
+      return e4m3 ? launch_tc<TcShape<256, true, 1>>(p, c, dev, st, who) : launch_tc<TcShape<256, false, 1>>(p, c, dev, st, who);
+  }
+}
+
+}  // namespace aq

@@ -152,7 +152,7 @@ def call_attention(lib, d=None, c=None, q=C, heads=4, qt=256, qh=64, o=D_, ot=25
     (dict(qt=252), b.AQ_ERR_ALIGNMENT), (dict(ot=128), b.AQ_ERR_SHAPE), (dict(o=C), b.AQ_ERR_OVERLAP), (dict(o=A), b.AQ_ERR_OVERLAP),
     (dict(lse=D_ + 16), b.AQ_ERR_OVERLAP), (dict(lse=2), b.AQ_ERR_ALIGNMENT), (dict(ws=0), b.AQ_ERR_WORKSPACE),
     (dict(ws=0x80000010), b.AQ_ERR_WORKSPACE), (dict(ws_bytes=4096), b.AQ_ERR_WORKSPACE), (dict(ws=A), b.AQ_ERR_OVERLAP),
-    (dict(ws=D_), b.AQ_ERR_OVERLAP), (dict(d=dict(batch=1 << 22, max_q=64)), b.AQ_ERR_SHAPE),
+    (dict(ws=D_), b.AQ_ERR_OVERLAP), (dict(d=dict(batch=1 << 23, max_q=64)), b.AQ_ERR_SHAPE),
 ])
 def test_attention_refusals(lib, kw, status):
     assert call_attention(lib, **kw) == status, b.aq_last_error()
