@@ -79,6 +79,25 @@ __device__ __forceinline__ void tmem_ld32(uint32_t addr, float (&v)[32]) {
       : "r"(addr)
       : "memory");
 }
+// The same in two halves, for loads under other work: the values may be used past tmem_ld32_wait alone.
+__device__ __forceinline__ void tmem_ld32_issue(uint32_t addr, float (&v)[32]) {
+  asm volatile(
+      "tcgen05.ld.sync.aligned.32x32b.x32.b32 "
+      "{%0, %1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, %15, "
+      "%16, %17, %18, %19, %20, %21, %22, %23, %24, %25, %26, %27, %28, %29, %30, %31}, [%32];"
+      : "=f"(v[0]), "=f"(v[1]), "=f"(v[2]), "=f"(v[3]), "=f"(v[4]), "=f"(v[5]), "=f"(v[6]), "=f"(v[7]), "=f"(v[8]), "=f"(v[9]),
+        "=f"(v[10]), "=f"(v[11]), "=f"(v[12]), "=f"(v[13]), "=f"(v[14]), "=f"(v[15]), "=f"(v[16]), "=f"(v[17]), "=f"(v[18]),
+        "=f"(v[19]), "=f"(v[20]), "=f"(v[21]), "=f"(v[22]), "=f"(v[23]), "=f"(v[24]), "=f"(v[25]), "=f"(v[26]), "=f"(v[27]),
+        "=f"(v[28]), "=f"(v[29]), "=f"(v[30]), "=f"(v[31])
+      : "r"(addr)
+      : "memory");
+}
+__device__ __forceinline__ void tmem_ld32_wait(float (&v)[32]) {
+  asm volatile("tcgen05.wait::ld.sync.aligned;" ::: "memory");
+#pragma unroll
+  for (int i = 0; i < 32; i += 8)   // the values pass through here, so no use of them moves before the wait
+    asm volatile("" : "+f"(v[i]), "+f"(v[i + 1]), "+f"(v[i + 2]), "+f"(v[i + 3]), "+f"(v[i + 4]), "+f"(v[i + 5]), "+f"(v[i + 6]), "+f"(v[i + 7])::"memory");
+}
 __device__ __forceinline__ void tmem_ld16u(uint32_t addr, uint32_t (&v)[16]) {
   asm volatile(
       "tcgen05.ld.sync.aligned.32x32b.x16.b32 "
@@ -140,6 +159,19 @@ __device__ __forceinline__ uint32_t tile_addr(uint32_t base, int rows, int row, 
   return base + (c >> 3) * rows * 128 + row * 128 + (((c & 7) ^ (row & 7)) << 4);
 }
 
+// A position in a ring of `n` buffers: index, and the parity of the phase its use completes.
+struct Ring {
+  int n, i = 0;
+  uint32_t phase = 0;
+  __device__ __forceinline__ explicit Ring(int size) : n(size) {}
+  __device__ __forceinline__ void next() {
+    if (++i == n) {
+      i = 0;
+      phase ^= 1;
+    }
+  }
+};
+
 // ---------------------------------------------------------------------------------
 // producer
 // ---------------------------------------------------------------------------------
@@ -154,8 +186,8 @@ __device__ __forceinline__ void tc_produce(const AttnParams& p, TcShared& sh, ui
   const int lane = threadIdx.x & 31;
   const int page = 1 << p.page_shift;
   const int box = min(page, S::BN), np = S::BN / box;
-  int b_of = 0, uses = 0, tile = 0;
-  uint32_t parity = 1;
+  int uses = 0, tile = 0;
+  Ring at(nring);
   Walk<S::M, S::BN> w(p, sh.work, range);
   bool ok = true;
   while (ok && w.left > 0) {
@@ -182,7 +214,7 @@ __device__ __forceinline__ void tc_produce(const AttnParams& p, TcShared& sh, ui
       const int row = id * p.hk + w.head;
 #pragma unroll 1
       for (int kv = 0; kv < 2; ++kv) {
-        ok = __all_sync(0xffffffffu, mbar_wait(&empty[b_of], parity, ctl));
+        ok = __all_sync(0xffffffffu, mbar_wait(&empty[at.i], at.phase ^ 1, ctl));
         if (!ok) break;
         const int slot = tile % kInfo;
         if (lane == 0) {
@@ -190,14 +222,14 @@ __device__ __forceinline__ void tc_produce(const AttnParams& p, TcShared& sh, ui
             sh.valid[slot] = mask;
             mbar_arrive_expect_tx(&sh.info[slot], S::E4M3 ? __popc(mask) * box * 8 : 0);
           }
-          mbar_arrive_expect_tx(&full[b_of], __popc(mask) * box * S::D * ES);
+          mbar_arrive_expect_tx(&full[at.i], __popc(mask) * box * S::D * ES);
         }
         __syncwarp();
         if (valid) {
-          uint8_t* dst = ring + b_of * kBytes + lane * box * RB;
+          uint8_t* dst = ring + at.i * kBytes + lane * box * RB;
 #pragma unroll
           for (int c = 0; c < NC; ++c)
-            tma_load_3d(dst + c * S::BN * RB, kv ? &p.tm_v : &p.tm_k, c * (RB / ES), off, row, &full[b_of]);
+            tma_load_3d(dst + c * S::BN * RB, kv ? &p.tm_v : &p.tm_k, c * (RB / ES), off, row, &full[at.i]);
           if (S::E4M3 && kv == 0) {
             const int64_t cell = (static_cast<int64_t>(row) << p.page_shift) + off;
             uint8_t* sd = scales + slot * 2 * S::BN * 4 + lane * box * 4;
@@ -206,10 +238,7 @@ __device__ __forceinline__ void tc_produce(const AttnParams& p, TcShared& sh, ui
           }
         }
         ++uses;
-        if (++b_of == nring) {
-          b_of = 0;
-          parity ^= 1;
-        }
+        at.next();
       }
     }
     if (ok) w.next(p);
@@ -240,31 +269,43 @@ __device__ __forceinline__ void tc_convert(TcShared& sh, const uint8_t* codes, c
   constexpr int XC = S::D / 16;                // 16-byte chunks of a key's codes
   constexpr int NF = S::E4M3 ? S::NF : 1;
   const int tid = threadIdx.x - S::kConvWarp * 32, lane = tid & 31;
-  for (int64_t u = 0; u < 2 * count; ++u) {
-    const int c = static_cast<int>(u % ncode), f = static_cast<int>(u % NF);
-    if (!__all_sync(0xffffffffu, mbar_wait(&sh.cfull[c], static_cast<uint32_t>(u / ncode) & 1, ctl))) return;
-    if (!__all_sync(0xffffffffu, mbar_wait(&sh.empty[f], (static_cast<uint32_t>(u / NF) & 1) ^ 1, ctl))) return;
-    const uint32_t src = smem_u32(codes + c * S::kCode), dst = smem_u32(tiles + f * S::kTile);
-#pragma unroll 4
-    for (int i = tid; i < S::BN * XC; i += 128) {
-      const int key = i / XC, x = i % XC;
-      constexpr int XB = S::CB / 16;
-      const uint32_t from = src + (x / XB) * S::BN * S::CB + key * S::CB + (((x % XB) ^ (S::CB == 128 ? key & 7 : (key >> 1) & 3)) << 4);
-      uint32_t q[4], h[8];
-      asm volatile("ld.shared.v4.u32 {%0, %1, %2, %3}, [%4];" : "=r"(q[0]), "=r"(q[1]), "=r"(q[2]), "=r"(q[3]) : "r"(from) : "memory");
+  Ring from(ncode), to(NF);
+  for (int64_t u = 0; u < 2 * count; ++u, from.next(), to.next()) {
+    if (!__all_sync(0xffffffffu, mbar_wait(&sh.cfull[from.i], from.phase, ctl))) return;
+    if (!__all_sync(0xffffffffu, mbar_wait(&sh.empty[to.i], to.phase ^ 1, ctl))) return;
+    const uint32_t src = smem_u32(codes + from.i * S::kCode), dst = smem_u32(tiles + to.i * S::kTile);
+    constexpr int kRounds = S::BN * XC / 128, kBatch = kRounds < 4 ? kRounds : 4, XB = S::CB / 16;
+#pragma unroll 1
+    for (int k = 0; k < kRounds; k += kBatch) {
+      uint32_t q[kBatch][4];
 #pragma unroll
-      for (int e = 0; e < 4; ++e) widen(q[e], h[2 * e], h[2 * e + 1]);
+      for (int j = 0; j < kBatch; ++j) {
+        const int i = (k + j) * 128 + tid, key = i / XC, x = i % XC;
+        const uint32_t at = src + (x / XB) * S::BN * S::CB + key * S::CB + (((x % XB) ^ (S::CB == 128 ? key & 7 : (key >> 1) & 3)) << 4);
+        asm volatile("ld.shared.v4.u32 {%0, %1, %2, %3}, [%4];" : "=r"(q[j][0]), "=r"(q[j][1]), "=r"(q[j][2]), "=r"(q[j][3]) : "r"(at) : "memory");
+      }
 #pragma unroll
-      for (int e = 0; e < 2; ++e)
-        asm volatile("st.shared.v4.u32 [%0], {%1, %2, %3, %4};" ::"r"(tile_addr(dst, S::BN, key, 2 * x + e)), "r"(h[4 * e]),
-                     "r"(h[4 * e + 1]), "r"(h[4 * e + 2]), "r"(h[4 * e + 3])
-                     : "memory");
+      for (int j = 0; j < kBatch; ++j) {
+        const int i = (k + j) * 128 + tid, key = i / XC, x = i % XC;
+        uint32_t h[8];
+#pragma unroll
+        for (int e = 0; e < 4; ++e) widen(q[j][e], h[2 * e], h[2 * e + 1]);
+        // eight neighbouring lanes store to eight different 16-byte columns: every second four begin with the upper half
+        const int swap = XC > 4 ? (x >> 2) & 1 : 0;
+#pragma unroll
+        for (int e = 0; e < 2; ++e) {
+          const bool up = (e ^ swap) != 0;
+          asm volatile("st.shared.v4.u32 [%0], {%1, %2, %3, %4};" ::"r"(tile_addr(dst, S::BN, key, 2 * x + (up ? 1 : 0))), "r"(up ? h[4] : h[0]),
+                       "r"(up ? h[5] : h[1]), "r"(up ? h[6] : h[2]), "r"(up ? h[7] : h[3])
+                       : "memory");
+        }
+      }
     }
     fence_proxy_async_smem();
     __syncwarp();
     if (lane == 0) {
-      mbar_arrive(&sh.full[f]);
-      mbar_arrive(&sh.cempty[c]);
+      mbar_arrive(&sh.full[to.i]);
+      mbar_arrive(&sh.cempty[from.i]);
     }
   }
 }
@@ -277,24 +318,27 @@ __device__ __forceinline__ bool tc_issue(const AttnParams& p, TcShared& sh, cons
                                          uint32_t tmem, const int64_t (&range)[2], const AbortCtl& ctl) {
   constexpr uint32_t kIdS = tc_idesc(S::E4M3, false, S::BN), kIdO = tc_idesc(S::E4M3, true, S::D);
   Walk<S::M, S::BN> w(p, sh.work, range);
-  int64_t tile = 0;          // tiles so far, of all segments
-  uint32_t seg = 0;
-  auto x_of = [](int t, int64_t n) { return S::TILES == 2 ? t : static_cast<int>(n & 1); };
-  auto x_parity = [](int64_t n) { return static_cast<uint32_t>(S::TILES == 2 ? n & 1 : (n >> 1) & 1); };
-  auto scores = [&](int t, int64_t n) {
-    const int64_t u = 2 * n;
-    const uint32_t q = smem_u32(qbuf) + t * 128 * S::D * 2, k = smem_u32(tiles) + static_cast<uint32_t>(u % nring) * S::kTile;
+  uint32_t tile = 0, seg = 0;          // so far, of all segments
+  // buffers in order of use: K 0, V 0, K 1, V 1, ...; this tile's V, and the K whose scores come next
+  Ring k_at(nring), v_at(nring);
+  v_at.next();
+  auto x_of = [](int t, uint32_t n) { return S::TILES == 2 ? t : static_cast<int>(n & 1); };
+  auto scores = [&](int t, uint32_t n) {
+    const uint32_t q = smem_u32(qbuf) + t * 128 * S::D * 2, k = smem_u32(tiles) + k_at.i * S::kTile;
     const int x = x_of(t, n);
 #pragma unroll
     for (int i = 0; i < S::D / 16; ++i)
       tc_mma_bf16(tmem + S::kS(x), smem_desc_k128(q + (i >> 2) * 128 * 128 + (i & 3) * 32),
                   smem_desc_k128(k + (i >> 2) * S::BN * 128 + (i & 3) * 32), kIdS, i > 0);
     tc_commit(&sh.s_full[x]);
-    if (t == S::TILES - 1) tc_commit(&sh.empty[u % nring]);
+    if (t == S::TILES - 1) {
+      tc_commit(&sh.empty[k_at.i]);
+      k_at.next();
+      k_at.next();
+    }
   };
-  auto sums = [&](int t, int64_t n, bool first) {
-    const int64_t u = 2 * n + 1;
-    const uint32_t v = smem_u32(tiles) + static_cast<uint32_t>(u % nring) * S::kTile;
+  auto sums = [&](int t, uint32_t n, bool first) {
+    const uint32_t v = smem_u32(tiles) + v_at.i * S::kTile;
     const int x = x_of(t, n);
     if (!*reinterpret_cast<volatile int32_t*>(&sh.skip[x])) {
 #pragma unroll
@@ -302,27 +346,32 @@ __device__ __forceinline__ bool tc_issue(const AttnParams& p, TcShared& sh, cons
         tc_mma_ts(tmem + S::kO(t), tmem + S::kS(x) + 8 * i, smem_desc_mn128(v + i * 2048, S::BN * 128), kIdO, !(first && i == 0));
     }
     tc_commit(&sh.o_done[t]);
-    if (t == S::TILES - 1) tc_commit(&sh.empty[u % nring]);
+    if (t == S::TILES - 1) {
+      tc_commit(&sh.empty[v_at.i]);
+      v_at.next();
+      v_at.next();
+    }
   };
-  auto arrived = [&](int64_t u) { return mbar_wait(&sh.full[u % nring], static_cast<uint32_t>(u / nring) & 1, ctl); };
-  for (; w.left > 0; w.next(p), ++seg) {
-    if (!mbar_wait(&sh.q_ready, seg & 1, ctl) || !arrived(2 * tile)) return false;
+  auto arrived = [&](const Ring& at) {
+    if (!mbar_wait(&sh.full[at.i], at.phase, ctl)) return false;
     tc_fence_after();
+    return true;
+  };
+  for (; w.left > 0; w.next(p), ++seg) {
+    if (!mbar_wait(&sh.q_ready, seg & 1, ctl) || !arrived(k_at)) return false;
     for (int t = 0; t < S::TILES; ++t) scores(t, tile);
     for (int i = 0; i < w.n; ++i, ++tile) {
       const bool more = i + 1 < w.n;
       if (S::TILES == 1 && more) {
-        if (!arrived(2 * tile + 2)) return false;
-        tc_fence_after();
+        if (!arrived(k_at)) return false;
         scores(0, tile + 1);
       }
       for (int t = 0; t < S::TILES; ++t) {
-        if (!mbar_wait(&sh.p_ready[x_of(t, tile)], x_parity(tile), ctl) || !arrived(2 * tile + 1)) return false;
-        tc_fence_after();
+        const uint32_t x_parity = S::TILES == 2 ? tile & 1 : (tile >> 1) & 1;
+        if (!mbar_wait(&sh.p_ready[x_of(t, tile)], x_parity, ctl) || !arrived(v_at)) return false;
         sums(t, tile, i == 0);
         if (S::TILES == 2 && more) {
-          if (!arrived(2 * tile + 2)) return false;
-          tc_fence_after();
+          if (!arrived(k_at)) return false;
           scores(t, tile + 1);
         }
       }
@@ -396,9 +445,10 @@ __device__ __forceinline__ void tc_weigh(const AttnParams& p, TcShared& sh, uint
   const float scale2 = p.scale * 1.4426950408889634f;
   const uint32_t sign = scale2 < 0.0f ? 0x80008000u : 0u;
   const uint32_t group = p.group;
-  int64_t tile = 0;
-  uint32_t together = 0;     // uses of the group's own barrier
+  uint32_t tile = 0, together = 0;     // tiles so far; uses of the group's own barrier
+  Ring v_at(nring);                    // this tile's V
   bool ok = true;
+  v_at.next();
   auto wait = [&](uint64_t* bar, uint32_t parity) {
     ok = ok && mbar_wait(bar, parity, ctl);
     ok = __all_sync(0xffffffffu, ok);
@@ -475,19 +525,78 @@ __device__ __forceinline__ void tc_weigh(const AttnParams& p, TcShared& sh, uint
     const int64_t whole1 = min(static_cast<int64_t>(w.s.ctx), w.s.hi), whole0 = p.window > 0 ? top - p.window + 1 : 0;
 
     float m = -INFINITY, l = 0.0f;
-    for (int it = 0; it < w.n; ++it, ++tile) {
+    for (int it = 0; it < w.n; ++it, ++tile, v_at.next(), v_at.next()) {
       const int x = S::TILES == 2 ? t : static_cast<int>(tile & 1);
-      const uint32_t x_parity = static_cast<uint32_t>(S::TILES == 2 ? tile & 1 : (tile >> 1) & 1);
-      const int slot = static_cast<int>(tile % kInfo);
+      const uint32_t x_parity = S::TILES == 2 ? tile & 1 : (tile >> 1) & 1;
+      const int slot = tile % kInfo;
       const uint32_t s_addr = tmem + lanes + S::kS(x), o_addr = tmem + lanes + S::kO(t);
-      if (!wait(&sh.info[slot], static_cast<uint32_t>(tile / kInfo) & 1) || !wait(&sh.s_full[x], x_parity)) return;
+      if (!wait(&sh.info[slot], (tile / kInfo) & 1) || !wait(&sh.s_full[x], x_parity)) return;
       tc_fence_after();
       const uint32_t pages = *reinterpret_cast<volatile uint32_t*>(&sh.valid[slot]);
       const int64_t ka = static_cast<int64_t>(w.tile0 + it) * BN;
       const bool whole = ka >= whole0 && ka + BN <= whole1 && pages == all_pages;
       const float4* ks = reinterpret_cast<const float4*>(scales + slot * 2 * BN * 4);
       const float4* vs = ks + BN / 4;
-      if (live_warp) {
+      auto tile_scale = [&]() {   // the tile's largest scale of a value; a NaN counts as the largest: every row sees it and is NaN
+        const float* f = reinterpret_cast<const float*>(vs);
+        uint32_t big = 0;
+#pragma unroll
+        for (int k = 0; k < BN / 32; ++k) big = max(big, __float_as_uint(f[32 * k + lane]));
+        return __uint_as_float(__reduce_max_sync(0xffffffffu, big));
+      };
+      bool done = false;
+      if (live_warp && whole && it > 0) {
+        // One pass, the weights taken against the reference as it stands; the largest logit is looked at afterwards, and
+        // where it has passed the reference (rare past an item's first tiles) the tile is done again below.
+        const float mz = m == -INFINITY ? 0.0f : m;
+        uint32_t pk[BN / 2];
+        float sum[4] = {0.0f, 0.0f, 0.0f, 0.0f}, mx[2] = {-INFINITY, -INFINITY};
+        float v[2][32];
+        tmem_ld32_issue(s_addr, v[0]);
+#pragma unroll
+        for (int c = 0; c < BN / 32; ++c) {
+          tmem_ld32_wait(v[c & 1]);
+          if (c + 1 < BN / 32) tmem_ld32_issue(s_addr + 32 * (c + 1), v[(c + 1) & 1]);
+          float(&y)[32] = v[c & 1];
+#pragma unroll
+          for (int e = 0; e < 32; e += 4) {
+            float4 vf = make_float4(1.0f, 1.0f, 1.0f, 1.0f);
+            if constexpr (S::E4M3) {
+              const float4 kf = ks[8 * c + e / 4];
+              vf = vs[8 * c + e / 4];
+              fmul2_rn(y[e], y[e + 1], y[e], y[e + 1], kf.x, kf.y);
+              fmul2_rn(y[e + 2], y[e + 3], y[e + 2], y[e + 3], kf.z, kf.w);
+            }
+            mx[0] = fmaxf(mx[0], fmaxf(y[e], y[e + 1]));
+            mx[1] = fmaxf(mx[1], fmaxf(y[e + 2], y[e + 3]));
+            ffma2_rn(y[e], y[e + 1], y[e], y[e + 1], fac, fac, -mz, -mz);
+            ffma2_rn(y[e + 2], y[e + 3], y[e + 2], y[e + 3], fac, fac, -mz, -mz);
+#pragma unroll
+            for (int k = 0; k < 4; ++k) {
+              y[e + k] = ex2(y[e + k]);
+              sum[k] += y[e + k];
+            }
+            if constexpr (S::E4M3) {
+              fmul2_rn(y[e], y[e + 1], y[e], y[e + 1], vf.x, vf.y);
+              fmul2_rn(y[e + 2], y[e + 3], y[e + 2], y[e + 3], vf.z, vf.w);
+            }
+            pk[16 * c + e / 2] = S::E4M3 ? pack_f16x2(y[e], y[e + 1]) : pack_bf16x2_cvt(y[e], y[e + 1]);
+            pk[16 * c + e / 2 + 1] = S::E4M3 ? pack_f16x2(y[e + 2], y[e + 3]) : pack_bf16x2_cvt(y[e + 2], y[e + 3]);
+          }
+        }
+        const float big = fmaxf(mx[0], mx[1]);
+        float cover = 0.0f;
+        if constexpr (S::E4M3) cover = scale_exponent(tile_scale()) - kTop;
+        const float want = big == -INFINITY ? big : fmaf(big, fac, cover);
+        if (!__any_sync(0xffffffffu, want > m + kLag)) {
+          l += (sum[0] + sum[1]) + (sum[2] + sum[3]);
+#pragma unroll
+          for (int c = 0; c < BN / 32; ++c) tmem_st16u(s_addr + 16 * c, reinterpret_cast<const uint32_t(&)[16]>(pk[16 * c]));
+          tmem_st_wait();
+          done = true;
+        }
+      }
+      if (live_warp && !done) {
         // the row's largest logit, and what the reference has to cover
         float want = -INFINITY;
         if (whole) {
@@ -508,13 +617,7 @@ __device__ __forceinline__ void tc_weigh(const AttnParams& p, TcShared& sh, uint
             }
           }
           float e = 0.0f;
-          if constexpr (S::E4M3) {
-            const float* f = reinterpret_cast<const float*>(vs);
-            uint32_t big = 0;   // a NaN counts as the largest: every row sees it and is NaN
-#pragma unroll
-            for (int k = 0; k < BN / 32; ++k) big = max(big, __float_as_uint(f[32 * k + lane]));
-            e = scale_exponent(__uint_as_float(__reduce_max_sync(0xffffffffu, big))) - kTop;
-          }
+          if constexpr (S::E4M3) e = scale_exponent(tile_scale()) - kTop;
           want = mx == -INFINITY ? mx : fmaf(mx, fac, e);
         } else {
 #pragma unroll 1
@@ -537,7 +640,7 @@ __device__ __forceinline__ void tc_weigh(const AttnParams& p, TcShared& sh, uint
           m = mx;
           l *= keep;
           if (it > 0) {   // the sums of the item so far
-            if (!wait(&sh.o_done[t], static_cast<uint32_t>(tile - 1) & 1)) return;
+            if (!wait(&sh.o_done[t], (tile - 1) & 1)) return;
             tc_fence_after();
 #pragma unroll 1
             for (int d = 0; d < D; d += 32) {
@@ -587,9 +690,8 @@ __device__ __forceinline__ void tc_weigh(const AttnParams& p, TcShared& sh, uint
       if (!whole) {
         // Values behind the last key and in pages left out may hold anything: zeros in their place. Infinities and NaN in
         // keys that some row sees: the product is done by hand.
-        const int64_t u = 2 * tile + 1;
-        if (!wait(&sh.full[u % nring], static_cast<uint32_t>(u / nring) & 1)) return;
-        const uint32_t vb = smem_u32(tiles) + static_cast<uint32_t>(u % nring) * S::kTile;
+        if (!wait(&sh.full[v_at.i], v_at.phase)) return;
+        const uint32_t vb = smem_u32(tiles) + v_at.i * S::kTile;
         if (r == 0) sh.special[t][tile & 1] = 0;
         if (!meet()) return;
         bool special = false;
@@ -616,7 +718,7 @@ __device__ __forceinline__ void tc_weigh(const AttnParams& p, TcShared& sh, uint
         if (!meet()) return;
         const bool by_hand = *reinterpret_cast<volatile int32_t*>(&sh.special[t][tile & 1]) != 0;
         if (by_hand) {
-          if (it > 0 && !wait(&sh.o_done[t], static_cast<uint32_t>(tile - 1) & 1)) return;
+          if (it > 0 && !wait(&sh.o_done[t], (tile - 1) & 1)) return;
           tc_fence_after();
           if (live_warp) sums_by_hand<S>(p, w.s, i_row, pos, ka, pages, box_shift, s_addr, o_addr, vb, it == 0);
         }
@@ -629,7 +731,7 @@ __device__ __forceinline__ void tc_weigh(const AttnParams& p, TcShared& sh, uint
       if (lane == 0) mbar_arrive(&sh.p_ready[x]);
     }
     // the item's rows
-    if (!wait(&sh.o_done[t], static_cast<uint32_t>(tile - 1) & 1)) return;
+    if (!wait(&sh.o_done[t], (tile - 1) & 1)) return;
     tc_fence_after();
     if (live_warp) {
       const bool complete = w.n == w.len;
