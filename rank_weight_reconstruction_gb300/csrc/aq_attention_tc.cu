@@ -127,6 +127,13 @@ __device__ __forceinline__ void tmem_st16u(uint32_t addr, const uint32_t (&v)[16
       "r"(v[11]), "r"(v[12]), "r"(v[13]), "r"(v[14]), "r"(v[15])
       : "memory");
 }
+// One lane of a converged warp. The MMA warp runs its loops and waits as a whole, so that what it computes stays
+// uniform, and one lane issues.
+__device__ __forceinline__ bool elect_one() {
+  uint32_t is;
+  asm volatile("{\n\t.reg .pred p;\n\telect.sync _|p, 0xffffffff;\n\tselp.u32 %0, 1, 0, p;\n\t}" : "=r"(is));
+  return is != 0;
+}
 // D (+)= A B^T with A from tensor memory (rows the lanes, two 16-bit elements a column), B from shared memory.
 __device__ __forceinline__ void tc_mma_ts(uint32_t d, uint32_t a, uint64_t b_desc, uint32_t idesc, uint32_t accumulate) {
   asm volatile(
@@ -311,7 +318,7 @@ __device__ __forceinline__ void tc_convert(TcShared& sh, const uint8_t* codes, c
 }
 
 // ---------------------------------------------------------------------------------
-// MMA issue, one thread
+// MMA issue, one warp
 // ---------------------------------------------------------------------------------
 template <class S>
 __device__ __forceinline__ bool tc_issue(const AttnParams& p, TcShared& sh, const uint8_t* qbuf, const uint8_t* tiles, int nring,
@@ -324,41 +331,48 @@ __device__ __forceinline__ bool tc_issue(const AttnParams& p, TcShared& sh, cons
   v_at.next();
   auto x_of = [](int t, uint32_t n) { return S::TILES == 2 ? t : static_cast<int>(n & 1); };
   auto scores = [&](int t, uint32_t n) {
-    const uint32_t q = smem_u32(qbuf) + t * 128 * S::D * 2, k = smem_u32(tiles) + k_at.i * S::kTile;
     const int x = x_of(t, n);
+    if (elect_one()) {
+      const uint64_t q = smem_desc_k128(smem_u32(qbuf) + t * 128 * S::D * 2), k = smem_desc_k128(smem_u32(tiles) + k_at.i * S::kTile);
 #pragma unroll
-    for (int i = 0; i < S::D / 16; ++i)
-      tc_mma_bf16(tmem + S::kS(x), smem_desc_k128(q + (i >> 2) * 128 * 128 + (i & 3) * 32),
-                  smem_desc_k128(k + (i >> 2) * S::BN * 128 + (i & 3) * 32), kIdS, i > 0);
-    tc_commit(&sh.s_full[x]);
+      for (int i = 0; i < S::D / 16; ++i)   // descriptor addresses count 16 bytes
+        tc_mma_bf16(tmem + S::kS(x), q + (((i >> 2) * 128 * 128 + (i & 3) * 32) >> 4), k + (((i >> 2) * S::BN * 128 + (i & 3) * 32) >> 4),
+                    kIdS, i > 0);
+      tc_commit(&sh.s_full[x]);
+      if (t == S::TILES - 1) tc_commit(&sh.empty[k_at.i]);
+    }
+    __syncwarp();
     if (t == S::TILES - 1) {
-      tc_commit(&sh.empty[k_at.i]);
       k_at.next();
       k_at.next();
     }
   };
   auto sums = [&](int t, uint32_t n, bool first) {
-    const uint32_t v = smem_u32(tiles) + v_at.i * S::kTile;
     const int x = x_of(t, n);
-    if (!*reinterpret_cast<volatile int32_t*>(&sh.skip[x])) {
+    const bool skip = *reinterpret_cast<volatile int32_t*>(&sh.skip[x]) != 0;
+    if (elect_one()) {
+      if (!skip) {
+        const uint64_t v = smem_desc_mn128(smem_u32(tiles) + v_at.i * S::kTile, S::BN * 128);
 #pragma unroll
-      for (int i = 0; i < S::BN / 16; ++i)
-        tc_mma_ts(tmem + S::kO(t), tmem + S::kS(x) + 8 * i, smem_desc_mn128(v + i * 2048, S::BN * 128), kIdO, !(first && i == 0));
+        for (int i = 0; i < S::BN / 16; ++i)
+          tc_mma_ts(tmem + S::kO(t), tmem + S::kS(x) + 8 * i, v + ((i * 2048) >> 4), kIdO, !(first && i == 0));
+      }
+      tc_commit(&sh.o_done[t]);
+      if (t == S::TILES - 1) tc_commit(&sh.empty[v_at.i]);
     }
-    tc_commit(&sh.o_done[t]);
+    __syncwarp();
     if (t == S::TILES - 1) {
-      tc_commit(&sh.empty[v_at.i]);
       v_at.next();
       v_at.next();
     }
   };
   auto arrived = [&](const Ring& at) {
-    if (!mbar_wait(&sh.full[at.i], at.phase, ctl)) return false;
+    if (!__all_sync(0xffffffffu, mbar_wait(&sh.full[at.i], at.phase, ctl))) return false;
     tc_fence_after();
     return true;
   };
   for (; w.left > 0; w.next(p), ++seg) {
-    if (!mbar_wait(&sh.q_ready, seg & 1, ctl) || !arrived(k_at)) return false;
+    if (!__all_sync(0xffffffffu, mbar_wait(&sh.q_ready, seg & 1, ctl)) || !arrived(k_at)) return false;
     for (int t = 0; t < S::TILES; ++t) scores(t, tile);
     for (int i = 0; i < w.n; ++i, ++tile) {
       const bool more = i + 1 < w.n;
@@ -368,7 +382,7 @@ __device__ __forceinline__ bool tc_issue(const AttnParams& p, TcShared& sh, cons
       }
       for (int t = 0; t < S::TILES; ++t) {
         const uint32_t x_parity = S::TILES == 2 ? tile & 1 : (tile >> 1) & 1;
-        if (!mbar_wait(&sh.p_ready[x_of(t, tile)], x_parity, ctl) || !arrived(v_at)) return false;
+        if (!__all_sync(0xffffffffu, mbar_wait(&sh.p_ready[x_of(t, tile)], x_parity, ctl)) || !arrived(v_at)) return false;
         sums(t, tile, i == 0);
         if (S::TILES == 2 && more) {
           if (!arrived(k_at)) return false;
@@ -818,9 +832,11 @@ __global__ void __launch_bounds__(S::kThreads, 1) aq_tree_attention_tc_kernel(co
   } else if (warp == S::kTmaWarp) {
     tc_produce<S>(p, sh, S::E4M3 ? codes : tiles, scales, p.stages, range, ctl);
   } else if (warp == S::kMmaWarp) {
-    if ((threadIdx.x & 31) == 0 && range[1] > range[0]) {
+    if (range[1] > range[0]) {
       tc_issue<S>(p, sh, qbuf, tiles, nring, tmem, range, ctl);
-      tc_commit(&sh.drain);   // nothing is in flight when tensor memory is freed
+      // nothing is in flight when tensor memory is freed
+      __syncwarp();
+      if (elect_one()) tc_commit(&sh.drain);
       const uint64_t t0 = global_timer_ns();
       while (!mbar_try_wait(&sh.drain, 0))
         if (global_timer_ns() - t0 > p.timeout_ns) break;
