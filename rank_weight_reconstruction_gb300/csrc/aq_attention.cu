@@ -87,7 +87,7 @@ __device__ __forceinline__ uint32_t transpose8(uint32_t x) {
 }
 constexpr int kAttnStages = 6;          // most stages of the ring
 constexpr int kAttnMaxWarps = 8;        // most consumer warps
-constexpr int kAttnMaxRows = 64;        // rows of the largest tile
+constexpr int kAttnMaxRows = 32;        // rows of the largest tile
 // ---------------------------------------------------------------------------------
 // shapes: D elements a head; a warp takes 8 NR rows against CK keys at a time; NW warps are RG row groups by
 // KG key groups. Keys are the matrix instruction's 16 lanes and rows its 8 columns, in both products: S^T = K Q^T
@@ -145,8 +145,7 @@ __device__ __forceinline__ void produce(const AttnParams& p, AttnShared& sh, uin
   Walk<S::M, S::KS> w(p, sh.work, range);
   bool ok = true;
   while (ok && w.left > 0) {
-    const int b = w.entry / p.row_tiles;
-    const int32_t* table = p.table + b * p.ld_table;
+    const int32_t* table = p.table + w.b * p.ld_table;
     auto page_id = [&](int64_t i) {   // -1: left out
       if (i >= p.pages_per_seq || (i << p.page_shift) >= w.s.hi || ((i + 1) << p.page_shift) <= w.s.lo) return -1;
       const int id = table[i];
@@ -235,7 +234,7 @@ __device__ __forceinline__ void load_queries(const AttnParams& p, AttnShared& sh
   const uint32_t rows = static_cast<uint32_t>(s.T) * p.group, group = p.group;
   if (tid < S::M) {
     const uint32_t rr = static_cast<uint32_t>(rt) * S::M + tid;
-    const int i = rr < rows ? rr / group : 0;
+    const int i = rr < rows ? p.by_group.quot(rr) : 0;
     sh.i[tid] = i;
     sh.pos[tid] = static_cast<int64_t>(s.ctx) + (p.mask && p.depth ? max(p.depth[s.first + i], 0) : i);
   }
@@ -243,12 +242,9 @@ __device__ __forceinline__ void load_queries(const AttnParams& p, AttnShared& sh
 #pragma unroll
   for (int k = 0; k < kRounds; ++k) {
     const int r = (tid >> 5) * (32 / L) + lane / L + k * kStep;
-    const uint32_t rr = static_cast<uint32_t>(rt) * S::M + r;
-    v[k] = make_uint4(0, 0, 0, 0);
-    if (r < S::M && rr < rows) {
-      const uint32_t i = rr / group;
-      v[k] = *reinterpret_cast<const uint4*>(p.q + (static_cast<int64_t>(s.first) + i) * p.q_tok + (head * group + (rr - i * group)) * p.q_head + c * 8);
-    }
+    // rows past the last load the last and are zeroed on use: a load under a condition would be waited for at once
+    const uint32_t rr = min(static_cast<uint32_t>(rt) * S::M + r, rows - 1), i = p.by_group.quot(rr);
+    v[k] = *reinterpret_cast<const uint4*>(p.q + (static_cast<int64_t>(s.first) + i) * p.q_tok + (head * group + (rr - i * group)) * p.q_head + c * 8);
   }
 #pragma unroll
   for (int k = 0; k < kRounds; ++k) {
@@ -256,6 +252,7 @@ __device__ __forceinline__ void load_queries(const AttnParams& p, AttnShared& sh
     if (r >= S::M) break;                      // whole groups of L lanes
     float fac = fabsf(scale2);
     uint32_t x[4] = {v[k].x ^ sign, v[k].y ^ sign, v[k].z ^ sign, v[k].w ^ sign};
+    if (static_cast<uint32_t>(rt) * S::M + r >= rows) x[0] = x[1] = x[2] = x[3] = 0;
     if constexpr (S::E4M3) {
       uint32_t top = 0;
 #pragma unroll
@@ -554,7 +551,7 @@ __device__ __forceinline__ void consume(const AttnParams& p, AttnShared& sh, con
   float* mine = join + warp * 8 * NR * S::kJoinLd;
   bool ok = true;
   while (w.left > 0) {
-    const int rt = w.entry % p.row_tiles;
+    const int rt = w.rt;
     load_queries<S>(p, sh, qs, w.s, w.head, rt);
     named_bar_sync(1, kConsumers);
     const uint2* qw = qs + rg * 8 * NR * 4;
@@ -716,6 +713,7 @@ __global__ void __launch_bounds__(S::kThreads, S::kPerSm) aq_tree_attention_kern
   pdl_wait_prior_grid();
   int64_t range[2];
   locate<S::M, S::KS>(p, sh.work, p.prefix, blockIdx.x == 0, range);
+  pdl_launch_dependents();   // the joining blocks find their rows meanwhile; they wait for this grid before its results
   const AbortCtl ctl = {&sh.abort, p.status, p.timeout_ns};
   if (threadIdx.x >= S::NW * 32) {
     // 384 threads at 168 registers: 256 at 232 and 128 at 40
@@ -725,7 +723,6 @@ __global__ void __launch_bounds__(S::kThreads, S::kPerSm) aq_tree_attention_kern
     if (S::kSplitRegs) asm volatile("setmaxnreg.inc.sync.aligned.u32 232;");
     consume<S>(p, sh, stage0, scale0, qs, join, range, p.stages, ctl);
   }
-  pdl_launch_dependents();
 }
 
 // Adds the partial sums of the items that were shared between CTAs, in the CTAs' order. One block per row and
@@ -737,24 +734,28 @@ __global__ void __launch_bounds__(128) aq_attention_join_kernel(const __grid_con
   __shared__ float sm[4], sl[4], so[4][D];
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
   const int heads = p.hk * p.group;
-  const int row = blockIdx.x / static_cast<uint32_t>(heads), head = blockIdx.x - row * heads;
+  const int row = p.by_heads.quot(blockIdx.x), head = blockIdx.x - row * heads, kv_head = p.by_group.quot(head);
   if (tid == 0) b_of = -1;
   __syncthreads();
-  pdl_wait_prior_grid();
-  pdl_launch_dependents();
+  // Before the wait: the batch's layout is an input that was complete when the main grid, whose blocks all got past their
+  // own wait before these could start, began to read it.
   for (int b = tid; b < p.batch; b += 128) {
     const int c0 = p.cu[b], c1 = p.cu[b + 1];
     if (c0 >= 0 && c0 <= row && row < c1 && row - c0 < p.max_q) b_of = b;
   }
-  const int64_t total = p.prefix[p.batch * p.row_tiles];
   __syncthreads();
   const int b = b_of;
+  const int in_seq = b < 0 ? 0 : row - p.cu[b];
+  pdl_wait_prior_grid();
+  pdl_launch_dependents();
   if (b < 0) return;
-  const uint32_t r = static_cast<uint32_t>(row - p.cu[b]) * p.group + head % static_cast<uint32_t>(p.group);
-  const int entry = b * p.row_tiles + r / static_cast<uint32_t>(p.rows_per_tile);
-  const int rr = r % static_cast<uint32_t>(p.rows_per_tile);
+  const int64_t total = p.prefix[p.batch * p.row_tiles];
+  const uint32_t r = static_cast<uint32_t>(in_seq) * p.group + (head - kv_head * p.group);
+  const int shift = 31 - __clz(p.rows_per_tile);   // a power of two
+  const int entry = b * p.row_tiles + (r >> shift);
+  const int rr = r & (p.rows_per_tile - 1);
   const int64_t first = p.prefix[entry], len = quot(p.prefix[entry + 1] - first, p.hk);
-  const int64_t t0 = first + head / p.group * len, t1 = t0 + len;
+  const int64_t t0 = first + kv_head * len, t1 = t0 + len;
   const int64_t share = quot(total + p.main_grid - 1, p.main_grid);
   const int c0 = static_cast<int>(quot(t0, share)), c1 = static_cast<int>(quot(t1 - 1, share));
   if (c0 == c1) return;   // one CTA had it all
@@ -764,16 +765,23 @@ __global__ void __launch_bounds__(128) aq_attention_join_kernel(const __grid_con
   constexpr int kParts = 4;   // of each warp in flight at once
   for (int c = c0 + warp; c <= c1; c += 4 * kParts) {
     float2 ml[kParts];
-    float v[kParts][N];
+    __align__(8) float v[kParts][N];
 #pragma unroll
     for (int k = 0; k < kParts; ++k) {
-      const int cc = c + 4 * k;
+      const int cc = min(c + 4 * k, c1);   // past the last: the last again, left out below
       const int64_t at = (static_cast<int64_t>(cc) * 2 + (cc > c0 ? 0 : 1)) * p.rows_per_tile + rr;
-      ml[k] = cc <= c1 ? p.part_ml[at] : make_float2(-INFINITY, 0.0f);
+      ml[k] = p.part_ml[at];
       const float* src = p.part_o + at * D + lane * N;
 #pragma unroll
-      for (int e = 0; e < N; ++e) v[k][e] = cc <= c1 ? src[e] : 0.0f;
+      for (int e = 0; e < N; e += 2) *reinterpret_cast<float2*>(&v[k][e]) = *reinterpret_cast<const float2*>(src + e);
     }
+#pragma unroll
+    for (int k = 0; k < kParts; ++k)
+      if (c + 4 * k > c1) {
+        ml[k] = make_float2(-INFINITY, 0.0f);
+#pragma unroll
+        for (int e = 0; e < N; ++e) v[k][e] = 0.0f;
+      }
     float mx = m;
 #pragma unroll
     for (int k = 0; k < kParts; ++k) mx = fmaxf(mx, ml[k].x);
@@ -820,10 +828,11 @@ __global__ void __launch_bounds__(128) aq_attention_join_kernel(const __grid_con
 // ---------------------------------------------------------------------------------
 // host
 // ---------------------------------------------------------------------------------
-// Rows of a tile: the fewest of 8, 16, 32, 64 (mma.sync), 128, 256 (tcgen05; 256 sums of D = 256 do not fit tensor
-// memory) that hold a sequence's rows of one key/value head.
+// Rows of a tile: the fewest of 8, 16, 32 (mma.sync), 128, 256 (tcgen05; two tiles' sums of D = 256 do not fit tensor
+// memory) that hold a sequence's rows of one key/value head. Measured, trees of 8 and 16 on 32 query and 8 key/value heads
+// of 128 (32 and 64 rows), mma.sync against tcgen05: 32 rows bf16 139 and 180 us; 64 rows bf16 272 and 219, E4M3 256 and 217.
 int rows_per_tile(int64_t rows, int D) {
-  return rows <= 8 ? 8 : rows <= 16 ? 16 : rows <= 32 ? 32 : rows <= 64 ? 64 : rows <= 128 || D == 256 ? 128 : 256;
+  return rows <= 8 ? 8 : rows <= 16 ? 16 : rows <= 32 ? 32 : rows <= 128 || D == 256 ? 128 : 256;
 }
 
 struct AttnLayout {
@@ -881,7 +890,6 @@ aq_status launch_rows(AttnParams& p, const aq_kv_cache* c, const ServeDev& dev, 
     case 8: s = launch_attention<Shape<D, E4M3, 1, 1, 4, per1>>(p, c, dev, st, who); break;
     case 16: s = launch_attention<Shape<D, E4M3, 2, 1, 4, per2>>(p, c, dev, st, who); break;
     case 32: s = launch_attention<std::conditional_t<D == 256, Shape<D, E4M3, 2, 2, 8, 1>, Shape<D, E4M3, 4, 1, 8, 1>>>(p, c, dev, st, who); break;
-    case 64: s = launch_attention<std::conditional_t<D == 256, Shape<D, E4M3, 2, 4, 8, 1>, Shape<D, E4M3, 4, 2, 8, 1>>>(p, c, dev, st, who); break;
     default: s = launch_attention_tc(p, c, dev, st, who);
   }
   if (s != AQ_OK) return s;
@@ -1007,6 +1015,9 @@ extern "C" aq_status aq_tree_attention(const aq_kv_cache* cache, const aq_draft_
   p.scale = scale;
   uint8_t* base = static_cast<uint8_t*>(workspace);
   p.rows_per_tile = l.rows;
+  p.by_group = FastDiv(p.group);
+  p.by_tiles = FastDiv(l.row_tiles);
+  p.by_heads = FastDiv(q_heads);
   p.row_tiles = l.row_tiles;
   p.prefix = reinterpret_cast<int64_t*>(base);
   p.part_ml = reinterpret_cast<float2*>(base + l.part_ml);

@@ -8,6 +8,25 @@
 
 namespace aq {
 
+// Division of 32-bit numbers by a number known to the host (Granlund and Montgomery, 1994): a product, a subtraction and
+// two shifts, where a division by a variable takes some forty dependent instructions.
+struct FastDiv {
+  uint32_t d = 1, mul = 0;
+  int32_t s1 = 0, s2 = 0;
+  __host__ __device__ FastDiv() {}
+  __host__ explicit FastDiv(uint32_t by) : d(by) {
+    int l = 0;
+    while (l < 32 && (1ull << l) < by) ++l;
+    mul = static_cast<uint32_t>(((1ull << 32) * ((1ull << l) - by)) / by + 1);
+    s1 = l < 1 ? l : 1;
+    s2 = l > 1 ? l - 1 : 0;
+  }
+  __device__ __forceinline__ uint32_t quot(uint32_t n) const {
+    const uint32_t t = __umulhi(mul, n);
+    return (t + ((n - t) >> s1)) >> s2;
+  }
+};
+
 struct AttnParams {
   CUtensorMap tm_k, tm_v;
   const float* ks;
@@ -30,6 +49,7 @@ struct AttnParams {
   int64_t total_q;
   float scale;
   int32_t rows_per_tile, row_tiles;   // rows of a tile, tiles of a sequence
+  FastDiv by_group, by_tiles, by_heads;   // query heads a key/value head; row_tiles; query heads
   int32_t main_grid, stages;
   int64_t* prefix;                    // [batch * row_tiles + 1] first tile of each entry
   float2* part_ml;                    // [CTA][2][rows of a tile] maximum (base 2) and sum of a partial item
@@ -90,17 +110,18 @@ __device__ __forceinline__ int top_exponent(float x) { return min(max(static_cas
 // ... of a value's scale, for the reference.
 __device__ __forceinline__ float scale_exponent(float x) { return static_cast<float>(max(static_cast<int>(__float_as_uint(x) >> 23) - 127, kLeast)); }
 
-// Where a CTA begins: entry, tile within it; the warps' parts of the tile count.
-struct AttnWork {
-  int64_t start_entry, start_tile;
-  int64_t part[16];
-};
-
 // Keys [lo, hi) and tiles [t0, t1) that the rows of entry (sequence b, row tile rt) can see.
 struct KeySpan {
   int64_t lo, hi;
   int32_t t0, t1;
   int32_t first, T, ctx;    // first row in q, rows, context
+};
+
+// Where a CTA begins: entry, head and tile of the item; the warps' parts of the tile count.
+struct AttnWork {
+  KeySpan span;
+  int32_t entry, head, offset, len;
+  int64_t part[16];
 };
 
 template <int M, int KS>
@@ -114,7 +135,7 @@ __device__ __forceinline__ KeySpan entry_span(const AttnParams& p, int b, int rt
   s.t0 = s.t1 = 0;
   s.lo = s.hi = 0;
   if (r0 >= rows) return s;
-  const int i0 = r0 / static_cast<uint32_t>(p.group), i1 = (min(r0 + M, rows) - 1) / static_cast<uint32_t>(p.group);
+  const int i0 = p.by_group.quot(r0), i1 = p.by_group.quot(min(r0 + M, rows) - 1);
   s.hi = min(static_cast<int64_t>(s.ctx) + (p.mask ? s.T : i1 + 1), static_cast<int64_t>(p.pages_per_seq) << p.page_shift);
   if (p.window > 0) s.lo = max(static_cast<int64_t>(s.ctx) + (p.mask ? 0 : i0) - p.window + 1, static_cast<int64_t>(0));
   s.lo = min(s.lo, s.hi);
@@ -133,8 +154,10 @@ __device__ __forceinline__ void locate(const AttnParams& p, AttnWork& sh, int64_
   const int per = (n + threads - 1) / threads;
   const int e0 = min(tid * per, n), e1 = min(e0 + per, n);
   int64_t sum = 0;
+  KeySpan s = {};
   for (int e = e0; e < e1; ++e) {
-    const KeySpan s = entry_span<M, KS>(p, e / p.row_tiles, e % p.row_tiles);
+    const int b = p.by_tiles.quot(e);
+    s = entry_span<M, KS>(p, b, e - b * p.row_tiles);
     sum += static_cast<int64_t>(s.t1 - s.t0) * p.hk;
   }
   int64_t upto = sum;   // within the warp, this thread's own among them
@@ -156,11 +179,18 @@ __device__ __forceinline__ void locate(const AttnParams& p, AttnWork& sh, int64_
   if (write || (range[0] >= before && range[0] < before + sum)) {
     int64_t at = before;
     for (int e = e0; e < e1; ++e) {
-      const KeySpan s = entry_span<M, KS>(p, e / p.row_tiles, e % p.row_tiles);
+      if (e1 - e0 > 1) {     // a thread's one entry is known already
+        const int b = p.by_tiles.quot(e);
+        s = entry_span<M, KS>(p, b, e - b * p.row_tiles);
+      }
       const int64_t len = static_cast<int64_t>(s.t1 - s.t0) * p.hk;
       if (range[0] >= at && range[0] < at + len) {
-        sh.start_entry = e;
-        sh.start_tile = range[0] - at;
+        const int64_t in = range[0] - at;
+        sh.span = s;
+        sh.entry = e;
+        sh.len = s.t1 - s.t0;
+        sh.head = static_cast<int>(quot(in, sh.len));
+        sh.offset = static_cast<int>(in - static_cast<int64_t>(sh.head) * sh.len);
       }
       if (write) prefix[e] = at;
       at += len;
@@ -175,7 +205,8 @@ __device__ __forceinline__ void locate(const AttnParams& p, AttnWork& sh, int64_
 template <int M, int KS>
 struct Walk {
   int64_t left;          // tiles of the CTA's range still to come
-  int entry, head;
+  int entry, head;       // entry: sequence b, row tile rt
+  int b, rt;
   int tile0, n;          // this segment: first tile (within the sequence) and how many
   int len;               // tiles of the whole item
   int offset;            // of them before this segment
@@ -183,12 +214,17 @@ struct Walk {
   __device__ __forceinline__ Walk(const AttnParams& p, const AttnWork& sh, const int64_t (&range)[2]) {
     left = range[1] - range[0];
     if (left <= 0) return;
-    entry = static_cast<int>(sh.start_entry);
-    s = entry_span<M, KS>(p, entry / p.row_tiles, entry % p.row_tiles);
-    len = s.t1 - s.t0;
-    head = static_cast<int>(quot(sh.start_tile, len));
-    offset = static_cast<int>(sh.start_tile - static_cast<int64_t>(head) * len);
+    entry = sh.entry;
+    head = sh.head;
+    offset = sh.offset;
+    len = sh.len;
+    s = sh.span;
+    place(p);
     cut();
+  }
+  __device__ __forceinline__ void place(const AttnParams& p) {
+    b = p.by_tiles.quot(entry);
+    rt = entry - b * p.row_tiles;
   }
   __device__ __forceinline__ void cut() {
     tile0 = s.t0 + offset;
@@ -202,7 +238,8 @@ struct Walk {
       head = 0;
       do {
         ++entry;
-        s = entry_span<M, KS>(p, entry / p.row_tiles, entry % p.row_tiles);
+        place(p);
+        s = entry_span<M, KS>(p, b, rt);
         len = s.t1 - s.t0;
       } while (len == 0);
     }

@@ -198,7 +198,7 @@ __device__ __forceinline__ void tc_produce(const AttnParams& p, TcShared& sh, ui
   Walk<S::M, S::BN> w(p, sh.work, range);
   bool ok = true;
   while (ok && w.left > 0) {
-    const int32_t* table = p.table + static_cast<int64_t>(w.entry / p.row_tiles) * p.ld_table;
+    const int32_t* table = p.table + w.b * p.ld_table;
     auto page_id = [&](int64_t i) {   // -1: left out
       if (i >= p.pages_per_seq || (i << p.page_shift) >= w.s.hi || ((i + 1) << p.page_shift) <= w.s.lo) return -1;
       const int id = table[i];
@@ -475,33 +475,31 @@ __device__ __forceinline__ void tc_weigh(const AttnParams& p, TcShared& sh, uint
   };
   Walk<S::M, BN> w(p, sh.work, range);
   for (; w.left > 0; w.next(p)) {
-    const int rt = w.entry % p.row_tiles;
+    const int rt = w.rt;
     const uint32_t rows = static_cast<uint32_t>(w.s.T) * group, row0 = static_cast<uint32_t>(rt) * S::M + t * 128;
     const uint32_t row = row0 + r;
     const bool live_warp = row0 + wq * 32 < rows;
-    const int i_row = row < rows ? row / group : 0;
-    const int64_t pos = static_cast<int64_t>(w.s.ctx) + (p.mask && p.depth ? max(p.depth[w.s.first + i_row], 0) : i_row);
+    const int i_row = row < rows ? p.by_group.quot(row) : 0;
+    const int depth = p.mask && p.depth ? max(p.depth[w.s.first + i_row], 0) : i_row;   // used behind the queries' loads
     // queries of the warp's 32 rows, as the MMA reads them
     constexpr int L = D / 8, RPW = 32 / L;       // lanes a row, rows at once
     const int c = lane % L;
-    constexpr int kBatch = 8;
+    constexpr int kBatch = 32 / RPW < 16 ? 32 / RPW : 16;   // loads in flight
 #pragma unroll 1
     for (int k0 = 0; k0 < 32 / RPW; k0 += kBatch) {
       uint4 v[kBatch];
 #pragma unroll
       for (int k = 0; k < kBatch; ++k) {
-        const uint32_t rr = row0 + wq * 32 + (k0 + k) * RPW + lane / L;
-        v[k] = make_uint4(0, 0, 0, 0);
-        if (rr < rows) {
-          const uint32_t i = rr / group;
-          v[k] = *reinterpret_cast<const uint4*>(p.q + (static_cast<int64_t>(w.s.first) + i) * p.q_tok + (w.head * group + (rr - i * group)) * p.q_head + c * 8);
-        }
+        // rows past the last load the last and are zeroed on use: a load under a condition would be waited for at once
+        const uint32_t rr = min(row0 + wq * 32 + (k0 + k) * RPW + lane / L, rows - 1), i = p.by_group.quot(rr);
+        v[k] = *reinterpret_cast<const uint4*>(p.q + (static_cast<int64_t>(w.s.first) + i) * p.q_tok + (w.head * group + (rr - i * group)) * p.q_head + c * 8);
       }
 #pragma unroll
       for (int k = 0; k < kBatch; ++k) {
         const int lr = wq * 32 + (k0 + k) * RPW + lane / L;   // row within the tile
         float fac = fabsf(scale2);
         uint32_t x[4] = {v[k].x ^ sign, v[k].y ^ sign, v[k].z ^ sign, v[k].w ^ sign};
+        if (row0 + lr >= rows) x[0] = x[1] = x[2] = x[3] = 0;
         if constexpr (S::E4M3) {
           uint32_t top = 0;
 #pragma unroll
@@ -523,6 +521,7 @@ __device__ __forceinline__ void tc_weigh(const AttnParams& p, TcShared& sh, uint
                      : "memory");
       }
     }
+    const int64_t pos = static_cast<int64_t>(w.s.ctx) + depth;
     int64_t top = pos;
 #pragma unroll
     for (int off = 16; off > 0; off >>= 1) top = max(top, __shfl_xor_sync(0xffffffffu, top, off));
@@ -751,29 +750,45 @@ __device__ __forceinline__ void tc_weigh(const AttnParams& p, TcShared& sh, uint
       const bool complete = w.n == w.len;
       const int slot = w.offset > 0 ? 0 : 1;   // partial sums: an item begun elsewhere, or one that goes on elsewhere
       const bool none = m == -INFINITY && l == 0.0f;
-      const float inv = complete ? (none ? 0.0f : 1.0f / l) : 1.0f;
+      const float inv = complete ? 1.0f / l : 1.0f;
       const int head = w.head * group + static_cast<int>(row - static_cast<uint32_t>(i_row) * group);
       const int64_t out_row = static_cast<int64_t>(w.s.first) + i_row;
       const int64_t at = (static_cast<int64_t>(blockIdx.x) * 2 + slot) * S::M + t * 128 + r;
+      // 32 columns at a time through the warp's own rows of the query buffer (their last product is done), so that the
+      // stores leave in whole lines: row-wise in, swizzled by 16 bytes, four rows of eight chunks out
+      const uint32_t stage = smem_u32(qbuf) + (t * 128 + wq * 32) * D * 2;
+      const uint32_t first_row = row0 + wq * 32;
 #pragma unroll 1
       for (int d = 0; d < D; d += 32) {
         float v[32];
         tmem_ld32(tmem + lanes + S::kO(t) + d, v);
-        if (row >= rows) continue;
-        if (complete) {
-          uint4* dst = reinterpret_cast<uint4*>(p.o + out_row * p.o_tok + head * p.o_head + d);
 #pragma unroll
-          for (int q = 0; q < 4; ++q) {
-            const float* f = v + 8 * q;
-            dst[q] = none ? make_uint4(0, 0, 0, 0)
-                          : make_uint4(pack_bf16x2_cvt(f[0] * inv, f[1] * inv), pack_bf16x2_cvt(f[2] * inv, f[3] * inv),
-                                       pack_bf16x2_cvt(f[4] * inv, f[5] * inv), pack_bf16x2_cvt(f[6] * inv, f[7] * inv));
+        for (int q = 0; q < 8; ++q)
+          asm volatile("st.shared.v4.f32 [%0], {%1, %2, %3, %4};" ::"r"(stage + lane * 128 + ((q ^ (lane & 7)) << 4)),
+                       "f"(none ? 0.0f : v[4 * q] * inv), "f"(none ? 0.0f : v[4 * q + 1] * inv), "f"(none ? 0.0f : v[4 * q + 2] * inv),
+                       "f"(none ? 0.0f : v[4 * q + 3] * inv)
+                       : "memory");
+        __syncwarp();
+#pragma unroll
+        for (int k = 0; k < 8; ++k) {
+          const int lr = 4 * k + (lane >> 3), q = lane & 7;
+          float4 f;
+          asm volatile("ld.shared.v4.f32 {%0, %1, %2, %3}, [%4];"
+                       : "=f"(f.x), "=f"(f.y), "=f"(f.z), "=f"(f.w)
+                       : "r"(stage + lr * 128 + ((q ^ (lr & 7)) << 4))
+                       : "memory");
+          const uint32_t rr = first_row + lr;
+          if (rr >= rows) continue;
+          if (complete) {
+            const uint32_t i = p.by_group.quot(rr);
+            uint16_t* dst = p.o + (static_cast<int64_t>(w.s.first) + i) * p.o_tok + (w.head * group + (rr - i * group)) * p.o_head + d + 4 * q;
+            *reinterpret_cast<uint2*>(dst) = make_uint2(pack_bf16x2_cvt(f.x, f.y), pack_bf16x2_cvt(f.z, f.w));
+          } else {
+            *reinterpret_cast<float4*>(p.part_o + (static_cast<int64_t>(blockIdx.x) * 2 + slot) * S::M * D +
+                                       static_cast<int64_t>(t * 128 + wq * 32 + lr) * D + d + 4 * q) = f;
           }
-        } else {
-          float4* dst = reinterpret_cast<float4*>(p.part_o + at * D + d);
-#pragma unroll
-          for (int q = 0; q < 8; ++q) dst[q] = make_float4(v[4 * q], v[4 * q + 1], v[4 * q + 2], v[4 * q + 3]);
         }
+        __syncwarp();
       }
       if (row < rows) {
         if (!complete) p.part_ml[at] = make_float2(m, l);
@@ -826,6 +841,7 @@ __global__ void __launch_bounds__(S::kThreads, 1) aq_tree_attention_tc_kernel(co
   pdl_wait_prior_grid();
   int64_t range[2];
   locate<S::M, S::BN>(p, sh.work, p.prefix, blockIdx.x == 0, range);
+  pdl_launch_dependents();   // the joining blocks find their rows meanwhile; they wait for this grid before its results
   const AbortCtl ctl = {&sh.abort, p.status, p.timeout_ns};
   if (warp < S::kSoftWarps) {
     tc_weigh<S>(p, sh, qbuf, tiles, scales, nring, tmem, range, ctl);
@@ -851,7 +867,6 @@ __global__ void __launch_bounds__(S::kThreads, 1) aq_tree_attention_tc_kernel(co
     tc_fence_after();
     tmem_dealloc(tmem, 512);
   }
-  pdl_launch_dependents();
 }
 
 template <class S>

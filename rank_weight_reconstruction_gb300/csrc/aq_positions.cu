@@ -259,7 +259,7 @@ __global__ void __launch_bounds__(256, 4) aq_positions_kernel(const __grid_const
 
   // groups of one warp may be at different kinds of heads, so each shuffles by itself
   const uint32_t group = (GW == 32 ? 0xffffffffu : (1u << GW) - 1) << ((threadIdx.x & 31) & ~(GW - 1));
-  const uint4 zero = make_uint4(0, 0, 0, 0);
+  const int k0 = live ? ch.c0 : 0, k1 = live ? ch.c1 : 0;
   auto source = [&](int h) {
     if (h < p.hq) return p.q + tt * p.q_tok + h * p.q_head;
     if (h < p.hq + p.hk) return p.k + tt * p.k_tok + (h - p.hq) * p.k_head;
@@ -275,8 +275,8 @@ __global__ void __launch_bounds__(256, 4) aq_positions_kernel(const __grid_const
       return;
     }
     float a[8], b[8];
-    unpack8(r0, a);
-    unpack8(r1, b);
+    unpack8(live ? r0 : make_uint4(0, 0, 0, 0), a);
+    unpack8(live ? r1 : make_uint4(0, 0, 0, 0), b);
     if (turns) rotate16<HALF>(a, b, c, s);
     if (h < p.hq) {
       uint16_t* dst = p.qo + tt * p.qo_tok + h * p.qo_head;
@@ -320,8 +320,8 @@ __global__ void __launch_bounds__(256, 4) aq_positions_kernel(const __grid_const
     const bool two = h + hl < heads;
     const uint16_t* s0 = source(h);
     const uint16_t* s1 = source(two ? h + hl : h);
-    const uint4 r0 = live ? ld_stream(s0 + ch.c0 * 8) : zero, r1 = live ? ld_stream(s0 + ch.c1 * 8) : zero;
-    const uint4 r2 = live && two ? ld_stream(s1 + ch.c0 * 8) : zero, r3 = live && two ? ld_stream(s1 + ch.c1 * 8) : zero;
+    // lanes without work load lane 0's chunks: a load under a condition would be waited for at once
+    const uint4 r0 = ld_stream(s0 + k0 * 8), r1 = ld_stream(s0 + k1 * 8), r2 = ld_stream(s1 + k0 * 8), r3 = ld_stream(s1 + k1 * 8);
     finish(h, r0, r1);
     if (two) finish(h + hl, r2, r3);
   }
