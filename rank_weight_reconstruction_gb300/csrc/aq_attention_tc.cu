@@ -476,30 +476,31 @@ __device__ __forceinline__ void tc_weigh(const AttnParams& p, TcShared& sh, uint
   Walk<S::M, BN> w(p, sh.work, range);
   for (; w.left > 0; w.next(p)) {
     const int rt = w.rt;
-    const uint32_t rows = static_cast<uint32_t>(w.s.T) * group, row0 = static_cast<uint32_t>(rt) * S::M + t * 128;
-    const uint32_t row = row0 + r;
-    const bool live_warp = row0 + wq * 32 < rows;
+    // Lane l of warp wq holds row 4 l + wq of the tile: a tile that is not full is spread over all four warps.
+    const uint32_t rows = static_cast<uint32_t>(w.s.T) * group, row0 = static_cast<uint32_t>(rt) * S::M + t * 128 + wq;
+    const uint32_t row = row0 + 4 * lane;
+    const int count = rows > row0 ? min((rows - row0 + 3) / 4, 32u) : 0;   // rows of the warp
+    const bool live_warp = count > 0;
     const int i_row = row < rows ? p.by_group.quot(row) : 0;
     const int depth = p.mask && p.depth ? max(p.depth[w.s.first + i_row], 0) : i_row;   // used behind the queries' loads
-    // queries of the warp's 32 rows, as the MMA reads them
+    // queries of the warp's rows, as the MMA reads them; what lies in lanes without a row reaches no other
     constexpr int L = D / 8, RPW = 32 / L;       // lanes a row, rows at once
     const int c = lane % L;
     constexpr int kBatch = 32 / RPW < 16 ? 32 / RPW : 16;   // loads in flight
 #pragma unroll 1
-    for (int k0 = 0; k0 < 32 / RPW; k0 += kBatch) {
+    for (int k0 = 0; k0 * RPW < count; k0 += kBatch) {
       uint4 v[kBatch];
 #pragma unroll
       for (int k = 0; k < kBatch; ++k) {
-        // rows past the last load the last and are zeroed on use: a load under a condition would be waited for at once
-        const uint32_t rr = min(row0 + wq * 32 + (k0 + k) * RPW + lane / L, rows - 1), i = p.by_group.quot(rr);
+        // rows past the last load the last: a load under a condition would be waited for at once
+        const uint32_t rr = min(row0 + 4 * ((k0 + k) * RPW + lane / L), rows - 1), i = p.by_group.quot(rr);
         v[k] = *reinterpret_cast<const uint4*>(p.q + (static_cast<int64_t>(w.s.first) + i) * p.q_tok + (w.head * group + (rr - i * group)) * p.q_head + c * 8);
       }
 #pragma unroll
       for (int k = 0; k < kBatch; ++k) {
-        const int lr = wq * 32 + (k0 + k) * RPW + lane / L;   // row within the tile
+        const int lr = wq * 32 + (k0 + k) * RPW + lane / L;   // lane of the tensor memory
         float fac = fabsf(scale2);
         uint32_t x[4] = {v[k].x ^ sign, v[k].y ^ sign, v[k].z ^ sign, v[k].w ^ sign};
-        if (row0 + lr >= rows) x[0] = x[1] = x[2] = x[3] = 0;
         if constexpr (S::E4M3) {
           uint32_t top = 0;
 #pragma unroll
@@ -753,44 +754,39 @@ __device__ __forceinline__ void tc_weigh(const AttnParams& p, TcShared& sh, uint
       const float inv = complete ? 1.0f / l : 1.0f;
       const int head = w.head * group + static_cast<int>(row - static_cast<uint32_t>(i_row) * group);
       const int64_t out_row = static_cast<int64_t>(w.s.first) + i_row;
-      const int64_t at = (static_cast<int64_t>(blockIdx.x) * 2 + slot) * S::M + t * 128 + r;
+      const int64_t at = (static_cast<int64_t>(blockIdx.x) * 2 + slot) * S::M + t * 128 + 4 * lane + wq;
       // 32 columns at a time through the warp's own rows of the query buffer (their last product is done), so that the
       // stores leave in whole lines: row-wise in, swizzled by 16 bytes, four rows of eight chunks out
       const uint32_t stage = smem_u32(qbuf) + (t * 128 + wq * 32) * D * 2;
-      const uint32_t first_row = row0 + wq * 32;
+      // where this lane's chunk of a row goes: the row's own place, kept by its lane
+      int64_t place = complete ? out_row * p.o_tok + head * p.o_head : at * D;
+      const int q = lane & 7;
 #pragma unroll 1
       for (int d = 0; d < D; d += 32) {
         float v[32];
         tmem_ld32(tmem + lanes + S::kO(t) + d, v);
 #pragma unroll
-        for (int q = 0; q < 8; ++q)
-          asm volatile("st.shared.v4.f32 [%0], {%1, %2, %3, %4};" ::"r"(stage + lane * 128 + ((q ^ (lane & 7)) << 4)),
-                       "f"(none ? 0.0f : v[4 * q] * inv), "f"(none ? 0.0f : v[4 * q + 1] * inv), "f"(none ? 0.0f : v[4 * q + 2] * inv),
-                       "f"(none ? 0.0f : v[4 * q + 3] * inv)
+        for (int k = 0; k < 8; ++k)
+          asm volatile("st.shared.v4.f32 [%0], {%1, %2, %3, %4};" ::"r"(stage + lane * 128 + ((k ^ (lane & 7)) << 4)),
+                       "f"(none ? 0.0f : v[4 * k] * inv), "f"(none ? 0.0f : v[4 * k + 1] * inv), "f"(none ? 0.0f : v[4 * k + 2] * inv),
+                       "f"(none ? 0.0f : v[4 * k + 3] * inv)
                        : "memory");
         __syncwarp();
-#pragma unroll
-        for (int k = 0; k < 8; ++k) {
-          const int lr = 4 * k + (lane >> 3), q = lane & 7;
+        for (int k = 0; k < (count + 3) / 4; ++k) {
+          const int lr = 4 * k + (lane >> 3);
+          const int64_t to = __shfl_sync(0xffffffffu, place, lr) + d + 4 * q;
           float4 f;
           asm volatile("ld.shared.v4.f32 {%0, %1, %2, %3}, [%4];"
                        : "=f"(f.x), "=f"(f.y), "=f"(f.z), "=f"(f.w)
                        : "r"(stage + lr * 128 + ((q ^ (lr & 7)) << 4))
                        : "memory");
-          const uint32_t rr = first_row + lr;
-          if (rr >= rows) continue;
-          if (complete) {
-            const uint32_t i = p.by_group.quot(rr);
-            uint16_t* dst = p.o + (static_cast<int64_t>(w.s.first) + i) * p.o_tok + (w.head * group + (rr - i * group)) * p.o_head + d + 4 * q;
-            *reinterpret_cast<uint2*>(dst) = make_uint2(pack_bf16x2_cvt(f.x, f.y), pack_bf16x2_cvt(f.z, f.w));
-          } else {
-            *reinterpret_cast<float4*>(p.part_o + (static_cast<int64_t>(blockIdx.x) * 2 + slot) * S::M * D +
-                                       static_cast<int64_t>(t * 128 + wq * 32 + lr) * D + d + 4 * q) = f;
-          }
+          if (lr >= count) continue;
+          if (complete) *reinterpret_cast<uint2*>(p.o + to) = make_uint2(pack_bf16x2_cvt(f.x, f.y), pack_bf16x2_cvt(f.z, f.w));
+          else *reinterpret_cast<float4*>(p.part_o + to) = f;
         }
         __syncwarp();
       }
-      if (row < rows) {
+      if (lane < count) {
         if (!complete) p.part_ml[at] = make_float2(m, l);
         else if (p.lse) p.lse[out_row * (p.hk * p.group) + head] = none ? -INFINITY : ((m == -INFINITY ? 0.0f : m) + log2f(l)) * 0.6931471805599453f;
       }
