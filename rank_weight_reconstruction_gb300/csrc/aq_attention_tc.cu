@@ -47,7 +47,8 @@ struct TcShape {
   static constexpr int kS(int x) { return x * 128; }
   static constexpr int kO(int t) { return 256 + t * D; }
   static_assert(256 + TILES * D <= 512, "tensor memory");
-  static constexpr int NF = E4M3 ? 3 : 0;                  // f16 buffers of an E4M3 cache
+  // f16 buffers of an E4M3 cache: a fourth lets the next keys be widened under this tile's sums
+  static constexpr int NF = !E4M3 ? 0 : kQ + 4 * kTile + 3 * kCode + kScale <= 224 * 1024 ? 4 : 3;
 };
 
 struct TcShared {
@@ -496,20 +497,28 @@ __device__ __forceinline__ void tc_weigh(const AttnParams& p, TcShared& sh, uint
         const uint32_t rr = min(row0 + 4 * ((k0 + k) * RPW + lane / L), rows - 1), i = p.by_group.quot(rr);
         v[k] = *reinterpret_cast<const uint4*>(p.q + (static_cast<int64_t>(w.s.first) + i) * p.q_tok + (w.head * group + (rr - i * group)) * p.q_head + c * 8);
       }
+      uint32_t top_bits[kBatch];
+      if constexpr (S::E4M3) {
+        const uint32_t who = (L == 32 ? 0xffffffffu : (1u << L) - 1) << (lane & ~(L - 1));
+#pragma unroll
+        for (int k = 0; k < kBatch; ++k) {
+          const uint32_t m16 = 0x7fff0000u;
+          top_bits[k] = max(max(max((v[k].x << 16) & m16, v[k].x & m16), max((v[k].y << 16) & m16, v[k].y & m16)),
+                            max(max((v[k].z << 16) & m16, v[k].z & m16), max((v[k].w << 16) & m16, v[k].w & m16)));
+        }
+#pragma unroll
+        for (int off = L / 2; off > 0; off >>= 1)
+#pragma unroll
+          for (int k = 0; k < kBatch; ++k) top_bits[k] = max(top_bits[k], __shfl_xor_sync(who, top_bits[k], off));
+      }
 #pragma unroll
       for (int k = 0; k < kBatch; ++k) {
         const int lr = wq * 32 + (k0 + k) * RPW + lane / L;   // lane of the tensor memory
         float fac = fabsf(scale2);
         uint32_t x[4] = {v[k].x ^ sign, v[k].y ^ sign, v[k].z ^ sign, v[k].w ^ sign};
         if constexpr (S::E4M3) {
-          uint32_t top = 0;
-#pragma unroll
-          for (int e = 0; e < 4; ++e) top = max(top, max((x[e] << 16) & 0x7fff0000u, x[e] & 0x7fff0000u));
-          const uint32_t who = (L == 32 ? 0xffffffffu : (1u << L) - 1) << (lane & ~(L - 1));
-#pragma unroll
-          for (int off = L / 2; off > 0; off >>= 1) top = max(top, __shfl_xor_sync(who, top, off));
-          const bool finite = top < 0x7f800000u;
-          const int e = finite ? top_exponent(__uint_as_float(top)) : 0;
+          const bool finite = top_bits[k] < 0x7f800000u;
+          const int e = finite ? top_exponent(__uint_as_float(top_bits[k])) : 0;
           const float f = pow2(14 - e);
           fac = finite ? pow2(e - 14) * fac : __uint_as_float(0x7fc00000u);   // no finite score
 #pragma unroll
@@ -772,17 +781,22 @@ __device__ __forceinline__ void tc_weigh(const AttnParams& p, TcShared& sh, uint
                        "f"(none ? 0.0f : v[4 * k + 3] * inv)
                        : "memory");
         __syncwarp();
-        for (int k = 0; k < (count + 3) / 4; ++k) {
+        float4 f[8];
+        int64_t to[8];
+#pragma unroll
+        for (int k = 0; k < 8; ++k) {
           const int lr = 4 * k + (lane >> 3);
-          const int64_t to = __shfl_sync(0xffffffffu, place, lr) + d + 4 * q;
-          float4 f;
+          to[k] = __shfl_sync(0xffffffffu, place, lr) + d + 4 * q;
           asm volatile("ld.shared.v4.f32 {%0, %1, %2, %3}, [%4];"
-                       : "=f"(f.x), "=f"(f.y), "=f"(f.z), "=f"(f.w)
+                       : "=f"(f[k].x), "=f"(f[k].y), "=f"(f[k].z), "=f"(f[k].w)
                        : "r"(stage + lr * 128 + ((q ^ (lr & 7)) << 4))
                        : "memory");
-          if (lr >= count) continue;
-          if (complete) *reinterpret_cast<uint2*>(p.o + to) = make_uint2(pack_bf16x2_cvt(f.x, f.y), pack_bf16x2_cvt(f.z, f.w));
-          else *reinterpret_cast<float4*>(p.part_o + to) = f;
+        }
+#pragma unroll
+        for (int k = 0; k < 8; ++k) {
+          if (4 * k + (lane >> 3) >= count) continue;
+          if (complete) *reinterpret_cast<uint2*>(p.o + to[k]) = make_uint2(pack_bf16x2_cvt(f[k].x, f[k].y), pack_bf16x2_cvt(f[k].z, f[k].w));
+          else *reinterpret_cast<float4*>(p.part_o + to[k]) = f[k];
         }
         __syncwarp();
       }
