@@ -712,7 +712,7 @@ __global__ void __launch_bounds__(S::kThreads, S::kPerSm) aq_tree_attention_kern
   }
   pdl_wait_prior_grid();
   int64_t range[2];
-  locate<S::M, S::KS>(p, sh.work, p.prefix, blockIdx.x == 0, range);
+  locate<S::M, S::KS>(p, sh.work, blockIdx.x == 0, range);
   pdl_launch_dependents();   // the joining blocks find their rows meanwhile; they wait for this grid before its results
   const AbortCtl ctl = {&sh.abort, p.status, p.timeout_ns};
   if (threadIdx.x >= S::NW * 32) {
@@ -749,15 +749,12 @@ __global__ void __launch_bounds__(128) aq_attention_join_kernel(const __grid_con
   pdl_wait_prior_grid();
   pdl_launch_dependents();
   if (b < 0) return;
-  const int64_t total = p.prefix[p.batch * p.row_tiles];
   const uint32_t r = static_cast<uint32_t>(in_seq) * p.group + (head - kv_head * p.group);
   const int shift = 31 - __clz(p.rows_per_tile);   // a power of two
-  const int entry = b * p.row_tiles + (r >> shift);
+  const AttnShare own = p.shares[b * p.row_tiles + (r >> shift)];
   const int rr = r & (p.rows_per_tile - 1);
-  const int64_t first = p.prefix[entry], len = quot(p.prefix[entry + 1] - first, p.hk);
-  const int64_t t0 = first + kv_head * len, t1 = t0 + len;
-  const int64_t share = quot(total + p.main_grid - 1, p.main_grid);
-  const int c0 = static_cast<int>(quot(t0, share)), c1 = static_cast<int>(quot(t1 - 1, share));
+  const int64_t t0 = own.first + static_cast<int64_t>(kv_head) * own.step;
+  const int c0 = own.base + static_cast<int>(quot(t0, own.share)), c1 = own.base + static_cast<int>(quot(t0 + own.len - 1, own.share));
   if (c0 == c1) return;   // one CTA had it all
   float m = -INFINITY, l = 0.0f, o[N];
 #pragma unroll
@@ -837,9 +834,9 @@ int rows_per_tile(int64_t rows, int D) {
 
 struct AttnLayout {
   int rows = 0, row_tiles = 0;
-  size_t part_o = 0, part_ml = 0, total = 0;   // prefix at 0
+  size_t part_o = 0, part_ml = 0, total = 0;   // shares at 0
 };
-// Entries (sequences x row tiles) beyond this are refused: the prefix is scanned by every CTA.
+// Entries (sequences x row tiles) beyond this are refused: every CTA looks through them.
 constexpr int64_t kAttnMaxEntries = 1 << 22;
 
 bool attn_layout(const aq_kv_cache* c, const aq_draft_batch* d, int32_t q_heads, AttnLayout* out) {
@@ -851,7 +848,7 @@ bool attn_layout(const aq_kv_cache* c, const aq_draft_batch* d, int32_t q_heads,
   l.row_tiles = static_cast<int>(tiles);
   const int64_t ctas = kAttnSmsBound * (l.rows >= 128 ? 1 : kAttnMaxPerSm);
   auto up = [](size_t v) { return (v + 255) / 256 * 256; };
-  l.part_ml = up((tiles * d->batch + 1) * 8);
+  l.part_ml = up(tiles * d->batch * sizeof(AttnShare));
   l.part_o = up(l.part_ml + ctas * 2 * l.rows * 8);
   l.total = up(l.part_o + static_cast<size_t>(ctas) * 2 * l.rows * c->head_dim * 4);
   *out = l;
@@ -1019,7 +1016,7 @@ extern "C" aq_status aq_tree_attention(const aq_kv_cache* cache, const aq_draft_
   p.by_tiles = FastDiv(l.row_tiles);
   p.by_heads = FastDiv(q_heads);
   p.row_tiles = l.row_tiles;
-  p.prefix = reinterpret_cast<int64_t*>(base);
+  p.shares = reinterpret_cast<AttnShare*>(base);
   p.part_ml = reinterpret_cast<float2*>(base + l.part_ml);
   p.part_o = reinterpret_cast<float*>(base + l.part_o);
   p.status = dev.status;

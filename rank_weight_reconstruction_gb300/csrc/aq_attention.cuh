@@ -27,6 +27,13 @@ struct FastDiv {
   }
 };
 
+// How an entry (a sequence's row tile) was shared out, for the joining launch: its item of key/value head h lies in the
+// CTAs base + (first + h step + i) / share, i = 0 .. len - 1.
+struct AttnShare {
+  int64_t first;
+  int32_t base, step, len, share;
+};
+
 struct AttnParams {
   CUtensorMap tm_k, tm_v;
   const float* ks;
@@ -51,7 +58,7 @@ struct AttnParams {
   int32_t rows_per_tile, row_tiles;   // rows of a tile, tiles of a sequence
   FastDiv by_group, by_tiles, by_heads;   // query heads a key/value head; row_tiles; query heads
   int32_t main_grid, stages;
-  int64_t* prefix;                    // [batch * row_tiles + 1] first tile of each entry
+  AttnShare* shares;                  // [batch * row_tiles]
   float2* part_ml;                    // [CTA][2][rows of a tile] maximum (base 2) and sum of a partial item
   float* part_o;                      // [CTA][2][rows of a tile][D]
   int32_t* status;
@@ -117,11 +124,12 @@ struct KeySpan {
   int32_t first, T, ctx;    // first row in q, rows, context
 };
 
-// Where a CTA begins: entry, head and tile of the item; the warps' parts of the tile count.
+// Where a CTA begins: entry, head and tile of the item; what the warps exchange to find it.
 struct AttnWork {
   KeySpan span;
   int32_t entry, head, offset, len;
-  int64_t part[16];
+  int64_t left;          // tiles of the CTA
+  int64_t part[2][16];
 };
 
 template <int M, int KS>
@@ -144,61 +152,91 @@ __device__ __forceinline__ KeySpan entry_span(const AttnParams& p, int b, int rt
   return s;
 }
 
-// Where tile number `at` of the whole call lies; called by every thread, the answer in sh. CTA 0 also leaves
-// the entries' first tiles for the joining launch.
-template <int M, int KS>
-__device__ __forceinline__ void locate(const AttnParams& p, AttnWork& sh, int64_t* prefix, bool write,
-                                       int64_t (&range)[2]) {
-  const int n = p.batch * p.row_tiles, tid = threadIdx.x;
-  const int threads = blockDim.x;
-  const int per = (n + threads - 1) / threads;
-  const int e0 = min(tid * per, n), e1 = min(e0 + per, n);
-  int64_t sum = 0;
-  KeySpan s = {};
-  for (int e = e0; e < e1; ++e) {
-    const int b = p.by_tiles.quot(e);
-    s = entry_span<M, KS>(p, b, e - b * p.row_tiles);
-    sum += static_cast<int64_t>(s.t1 - s.t0) * p.hk;
-  }
-  int64_t upto = sum;   // within the warp, this thread's own among them
+// A number's sum over the threads before this one, and over all; `part` is the warps' exchange.
+__device__ __forceinline__ void block_scan(int64_t mine, int64_t (&part)[16], int64_t& before, int64_t& total) {
+  const int tid = threadIdx.x;
+  int64_t upto = mine;
 #pragma unroll
   for (int off = 1; off < 32; off *= 2) {
     const int64_t v = __shfl_up_sync(0xffffffffu, upto, off);
     if ((tid & 31) >= off) upto += v;
   }
-  if ((tid & 31) == 31) sh.part[tid >> 5] = upto;
+  if ((tid & 31) == 31) part[tid >> 5] = upto;
   __syncthreads();
-  int64_t before = upto - sum, total = 0;
-  for (int i = 0; i < threads / 32; ++i) {
-    if (i < (tid >> 5)) before += sh.part[i];
-    total += sh.part[i];
+  before = upto - mine;
+  total = 0;
+  for (int i = 0; i < static_cast<int>(blockDim.x) / 32; ++i) {
+    if (i < (tid >> 5)) before += part[i];
+    total += part[i];
   }
-  const int64_t share = quot(total + gridDim.x - 1, gridDim.x);
-  range[0] = min(share * blockIdx.x, total);
-  range[1] = min(range[0] + share, total);
-  if (write || (range[0] >= before && range[0] < before + sum)) {
-    int64_t at = before;
+}
+
+// A CTA pays for every item it takes part in with the item's start and its sums' way out, about as long as this many
+// tiles: a call of fewer tiles a CTA gives every CTA one item.
+constexpr int kItemTiles = 6;
+
+// The CTA's share of the call's tiles, in sh and `range` (tiles range[0] .. range[1]-1 of the CTA's own count); called by
+// every thread. CTA 0 also leaves the shares for the joining launch. Either all items' tiles are laid end to end and cut
+// into equal pieces, or (short calls) each item has CTAs of its own in proportion to its length.
+template <int M, int KS>
+__device__ __forceinline__ void locate(const AttnParams& p, AttnWork& sh, bool write, int64_t (&range)[2]) {
+  const int n = p.batch * p.row_tiles, tid = threadIdx.x, G = gridDim.x;
+  const int threads = blockDim.x;
+  const int per = n <= threads ? 1 : (n + threads - 1) / threads;
+  const int e0 = min(tid * per, n), e1 = min(e0 + per, n);
+  KeySpan s = {};
+  auto span_of = [&](int e) {
+    const int b = p.by_tiles.quot(e);
+    return entry_span<M, KS>(p, b, e - b * p.row_tiles);
+  };
+  int64_t sum = 0;   // tiles, and above 2^40 items
+  for (int e = e0; e < e1; ++e) {
+    s = span_of(e);
+    const int len = s.t1 - s.t0;
+    sum += static_cast<int64_t>(len) * p.hk + (len > 0 ? static_cast<int64_t>(p.hk) << 40 : 0);
+  }
+  constexpr int64_t kTiles = (1ll << 40) - 1;
+  int64_t before, total;
+  block_scan(sum, sh.part[0], before, total);
+  const int64_t items = total >> 40;
+  before &= kTiles;
+  total &= kTiles;
+  const int64_t share = quot(total + G - 1, G);
+  const bool own = items <= G && share <= kItemTiles;   // CTAs of its own for each item
+  auto ctas_of = [&](int len) { return 1 + static_cast<int>(quot(len * (G - items), total)); };
+  if (own) {
+    int64_t mine = 0, all;
     for (int e = e0; e < e1; ++e) {
-      if (e1 - e0 > 1) {     // a thread's one entry is known already
-        const int b = p.by_tiles.quot(e);
-        s = entry_span<M, KS>(p, b, e - b * p.row_tiles);
-      }
-      const int64_t len = static_cast<int64_t>(s.t1 - s.t0) * p.hk;
-      if (range[0] >= at && range[0] < at + len) {
-        const int64_t in = range[0] - at;
-        sh.span = s;
-        sh.entry = e;
-        sh.len = s.t1 - s.t0;
-        sh.head = static_cast<int>(quot(in, sh.len));
-        sh.offset = static_cast<int>(in - static_cast<int64_t>(sh.head) * sh.len);
-      }
-      if (write) prefix[e] = at;
-      at += len;
+      if (e1 - e0 > 1) s = span_of(e);
+      if (s.t1 > s.t0) mine += p.hk * ctas_of(s.t1 - s.t0);
     }
-    if (write && e1 == n && e0 < n) prefix[n] = at;
+    block_scan(mine, sh.part[1], before, all);
   }
-  if (write && n == 0 && tid == 0) prefix[0] = 0;
+  range[0] = own ? 0 : min(share * blockIdx.x, total);
+  range[1] = own ? 0 : min(range[0] + share, total);
+  if (tid == 0) sh.left = 0;
   __syncthreads();
+  int64_t at = before;   // of tiles, or of CTAs
+  for (int e = e0; e < e1; ++e) {
+    if (e1 - e0 > 1) s = span_of(e);     // a thread's one entry is known already
+    const int len = s.t1 - s.t0;
+    if (len == 0) continue;
+    const int ctas = own ? ctas_of(len) : 0, piece = own ? static_cast<int>(quot(len + ctas - 1, ctas)) : 0;
+    const int64_t size = static_cast<int64_t>(own ? ctas : len) * p.hk, me = own ? blockIdx.x : range[0];
+    if (me >= at && me < at + size) {
+      const int64_t in = me - at;
+      sh.span = s;
+      sh.entry = e;
+      sh.len = len;
+      sh.head = static_cast<int>(quot(in, own ? ctas : len));
+      sh.offset = static_cast<int>(in - static_cast<int64_t>(sh.head) * (own ? ctas : len)) * (own ? piece : 1);
+      sh.left = own ? max(min(piece, len - sh.offset), 0) : range[1] - range[0];
+    }
+    if (write) p.shares[e] = own ? AttnShare{0, static_cast<int32_t>(at), ctas * piece, len, piece} : AttnShare{at, 0, len, len, static_cast<int32_t>(share)};
+    at += size;
+  }
+  __syncthreads();
+  if (own) range[1] = sh.left;
 }
 
 // Walks the segments of a CTA's range: consecutive tiles of one item.

@@ -850,7 +850,7 @@ __global__ void __launch_bounds__(S::kThreads, 1) aq_tree_attention_tc_kernel(co
   const uint32_t tmem = sh.tmem;
   pdl_wait_prior_grid();
   int64_t range[2];
-  locate<S::M, S::BN>(p, sh.work, p.prefix, blockIdx.x == 0, range);
+  locate<S::M, S::BN>(p, sh.work, blockIdx.x == 0, range);
   pdl_launch_dependents();   // the joining blocks find their rows meanwhile; they wait for this grid before its results
   const AbortCtl ctl = {&sh.abort, p.status, p.timeout_ns};
   if (warp < S::kSoftWarps) {
