@@ -15,15 +15,17 @@
 // distributed shared memory: one launch, no workspace. Only a refused child that has siblings left, with
 // q given, needs a normaliser in between: one more pass, its partial sums added in rank order by every CTA.
 #include <atomic>
+#include <type_traits>
 
 #include "aq_serve.h"
 
 namespace aq {
 namespace {
 
-// Threads of a CTA: 1024 where the clusters of a call leave SMs to spare (one sequence then loads its rows
-// in one or two rounds), else 256, four CTAs an SM.
-constexpr int kVerWide = 1024, kVerNarrow = 256;
+// Threads of a CTA: 1024 in clusters of 16 for a few sequences (each loads its rows in one or two rounds; measured on
+// 262144 words, one sequence: 11.0 us against 17.7 with 256 threads; eight: 17.8 against 10.9, as few such clusters fit at
+// once), else 256, three CTAs an SM (80 registers: with four, the rows of q spill: 61 us for 48 sequences against 41).
+constexpr int kVerWide = 1024, kVerNarrow = 256, kVerPerSm = 3, kVerWideBatch = 4;
 constexpr int kVerMaxCluster = 16;
 
 struct VerifyParams {
@@ -107,19 +109,23 @@ struct VerShared {
   int32_t cur, refused, next, count, done;
 };
 
+// What the draw's weights are made of: p with `k` refused tokens left out, max(p - q, 0) after one refusal, or the
+// residual after several.
+enum Draw { kPlain, kOnce, kSeveral };
+
 // Largest r(v) / E(v) of this CTA's share of the vocabulary, N words at a time.
-template <typename T, bool HASQ, int N, int kVerThreads>
+template <typename T, Draw MODE, int N, int kVerThreads>
 __device__ __forceinline__ void race(const T* pr, const T* qr, const float* er, int vocab, int k, const VerShared& sh,
                                      int rank, int cluster, float& best, int& at) {
   // A quotient can pass the warp's best so far only if w > best e (1 - 2^-21), rounding included: one product and
   // one comparison a word, and the divisions only where some word of a thread's batch gets that far. Words equal to
   // the best pass too, and the lowest index is sorted out when the threads' bests meet.
   float bar = 0.0f;
-  auto weigh = [&](float w, float q) { return HASQ ? residual(w, q, k, k - 1, sh.zinv) : w; };
+  auto weigh = [&](float w, float q) { return MODE == kPlain ? w : MODE == kOnce ? fmaxf(w - q, 0.0f) : residual(w, q, k, k - 1, sh.zinv); };
   auto offer = [&](float w, float e, int v) {
     const float s = __fdiv_rn(w, e);
     if (s > best) {
-      if (!HASQ)
+      if (MODE == kPlain)
         for (int j = 0; j < k; ++j)
           if (sh.gone[j] == v) return;   // a refused token has no mass; looked up only for a new best
       best = s;
@@ -136,7 +142,7 @@ __device__ __forceinline__ void race(const T* pr, const T* qr, const float* er, 
 #pragma unroll
     for (int j = 0; j < U; ++j) {
       w[j].load(pr + v + j * step);
-      if (HASQ && k > 0) q[j].load(qr + v + j * step);
+      if (MODE != kPlain) q[j].load(qr + v + j * step);
       e[j].load(er + v + j * step);
     }
     bool hit = false;
@@ -144,7 +150,7 @@ __device__ __forceinline__ void race(const T* pr, const T* qr, const float* er, 
     for (int j = 0; j < U; ++j)
 #pragma unroll
       for (int i = 0; i < N; ++i) {
-        if (HASQ && k > 0) w[j].x[i] = weigh(w[j].x[i], q[j].x[i]);
+        if (MODE != kPlain) w[j].x[i] = weigh(w[j].x[i], q[j].x[i]);
         hit = hit || w[j].x[i] > bar * e[j].x[i];
       }
     if (__any_sync(0xffffffffu, hit)) {
@@ -160,13 +166,13 @@ __device__ __forceinline__ void race(const T* pr, const T* qr, const float* er, 
   }
   for (; v < vocab; v += step)
     for (int i = 0; i < N && v + i < vocab; ++i) {
-      const float w = weigh(prob(pr, v + i), HASQ && k > 0 ? prob(qr, v + i) : 0.0f), e = er[v + i];
+      const float w = weigh(prob(pr, v + i), MODE != kPlain ? prob(qr, v + i) : 0.0f), e = er[v + i];
       if (w > bar * e) offer(w, e, v + i);
     }
 }
 
 template <typename T, bool HASQ, int kVerThreads>
-__global__ void __launch_bounds__(kVerThreads, 1024 / kVerThreads) aq_verify_kernel(const __grid_constant__ VerifyParams p) {
+__global__ void __launch_bounds__(kVerThreads, kVerThreads == kVerWide ? 1 : kVerPerSm) aq_verify_kernel(const __grid_constant__ VerifyParams p) {
   __shared__ VerShared sh;
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
   const int C = p.cluster;
@@ -305,10 +311,16 @@ __global__ void __launch_bounds__(kVerThreads, 1024 / kVerThreads) aq_verify_ker
     const float* er = p.noise + b * p.ld_noise;
     const uintptr_t low = reinterpret_cast<uintptr_t>(pr) | reinterpret_cast<uintptr_t>(qr);
     constexpr int kVec = 16 / sizeof(T);
-    if (((low | reinterpret_cast<uintptr_t>(er)) & 15) == 0)
-      race<T, HASQ, kVec, kVerThreads>(pr, qr, er, p.vocab, k, sh, rank, C, best, at);
-    else
-      race<T, HASQ, 1, kVerThreads>(pr, qr, er, p.vocab, k, sh, rank, C, best, at);
+    const bool whole = ((low | reinterpret_cast<uintptr_t>(er)) & 15) == 0;
+    // with q, k counts refusals of the residual; without, tokens that are left out
+    auto pass_over = [&](auto mode) {
+      constexpr Draw kMode = decltype(mode)::value;
+      if (whole) race<T, kMode, kVec, kVerThreads>(pr, qr, er, p.vocab, k, sh, rank, C, best, at);
+      else race<T, kMode, 1, kVerThreads>(pr, qr, er, p.vocab, k, sh, rank, C, best, at);
+    };
+    if (!HASQ || k == 0) pass_over(std::integral_constant<Draw, kPlain>());
+    else if (k == 1) pass_over(std::integral_constant<Draw, kOnce>());
+    else pass_over(std::integral_constant<Draw, kSeveral>());
     unsigned long long key = (static_cast<unsigned long long>(__float_as_uint(best)) << 32) | (0xffffffffu - static_cast<uint32_t>(at));
 #pragma unroll
     for (int o = 16; o > 0; o >>= 1) {
@@ -423,10 +435,10 @@ extern "C" aq_status aq_verify_drafts(int32_t batch, int32_t vocab, const int32_
   v.path_cap = path_cap;
   // the largest cluster that keeps the launch within the CTAs that are resident at once and gives every CTA at
   // least one round of its threads
-  const bool wide = static_cast<int64_t>(batch) * kVerMaxCluster <= dev.sms;
+  const bool wide = batch <= kVerWideBatch;
   const int threads = wide ? kVerWide : kVerNarrow;
   int c = kVerMaxCluster;
-  while (c > 1 && (static_cast<int64_t>(batch) * c > (wide ? 1 : 4) * dev.sms || vocab < c * threads)) c /= 2;
+  while (c > 1 && (static_cast<int64_t>(batch) * c > (wide ? 1 : kVerPerSm) * dev.sms || vocab < c * threads)) c /= 2;
   v.cluster = c;
   v.device = dev.index;
   if (static_cast<int64_t>(batch) * c > 0x7fffffffLL) return serve_fail(AQ_ERR_SHAPE, "%s: batch=%d is too large", who, batch);
