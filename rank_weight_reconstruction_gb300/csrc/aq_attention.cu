@@ -725,26 +725,29 @@ __global__ void __launch_bounds__(S::kThreads, S::kPerSm) aq_tree_attention_kern
   }
 }
 
-// Adds the partial sums of the items that were shared between CTAs, in the CTAs' order. One block per row and
-// query head: its four warps take every fourth part.
-template <int D>
+// Adds the partial sums of the items that were shared between CTAs, in the CTAs' order. W warps to a row and query head,
+// each taking every W-th part: one where an item has few parts (up to about eight: two rounds of loads), as the rows are then
+// many and the blocks' waves are what they cost; four where a few items are cut into many. Measured, calls whole: 16384
+// rows and heads of three parts 255 us with four warps and 247 with one, 256 of five parts 19.5 and 18.9, 512 of
+// nineteen parts 29.2 and 41.6.
+template <int D, int W>
 __global__ void __launch_bounds__(128) aq_attention_join_kernel(const __grid_constant__ AttnParams p) {
   constexpr int N = D / 32;
-  __shared__ int b_of;
-  __shared__ float sm[4], sl[4], so[4][D];
+  __shared__ float sm[4], sl[4], so[W == 1 ? 1 : 4][D];
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
   const int heads = p.hk * p.group;
-  const int row = p.by_heads.quot(blockIdx.x), head = blockIdx.x - row * heads, kv_head = p.by_group.quot(head);
-  if (tid == 0) b_of = -1;
-  __syncthreads();
+  const uint32_t unit = blockIdx.x * (4u / W) + (W == 1 ? warp : 0), part = W == 1 ? 0 : warp;
+  const int row = p.by_heads.quot(unit), head = unit - row * heads, kv_head = p.by_group.quot(head);
   // Before the wait: the batch's layout is an input that was complete when the main grid, whose blocks all got past their
   // own wait before these could start, began to read it.
-  for (int b = tid; b < p.batch; b += 128) {
-    const int c0 = p.cu[b], c1 = p.cu[b + 1];
-    if (c0 >= 0 && c0 <= row && row < c1 && row - c0 < p.max_q) b_of = b;
+  int b = -1;
+  if (row < p.total_q) {
+    for (int k = lane; k < p.batch; k += 32) {
+      const int c0 = p.cu[k], c1 = p.cu[k + 1];
+      if (c0 >= 0 && c0 <= row && row < c1 && row - c0 < p.max_q) b = k;
+    }
   }
-  __syncthreads();
-  const int b = b_of;
+  b = __reduce_max_sync(0xffffffffu, b);
   const int in_seq = b < 0 ? 0 : row - p.cu[b];
   pdl_wait_prior_grid();
   pdl_launch_dependents();
@@ -760,12 +763,12 @@ __global__ void __launch_bounds__(128) aq_attention_join_kernel(const __grid_con
 #pragma unroll
   for (int e = 0; e < N; ++e) o[e] = 0.0f;
   constexpr int kParts = 4;   // of each warp in flight at once
-  for (int c = c0 + warp; c <= c1; c += 4 * kParts) {
+  for (int c = c0 + part; c <= c1; c += W * kParts) {
     float2 ml[kParts];
     __align__(8) float v[kParts][N];
 #pragma unroll
     for (int k = 0; k < kParts; ++k) {
-      const int cc = min(c + 4 * k, c1);   // past the last: the last again, left out below
+      const int cc = min(c + W * k, c1);   // past the last: the last again, left out below
       const int64_t at = (static_cast<int64_t>(cc) * 2 + (cc > c0 ? 0 : 1)) * p.rows_per_tile + rr;
       ml[k] = p.part_ml[at];
       const float* src = p.part_o + at * D + lane * N;
@@ -774,7 +777,7 @@ __global__ void __launch_bounds__(128) aq_attention_join_kernel(const __grid_con
     }
 #pragma unroll
     for (int k = 0; k < kParts; ++k)
-      if (c + 4 * k > c1) {
+      if (c + W * k > c1) {
         ml[k] = make_float2(-INFINITY, 0.0f);
 #pragma unroll
         for (int e = 0; e < N; ++e) v[k][e] = 0.0f;
@@ -795,31 +798,45 @@ __global__ void __launch_bounds__(128) aq_attention_join_kernel(const __grid_con
     }
     m = mx;
   }
+  uint16_t* out = p.o + static_cast<int64_t>(row) * p.o_tok + head * p.o_head;
+  auto finish = [&](float mt, float lt) {   // the row's factor; its logarithm's sum by the first lane
+    const bool none = mt == -INFINITY && lt == 0.0f;
+    if (p.lse && lane == 0 && part == 0)
+      p.lse[static_cast<int64_t>(row) * heads + head] = none ? -INFINITY : ((mt == -INFINITY ? 0.0f : mt) + log2f(lt)) * 0.6931471805599453f;
+    return none ? 0.0f : 1.0f / lt;
+  };
+  if constexpr (W == 1) {
+    const float inv = finish(m, l);
+    const bool none = m == -INFINITY && l == 0.0f;
 #pragma unroll
-  for (int e = 0; e < N; ++e) so[warp][lane * N + e] = o[e];
-  if (lane == 0) {
-    sm[warp] = m;
-    sl[warp] = l;
+    for (int e = 0; e < N; e += 2)
+      *reinterpret_cast<uint32_t*>(out + lane * N + e) = none ? 0u : pack_bf16x2_cvt(o[e] * inv, o[e + 1] * inv);
+  } else {
+#pragma unroll
+    for (int e = 0; e < N; ++e) so[warp][lane * N + e] = o[e];
+    if (lane == 0) {
+      sm[warp] = m;
+      sl[warp] = l;
+    }
+    __syncthreads();
+    float mt = -INFINITY, lt = 0.0f, f[4];
+#pragma unroll
+    for (int k = 0; k < 4; ++k) mt = fmaxf(mt, sm[k]);
+    const float mz = mt == -INFINITY ? 0.0f : mt;
+#pragma unroll
+    for (int k = 0; k < 4; ++k) {
+      f[k] = ex2(sm[k] - mz);
+      lt += sl[k] * f[k];
+    }
+    const float inv = finish(mt, lt);
+    const bool none = mt == -INFINITY && lt == 0.0f;
+    for (int d = tid; d < D; d += 128) {
+      float x = 0.0f;
+#pragma unroll
+      for (int k = 0; k < 4; ++k) x += so[k][d] * f[k];
+      out[d] = f32_to_bf16_rn(none ? 0.0f : x * inv);
+    }
   }
-  __syncthreads();
-  float mt = -INFINITY, lt = 0.0f, f[4];
-#pragma unroll
-  for (int k = 0; k < 4; ++k) mt = fmaxf(mt, sm[k]);
-  const float mz = mt == -INFINITY ? 0.0f : mt;
-#pragma unroll
-  for (int k = 0; k < 4; ++k) {
-    f[k] = ex2(sm[k] - mz);
-    lt += sl[k] * f[k];
-  }
-  const bool none = mt == -INFINITY && lt == 0.0f;
-  const float inv = none ? 0.0f : 1.0f / lt;
-  for (int d = tid; d < D; d += 128) {
-    float x = 0.0f;
-#pragma unroll
-    for (int k = 0; k < 4; ++k) x += so[k][d] * f[k];
-    p.o[static_cast<int64_t>(row) * p.o_tok + head * p.o_head + d] = f32_to_bf16_rn(none ? 0.0f : x * inv);
-  }
-  if (p.lse && tid == 0) p.lse[static_cast<int64_t>(row) * heads + head] = none ? -INFINITY : (mz + log2f(lt)) * 0.6931471805599453f;
 }
 
 // ---------------------------------------------------------------------------------
@@ -890,7 +907,9 @@ aq_status launch_rows(AttnParams& p, const aq_kv_cache* c, const ServeDev& dev, 
     default: s = launch_attention_tc(p, c, dev, st, who);
   }
   if (s != AQ_OK) return s;
-  return serve_launched(launch_serve(aq_attention_join_kernel<D>, p, dim3(static_cast<unsigned>(p.total_q * p.hk * p.group)), 128, 0, st), who);
+  const int64_t units = p.total_q * p.hk * p.group, items = static_cast<int64_t>(p.batch) * p.row_tiles * p.hk;
+  if (p.main_grid <= 8 * items) return serve_launched(launch_serve(aq_attention_join_kernel<D, 1>, p, dim3(static_cast<unsigned>((units + 3) / 4)), 128, 0, st), who);
+  return serve_launched(launch_serve(aq_attention_join_kernel<D, 4>, p, dim3(static_cast<unsigned>(units)), 128, 0, st), who);
 }
 
 aq_status check_batch(const aq_kv_cache* c, const aq_draft_batch* d, int32_t q_heads, const char* who) {

@@ -18,6 +18,7 @@
 
 #include <algorithm>
 #include <atomic>
+#include <type_traits>
 
 #include "aq_attention.cuh"
 
@@ -167,6 +168,18 @@ __device__ __forceinline__ uint32_t tile_addr(uint32_t base, int rows, int row, 
   return base + (c >> 3) * rows * 128 + row * 128 + (((c & 7) ^ (row & 7)) << 4);
 }
 
+// Whether the phase with the given parity is complete, without waiting.
+__device__ __forceinline__ bool mbar_test(uint64_t* bar, uint32_t parity) {
+  uint32_t done;
+  asm volatile(
+      "{\n\t.reg .pred p;\n\t"
+      "mbarrier.test_wait.parity.shared::cta.b64 p, [%1], %2;\n\t"
+      "selp.u32 %0, 1, 0, p;\n\t}"
+      : "=r"(done)
+      : "r"(smem_u32(bar)), "r"(parity)
+      : "memory");
+  return done != 0;
+}
 // A position in a ring of `n` buffers: index, and the parity of the phase its use completes.
 struct Ring {
   int n, i = 0;
@@ -321,78 +334,136 @@ __device__ __forceinline__ void tc_convert(TcShared& sh, const uint8_t* codes, c
 // ---------------------------------------------------------------------------------
 // MMA issue, one warp
 // ---------------------------------------------------------------------------------
+// The tensor pipe holds about one product more than it runs, and a wait costs this warp some 100 clocks even where its
+// phase is long complete (78 on an idle SM): with two row tiles, waits between the bursts of eight products left the pipe
+// idle for 1200 of 3830 clocks a pair of tiles (D = 128). So what the next burst waits for is looked at before the
+// last products of this one, and waited for only where it was not there yet.
 template <class S>
 __device__ __forceinline__ bool tc_issue(const AttnParams& p, TcShared& sh, const uint8_t* qbuf, const uint8_t* tiles, int nring,
                                          uint32_t tmem, const int64_t (&range)[2], const AbortCtl& ctl) {
   constexpr uint32_t kIdS = tc_idesc(S::E4M3, false, S::BN), kIdO = tc_idesc(S::E4M3, true, S::D);
+  constexpr int kScores = S::D / 16, kSums = S::BN / 16, kLast = kScores > 4 ? 3 : 2;   // products; those behind a look ahead
   Walk<S::M, S::BN> w(p, sh.work, range);
   uint32_t tile = 0, seg = 0;          // so far, of all segments
   // buffers in order of use: K 0, V 0, K 1, V 1, ...; this tile's V, and the K whose scores come next
   Ring k_at(nring), v_at(nring);
   v_at.next();
-  auto x_of = [](int t, uint32_t n) { return S::TILES == 2 ? t : static_cast<int>(n & 1); };
-  auto scores = [&](int t, uint32_t n) {
-    const int x = x_of(t, n);
-    if (elect_one()) {
-      const uint64_t q = smem_desc_k128(smem_u32(qbuf) + t * 128 * S::D * 2), k = smem_desc_k128(smem_u32(tiles) + k_at.i * S::kTile);
-#pragma unroll
-      for (int i = 0; i < S::D / 16; ++i)   // descriptor addresses count 16 bytes
-        tc_mma_bf16(tmem + S::kS(x), q + (((i >> 2) * 128 * 128 + (i & 3) * 32) >> 4), k + (((i >> 2) * S::BN * 128 + (i & 3) * 32) >> 4),
-                    kIdS, i > 0);
-      tc_commit(&sh.s_full[x]);
-      if (t == S::TILES - 1) tc_commit(&sh.empty[k_at.i]);
-    }
-    __syncwarp();
+  bool k_here = false, v_here = false, p_here = false;   // seen: the next scores' K, this tile's V, the next sums' weights
+  bool skip = false;                                     // with p_here: those sums are done by the threads
+  const uint64_t q0 = smem_desc_k128(smem_u32(qbuf)), k0 = smem_desc_k128(smem_u32(tiles)), v0 = smem_desc_mn128(smem_u32(tiles), S::BN * 128);
+  auto wait = [&](uint64_t* bar, uint32_t parity) { return __all_sync(0xffffffffu, mbar_wait(bar, parity, ctl)); };
+  auto need = [&](bool& here, uint64_t* bar, uint32_t parity) {
+    if (!here) here = wait(bar, parity);
+    return here;
+  };
+  // t: row tile; x: score buffer
+  auto scores = [&](auto tc, int x, uint32_t n, bool look) {
+    constexpr int t = decltype(tc)::value;
+    const uint64_t k = k0 + k_at.i * (S::kTile >> 4);
+    const uint32_t d = tmem + S::kS(x);
+    auto product = [&](int i) {   // descriptor addresses count 16 bytes
+      tc_mma_bf16(d, q0 + ((t * 128 * S::D * 2 + (i >> 2) * 128 * 128 + (i & 3) * 32) >> 4), k + (((i >> 2) * S::BN * 128 + (i & 3) * 32) >> 4), kIdS, i > 0);
+    };
+    uint64_t* const k_empty = &sh.empty[k_at.i];
     if (t == S::TILES - 1) {
       k_at.next();
       k_at.next();
+      k_here = false;
     }
+    if (S::TILES == 2) {
+      if (elect_one()) {
+#pragma unroll
+        for (int i = 0; i < kScores - kLast; ++i) product(i);
+      }
+      __syncwarp();
+      if (look) {
+        bool vn = true, kn = true;
+        const bool pn = mbar_test(&sh.p_ready[1 - t], (t == 0 ? n - 1 : n) & 1);   // the other row tile's weights
+        if (t == 1) {
+          vn = mbar_test(&sh.full[v_at.i], v_at.phase);
+          kn = mbar_test(&sh.full[k_at.i], k_at.phase);
+        }
+        const bool sn = *reinterpret_cast<volatile int32_t*>(&sh.skip[1 - t]) != 0;
+        const uint32_t all = __reduce_and_sync(0xffffffffu, (pn ? 1u : 0u) | (vn ? 2u : 0u) | (kn ? 4u : 0u) | (sn ? 8u : 0u));
+        p_here = (all & 1) != 0;
+        skip = (all & 8) != 0;
+        if (t == 1) {
+          v_here = (all & 2) != 0;
+          k_here = (all & 4) != 0;
+        }
+      }
+    }
+    if (elect_one()) {
+#pragma unroll
+      for (int i = S::TILES == 2 ? kScores - kLast : 0; i < kScores; ++i) product(i);
+      tc_commit(&sh.s_full[x]);
+      if (t == S::TILES - 1) tc_commit(k_empty);
+    }
+    __syncwarp();
   };
-  auto sums = [&](int t, uint32_t n, bool first) {
-    const int x = x_of(t, n);
-    const bool skip = *reinterpret_cast<volatile int32_t*>(&sh.skip[x]) != 0;
+  auto sums = [&](auto tc, int x, bool first) {
+    constexpr int t = decltype(tc)::value;
+    const uint64_t v = v0 + v_at.i * (S::kTile >> 4);
+    const uint32_t a = tmem + S::kS(x);
     if (elect_one()) {
       if (!skip) {
-        const uint64_t v = smem_desc_mn128(smem_u32(tiles) + v_at.i * S::kTile, S::BN * 128);
 #pragma unroll
-        for (int i = 0; i < S::BN / 16; ++i)
-          tc_mma_ts(tmem + S::kO(t), tmem + S::kS(x) + 8 * i, v + ((i * 2048) >> 4), kIdO, !(first && i == 0));
+        for (int i = 0; i < kSums; ++i) tc_mma_ts(tmem + S::kO(t), a + 8 * i, v + ((i * 2048) >> 4), kIdO, !(first && i == 0));
       }
       tc_commit(&sh.o_done[t]);
       if (t == S::TILES - 1) tc_commit(&sh.empty[v_at.i]);
     }
     __syncwarp();
+    p_here = false;
     if (t == S::TILES - 1) {
       v_at.next();
       v_at.next();
+      v_here = false;
     }
   };
-  auto arrived = [&](const Ring& at) {
-    if (!__all_sync(0xffffffffu, mbar_wait(&sh.full[at.i], at.phase, ctl))) return false;
+  constexpr std::integral_constant<int, 0> kFirst{};
+  constexpr std::integral_constant<int, S::TILES - 1> kSecond{};
+  // the weights in score buffer x, their sums, and with `more` the scores of the next tile
+  auto turn = [&](auto tc, int x, uint32_t parity, bool first) {
+    if (!p_here) {
+      if (!need(p_here, &sh.p_ready[x], parity)) return false;
+      skip = __any_sync(0xffffffffu, *reinterpret_cast<volatile int32_t*>(&sh.skip[x]) != 0);
+    }
+    if (!need(v_here, &sh.full[v_at.i], v_at.phase)) return false;
     tc_fence_after();
+    sums(tc, x, first);
     return true;
   };
-  for (; w.left > 0; w.next(p), ++seg) {
-    if (!__all_sync(0xffffffffu, mbar_wait(&sh.q_ready, seg & 1, ctl)) || !arrived(k_at)) return false;
-    for (int t = 0; t < S::TILES; ++t) scores(t, tile);
-    for (int i = 0; i < w.n; ++i, ++tile) {
-      const bool more = i + 1 < w.n;
-      if (S::TILES == 1 && more) {
-        if (!arrived(k_at)) return false;
-        scores(0, tile + 1);
-      }
-      for (int t = 0; t < S::TILES; ++t) {
-        const uint32_t x_parity = S::TILES == 2 ? tile & 1 : (tile >> 1) & 1;
-        if (!__all_sync(0xffffffffu, mbar_wait(&sh.p_ready[x_of(t, tile)], x_parity, ctl)) || !arrived(v_at)) return false;
-        sums(t, tile, i == 0);
-        if (S::TILES == 2 && more) {
-          if (!arrived(k_at)) return false;
-          scores(t, tile + 1);
+  auto next_keys = [&]() {
+    const bool ok = need(k_here, &sh.full[k_at.i], k_at.phase);
+    tc_fence_after();
+    return ok;
+  };
+  for (;; w.next(p), ++seg) {
+    const int len = __shfl_sync(0xffffffffu, w.left > 0 ? w.n : 0, 0);   // the same in every lane, and known to be
+    if (len == 0) return true;
+    if (!wait(&sh.q_ready, seg & 1) || !next_keys()) return false;
+    scores(kFirst, S::TILES == 2 ? 0 : tile & 1, tile, false);
+    if (S::TILES == 2) scores(kSecond, 1, tile, false);
+    for (int i = 0; i < len; ++i, ++tile) {
+      const bool more = i + 1 < len;
+      if (S::TILES == 2) {
+        if (!turn(kFirst, 0, tile & 1, i == 0)) return false;
+        if (more) {
+          if (!next_keys()) return false;
+          scores(kFirst, 0, tile + 1, true);
         }
+        if (!turn(kSecond, 1, tile & 1, i == 0)) return false;
+        if (more) scores(kSecond, 1, tile + 1, i + 2 < len);
+      } else {
+        if (more) {
+          if (!next_keys()) return false;
+          scores(kFirst, (tile + 1) & 1, tile + 1, false);
+        }
+        if (!turn(kFirst, tile & 1, (tile >> 1) & 1, i == 0)) return false;
       }
     }
   }
-  return true;
 }
 
 // ---------------------------------------------------------------------------------
@@ -487,16 +558,17 @@ __device__ __forceinline__ void tc_weigh(const AttnParams& p, TcShared& sh, uint
     // queries of the warp's rows, as the MMA reads them; what lies in lanes without a row reaches no other
     constexpr int L = D / 8, RPW = 32 / L;       // lanes a row, rows at once
     const int c = lane % L;
+    auto query = [&](uint32_t rr) {
+      const uint32_t i = p.by_group.quot(rr);
+      return p.q + (static_cast<int64_t>(w.s.first) + i) * p.q_tok + (w.head * group + (rr - i * group)) * p.q_head + c * 8;
+    };
     constexpr int kBatch = 32 / RPW < 16 ? 32 / RPW : 16;   // loads in flight
 #pragma unroll 1
     for (int k0 = 0; k0 * RPW < count; k0 += kBatch) {
       uint4 v[kBatch];
 #pragma unroll
-      for (int k = 0; k < kBatch; ++k) {
-        // rows past the last load the last: a load under a condition would be waited for at once
-        const uint32_t rr = min(row0 + 4 * ((k0 + k) * RPW + lane / L), rows - 1), i = p.by_group.quot(rr);
-        v[k] = *reinterpret_cast<const uint4*>(p.q + (static_cast<int64_t>(w.s.first) + i) * p.q_tok + (w.head * group + (rr - i * group)) * p.q_head + c * 8);
-      }
+      for (int k = 0; k < kBatch; ++k)   // rows past the last load the last: a load under a condition would be waited for at once
+        v[k] = *reinterpret_cast<const uint4*>(query(min(row0 + 4 * ((k0 + k) * RPW + lane / L), rows - 1)));
       uint32_t top_bits[kBatch];
       if constexpr (S::E4M3) {
         const uint32_t who = (L == 32 ? 0xffffffffu : (1u << L) - 1) << (lane & ~(L - 1));
@@ -514,18 +586,16 @@ __device__ __forceinline__ void tc_weigh(const AttnParams& p, TcShared& sh, uint
 #pragma unroll
       for (int k = 0; k < kBatch; ++k) {
         const int lr = wq * 32 + (k0 + k) * RPW + lane / L;   // lane of the tensor memory
-        float fac = fabsf(scale2);
         uint32_t x[4] = {v[k].x ^ sign, v[k].y ^ sign, v[k].z ^ sign, v[k].w ^ sign};
         if constexpr (S::E4M3) {
           const bool finite = top_bits[k] < 0x7f800000u;
           const int e = finite ? top_exponent(__uint_as_float(top_bits[k])) : 0;
           const float f = pow2(14 - e);
-          fac = finite ? pow2(e - 14) * fac : __uint_as_float(0x7fc00000u);   // no finite score
 #pragma unroll
           for (int y = 0; y < 4; ++y)
             x[y] = finite ? pack_f16x2(__uint_as_float(x[y] << 16) * f, __uint_as_float(x[y] & 0xffff0000u) * f) : 0u;
+          if (c == 0) sh.fac[t * 128 + lr] = finite ? pow2(e - 14) * fabsf(scale2) : __uint_as_float(0x7fc00000u);   // NaN: no finite score
         }
-        if (c == 0) sh.fac[t * 128 + lr] = fac;
         asm volatile("st.shared.v4.u32 [%0], {%1, %2, %3, %4};" ::"r"(tile_addr(smem_u32(qbuf) + t * 128 * D * 2, 128, lr, c)), "r"(x[0]),
                      "r"(x[1]), "r"(x[2]), "r"(x[3])
                      : "memory");
@@ -541,7 +611,7 @@ __device__ __forceinline__ void tc_weigh(const AttnParams& p, TcShared& sh, uint
     __syncwarp();
     if (lane == 0) mbar_arrive(&sh.q_ready);
     if (!meet()) return;
-    const float fac = sh.fac[t * 128 + r];
+    const float fac = S::E4M3 ? sh.fac[t * 128 + r] : fabsf(scale2);
 #pragma unroll
     for (int k = 0; k < 4; ++k) top = max(top, sh.top[t][k]);
     // keys [whole0, whole1) are seen by every row of the tile
@@ -553,13 +623,18 @@ __device__ __forceinline__ void tc_weigh(const AttnParams& p, TcShared& sh, uint
       const uint32_t x_parity = S::TILES == 2 ? tile & 1 : (tile >> 1) & 1;
       const int slot = tile % kInfo;
       const uint32_t s_addr = tmem + lanes + S::kS(x), o_addr = tmem + lanes + S::kO(t);
-      if (!wait(&sh.info[slot], (tile / kInfo) & 1) || !wait(&sh.s_full[x], x_parity)) return;
-      tc_fence_after();
+      if (!wait(&sh.info[slot], (tile / kInfo) & 1)) return;
       const uint32_t pages = *reinterpret_cast<volatile uint32_t*>(&sh.valid[slot]);
       const int64_t ka = static_cast<int64_t>(w.tile0 + it) * BN;
       const bool whole = ka >= whole0 && ka + BN <= whole1 && pages == all_pages;
       const float4* ks = reinterpret_cast<const float4*>(scales + slot * 2 * BN * 4);
       const float4* vs = ks + BN / 4;
+      uint32_t seen[BN / 32];   // of a tile that not every row sees in full; looked up while its scores form
+      if (live_warp && !whole)
+#pragma unroll 1
+        for (int c = 0; c < BN / 32; ++c) seen[c] = seen_bits(p, w.s, i_row, pos, ka + 32 * c, 32 * c, 32, pages, box_shift);
+      if (!wait(&sh.s_full[x], x_parity)) return;
+      tc_fence_after();
       auto tile_scale = [&]() {   // the tile's largest scale of a value; a NaN counts as the largest: every row sees it and is NaN
         const float* f = reinterpret_cast<const float*>(vs);
         uint32_t big = 0;
@@ -645,7 +720,7 @@ __device__ __forceinline__ void tc_weigh(const AttnParams& p, TcShared& sh, uint
         } else {
 #pragma unroll 1
           for (int c = 0; c < BN / 32; ++c) {
-            const uint32_t bits = seen_bits(p, w.s, i_row, pos, ka + 32 * c, 32 * c, 32, pages, box_shift);
+            const uint32_t bits = seen[c];
             float v[32];
             tmem_ld32(s_addr + 32 * c, v);
             const float* kf = reinterpret_cast<const float*>(ks) + 32 * c;
@@ -679,7 +754,7 @@ __device__ __forceinline__ void tc_weigh(const AttnParams& p, TcShared& sh, uint
         const float mz = m == -INFINITY ? 0.0f : m;
 #pragma unroll 1
         for (int c = 0; c < BN / 32; ++c) {
-          const uint32_t bits = whole ? 0xffffffffu : seen_bits(p, w.s, i_row, pos, ka + 32 * c, 32 * c, 32, pages, box_shift);
+          const uint32_t bits = whole ? 0xffffffffu : seen[c];
           float v[32];
           tmem_ld32(s_addr + 32 * c, v);
           uint32_t pk[16];
