@@ -540,7 +540,7 @@ def aq_mlp(gate: Theta, up: Theta, down: Theta, x, act=AQ_ACT_GELU_TANH, y=None,
 
 # ----------------------------------------------------------------------------------
 # serving: rotary positions, the paged key/value cache, drafted-token attention, verification. Their
-# tensors are marshalled by the compiled module _marshal (csrc/aq_python.c), which checks types, shapes and
+# tensors are marshalled by the compiled module _marshal (csrc/aq_python.cpp), which checks types, shapes and
 # strides, calls the entry point and returns its status.
 # ----------------------------------------------------------------------------------
 _marshal = None
@@ -552,7 +552,7 @@ def _serve():
     if _marshal is None:
         import importlib.util
 
-        import torch
+        import torch  # noqa: F401  (the module links against its libraries)
         lib = load()
         if not os.path.exists(build_lib.MARSHAL_PATH):
             raise RuntimeError(f"{build_lib.MARSHAL_PATH} is missing: build it with "
@@ -562,17 +562,14 @@ def _serve():
         spec.loader.exec_module(module)
         names = ("aq_rope", "aq_kv_write", "aq_kv_read", "aq_tree_attention_workspace_bytes", "aq_tree_attention",
                  "aq_verify_drafts")
-        module.bind(tuple(ctypes.cast(getattr(lib, n), ctypes.c_void_p).value for n in names),
-                    (torch.bfloat16, torch.float32, torch.int32, torch.int64, torch.uint64, torch.uint8))
+        module.bind(tuple(ctypes.cast(getattr(lib, n), ctypes.c_void_p).value for n in names), _check)
         _marshal = module
     return _marshal
 
 
-def _raw_stream(stream, t) -> int:
-    if stream is None:
-        import torch
-        return torch._C._cuda_getCurrentRawStream(t.get_device()) if t.is_cuda else 0
-    return int(stream.cuda_stream) if hasattr(stream, "cuda_stream") else int(stream)
+def _raw_stream(stream):
+    """None (the current stream of the call's device), a stream object or a raw handle."""
+    return stream if stream is None else int(getattr(stream, "cuda_stream", stream))
 
 
 @dataclass
@@ -602,13 +599,7 @@ def rope_frequencies(rotary_dim: int, base: float = 10000.0, scaling: int = AQ_R
 def aq_rope(rope: Rope, pos, x, inverse: bool = False, y=None, stream=None):
     """x [T, heads, head_dim] (bf16, any token and head strides) rotated at positions pos (int32 [T]);
     ``inverse`` turns back, which is the gradient of the rotation. y may be x."""
-    if y is None:
-        import torch
-        y = torch.empty_like(x)
-    st = _serve().rope(rope, pos, x, y, inverse, _raw_stream(stream, x))
-    if st:
-        _check(st)
-    return y
+    return _serve().rope(rope, pos, x, y, inverse, _raw_stream(stream))
 
 
 @dataclass
@@ -638,37 +629,18 @@ def aq_kv_write(cache: KvCache, k, v, slots, rope: Rope | None = None, pos=None,
     """Writes k and v [T, kv_heads, head_dim] into the cache's slots (int64 [T]), rotating k with
     ``rope`` at ``pos``. With q [T, q_heads, head_dim] the rotated queries are returned too (into q_out,
     which may be q)."""
-    if q is not None and q_out is None:
-        import torch
-        q_out = torch.empty_like(q)
-    st = _serve().kv_write(cache, k, v, slots, rope, pos, q, q_out, _raw_stream(stream, k))
-    if st:
-        _check(st)
-    return q_out
+    return _serve().kv_write(cache, k, v, slots, rope, pos, q, q_out, _raw_stream(stream))
 
 
 def aq_kv_read(cache: KvCache, slots, k=None, v=None, stream=None):
     """The tokens in the cache's slots (int64 [T]) as bf16: (k, v), each [T, kv_heads, head_dim]."""
-    if k is None or v is None:
-        import torch
-        if k is None:
-            _, heads, _, dim = cache.k.shape
-            k = torch.empty(slots.shape[0], heads, dim, dtype=torch.bfloat16, device=slots.device)
-        if v is None:
-            v = torch.empty_like(k)
-    st = _serve().kv_read(cache, slots, k, v, _raw_stream(stream, k))
-    if st:
-        _check(st)
-    return k, v
+    return _serve().kv_read(cache, slots, k, v, _raw_stream(stream))
 
 
 def aq_tree_attention_workspace_bytes(cache: KvCache, q_heads: int, batch: int, max_q: int, total_q: int) -> int:
     """Bytes of device workspace of aq_tree_attention for `batch` sequences that bring at most max_q rows
     each and total_q in all."""
-    need = _serve().attention_bytes(cache, q_heads, batch, max_q, total_q)
-    if need < 0:
-        raise AqError(AQ_ERR_INVALID_ARG, aq_last_error())
-    return need
+    return _serve().attention_bytes(cache, q_heads, batch, max_q, total_q)
 
 
 def aq_tree_attention(cache: KvCache, q, cu_q, ctx, page_table, max_q: int, mask=None, depth=None, window: int = 0,
@@ -679,20 +651,8 @@ def aq_tree_attention(cache: KvCache, q, cu_q, ctx, page_table, max_q: int, mask
     ceil(max_q / 64)] (bit j of a row: drafted token j of its sequence is seen; None: a chain), depth int32
     [total_q]. Returns out, or (out, lse [total_q, q_heads] fp32) with ``return_lse``. A workspace that is
     not given is allocated (its size: ``aq_tree_attention_workspace_bytes``)."""
-    import torch
-    total, heads, dim = q.shape
-    if out is None:
-        out = torch.empty_like(q)
-    if lse is None and return_lse:
-        lse = torch.empty(total, heads, dtype=torch.float32, device=q.device)
-    if workspace is None:
-        need = aq_tree_attention_workspace_bytes(cache, heads, page_table.shape[0], max_q, total)
-        workspace = torch.empty(need, dtype=torch.uint8, device=q.device) if need else None
-    st = _serve().attention(cache, q, cu_q, ctx, page_table, max_q, mask, depth, window, dim ** -0.5 if scale is None else scale,
-                            out, lse, workspace, _raw_stream(stream, q))
-    if st:
-        _check(st)
-    return (out, lse) if return_lse else out
+    return _serve().attention(cache, q, cu_q, ctx, page_table, max_q, mask, depth, window, scale, out, lse, return_lse, workspace,
+                              _raw_stream(stream))
 
 
 def aq_verify_drafts(p, tokens, cu, u, noise, q=None, parent=None, path_cap: int | None = None,
@@ -700,14 +660,4 @@ def aq_verify_drafts(p, tokens, cu, u, noise, q=None, parent=None, path_cap: int
     """Accepted drafts and the next token of each sequence: (n_accepted [batch], path [batch, path_cap],
     token [batch]), all int32. p (and q): [nodes + batch, vocab] fp32 or bf16; tokens, parent int32 [nodes]; cu
     int32 [batch + 1]; u fp32 [nodes]; noise fp32 [batch, vocab]. path_cap and max_nodes default to nodes."""
-    import torch
-    nodes, batch = tokens.shape[0], cu.shape[0] - 1
-    path_cap = min(nodes, AQ_MAX_DRAFT_NODES) if path_cap is None else path_cap
-    max_nodes = min(nodes, AQ_MAX_DRAFT_NODES) if max_nodes is None else max_nodes
-    path = torch.empty(batch, path_cap, dtype=torch.int32, device=p.device)
-    n_accepted = torch.empty(batch, dtype=torch.int32, device=p.device)
-    token = torch.empty_like(n_accepted)
-    st = _serve().verify(p, tokens, cu, u, noise, q, parent, path_cap, max_nodes, n_accepted, path, token, _raw_stream(stream, p))
-    if st:
-        _check(st)
-    return n_accepted, path, token
+    return _serve().verify(p, tokens, cu, u, noise, q, parent, path_cap, max_nodes, _raw_stream(stream))

@@ -27,8 +27,8 @@ SOURCES = ["aq_kernels.cu", "aq_decode.cu", "aq_decode2.cu", "aq_decompose.cu", 
            "aq_verify.cu"]
 HEADERS = ["aq_ptx.cuh", "aq_internal.h", "aq_serve.h", "aq_attention.cuh"]
 
-# The serving calls' marshalling, a CPython module of host code (see csrc/aq_python.c).
-MARSHAL_SOURCE = "aq_python.c"
+# The serving calls' marshalling, a CPython module of host code over torch tensors (see csrc/aq_python.cpp).
+MARSHAL_SOURCE = "aq_python.cpp"
 MARSHAL_PATH = os.path.join(PKG_DIR, "_marshal.so")
 
 ARCH_FLAGS = ["-gencode", "arch=compute_103a,code=sm_103a"]
@@ -58,13 +58,19 @@ def up_to_date(lib: str = LIB_PATH) -> bool:
 
 
 def build_marshal(verbose: bool = False) -> str:
-    """Compile the marshalling module with the host compiler (needs Python.h)."""
+    """Compile the marshalling module with the host compiler (needs Python.h and torch's headers)."""
+    import torch
     include = sysconfig.get_paths()["include"]
-    if not os.path.exists(os.path.join(include, "Python.h")):
-        raise RuntimeError(f"{include}/Python.h not found: the Python headers are required to build {MARSHAL_PATH}")
+    torch_dir = os.path.dirname(os.path.abspath(torch.__file__))
+    for need in (os.path.join(include, "Python.h"), os.path.join(torch_dir, "include", "torch", "csrc", "Exceptions.h")):
+        if not os.path.exists(need):
+            raise RuntimeError(f"{need} not found: the headers are required to build {MARSHAL_PATH}")
+    cuda = os.path.join(os.path.dirname(os.path.dirname(os.path.realpath(nvcc_path()))), "include")
     tmp = MARSHAL_PATH + f".{os.getpid()}.tmp"
-    cmd = [os.environ.get("CC") or shutil.which("gcc") or "cc", "-O2", "-shared", "-fPIC", "-fvisibility=hidden", f"-I{include}",
-           f"-I{INCLUDE}", os.path.join(CSRC, MARSHAL_SOURCE), "-o", tmp]
+    cmd = [os.environ.get("CXX") or shutil.which("g++") or "c++", "-std=c++17", "-O2", "-shared", "-fPIC", "-fvisibility=hidden",
+           f"-D_GLIBCXX_USE_CXX11_ABI={int(torch._C._GLIBCXX_USE_CXX11_ABI)}", f"-I{include}", f"-I{INCLUDE}",
+           *(f"-isystem{d}" for d in (os.path.join(torch_dir, "include"), os.path.join(torch_dir, "include", "torch", "csrc", "api", "include"), cuda)),
+           os.path.join(CSRC, MARSHAL_SOURCE), "-o", tmp, f"-L{os.path.join(torch_dir, 'lib')}", "-lc10", "-lc10_cuda", "-ltorch_cpu", "-ltorch_python"]
     if verbose:
         print(" ".join(cmd), file=sys.stderr)
     r = subprocess.run(cmd, stdout=subprocess.PIPE, stderr=subprocess.STDOUT)
