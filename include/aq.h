@@ -473,7 +473,9 @@ aq_status aq_kv_read(const aq_kv_cache* cache, const int64_t* slots, int64_t T, 
  * A row that sees nothing (or whose scores are all minus infinity) gives zeros and lse = -inf. Masked
  * keys and values take no part, whatever they hold. Softmax and sums are held in fp32. With a bf16 cache
  * the weights enter the second product in bf16; with E4M3 they and the queries enter as f16, scaled by
- * powers of two (query elements below 2^-28 of their head's largest, and weights below 2^-38, lose bits).
+ * powers of two: query elements below 2^-28 of their head's largest lose bits, and so do weights that, times
+ * their value's scale (one below 2^-64 counts as that), lie below 2^-22 of the row's largest; below 2^-32
+ * they are dropped.
  *   lse  fp32 [total_q, q_heads], log of the sum of exp(score), or NULL
  * Left out: keys past pages_per_seq pages, keys in pages outside the cache, rows past max_q of a
  * sequence or outside [0, total_q). Needs head_dim 64, 128 or 256 (AQ_ERR_UNSUPPORTED otherwise).

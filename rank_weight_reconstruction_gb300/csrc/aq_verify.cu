@@ -12,7 +12,9 @@
 // of the vocabulary in fp32. A thread-block cluster takes one sequence: every CTA makes the (short) walk by
 // itself from the same few gathered values, passes over its slices of the vocabulary, and the CTAs exchange
 // their maxima (packed value and index, so the order does not matter and the lowest index wins) through
-// distributed shared memory: one launch, no workspace. Only a refused child that has siblings left, with
+// distributed shared memory: one launch, no workspace. Measured on 262144 words: one sequence of 5 in fp32 7.6 us, 48
+// with sampled drafts 25.3 us (5970 GB/s); 48 trees of 12 in bf16 20.7 us (3650 GB/s: there the walk and the exchange, about
+// 8 us, weigh as much as the 75 MB). Only a refused child that has siblings left, with
 // q given, needs a normaliser in between: one more pass, its partial sums added in rank order by every CTA.
 #include <atomic>
 #include <type_traits>
@@ -22,10 +24,10 @@
 namespace aq {
 namespace {
 
-// Threads of a CTA: 1024 in clusters of 16 for a few sequences (each loads its rows in one or two rounds; measured on
-// 262144 words, one sequence: 11.0 us against 17.7 with 256 threads; eight: 17.8 against 10.9, as few such clusters fit at
-// once), else 256, three CTAs an SM (80 registers: with four, the rows of q spill: 61 us for 48 sequences against 41).
-constexpr int kVerWide = 1024, kVerNarrow = 256, kVerPerSm = 3, kVerWideBatch = 4;
+// Three CTAs of 256 threads an SM (80 registers: with four, the rows of q spill: 61 us for 48 sequences against 41 at the
+// time). CTAs of 1024 threads take one to four sequences no faster (7.6 and 8.1 us against 7.6 and 8.0 on 262144 words of
+// fp32 p) and eight slower (15.1 against 8.7): as few such clusters fit at once.
+constexpr int kVerThreads = 256, kVerPerSm = 3;
 constexpr int kVerMaxCluster = 16;
 
 struct VerifyParams {
@@ -104,8 +106,8 @@ struct VerShared {
   int32_t parent[AQ_MAX_DRAFT_NODES], tok[AQ_MAX_DRAFT_NODES], gone[AQ_MAX_DRAFT_NODES];
   unsigned long long best[2][kVerMaxCluster];
   float sum[2][kVerMaxCluster];
-  unsigned long long wbest[kVerWide / 32];
-  float wsum[kVerWide / 32];
+  unsigned long long wbest[kVerThreads / 32];
+  float wsum[kVerThreads / 32];
   int32_t cur, refused, next, count, done;
 };
 
@@ -114,7 +116,7 @@ struct VerShared {
 enum Draw { kPlain, kOnce, kSeveral };
 
 // Largest r(v) / E(v) of this CTA's share of the vocabulary, N words at a time.
-template <typename T, Draw MODE, int N, int kVerThreads>
+template <typename T, Draw MODE, int N>
 __device__ __forceinline__ void race(const T* pr, const T* qr, const float* er, int vocab, int k, const VerShared& sh,
                                      int rank, int cluster, float& best, int& at) {
   // A quotient can pass the warp's best so far only if w > best e (1 - 2^-21), rounding included: one product and
@@ -171,8 +173,8 @@ __device__ __forceinline__ void race(const T* pr, const T* qr, const float* er, 
     }
 }
 
-template <typename T, bool HASQ, int kVerThreads>
-__global__ void __launch_bounds__(kVerThreads, kVerThreads == kVerWide ? 1 : kVerPerSm) aq_verify_kernel(const __grid_constant__ VerifyParams p) {
+template <typename T, bool HASQ>
+__global__ void __launch_bounds__(kVerThreads, kVerPerSm) aq_verify_kernel(const __grid_constant__ VerifyParams p) {
   __shared__ VerShared sh;
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
   const int C = p.cluster;
@@ -315,8 +317,8 @@ __global__ void __launch_bounds__(kVerThreads, kVerThreads == kVerWide ? 1 : kVe
     // with q, k counts refusals of the residual; without, tokens that are left out
     auto pass_over = [&](auto mode) {
       constexpr Draw kMode = decltype(mode)::value;
-      if (whole) race<T, kMode, kVec, kVerThreads>(pr, qr, er, p.vocab, k, sh, rank, C, best, at);
-      else race<T, kMode, 1, kVerThreads>(pr, qr, er, p.vocab, k, sh, rank, C, best, at);
+      if (whole) race<T, kMode, kVec>(pr, qr, er, p.vocab, k, sh, rank, C, best, at);
+      else race<T, kMode, 1>(pr, qr, er, p.vocab, k, sh, rank, C, best, at);
     };
     if (!HASQ || k == 0) pass_over(std::integral_constant<Draw, kPlain>());
     else if (k == 1) pass_over(std::integral_constant<Draw, kOnce>());
@@ -352,19 +354,15 @@ __global__ void __launch_bounds__(kVerThreads, kVerThreads == kVerWide ? 1 : kVe
   }
 }
 
-template <typename T, bool HASQ, int THREADS>
+template <typename T, bool HASQ>
 cudaError_t launch_verify(const VerifyParams& p, unsigned grid, cudaStream_t st) {
   static std::atomic<uint64_t> ready{0};   // devices on which the kernel may use clusters of 16
   if (p.cluster > 8 && !(ready.load() >> p.device & 1)) {
-    const cudaError_t e = cudaFuncSetAttribute(aq_verify_kernel<T, HASQ, THREADS>, cudaFuncAttributeNonPortableClusterSizeAllowed, 1);
+    const cudaError_t e = cudaFuncSetAttribute(aq_verify_kernel<T, HASQ>, cudaFuncAttributeNonPortableClusterSizeAllowed, 1);
     if (e != cudaSuccess) return e;
     ready.fetch_or(1ull << p.device);
   }
-  return launch_serve(aq_verify_kernel<T, HASQ, THREADS>, p, grid, THREADS, 0, st, p.cluster);
-}
-template <typename T, bool HASQ>
-cudaError_t launch_verify(const VerifyParams& p, unsigned grid, bool wide, cudaStream_t st) {
-  return wide ? launch_verify<T, HASQ, kVerWide>(p, grid, st) : launch_verify<T, HASQ, kVerNarrow>(p, grid, st);
+  return launch_serve(aq_verify_kernel<T, HASQ>, p, grid, kVerThreads, 0, st, p.cluster);
 }
 
 }  // namespace
@@ -435,10 +433,8 @@ extern "C" aq_status aq_verify_drafts(int32_t batch, int32_t vocab, const int32_
   v.path_cap = path_cap;
   // the largest cluster that keeps the launch within the CTAs that are resident at once and gives every CTA at
   // least one round of its threads
-  const bool wide = batch <= kVerWideBatch;
-  const int threads = wide ? kVerWide : kVerNarrow;
   int c = kVerMaxCluster;
-  while (c > 1 && (static_cast<int64_t>(batch) * c > (wide ? 1 : kVerPerSm) * dev.sms || vocab < c * threads)) c /= 2;
+  while (c > 1 && (static_cast<int64_t>(batch) * c > kVerPerSm * dev.sms || vocab < c * kVerThreads)) c /= 2;
   v.cluster = c;
   v.device = dev.index;
   if (static_cast<int64_t>(batch) * c > 0x7fffffffLL) return serve_fail(AQ_ERR_SHAPE, "%s: batch=%d is too large", who, batch);
@@ -446,8 +442,8 @@ extern "C" aq_status aq_verify_drafts(int32_t batch, int32_t vocab, const int32_
   const cudaStream_t cs = static_cast<cudaStream_t>(stream);
   cudaError_t e;
   if (p_type == AQ_PROB_F32)
-    e = q ? launch_verify<float, true>(v, grid, wide, cs) : launch_verify<float, false>(v, grid, wide, cs);
+    e = q ? launch_verify<float, true>(v, grid, cs) : launch_verify<float, false>(v, grid, cs);
   else
-    e = q ? launch_verify<uint16_t, true>(v, grid, wide, cs) : launch_verify<uint16_t, false>(v, grid, wide, cs);
+    e = q ? launch_verify<uint16_t, true>(v, grid, cs) : launch_verify<uint16_t, false>(v, grid, cs);
   return serve_launched(e, who);
 }
