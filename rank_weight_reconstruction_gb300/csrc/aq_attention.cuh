@@ -286,9 +286,11 @@ struct Walk {
 };
 
 // The `count` <= 32 keys from ka on (place k0 of the tile) that a row sees, as bits; i: its drafted index, pos: its
-// position. Called by whole warps, each lane for a row of its own. One round of loads, whatever the mask.
+// position; word(w): word w of the row's mask. Called by whole warps, each lane for a row of its own. One round of loads,
+// whatever the mask.
+template <class Word>
 __device__ __forceinline__ uint32_t seen_bits(const AttnParams& p, const KeySpan& s, int i, int64_t pos, int64_t ka, int k0,
-                                              int count, uint32_t pages, int box_shift) {
+                                              int count, uint32_t pages, int box_shift, Word&& word) {
   const int lane = threadIdx.x & 31;
   auto below = [](int64_t n) { return n <= 0 ? 0u : n >= 32 ? 0xffffffffu : (1u << n) - 1; };   // bits [0, n)
   uint32_t bits = below(s.hi - ka) & below(count);
@@ -299,10 +301,9 @@ __device__ __forceinline__ uint32_t seen_bits(const AttnParams& p, const KeySpan
   if (drafted) {
     uint32_t see;
     if (p.mask) {
-      const uint64_t* m = p.mask + (static_cast<int64_t>(s.first) + i) * p.ld_mask;
       const int64_t at = max(t0, static_cast<int64_t>(0));
       const int last = (s.T - 1) >> 6, w0 = min(static_cast<int>(min(at >> 6, static_cast<int64_t>(last))), last), w1 = min(w0 + 1, last);
-      const uint64_t lo = m[w0], hi = m[w1];
+      const uint64_t lo = word(w0), hi = word(w1);
       const int sh0 = static_cast<int>(at & 63);
       const uint64_t v = sh0 ? (lo >> sh0) | (hi << (64 - sh0)) : lo;
       see = t0 < 0 ? static_cast<uint32_t>(v) << static_cast<int>(-t0) : static_cast<uint32_t>(v);
@@ -326,6 +327,14 @@ __device__ __forceinline__ uint32_t seen_bits(const AttnParams& p, const KeySpan
     }
   }
   return bits;
+}
+
+__device__ __forceinline__ const uint64_t* mask_row(const AttnParams& p, const KeySpan& s, int i) {
+  return p.mask + (static_cast<int64_t>(s.first) + i) * p.ld_mask;
+}
+__device__ __forceinline__ uint32_t seen_bits(const AttnParams& p, const KeySpan& s, int i, int64_t pos, int64_t ka, int k0,
+                                              int count, uint32_t pages, int box_shift) {
+  return seen_bits(p, s, i, pos, ka, k0, count, pages, box_shift, [&](int w) { return mask_row(p, s, i)[w]; });
 }
 
 }  // namespace aq

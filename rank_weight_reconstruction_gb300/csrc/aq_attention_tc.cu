@@ -641,9 +641,22 @@ __device__ __forceinline__ void tc_weigh(const AttnParams& p, TcShared& sh, uint
       const float4* ks = reinterpret_cast<const float4*>(scales + slot * 2 * BN * 4);
       const float4* vs = ks + BN / 4;
       uint32_t seen[BN / 32];   // of a tile that not every row sees in full; looked up while its scores form
-      if (live_warp && !whole)
+      if (live_warp && !whole) {
+        // the words of the row's mask that a tile can touch, in one round
+        static_assert(BN <= 128, "three words");
+        const int last = (w.s.T - 1) >> 6;
+        const int first = static_cast<int>(min(max(ka - w.s.ctx, static_cast<int64_t>(0)) >> 6, static_cast<int64_t>(last)));
+        uint64_t word[3] = {0, 0, 0};
+        if (p.mask && ka + BN > w.s.ctx) {
+          const uint64_t* row = mask_row(p, w.s, i_row);
+#pragma unroll
+          for (int k = 0; k < 3; ++k) word[k] = row[min(first + k, last)];
+        }
 #pragma unroll 1
-        for (int c = 0; c < BN / 32; ++c) seen[c] = seen_bits(p, w.s, i_row, pos, ka + 32 * c, 32 * c, 32, pages, box_shift);
+        for (int c = 0; c < BN / 32; ++c)
+          seen[c] = seen_bits(p, w.s, i_row, pos, ka + 32 * c, 32 * c, 32, pages, box_shift,
+                              [&](int k) { return k <= first ? word[0] : k == first + 1 ? word[1] : word[2]; });
+      }
       if (!wait(&sh.s_full[x], x_parity)) return;
       tc_fence_after();
       auto tile_scale = [&]() {   // the tile's largest scale of a value; a NaN counts as the largest: every row sees it and is NaN
@@ -736,12 +749,21 @@ __device__ __forceinline__ void tc_weigh(const AttnParams& p, TcShared& sh, uint
             const uint32_t bits = seen[c];
             float v[32];
             tmem_ld32(s_addr + 32 * c, v);
-            const float* kf = reinterpret_cast<const float*>(ks) + 32 * c;
-            const float* vf = reinterpret_cast<const float*>(vs) + 32 * c;
 #pragma unroll
-            for (int e = 0; e < 32; ++e) {
-              const float y = S::E4M3 ? v[e] * kf[e] : v[e];
-              if (((bits >> e) & 1) && y != -INFINITY) want = fmaxf(want, fmaf(y, fac, S::E4M3 ? scale_exponent(vf[e]) - kTop : 0.0f));
+            for (int e = 0; e < 32; e += 4) {   // without branches: what a masked key's scales hold is selected away
+              float4 kf = make_float4(1.0f, 1.0f, 1.0f, 1.0f), vf = kf;
+              if constexpr (S::E4M3) {
+                kf = ks[8 * c + e / 4];
+                vf = vs[8 * c + e / 4];
+              }
+              const float k4[4] = {kf.x, kf.y, kf.z, kf.w}, v4[4] = {vf.x, vf.y, vf.z, vf.w};
+#pragma unroll
+              for (int k = 0; k < 4; ++k) {
+                const float y = S::E4M3 ? v[e + k] * k4[k] : v[e + k];
+                const float z = fmaf(y, fac, S::E4M3 ? scale_exponent(v4[k]) - kTop : 0.0f);
+                const bool in = ((bits >> (e + k)) & 1) != 0 & (y != -INFINITY);
+                want = fmaxf(want, in ? z : -INFINITY);
+              }
             }
           }
         }
@@ -806,20 +828,33 @@ __device__ __forceinline__ void tc_weigh(const AttnParams& p, TcShared& sh, uint
         if (r == 0) sh.special[t][tile & 1] = 0;
         if (!meet()) return;
         bool special = false;
+        constexpr int kLook = 8;   // chunks looked at together
 #pragma unroll 1
-        for (int e = r; e < BN * D / 8; e += kGroup) {
-          const int key = e / (D / 8), c = e % (D / 8);
-          const uint32_t at = tile_addr(vb, BN, key, c);
-          uint32_t q[4];
-          asm volatile("ld.shared.v4.u32 {%0, %1, %2, %3}, [%4];" : "=r"(q[0]), "=r"(q[1]), "=r"(q[2]), "=r"(q[3]) : "r"(at) : "memory");
-          const uint32_t exp = S::E4M3 ? 0x7c007c00u : 0x7f807f80u;
-          uint32_t odd = 0;
+        for (int e0 = r; e0 < BN * D / 8; e0 += kLook * kGroup) {
+          uint32_t q[kLook][4];
 #pragma unroll
-          for (int k = 0; k < 4; ++k) odd |= __vcmpeq2(q[k] & exp, exp);
-          if (odd) {
+          for (int j = 0; j < kLook; ++j)
+            asm volatile("ld.shared.v4.u32 {%0, %1, %2, %3}, [%4];"
+                         : "=r"(q[j][0]), "=r"(q[j][1]), "=r"(q[j][2]), "=r"(q[j][3])
+                         : "r"(tile_addr(vb, BN, (e0 + j * kGroup) / (D / 8), (e0 + j * kGroup) % (D / 8)))
+                         : "memory");
+          uint32_t odd[kLook], any = 0;
+          const uint32_t exp = S::E4M3 ? 0x7c007c00u : 0x7f807f80u;
+#pragma unroll
+          for (int j = 0; j < kLook; ++j) {
+            odd[j] = 0;
+#pragma unroll
+            for (int k = 0; k < 4; ++k) odd[j] |= __vcmpeq2(q[j][k] & exp, exp);
+            any |= odd[j];
+          }
+          if (!any) continue;
+#pragma unroll
+          for (int j = 0; j < kLook; ++j) {
+            if (!odd[j]) continue;
+            const int key = (e0 + j * kGroup) / (D / 8), c = (e0 + j * kGroup) % (D / 8);
             const int64_t kk = ka + key;
             if (kk < w.s.lo || kk >= w.s.hi || !((pages >> (key >> box_shift)) & 1))
-              asm volatile("st.shared.v4.u32 [%0], {%1, %1, %1, %1};" ::"r"(at), "r"(0) : "memory");
+              asm volatile("st.shared.v4.u32 [%0], {%1, %1, %1, %1};" ::"r"(tile_addr(vb, BN, key, c)), "r"(0) : "memory");
             else
               special = true;
           }
