@@ -890,9 +890,12 @@ __device__ __forceinline__ void tc_weigh(const AttnParams& p, TcShared& sh, uint
       // 32 columns at a time through the warp's own rows of the query buffer (their last product is done), so that the
       // stores leave in whole lines: row-wise in, swizzled by 16 bytes, four rows of eight chunks out
       const uint32_t stage = smem_u32(qbuf) + (t * 128 + wq * 32) * D * 2;
-      // where this lane's chunk of a row goes: the row's own place, kept by its lane
-      int64_t place = complete ? out_row * p.o_tok + head * p.o_head : at * D;
-      const int q = lane & 7;
+      // where this lane's chunk of rows 4 k + lane / 8 goes: the row's own place, known to its lane
+      const int64_t place = complete ? out_row * p.o_tok + head * p.o_head : at * D;
+      const int q = lane & 7, below = count - (lane >> 3);   // row 4 k + lane / 8 is one of the warp's: 4 k < below
+      int64_t to[8];
+#pragma unroll
+      for (int k = 0; k < 8; ++k) to[k] = __shfl_sync(0xffffffffu, place, 4 * k + (lane >> 3)) + 4 * q;
 #pragma unroll 1
       for (int d = 0; d < D; d += 32) {
         float v[32];
@@ -905,21 +908,23 @@ __device__ __forceinline__ void tc_weigh(const AttnParams& p, TcShared& sh, uint
                        : "memory");
         __syncwarp();
         float4 f[8];
-        int64_t to[8];
 #pragma unroll
         for (int k = 0; k < 8; ++k) {
           const int lr = 4 * k + (lane >> 3);
-          to[k] = __shfl_sync(0xffffffffu, place, lr) + d + 4 * q;
           asm volatile("ld.shared.v4.f32 {%0, %1, %2, %3}, [%4];"
                        : "=f"(f[k].x), "=f"(f[k].y), "=f"(f[k].z), "=f"(f[k].w)
                        : "r"(stage + lr * 128 + ((q ^ (lr & 7)) << 4))
                        : "memory");
         }
+        // one branch for all stores: one at each cost 500 clocks a round
+        if (complete) {
 #pragma unroll
-        for (int k = 0; k < 8; ++k) {
-          if (4 * k + (lane >> 3) >= count) continue;
-          if (complete) *reinterpret_cast<uint2*>(p.o + to[k]) = make_uint2(pack_bf16x2_cvt(f[k].x, f[k].y), pack_bf16x2_cvt(f[k].z, f[k].w));
-          else *reinterpret_cast<float4*>(p.part_o + to[k]) = f[k];
+          for (int k = 0; k < 8; ++k)
+            if (4 * k < below) *reinterpret_cast<uint2*>(p.o + to[k] + d) = make_uint2(pack_bf16x2_cvt(f[k].x, f[k].y), pack_bf16x2_cvt(f[k].z, f[k].w));
+        } else {
+#pragma unroll
+          for (int k = 0; k < 8; ++k)
+            if (4 * k < below) *reinterpret_cast<float4*>(p.part_o + to[k] + d) = f[k];
         }
         __syncwarp();
       }
