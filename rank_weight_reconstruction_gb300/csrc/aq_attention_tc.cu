@@ -582,17 +582,21 @@ __device__ __forceinline__ void tc_weigh(const AttnParams& p, TcShared& sh, uint
         v[k] = *reinterpret_cast<const uint4*>(query(min(row0 + 4 * ((k0 + k) * RPW + lane / L), rows - 1)));
       uint32_t top_bits[kBatch];
       if constexpr (S::E4M3) {
-        const uint32_t who = (L == 32 ? 0xffffffffu : (1u << L) - 1) << (lane & ~(L - 1));
 #pragma unroll
         for (int k = 0; k < kBatch; ++k) {
           const uint32_t m16 = 0x7fff0000u;
           top_bits[k] = max(max(max((v[k].x << 16) & m16, v[k].x & m16), max((v[k].y << 16) & m16, v[k].y & m16)),
                             max(max((v[k].z << 16) & m16, v[k].z & m16), max((v[k].w << 16) & m16, v[k].w & m16)));
         }
+        if constexpr (L == 32) {
 #pragma unroll
-        for (int off = L / 2; off > 0; off >>= 1)
+          for (int k = 0; k < kBatch; ++k) top_bits[k] = __reduce_max_sync(0xffffffffu, top_bits[k]);
+        } else {
 #pragma unroll
-          for (int k = 0; k < kBatch; ++k) top_bits[k] = max(top_bits[k], __shfl_xor_sync(who, top_bits[k], off));
+          for (int off = L / 2; off > 0; off >>= 1)
+#pragma unroll
+            for (int k = 0; k < kBatch; ++k) top_bits[k] = max(top_bits[k], __shfl_xor_sync(0xffffffffu, top_bits[k], off));
+        }
       }
 #pragma unroll
       for (int k = 0; k < kBatch; ++k) {
@@ -603,8 +607,11 @@ __device__ __forceinline__ void tc_weigh(const AttnParams& p, TcShared& sh, uint
           const int e = finite ? top_exponent(__uint_as_float(top_bits[k])) : 0;
           const float f = pow2(14 - e);
 #pragma unroll
-          for (int y = 0; y < 4; ++y)
-            x[y] = finite ? pack_f16x2(__uint_as_float(x[y] << 16) * f, __uint_as_float(x[y] & 0xffff0000u) * f) : 0u;
+          for (int y = 0; y < 4; ++y) {
+            float lo, hi;
+            fmul2_rn(lo, hi, __uint_as_float(x[y] << 16), __uint_as_float(x[y] & 0xffff0000u), f, f);
+            x[y] = finite ? pack_f16x2(lo, hi) : 0u;
+          }
           if (c == 0) sh.fac[t * 128 + lr] = finite ? pow2(e - 14) * fabsf(scale2) : __uint_as_float(0x7fc00000u);   // NaN: no finite score
         }
         asm volatile("st.shared.v4.u32 [%0], {%1, %2, %3, %4};" ::"r"(tile_addr(smem_u32(qbuf) + t * 128 * D * 2, 128, lr, c)), "r"(x[0]),
