@@ -210,7 +210,8 @@ __device__ __forceinline__ void rotate16(float (&a)[8], float (&b)[8], const flo
 }
 
 // GW lanes per vector (a power of two, >= D / 16).
-// SPLIT: the groups of a warp are at one token.
+// SPLIT: the groups of a warp are at one token. Four blocks an SM: a rotation of 8192 tokens takes 19.1 us, with three
+// blocks 21.7, with five 25.3; the next heads' loads under these heads' work 20.6 (three) and 23.1 (four).
 template <bool HALF, int GW, bool E4M3, bool SPLIT>
 __global__ void __launch_bounds__(256, 4) aq_positions_kernel(const __grid_constant__ PosParams p) {
   pdl_wait_prior_grid();
