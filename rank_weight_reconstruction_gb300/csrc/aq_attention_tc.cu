@@ -17,8 +17,8 @@
 //
 // Measured, eight trees of 64 over 32768 keys, 32 query and 8 key/value heads (256 rows an item): D = 128 bf16 218 to 238 us
 // (1160 to 1260 TFLOP/s, 4550 to 4970 GB/s), of which about 190 are the stream at 3330 clocks a pair of 128-key tiles (the products
-// alone 2050), the rest starts, ends of items and the joining launch; E4M3 337 us (the widening lies between two products:
-// three f16 buffers are all that fits), D = 64 180, D = 256 645 (one row tile, and 64-key products that re-read Q).
+// alone 2050), the rest starts, ends of items and the joining launch; E4M3 307 to 313 us (every weighing
+// thread reads the scales of all keys from shared memory, 128 KB a row tile, beside the widening), D = 64 180, D = 256 645 (one row tile, and 64-key products that re-read Q).
 #include <math.h>
 
 #include <algorithm>
@@ -48,7 +48,10 @@ struct TcShape {
   static constexpr int kSoftWarps = 4 * TILES;
   static constexpr int kConvWarp = kSoftWarps;             // first of four converting warps (E4M3)
   static constexpr int kTmaWarp = kSoftWarps + (E4M3 ? 4 : 0), kMmaWarp = kTmaWarp + 1;
-  static constexpr int kThreads = (kMmaWarp + 1) * 32;
+  // Two row tiles of an E4M3 cache: 16 warps launched with 128 registers a thread, of which the weighing warps take a
+  // part from the others (256 x 176 + 128 x 88 + 128 x 72 = 65536 = 512 x 128): 307 to 313 us against 342 without.
+  static constexpr bool kSplitRegs = E4M3 && TILES == 2;
+  static constexpr int kThreads = kSplitRegs ? 512 : (kMmaWarp + 1) * 32;
   // tensor memory: two score buffers, one a row tile or two of one tile (the weights over them), then the sums
   static constexpr int kS(int x) { return x * 128; }
   static constexpr int kO(int t) { return 256 + t * D; }
@@ -989,22 +992,27 @@ __global__ void __launch_bounds__(S::kThreads, 1) aq_tree_attention_tc_kernel(co
   pdl_launch_dependents();   // the joining blocks find their rows meanwhile; they wait for this grid before its results
   const AbortCtl ctl = {&sh.abort, p.status, p.timeout_ns};
   if (warp < S::kSoftWarps) {
+    if (S::kSplitRegs) asm volatile("setmaxnreg.inc.sync.aligned.u32 176;");
     tc_weigh<S>(p, sh, qbuf, tiles, scales, nring, tmem, range, ctl);
-  } else if (warp == S::kTmaWarp) {
-    tc_produce<S>(p, sh, S::E4M3 ? codes : tiles, scales, p.stages, range, ctl);
-  } else if (warp == S::kMmaWarp) {
-    if (range[1] > range[0]) {
-      tc_issue<S>(p, sh, qbuf, tiles, nring, tmem, range, ctl);
-      // nothing is in flight when tensor memory is freed
-      __syncwarp();
-      if (elect_one()) tc_commit(&sh.drain);
-      const uint64_t t0 = global_timer_ns();
-      while (!mbar_try_wait(&sh.drain, 0))
-        if (global_timer_ns() - t0 > p.timeout_ns) break;
-    }
-    __syncwarp();
-  } else if (S::E4M3) {
+  } else if (S::E4M3 && warp < S::kTmaWarp) {
+    if (S::kSplitRegs) asm volatile("setmaxnreg.dec.sync.aligned.u32 88;");
     tc_convert<S>(sh, codes, tiles, p.stages, range[1] - range[0], ctl);
+  } else {
+    if (S::kSplitRegs) asm volatile("setmaxnreg.dec.sync.aligned.u32 72;");
+    if (warp == S::kTmaWarp) {
+      tc_produce<S>(p, sh, S::E4M3 ? codes : tiles, scales, p.stages, range, ctl);
+    } else if (warp == S::kMmaWarp) {
+      if (range[1] > range[0]) {
+        tc_issue<S>(p, sh, qbuf, tiles, nring, tmem, range, ctl);
+        // nothing is in flight when tensor memory is freed
+        __syncwarp();
+        if (elect_one()) tc_commit(&sh.drain);
+        const uint64_t t0 = global_timer_ns();
+        while (!mbar_try_wait(&sh.drain, 0))
+          if (global_timer_ns() - t0 > p.timeout_ns) break;
+      }
+      __syncwarp();
+    }
   }
   tc_fence_before();
   __syncthreads();
