@@ -850,7 +850,7 @@ __global__ void __launch_bounds__(128) aq_attention_join_kernel(const __grid_con
 // Rows of a tile: the fewest of 8, 16, 32 (mma.sync), 128, 256 (tcgen05; two tiles' sums of D = 256 do not fit tensor
 // memory) that hold a sequence's rows of one key/value head. Measured, 32 trees over 8192 keys on 32 query and 8 key/value
 // heads of 128, mma.sync against tcgen05: trees of 8 (32 rows) bf16 127 and 127 us, E4M3 120 and 186; trees of 16 (64
-// rows: two tiles of 32) bf16 245 and 140, E4M3 216 and 203.
+// rows: two tiles of 32) bf16 245 and 133, E4M3 216 and 197.
 int rows_per_tile(int64_t rows, int D) {
   return rows <= 8 ? 8 : rows <= 16 ? 16 : rows <= 32 ? 32 : rows <= 128 || D == 256 ? 128 : 256;
 }

@@ -17,8 +17,8 @@
 //
 // Measured, eight trees of 64 over 32768 keys, 32 query and 8 key/value heads (256 rows an item): D = 128 bf16 218 to 238 us
 // (1160 to 1260 TFLOP/s, 4550 to 4970 GB/s), of which about 190 are the stream at 3330 clocks a pair of 128-key tiles (the products
-// alone 2050), the rest starts, ends of items and the joining launch; E4M3 307 to 313 us (every weighing
-// thread reads the scales of all keys from shared memory, 128 KB a row tile, beside the widening), D = 64 180, D = 256 645 (one row tile, and 64-key products that re-read Q).
+// alone 2050), the rest starts, ends of items and the joining launch; E4M3 307 to 313 us (a scale
+// on every score and every weight, beside the widening's instructions), D = 64 177, D = 256 645 (one row tile, and 64-key products that re-read Q).
 #include <math.h>
 
 #include <algorithm>
