@@ -20,6 +20,8 @@
 #include <torch/csrc/Exceptions.h>
 #include <torch/csrc/autograd/python_variable.h>
 
+#include <optional>
+
 #include "aq.h"
 
 namespace {
@@ -35,6 +37,8 @@ PyObject* f_check;   // raises for a status that is not AQ_OK
 PyObject *s_freq, *s_layout, *s_magnitude, *s_k, *s_v, *s_k_scale, *s_v_scale;
 
 constexpr at::ScalarType kBf16 = at::kBFloat16, kF32 = at::kFloat, kI32 = at::kInt, kI64 = at::kLong, kU64 = at::kUInt64, kU8 = at::kByte;
+
+std::optional<c10::Device> call_device;   // of the tensors read so far in this call (the interpreter's lock is held)
 
 struct Tensor {
   int64_t shape[4] = {0, 0, 0, 0}, stride[4] = {0, 0, 0, 0};
@@ -67,6 +71,11 @@ bool read(PyObject* obj, const char* name, at::ScalarType a, at::ScalarType b, i
   }
   if (t.layout() != at::kStrided || t.dim() != nd) {
     PyErr_Format(PyExc_ValueError, "%s: expected a strided tensor of %d dimensions, got %d", name, nd, static_cast<int>(t.dim()));
+    return false;
+  }
+  if (!call_device) call_device = t.device();
+  if (*call_device != t.device()) {
+    PyErr_Format(PyExc_ValueError, "%s: on %s, the call's other tensors on %s", name, t.device().str().c_str(), call_device->str().c_str());
     return false;
   }
   take(t, x);
@@ -219,6 +228,7 @@ struct Cache {
 };
 
 bool want(Py_ssize_t got, Py_ssize_t n, const char* name) {
+  call_device.reset();
   if (got == n && f_check) return true;
   PyErr_Format(PyExc_TypeError, f_check ? "%s: wrong number of arguments" : "%s: bind() has not been called", name);
   return false;
@@ -238,6 +248,13 @@ bool ok(aq_status st) {
   if (st == AQ_OK) return true;
   Ref r(PyObject_CallFunction(f_check, "i", static_cast<int>(st)));
   if (r.o) PyErr_SetString(PyExc_RuntimeError, "the call was refused");
+  return false;
+}
+
+// The library takes device pointers: a host tensor's is not passed on.
+bool on_gpu() {
+  if (call_device && call_device->is_cuda()) return true;
+  PyErr_Format(PyExc_ValueError, "the tensors of a call must be on a CUDA device, not on %s", call_device ? call_device->str().c_str() : "none");
   return false;
 }
 
@@ -279,7 +296,7 @@ PyObject* py_rope(PyObject*, PyObject* const* a, Py_ssize_t n) {
     take(made, &y);
     if (!head_strides("y", &y)) return nullptr;
   }
-  if (!ok(f_rope(&r.spec, static_cast<const int32_t*>(pos.ptr), x.shape[0], small(x.shape[1]), small(x.shape[2]), x.ptr, x.stride[0], x.stride[1],
+  if (!on_gpu() || !ok(f_rope(&r.spec, static_cast<const int32_t*>(pos.ptr), x.shape[0], small(x.shape[1]), small(x.shape[2]), x.ptr, x.stride[0], x.stride[1],
                  y.ptr, y.stride[0], y.stride[1], inverse, st)))
     return nullptr;
   return made.defined() ? THPVariable_Wrap(std::move(made)) : given(a[3]);
@@ -307,7 +324,7 @@ PyObject* py_kv_write(PyObject*, PyObject* const* a, Py_ssize_t n) {
     take(made, &o);
     if (!head_strides("q_out", &o)) return nullptr;
   }
-  if (!ok(f_kv_write(&c.c, static_cast<const int64_t*>(slots.ptr), T, k.ptr, k.stride[0], k.stride[1], v.ptr, v.stride[0], v.stride[1],
+  if (!on_gpu() || !ok(f_kv_write(&c.c, static_cast<const int64_t*>(slots.ptr), T, k.ptr, k.stride[0], k.stride[1], v.ptr, v.stride[0], v.stride[1],
                      turned ? &r.spec : nullptr, static_cast<const int32_t*>(pos.ptr), q.ptr, small(q.shape[1]), q.stride[0], q.stride[1], o.ptr,
                      o.stride[0], o.stride[1], st)))
     return nullptr;
@@ -334,7 +351,7 @@ PyObject* py_kv_read(PyObject*, PyObject* const* a, Py_ssize_t n) {
       take(made[i], &x[i]);
       if (!head_strides(name[i], &x[i])) return nullptr;
     }
-  if (!ok(f_kv_read(&c.c, static_cast<const int64_t*>(slots.ptr), slots.shape[0], x[0].ptr, x[0].stride[0], x[0].stride[1], x[1].ptr, x[1].stride[0],
+  if (!on_gpu() || !ok(f_kv_read(&c.c, static_cast<const int64_t*>(slots.ptr), slots.shape[0], x[0].ptr, x[0].stride[0], x[0].stride[1], x[1].ptr, x[1].stride[0],
                     x[1].stride[1], st)))
     return nullptr;
   return pack({made[0].defined() ? THPVariable_Wrap(std::move(made[0])) : given(a[2]), made[1].defined() ? THPVariable_Wrap(std::move(made[1])) : given(a[3])});
@@ -421,7 +438,7 @@ PyObject* py_attention(PyObject*, PyObject* const* a, Py_ssize_t n) {
       take(made_ws, &ws);
     }
   }
-  if (!ok(f_attention(&c.c, &d, q.ptr, small(heads), q.stride[0], q.stride[1], static_cast<float>(scale), out.ptr, out.stride[0], out.stride[1],
+  if (!on_gpu() || !ok(f_attention(&c.c, &d, q.ptr, small(heads), q.stride[0], q.stride[1], static_cast<float>(scale), out.ptr, out.stride[0], out.stride[1],
                       static_cast<float*>(lse.ptr), ws.ptr, static_cast<size_t>(ws.shape[0]), st)))
     return nullptr;
   PyObject* o = made_out.defined() ? THPVariable_Wrap(std::move(made_out)) : given(a[10]);
@@ -465,7 +482,7 @@ PyObject* py_verify(PyObject*, PyObject* const* a, Py_ssize_t n) {
   take(made[0], &count);
   take(made[1], &path);
   take(made[2], &token);
-  if (!ok(f_verify(small(batch), small(vocab), static_cast<const int32_t*>(cu.ptr), static_cast<const int32_t*>(tokens.ptr),
+  if (!on_gpu() || !ok(f_verify(small(batch), small(vocab), static_cast<const int32_t*>(cu.ptr), static_cast<const int32_t*>(tokens.ptr),
                    static_cast<const int32_t*>(parent.ptr), nodes, most, p.ptr, p.stride[0], q.ptr, q.stride[0], p.shape[0],
                    dtype == kF32 ? AQ_PROB_F32 : AQ_PROB_BF16, static_cast<const float*>(u.ptr), static_cast<const float*>(noise.ptr), noise.stride[0],
                    static_cast<int32_t*>(count.ptr), static_cast<int32_t*>(path.ptr), cap, cap, static_cast<int32_t*>(token.ptr), st)))

@@ -209,3 +209,21 @@ def test_binding_checks_types_before_pointers():
     with pytest.raises(b.AqError):   # well-formed tensors on the host: refused by the library, not read
         b.aq_tree_attention(kv, torch.zeros(2, 3, 64, dtype=torch.bfloat16), torch.tensor([0, 2], dtype=torch.int32),
                             torch.tensor([1], dtype=torch.int32), torch.zeros(1, 2, dtype=torch.int32), max_q=2)
+
+
+def test_binding_passes_no_host_pointer_on():
+    torch = pytest.importorskip("torch")
+    x = torch.zeros(3, 2, 64, dtype=torch.bfloat16)
+    r = b.Rope(torch.zeros(32, dtype=torch.int64))
+    pos, slots = torch.zeros(3, dtype=torch.int32), torch.zeros(3, dtype=torch.int64)
+    kv = b.KvCache.empty(2, 16, 2, 64, b.AQ_KV_E4M3, device="cpu")
+    cu, one = torch.tensor([0, 3], dtype=torch.int32), torch.tensor([1], dtype=torch.int32)
+    calls = [lambda p: b.aq_rope(r, p, x), lambda p: b.aq_kv_write(kv, x, x, slots, rope=r, pos=p),
+             lambda p: b.aq_kv_read(kv, slots.to(p.device)),
+             lambda p: b.aq_tree_attention(kv, x, cu, one, torch.zeros(1, 2, dtype=torch.int32), max_q=3, depth=p),
+             lambda p: b.aq_verify_drafts(torch.zeros(4, 8), p, cu, torch.zeros(3), torch.ones(1, 8))]
+    for call in calls:
+        with pytest.raises(ValueError, match="CUDA device"):
+            call(pos)
+        with pytest.raises(ValueError, match="other tensors on"):   # of two devices
+            call(pos.to("meta"))
