@@ -176,11 +176,25 @@ constexpr uint32_t tc_idesc(bool f16, bool b_mn, int n) {
          (static_cast<uint32_t>(128 >> 4) << 24);
 }
 
-// Address of 16 bytes (eight elements from 8 c on) of a row of a 16-bit tile: column blocks of 64 elements, each
+// Byte offset of 16 bytes (eight elements from 8 c on) of a row of a 16-bit tile: column blocks of 64 elements, each
 // `rows` rows of 128 swizzled bytes.
-__device__ __forceinline__ uint32_t tile_addr(uint32_t base, int rows, int row, int c) {
-  return base + (c >> 3) * rows * 128 + row * 128 + (((c & 7) ^ (row & 7)) << 4);
+__host__ __device__ constexpr uint32_t tile_offset(int rows, int row, int c) {
+  return (c >> 3) * rows * 128 + row * 128 + (((c & 7) ^ (row & 7)) << 4);
 }
+__device__ __forceinline__ uint32_t tile_addr(uint32_t base, int rows, int row, int c) { return base + tile_offset(rows, row, c); }
+// Where the epilogue keeps 16 bytes (k of eight) of a row's sums on their way out: in the first column block of that row's
+// query, for any D. Nothing stands between one warp's epilogue and another's next queries, so a warp writes to its own rows alone.
+__host__ __device__ constexpr uint32_t stage_offset(int row, int k) { return tile_offset(128, row, k); }
+constexpr bool stages_in_own_rows() {
+  for (int row = 0; row < 128; ++row) {
+    for (int c = 0; c < 256 / 8; ++c)
+      if (((tile_offset(128, row, c) >> 7) & 127) != static_cast<uint32_t>(row)) return false;   // a query's bytes by their row
+    for (int k = 0; k < 8; ++k)
+      if (((stage_offset(row, k) >> 7) & 127) != static_cast<uint32_t>(row)) return false;
+  }
+  return true;
+}
+static_assert(stages_in_own_rows(), "the epilogue of one warp would meet another warp's queries");
 
 // Whether the phase with the given parity is complete, without waiting.
 __device__ __forceinline__ bool mbar_test(uint64_t* bar, uint32_t parity) {
@@ -899,7 +913,7 @@ __device__ __forceinline__ void tc_weigh(const AttnParams& p, TcShared& sh, uint
       const int64_t at = (static_cast<int64_t>(blockIdx.x) * 2 + slot) * S::M + t * 128 + 4 * lane + wq;
       // 32 columns at a time through the warp's own rows of the query buffer (their last product is done), so that the
       // stores leave in whole lines: row-wise in, swizzled by 16 bytes, four rows of eight chunks out
-      const uint32_t stage = smem_u32(qbuf) + (t * 128 + wq * 32) * D * 2;
+      const uint32_t stage = smem_u32(qbuf) + t * 128 * D * 2;
       // where this lane's chunk of rows 4 k + lane / 8 goes: the row's own place, known to its lane
       const int64_t place = complete ? out_row * p.o_tok + head * p.o_head : at * D;
       const int q = lane & 7, below = count - (lane >> 3);   // row 4 k + lane / 8 is one of the warp's: 4 k < below
@@ -912,7 +926,7 @@ __device__ __forceinline__ void tc_weigh(const AttnParams& p, TcShared& sh, uint
         tmem_ld32(tmem + lanes + S::kO(t) + d, v);
 #pragma unroll
         for (int k = 0; k < 8; ++k)
-          asm volatile("st.shared.v4.f32 [%0], {%1, %2, %3, %4};" ::"r"(stage + lane * 128 + ((k ^ (lane & 7)) << 4)),
+          asm volatile("st.shared.v4.f32 [%0], {%1, %2, %3, %4};" ::"r"(stage + stage_offset(r, k)),
                        "f"(none ? 0.0f : v[4 * k] * inv), "f"(none ? 0.0f : v[4 * k + 1] * inv), "f"(none ? 0.0f : v[4 * k + 2] * inv),
                        "f"(none ? 0.0f : v[4 * k + 3] * inv)
                        : "memory");
@@ -920,10 +934,10 @@ __device__ __forceinline__ void tc_weigh(const AttnParams& p, TcShared& sh, uint
         float4 f[8];
 #pragma unroll
         for (int k = 0; k < 8; ++k) {
-          const int lr = 4 * k + (lane >> 3);
+          const int lr = wq * 32 + 4 * k + (lane >> 3);
           asm volatile("ld.shared.v4.f32 {%0, %1, %2, %3}, [%4];"
                        : "=f"(f[k].x), "=f"(f[k].y), "=f"(f[k].z), "=f"(f[k].w)
-                       : "r"(stage + lr * 128 + ((q ^ (lr & 7)) << 4))
+                       : "r"(stage + stage_offset(lr, q))
                        : "memory");
         }
         // one branch for all stores: one at each cost 500 clocks a round
