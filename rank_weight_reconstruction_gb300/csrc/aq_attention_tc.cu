@@ -64,7 +64,7 @@ struct TcShared {
   uint64_t full[kMaxRing], empty[kMaxRing];     // 16-bit tiles: K of tile n is buffer use 2 n, V use 2 n + 1
   uint64_t cfull[kMaxRing], cempty[kMaxRing];   // codes
   uint64_t info[kInfo];                         // page mask and scales of a tile
-  uint64_t q_ready, s_full[2], p_ready[2], o_done[2], together[2], drain;
+  uint64_t q_ready, s_full[2], p_ready[2], o_done[2], item_done, together[2], drain;   // item_done: with one row tile
   uint32_t valid[kInfo];
   int32_t skip[2];                              // the product P V of this score buffer is done by the threads
   int32_t special[2][2];                        // [row tile][tile & 1]
@@ -491,6 +491,10 @@ __device__ __forceinline__ bool tc_issue(const AttnParams& p, TcShared& sh, cons
         if (!turn(kFirst, tile & 1, (tile >> 1) & 1, i == 0)) return false;
       }
     }
+    if (S::TILES == 1) {
+      if (elect_one()) tc_commit(&sh.item_done);
+      __syncwarp();
+    }
   }
 }
 
@@ -559,7 +563,7 @@ __device__ __forceinline__ void tc_weigh(const AttnParams& p, TcShared& sh, uint
   const float scale2 = p.scale * 1.4426950408889634f;
   const uint32_t sign = scale2 < 0.0f ? 0x80008000u : 0u;
   const uint32_t group = p.group;
-  uint32_t tile = 0, together = 0;     // tiles so far; uses of the group's own barrier
+  uint32_t tile = 0, item = 0, together = 0;     // tiles and items so far; uses of the group's own barrier
   Ring v_at(nring);                    // this tile's V
   bool ok = true;
   v_at.next();
@@ -574,7 +578,7 @@ __device__ __forceinline__ void tc_weigh(const AttnParams& p, TcShared& sh, uint
     return wait(&sh.together[t], together++ & 1);
   };
   Walk<S::M, BN> w(p, sh.work, range);
-  for (; w.left > 0; w.next(p)) {
+  for (; w.left > 0; w.next(p), ++item) {
     const int rt = w.rt;
     // Lane l of warp wq holds row 4 l + wq of the tile: a tile that is not full is spread over all four warps.
     const uint32_t rows = static_cast<uint32_t>(w.s.T) * group, row0 = static_cast<uint32_t>(rt) * S::M + t * 128 + wq;
@@ -900,8 +904,10 @@ __device__ __forceinline__ void tc_weigh(const AttnParams& p, TcShared& sh, uint
       __syncwarp();
       if (lane == 0) mbar_arrive(&sh.p_ready[x]);
     }
-    // the item's rows
-    if (!wait(&sh.o_done[t], (tile - 1) & 1)) return;
+    // The item's rows, behind its last sums. A parity tells a phase from the one before alone. With two row tiles a tile's scores
+    // are issued behind the sums of the tile before, so those were complete when the scores were. With one they are issued ahead
+    // of them: of the last two sums neither may be complete here, or both, and the item has a barrier of its own.
+    if (!(S::TILES == 2 ? wait(&sh.o_done[t], (tile - 1) & 1) : wait(&sh.item_done, item & 1))) return;
     tc_fence_after();
     if (live_warp) {
       const bool complete = w.n == w.len;
@@ -986,6 +992,7 @@ __global__ void __launch_bounds__(S::kThreads, 1) aq_tree_attention_tc_kernel(co
       mbar_init(&sh.together[i], 4);
       sh.skip[i] = 0;
     }
+    mbar_init(&sh.item_done, 1);
     mbar_init(&sh.drain, 1);
     sh.abort = 0;
     fence_barrier_init();

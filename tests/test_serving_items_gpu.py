@@ -26,6 +26,12 @@ DT = {"bf16": aq.AQ_KV_BF16, "e4m3": aq.AQ_KV_E4M3}
 KINDS = pytest.mark.parametrize("kind", ["bf16", "e4m3"])
 
 
+@pytest.fixture(autouse=True)
+def no_wait_ran_out():
+    yield
+    assert aq.aq_device_status() == aq.AQ_OK
+
+
 class Batch:
     """Sequences of ctx context and drafted tokens in a paged cache whose every unnamed cell is NaN."""
 
@@ -155,12 +161,13 @@ class Batch:
         return worst
 
 
-DIMS = pytest.mark.parametrize("D", [64, 128])
+DIMS = pytest.mark.parametrize("D", [64, 128, 256])
 
 
 @KINDS
 @DIMS
-@pytest.mark.parametrize("group,T", [(4, [1, 64, 33, 2])], ids=["two-tiles"])
+@pytest.mark.parametrize("group,T", [(2, [1, 64]), (2, [64, 1, 33, 2, 17, 64]), (4, [1, 64, 33, 2]), (3, [43, 1, 42])],
+                         ids=["one-full", "mixed", "two-tiles", "odd-group"])
 def test_many_items_of_different_heights(kind, D, group, T):
     """Hundreds of items, short ones beside full ones: 2 to 128 rows of a tile of 128, 4 to 256 of 256."""
     r = np.random.RandomState(D + group)
@@ -181,7 +188,7 @@ def test_many_items_just_past_a_tile(kind, D):
 
 @KINDS
 @DIMS
-@pytest.mark.parametrize("group", [4])
+@pytest.mark.parametrize("group", [2, 4])
 def test_long_contexts_mixed_with_single_tokens(kind, D, group):
     """Few items of many tiles each: more than six key tiles a CTA, cut anywhere, single tokens beside trees of 64."""
     drafted = [1, 64] * 8
