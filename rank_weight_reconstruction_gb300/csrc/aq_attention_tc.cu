@@ -740,7 +740,7 @@ __device__ __forceinline__ void tc_weigh(const AttnParams& p, TcShared& sh, uint
         float cover = 0.0f;
         if constexpr (S::E4M3) cover = scale_exponent(tile_scale()) - kTop;
         const float want = big == -INFINITY ? big : fmaf(big, fac, cover);
-        if (!__any_sync(0xffffffffu, want > m + kLag)) {
+        if (!__any_sync(0xffffffffu, lane < count && want > m + kLag)) {
           l += (sum[0] + sum[1]) + (sum[2] + sum[3]);
 #pragma unroll
           for (int c = 0; c < BN / 32; ++c) tmem_st16u(s_addr + 16 * c, reinterpret_cast<const uint32_t(&)[16]>(pk[16 * c]));
@@ -795,7 +795,8 @@ __device__ __forceinline__ void tc_weigh(const AttnParams& p, TcShared& sh, uint
             }
           }
         }
-        const bool grown = want > m + kLag;
+        // a lane without a row has what an earlier item or call left there: it has no say, or bits would hang on that
+        const bool grown = lane < count && want > m + kLag;
         if (__any_sync(0xffffffffu, grown)) {
           const float mx = fmaxf(m, want), keep = ex2(m - (mx == -INFINITY ? 0.0f : mx));
           m = mx;

@@ -213,3 +213,20 @@ def test_max_q_far_above_most_sequences(kind):
     drafted[50] = 700
     c = Batch(3, kind, 128, 2, 2, 32, [int(x) for x in r.randint(0, 700, 200)], drafted)
     c.check(*c.run())
+
+
+@KINDS
+@DIMS
+@pytest.mark.parametrize("group", [2, 4])
+def test_items_repeat_bit_for_bit(kind, D, group):
+    """Equal calls give equal bits, however the warps of a CTA run ahead of one another and whatever shared memory held before:
+    row tiles of which some are partly filled, other calls in between."""
+    r = np.random.RandomState(4)
+    drafted = [[1, 64, 33][i % 3] for i in range(160)]
+    c = Batch(D + 7, kind, D, 2, group, 32, [int(x) for x in r.randint(0, 800, 160)], drafted)
+    d = Batch(D + 8, kind, D, 1, 2 * group, 32, [int(x) for x in r.randint(0, 300, 40)], [64] * 40, gain=30.0)
+    out, lse = c.run()
+    for _ in range(20):
+        again = c.run()
+        d.run()
+        assert torch.equal(out, again[0]) and torch.equal(lse, again[1])
