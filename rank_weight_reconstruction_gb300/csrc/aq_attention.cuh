@@ -114,8 +114,12 @@ __device__ __forceinline__ float pow2(int e) { return __int_as_float((e + 127) <
 // Exponent of a non-negative value, kept where 2^(14 - e) and 2^(e - 14) are finite; zero counts as 2^-112.
 __device__ __forceinline__ int top_exponent(float x) { return min(max(static_cast<int>(__float_as_uint(x) >> 23) - 127, -112), 126); }
 
-// ... of a value's scale, for the reference.
-__device__ __forceinline__ float scale_exponent(float x) { return static_cast<float>(max(static_cast<int>(__float_as_uint(x) >> 23) - 127, kLeast)); }
+// ... of a value's scale, for the reference. The scale of a vector that reads as NaN counts as the smallest: its key's weight
+// belongs in the row's sum like any other, and against a reference 2^120 above it the sum (and lse) would lose the rest.
+__device__ __forceinline__ float scale_exponent(float x) {
+  const int e = static_cast<int>((__float_as_uint(x) >> 23) & 0xff) - 127;
+  return static_cast<float>(e == 128 ? kLeast : max(e, kLeast));
+}
 
 // Keys [lo, hi) and tiles [t0, t1) that the rows of entry (sequence b, row tile rt) can see.
 struct KeySpan {

@@ -687,11 +687,14 @@ __device__ __forceinline__ void tc_weigh(const AttnParams& p, TcShared& sh, uint
       }
       if (!wait(&sh.s_full[x], x_parity)) return;
       tc_fence_after();
-      auto tile_scale = [&]() {   // the tile's largest scale of a value; a NaN counts as the largest: every row sees it and is NaN
+      auto tile_scale = [&]() {   // the tile's largest scale of a value, but for NaN
         const float* f = reinterpret_cast<const float*>(vs);
         uint32_t big = 0;
 #pragma unroll
-        for (int k = 0; k < BN / 32; ++k) big = max(big, __float_as_uint(f[32 * k + lane]));
+        for (int k = 0; k < BN / 32; ++k) {
+          const uint32_t bits = __float_as_uint(f[32 * k + lane]);
+          big = max(big, bits < 0x7f800000u ? bits : 0u);
+        }
         return __uint_as_float(__reduce_max_sync(0xffffffffu, big));
       };
       bool done = false;
