@@ -14,6 +14,8 @@
 #include <ATen/core/LegacyTypeDispatch.h>
 #include <ATen/ops/empty.h>
 #include <ATen/ops/empty_like.h>
+#include <c10/cuda/CUDACachingAllocator.h>
+#include <c10/cuda/CUDAGuard.h>
 #include <c10/cuda/CUDAStream.h>
 #include <math.h>
 #include <stdint.h>
@@ -234,15 +236,46 @@ bool want(Py_ssize_t got, Py_ssize_t n, const char* name) {
   return false;
 }
 
-// The stream that a call was given, or the current one of the tensor's device.
-bool stream_of(PyObject* obj, const Tensor& on, void** out) {
-  if (obj == Py_None) {
-    *out = on.t->is_cuda() ? static_cast<void*>(c10::cuda::getCurrentCUDAStream(on.t->get_device()).stream()) : nullptr;
+// The stream of a call: the one it was given, or the current one of the tensors' device. What a call allocates comes from its
+// own stream's memory: under the current stream, a workspace let go at the end of the call would be the next request's there
+// while the given stream's kernels still use it, and a block freed there would be written before its last reader is through.
+// Outputs that go back to the caller are noted as used by the current stream too, where they will be read.
+class Stream {
+ public:
+  void* handle = nullptr;
+  bool read_from(PyObject* obj, const Tensor& on) {
+    const bool gpu = on.t->is_cuda();
+    if (gpu) current_ = c10::cuda::getCurrentCUDAStream(on.t->get_device());
+    if (obj == Py_None) {
+      handle = gpu ? static_cast<void*>(current_->stream()) : nullptr;
+      return true;
+    }
+    const uintptr_t given = static_cast<uintptr_t>(PyLong_AsUnsignedLongLong(obj));
+    if (PyErr_Occurred()) return false;
+    handle = reinterpret_cast<void*>(given);
+    // 1 names the default stream; every other handle is a pointer, or 2 for the thread's own
+    cudaStream_t own = given == 1 ? nullptr : static_cast<cudaStream_t>(handle);
+    if ((given & 1) && given != 1) {
+      PyErr_Format(PyExc_ValueError, "stream: %p is no stream handle", handle);
+      return false;
+    }
+    if (gpu && own != current_->stream()) {
+      guard_.reset_stream(c10::cuda::getStreamFromExternal(own, on.t->get_device()));
+      elsewhere_ = true;
+    }
     return true;
   }
-  *out = reinterpret_cast<void*>(static_cast<uintptr_t>(PyLong_AsUnsignedLongLong(obj)));
-  return !PyErr_Occurred();
-}
+  // An output of this call on its way to the caller.
+  PyObject* hand_out(at::Tensor&& t) {
+    if (elsewhere_) c10::cuda::CUDACachingAllocator::recordStream(t.storage().data_ptr(), *current_);
+    return THPVariable_Wrap(std::move(t));
+  }
+
+ private:
+  std::optional<c10::cuda::CUDAStream> current_;
+  c10::cuda::OptionalCUDAStreamGuard guard_;
+  bool elsewhere_ = false;
+};
 
 bool ok(aq_status st) {
   if (st == AQ_OK) return true;
@@ -283,9 +316,9 @@ PyObject* py_rope(PyObject*, PyObject* const* a, Py_ssize_t n) {
   HANDLE_TH_ERRORS
   Rope r;
   Tensor pos, x, y;
-  void* st;
+  Stream st;
   if (!want(n, 6, "rope") || !r.read_from(a[0]) || !read_heads(a[2], "x", -1, -1, -1, &x) || !read_flat(a[1], "pos", kI32, x.shape[0], &pos) ||
-      (a[3] != Py_None && !read_heads(a[3], "y", x.shape[0], x.shape[1], x.shape[2], &y)) || !stream_of(a[5], x, &st))
+      (a[3] != Py_None && !read_heads(a[3], "y", x.shape[0], x.shape[1], x.shape[2], &y)) || !st.read_from(a[5], x))
     return nullptr;
   const int inverse = PyObject_IsTrue(a[4]);
   if (inverse < 0) return nullptr;
@@ -297,9 +330,9 @@ PyObject* py_rope(PyObject*, PyObject* const* a, Py_ssize_t n) {
     if (!head_strides("y", &y)) return nullptr;
   }
   if (!on_gpu() || !ok(f_rope(&r.spec, static_cast<const int32_t*>(pos.ptr), x.shape[0], small(x.shape[1]), small(x.shape[2]), x.ptr, x.stride[0], x.stride[1],
-                 y.ptr, y.stride[0], y.stride[1], inverse, st)))
+                 y.ptr, y.stride[0], y.stride[1], inverse, st.handle)))
     return nullptr;
-  return made.defined() ? THPVariable_Wrap(std::move(made)) : given(a[3]);
+  return made.defined() ? st.hand_out(std::move(made)) : given(a[3]);
   END_HANDLE_TH_ERRORS
 }
 
@@ -309,13 +342,13 @@ PyObject* py_kv_write(PyObject*, PyObject* const* a, Py_ssize_t n) {
   Cache c;
   Rope r;
   Tensor k, v, slots, pos, q, o;
-  void* st;
+  Stream st;
   if (!want(n, 9, "kv_write") || !c.read_from(a[0]) || !read_heads(a[1], "k", -1, c.c.kv_heads, c.c.head_dim, &k)) return nullptr;
   const int64_t T = k.shape[0];
   const bool turned = a[4] != Py_None, queries = a[6] != Py_None;
   if (!read_heads(a[2], "v", T, c.c.kv_heads, c.c.head_dim, &v) || !read_flat(a[3], "slots", kI64, T, &slots) || (turned && !r.read_from(a[4])) ||
       (a[5] != Py_None && !read_flat(a[5], "pos", kI32, T, &pos)) || (queries && !read_heads(a[6], "q", T, -1, c.c.head_dim, &q)) ||
-      (queries && a[7] != Py_None && !read_heads(a[7], "q_out", T, q.shape[1], c.c.head_dim, &o)) || !stream_of(a[8], k, &st))
+      (queries && a[7] != Py_None && !read_heads(a[7], "q_out", T, q.shape[1], c.c.head_dim, &o)) || !st.read_from(a[8], k))
     return nullptr;
   at::AutoDispatchBelowADInplaceOrView plain;
   at::Tensor made;
@@ -326,9 +359,9 @@ PyObject* py_kv_write(PyObject*, PyObject* const* a, Py_ssize_t n) {
   }
   if (!on_gpu() || !ok(f_kv_write(&c.c, static_cast<const int64_t*>(slots.ptr), T, k.ptr, k.stride[0], k.stride[1], v.ptr, v.stride[0], v.stride[1],
                      turned ? &r.spec : nullptr, static_cast<const int32_t*>(pos.ptr), q.ptr, small(q.shape[1]), q.stride[0], q.stride[1], o.ptr,
-                     o.stride[0], o.stride[1], st)))
+                     o.stride[0], o.stride[1], st.handle)))
     return nullptr;
-  return made.defined() ? THPVariable_Wrap(std::move(made)) : given(a[7]);
+  return made.defined() ? st.hand_out(std::move(made)) : given(a[7]);
   END_HANDLE_TH_ERRORS
 }
 
@@ -337,12 +370,12 @@ PyObject* py_kv_read(PyObject*, PyObject* const* a, Py_ssize_t n) {
   HANDLE_TH_ERRORS
   Cache c;
   Tensor slots, x[2];
-  void* st;
+  Stream st;
   if (!want(n, 5, "kv_read") || !c.read_from(a[0]) || !read_flat(a[1], "slots", kI64, -1, &slots)) return nullptr;
   const char* const name[2] = {"k", "v"};
   for (int i = 0; i < 2; ++i)
     if (a[2 + i] != Py_None && !read_heads(a[2 + i], name[i], slots.shape[0], c.c.kv_heads, c.c.head_dim, &x[i])) return nullptr;
-  if (!stream_of(a[4], slots, &st)) return nullptr;
+  if (!st.read_from(a[4], slots)) return nullptr;
   at::AutoDispatchBelowADInplaceOrView plain;
   at::Tensor made[2];
   for (int i = 0; i < 2; ++i)
@@ -352,9 +385,9 @@ PyObject* py_kv_read(PyObject*, PyObject* const* a, Py_ssize_t n) {
       if (!head_strides(name[i], &x[i])) return nullptr;
     }
   if (!on_gpu() || !ok(f_kv_read(&c.c, static_cast<const int64_t*>(slots.ptr), slots.shape[0], x[0].ptr, x[0].stride[0], x[0].stride[1], x[1].ptr, x[1].stride[0],
-                    x[1].stride[1], st)))
+                    x[1].stride[1], st.handle)))
     return nullptr;
-  return pack({made[0].defined() ? THPVariable_Wrap(std::move(made[0])) : given(a[2]), made[1].defined() ? THPVariable_Wrap(std::move(made[1])) : given(a[3])});
+  return pack({made[0].defined() ? st.hand_out(std::move(made[0])) : given(a[2]), made[1].defined() ? st.hand_out(std::move(made[1])) : given(a[3])});
   END_HANDLE_TH_ERRORS
 }
 
@@ -385,7 +418,7 @@ PyObject* py_attention(PyObject*, PyObject* const* a, Py_ssize_t n) {
   Cache c;
   aq_draft_batch d = {};
   Tensor q, cu, ctx, table, mask, depth, out, lse, ws;
-  void* st;
+  Stream st;
   if (!want(n, 15, "attention") || !c.read_from(a[0]) || !read_heads(a[1], "q", -1, -1, c.c.head_dim, &q) ||
       !read_rows(a[4], "page_table", kI32, kI32, -1, 0, &table) || !read_flat(a[2], "cu_q", kI32, table.shape[0] + 1, &cu) ||
       !read_flat(a[3], "ctx", kI32, table.shape[0], &ctx) || !read_int32(a[5], "max_q", &d.max_q))
@@ -405,7 +438,7 @@ PyObject* py_attention(PyObject*, PyObject* const* a, Py_ssize_t n) {
       return nullptr;
     }
   }
-  if ((a[13] != Py_None && !read_flat(a[13], "workspace", kU8, -1, &ws)) || !stream_of(a[14], q, &st)) return nullptr;
+  if ((a[13] != Py_None && !read_flat(a[13], "workspace", kU8, -1, &ws)) || !st.read_from(a[14], q)) return nullptr;
   d.batch = small(table.shape[0]);
   d.total_q = total;
   d.cu_q = static_cast<const int32_t*>(cu.ptr);
@@ -439,11 +472,11 @@ PyObject* py_attention(PyObject*, PyObject* const* a, Py_ssize_t n) {
     }
   }
   if (!on_gpu() || !ok(f_attention(&c.c, &d, q.ptr, small(heads), q.stride[0], q.stride[1], static_cast<float>(scale), out.ptr, out.stride[0], out.stride[1],
-                      static_cast<float*>(lse.ptr), ws.ptr, static_cast<size_t>(ws.shape[0]), st)))
+                      static_cast<float*>(lse.ptr), ws.ptr, static_cast<size_t>(ws.shape[0]), st.handle)))
     return nullptr;
-  PyObject* o = made_out.defined() ? THPVariable_Wrap(std::move(made_out)) : given(a[10]);
+  PyObject* o = made_out.defined() ? st.hand_out(std::move(made_out)) : given(a[10]);
   if (!with_lse) return o;
-  return pack({o, made_lse.defined() ? THPVariable_Wrap(std::move(made_lse)) : given(a[11])});
+  return pack({o, made_lse.defined() ? st.hand_out(std::move(made_lse)) : given(a[11])});
   END_HANDLE_TH_ERRORS
 }
 
@@ -452,7 +485,7 @@ PyObject* py_verify(PyObject*, PyObject* const* a, Py_ssize_t n) {
   HANDLE_TH_ERRORS
   Tensor p, tokens, cu, u, noise, q, parent, count, path, token;
   int32_t cap = AQ_MAX_DRAFT_NODES, most = AQ_MAX_DRAFT_NODES;
-  void* st;
+  Stream st;
   if (!want(n, 10, "verify") || !read_rows(a[0], "p", kF32, kBf16, -1, 0, &p) || !read_flat(a[1], "tokens", kI32, -1, &tokens) ||
       !read_flat(a[2], "cu", kI32, -1, &cu) || !read_flat(a[3], "u", kF32, tokens.shape[0], &u))
     return nullptr;
@@ -471,7 +504,7 @@ PyObject* py_verify(PyObject*, PyObject* const* a, Py_ssize_t n) {
   }
   if (nodes < cap) cap = most = static_cast<int32_t>(nodes);
   if ((a[6] != Py_None && !read_flat(a[6], "parent", kI32, nodes, &parent)) || (a[7] != Py_None && !read_int32(a[7], "path_cap", &cap)) ||
-      (a[8] != Py_None && !read_int32(a[8], "max_nodes", &most)) || !stream_of(a[9], p, &st))
+      (a[8] != Py_None && !read_int32(a[8], "max_nodes", &most)) || !st.read_from(a[9], p))
     return nullptr;
   if (cap < 0) {
     PyErr_Format(PyExc_ValueError, "path_cap=%d is negative", cap);
@@ -485,9 +518,9 @@ PyObject* py_verify(PyObject*, PyObject* const* a, Py_ssize_t n) {
   if (!on_gpu() || !ok(f_verify(small(batch), small(vocab), static_cast<const int32_t*>(cu.ptr), static_cast<const int32_t*>(tokens.ptr),
                    static_cast<const int32_t*>(parent.ptr), nodes, most, p.ptr, p.stride[0], q.ptr, q.stride[0], p.shape[0],
                    dtype == kF32 ? AQ_PROB_F32 : AQ_PROB_BF16, static_cast<const float*>(u.ptr), static_cast<const float*>(noise.ptr), noise.stride[0],
-                   static_cast<int32_t*>(count.ptr), static_cast<int32_t*>(path.ptr), cap, cap, static_cast<int32_t*>(token.ptr), st)))
+                   static_cast<int32_t*>(count.ptr), static_cast<int32_t*>(path.ptr), cap, cap, static_cast<int32_t*>(token.ptr), st.handle)))
     return nullptr;
-  return pack({THPVariable_Wrap(std::move(made[0])), THPVariable_Wrap(std::move(made[1])), THPVariable_Wrap(std::move(made[2]))});
+  return pack({st.hand_out(std::move(made[0])), st.hand_out(std::move(made[1])), st.hand_out(std::move(made[2]))});
   END_HANDLE_TH_ERRORS
 }
 
