@@ -40,7 +40,7 @@ PyObject *s_freq, *s_layout, *s_magnitude, *s_k, *s_v, *s_k_scale, *s_v_scale;
 
 constexpr at::ScalarType kBf16 = at::kBFloat16, kF32 = at::kFloat, kI32 = at::kInt, kI64 = at::kLong, kU64 = at::kUInt64, kU8 = at::kByte;
 
-std::optional<c10::Device> call_device;   // of the tensors read so far in this call (the interpreter's lock is held)
+using Device = std::optional<c10::Device>;   // of the tensors read so far in a call
 
 struct Tensor {
   int64_t shape[4] = {0, 0, 0, 0}, stride[4] = {0, 0, 0, 0};
@@ -61,7 +61,7 @@ void take(const at::Tensor& t, Tensor* x) {
 
 // A tensor of dtype a or b and nd dimensions; false with a Python error otherwise. The functions below take views of
 // tensors that their caller's arguments keep alive.
-bool read(PyObject* obj, const char* name, at::ScalarType a, at::ScalarType b, int nd, Tensor* x) {
+bool read(Device& dev, PyObject* obj, const char* name, at::ScalarType a, at::ScalarType b, int nd, Tensor* x) {
   if (!THPVariable_Check(obj)) {
     PyErr_Format(PyExc_TypeError, "%s: expected a tensor, got %R", name, reinterpret_cast<PyObject*>(Py_TYPE(obj)));
     return false;
@@ -75,9 +75,9 @@ bool read(PyObject* obj, const char* name, at::ScalarType a, at::ScalarType b, i
     PyErr_Format(PyExc_ValueError, "%s: expected a strided tensor of %d dimensions, got %d", name, nd, static_cast<int>(t.dim()));
     return false;
   }
-  if (!call_device) call_device = t.device();
-  if (*call_device != t.device()) {
-    PyErr_Format(PyExc_ValueError, "%s: on %s, the call's other tensors on %s", name, t.device().str().c_str(), call_device->str().c_str());
+  if (!dev) dev = t.device();
+  if (*dev != t.device()) {
+    PyErr_Format(PyExc_ValueError, "%s: on %s, the call's other tensors on %s", name, t.device().str().c_str(), dev->str().c_str());
     return false;
   }
   take(t, x);
@@ -95,8 +95,8 @@ bool contiguous(const Tensor& x) {
 }
 
 // A contiguous 1-D tensor of n elements (n < 0: any number).
-bool read_flat(PyObject* obj, const char* name, at::ScalarType dtype, int64_t n, Tensor* x) {
-  if (!read(obj, name, dtype, dtype, 1, x)) return false;
+bool read_flat(Device& dev, PyObject* obj, const char* name, at::ScalarType dtype, int64_t n, Tensor* x) {
+  if (!read(dev, obj, name, dtype, dtype, 1, x)) return false;
   if ((n < 0 || x->shape[0] == n) && contiguous(*x)) return true;
   if (n >= 0)
     PyErr_Format(PyExc_ValueError, "%s: expected a contiguous tensor of %lld elements, got %lld", name, static_cast<long long>(n),
@@ -118,8 +118,8 @@ bool head_strides(const char* name, Tensor* x) {
 }
 
 // A bf16 [tokens, heads, head_dim] tensor or view; -1: any.
-bool read_heads(PyObject* obj, const char* name, int64_t tokens, int64_t heads, int64_t dim, Tensor* x) {
-  if (!read(obj, name, kBf16, kBf16, 3, x)) return false;
+bool read_heads(Device& dev, PyObject* obj, const char* name, int64_t tokens, int64_t heads, int64_t dim, Tensor* x) {
+  if (!read(dev, obj, name, kBf16, kBf16, 3, x)) return false;
   if ((tokens >= 0 && x->shape[0] != tokens) || (heads >= 0 && x->shape[1] != heads) || (dim >= 0 && x->shape[2] != dim)) {
     PyErr_Format(PyExc_ValueError, "%s: expected shape (%lld, %lld, %lld), got (%lld, %lld, %lld) (-1: any)", name,
                  static_cast<long long>(tokens), static_cast<long long>(heads), static_cast<long long>(dim),
@@ -130,8 +130,8 @@ bool read_heads(PyObject* obj, const char* name, int64_t tokens, int64_t heads, 
 }
 
 // A 2-D tensor of `rows` rows (-1: any) and at least `cols` columns with unit column stride.
-bool read_rows(PyObject* obj, const char* name, at::ScalarType a, at::ScalarType b, int64_t rows, int64_t cols, Tensor* x) {
-  if (!read(obj, name, a, b, 2, x)) return false;
+bool read_rows(Device& dev, PyObject* obj, const char* name, at::ScalarType a, at::ScalarType b, int64_t rows, int64_t cols, Tensor* x) {
+  if (!read(dev, obj, name, a, b, 2, x)) return false;
   if ((rows >= 0 && x->shape[0] != rows) || x->shape[1] < cols) {
     PyErr_Format(PyExc_ValueError, "%s: expected [%lld, %lld], got [%lld, %lld]", name, static_cast<long long>(rows),
                  static_cast<long long>(cols), static_cast<long long>(x->shape[0]), static_cast<long long>(x->shape[1]));
@@ -168,10 +168,10 @@ struct Rope {
   PyObject* freq = nullptr;
   aq_rope_spec spec = {};
   ~Rope() { Py_XDECREF(freq); }
-  bool read_from(PyObject* obj) {
+  bool read_from(Device& dev, PyObject* obj) {
     Tensor t;
     freq = PyObject_GetAttr(obj, s_freq);
-    if (!freq || !read(freq, "Rope.freq", kI64, kU64, 1, &t)) return false;
+    if (!freq || !read(dev, freq, "Rope.freq", kI64, kU64, 1, &t)) return false;
     if (!contiguous(t)) {
       PyErr_SetString(PyExc_ValueError, "Rope.freq: expected a contiguous tensor");
       return false;
@@ -193,19 +193,19 @@ struct Cache {
   ~Cache() {
     for (PyObject* o : part) Py_XDECREF(o);
   }
-  bool read_from(PyObject* obj) {
+  bool read_from(Device& dev, PyObject* obj) {
     PyObject* const name[4] = {s_k, s_v, s_k_scale, s_v_scale};
     for (int i = 0; i < 4; ++i)
       if (!(part[i] = PyObject_GetAttr(obj, name[i]))) return false;
     Tensor t[4];
     const bool scaled = part[2] != Py_None;
     const at::ScalarType code = scaled ? kU8 : kBf16;
-    if (!read(part[0], "KvCache.k", code, code, 4, &t[0]) || !read(part[1], "KvCache.v", code, code, 4, &t[1])) return false;
+    if (!read(dev, part[0], "KvCache.k", code, code, 4, &t[0]) || !read(dev, part[1], "KvCache.v", code, code, 4, &t[1])) return false;
     if (scaled != (part[3] != Py_None)) {
       PyErr_SetString(PyExc_ValueError, "KvCache: k_scale and v_scale go together");
       return false;
     }
-    if (scaled && (!read(part[2], "KvCache.k_scale", kF32, kF32, 3, &t[2]) || !read(part[3], "KvCache.v_scale", kF32, kF32, 3, &t[3]))) return false;
+    if (scaled && (!read(dev, part[2], "KvCache.k_scale", kF32, kF32, 3, &t[2]) || !read(dev, part[3], "KvCache.v_scale", kF32, kF32, 3, &t[3]))) return false;
     bool bad = false;
     for (int i = 0; i < (scaled ? 4 : 2); ++i) {
       for (int k = 0; k < (i < 2 ? 4 : 3); ++k) bad = bad || t[i].shape[k] != t[0].shape[k];
@@ -230,7 +230,6 @@ struct Cache {
 };
 
 bool want(Py_ssize_t got, Py_ssize_t n, const char* name) {
-  call_device.reset();
   if (got == n && f_check) return true;
   PyErr_Format(PyExc_TypeError, f_check ? "%s: wrong number of arguments" : "%s: bind() has not been called", name);
   return false;
@@ -285,9 +284,9 @@ bool ok(aq_status st) {
 }
 
 // The library takes device pointers: a host tensor's is not passed on.
-bool on_gpu() {
-  if (call_device && call_device->is_cuda()) return true;
-  PyErr_Format(PyExc_ValueError, "the tensors of a call must be on a CUDA device, not on %s", call_device ? call_device->str().c_str() : "none");
+bool on_gpu(const Device& dev) {
+  if (dev && dev->is_cuda()) return true;
+  PyErr_Format(PyExc_ValueError, "the tensors of a call must be on a CUDA device, not on %s", dev ? dev->str().c_str() : "none");
   return false;
 }
 
@@ -314,11 +313,12 @@ PyObject* pack(std::initializer_list<PyObject*> items) {   // takes the referenc
 // rope(rope, pos, x, y, inverse, stream) -> y
 PyObject* py_rope(PyObject*, PyObject* const* a, Py_ssize_t n) {
   HANDLE_TH_ERRORS
+  Device dev;
   Rope r;
   Tensor pos, x, y;
   Stream st;
-  if (!want(n, 6, "rope") || !r.read_from(a[0]) || !read_heads(a[2], "x", -1, -1, -1, &x) || !read_flat(a[1], "pos", kI32, x.shape[0], &pos) ||
-      (a[3] != Py_None && !read_heads(a[3], "y", x.shape[0], x.shape[1], x.shape[2], &y)) || !st.read_from(a[5], x))
+  if (!want(n, 6, "rope") || !r.read_from(dev, a[0]) || !read_heads(dev, a[2], "x", -1, -1, -1, &x) || !read_flat(dev, a[1], "pos", kI32, x.shape[0], &pos) ||
+      (a[3] != Py_None && !read_heads(dev, a[3], "y", x.shape[0], x.shape[1], x.shape[2], &y)) || !st.read_from(a[5], x))
     return nullptr;
   const int inverse = PyObject_IsTrue(a[4]);
   if (inverse < 0) return nullptr;
@@ -329,7 +329,7 @@ PyObject* py_rope(PyObject*, PyObject* const* a, Py_ssize_t n) {
     take(made, &y);
     if (!head_strides("y", &y)) return nullptr;
   }
-  if (!on_gpu() || !ok(f_rope(&r.spec, static_cast<const int32_t*>(pos.ptr), x.shape[0], small(x.shape[1]), small(x.shape[2]), x.ptr, x.stride[0], x.stride[1],
+  if (!on_gpu(dev) || !ok(f_rope(&r.spec, static_cast<const int32_t*>(pos.ptr), x.shape[0], small(x.shape[1]), small(x.shape[2]), x.ptr, x.stride[0], x.stride[1],
                  y.ptr, y.stride[0], y.stride[1], inverse, st.handle)))
     return nullptr;
   return made.defined() ? st.hand_out(std::move(made)) : given(a[3]);
@@ -339,16 +339,17 @@ PyObject* py_rope(PyObject*, PyObject* const* a, Py_ssize_t n) {
 // kv_write(cache, k, v, slots, rope, pos, q, q_out, stream) -> q_out
 PyObject* py_kv_write(PyObject*, PyObject* const* a, Py_ssize_t n) {
   HANDLE_TH_ERRORS
+  Device dev;
   Cache c;
   Rope r;
   Tensor k, v, slots, pos, q, o;
   Stream st;
-  if (!want(n, 9, "kv_write") || !c.read_from(a[0]) || !read_heads(a[1], "k", -1, c.c.kv_heads, c.c.head_dim, &k)) return nullptr;
+  if (!want(n, 9, "kv_write") || !c.read_from(dev, a[0]) || !read_heads(dev, a[1], "k", -1, c.c.kv_heads, c.c.head_dim, &k)) return nullptr;
   const int64_t T = k.shape[0];
   const bool turned = a[4] != Py_None, queries = a[6] != Py_None;
-  if (!read_heads(a[2], "v", T, c.c.kv_heads, c.c.head_dim, &v) || !read_flat(a[3], "slots", kI64, T, &slots) || (turned && !r.read_from(a[4])) ||
-      (a[5] != Py_None && !read_flat(a[5], "pos", kI32, T, &pos)) || (queries && !read_heads(a[6], "q", T, -1, c.c.head_dim, &q)) ||
-      (queries && a[7] != Py_None && !read_heads(a[7], "q_out", T, q.shape[1], c.c.head_dim, &o)) || !st.read_from(a[8], k))
+  if (!read_heads(dev, a[2], "v", T, c.c.kv_heads, c.c.head_dim, &v) || !read_flat(dev, a[3], "slots", kI64, T, &slots) || (turned && !r.read_from(dev, a[4])) ||
+      (a[5] != Py_None && !read_flat(dev, a[5], "pos", kI32, T, &pos)) || (queries && !read_heads(dev, a[6], "q", T, -1, c.c.head_dim, &q)) ||
+      (queries && a[7] != Py_None && !read_heads(dev, a[7], "q_out", T, q.shape[1], c.c.head_dim, &o)) || !st.read_from(a[8], k))
     return nullptr;
   at::AutoDispatchBelowADInplaceOrView plain;
   at::Tensor made;
@@ -357,7 +358,7 @@ PyObject* py_kv_write(PyObject*, PyObject* const* a, Py_ssize_t n) {
     take(made, &o);
     if (!head_strides("q_out", &o)) return nullptr;
   }
-  if (!on_gpu() || !ok(f_kv_write(&c.c, static_cast<const int64_t*>(slots.ptr), T, k.ptr, k.stride[0], k.stride[1], v.ptr, v.stride[0], v.stride[1],
+  if (!on_gpu(dev) || !ok(f_kv_write(&c.c, static_cast<const int64_t*>(slots.ptr), T, k.ptr, k.stride[0], k.stride[1], v.ptr, v.stride[0], v.stride[1],
                      turned ? &r.spec : nullptr, static_cast<const int32_t*>(pos.ptr), q.ptr, small(q.shape[1]), q.stride[0], q.stride[1], o.ptr,
                      o.stride[0], o.stride[1], st.handle)))
     return nullptr;
@@ -368,13 +369,14 @@ PyObject* py_kv_write(PyObject*, PyObject* const* a, Py_ssize_t n) {
 // kv_read(cache, slots, k, v, stream) -> (k, v)
 PyObject* py_kv_read(PyObject*, PyObject* const* a, Py_ssize_t n) {
   HANDLE_TH_ERRORS
+  Device dev;
   Cache c;
   Tensor slots, x[2];
   Stream st;
-  if (!want(n, 5, "kv_read") || !c.read_from(a[0]) || !read_flat(a[1], "slots", kI64, -1, &slots)) return nullptr;
+  if (!want(n, 5, "kv_read") || !c.read_from(dev, a[0]) || !read_flat(dev, a[1], "slots", kI64, -1, &slots)) return nullptr;
   const char* const name[2] = {"k", "v"};
   for (int i = 0; i < 2; ++i)
-    if (a[2 + i] != Py_None && !read_heads(a[2 + i], name[i], slots.shape[0], c.c.kv_heads, c.c.head_dim, &x[i])) return nullptr;
+    if (a[2 + i] != Py_None && !read_heads(dev, a[2 + i], name[i], slots.shape[0], c.c.kv_heads, c.c.head_dim, &x[i])) return nullptr;
   if (!st.read_from(a[4], slots)) return nullptr;
   at::AutoDispatchBelowADInplaceOrView plain;
   at::Tensor made[2];
@@ -384,7 +386,7 @@ PyObject* py_kv_read(PyObject*, PyObject* const* a, Py_ssize_t n) {
       take(made[i], &x[i]);
       if (!head_strides(name[i], &x[i])) return nullptr;
     }
-  if (!on_gpu() || !ok(f_kv_read(&c.c, static_cast<const int64_t*>(slots.ptr), slots.shape[0], x[0].ptr, x[0].stride[0], x[0].stride[1], x[1].ptr, x[1].stride[0],
+  if (!on_gpu(dev) || !ok(f_kv_read(&c.c, static_cast<const int64_t*>(slots.ptr), slots.shape[0], x[0].ptr, x[0].stride[0], x[0].stride[1], x[1].ptr, x[1].stride[0],
                     x[1].stride[1], st.handle)))
     return nullptr;
   return pack({made[0].defined() ? st.hand_out(std::move(made[0])) : given(a[2]), made[1].defined() ? st.hand_out(std::move(made[1])) : given(a[3])});
@@ -394,10 +396,11 @@ PyObject* py_kv_read(PyObject*, PyObject* const* a, Py_ssize_t n) {
 // attention_bytes(cache, q_heads, batch, max_q, total_q)
 PyObject* py_attention_bytes(PyObject*, PyObject* const* a, Py_ssize_t n) {
   HANDLE_TH_ERRORS
+  Device dev;
   Cache c;
   aq_draft_batch d = {};
   int32_t heads;
-  if (!want(n, 5, "attention_bytes") || !c.read_from(a[0]) || !read_int32(a[1], "q_heads", &heads) || !read_int32(a[2], "batch", &d.batch) ||
+  if (!want(n, 5, "attention_bytes") || !c.read_from(dev, a[0]) || !read_int32(a[1], "q_heads", &heads) || !read_int32(a[2], "batch", &d.batch) ||
       !read_int32(a[3], "max_q", &d.max_q))
     return nullptr;
   d.total_q = PyLong_AsLongLong(a[4]);
@@ -415,30 +418,31 @@ PyObject* py_attention_bytes(PyObject*, PyObject* const* a, Py_ssize_t n) {
 //   -> out or (out, lse); scale None: head_dim^-1/2
 PyObject* py_attention(PyObject*, PyObject* const* a, Py_ssize_t n) {
   HANDLE_TH_ERRORS
+  Device dev;
   Cache c;
   aq_draft_batch d = {};
   Tensor q, cu, ctx, table, mask, depth, out, lse, ws;
   Stream st;
-  if (!want(n, 15, "attention") || !c.read_from(a[0]) || !read_heads(a[1], "q", -1, -1, c.c.head_dim, &q) ||
-      !read_rows(a[4], "page_table", kI32, kI32, -1, 0, &table) || !read_flat(a[2], "cu_q", kI32, table.shape[0] + 1, &cu) ||
-      !read_flat(a[3], "ctx", kI32, table.shape[0], &ctx) || !read_int32(a[5], "max_q", &d.max_q))
+  if (!want(n, 15, "attention") || !c.read_from(dev, a[0]) || !read_heads(dev, a[1], "q", -1, -1, c.c.head_dim, &q) ||
+      !read_rows(dev, a[4], "page_table", kI32, kI32, -1, 0, &table) || !read_flat(dev, a[2], "cu_q", kI32, table.shape[0] + 1, &cu) ||
+      !read_flat(dev, a[3], "ctx", kI32, table.shape[0], &ctx) || !read_int32(a[5], "max_q", &d.max_q))
     return nullptr;
   const int64_t total = q.shape[0], heads = q.shape[1];
-  if ((a[6] != Py_None && !read_rows(a[6], "mask", kI64, kI64, total, (static_cast<int64_t>(d.max_q) + 63) / 64, &mask)) ||
-      (a[7] != Py_None && !read_flat(a[7], "depth", kI32, total, &depth)) || !read_int32(a[8], "window", &d.window) ||
-      (a[10] != Py_None && !read_heads(a[10], "out", total, heads, c.c.head_dim, &out)))
+  if ((a[6] != Py_None && !read_rows(dev, a[6], "mask", kI64, kI64, total, (static_cast<int64_t>(d.max_q) + 63) / 64, &mask)) ||
+      (a[7] != Py_None && !read_flat(dev, a[7], "depth", kI32, total, &depth)) || !read_int32(a[8], "window", &d.window) ||
+      (a[10] != Py_None && !read_heads(dev, a[10], "out", total, heads, c.c.head_dim, &out)))
     return nullptr;
   const double scale = a[9] == Py_None ? 1.0 / sqrt(static_cast<double>(c.c.head_dim)) : PyFloat_AsDouble(a[9]);
   const int with_lse = PyObject_IsTrue(a[12]);
   if (PyErr_Occurred()) return nullptr;
   if (a[11] != Py_None) {
-    if (!read(a[11], "lse", kF32, kF32, 2, &lse)) return nullptr;
+    if (!read(dev, a[11], "lse", kF32, kF32, 2, &lse)) return nullptr;
     if (lse.shape[0] != total || lse.shape[1] != heads || !contiguous(lse)) {
       PyErr_Format(PyExc_ValueError, "lse: expected a contiguous [%lld, %lld] tensor", static_cast<long long>(total), static_cast<long long>(heads));
       return nullptr;
     }
   }
-  if ((a[13] != Py_None && !read_flat(a[13], "workspace", kU8, -1, &ws)) || !st.read_from(a[14], q)) return nullptr;
+  if ((a[13] != Py_None && !read_flat(dev, a[13], "workspace", kU8, -1, &ws)) || !st.read_from(a[14], q)) return nullptr;
   d.batch = small(table.shape[0]);
   d.total_q = total;
   d.cu_q = static_cast<const int32_t*>(cu.ptr);
@@ -471,7 +475,7 @@ PyObject* py_attention(PyObject*, PyObject* const* a, Py_ssize_t n) {
       take(made_ws, &ws);
     }
   }
-  if (!on_gpu() || !ok(f_attention(&c.c, &d, q.ptr, small(heads), q.stride[0], q.stride[1], static_cast<float>(scale), out.ptr, out.stride[0], out.stride[1],
+  if (!on_gpu(dev) || !ok(f_attention(&c.c, &d, q.ptr, small(heads), q.stride[0], q.stride[1], static_cast<float>(scale), out.ptr, out.stride[0], out.stride[1],
                       static_cast<float*>(lse.ptr), ws.ptr, static_cast<size_t>(ws.shape[0]), st.handle)))
     return nullptr;
   PyObject* o = made_out.defined() ? st.hand_out(std::move(made_out)) : given(a[10]);
@@ -483,11 +487,12 @@ PyObject* py_attention(PyObject*, PyObject* const* a, Py_ssize_t n) {
 // verify(p, tokens, cu, u, noise, q, parent, path_cap, max_nodes, stream) -> (n_accepted, path, token)
 PyObject* py_verify(PyObject*, PyObject* const* a, Py_ssize_t n) {
   HANDLE_TH_ERRORS
+  Device dev;
   Tensor p, tokens, cu, u, noise, q, parent, count, path, token;
   int32_t cap = AQ_MAX_DRAFT_NODES, most = AQ_MAX_DRAFT_NODES;
   Stream st;
-  if (!want(n, 10, "verify") || !read_rows(a[0], "p", kF32, kBf16, -1, 0, &p) || !read_flat(a[1], "tokens", kI32, -1, &tokens) ||
-      !read_flat(a[2], "cu", kI32, -1, &cu) || !read_flat(a[3], "u", kF32, tokens.shape[0], &u))
+  if (!want(n, 10, "verify") || !read_rows(dev, a[0], "p", kF32, kBf16, -1, 0, &p) || !read_flat(dev, a[1], "tokens", kI32, -1, &tokens) ||
+      !read_flat(dev, a[2], "cu", kI32, -1, &cu) || !read_flat(dev, a[3], "u", kF32, tokens.shape[0], &u))
     return nullptr;
   const int64_t nodes = tokens.shape[0], batch = cu.shape[0] - 1, vocab = p.shape[1];
   const at::ScalarType dtype = p.t->scalar_type();
@@ -496,14 +501,14 @@ PyObject* py_verify(PyObject*, PyObject* const* a, Py_ssize_t n) {
     return nullptr;
   }
   const bool sampled = a[5] != Py_None;
-  if (!read_rows(a[4], "noise", kF32, kF32, batch, vocab, &noise) || (sampled && !read_rows(a[5], "q", dtype, dtype, p.shape[0], vocab, &q)))
+  if (!read_rows(dev, a[4], "noise", kF32, kF32, batch, vocab, &noise) || (sampled && !read_rows(dev, a[5], "q", dtype, dtype, p.shape[0], vocab, &q)))
     return nullptr;
   if (noise.shape[1] != vocab || (sampled && q.shape[1] != vocab)) {
     PyErr_Format(PyExc_ValueError, "noise and q: expected %lld columns", static_cast<long long>(vocab));
     return nullptr;
   }
   if (nodes < cap) cap = most = static_cast<int32_t>(nodes);
-  if ((a[6] != Py_None && !read_flat(a[6], "parent", kI32, nodes, &parent)) || (a[7] != Py_None && !read_int32(a[7], "path_cap", &cap)) ||
+  if ((a[6] != Py_None && !read_flat(dev, a[6], "parent", kI32, nodes, &parent)) || (a[7] != Py_None && !read_int32(a[7], "path_cap", &cap)) ||
       (a[8] != Py_None && !read_int32(a[8], "max_nodes", &most)) || !st.read_from(a[9], p))
     return nullptr;
   if (cap < 0) {
@@ -515,7 +520,7 @@ PyObject* py_verify(PyObject*, PyObject* const* a, Py_ssize_t n) {
   take(made[0], &count);
   take(made[1], &path);
   take(made[2], &token);
-  if (!on_gpu() || !ok(f_verify(small(batch), small(vocab), static_cast<const int32_t*>(cu.ptr), static_cast<const int32_t*>(tokens.ptr),
+  if (!on_gpu(dev) || !ok(f_verify(small(batch), small(vocab), static_cast<const int32_t*>(cu.ptr), static_cast<const int32_t*>(tokens.ptr),
                    static_cast<const int32_t*>(parent.ptr), nodes, most, p.ptr, p.stride[0], q.ptr, q.stride[0], p.shape[0],
                    dtype == kF32 ? AQ_PROB_F32 : AQ_PROB_BF16, static_cast<const float*>(u.ptr), static_cast<const float*>(noise.ptr), noise.stride[0],
                    static_cast<int32_t*>(count.ptr), static_cast<int32_t*>(path.ptr), cap, cap, static_cast<int32_t*>(token.ptr), st.handle)))

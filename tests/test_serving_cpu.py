@@ -227,3 +227,28 @@ def test_binding_passes_no_host_pointer_on():
             call(pos)
         with pytest.raises(ValueError, match="other tensors on"):   # of two devices
             call(pos.to("meta"))
+
+
+def test_a_call_within_a_call_leaves_the_outer_ones_checks_alone():
+    """A Rope whose table is made on access, by other calls: the outer call's tensors are still checked among themselves."""
+    torch = pytest.importorskip("torch")
+    x, pos = torch.zeros(3, 2, 64, dtype=torch.bfloat16), torch.zeros(3, dtype=torch.int32)
+
+    class Lazy:
+        layout, magnitude = b.AQ_ROPE_HALF, 1.0
+
+        def __init__(self, device):
+            self.device = device
+
+        @property
+        def freq(self):
+            with pytest.raises(ValueError, match="other tensors on"):
+                b.aq_rope(b.Rope(torch.zeros(32, dtype=torch.int64, device="meta")), pos, x)
+            return torch.zeros(32, dtype=torch.int64, device=self.device)
+
+    kv = b.KvCache.empty(2, 16, 2, 64, b.AQ_KV_E4M3, device="cpu")
+    slots = torch.zeros(3, dtype=torch.int64)
+    with pytest.raises(ValueError, match="Rope.freq: on meta, the call's other tensors on cpu"):
+        b.aq_kv_write(kv, x, x, slots, rope=Lazy("meta"), pos=pos)
+    with pytest.raises(ValueError, match="CUDA device"):
+        b.aq_kv_write(kv, x, x, slots, rope=Lazy("cpu"), pos=pos)
