@@ -541,7 +541,8 @@ def aq_mlp(gate: Theta, up: Theta, down: Theta, x, act=AQ_ACT_GELU_TANH, y=None,
 # ----------------------------------------------------------------------------------
 # serving: rotary positions, the paged key/value cache, drafted-token attention, verification. Their
 # tensors are marshalled by the compiled module _marshal (csrc/aq_python.cpp), which checks types, shapes and
-# strides, calls the entry point and returns its status.
+# strides, calls the entry point and returns its status. A call's tensors lie on the current device. With ``stream`` what a call
+# allocates comes from that stream's memory.
 # ----------------------------------------------------------------------------------
 _marshal = None
 

@@ -15,6 +15,7 @@
 #include <ATen/ops/empty.h>
 #include <ATen/ops/empty_like.h>
 #include <c10/cuda/CUDACachingAllocator.h>
+#include <c10/cuda/CUDAFunctions.h>
 #include <c10/cuda/CUDAGuard.h>
 #include <c10/cuda/CUDAStream.h>
 #include <math.h>
@@ -244,6 +245,13 @@ class Stream {
   void* handle = nullptr;
   bool read_from(PyObject* obj, const Tensor& on) {
     const bool gpu = on.t->is_cuda();
+    if (gpu) {   // the library takes the current device's facts and launches there
+      c10::DeviceIndex now = -1;
+      if (c10::cuda::GetDevice(&now) != cudaSuccess || now != on.t->get_device()) {
+        PyErr_Format(PyExc_ValueError, "the tensors of a call are on %s, which is not the current device", on.t->device().str().c_str());
+        return false;
+      }
+    }
     if (gpu) current_ = c10::cuda::getCurrentCUDAStream(on.t->get_device());
     if (obj == Py_None) {
       handle = gpu ? static_cast<void*>(current_->stream()) : nullptr;

@@ -252,3 +252,24 @@ def test_a_call_within_a_call_leaves_the_outer_ones_checks_alone():
         b.aq_kv_write(kv, x, x, slots, rope=Lazy("meta"), pos=pos)
     with pytest.raises(ValueError, match="CUDA device"):
         b.aq_kv_write(kv, x, x, slots, rope=Lazy("cpu"), pos=pos)
+
+
+@pytest.mark.parametrize("stream", [None, 0])
+def test_tensors_on_a_device_that_is_not_current_are_refused(stream):
+    """Tensors without memory stand for those of a device that is not current; the refusal comes before any device work."""
+    torch = pytest.importorskip("torch")
+    if torch.cuda.is_available():
+        pytest.skip("such tensors cannot be made beside a device")
+    from torch._subclasses.fake_tensor import FakeTensorMode
+    with FakeTensorMode():
+        make = lambda dtype: lambda *shape: torch.empty(*shape, dtype=dtype, device="cuda:1")  # noqa: E731
+        bf16, i32, i64, f32 = (make(d) for d in (torch.bfloat16, torch.int32, torch.int64, torch.float32))
+        rope, cache = b.Rope(i64(64)), b.KvCache(bf16(4, 2, 16, 128), bf16(4, 2, 16, 128))
+        x, pos, slots = bf16(3, 2, 128), i32(3), i64(3)
+        p, cu, u, noise, table, one = f32(4, 50), i32(2), f32(3), f32(1, 50), i32(1, 4), i32(1)
+    for call in (lambda: b.aq_rope(rope, pos, x, stream=stream), lambda: b.aq_kv_write(cache, x, x, slots, stream=stream),
+                 lambda: b.aq_kv_read(cache, slots, stream=stream),
+                 lambda: b.aq_tree_attention(cache, x, cu, one, table, max_q=3, stream=stream),
+                 lambda: b.aq_verify_drafts(p, pos, cu, u, noise, stream=stream)):
+        with pytest.raises(ValueError, match="are on cuda:1, which is not the current device"):
+            call()
