@@ -8,6 +8,8 @@ the CUDA kernels of ``libaq_gb300.so``; if that library is missing the first cal
 from __future__ import annotations
 
 import ctypes
+import functools
+import inspect
 import os
 from dataclasses import dataclass
 
@@ -240,6 +242,32 @@ def _stream(stream) -> int:
     return int(stream.cuda_stream) if hasattr(stream, "cuda_stream") else int(stream)
 
 
+def _on_its_stream(call):
+    """Makes a call that is given a stream allocate (and zero) from that stream's memory: under the current stream its
+    workspace would be the next request's there while the given stream's kernels still use it, and be zeroed in the wrong order.
+    What it returns is noted as used by the current stream too."""
+    place = list(inspect.signature(call).parameters).index("stream")
+
+    @functools.wraps(call)
+    def wrapper(*args, **kw):
+        stream = args[place] if len(args) > place else kw.get("stream")
+        if stream is None:
+            return call(*args, **kw)
+        import torch
+        current, handle = torch.cuda.current_stream(), _stream(stream)
+        if handle == 1:   # another name of the default stream
+            handle = 0
+        if handle == current.cuda_stream:
+            return call(*args, **kw)
+        with torch.cuda.stream(torch.cuda.ExternalStream(handle) if handle else torch.cuda.default_stream()):
+            out = call(*args, **kw)
+        for t in out if isinstance(out, (tuple, list)) else (out,):
+            if t.numel():
+                t.record_stream(current)
+        return out
+    return wrapper
+
+
 @dataclass
 class Theta:
     """A theta bundle on the device: W0 [out, in], s [out], U [out, r], V [in, r], each a
@@ -300,6 +328,7 @@ def new_workspace(nbytes: int, device):
 _workspace = new_workspace
 
 
+@_on_its_stream
 def aq_linear(theta: Theta, x, y=None, workspace=None, stream=None):
     """y = s * (W0 x) + U (V^T x) for x [M, in] -> y [M, out] (bf16)."""
     import torch
@@ -316,6 +345,7 @@ def aq_linear(theta: Theta, x, y=None, workspace=None, stream=None):
     return y
 
 
+@_on_its_stream
 def aq_linear_noalloc(theta: Theta, x, y=None, stream=None):
     """aq_linear without a workspace argument: the library's built-in scratch array is
     used, so the library itself allocates nothing (y is allocated here only if not
@@ -328,6 +358,7 @@ def aq_linear_noalloc(theta: Theta, x, y=None, stream=None):
     return y
 
 
+@_on_its_stream
 def aq_linear_qkv(thetas, x, ys=None, workspace=None, stream=None):
     """The q, k, v projections over one x in one pass; returns the three outputs."""
     import torch
@@ -348,6 +379,7 @@ def aq_linear_qkv(thetas, x, ys=None, workspace=None, stream=None):
     return ys
 
 
+@_on_its_stream
 def aq_linear_multi(thetas, x, ys=None, workspace=None, stream=None):
     """1..3 projections sharing one x (e.g. gate and up) in one pass; returns the outputs."""
     thetas = list(thetas)
@@ -367,6 +399,7 @@ def aq_linear_multi(thetas, x, ys=None, workspace=None, stream=None):
     return ys
 
 
+@_on_its_stream
 def aq_precompute(theta: Theta, W_eff=None, stream=None):
     """W_eff = diag(s) W0 + U V^T as a bf16 [out, in] tensor."""
     import torch
@@ -384,6 +417,7 @@ def nvfp4_scale_bytes(out: int, inp: int, layout: int) -> int:
     return -(-out // 128) * 128 * (-(-(inp // 16) // 4) * 4)
 
 
+@_on_its_stream
 def aq_precompute_nvfp4(theta: Theta, sf_layout: int = AQ_SF_LINEAR, global_scale=None, scale_given=None,
                         q=None, sf=None, workspace=None, stream=None):
     """W_eff quantized to NVFP4 without forming it in bf16: returns (q, sf, global_scale) with
@@ -425,6 +459,7 @@ def aq_selftest_bounded_wait(timeout_us: int, stream=None) -> None:
     _check(load().aq_selftest_bounded_wait(int(timeout_us), _stream(stream)))
 
 
+@_on_its_stream
 def aq_selftest_prefill_timeout(theta: Theta, x, timeout_us: int, y=None, workspace=None, stream=None):
     """aq_linear on the prefill GEMM with its t-flag wait made unreachable (test hook)."""
     M = int(x.shape[0])
@@ -470,6 +505,7 @@ def aq_status_string(st: int) -> str:
 # ----------------------------------------------------------------------------------
 # the decomposition (load time): band mean, least-squares scale and residual, randomized SVD
 # ----------------------------------------------------------------------------------
+@_on_its_stream
 def aq_band_mean(weights, W0=None, stream=None):
     """W0 = RN_bf16(mean of the band's bf16 [out, in] weights), on the GPU."""
     import torch
@@ -485,6 +521,7 @@ def aq_band_mean(weights, W0=None, stream=None):
     return W0
 
 
+@_on_its_stream
 def aq_ls_residual(weight, W0, s=None, resid=None, stream=None):
     """s = RN_bf16(per-row least-squares scale of W0 toward weight) and resid = weight − s·W0
     (float64), on the GPU. Returns (s, resid)."""
@@ -499,6 +536,7 @@ def aq_ls_residual(weight, W0, s=None, resid=None, stream=None):
     return s, resid
 
 
+@_on_its_stream
 def aq_randomized_svd(A, r, omega, power_iters=0, U=None, V=None, stream=None):
     """Rank-r factors (U [m, r], V [n, r], bf16) of the float64 matrix A by the randomized SVD
     with the caller's test matrix omega [n, k] (float64), on the GPU."""
@@ -525,6 +563,7 @@ def aq_mlp_workspace_bytes(gate: Theta, up: Theta, down: Theta, M: int) -> int:
     return int(load().aq_mlp_workspace_bytes(ctypes.byref(g), ctypes.byref(u), ctypes.byref(d), M))
 
 
+@_on_its_stream
 def aq_mlp(gate: Theta, up: Theta, down: Theta, x, act=AQ_ACT_GELU_TANH, y=None, workspace=None, stream=None):
     """y = down(act(gate(x)) * up(x)) with every projection a reconstruction linear."""
     M = int(x.size(0))
