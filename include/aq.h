@@ -517,8 +517,9 @@ aq_status aq_tree_attention(const aq_kv_cache* cache, const aq_draft_batch* batc
  *   n_accepted int32 [batch]; path int32 [batch, path_cap] (row stride ld_path): the accepted nodes' indices
  *              in order, then -1; the walk ends after path_cap of them; token int32 [batch]
  * max_nodes: at least the most nodes of a sequence (at most 1024). A node whose token lies outside the
- * vocabulary, or whose parent or row is out of range, is never accepted. Sums over the vocabulary are taken
- * in a fixed order. */
+ * vocabulary (-1, for one, where trees are padded to one shape), or whose parent or row is out of range,
+ * is left out: neither accepted nor refused, as though it were not there. Sums over the vocabulary are
+ * taken in a fixed order. */
 typedef enum aq_prob_type { AQ_PROB_F32 = 0, AQ_PROB_BF16 = 1 } aq_prob_type;
 #define AQ_MAX_DRAFT_NODES 1024
 aq_status aq_verify_drafts(int32_t batch, int32_t vocab, const int32_t* cu, const int32_t* tokens,

@@ -103,18 +103,19 @@ def verify(tokens, parent, p, u, noise, q=None, cap=None):
         for c in range(here + 1, n) if len(path) < cap else ():
             if parent[c] != here:
                 continue
-            x, known = tokens[c], 0 <= tokens[c] < len(target)
-            if known:
-                bar = u[c] * (1.0 - gone if q is None else q[here + 1][x])
-                near(bar, left[x])
-                if bar < left[x]:
-                    path.append(c)
-                    here, moved = c, True
-                    break
+            x = tokens[c]
+            if not 0 <= x < len(target):      # no token: no draft
+                continue
+            bar = u[c] * (1.0 - gone if q is None else q[here + 1][x])
+            near(bar, left[x])
+            if bar < left[x]:
+                path.append(c)
+                here, moved = c, True
+                break
             if q is not None:
                 left = np.maximum(left - np.asarray(q[here + 1], np.float64), 0.0)
                 left = left / left.sum() if left.sum() > 0 else left
-            elif known:
+            else:
                 gone += left[x]
                 left[x] = 0.0
         if not moved:

@@ -198,7 +198,7 @@ __global__ void __launch_bounds__(kVerThreads, kVerPerSm) aq_verify_kernel(const
     const int tok = p.tokens[first + i];
     const bool good = par >= -1 && par < i && tok >= 0 && tok < p.vocab;
     const int64_t row = row0 + 1 + par;
-    sh.parent[i] = par;
+    sh.parent[i] = good ? par : -2;   // no one's child: what was never drafted from q is not refused, either
     sh.tok[i] = tok;
     sh.px[i] = good ? prob(P, row * p.ld_p + tok) : 0.0f;
     sh.qx[i] = HASQ ? (good ? prob(Q, row * p.ld_q + tok) : 0.0f) : 1.0f;

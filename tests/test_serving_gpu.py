@@ -629,3 +629,23 @@ def test_verify_repeats_and_graph():
     a = run_verify(seqs, "wide")
     b = run_verify(seqs, "wide")
     assert all(torch.equal(x, y) for x, y in zip(a, b))
+
+
+@pytest.mark.parametrize("dtype", [torch.float32, torch.bfloat16], ids=["f32", "bf16"])
+@pytest.mark.parametrize("with_q", [True, False])
+def test_verify_padded_trees(with_q, dtype):
+    """Trees padded to one shape with nodes that have no token: as the oracle's, and as the trees without them."""
+    r = np.random.RandomState(31)
+    seqs = verify_inputs(30, [12] * 40, 1000, "wide", with_q)
+    for b, s in enumerate(seqs):
+        for i in range(12):
+            if r.rand() < (1.0 if b < 4 else 0.4):
+                s[0][i] = int(r.choice([-1, 1000, -2 ** 31]))
+    rnd = lambda x: None if x is None else torch.from_numpy(x).to(dtype).double().numpy()  # noqa: E731
+    count, path, token = (t.cpu().numpy() for t in run_verify(seqs, "wide", dtype, cap=12))
+    for b, (tokens, parent, p, q, u, noise) in enumerate(seqs):
+        want, nxt, margin = serving.verify(tokens, parent, rnd(p), u, noise, q=rnd(q), cap=12)
+        if b < 4:
+            assert nxt == int((rnd(p)[0] / noise.astype(np.float64)).argmax())
+        if margin >= 1e-5:
+            assert count[b] == len(want) and path[b].tolist() == want + [-1] * (12 - len(want)) and token[b] == nxt, b

@@ -126,3 +126,20 @@ def test_verification_limits():
     assert path == [] and token == 2
     # the walk ends at the cap, and its draw is from that row in full
     assert serving.verify([1, 2], None, p, [0.0, 0.0], [1, 1, 1, 0.5], cap=1)[:2] == ([0], 3)
+
+
+@pytest.mark.parametrize("q_given", [True, False])
+def test_padded_nodes_keep_the_targets_distribution(q_given):
+    """Nodes without a token (-1) are not there: alone, the draw is the target's; beside a real draft, as without them."""
+    r = np.random.RandomState(8)
+    V, n = 5, 3
+    p, q = _softmax(r.randn(n + 1, V) * 1.5), _softmax(r.randn(n + 1, V) * 1.5)
+    for _ in range(200):
+        u, noise = r.rand(n), r.exponential(size=V)
+        Q = q if q_given else None
+        path, token, _ = serving.verify([-1, V, -7], [-1, -1, 1], p, u, noise, q=Q)
+        assert path == [] and token == int((p[0] / noise).argmax())
+        x = int(r.choice(V, p=q[0]))
+        padded = serving.verify([-1, x, V], [-1, -1, -1], p, u, noise, q=Q)
+        plain = serving.verify([x], [-1], p[[0, 2]], u[1:2], noise, q=None if Q is None else q[[0, 2]])
+        assert [1] * len(plain[0]) == padded[0] and padded[1] == plain[1]
