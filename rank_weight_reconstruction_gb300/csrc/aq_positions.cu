@@ -187,8 +187,10 @@ struct Chunks {
   __device__ __forceinline__ int pair(int u, int i) const { return HALF ? u * 8 + i : (i < 4 ? c0 * 4 + i : c1 * 4 + i - 4); }
 };
 
+// second: whether b turns (interleaved, part of a head: a lane's second chunk may lie past rotary_dim, where a sine of 0 would
+// still make NaN of an infinity's neighbour).
 template <bool HALF>
-__device__ __forceinline__ void rotate16(float (&a)[8], float (&b)[8], const float (&c)[8], const float (&s)[8]) {
+__device__ __forceinline__ void rotate16(float (&a)[8], float (&b)[8], const float (&c)[8], const float (&s)[8], bool second) {
   if (HALF) {
 #pragma unroll
     for (int i = 0; i < 8; ++i) {
@@ -203,8 +205,9 @@ __device__ __forceinline__ void rotate16(float (&a)[8], float (&b)[8], const flo
       a[2 * i] = fmaf(x, c[i], -(y * s[i]));
       a[2 * i + 1] = fmaf(y, c[i], x * s[i]);
       const float z = b[2 * i], w = b[2 * i + 1];
-      b[2 * i] = fmaf(z, c[4 + i], -(w * s[4 + i]));
-      b[2 * i + 1] = fmaf(w, c[4 + i], z * s[4 + i]);
+      const float z1 = fmaf(z, c[4 + i], -(w * s[4 + i])), w1 = fmaf(w, c[4 + i], z * s[4 + i]);
+      b[2 * i] = second ? z1 : z;
+      b[2 * i + 1] = second ? w1 : w;
     }
   }
 }
@@ -281,7 +284,7 @@ __global__ void __launch_bounds__(256, 4) aq_positions_kernel(const __grid_const
     float a[8], b[8];
     unpack8(live ? r0 : make_uint4(0, 0, 0, 0), a);
     unpack8(live ? r1 : make_uint4(0, 0, 0, 0), b);
-    if (turns) rotate16<HALF>(a, b, c, s);
+    if (turns) rotate16<HALF>(a, b, c, s, ch.turns1);
     if (h < p.hq) {
       uint16_t* dst = p.qo + tt * p.qo_tok + h * p.qo_head;
       if (live) *reinterpret_cast<uint4*>(dst + ch.c0 * 8) = pack8(a);

@@ -649,3 +649,28 @@ def test_verify_padded_trees(with_q, dtype):
             assert nxt == int((rnd(p)[0] / noise.astype(np.float64)).argmax())
         if margin >= 1e-5:
             assert count[b] == len(want) and path[b].tolist() == want + [-1] * (12 - len(want)) and token[b] == nxt, b
+
+
+@pytest.mark.parametrize("layout", [aq.AQ_ROPE_HALF, aq.AQ_ROPE_INTERLEAVED], ids=["half", "interleaved"])
+@pytest.mark.parametrize("D,rot", [(128, 64), (128, 16), (256, 128), (64, 48), (80, 32)])
+def test_rotation_of_a_part_leaves_the_rest(layout, D, rot):
+    """What lies past rotary_dim comes through bit for bit: infinities, zeros of either sign, the largest and the smallest."""
+    r = np.random.RandomState(D + rot)
+    rest = torch.tensor([float("inf"), -0.0, -float("inf"), 0.0, 3e38, -1e-39, 1.0, -1.0])
+    x = randn(r, 9, 3, D)
+    x[..., rot:] = rest.repeat((D - rot + 7) // 8)[:D - rot].to(torch.bfloat16).cuda()
+    rope = aq.rope_frequencies(rot, layout=layout)
+    pos = torch.tensor([0, 1, 5, 100, 7, 8, 9, 1000, -3], dtype=torch.int32, device="cuda")
+    bits = lambda t: t.contiguous().view(torch.int16)  # noqa: E731
+    for inverse in (False, True):
+        y = aq.aq_rope(rope, pos, x, inverse=inverse)
+        assert torch.equal(bits(y[..., rot:]), bits(x[..., rot:]))
+        rope_ok(f64(y[..., :rot]), f64(x[..., :rot]), pos.cpu().numpy(), *serving.rope_angles(rot),
+                "half" if layout == aq.AQ_ROPE_HALF else "interleaved", inverse=inverse)
+    if D in (64, 128, 256):
+        cache = aq.KvCache.empty(2, 16, 3, D, aq.AQ_KV_BF16)
+        slots = torch.arange(9, device="cuda")
+        q = aq.aq_kv_write(cache, x, x, slots, rope=rope, pos=pos, q=x)
+        k, v = aq.aq_kv_read(cache, slots)
+        assert torch.equal(bits(q[..., rot:]), bits(x[..., rot:])) and torch.equal(bits(k[..., rot:]), bits(x[..., rot:]))
+        assert torch.equal(bits(v), bits(x))
