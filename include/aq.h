@@ -444,7 +444,8 @@ typedef struct aq_kv_cache {
 } aq_kv_cache;
 
 /* Writes the keys and values of T tokens into their slots (device int64 [T]; a slot outside the
- * cache, -1 for one, writes nothing; a slot named twice holds either token). With rope, keys are
+ * cache, -1 for one, writes nothing; the others must differ: a slot named twice in one call may hold
+ * parts of either token, codes of one under the scale of the other among them). With rope, keys are
  * rotated at pos[t] on the way; with q and q_out too, the queries are rotated in the same launch
  * (q_out may be q). E4M3: scale = max(max|x| / 448, 2^-100) over a token's head, taken after the
  * rotation and before any rounding, code = nearest E4M3 of x / scale, by the reciprocals of 448 and of

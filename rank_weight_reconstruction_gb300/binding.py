@@ -666,7 +666,7 @@ class KvCache:
 
 
 def aq_kv_write(cache: KvCache, k, v, slots, rope: Rope | None = None, pos=None, q=None, q_out=None, stream=None):
-    """Writes k and v [T, kv_heads, head_dim] into the cache's slots (int64 [T]), rotating k with
+    """Writes k and v [T, kv_heads, head_dim] into the cache's slots (int64 [T], each but once), rotating k with
     ``rope`` at ``pos``. With q [T, q_heads, head_dim] the rotated queries are returned too (into q_out,
     which may be q)."""
     return _serve().kv_write(cache, k, v, slots, rope, pos, q, q_out, _raw_stream(stream))
