@@ -1,7 +1,6 @@
 """Attention over tall row tiles (more than 32 rows of a key/value head, the tcgen05 kernel) at special values, with several key
-tiles. Tolerances: those of test_serving_items_gpu.
+tiles; and the bounds that include/aq.h states for an E4M3 cache, in both kernels. Tolerances: those of test_serving_items_gpu.
 """
-import numpy as np
 import pytest
 import torch
 
@@ -152,3 +151,35 @@ def test_left_out_pages_and_empty_rows(kind, D, T):
     see[:, 32:48] = False
     c.check(gone, lse)
     assert not torch.equal(gone[T:], full[T:])
+
+
+@pytest.mark.parametrize("D,T,group", [(64, 1, 4), (128, 2, 4), (128, 8, 4), (256, 8, 4), (64, 24, 4), (128, 64, 4), (256, 64, 2), (128, 30, 2)])
+def test_e4m3_queries_keep_elements_far_below_the_largest(D, T, group):
+    """One element of 1024 meets keys of zero there; the scores come from the elements 2^-18 to 2^-25 below it. (Held in fewer
+    bits or with less range they would be lost: every weight equal.)"""
+    c = Batch(D + T + 7, "e4m3", D, 1, group, 16, [90], [T], tree=True)
+    c.k = (c.k.float() * 2.0 ** 12).to(torch.bfloat16)
+    c.k[:, :, 0] = 0
+    c.write()
+    c.q = (torch.randn(*c.q.shape, generator=c.g, device="cuda") * 2.0 ** -11).to(torch.bfloat16)
+    c.q[:, :, 0] = 1024.0
+    out, lse = c.run()
+    c.check(out, lse)
+    c.q[:, :, 1:] = 0
+    assert float((c.run()[1] - lse).abs().min()) > 1e-3
+
+
+@pytest.mark.parametrize("D,T,group", [(64, 1, 1), (128, 2, 4), (128, 8, 4), (256, 8, 4), (64, 24, 4), (128, 64, 4), (256, 64, 2)])
+def test_e4m3_weights_have_eleven_bits(D, T, group):
+    """Two keys whose values nearly cancel: what is left shows the weights' own rounding, 2^-11 of a, and not bf16's 2^-8."""
+    c = Batch(D + T + 8, "e4m3", D, 1, group, 16, [2], [T], tree=True)
+    for i in range(T):     # every row sees the two context tokens alone
+        c.bits[0][i] = False
+    c.mask = torch.zeros_like(c.mask)
+    c.q = (c.q.float() * 0.5).to(torch.bfloat16)
+    c.v[0], c.v[1] = 448.0, -448.0
+    r = torch.randint(0, 8, (D,), generator=c.g, device="cuda")
+    c.v[1, 0] = -(torch.tensor([448.0, 416, 384, 352, 320, 288, 256, 240], device="cuda")[r]).to(torch.bfloat16)
+    c.v[1, 0, 0], c.v[0, 0, 1:] = -448.0, torch.tensor([448.0, 416, 384, 352, 320, 288, 256, 240], device="cuda")[r.flip(0)][1:].to(torch.bfloat16)
+    c.write()
+    c.check(*c.run())
