@@ -476,7 +476,8 @@ aq_status aq_kv_read(const aq_kv_cache* cache, const int64_t* slots, int64_t T, 
  * the weights enter the second product in bf16; with E4M3 they and the queries enter as f16, scaled by
  * powers of two: query elements below 2^-28 of their head's largest lose bits, and so do weights that, times
  * their value's scale (one below 2^-64 counts as that), lie below 2^-22 of the row's largest; below 2^-32
- * they are dropped.
+ * they are dropped. From the weights' sum (and lse) one drops out below 2^(e - 134) of the row's largest, 2^e
+ * being the largest scale that the row sees: nothing that counts until values pass 2^110.
  *   lse  fp32 [total_q, q_heads], log of the sum of exp(score), or NULL
  * Left out: keys past pages_per_seq pages, keys in pages outside the cache, rows past max_q of a
  * sequence or outside [0, total_q). Needs head_dim 64, 128 or 256 (AQ_ERR_UNSUPPORTED otherwise).
@@ -507,11 +508,11 @@ aq_status aq_tree_attention(const aq_kv_cache* cache, const aq_draft_batch* batc
  * cu[b] + b, then cu[b] + b + 1 + i for node i. Walking from the context, with r = p of the row:
  *   children c in index order: accepted when u[c] * q(x_c) < r(x_c), and the walk moves to c;
  *   a child refused makes r the normalised max(r - q, 0)
- * where q is the row (of the same index as r's) that the children were drawn from; q NULL says that
- * each draft was taken for certain, so that a refused token's r becomes 0. At the end of the walk, the
- * next token is the v with the largest r(v) / noise[b, v], the lowest of equal ones; where r has no mass
- * left, r = p. With u uniform in [0, 1) and noise exponential with mean 1, the tokens are distributed as
- * the target's own.
+ * where q is the row (of the same index as r's) that the children were drawn from, each independently of
+ * its siblings (with replacement); q NULL says that each draft was taken for certain, so that a refused
+ * token's r becomes 0. At the end of the walk, the next token is the v with the largest r(v) / noise[b, v],
+ * the lowest of equal ones; where r has no mass left, r = p. With u uniform in [0, 1) and noise
+ * exponential with mean 1, the tokens are distributed as the target's own.
  *   p_type     AQ_PROB_F32 or AQ_PROB_BF16, of p and q; rows of `vocab` (up to 2^30), row strides ld_p and ld_q; rows:
  *              number of rows of p and of q
  *   u [nodes], noise [batch, vocab] (row stride ld_noise): fp32

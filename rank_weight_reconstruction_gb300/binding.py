@@ -638,7 +638,8 @@ def rope_frequencies(rotary_dim: int, base: float = 10000.0, scaling: int = AQ_R
 
 def aq_rope(rope: Rope, pos, x, inverse: bool = False, y=None, stream=None):
     """x [T, heads, head_dim] (bf16, any token and head strides) rotated at positions pos (int32 [T]);
-    ``inverse`` turns back, which is the gradient of the rotation. y may be x."""
+    ``inverse`` turns back, which is the gradient of the rotation. y may be x. Like every call here it records no
+    history: a training step makes the inverse call itself, on the gradient of y."""
     return _serve().rope(rope, pos, x, y, inverse, _raw_stream(stream))
 
 

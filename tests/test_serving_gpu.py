@@ -674,3 +674,23 @@ def test_rotation_of_a_part_leaves_the_rest(layout, D, rot):
         k, v = aq.aq_kv_read(cache, slots)
         assert torch.equal(bits(q[..., rot:]), bits(x[..., rot:])) and torch.equal(bits(k[..., rot:]), bits(x[..., rot:]))
         assert torch.equal(bits(v), bits(x))
+
+
+def test_rotation_records_no_history_and_its_inverse_is_the_backward_pass():
+    """As the call's documentation says: used in a step of torch's own by a function whose backward pass is the inverse call."""
+    r = np.random.RandomState(40)
+    x, g = randn(r, 6, 2, 64).requires_grad_(), randn(r, 6, 2, 64)
+    rope, pos = aq.rope_frequencies(64), torch.arange(6, dtype=torch.int32, device="cuda") * 50
+    assert not aq.aq_rope(rope, pos, x).requires_grad
+
+    class Turn(torch.autograd.Function):
+        @staticmethod
+        def forward(ctx, x):
+            return aq.aq_rope(rope, pos, x)
+
+        @staticmethod
+        def backward(ctx, g):
+            return aq.aq_rope(rope, pos, g, inverse=True)
+
+    Turn.apply(x).backward(g)
+    rope_ok(f64(x.grad), f64(g), pos.cpu().numpy(), *serving.rope_angles(64), "half", inverse=True)
