@@ -119,10 +119,11 @@ enum Draw { kPlain, kOnce, kSeveral };
 template <typename T, Draw MODE, int N>
 __device__ __forceinline__ void race(const T* pr, const T* qr, const float* er, int vocab, int k, const VerShared& sh,
                                      int rank, int cluster, float& best, int& at) {
-  // A quotient can pass the warp's best so far only if w > best e (1 - 2^-21), rounding included: one product and
+  // A quotient can pass the warp's best so far only if w > best e (1 - 2^-21), rounding included: one fused product and
   // one comparison a word, and the divisions only where some word of a thread's batch gets that far. Words equal to
-  // the best pass too, and the lowest index is sorted out when the threads' bests meet.
-  float bar = 0.0f;
+  // the best pass too, and the lowest index is sorted out when the threads' bests meet. Where the product is below the
+  // normal numbers its rounding has no such bound: 2^-126 less covers that, and changes no product above 2^-102.
+  float bar = 0.0f, slack = 0.0f;
   auto weigh = [&](float w, float q) { return MODE == kPlain ? w : MODE == kOnce ? fmaxf(w - q, 0.0f) : residual(w, q, k, k - 1, sh.zinv); };
   auto offer = [&](float w, float e, int v) {
     const float s = __fdiv_rn(w, e);
@@ -153,7 +154,7 @@ __device__ __forceinline__ void race(const T* pr, const T* qr, const float* er, 
 #pragma unroll
       for (int i = 0; i < N; ++i) {
         if (MODE != kPlain) w[j].x[i] = weigh(w[j].x[i], q[j].x[i]);
-        hit = hit || w[j].x[i] > bar * e[j].x[i];
+        hit = hit || w[j].x[i] > fmaf(bar, e[j].x[i], slack);
       }
     if (__any_sync(0xffffffffu, hit)) {
       if (hit) {
@@ -161,15 +162,16 @@ __device__ __forceinline__ void race(const T* pr, const T* qr, const float* er, 
         for (int j = 0; j < U; ++j)
 #pragma unroll
           for (int i = 0; i < N; ++i)
-            if (w[j].x[i] > bar * e[j].x[i]) offer(w[j].x[i], e[j].x[i], v + j * step + i);
+            if (w[j].x[i] > fmaf(bar, e[j].x[i], slack)) offer(w[j].x[i], e[j].x[i], v + j * step + i);
       }
       bar = __uint_as_float(__reduce_max_sync(0xffffffffu, __float_as_uint(best))) * (1.0f - 0x1p-21f);
+      slack = bar > 0.0f ? -0x1p-126f : 0.0f;
     }
   }
   for (; v < vocab; v += step)
     for (int i = 0; i < N && v + i < vocab; ++i) {
       const float w = weigh(prob(pr, v + i), MODE != kPlain ? prob(qr, v + i) : 0.0f), e = er[v + i];
-      if (w > bar * e) offer(w, e, v + i);
+      if (w > fmaf(bar, e, slack)) offer(w, e, v + i);
     }
 }
 

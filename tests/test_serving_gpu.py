@@ -694,3 +694,20 @@ def test_rotation_records_no_history_and_its_inverse_is_the_backward_pass():
 
     Turn.apply(x).backward(g)
     rope_ok(f64(x.grad), f64(g), pos.cpu().numpy(), *serving.rope_angles(64), "half", inverse=True)
+
+
+@pytest.mark.parametrize("dtype", [torch.float32, torch.bfloat16], ids=["f32", "bf16"])
+def test_verify_draws_among_subnormal_probabilities(dtype):
+    """Rows whose probabilities, or whose noise, lie below the normal numbers: the largest quotient, the lowest of equal ones."""
+    r = np.random.RandomState(50)
+    B, V = 64, 5000
+    unit = 2.0 ** -149 if dtype == torch.float32 else 2.0 ** -133
+    p = torch.from_numpy((r.randint(0, 12, (B, V)) * unit).astype(np.float32)).to(dtype).cuda()
+    p[1::2] = torch.from_numpy(r.rand(B // 2, V).astype(np.float32)).to(dtype).cuda()
+    noise = (r.exponential(size=(B, V)) + 1e-6).astype(np.float32)
+    noise[1::2] = (r.randint(1, 50, (B // 2, V)) * 2.0 ** -149).astype(np.float32)
+    p[1::2] *= 2.0 ** -30    # quotients that fp32 holds
+    empty, none = torch.zeros(0, dtype=torch.int32, device="cuda"), torch.zeros(0, device="cuda")
+    _, _, token = aq.aq_verify_drafts(p, empty, torch.zeros(B + 1, dtype=torch.int32, device="cuda"), none, torch.from_numpy(noise).cuda())
+    score = (p.double().cpu().numpy() / noise.astype(np.float64)).astype(np.float32)      # to fp32 as the kernel divides
+    assert np.array_equal(token.cpu().numpy(), score.argmax(1))
