@@ -124,6 +124,8 @@ class Batch:
         K, V, S = self.stored()
         worst = 0.0
         for b, (c, t) in enumerate(zip(self.ctx, self.T)):
+            if t == 0:
+                continue
             at = slice(int(self.first[b]), int(self.first[b + 1]))
             see = self.seen(b)
             # [heads, t, group, ...]
@@ -230,3 +232,48 @@ def test_items_repeat_bit_for_bit(kind, D, group):
         again = c.run()
         d.run()
         assert torch.equal(out, again[0]) and torch.equal(lse, again[1])
+
+
+@KINDS
+@DIMS
+@pytest.mark.parametrize("T", [[0, 64, 1, 0, 0, 33], [0, 1, 3, 0], [0, 0, 0, 5]], ids=["tall", "short", "few"])
+def test_sequences_without_rows_between_others(kind, D, T):
+    r = np.random.RandomState(D + 9)
+    drafted = [T[i % len(T)] for i in range(90)]
+    c = Batch(D + 9, kind, D, 2, 2, 16, [int(x) for x in r.randint(0, 400, 90)], drafted, tree=True)
+    c.check(*c.run())
+
+
+@KINDS
+@DIMS
+@pytest.mark.parametrize("T", [1, 3, 6, 9])
+def test_short_items_repeat_bit_for_bit(kind, D, T):
+    """The same for row tiles of 8, 16 and 32, with tall calls in between."""
+    r = np.random.RandomState(T)
+    c = Batch(D + T, kind, D, 2, 4, 32, [int(x) for x in r.randint(0, 700, 170)], [1 + i % T for i in range(170)])
+    d = Batch(D + 8, kind, D, 1, 4, 32, [int(x) for x in r.randint(0, 300, 40)], [40] * 40, gain=30.0)
+    out, lse = c.run()
+    c.check(out, lse)
+    for _ in range(10):
+        d.run()
+        again = c.run()
+        assert torch.equal(out, again[0]) and torch.equal(lse, again[1])
+
+
+@KINDS
+@DIMS
+@pytest.mark.parametrize("T", [5, 40, 64])
+def test_strided_rows(kind, D, T):
+    """Queries as columns of a wider row, outputs with heads outermost or as columns; nothing beside them is written."""
+    c = Batch(D + T, kind, D, 2, 4, 32, [500, 3, 77], [T, 1, T - 2], tree=True)
+    want, lse = c.run()
+    total = c.q.size(0)
+    wide = torch.full((total, 10 * D), float("nan"), dtype=torch.bfloat16, device="cuda")
+    wide[:, D:9 * D] = c.q.flatten(1)
+    c.q = wide[:, D:9 * D].unflatten(1, (8, D))
+    heads = torch.full((8, total + 2, D), 7.0, dtype=torch.bfloat16, device="cuda")
+    got, _ = c.run(out=heads[:, 1:-1].transpose(0, 1))
+    assert torch.equal(got, want) and bool((heads[:, 0] == 7).all()) and bool((heads[:, -1] == 7).all())
+    cols = torch.full((total, 10 * D), 7.0, dtype=torch.bfloat16, device="cuda")
+    c.run(out=cols[:, D:9 * D].unflatten(1, (8, D)))
+    assert torch.equal(cols[:, D:9 * D].unflatten(1, (8, D)), want) and bool((cols[:, :D] == 7).all()) and bool((cols[:, 9 * D:] == 7).all())
