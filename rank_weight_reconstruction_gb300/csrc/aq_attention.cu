@@ -24,8 +24,8 @@
 // bf16 cache the weights are rounded to bf16 (2^-9).
 //
 // Measured, 32 query and 8 key/value heads of 128: 48 sequences of one token over 750 to 6000 E4M3 keys 64 us
-// (343 MB: 5350 GB/s), 32 trees of 8 over 1024 to 8192 bf16 keys 126 us (609 MB: 4820 GB/s); eight tokens over 60000
-// keys 92 us (6150 GB/s). What the short calls pay beside the stream is the start (locating the work and the first loads, about
+// (343 MB: 5390 GB/s), over bf16 keys 106 us (665 MB: 6300 GB/s), 32 trees of 8 over 1024 to 8192 bf16 keys 126 us (609 MB: 4820
+// GB/s); eight sequences of one token over 7500 to 60000 E4M3 keys 94 us (6090 GB/s), over 60000 each 158 us (6410). What the short calls pay beside the stream is the start (locating the work and the first loads, about
 // 6 us) and the joining launch (about 4).
 #include <math.h>
 

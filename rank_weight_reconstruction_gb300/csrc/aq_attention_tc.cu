@@ -15,10 +15,12 @@
 // E4M3 codes are widened to f16 tiles in shared memory by four warps in between (exact), once for all rows; scales
 // and f16 scaling as in the mma.sync kernel.
 //
-// Measured, eight trees of 64 over 32768 keys, 32 query and 8 key/value heads (256 rows an item): D = 128 bf16 218 to 238 us
-// (1160 to 1260 TFLOP/s, 4550 to 4970 GB/s), of which about 190 are the stream at 3330 clocks a pair of 128-key tiles (the products
-// alone 2050), the rest starts, ends of items and the joining launch; E4M3 307 to 313 us (a scale
-// on every score and every weight, beside the widening's instructions), D = 64 177, D = 256 645 (one row tile, and 64-key products that re-read Q).
+// Measured, eight trees of 64 over 32768 keys, 32 query and 8 key/value heads (256 rows an item): D = 128 bf16 220 to 225 us in a
+// graph, 240 a call (1150 to 1250 TFLOP/s, 4520 to 4930 GB/s), of which about 190 are the stream at 3330 clocks a pair of 128-key tiles (the products
+// alone 2050), the rest starts, ends of items and the joining launch; E4M3 299 to 313 us (a scale
+// on every score and every weight, beside the widening's instructions), D = 64 173, D = 256 650 (one row tile, and 64-key products that
+// re-read Q). Chunks of 512 tokens of four prompts over 4096 keys: bf16 177 us (826 TFLOP/s), E4M3 283; one of 4096 from the start 528
+// (260: every key of the chunk is a masked one).
 #include <math.h>
 
 #include <algorithm>

@@ -19,8 +19,9 @@
 // each other), so a vector is loaded in whole 128-byte lines and its maximum is a few shuffles. The
 // eight sines and cosines of a lane depend on the token alone, so a group walks several heads of its token
 // with them in registers, two heads' loads in flight. Measured: a
-// rotation of 8192 tokens x 32 heads of 128 (64 of them turned) 19.0 us (134 MB: 7050 GB/s), of 4099 x 16, heads outermost, 7.1 us
-// (34 MB: 4740 GB/s, start and end included); an E4M3 write of 8192 tokens with 32 query and 8 key/value heads of
+// rotation of 8192 tokens x 32 heads of 128 (64 of them turned) 19.3 us in a graph (134 MB, of whose writes most are still in L2 at
+// the launch's end; calls one after another 23.3 us: 5770 GB/s), of 4099 x 16, heads outermost, 7.0 us
+// (34 MB: 4770 GB/s, start and end included); an E4M3 write of 8192 tokens with 32 query and 8 key/value heads of
 // 128 and its read back 44.7 us together (236 MB: 5280 GB/s), of which the write takes about 34; calls of a few tokens 2.2 us.
 #include <math.h>
 

@@ -4,8 +4,9 @@
 // A decode step makes these calls one after another on a few tokens, each a launch of a few microseconds, and what
 // a call costs the host decides the step's time. Converted in Python (shapes, strides, pointers, then up to 23 ctypes
 // arguments) a call took 13 to 18 us, its kernel 2 to 10. Here the tensors are read as the C++ objects they are and
-// the outputs allocated without passing through Python: 2.2 to 4.7 us a call, launch and outputs included (a rotation of
-// one token 4.4 us where the attributes read in C and torch.empty took 10.7; a cache write and its read 10.2 where 28.3).
+// the outputs allocated without passing through Python: 2.4 us a call with outputs given, launch included, and 4.5 to 7.3 with outputs
+// made, from process to process (a rotation of one token 4.8 us where the attributes read in C and torch.empty took 10.7; a cache
+// write and its read 11.1 where 28.3).
 // The module is given the library's entry points by address, so that it serves whichever build of the library the binding
 // has loaded, and a function of the binding that raises for an aq_status.
 #define PY_SSIZE_T_CLEAN
