@@ -383,7 +383,7 @@ __device__ __forceinline__ void step(const AttnParams& p, const AttnShared& sh, 
         }
       }
   }
-  float vs[KT][2], ve[KT][2], vtop = 0.0f;   // values' scales, their exponents, the lane's largest
+  float vs[KT][2], ve[KT][2];   // values' scales; what they add to their keys' logits in the reference
 #pragma unroll
   for (int j = 0; j < KT; ++j)
 #pragma unroll
@@ -393,8 +393,7 @@ __device__ __forceinline__ void step(const AttnParams& p, const AttnShared& sh, 
       if constexpr (S::E4M3) {
         const float ks = ksc[k0 + 16 * j + 8 * h + g];
         vs[j][h] = vsc[k0 + 16 * j + 8 * h + g];
-        vtop = fmaxf(vtop, vs[j][h]);
-        if (!WHOLE) ve[j][h] = scale_exponent(vs[j][h]);
+        ve[j][h] = scale_log2(vs[j][h]) - kTop;
 #pragma unroll
         for (int n = 0; n < NR; ++n) {
           sc[j][n][2 * h] *= ks;
@@ -402,20 +401,25 @@ __device__ __forceinline__ void step(const AttnParams& p, const AttnShared& sh, 
         }
       }
     }
-  // What the reference has to cover: the logits, and with E4M3 the exponents of the values' scales on them. Looked
-  // at by each lane for itself (where all is seen by its largest logit and its largest scale), put together only
-  // where one lane's passes the reference.
+  // What the reference has to cover: the logits, and with E4M3 the values' scales on them. Looked at by each lane for
+  // itself, put together only where one lane's passes the reference.
   float mt[NR][2];
   if constexpr (WHOLE) {
-    const float e = S::E4M3 ? scale_exponent(vtop) - kTop : 0.0f;
 #pragma unroll
     for (int n = 0; n < NR; ++n)
 #pragma unroll
       for (int c = 0; c < 2; ++c) {
-        float x = fmaxf(sc[0][n][c], sc[0][n][2 + c]);
+        if constexpr (S::E4M3) {
+          mt[n][c] = -INFINITY;
 #pragma unroll
-        for (int j = 1; j < KT; ++j) x = fmaxf(x, fmaxf(sc[j][n][c], sc[j][n][2 + c]));
-        mt[n][c] = x == -INFINITY ? x : fmaf(x, fac[n][c], e);
+          for (int j = 0; j < KT; ++j)
+            mt[n][c] = fmaxf(mt[n][c], fmaxf(fmaf(sc[j][n][c], fac[n][c], ve[j][0]), fmaf(sc[j][n][2 + c], fac[n][c], ve[j][1])));
+        } else {
+          float x = fmaxf(sc[0][n][c], sc[0][n][2 + c]);
+#pragma unroll
+          for (int j = 1; j < KT; ++j) x = fmaxf(x, fmaxf(sc[j][n][c], sc[j][n][2 + c]));
+          mt[n][c] = x == -INFINITY ? x : x * fac[n][c];
+        }
       }
   } else {
     const uint32_t bits = seen_bits(p, span, sh.i[info.rg * 8 * NR + min(lane, 8 * NR - 1)], sh.pos[info.rg * 8 * NR + min(lane, 8 * NR - 1)],
@@ -432,7 +436,7 @@ __device__ __forceinline__ void step(const AttnParams& p, const AttnShared& sh, 
           for (int h = 0; h < 2; ++h) {
             float& x = sc[j][n][2 * h + c];
             if (!((mine_bits >> (16 * j + 8 * h)) & 1)) x = -INFINITY;
-            if (x != -INFINITY) mt[n][c] = fmaxf(mt[n][c], fmaf(x, fac[n][c], S::E4M3 ? ve[j][h] - kTop : 0.0f));
+            if (x != -INFINITY) mt[n][c] = fmaxf(mt[n][c], fmaf(x, fac[n][c], ve[j][h]));
           }
       }
   }

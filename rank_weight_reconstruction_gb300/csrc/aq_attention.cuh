@@ -75,8 +75,10 @@ constexpr int kAttnSmsBound = 192;      // SMs (of any sm_103 part) and CTAs an 
 constexpr int kAttnMaxPerSm = 2;        // workspace without a device
 // The reference that a row's weights are taken against may lag by this power of two before the sums are scaled over.
 constexpr float kLag = 6.0f;
-// E4M3: the reference also follows the values' scales, so that a weight times its value's scale, in f16, stays
-// below 2^(kTop + kLag + 1) = 2^15. Scales under 2^kLeast count as that: the weights' own sum stays finite.
+// E4M3: the reference is that of the weights times their values' scales, key by key (the largest logit and the largest scale by
+// themselves may be different keys', and their product far above every key's), so that such a product, in f16, stays below
+// 2^(kTop + kLag + 1) = 2^15, and the largest is not below 2^kTop. Scales under 2^kLeast count as that: the weights' own sum
+// stays finite.
 constexpr int kTop = 8;
 constexpr int kLeast = -64;
 
@@ -114,11 +116,13 @@ __device__ __forceinline__ float pow2(int e) { return __int_as_float((e + 127) <
 // Exponent of a non-negative value, kept where 2^(14 - e) and 2^(e - 14) are finite; zero counts as 2^-112.
 __device__ __forceinline__ int top_exponent(float x) { return min(max(static_cast<int>(__float_as_uint(x) >> 23) - 127, -112), 126); }
 
-// ... of a value's scale, for the reference. The scale of a vector that reads as NaN counts as the smallest: its key's weight
-// belongs in the row's sum like any other, and against a reference 2^120 above it the sum (and lse) would lose the rest.
-__device__ __forceinline__ float scale_exponent(float x) {
-  const int e = static_cast<int>((__float_as_uint(x) >> 23) & 0xff) - 127;
-  return static_cast<float>(e == 128 ? kLeast : max(e, kLeast));
+// Logarithm (base 2) of a value's scale, for the reference. The scale of a vector that reads as NaN counts as the smallest: its
+// key's weight belongs in the row's sum like any other, and against a reference 2^120 above it the sum (and lse) would lose
+// the rest.
+__device__ __forceinline__ float scale_log2(float x) {
+  float r;
+  asm("lg2.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(x));
+  return fminf(fmaxf(r, static_cast<float>(kLeast)), 127.0f);
 }
 
 // Keys [lo, hi) and tiles [t0, t1) that the rows of entry (sequence b, row tile rt) can see.

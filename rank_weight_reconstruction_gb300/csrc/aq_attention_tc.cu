@@ -17,7 +17,7 @@
 //
 // Measured, eight trees of 64 over 32768 keys, 32 query and 8 key/value heads (256 rows an item): D = 128 bf16 220 to 225 us in a
 // graph, 240 a call (1150 to 1250 TFLOP/s, 4520 to 4930 GB/s), of which about 190 are the stream at 3330 clocks a pair of 128-key tiles (the products
-// alone 2050), the rest starts, ends of items and the joining launch; E4M3 299 to 313 us (a scale
+// alone 2050), the rest starts, ends of items and the joining launch; E4M3 317 us (a scale
 // on every score and every weight, beside the widening's instructions), D = 64 173, D = 256 650 (one row tile, and 64-key products that
 // re-read Q). Chunks of 512 tokens of four prompts over 4096 keys: bf16 177 us (826 TFLOP/s), E4M3 283; one of 4096 from the start 528
 // (260: every key of the chunk is a masked one).
@@ -51,7 +51,7 @@ struct TcShape {
   static constexpr int kConvWarp = kSoftWarps;             // first of four converting warps (E4M3)
   static constexpr int kTmaWarp = kSoftWarps + (E4M3 ? 4 : 0), kMmaWarp = kTmaWarp + 1;
   // Two row tiles of an E4M3 cache: 16 warps launched with 128 registers a thread, of which the weighing warps take a
-  // part from the others (256 x 176 + 128 x 88 + 128 x 72 = 65536 = 512 x 128): 307 to 313 us against 342 without.
+  // part from the others (256 x 176 + 128 x 88 + 128 x 72 = 65536 = 512 x 128): 307 to 313 us against 342 without, then.
   static constexpr bool kSplitRegs = E4M3 && TILES == 2;
   static constexpr int kThreads = kSplitRegs ? 512 : (kMmaWarp + 1) * 32;
   // tensor memory: two score buffers, one a row tile or two of one tile (the weights over them), then the sums
@@ -689,20 +689,12 @@ __device__ __forceinline__ void tc_weigh(const AttnParams& p, TcShared& sh, uint
       }
       if (!wait(&sh.s_full[x], x_parity)) return;
       tc_fence_after();
-      auto tile_scale = [&]() {   // the tile's largest scale of a value, but for NaN
-        const float* f = reinterpret_cast<const float*>(vs);
-        uint32_t big = 0;
-#pragma unroll
-        for (int k = 0; k < BN / 32; ++k) {
-          const uint32_t bits = __float_as_uint(f[32 * k + lane]);
-          big = max(big, bits < 0x7f800000u ? bits : 0u);
-        }
-        return __uint_as_float(__reduce_max_sync(0xffffffffu, big));
-      };
       bool done = false;
       if (live_warp && whole && it > 0) {
-        // One pass, the weights taken against the reference as it stands; the largest logit is looked at afterwards, and
-        // where it has passed the reference (rare past an item's first tiles) the tile is done again below.
+        // One pass, the weights taken against the reference as it stands; the largest logit (E4M3: with the tile's largest scale
+        // of a value, which is no less than any key's own) is looked at afterwards, and where it has passed the reference (rare
+        // past an item's first tiles) the tile is done again below. (The largest product of weight and scale itself, as fp32 or
+        // in the packed pairs, is known a step later: trees of 64 over 32768 E4M3 keys 323 us against 319.)
         const float mz = m == -INFINITY ? 0.0f : m;
         uint32_t pk[BN / 2];
         float sum[4] = {0.0f, 0.0f, 0.0f, 0.0f}, mx[2] = {-INFINITY, -INFINITY};
@@ -741,12 +733,22 @@ __device__ __forceinline__ void tc_weigh(const AttnParams& p, TcShared& sh, uint
             pk[16 * c + e / 2 + 1] = S::E4M3 ? pack_f16x2(y[e + 2], y[e + 3]) : pack_bf16x2_cvt(y[e + 2], y[e + 3]);
           }
         }
+        const float tile_sum = (sum[0] + sum[1]) + (sum[2] + sum[3]);
         const float big = fmaxf(mx[0], mx[1]);
         float cover = 0.0f;
-        if constexpr (S::E4M3) cover = scale_exponent(tile_scale()) - kTop;
+        if constexpr (S::E4M3) {
+          const float* f = reinterpret_cast<const float*>(vs);
+          uint32_t most = 0;   // but for NaN
+#pragma unroll
+          for (int k = 0; k < BN / 32; ++k) {
+            const uint32_t bits = __float_as_uint(f[32 * k + lane]);
+            most = max(most, bits < 0x7f800000u ? bits : 0u);
+          }
+          cover = scale_log2(__uint_as_float(__reduce_max_sync(0xffffffffu, most))) - kTop;
+        }
         const float want = big == -INFINITY ? big : fmaf(big, fac, cover);
         if (!__any_sync(0xffffffffu, lane < count && want > m + kLag)) {
-          l += (sum[0] + sum[1]) + (sum[2] + sum[3]);
+          l += tile_sum;
 #pragma unroll
           for (int c = 0; c < BN / 32; ++c) tmem_st16u(s_addr + 16 * c, reinterpret_cast<const uint32_t(&)[16]>(pk[16 * c]));
           tmem_st_wait();
@@ -754,7 +756,7 @@ __device__ __forceinline__ void tc_weigh(const AttnParams& p, TcShared& sh, uint
         }
       }
       if (live_warp && !done) {
-        // the row's largest logit, and what the reference has to cover
+        // what the reference has to cover: the row's largest logit, with E4M3 key by key with the values' scales
         float want = -INFINITY;
         if (whole) {
           float mx = -INFINITY;
@@ -765,17 +767,16 @@ __device__ __forceinline__ void tc_weigh(const AttnParams& p, TcShared& sh, uint
             if constexpr (S::E4M3) {
 #pragma unroll
               for (int e = 0; e < 8; ++e) {
-                const float4 f = ks[8 * c + e];
-                mx = fmaxf(fmaxf(fmaxf(mx, v[4 * e] * f.x), fmaxf(v[4 * e + 1] * f.y, v[4 * e + 2] * f.z)), v[4 * e + 3] * f.w);
+                const float4 kf = ks[8 * c + e], vf = vs[8 * c + e];
+                mx = fmaxf(fmaxf(mx, fmaf(v[4 * e] * kf.x, fac, scale_log2(vf.x))), fmaf(v[4 * e + 1] * kf.y, fac, scale_log2(vf.y)));
+                mx = fmaxf(fmaxf(mx, fmaf(v[4 * e + 2] * kf.z, fac, scale_log2(vf.z))), fmaf(v[4 * e + 3] * kf.w, fac, scale_log2(vf.w)));
               }
             } else {
 #pragma unroll
               for (int e = 0; e < 32; e += 2) mx = fmaxf(mx, fmaxf(v[e], v[e + 1]));
             }
           }
-          float e = 0.0f;
-          if constexpr (S::E4M3) e = scale_exponent(tile_scale()) - kTop;
-          want = mx == -INFINITY ? mx : fmaf(mx, fac, e);
+          want = S::E4M3 ? mx - kTop : mx == -INFINITY ? mx : mx * fac;
         } else {
 #pragma unroll 1
           for (int c = 0; c < BN / 32; ++c) {
@@ -793,7 +794,7 @@ __device__ __forceinline__ void tc_weigh(const AttnParams& p, TcShared& sh, uint
 #pragma unroll
               for (int k = 0; k < 4; ++k) {
                 const float y = S::E4M3 ? v[e + k] * k4[k] : v[e + k];
-                const float z = fmaf(y, fac, S::E4M3 ? scale_exponent(v4[k]) - kTop : 0.0f);
+                const float z = fmaf(y, fac, S::E4M3 ? scale_log2(v4[k]) - kTop : 0.0f);
                 const bool in = ((bits >> (e + k)) & 1) != 0 & (y != -INFINITY);
                 want = fmaxf(want, in ? z : -INFINITY);
               }
@@ -827,6 +828,7 @@ __device__ __forceinline__ void tc_weigh(const AttnParams& p, TcShared& sh, uint
           float v[32];
           tmem_ld32(s_addr + 32 * c, v);
           uint32_t pk[16];
+          float part = 0.0f;
 #pragma unroll
           for (int e = 0; e < 8; ++e) {
             float4 kf = make_float4(1.0f, 1.0f, 1.0f, 1.0f), vf = kf;
@@ -840,7 +842,7 @@ __device__ __forceinline__ void tc_weigh(const AttnParams& p, TcShared& sh, uint
               const float y = S::E4M3 ? v[4 * e + k] * k4[k] : v[4 * e + k];
               float u = ex2(fmaf(y, fac, -mz));
               if (!whole && (!((bits >> (4 * e + k)) & 1) || y == -INFINITY)) u = 0.0f;
-              l += u;
+              part += u;
               if (S::E4M3) {
                 u *= v4[k];
                 if (!whole && !((bits >> (4 * e + k)) & 1)) u = 0.0f;   // whatever scale lies there
@@ -850,6 +852,7 @@ __device__ __forceinline__ void tc_weigh(const AttnParams& p, TcShared& sh, uint
             pk[2 * e] = S::E4M3 ? pack_f16x2(v[4 * e], v[4 * e + 1]) : pack_bf16x2_cvt(v[4 * e], v[4 * e + 1]);
             pk[2 * e + 1] = S::E4M3 ? pack_f16x2(v[4 * e + 2], v[4 * e + 3]) : pack_bf16x2_cvt(v[4 * e + 2], v[4 * e + 3]);
           }
+          l += part;
           tmem_st16u(s_addr + 16 * c, pk);   // over scores already read
         }
         tmem_st_wait();

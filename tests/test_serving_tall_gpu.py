@@ -183,3 +183,22 @@ def test_e4m3_weights_have_eleven_bits(D, T, group):
     c.v[1, 0, 0], c.v[0, 0, 1:] = -448.0, torch.tensor([448.0, 416, 384, 352, 320, 288, 256, 240], device="cuda")[r.flip(0)][1:].to(torch.bfloat16)
     c.write()
     c.check(*c.run())
+
+
+@pytest.mark.parametrize("spread", [12, 40])
+@pytest.mark.parametrize("D,T,group", [(64, 1, 4), (128, 1, 4), (128, 8, 4), (256, 8, 4), (64, 24, 4), (64, 64, 4), (128, 24, 4), (128, 64, 4), (256, 64, 2)])
+def test_e4m3_large_logits_on_keys_of_small_values(D, T, group, spread):
+    """Context in which every other key has the larger logit, by about `spread` powers of two, and values smaller by as many: no
+    key's weight times scale is far from another's, and none may be lost for the largest logit's and the largest scale's sake."""
+    c = Batch(D + T + 9, "e4m3", D, 1, group, 32, [700], [T], tree=True)
+    c.q = (c.q.float() * 0.25).to(torch.bfloat16)
+    c.q[:, :, 0] = 4.0
+    up = (torch.arange(c.k.size(0), device="cuda") % 2 == 0)[:, None]
+    c.k[:, :, 0] = torch.where(up, spread * 0.6931 * D ** 0.5 / 8.0, -spread * 0.6931 * D ** 0.5 / 8.0).to(torch.bfloat16)
+    c.v = (c.v.float() * torch.where(up, 2.0 ** -spread, 1.0)[..., None]).to(torch.bfloat16)
+    c.write()
+    c.check(*c.run())
+    # the same with the small values under the small logits: those are dropped, within the bound
+    c.v = c.v.roll(1, 0)
+    c.write()
+    c.check(*c.run())
