@@ -252,6 +252,31 @@ aq_status aq_precompute_nvfp4(const aq_theta* th, void* q, int64_t ldq, void* sf
                               float* global_scale, int scale_mode, void* workspace, size_t workspace_bytes,
                               void* stream);
 
+/* Products with NVFP4 weights, as aq_precompute_nvfp4 leaves them:
+ *   y[m, o] = RN_bf16( g * sum over k of E2M1(q[o, k]) * E4M3(sf[o, k / 16]) * x[m, k] )
+ * q, ldq, sf, sf_layout and global_scale as there; in a multiple of 16 up to AQ_NVFP4_MAX_IN. Code times block scale is exact;
+ * x enters as f16 scaled by a power of two for each token and a part of K, so that elements below 2^-32 of the largest there lose
+ * bits; sums are fp32, in an order that the sizes fix; one rounding at the end. A block scale that is NaN makes its row NaN, an
+ * infinity or NaN in x its token alone.
+ * x [M, in] bf16, 16-byte aligned, ldx a multiple of 8. y[i] [M, out] bf16 with any row stride (aligned to its elements),
+ * apart from every input. M == 0 is a no-op. Any M is served; the weights are read once for every 32 tokens (fewer where
+ * in * M passes what a cluster's shared memory holds), so for many tokens the bf16 product on W_eff is the faster one.
+ * aq_nvfp4_linear_multi: one to three weights (AQ_MAX_FAMILIES) of one `in` and one layout over one x, in one launch.
+ * No workspace; these calls leave aq_last_launch_count() and aq_last_path() alone. Weights may be read before the previous
+ * kernel in the stream has finished, as stated at the top. */
+#define AQ_NVFP4_MAX_IN 65536
+typedef struct aq_nvfp4_weight {
+  const void* q;             /* [out, in / 2] bytes, row stride ldq */
+  int64_t ldq;
+  const void* sf;
+  const float* global_scale; /* one fp32 in device memory */
+  int32_t sf_layout;         /* aq_sf_layout */
+  int32_t out, in;
+} aq_nvfp4_weight;
+aq_status aq_nvfp4_linear(const aq_nvfp4_weight* w, const void* x, int64_t M, int64_t ldx, void* y, int64_t ldy, void* stream);
+aq_status aq_nvfp4_linear_multi(const aq_nvfp4_weight* w, int32_t n, const void* x, int64_t M, int64_t ldx, void* const* y,
+                                const int64_t* ldy, void* stream);
+
 /* Synchronises `stream`, then returns the device status word of the current device
  * (AQ_OK, AQ_ERR_TIMEOUT if a kernel's bounded wait expired since the last clear, or in the
  * checked build AQ_ERR_BOUNDS if a kernel skipped an out-of-range store)
@@ -427,6 +452,42 @@ aq_status aq_rope(const aq_rope_spec* rope, const int32_t* pos, int64_t T, int32
                   const void* x, int64_t x_tok, int64_t x_head, void* y, int64_t y_tok, int64_t y_head,
                   int32_t inverse, void* stream);
 
+/* T tokens' heads, [T, heads, head_dim] bf16 with a stride from token to token and one from head to head. */
+typedef struct aq_heads {
+  void* data;
+  int64_t tok, head;
+  int32_t heads;
+} aq_heads;
+
+/* Root-mean-square norm of one head: x * (offset + weight) / sqrt(mean(x^2) + eps). weight: device bf16 [head_dim], 16-byte
+ * aligned, or NULL for a factor of one. eps > 0. */
+typedef struct aq_head_norm {
+  const void* weight;
+  float eps;
+  float offset;   /* 0, or 1 for weights held as their distance from one */
+} aq_head_norm;
+
+/* q_out = rotated norm of q, and k_out of k in the same launch (k, k_out NULL: q alone): each head normed by its set's norm
+ * (NULL: none), then rotated at pos[t] as in aq_rope (rope NULL: not rotated), and rounded to bf16 once, at the end. Each set in
+ * place (same pointer and strides) or apart from all inputs. head_dim: a multiple of 16 up to 256. T == 0 is a no-op. A head
+ * that holds an infinity or a NaN gives NaN there (an infinity's finite neighbours zeros before the rotation). */
+aq_status aq_qk_norm_rope(const aq_head_norm* q_norm, const aq_head_norm* k_norm, const aq_rope_spec* rope, const int32_t* pos,
+                          int64_t T, int32_t head_dim, const aq_heads* q, const aq_heads* q_out, const aq_heads* k,
+                          const aq_heads* k_out, void* stream);
+
+/* Its gradient: from dq_out (of q_out) and q, with n = q / sqrt(mean(q^2) + eps), f = offset + weight and r = 1 / sqrt(...),
+ *   g = turned back dq_out,  dq = r (g f - n mean(g f n)),  dq_weight[i] = sum over tokens and heads of g_i n_i
+ * and the same for k (k, dk_out, dk NULL: q alone). Norms are needed for what is given. dq is bf16, rounded once; dq_weight fp32
+ * [head_dim], or NULL; sums in fp32, in an order that the sizes fix. dq may be dq_out (same pointer and strides), otherwise
+ * outputs lie apart from all inputs. T == 0 sets the weights' gradients to zero.
+ * workspace: aq_qk_norm_rope_backward_workspace_bytes(...) bytes, 16-byte aligned, no initial contents; none is needed (NULL)
+ * without weight gradients. */
+size_t aq_qk_norm_rope_backward_workspace_bytes(int64_t T, int32_t head_dim, int32_t q_heads, int32_t k_heads);
+aq_status aq_qk_norm_rope_backward(const aq_head_norm* q_norm, const aq_head_norm* k_norm, const aq_rope_spec* rope, const int32_t* pos,
+                                   int64_t T, int32_t head_dim, const aq_heads* dq_out, const aq_heads* q, const aq_heads* dq,
+                                   float* dq_weight, const aq_heads* dk_out, const aq_heads* k, const aq_heads* dk, float* dk_weight,
+                                   void* workspace, size_t workspace_bytes, void* stream);
+
 /* A paged key/value cache of one layer. Token slot n is offset n % page_size of page n / page_size.
  *   k, v              [pages, kv_heads, page_size, head_dim], bf16 or E4M3 codes
  *   k_scale, v_scale  [pages, kv_heads, page_size] fp32 with AQ_KV_E4M3 (one scale for each token
@@ -454,6 +515,13 @@ aq_status aq_kv_write(const aq_kv_cache* cache, const int64_t* slots, int64_t T,
                       int64_t k_head, const void* v, int64_t v_tok, int64_t v_head, const aq_rope_spec* rope,
                       const int32_t* pos, const void* q, int32_t q_heads, int64_t q_tok, int64_t q_head, void* q_out,
                       int64_t qo_tok, int64_t qo_head, void* stream);
+
+/* The same with the heads of q and k normed first (either norm NULL: not normed): norm, rotation and the cache's rounding in one
+ * pass. With q_norm, rope may be NULL. Values are stored as they are. */
+aq_status aq_kv_write_norm(const aq_kv_cache* cache, const int64_t* slots, int64_t T, const void* k, int64_t k_tok,
+                           int64_t k_head, const void* v, int64_t v_tok, int64_t v_head, const aq_rope_spec* rope,
+                           const int32_t* pos, const void* q, int32_t q_heads, int64_t q_tok, int64_t q_head, void* q_out,
+                           int64_t qo_tok, int64_t qo_head, const aq_head_norm* q_norm, const aq_head_norm* k_norm, void* stream);
 
 /* Reads T slots back as bf16 (code * scale rounded once); a slot outside the cache reads as zeros.
  * k or v may be NULL (not both). */
@@ -529,6 +597,30 @@ aq_status aq_verify_drafts(int32_t batch, int32_t vocab, const int32_t* cu, cons
                            const void* q, int64_t ld_q, int64_t rows, int32_t p_type, const float* u,
                            const float* noise, int64_t ld_noise, int32_t* n_accepted, int32_t* path, int64_t ld_path,
                            int32_t path_cap, int32_t* token, void* stream);
+
+/* Scores of words from rows of logits [rows, vocab] (row stride ld, aligned to their elements; type AQ_PROB_F32 or AQ_PROB_BF16,
+ * vocab up to 2^30). With z = scale * logit:
+ *   lse      [rows] log of the sum of e^z
+ *   logprob  [rows] z[tokens[row]] - lse; 0 where tokens[row] (int32) lies outside the vocabulary (padding)
+ *   entropy  [rows] of the distribution, in nats
+ *   top_token, top_logprob  [rows, top] the `top` (up to AQ_MAX_TOP) most likely words in falling order, of equal logits the lowest
+ *            index first, and their log probabilities; a NaN ranks below every number
+ * Outputs are contiguous, fp32 (top_token int32); logprob, lse and entropy may each be NULL. Words of logit minus infinity have no
+ * part in the sums. A row of nothing else gives lse and log probabilities -inf and entropy 0; a row with a NaN or plus infinity
+ * gives NaN for all but top_token. Sums are fp32, in an order that the sizes and the device's SM count fix. rows == 0 is a no-op. */
+#define AQ_MAX_TOP 32
+aq_status aq_token_logprobs(const void* logits, int64_t ld, int64_t rows, int32_t vocab, int32_t type, const int32_t* tokens,
+                            float scale, float* logprob, float* lse, float* entropy, int32_t top, float* top_logprob,
+                            int32_t* top_token, void* stream);
+
+/* Gradient of the above with respect to the logits, from what it returned and the gradients of logprob (with its tokens), entropy
+ * and lse, fp32 [rows] each, NULL where there is none:
+ *   dlogits = scale * ( dlogprob ([v = token] - p) - dentropy p (log p + entropy) + dlse p ),  p = e^(z - lse)
+ * in the logits' type, rounded once. A token outside the vocabulary has no gradient of its logprob; a row with lse -inf gives zeros.
+ * dlogits may be logits (same pointer and stride); otherwise it lies apart from every input. */
+aq_status aq_token_logprobs_backward(const void* logits, int64_t ld, int64_t rows, int32_t vocab, int32_t type, const int32_t* tokens,
+                                     float scale, const float* lse, const float* entropy, const float* dlogprob, const float* dentropy,
+                                     const float* dlse, void* dlogits, int64_t ld_out, void* stream);
 
 const char* aq_status_string(aq_status status);
 /* Thread-local description of the last error returned on this thread ("" if none). */

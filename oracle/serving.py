@@ -127,3 +127,72 @@ def verify(tokens, parent, p, u, noise, q=None, cap=None):
     if len(best) > 1:
         near(score[best[0]], score[best[1]])
     return path, int(best[0]), margin
+
+
+def head_norm_rope(x, weight, pos, angles, eps, offset=0.0, magnitude=1.0, layout="half"):
+    """x [T, H, D] normed head by head, times offset + weight (weight None: one), then rotated (angles None: not)."""
+    x = np.asarray(x, np.float64)
+    f = 1.0 if weight is None else offset + np.asarray(weight, np.float64)
+    y = x / np.sqrt((x * x).mean(-1, keepdims=True) + eps) * f
+    return y if angles is None else rope(y, pos, angles, magnitude, layout)
+
+
+def head_norm_rope_backward(dy, x, weight, pos, angles, eps, offset=0.0, magnitude=1.0, layout="half"):
+    """(dx, dweight) of the above, and what bounds a rounding of each: the sums of the absolute values of its terms."""
+    x = np.asarray(x, np.float64)
+    g = np.asarray(dy, np.float64) if angles is None else rope(dy, pos, angles, magnitude, layout, inverse=True)
+    f = 1.0 if weight is None else offset + np.asarray(weight, np.float64)
+    r = 1.0 / np.sqrt((x * x).mean(-1, keepdims=True) + eps)
+    n = x * r
+    dx = r * (g * f - n * (g * f * n).mean(-1, keepdims=True))
+    size = r * (np.abs(g * f) + np.abs(n) * np.abs(g * f * n).mean(-1, keepdims=True))
+    return dx, (g * n).sum((0, 1)), size, np.abs(g * n).sum((0, 1))
+
+
+def token_scores(logits, tokens=None, scale=1.0, top=0):
+    """(logprob, lse, entropy, top_logprob, top_token) of rows of logits."""
+    x = np.asarray(logits, np.float64)
+    z = x * scale
+    rows, vocab = z.shape
+    bad = np.isnan(z).any(-1) | (z == np.inf).any(-1)
+    m = np.where(bad, 0.0, z.max(-1))
+    none = ~bad & (m == -np.inf)
+    m = np.where(none, 0.0, m)
+    with np.errstate(divide="ignore", invalid="ignore"):
+        e = np.exp(z - m[:, None])
+        lse = m + np.log(e.sum(-1))
+        logp = (z - m[:, None]) - np.log(e.sum(-1))[:, None]     # lse may have swallowed the logarithm
+        p = np.exp(logp)
+        entropy = -np.where(p > 0, p * logp, 0.0).sum(-1)
+    lse, entropy = np.where(bad, np.nan, np.where(none, -np.inf, lse)), np.where(bad, np.nan, np.where(none, 0.0, entropy))
+    logp = np.where(bad[:, None], np.nan, np.where(none[:, None], -np.inf, logp))
+    logprob = None
+    if tokens is not None:
+        t = np.asarray(tokens)
+        here = (t >= 0) & (t < vocab)
+        logprob = np.where(here, logp[np.arange(rows), np.where(here, t, 0)], 0.0)
+    order = np.argsort(np.where(np.isnan(x), np.inf, -x), axis=-1, kind="stable")
+    # of -inf and NaN, both at the end, the numbers come first
+    order = np.stack([np.concatenate([o[~np.isnan(r[o])], o[np.isnan(r[o])]]) for o, r in zip(order, x)])[:, :top]
+    return logprob, lse, entropy, np.take_along_axis(logp, order, -1), order
+
+
+def token_scores_backward(logits, tokens, lse, entropy, dlogprob=None, dentropy=None, dlse=None, scale=1.0):
+    """dlogits, and the sum of the absolute values of its terms."""
+    z = np.asarray(logits, np.float64) * scale
+    rows, vocab = z.shape
+    col = lambda v: np.zeros((rows, 1)) if v is None else np.asarray(v, np.float64)[:, None]  # noqa: E731
+    gp, gh, gl = col(dlogprob), col(dentropy), col(dlse)
+    t = np.full(rows, -1) if tokens is None else np.asarray(tokens)
+    here = ((t >= 0) & (t < vocab))[:, None]
+    gp = np.where(here, gp, 0.0)
+    hit = np.arange(vocab)[None] == t[:, None]
+    none = np.isneginf(col(lse))
+    with np.errstate(invalid="ignore"):
+        logp = np.where(none, -np.inf, z - np.where(none, 0.0, col(lse)))
+    p = np.exp(logp)
+    logp = np.where(p > 0, logp, 0.0)
+    h = col(entropy)
+    d = gp * (hit & here & ~none) - gp * p - gh * p * (logp + h) + gl * p
+    size = np.abs(gp) * (hit & here) + p * (np.abs(gp) + np.abs(gh) * (np.abs(logp) + np.abs(h)) + np.abs(gl))
+    return scale * d, scale * size

@@ -12,6 +12,7 @@ import functools
 import inspect
 import os
 from dataclasses import dataclass
+from typing import NamedTuple
 
 from . import build_lib
 
@@ -50,6 +51,8 @@ AQ_KV_E4M3 = 1
 AQ_PROB_F32 = 0
 AQ_PROB_BF16 = 1
 AQ_MAX_DRAFT_NODES = 1024
+AQ_MAX_TOP = 32
+AQ_NVFP4_MAX_IN = 65536
 
 EXPORTED_SYMBOLS = [
     "aq_linear_workspace_bytes", "aq_linear", "aq_linear_qkv", "aq_precompute",
@@ -60,7 +63,9 @@ EXPORTED_SYMBOLS = [
     "aq_mlp_workspace_bytes", "aq_mlp", "aq_precompute_nvfp4_workspace_bytes", "aq_precompute_nvfp4",
     "aq_selftest_prefill_timeout", "aq_checked_build", "aq_selftest_bounds_check",
     "aq_rope_frequencies", "aq_rope", "aq_kv_write", "aq_kv_read", "aq_tree_attention_workspace_bytes",
-    "aq_tree_attention", "aq_verify_drafts",
+    "aq_tree_attention", "aq_verify_drafts", "aq_kv_write_norm", "aq_qk_norm_rope",
+    "aq_qk_norm_rope_backward_workspace_bytes", "aq_qk_norm_rope_backward", "aq_nvfp4_linear", "aq_nvfp4_linear_multi",
+    "aq_token_logprobs", "aq_token_logprobs_backward",
 ]
 AQ_MAX_FAMILIES = 3
 AQ_NOALLOC_WORKSPACE_BYTES = 8 * 1024 * 1024
@@ -104,6 +109,19 @@ class c_draft_batch(ctypes.Structure):
                 ("cu_q", ctypes.c_void_p), ("ctx", ctypes.c_void_p), ("page_table", ctypes.c_void_p),
                 ("pages_per_seq", ctypes.c_int32), ("ld_table", ctypes.c_int64), ("mask", ctypes.c_void_p),
                 ("ld_mask", ctypes.c_int64), ("depth", ctypes.c_void_p), ("window", ctypes.c_int32)]
+
+
+class c_heads(ctypes.Structure):
+    _fields_ = [("data", ctypes.c_void_p), ("tok", ctypes.c_int64), ("head", ctypes.c_int64), ("heads", ctypes.c_int32)]
+
+
+class c_head_norm(ctypes.Structure):
+    _fields_ = [("weight", ctypes.c_void_p), ("eps", ctypes.c_float), ("offset", ctypes.c_float)]
+
+
+class c_nvfp4_weight(ctypes.Structure):
+    _fields_ = [("q", ctypes.c_void_p), ("ldq", ctypes.c_int64), ("sf", ctypes.c_void_p), ("global_scale", ctypes.c_void_p),
+                ("sf_layout", ctypes.c_int32), ("out", ctypes.c_int32), ("in_", ctypes.c_int32)]
 
 
 _lib = None
@@ -187,6 +205,24 @@ def load(path: str | None = None) -> ctypes.CDLL:
     lib.aq_verify_drafts.argtypes = [i32, i32, vp, vp, vp, i64, i32, vp, i64, vp, i64, i64, i32, vp, vp, i64, vp, vp,
                                      i64, i32, vp, vp]
     lib.aq_verify_drafts.restype = ctypes.c_int
+    norm_p, heads_p, w4_p = ctypes.POINTER(c_head_norm), ctypes.POINTER(c_heads), ctypes.POINTER(c_nvfp4_weight)
+    lib.aq_kv_write_norm.argtypes = lib.aq_kv_write.argtypes[:-1] + [norm_p, norm_p, vp]
+    lib.aq_kv_write_norm.restype = ctypes.c_int
+    lib.aq_qk_norm_rope.argtypes = [norm_p, norm_p, rope_p, vp, i64, i32, heads_p, heads_p, heads_p, heads_p, vp]
+    lib.aq_qk_norm_rope.restype = ctypes.c_int
+    lib.aq_qk_norm_rope_backward_workspace_bytes.argtypes = [i64, i32, i32, i32]
+    lib.aq_qk_norm_rope_backward_workspace_bytes.restype = sz
+    lib.aq_qk_norm_rope_backward.argtypes = [norm_p, norm_p, rope_p, vp, i64, i32, heads_p, heads_p, heads_p, vp, heads_p,
+                                             heads_p, heads_p, vp, vp, sz, vp]
+    lib.aq_qk_norm_rope_backward.restype = ctypes.c_int
+    lib.aq_nvfp4_linear.argtypes = [w4_p, vp, i64, i64, vp, i64, vp]
+    lib.aq_nvfp4_linear.restype = ctypes.c_int
+    lib.aq_nvfp4_linear_multi.argtypes = [w4_p, i32, vp, i64, i64, ctypes.POINTER(vp), ctypes.POINTER(i64), vp]
+    lib.aq_nvfp4_linear_multi.restype = ctypes.c_int
+    lib.aq_token_logprobs.argtypes = [vp, i64, i64, i32, i32, vp, f32, vp, vp, vp, i32, vp, vp, vp]
+    lib.aq_token_logprobs.restype = ctypes.c_int
+    lib.aq_token_logprobs_backward.argtypes = [vp, i64, i64, i32, i32, vp, f32, vp, vp, vp, vp, vp, vp, i64, vp]
+    lib.aq_token_logprobs_backward.restype = ctypes.c_int
     for name in ("aq_decode_max_m", "aq_last_path", "aq_last_launch_count", "aq_abi_version"):
         getattr(lib, name).argtypes = []
         getattr(lib, name).restype = i32
@@ -600,8 +636,9 @@ def _serve():
         spec = importlib.util.spec_from_file_location("_marshal", build_lib.MARSHAL_PATH)
         module = importlib.util.module_from_spec(spec)
         spec.loader.exec_module(module)
-        names = ("aq_rope", "aq_kv_write", "aq_kv_read", "aq_tree_attention_workspace_bytes", "aq_tree_attention",
-                 "aq_verify_drafts")
+        names = ("aq_rope", "aq_kv_write_norm", "aq_kv_read", "aq_tree_attention_workspace_bytes", "aq_tree_attention",
+                 "aq_verify_drafts", "aq_qk_norm_rope", "aq_qk_norm_rope_backward_workspace_bytes", "aq_qk_norm_rope_backward",
+                 "aq_nvfp4_linear_multi", "aq_token_logprobs", "aq_token_logprobs_backward")
         module.bind(tuple(ctypes.cast(getattr(lib, n), ctypes.c_void_p).value for n in names), _check)
         _marshal = module
     return _marshal
@@ -666,11 +703,36 @@ class KvCache:
         return AQ_KV_BF16 if self.k_scale is None else AQ_KV_E4M3
 
 
-def aq_kv_write(cache: KvCache, k, v, slots, rope: Rope | None = None, pos=None, q=None, q_out=None, stream=None):
+@dataclass
+class HeadNorm:
+    """Norm of one head: x * (offset + weight) / sqrt(mean(x^2) + eps). ``weight`` bf16 [head_dim], or None for a factor of
+    one; ``offset`` 1 for weights held as their distance from one."""
+    weight: object = None
+    eps: float = 1e-6
+    offset: float = 0.0
+
+
+def aq_kv_write(cache: KvCache, k, v, slots, rope: Rope | None = None, pos=None, q=None, q_out=None, stream=None,
+                q_norm: HeadNorm | None = None, k_norm: HeadNorm | None = None):
     """Writes k and v [T, kv_heads, head_dim] into the cache's slots (int64 [T], each but once), rotating k with
     ``rope`` at ``pos``. With q [T, q_heads, head_dim] the rotated queries are returned too (into q_out,
-    which may be q)."""
-    return _serve().kv_write(cache, k, v, slots, rope, pos, q, q_out, _raw_stream(stream))
+    which may be q). ``q_norm`` and ``k_norm`` norm each head of q and k before the rotation, in the same pass."""
+    return _serve().kv_write(cache, k, v, slots, rope, pos, q, q_out, q_norm, k_norm, _raw_stream(stream))
+
+
+def aq_qk_norm_rope(q, k=None, q_norm: HeadNorm | None = None, k_norm: HeadNorm | None = None, rope: Rope | None = None,
+                    pos=None, q_out=None, k_out=None, stream=None):
+    """Each head of q [T, q_heads, head_dim] and k [T, kv_heads, head_dim] normed, then rotated with ``rope`` at pos (int32
+    [T]), in one launch: (q_out, k_out), either of which may be its input; k_out is None without k. Records no history: a
+    training step calls aq_qk_norm_rope_backward itself."""
+    return _serve().qk_norm_rope(q, k, q_norm, k_norm, rope, pos, q_out, k_out, _raw_stream(stream))
+
+
+def aq_qk_norm_rope_backward(dq_out, dk_out, q, k, q_norm: HeadNorm, k_norm: HeadNorm | None, rope: Rope | None = None, pos=None,
+                             dq=None, dk=None, workspace=None, stream=None):
+    """Gradients of aq_qk_norm_rope from those of its outputs: (dq, dk, dq_weight, dk_weight), the weights' in fp32 [head_dim]
+    (None where there is no weight; dk and dk_weight None without k). dq may be dq_out, dk dk_out."""
+    return _serve().qk_norm_rope_backward(dq_out, dk_out, q, k, q_norm, k_norm, rope, pos, dq, dk, workspace, _raw_stream(stream))
 
 
 def aq_kv_read(cache: KvCache, slots, k=None, v=None, stream=None):
@@ -702,3 +764,46 @@ def aq_verify_drafts(p, tokens, cu, u, noise, q=None, parent=None, path_cap: int
     token [batch]), all int32. p (and q): [nodes + batch, vocab] fp32 or bf16; tokens, parent int32 [nodes]; cu
     int32 [batch + 1]; u fp32 [nodes]; noise fp32 [batch, vocab]. path_cap and max_nodes default to nodes."""
     return _serve().verify(p, tokens, cu, u, noise, q, parent, path_cap, max_nodes, _raw_stream(stream))
+
+
+@dataclass
+class Nvfp4Weight:
+    """A weight as ``aq_precompute_nvfp4`` returns it: q uint8 [out, in / 2], sf uint8 (E4M3 block scales in ``layout``),
+    global_scale fp32 [1]."""
+    q: object
+    sf: object
+    global_scale: object
+    layout: int = AQ_SF_LINEAR
+
+
+def aq_nvfp4_linear(weight: Nvfp4Weight, x, y=None, stream=None):
+    """y [M, out] = x [M, in] times an NVFP4 weight, both bf16: decode's product on the weights of aq_precompute_nvfp4."""
+    return _serve().nvfp4_linear((weight,), x, None if y is None else (y,), _raw_stream(stream))[0]
+
+
+def aq_nvfp4_linear_multi(weights, x, ys=None, stream=None):
+    """One to three NVFP4 weights (of one layout) over one x in one launch; returns the outputs."""
+    return _serve().nvfp4_linear(weights, x, ys, _raw_stream(stream))
+
+
+class TokenScores(NamedTuple):
+    """What aq_token_logprobs returns: fp32 [rows] (logprob None without tokens) and [rows, top] (None with top=0)."""
+    logprob: object
+    lse: object
+    entropy: object
+    top_logprob: object
+    top_token: object
+
+
+def aq_token_logprobs(logits, tokens=None, scale: float = 1.0, top: int = 0, stream=None) -> TokenScores:
+    """Scores from logits [rows, vocab] (fp32 or bf16) times ``scale``: log probabilities of ``tokens`` (int32 [rows]; 0 where a
+    token lies outside the vocabulary), the log of the normaliser, the entropy, and the ``top`` (up to 32) most likely
+    words with their log probabilities."""
+    return TokenScores(*_serve().scores(logits, tokens, scale, top, _raw_stream(stream)))
+
+
+def aq_token_logprobs_backward(logits, tokens, lse, entropy=None, dlogprob=None, dentropy=None, dlse=None, scale: float = 1.0,
+                               dlogits=None, stream=None):
+    """Gradient with respect to the logits, in their type, from what aq_token_logprobs returned (lse, and entropy where dentropy
+    is given) and the gradients of logprob, entropy and lse (fp32 [rows], None for none). dlogits may be logits."""
+    return _serve().scores_backward(logits, tokens, lse, entropy, dlogprob, dentropy, dlse, scale, dlogits, _raw_stream(stream))

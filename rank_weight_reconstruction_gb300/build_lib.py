@@ -27,8 +27,8 @@ DEBUG_BUILD_DIR = os.path.join(PKG_DIR, "_build_debug")
 DEBUG_LIB_PATH = os.path.join(PKG_DIR, "libaq_gb300_debug.so")
 SOURCES = ["aq_kernels.cu", "aq_decode.cu", "aq_decode2.cu", "aq_decompose.cu", "aq_host.cu", "aq_noalloc.cu",
            "aq_positions.cu", "aq_attention.cu", "aq_attention_tc.cu",
-           "aq_verify.cu"]
-HEADERS = ["aq_ptx.cuh", "aq_internal.h", "aq_serve.h", "aq_attention.cuh"]
+           "aq_verify.cu", "aq_norm.cu", "aq_nvfp4.cu", "aq_scores.cu"]
+HEADERS = ["aq_ptx.cuh", "aq_internal.h", "aq_serve.h", "aq_attention.cuh", "aq_positions.cuh"]
 
 # The serving calls' marshalling, a CPython module of host code over torch tensors (see csrc/aq_python.cpp).
 MARSHAL_SOURCE = "aq_python.cpp"

@@ -31,14 +31,20 @@
 namespace {
 
 decltype(&aq_rope) f_rope;
-decltype(&aq_kv_write) f_kv_write;
 decltype(&aq_kv_read) f_kv_read;
 decltype(&aq_tree_attention_workspace_bytes) f_attention_bytes;
 decltype(&aq_tree_attention) f_attention;
 decltype(&aq_verify_drafts) f_verify;
+decltype(&aq_kv_write_norm) f_kv_write_norm;
+decltype(&aq_qk_norm_rope) f_norm;
+decltype(&aq_qk_norm_rope_backward_workspace_bytes) f_norm_bytes;
+decltype(&aq_qk_norm_rope_backward) f_norm_backward;
+decltype(&aq_nvfp4_linear_multi) f_nvfp4;
+decltype(&aq_token_logprobs) f_scores;
+decltype(&aq_token_logprobs_backward) f_scores_backward;
 PyObject* f_check;   // raises for a status that is not AQ_OK
 
-PyObject *s_freq, *s_layout, *s_magnitude, *s_k, *s_v, *s_k_scale, *s_v_scale;
+PyObject *s_freq, *s_layout, *s_magnitude, *s_k, *s_v, *s_k_scale, *s_v_scale, *s_weight, *s_eps, *s_offset, *s_q, *s_sf, *s_global_scale;
 
 constexpr at::ScalarType kBf16 = at::kBFloat16, kF32 = at::kFloat, kI32 = at::kInt, kI64 = at::kLong, kU64 = at::kUInt64, kU8 = at::kByte;
 
@@ -184,6 +190,32 @@ struct Rope {
     spec.freq = static_cast<const uint64_t*>(t.ptr);
     spec.rotary_dim = static_cast<int32_t>(2 * t.shape[0]);
     return !PyErr_Occurred();
+  }
+};
+
+bool read_float(PyObject* obj, float* out) {
+  *out = static_cast<float>(PyFloat_AsDouble(obj));
+  return !PyErr_Occurred();
+}
+
+// A HeadNorm over heads of `dim`, or None.
+struct Norm {
+  PyObject* weight = nullptr;
+  Tensor w;
+  aq_head_norm n = {};
+  bool given = false;
+  ~Norm() { Py_XDECREF(weight); }
+  const aq_head_norm* c() const { return given ? &n : nullptr; }
+  bool read_from(Device& dev, PyObject* obj, int64_t dim) {
+    if (obj == Py_None) return true;
+    given = true;
+    weight = PyObject_GetAttr(obj, s_weight);
+    Ref eps(PyObject_GetAttr(obj, s_eps)), offset(PyObject_GetAttr(obj, s_offset));
+    if (!weight || !eps.o || !offset.o || !read_float(eps.o, &n.eps) || !read_float(offset.o, &n.offset)) return false;
+    if (weight == Py_None) return true;
+    if (!read_flat(dev, weight, "HeadNorm.weight", kBf16, dim, &w)) return false;
+    n.weight = w.ptr;
+    return true;
   }
 };
 
@@ -345,20 +377,22 @@ PyObject* py_rope(PyObject*, PyObject* const* a, Py_ssize_t n) {
   END_HANDLE_TH_ERRORS
 }
 
-// kv_write(cache, k, v, slots, rope, pos, q, q_out, stream) -> q_out
+// kv_write(cache, k, v, slots, rope, pos, q, q_out, q_norm, k_norm, stream) -> q_out
 PyObject* py_kv_write(PyObject*, PyObject* const* a, Py_ssize_t n) {
   HANDLE_TH_ERRORS
   Device dev;
   Cache c;
   Rope r;
+  Norm qn, kn;
   Tensor k, v, slots, pos, q, o;
   Stream st;
-  if (!want(n, 9, "kv_write") || !c.read_from(dev, a[0]) || !read_heads(dev, a[1], "k", -1, c.c.kv_heads, c.c.head_dim, &k)) return nullptr;
+  if (!want(n, 11, "kv_write") || !c.read_from(dev, a[0]) || !read_heads(dev, a[1], "k", -1, c.c.kv_heads, c.c.head_dim, &k)) return nullptr;
   const int64_t T = k.shape[0];
   const bool turned = a[4] != Py_None, queries = a[6] != Py_None;
   if (!read_heads(dev, a[2], "v", T, c.c.kv_heads, c.c.head_dim, &v) || !read_flat(dev, a[3], "slots", kI64, T, &slots) || (turned && !r.read_from(dev, a[4])) ||
       (a[5] != Py_None && !read_flat(dev, a[5], "pos", kI32, T, &pos)) || (queries && !read_heads(dev, a[6], "q", T, -1, c.c.head_dim, &q)) ||
-      (queries && a[7] != Py_None && !read_heads(dev, a[7], "q_out", T, q.shape[1], c.c.head_dim, &o)) || !st.read_from(a[8], k))
+      (queries && a[7] != Py_None && !read_heads(dev, a[7], "q_out", T, q.shape[1], c.c.head_dim, &o)) || !qn.read_from(dev, a[8], c.c.head_dim) ||
+      !kn.read_from(dev, a[9], c.c.head_dim) || !st.read_from(a[10], k))
     return nullptr;
   at::AutoDispatchBelowADInplaceOrView plain;
   at::Tensor made;
@@ -367,9 +401,9 @@ PyObject* py_kv_write(PyObject*, PyObject* const* a, Py_ssize_t n) {
     take(made, &o);
     if (!head_strides("q_out", &o)) return nullptr;
   }
-  if (!on_gpu(dev) || !ok(f_kv_write(&c.c, static_cast<const int64_t*>(slots.ptr), T, k.ptr, k.stride[0], k.stride[1], v.ptr, v.stride[0], v.stride[1],
+  if (!on_gpu(dev) || !ok(f_kv_write_norm(&c.c, static_cast<const int64_t*>(slots.ptr), T, k.ptr, k.stride[0], k.stride[1], v.ptr, v.stride[0], v.stride[1],
                      turned ? &r.spec : nullptr, static_cast<const int32_t*>(pos.ptr), q.ptr, small(q.shape[1]), q.stride[0], q.stride[1], o.ptr,
-                     o.stride[0], o.stride[1], st.handle)))
+                     o.stride[0], o.stride[1], qn.c(), kn.c(), st.handle)))
     return nullptr;
   return made.defined() ? st.hand_out(std::move(made)) : given(a[7]);
   END_HANDLE_TH_ERRORS
@@ -538,18 +572,302 @@ PyObject* py_verify(PyObject*, PyObject* const* a, Py_ssize_t n) {
   END_HANDLE_TH_ERRORS
 }
 
+aq_heads heads_of(const Tensor& x) { return {x.ptr, x.stride[0], x.stride[1], small(x.shape[1])}; }
+
+// qk_norm_rope(q, k, q_norm, k_norm, rope, pos, q_out, k_out, stream) -> (q_out, k_out)
+PyObject* py_qk_norm_rope(PyObject*, PyObject* const* a, Py_ssize_t n) {
+  HANDLE_TH_ERRORS
+  Device dev;
+  Rope r;
+  Norm norm[2];
+  Tensor pos, x[2], y[2];
+  Stream st;
+  if (!want(n, 9, "qk_norm_rope") || !read_heads(dev, a[0], "q", -1, -1, -1, &x[0])) return nullptr;
+  const int64_t T = x[0].shape[0], D = x[0].shape[2];
+  const int sets = a[1] == Py_None ? 1 : 2;
+  const bool turned = a[4] != Py_None;
+  if ((sets == 2 && !read_heads(dev, a[1], "k", T, -1, D, &x[1])) || !norm[0].read_from(dev, a[2], D) || !norm[1].read_from(dev, a[3], D) ||
+      (turned && !r.read_from(dev, a[4])) || (a[5] != Py_None && !read_flat(dev, a[5], "pos", kI32, T, &pos)))
+    return nullptr;
+  const char* const name[2] = {"q_out", "k_out"};
+  for (int i = 0; i < sets; ++i)
+    if (a[6 + i] != Py_None && !read_heads(dev, a[6 + i], name[i], T, x[i].shape[1], D, &y[i])) return nullptr;
+  if (!st.read_from(a[8], x[0])) return nullptr;
+  at::AutoDispatchBelowADInplaceOrView plain;
+  at::Tensor made[2];
+  for (int i = 0; i < sets; ++i)
+    if (a[6 + i] == Py_None) {
+      made[i] = like(x[i]);
+      take(made[i], &y[i]);
+      if (!head_strides(name[i], &y[i])) return nullptr;
+    }
+  const aq_heads q = heads_of(x[0]), k = heads_of(x[1]), qo = heads_of(y[0]), ko = heads_of(y[1]);
+  if (!on_gpu(dev) || !ok(f_norm(norm[0].c(), norm[1].c(), turned ? &r.spec : nullptr, static_cast<const int32_t*>(pos.ptr), T, small(D), &q, &qo,
+                                 sets == 2 ? &k : nullptr, sets == 2 ? &ko : nullptr, st.handle)))
+    return nullptr;
+  PyObject* out[2];
+  for (int i = 0; i < 2; ++i) out[i] = i < sets && made[i].defined() ? st.hand_out(std::move(made[i])) : given(i < sets ? a[6 + i] : Py_None);
+  return pack({out[0], out[1]});
+  END_HANDLE_TH_ERRORS
+}
+
+// qk_norm_rope_backward(dq_out, dk_out, q, k, q_norm, k_norm, rope, pos, dq, dk, workspace, stream) -> (dq, dk, dq_weight, dk_weight)
+PyObject* py_qk_norm_rope_backward(PyObject*, PyObject* const* a, Py_ssize_t n) {
+  HANDLE_TH_ERRORS
+  Device dev;
+  Rope r;
+  Norm norm[2];
+  Tensor pos, dy[2], x[2], dx[2], ws;
+  Stream st;
+  if (!want(n, 12, "qk_norm_rope_backward") || !read_heads(dev, a[2], "q", -1, -1, -1, &x[0])) return nullptr;
+  const int64_t T = x[0].shape[0], D = x[0].shape[2];
+  const int sets = a[3] == Py_None ? 1 : 2;
+  const bool turned = a[6] != Py_None;
+  const char* const names[2][2] = {{"dq_out", "dq"}, {"dk_out", "dk"}};
+  if ((sets == 2 && !read_heads(dev, a[3], "k", T, -1, D, &x[1])) || !norm[0].read_from(dev, a[4], D) || !norm[1].read_from(dev, a[5], D) ||
+      (turned && !r.read_from(dev, a[6])) || (a[7] != Py_None && !read_flat(dev, a[7], "pos", kI32, T, &pos)) ||
+      (a[10] != Py_None && !read_flat(dev, a[10], "workspace", kU8, -1, &ws)))
+    return nullptr;
+  if (!norm[0].given || (sets == 2) != norm[1].given || (sets == 2) != (a[1] != Py_None)) {
+    PyErr_SetString(PyExc_ValueError, "q comes with q_norm, and k, k_norm and dk_out together");
+    return nullptr;
+  }
+  for (int i = 0; i < sets; ++i)
+    if (!read_heads(dev, a[i], names[i][0], T, x[i].shape[1], D, &dy[i]) || (a[8 + i] != Py_None && !read_heads(dev, a[8 + i], names[i][1], T, x[i].shape[1], D, &dx[i])))
+      return nullptr;
+  if (!st.read_from(a[11], x[0])) return nullptr;
+  at::AutoDispatchBelowADInplaceOrView plain;
+  at::Tensor made[2], made_w[2], made_ws;
+  float* dw[2] = {nullptr, nullptr};
+  for (int i = 0; i < sets; ++i) {
+    if (a[8 + i] == Py_None) {
+      made[i] = like(x[i]);
+      take(made[i], &dx[i]);
+      if (!head_strides(names[i][1], &dx[i])) return nullptr;
+    }
+    if (norm[i].n.weight) {
+      made_w[i] = fresh({D}, kF32, x[0]);
+      dw[i] = static_cast<float*>(made_w[i].data_ptr());
+    }
+  }
+  if (a[10] == Py_None && (dw[0] || dw[1])) {
+    const size_t need = f_norm_bytes(T, small(D), small(x[0].shape[1]), sets == 2 ? small(x[1].shape[1]) : 0);
+    if (need == static_cast<size_t>(-1)) {
+      ok(AQ_ERR_INVALID_ARG);
+      return nullptr;
+    }
+    made_ws = fresh({static_cast<int64_t>(need)}, kU8, x[0]);
+    take(made_ws, &ws);
+  }
+  aq_heads h[2][3];
+  for (int i = 0; i < 2; ++i) {
+    h[i][0] = heads_of(dy[i]);
+    h[i][1] = heads_of(x[i]);
+    h[i][2] = heads_of(dx[i]);
+  }
+  const bool two = sets == 2;
+  if (!on_gpu(dev) || !ok(f_norm_backward(norm[0].c(), norm[1].c(), turned ? &r.spec : nullptr, static_cast<const int32_t*>(pos.ptr), T, small(D), &h[0][0],
+                                          &h[0][1], &h[0][2], dw[0], two ? &h[1][0] : nullptr, two ? &h[1][1] : nullptr, two ? &h[1][2] : nullptr, dw[1], ws.ptr,
+                                          static_cast<size_t>(ws.shape[0]), st.handle)))
+    return nullptr;
+  PyObject* out[4];
+  for (int i = 0; i < 2; ++i) {
+    out[i] = made[i].defined() ? st.hand_out(std::move(made[i])) : given(i < sets ? a[8 + i] : Py_None);
+    out[2 + i] = made_w[i].defined() ? st.hand_out(std::move(made_w[i])) : given(Py_None);
+  }
+  return pack({out[0], out[1], out[2], out[3]});
+  END_HANDLE_TH_ERRORS
+}
+
+// An Nvfp4Weight.
+struct Weight4 {
+  PyObject *q = nullptr, *sf = nullptr, *g = nullptr;
+  aq_nvfp4_weight w = {};
+  ~Weight4() {
+    Py_XDECREF(q);
+    Py_XDECREF(sf);
+    Py_XDECREF(g);
+  }
+  bool read_from(Device& dev, PyObject* obj) {
+    Tensor t, one;
+    q = PyObject_GetAttr(obj, s_q);
+    sf = PyObject_GetAttr(obj, s_sf);
+    g = PyObject_GetAttr(obj, s_global_scale);
+    Ref layout(PyObject_GetAttr(obj, s_layout));
+    if (!q || !sf || !g || !layout.o || !read_int32(layout.o, "layout", &w.sf_layout) || !read_rows(dev, q, "Nvfp4Weight.q", kU8, kU8, -1, 0, &t) ||
+        !read(dev, g, "Nvfp4Weight.global_scale", kF32, kF32, 1, &one))
+      return false;
+    if (one.shape[0] != 1) {
+      PyErr_SetString(PyExc_ValueError, "Nvfp4Weight.global_scale: expected one element");
+      return false;
+    }
+    w.q = t.ptr;
+    w.ldq = t.stride[0];
+    w.out = small(t.shape[0]);
+    w.in = small(2 * t.shape[1]);
+    w.global_scale = static_cast<const float*>(one.ptr);
+    const int64_t cols = t.shape[1] / 8;
+    const int64_t need = w.sf_layout == AQ_SF_128X4 ? (t.shape[0] + 127) / 128 * 128 * ((cols + 3) / 4 * 4) : t.shape[0] * cols;
+    Tensor s;
+    const bool flat = THPVariable_Check(sf) && THPVariable_Unpack(sf).dim() == 1;
+    if (!read(dev, sf, "Nvfp4Weight.sf", kU8, kU8, flat ? 1 : 2, &s)) return false;
+    if (!contiguous(s) || (flat ? s.shape[0] : s.shape[0] * s.shape[1]) != need) {
+      PyErr_Format(PyExc_ValueError, "Nvfp4Weight.sf: expected a contiguous tensor of %lld elements", static_cast<long long>(need));
+      return false;
+    }
+    w.sf = s.ptr;
+    return true;
+  }
+};
+
+// nvfp4_linear(weights, x, ys, stream) -> [y, ...]
+PyObject* py_nvfp4_linear(PyObject*, PyObject* const* a, Py_ssize_t n) {
+  HANDLE_TH_ERRORS
+  Device dev;
+  Weight4 w[AQ_MAX_FAMILIES];
+  Tensor x, y[AQ_MAX_FAMILIES];
+  Stream st;
+  if (!want(n, 4, "nvfp4_linear")) return nullptr;
+  Ref list(PySequence_Fast(a[0], "weights: expected a sequence of Nvfp4Weight")), outs(a[2] == Py_None ? nullptr : PySequence_Fast(a[2], "ys: expected a sequence of tensors"));
+  if (!list.o || (a[2] != Py_None && !outs.o)) return nullptr;
+  const Py_ssize_t count = PySequence_Fast_GET_SIZE(list.o);
+  if (count < 1 || count > AQ_MAX_FAMILIES || (outs.o && PySequence_Fast_GET_SIZE(outs.o) != count)) {
+    PyErr_Format(PyExc_ValueError, "expected one to %d weights, and as many ys", AQ_MAX_FAMILIES);
+    return nullptr;
+  }
+  for (Py_ssize_t i = 0; i < count; ++i)
+    if (!w[i].read_from(dev, PySequence_Fast_GET_ITEM(list.o, i))) return nullptr;
+  if (!read_rows(dev, a[1], "x", kBf16, kBf16, -1, 0, &x)) return nullptr;
+  if (x.shape[1] != w[0].w.in) {
+    PyErr_Format(PyExc_ValueError, "x: expected %d columns, got %lld", w[0].w.in, static_cast<long long>(x.shape[1]));
+    return nullptr;
+  }
+  const int64_t M = x.shape[0];
+  for (Py_ssize_t i = 0; outs.o && i < count; ++i) {
+    if (!read_rows(dev, PySequence_Fast_GET_ITEM(outs.o, i), "y", kBf16, kBf16, M, w[i].w.out, &y[i])) return nullptr;
+    if (y[i].shape[1] != w[i].w.out) {
+      PyErr_Format(PyExc_ValueError, "y: expected %d columns, got %lld", w[i].w.out, static_cast<long long>(y[i].shape[1]));
+      return nullptr;
+    }
+  }
+  if (!st.read_from(a[3], x)) return nullptr;
+  at::AutoDispatchBelowADInplaceOrView plain;
+  at::Tensor made[AQ_MAX_FAMILIES];
+  aq_nvfp4_weight cw[AQ_MAX_FAMILIES];
+  void* yp[AQ_MAX_FAMILIES];
+  int64_t ldy[AQ_MAX_FAMILIES];
+  for (Py_ssize_t i = 0; i < count; ++i) {
+    if (!outs.o) {
+      made[i] = fresh({M, w[i].w.out}, kBf16, x);
+      take(made[i], &y[i]);
+    }
+    cw[i] = w[i].w;
+    yp[i] = y[i].ptr;
+    ldy[i] = y[i].stride[0];
+  }
+  if (!on_gpu(dev) || !ok(f_nvfp4(cw, static_cast<int32_t>(count), x.ptr, M, x.stride[0], yp, ldy, st.handle))) return nullptr;
+  Ref result(PyList_New(count));
+  if (!result.o) return nullptr;
+  for (Py_ssize_t i = 0; i < count; ++i) {
+    PyObject* o = made[i].defined() ? st.hand_out(std::move(made[i])) : given(PySequence_Fast_GET_ITEM(outs.o, i));
+    if (!o) return nullptr;
+    PyList_SET_ITEM(result.o, i, o);
+  }
+  return given(result.o);
+  END_HANDLE_TH_ERRORS
+}
+
+// scores(logits, tokens, scale, top, stream) -> (logprob, lse, entropy, top_logprob, top_token)
+PyObject* py_scores(PyObject*, PyObject* const* a, Py_ssize_t n) {
+  HANDLE_TH_ERRORS
+  Device dev;
+  Tensor x, tokens;
+  float scale;
+  int32_t top;
+  Stream st;
+  if (!want(n, 5, "scores") || !read_rows(dev, a[0], "logits", kF32, kBf16, -1, 0, &x) || (a[1] != Py_None && !read_flat(dev, a[1], "tokens", kI32, x.shape[0], &tokens)) ||
+      !read_float(a[2], &scale) || !read_int32(a[3], "top", &top) || !st.read_from(a[4], x))
+    return nullptr;
+  if (top < 0 || top > AQ_MAX_TOP) {
+    PyErr_Format(PyExc_ValueError, "top=%d outside [0, %d]", top, AQ_MAX_TOP);
+    return nullptr;
+  }
+  if (!on_gpu(dev)) return nullptr;
+  at::AutoDispatchBelowADInplaceOrView plain;
+  const int64_t rows = x.shape[0];
+  at::Tensor made[5];
+  const bool scored = a[1] != Py_None;
+  if (scored) made[0] = fresh({rows}, kF32, x);
+  made[1] = fresh({rows}, kF32, x);
+  made[2] = fresh({rows}, kF32, x);
+  if (top) {
+    made[3] = fresh({rows, top}, kF32, x);
+    made[4] = fresh({rows, top}, kI32, x);
+  }
+  auto f32 = [&](int i) { return made[i].defined() ? static_cast<float*>(made[i].data_ptr()) : nullptr; };
+  if (!ok(f_scores(x.ptr, x.stride[0], rows, small(x.shape[1]), x.t->scalar_type() == kF32 ? AQ_PROB_F32 : AQ_PROB_BF16, static_cast<const int32_t*>(tokens.ptr), scale,
+                   f32(0), f32(1), f32(2), top, f32(3), top ? static_cast<int32_t*>(made[4].data_ptr()) : nullptr, st.handle)))
+    return nullptr;
+  PyObject* out[5];
+  for (int i = 0; i < 5; ++i) out[i] = made[i].defined() ? st.hand_out(std::move(made[i])) : given(Py_None);
+  return pack({out[0], out[1], out[2], out[3], out[4]});
+  END_HANDLE_TH_ERRORS
+}
+
+// scores_backward(logits, tokens, lse, entropy, dlogprob, dentropy, dlse, scale, dlogits, stream) -> dlogits
+PyObject* py_scores_backward(PyObject*, PyObject* const* a, Py_ssize_t n) {
+  HANDLE_TH_ERRORS
+  Device dev;
+  Tensor x, tokens, side[5], out;   // side: lse, entropy, dlogprob, dentropy, dlse
+  float scale;
+  Stream st;
+  if (!want(n, 10, "scores_backward") || !read_rows(dev, a[0], "logits", kF32, kBf16, -1, 0, &x)) return nullptr;
+  const int64_t rows = x.shape[0];
+  const char* const names[5] = {"lse", "entropy", "dlogprob", "dentropy", "dlse"};
+  const at::ScalarType dtype = x.t->scalar_type();
+  if (a[1] != Py_None && !read_flat(dev, a[1], "tokens", kI32, rows, &tokens)) return nullptr;
+  for (int i = 0; i < 5; ++i)
+    if (a[2 + i] != Py_None && !read_flat(dev, a[2 + i], names[i], kF32, rows, &side[i])) return nullptr;
+  if (!read_float(a[7], &scale) || (a[8] != Py_None && !read_rows(dev, a[8], "dlogits", dtype, dtype, rows, x.shape[1], &out)) || !st.read_from(a[9], x)) return nullptr;
+  if (a[8] != Py_None && out.shape[1] != x.shape[1]) {
+    PyErr_Format(PyExc_ValueError, "dlogits: expected %lld columns", static_cast<long long>(x.shape[1]));
+    return nullptr;
+  }
+  if (!on_gpu(dev)) return nullptr;
+  at::AutoDispatchBelowADInplaceOrView plain;
+  at::Tensor made;
+  if (a[8] == Py_None) {
+    made = like(x);   // rows as the logits have them, where those are not spread out
+    take(made, &out);
+    if (rows <= 1) out.stride[0] = x.shape[1];
+  }
+  auto f32 = [&](int i) { return static_cast<const float*>(side[i].ptr); };
+  // tokens matter to the gradient of logprob alone
+  if (!ok(f_scores_backward(x.ptr, x.stride[0], rows, small(x.shape[1]), dtype == kF32 ? AQ_PROB_F32 : AQ_PROB_BF16,
+                            side[2].ptr ? static_cast<const int32_t*>(tokens.ptr) : nullptr, scale, f32(0), f32(1), f32(2), f32(3), f32(4), out.ptr, out.stride[0], st.handle)))
+    return nullptr;
+  return made.defined() ? st.hand_out(std::move(made)) : given(a[8]);
+  END_HANDLE_TH_ERRORS
+}
+
 // bind((addresses of the entry points), check)
 PyObject* py_bind(PyObject*, PyObject* args) {
-  unsigned long long f[6];
+  unsigned long long f[12];
   PyObject* check;
-  if (!PyArg_ParseTuple(args, "(KKKKKK)O", &f[0], &f[1], &f[2], &f[3], &f[4], &f[5], &check)) return nullptr;
+  if (!PyArg_ParseTuple(args, "(KKKKKKKKKKKK)O", &f[0], &f[1], &f[2], &f[3], &f[4], &f[5], &f[6], &f[7], &f[8], &f[9], &f[10], &f[11], &check)) return nullptr;
   auto set = [](auto& to, unsigned long long at) { to = reinterpret_cast<std::decay_t<decltype(to)>>(static_cast<uintptr_t>(at)); };
   set(f_rope, f[0]);
-  set(f_kv_write, f[1]);
+  set(f_kv_write_norm, f[1]);
   set(f_kv_read, f[2]);
   set(f_attention_bytes, f[3]);
   set(f_attention, f[4]);
   set(f_verify, f[5]);
+  set(f_norm, f[6]);
+  set(f_norm_bytes, f[7]);
+  set(f_norm_backward, f[8]);
+  set(f_nvfp4, f[9]);
+  set(f_scores, f[10]);
+  set(f_scores_backward, f[11]);
   Py_INCREF(check);
   f_check = check;
   Py_RETURN_NONE;
@@ -557,6 +875,7 @@ PyObject* py_bind(PyObject*, PyObject* args) {
 
 #define FAST(name) {#name, reinterpret_cast<PyCFunction>(reinterpret_cast<void (*)()>(py_##name)), METH_FASTCALL, nullptr}
 PyMethodDef methods[] = {FAST(rope), FAST(kv_write), FAST(kv_read), FAST(attention_bytes), FAST(attention), FAST(verify),
+                         FAST(qk_norm_rope), FAST(qk_norm_rope_backward), FAST(nvfp4_linear), FAST(scores), FAST(scores_backward),
                          {"bind", py_bind, METH_VARARGS, nullptr}, {nullptr, nullptr, 0, nullptr}};
 PyModuleDef module = {PyModuleDef_HEAD_INIT, "_marshal", nullptr, -1, methods, nullptr, nullptr, nullptr, nullptr};
 
@@ -566,7 +885,8 @@ PyMODINIT_FUNC PyInit__marshal(void) {
   struct {
     PyObject** to;
     const char* name;
-  } names[] = {{&s_freq, "freq"}, {&s_layout, "layout"}, {&s_magnitude, "magnitude"}, {&s_k, "k"}, {&s_v, "v"}, {&s_k_scale, "k_scale"}, {&s_v_scale, "v_scale"}};
+  } names[] = {{&s_freq, "freq"}, {&s_layout, "layout"}, {&s_magnitude, "magnitude"}, {&s_k, "k"}, {&s_v, "v"}, {&s_k_scale, "k_scale"}, {&s_v_scale, "v_scale"},
+               {&s_weight, "weight"}, {&s_eps, "eps"}, {&s_offset, "offset"}, {&s_q, "q"}, {&s_sf, "sf"}, {&s_global_scale, "global_scale"}};
   for (auto& n : names)
     if (!(*n.to = PyUnicode_InternFromString(n.name))) return nullptr;
   return PyModule_Create(&module);

@@ -91,6 +91,22 @@ inline bool byte_overlap(const ByteSpan& a, const ByteSpan& b) {
   return a.bytes && b.bytes && a.base < b.base + b.bytes && b.base < a.base + a.bytes;
 }
 
+// Rows of a strided matrix, in bytes. Equal strides tell column slices of one buffer apart; otherwise their whole extents
+// are compared.
+struct ByteRows {
+  uintptr_t base = 0;
+  int64_t rows = 0, stride = 0, bytes = 0;
+  ByteRows() = default;
+  ByteRows(const void* p, int64_t r, int64_t st, int64_t by) : base(reinterpret_cast<uintptr_t>(p)), rows(p ? r : 0), stride(st), bytes(by) {}
+  uintptr_t end() const { return base + static_cast<uintptr_t>((rows - 1) * stride + bytes); }
+  bool meets(const ByteRows& b) const {
+    if (rows < 1 || bytes < 1 || b.rows < 1 || b.bytes < 1 || end() <= b.base || b.end() <= base) return false;
+    if (stride != b.stride || bytes >= stride || b.bytes >= stride) return true;
+    const int64_t d = static_cast<int64_t>(b.base - base) % stride, c = d < 0 ? d + stride : d;   // b's first column in this one's rows
+    return c < bytes || c + b.bytes > stride;
+  }
+};
+
 // Checks of an aq_kv_cache that every call taking one makes.
 aq_status check_kv_cache(const aq_kv_cache* c, const char* who);
 // Bytes of one of its two code arrays.
