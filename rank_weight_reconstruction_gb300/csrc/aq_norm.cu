@@ -1,12 +1,14 @@
-// aq_norm.cu -- aq_qk_norm_rope_backward: the gradient of the head norms with the rotation behind them (their forward is in
-// aq_positions.cu, beside the rotation and the cache's write).
+// aq_norm.cu -- head norms with the rotation behind them: aq_qk_norm_rope, the cache's write with norms, and the gradient
+// aq_qk_norm_rope_backward.
 //
-// With r = 1 / sqrt(mean(x^2) + eps), n = x r, f = offset + w and y = R (n f):
+// With r = 1 / sqrt(mean(x^2) + eps), n = x r, f = offset + w:  y = R (n f), and from dy
 //   g = R^T dy,  dx = r (g f - n mean(g f n)),  dw_i = sum over tokens and heads of g_i n_i.
-// Bound by memory: x and dy are read once, dx is written once, and a head needs two sums over its elements. A group of lanes
-// holds a head as in the forward, 16 elements a lane. The weight's gradient stays in 16 registers a lane over all
-// the heads that the lane sees, so a block is given heads of q alone or of k alone; the groups' sums meet in shared memory, the
-// blocks' in the workspace, and a second launch adds those up, all in an order fixed by the sizes.
+// Bound by memory: every element is read once (the gradient: x and dy) and written once. A group of lanes holds a head as in the
+// rotation, 16 elements a lane, kept as the eight pairs that turn against each other in either order, so that squares, scales and
+// turns are packed products of two; a head's sums are a few shuffles. The factors f stay in registers while a group walks the heads
+// of q, then those of k. In the gradient the weight's sums stay in 16 registers a lane over all the heads that the lane sees,
+// so a block is given heads of q alone or of k alone; the groups' sums meet in shared memory, the blocks' in the workspace, and a
+// second launch adds those up, all in an order fixed by the sizes and the device's SM count.
 #include <algorithm>
 
 #include "aq_positions.cuh"
@@ -14,6 +16,256 @@
 namespace aq {
 namespace {
 
+// Two chunks of a lane as pairs that turn against each other: (a[i], b[i]).
+template <bool HALF>
+__device__ __forceinline__ void unpack_pairs(const uint4& r0, const uint4& r1, float (&a)[8], float (&b)[8]) {
+  if (HALF) {
+    unpack8(r0, a);
+    unpack8(r1, b);
+  } else {
+    const uint32_t w[8] = {r0.x, r0.y, r0.z, r0.w, r1.x, r1.y, r1.z, r1.w};
+#pragma unroll
+    for (int i = 0; i < 8; ++i) {
+      a[i] = __uint_as_float(w[i] << 16);
+      b[i] = __uint_as_float(w[i] & 0xffff0000u);
+    }
+  }
+}
+template <bool HALF>
+__device__ __forceinline__ void pack_pairs(const float (&a)[8], const float (&b)[8], uint4& r0, uint4& r1) {
+  if (HALF) {
+    r0 = pack8(a);
+    r1 = pack8(b);
+  } else {
+    r0 = make_uint4(pack_bf16x2_cvt(a[0], b[0]), pack_bf16x2_cvt(a[1], b[1]), pack_bf16x2_cvt(a[2], b[2]), pack_bf16x2_cvt(a[3], b[3]));
+    r1 = make_uint4(pack_bf16x2_cvt(a[4], b[4]), pack_bf16x2_cvt(a[5], b[5]), pack_bf16x2_cvt(a[6], b[6]), pack_bf16x2_cvt(a[7], b[7]));
+  }
+}
+// The rotation, pairs FROM .. FROM + 3, each product rounded as in aq_rope.
+template <int FROM>
+__device__ __forceinline__ void turn4(float (&a)[8], float (&b)[8], const float (&c)[8], const float (&s)[8]) {
+#pragma unroll
+  for (int i = FROM; i < FROM + 4; i += 2) {
+    float t0, t1, u0, u1;
+    fmul2_rn(t0, t1, b[i], b[i + 1], s[i], s[i + 1]);
+    fmul2_rn(u0, u1, a[i], a[i + 1], s[i], s[i + 1]);
+    a[i] = fmaf(a[i], c[i], -t0);
+    a[i + 1] = fmaf(a[i + 1], c[i + 1], -t1);
+    ffma2_rn(b[i], b[i + 1], b[i], b[i + 1], c[i], c[i + 1], u0, u1);
+  }
+}
+__device__ __forceinline__ void scale8(float (&x)[8], const float (&y)[8]) {
+#pragma unroll
+  for (int i = 0; i < 8; i += 2) fmul2_rn(x[i], x[i + 1], x[i], x[i + 1], y[i], y[i + 1]);
+}
+__device__ __forceinline__ void scale8(float (&x)[8], float y) {
+#pragma unroll
+  for (int i = 0; i < 8; i += 2) fmul2_rn(x[i], x[i + 1], x[i], x[i + 1], y, y);
+}
+__device__ __forceinline__ void dot8(float& s0, float& s1, const float (&x)[8], const float (&y)[8]) {
+#pragma unroll
+  for (int i = 0; i < 8; i += 2) ffma2_rn(s0, s1, x[i], x[i + 1], y[i], y[i + 1], s0, s1);
+}
+template <int GW>
+__device__ __forceinline__ float group_sum(float s, uint32_t group) {
+#pragma unroll
+  for (int o = GW / 2; o > 0; o >>= 1) s += __shfl_xor_sync(group, s, o);
+  return s;
+}
+
+// 1 / sqrt(mean(x^2) + eps) of a head held by a group of GW lanes, 16 elements a lane (zeros past the head). Squares of numbers
+// past 2^60 could leave fp32: such a head is measured at 2^-70 of its size, where eps is nothing.
+template <int GW>
+__device__ __forceinline__ float head_rstd(const float (&a)[8], const float (&b)[8], uint32_t group, float inv_dim, float eps) {
+  float s0 = 0.0f, s1 = 0.0f;
+  dot8(s0, s1, a, a);
+  dot8(s0, s1, b, b);
+  float s = group_sum<GW>(s0 + s1, group);
+  if (s < 0x1p120f) return rsqrtf(fmaf(s, inv_dim, eps));
+  s0 = 0.0f;
+#pragma unroll
+  for (int i = 0; i < 8; ++i) {
+    const float x = a[i] * 0x1p-70f, y = b[i] * 0x1p-70f;
+    s0 = fmaf(x, x, s0);
+    s0 = fmaf(y, y, s0);
+  }
+  return rsqrtf(group_sum<GW>(s0, group) * inv_dim) * 0x1p-70f;
+}
+
+// offset + weight for a lane's pairs; ones without a weight.
+template <bool HALF>
+__device__ __forceinline__ void norm_factors(const uint16_t* w, int k0, int k1, float offset, float (&f)[8], float (&h)[8]) {
+  if (w) {
+    unpack_pairs<HALF>(__ldg(reinterpret_cast<const uint4*>(w + k0)), __ldg(reinterpret_cast<const uint4*>(w + k1)), f, h);
+#pragma unroll
+    for (int i = 0; i < 8; ++i) {
+      f[i] += offset;
+      h[i] += offset;
+    }
+  } else {
+#pragma unroll
+    for (int i = 0; i < 8; ++i) f[i] = h[i] = 1.0f;
+  }
+}
+
+// ---------------------------------------------------------------------------------
+// forward
+// ---------------------------------------------------------------------------------
+struct HeadSet {
+  const uint16_t* x;
+  uint16_t* y;            // NULL: to the cache
+  const uint16_t* w;
+  int64_t x_tok, x_head, y_tok, y_head;
+  float eps, offset;
+  int32_t heads, normed;
+};
+struct HeadNormParams {
+  HeadSet set[3];         // q, k, v (v: no norm, not turned)
+  const int32_t* pos;
+  const uint64_t* freq;   // NULL: nothing is turned
+  const int64_t* slots;
+  uint8_t* c[2];          // the cache's keys and values
+  float* sc[2];
+  int64_t T, n_slots;
+  int32_t D, rot16, page_shift, hl_shift;
+  float magnitude;
+};
+
+enum To { kTensor, kCacheBf16, kCacheE4m3 };
+
+template <bool HALF, int GW, To TO, bool SPLIT>
+__global__ void __launch_bounds__(256, 3) aq_head_norm_kernel(const __grid_constant__ HeadNormParams p) {
+  pdl_wait_prior_grid();
+  pdl_launch_dependents();
+  const int u = threadIdx.x % GW, lane = threadIdx.x & 31;
+  const int64_t item = static_cast<int64_t>(blockIdx.x) * (256 / GW) + threadIdx.x / GW;
+  const int64_t t = item >> p.hl_shift;
+  const int hl = 1 << p.hl_shift, h0 = static_cast<int>(item & (hl - 1));
+  const bool live = t < p.T && u * 16 < p.D;
+  const int64_t tt = live ? t : 0;
+  const Chunks<HALF> ch(u, p.rot16, p.D / 16);
+  float c[8], s[8];
+  angles<HALF, GW, SPLIT>(ch, u, p.freq, p.freq && live ? p.pos[tt] : 0, p.magnitude, p.magnitude, c, s);
+  const bool turn0 = p.freq && live && ch.turns0, turn1 = p.freq && live && ch.turns1;
+  int64_t cell0 = -1;
+  if (TO != kTensor && live) {
+    const int64_t slot = p.slots[tt];
+    if (slot >= 0 && slot < p.n_slots)
+      cell0 = (((slot >> p.page_shift) * p.set[1].heads) << p.page_shift) + (slot & ((1 << p.page_shift) - 1));
+  }
+  // groups of one warp may be at different heads, so each shuffles by itself
+  const uint32_t group = (GW == 32 ? 0xffffffffu : (1u << GW) - 1) << (lane & ~(GW - 1));
+  // lanes without work load lane 0's chunks: a load under a condition would be waited for at once
+  const int k0 = live ? ch.c0 * 8 : 0, k1 = live ? ch.c1 * 8 : 0;
+  const float inv_dim = 1.0f / p.D;
+
+  auto walk = [&](const HeadSet& q, int which, int first) {
+    float f0[8], f1[8];
+    if (which < 2 && q.normed) norm_factors<HALF>(q.w, k0, k1, q.offset, f0, f1);
+    const uint16_t* x = q.x + tt * q.x_tok;
+    auto finish = [&](int h, const uint4& r0, const uint4& r1) {
+      uint4 o0 = r0, o1 = r1;
+      float a[8], b[8];
+      if (which < 2 || TO == kCacheE4m3) {
+        const uint4 none = make_uint4(0, 0, 0, 0);
+        unpack_pairs<HALF>(live ? r0 : none, live ? r1 : none, a, b);
+      }
+      if (which < 2) {
+        if (q.normed) {
+          const float r = head_rstd<GW>(a, b, group, inv_dim, q.eps);
+          scale8(a, r);
+          scale8(b, r);
+          scale8(a, f0);
+          scale8(b, f1);
+        }
+        if (turn0) turn4<0>(a, b, c, s);
+        if (turn1) turn4<4>(a, b, c, s);
+        if (TO != kCacheE4m3 || which == 0) pack_pairs<HALF>(a, b, o0, o1);
+      }
+      if (which == 0 || TO == kTensor) {
+        uint16_t* dst = q.y + tt * q.y_tok + h * q.y_head;
+        if (live) *reinterpret_cast<uint4*>(dst + k0) = o0;
+        if (live) *reinterpret_cast<uint4*>(dst + k1) = o1;
+        return;
+      }
+      const int64_t cell = cell0 + (static_cast<int64_t>(h) << p.page_shift);
+      if (TO == kCacheBf16) {
+        if (cell0 < 0) return;
+        uint16_t* dst = reinterpret_cast<uint16_t*>(p.c[which - 1]) + cell * p.D;
+        if (live) *reinterpret_cast<uint4*>(dst + k0) = o0;
+        if (live) *reinterpret_cast<uint4*>(dst + k1) = o1;
+        return;
+      }
+      // as the cache's write without norms: max|x| on the bit patterns, a NaN or infinity stays the largest
+      uint32_t top = 0;
+#pragma unroll
+      for (int i = 0; i < 8; ++i) top = max(top, max(__float_as_uint(a[i]) & 0x7fffffffu, __float_as_uint(b[i]) & 0x7fffffffu));
+#pragma unroll
+      for (int o = GW / 2; o > 0; o >>= 1) top = max(top, __shfl_xor_sync(group, top, o));
+      if (cell0 < 0) return;
+      const bool finite = top < 0x7f800000u;
+      const float scale = finite ? fmaxf(__uint_as_float(top) * (1.0f / kE4m3Max), kKvScaleFloor) : __uint_as_float(0x7fc00000u);
+      const float inv = finite ? __frcp_rn(scale) : 0.0f;
+      uint8_t* dst = p.c[which - 1] + cell * p.D;
+      scale8(a, inv);
+      scale8(b, inv);
+      auto two = [&](float lo, float hi) { return static_cast<uint32_t>(e4m3x2_from_f32(lo, hi)); };
+      uint2 d0, d1;
+      if (HALF) {
+        d0 = make_uint2(two(a[0], a[1]) | (two(a[2], a[3]) << 16), two(a[4], a[5]) | (two(a[6], a[7]) << 16));
+        d1 = make_uint2(two(b[0], b[1]) | (two(b[2], b[3]) << 16), two(b[4], b[5]) | (two(b[6], b[7]) << 16));
+      } else {
+        d0 = make_uint2(two(a[0], b[0]) | (two(a[1], b[1]) << 16), two(a[2], b[2]) | (two(a[3], b[3]) << 16));
+        d1 = make_uint2(two(a[4], b[4]) | (two(a[5], b[5]) << 16), two(a[6], b[6]) | (two(a[7], b[7]) << 16));
+      }
+      if (!finite) d0 = d1 = make_uint2(0, 0);
+      if (live) *reinterpret_cast<uint2*>(dst + k0) = d0;
+      if (live) *reinterpret_cast<uint2*>(dst + k1) = d1;
+      if (u == 0) p.sc[which - 1][cell] = scale;
+    };
+    // two heads' loads in flight
+    for (int h = first; h < q.heads; h += 2 * hl) {
+      const bool two = h + hl < q.heads;
+      const uint16_t* s0 = x + h * q.x_head;
+      const uint16_t* s1 = two ? s0 + hl * q.x_head : s0;
+      const uint4 r0 = ld_stream(s0 + k0), r1 = ld_stream(s0 + k1), r2 = ld_stream(s1 + k0), r3 = ld_stream(s1 + k1);
+      finish(h, r0, r1);
+      if (two) finish(h + hl, r2, r3);
+    }
+  };
+  // the groups of a token take its heads in turn, all three sets as one list
+  walk(p.set[0], 0, h0);
+  walk(p.set[1], 1, (h0 - p.set[0].heads) & (hl - 1));
+  if (TO != kTensor) walk(p.set[2], 2, (h0 - p.set[0].heads - p.set[1].heads) & (hl - 1));
+}
+
+template <bool HALF, int GW, To TO>
+cudaError_t launch_head_norm(const HeadNormParams& p, unsigned blocks, cudaStream_t st) {
+  if (GW < 32 && (GW << p.hl_shift) >= 32) return launch_serve(aq_head_norm_kernel<HALF, GW, TO, true>, p, blocks, 256, 0, st);
+  return launch_serve(aq_head_norm_kernel<HALF, GW, TO, false>, p, blocks, 256, 0, st);
+}
+template <bool HALF, To TO>
+cudaError_t launch_head_norm(const HeadNormParams& p, unsigned blocks, int gw, cudaStream_t st) {
+  switch (gw) {
+    case 1: return launch_head_norm<HALF, 1, TO>(p, blocks, st);
+    case 2: return launch_head_norm<HALF, 2, TO>(p, blocks, st);
+    case 4: return launch_head_norm<HALF, 4, TO>(p, blocks, st);
+    case 8: return launch_head_norm<HALF, 8, TO>(p, blocks, st);
+    default: return launch_head_norm<HALF, 16, TO>(p, blocks, st);
+  }
+}
+template <bool HALF>
+cudaError_t launch_head_norm(const HeadNormParams& p, unsigned blocks, int gw, To to, cudaStream_t st) {
+  switch (to) {
+    case kTensor: return launch_head_norm<HALF, kTensor>(p, blocks, gw, st);
+    case kCacheBf16: return launch_head_norm<HALF, kCacheBf16>(p, blocks, gw, st);
+    default: return launch_head_norm<HALF, kCacheE4m3>(p, blocks, gw, st);
+  }
+}
+
+// ---------------------------------------------------------------------------------
+// gradient
+// ---------------------------------------------------------------------------------
 constexpr int kNormThreads = 256, kNormPerSm = 2;
 
 struct NormSet {
@@ -53,56 +305,56 @@ __global__ void __launch_bounds__(kNormThreads, kNormPerSm) aq_norm_grad_kernel(
   const int hl = 1 << s.hl_shift;
   const float inv_dim = 1.0f / p.D;
   float f0[8], f1[8], w0[8], w1[8];
-  norm_factor(s.w, k0 / 8, s.offset, f0);
-  norm_factor(s.w, k1 / 8, s.offset, f1);
+  norm_factors<HALF>(s.w, k0, k1, s.offset, f0, f1);
 #pragma unroll
   for (int i = 0; i < 8; ++i) w0[i] = w1[i] = 0.0f;
 
   const int64_t items = p.T << s.hl_shift, step = static_cast<int64_t>(s.blocks) * kGroups;
-  // a warp's groups walk together: every lane is there when angles are passed round
-  for (int64_t first = static_cast<int64_t>(block) * kGroups + (threadIdx.x / 32) * (32 / GW); first < items; first += step) {
-    const int64_t item = first + lane / GW;
-    const bool live = item < items && mine;
-    const int64_t t = live ? item >> s.hl_shift : 0;
+  for (int64_t item = static_cast<int64_t>(block) * kGroups + threadIdx.x / GW; item < items; item += step) {
+    const int64_t t = item >> s.hl_shift;
     float c[8], sn[8];
-    angles<HALF, GW, false>(ch, u, p.freq, p.freq && live ? p.pos[t] : 0, p.magnitude, -p.magnitude, c, sn);
-    const bool turns = p.freq && live && (ch.turns0 || ch.turns1);
+    angles<HALF, GW, false>(ch, u, p.freq, p.freq && mine ? p.pos[t] : 0, p.magnitude, -p.magnitude, c, sn);
+    const bool turn0 = p.freq && mine && ch.turns0, turn1 = p.freq && mine && ch.turns1;
+    const uint16_t* xs = s.x + t * s.x_tok;
+    const uint16_t* ys = s.dy + t * s.dy_tok;
+    uint16_t* ds = s.dx + t * s.dx_tok;
     for (int h = static_cast<int>(item & (hl - 1)); h < s.heads; h += hl) {
-      const uint16_t* xs = s.x + t * s.x_tok + h * s.x_head;
-      const uint16_t* ys = s.dy + t * s.dy_tok + h * s.dy_head;
-      const uint4 r0 = ld_stream(xs + k0), r1 = ld_stream(xs + k1), r2 = ld_stream(ys + k0), r3 = ld_stream(ys + k1);
+      const uint16_t* xh = xs + h * s.x_head;
+      const uint16_t* yh = ys + h * s.dy_head;
+      const uint4 r0 = ld_stream(xh + k0), r1 = ld_stream(xh + k1), r2 = ld_stream(yh + k0), r3 = ld_stream(yh + k1);
       float a[8], b[8], ga[8], gb[8];
       const uint4 none = make_uint4(0, 0, 0, 0);
-      unpack8(live ? r0 : none, a);
-      unpack8(live ? r1 : none, b);
-      unpack8(live ? r2 : none, ga);
-      unpack8(live ? r3 : none, gb);
-      if (turns) rotate16<HALF>(ga, gb, c, sn, ch.turns1);
+      unpack_pairs<HALF>(mine ? r0 : none, mine ? r1 : none, a, b);
+      unpack_pairs<HALF>(mine ? r2 : none, mine ? r3 : none, ga, gb);
+      if (turn0) turn4<0>(ga, gb, c, sn);
+      if (turn1) turn4<4>(ga, gb, c, sn);
       const float r = head_rstd<GW>(a, b, group, inv_dim, s.eps);
-      float dot = 0.0f;
+      scale8(a, r);
+      scale8(b, r);
 #pragma unroll
-      for (int i = 0; i < 8; ++i) {
-        a[i] *= r;
-        b[i] *= r;
-        w0[i] = fmaf(ga[i], a[i], w0[i]);
-        w1[i] = fmaf(gb[i], b[i], w1[i]);
-        ga[i] *= f0[i];
-        gb[i] *= f1[i];
-        dot = fmaf(ga[i], a[i], dot);
-        dot = fmaf(gb[i], b[i], dot);
+      for (int i = 0; i < 8; i += 2) {
+        ffma2_rn(w0[i], w0[i + 1], ga[i], ga[i + 1], a[i], a[i + 1], w0[i], w0[i + 1]);
+        ffma2_rn(w1[i], w1[i + 1], gb[i], gb[i + 1], b[i], b[i + 1], w1[i], w1[i + 1]);
       }
+      scale8(ga, f0);
+      scale8(gb, f1);
+      float d0 = 0.0f, d1 = 0.0f;
+      dot8(d0, d1, ga, a);
+      dot8(d0, d1, gb, b);
+      const float dot = -group_sum<GW>(d0 + d1, group) * inv_dim;
 #pragma unroll
-      for (int o = GW / 2; o > 0; o >>= 1) dot += __shfl_xor_sync(group, dot, o);
-      dot *= inv_dim;
-#pragma unroll
-      for (int i = 0; i < 8; ++i) {
-        a[i] = r * fmaf(-a[i], dot, ga[i]);
-        b[i] = r * fmaf(-b[i], dot, gb[i]);
+      for (int i = 0; i < 8; i += 2) {
+        ffma2_rn(a[i], a[i + 1], a[i], a[i + 1], dot, dot, ga[i], ga[i + 1]);
+        ffma2_rn(b[i], b[i + 1], b[i], b[i + 1], dot, dot, gb[i], gb[i + 1]);
       }
-      if (live) {
-        uint16_t* d = s.dx + t * s.dx_tok + h * s.dx_head;
-        *reinterpret_cast<uint4*>(d + k0) = pack8(a);
-        *reinterpret_cast<uint4*>(d + k1) = pack8(b);
+      scale8(a, r);
+      scale8(b, r);
+      if (mine) {
+        uint16_t* d = ds + h * s.dx_head;
+        uint4 o0, o1;
+        pack_pairs<HALF>(a, b, o0, o1);
+        *reinterpret_cast<uint4*>(d + k0) = o0;
+        *reinterpret_cast<uint4*>(d + k1) = o1;
       }
     }
   }
@@ -110,9 +362,9 @@ __global__ void __launch_bounds__(kNormThreads, kNormPerSm) aq_norm_grad_kernel(
   float* row = sums[threadIdx.x / GW];
   if (mine) {
 #pragma unroll
-    for (int i = 0; i < 8; ++i) {
-      row[k0 + i] = w0[i];
-      row[k1 + i] = w1[i];
+    for (int i = 0; i < 8; ++i) {   // pair i: elements i of either chunk, or 2 i and 2 i + 1
+      row[HALF ? k0 + i : (i < 4 ? k0 : k1) + 2 * (i & 3)] = w0[i];
+      row[HALF ? k1 + i : (i < 4 ? k0 : k1) + 2 * (i & 3) + 1] = w1[i];
     }
   }
   __syncthreads();
@@ -123,31 +375,32 @@ __global__ void __launch_bounds__(kNormThreads, kNormPerSm) aq_norm_grad_kernel(
   }
 }
 
-// dw = the blocks' sums, 32 elements of one set a block: eight threads an element, each every eighth block.
+// dw = the blocks' sums, 32 elements of one set a block: 32 threads an element, each every 32nd block.
 struct NormJoinParams {
   const float* part[2];
   float* dw[2];
   int32_t blocks[2];
   int32_t D, tiles;    // tiles of 32 elements of a set
 };
-__global__ void __launch_bounds__(256) aq_norm_join_kernel(const __grid_constant__ NormJoinParams p) {
+__global__ void __launch_bounds__(1024) aq_norm_join_kernel(const __grid_constant__ NormJoinParams p) {
   pdl_wait_prior_grid();
   pdl_launch_dependents();
-  __shared__ float sums[8][33];
+  __shared__ float sums[32][33];
   const int which = static_cast<int>(blockIdx.x) / p.tiles, d = (static_cast<int>(blockIdx.x) % p.tiles) * 32 + (threadIdx.x & 31);
   const int part = threadIdx.x / 32;
   if (!p.dw[which]) return;
   float v = 0.0f;
   if (d < p.D) {
-#pragma unroll 8
-    for (int i = part; i < p.blocks[which]; i += 8) v += p.part[which][static_cast<int64_t>(i) * p.D + d];
+#pragma unroll 4
+    for (int i = part; i < p.blocks[which]; i += 32) v += p.part[which][static_cast<int64_t>(i) * p.D + d];
   }
-  sums[part][threadIdx.x & 31] = v;
+  sums[threadIdx.x & 31][part] = v;
   __syncthreads();
-  if (part == 0 && d < p.D) {
-    for (int i = 1; i < 8; ++i) v += sums[i][threadIdx.x];
-    p.dw[which][d] = v;
-  }
+  v = sums[part][threadIdx.x & 31];   // a warp an element
+#pragma unroll
+  for (int o = 16; o > 0; o >>= 1) v += __shfl_xor_sync(0xffffffffu, v, o);
+  const int at = (static_cast<int>(blockIdx.x) % p.tiles) * 32 + part;
+  if ((threadIdx.x & 31) == 0 && at < p.D) p.dw[which][at] = v;
 }
 
 // Blocks of the two sets: what fills the GPU, shared out by their heads; no more than their groups of work.
@@ -158,11 +411,7 @@ void norm_blocks(int64_t T, int32_t D, int32_t hq, int32_t hk, int sms, int32_t*
     hl_shift[i] = 0;
     blocks[i] = 0;
     if (!heads[i]) continue;
-    // groups that share a token: a warp's, more while the call does not fill the GPU, and never more than heads
-    int most = 0;
-    while ((2 << most) <= heads[i] && (2 << most) <= groups) ++most;
-    hl_shift[i] = std::min(log2_of(32 / gw), most);
-    while (hl_shift[i] < most && (T << hl_shift[i]) < static_cast<int64_t>(fill) * groups / 2) ++hl_shift[i];
+    hl_shift[i] = share_token(T, heads[i], gw, static_cast<int64_t>(fill) * groups / 2);
     const int64_t need = ((T << hl_shift[i]) + groups - 1) / groups;
     const int64_t share = std::max<int64_t>(1, static_cast<int64_t>(fill) * heads[i] / (hq + hk));
     blocks[i] = static_cast<int32_t>(std::min(need, share));
@@ -183,9 +432,112 @@ cudaError_t launch_norm_grad(const NormGradParams& p, int gw, cudaStream_t st) {
 }
 
 }  // namespace
+
+aq_status run_head_norm(const aq_head_norm* q_norm, const aq_head_norm* k_norm, const aq_rope_spec* rope, const int32_t* pos, int64_t T,
+                        int32_t D, const aq_heads* q, const aq_heads* q_out, const aq_heads* k, const aq_heads* k_out, const aq_heads* v,
+                        const aq_kv_cache* cache, const int64_t* slots, cudaStream_t st, const char* who) {
+  ServeDev dev;
+  const aq_status s = serve_device(&dev);
+  if (s != AQ_OK) return s;
+  HeadNormParams p = {};
+  const aq_heads* const in[3] = {q, k, v};
+  const aq_heads* const out[3] = {q_out, k_out, nullptr};
+  const aq_head_norm* const norm[3] = {q_norm, k_norm, nullptr};
+  int heads = 0;
+  for (int i = 0; i < 3; ++i) {
+    if (!in[i]) continue;
+    HeadSet& h = p.set[i];
+    h.x = static_cast<const uint16_t*>(in[i]->data);
+    h.x_tok = in[i]->tok;
+    h.x_head = in[i]->head;
+    h.heads = in[i]->heads;
+    heads += h.heads;
+    if (out[i]) {
+      h.y = static_cast<uint16_t*>(out[i]->data);
+      h.y_tok = out[i]->tok;
+      h.y_head = out[i]->head;
+    }
+    if (norm[i]) {
+      h.normed = 1;
+      h.w = static_cast<const uint16_t*>(norm[i]->weight);
+      h.eps = norm[i]->eps;
+      h.offset = norm[i]->offset;
+    }
+  }
+  if (rope) {
+    p.pos = pos;
+    p.freq = rope->freq;
+    p.rot16 = rope->rotary_dim / 16;
+    p.magnitude = rope->magnitude;
+  }
+  if (cache) {
+    p.slots = slots;
+    p.c[0] = static_cast<uint8_t*>(cache->k);
+    p.c[1] = static_cast<uint8_t*>(cache->v);
+    p.sc[0] = cache->k_scale;
+    p.sc[1] = cache->v_scale;
+    p.n_slots = static_cast<int64_t>(cache->pages) * cache->page_size;
+    p.page_shift = log2_of(cache->page_size);
+  }
+  p.T = T;
+  p.D = D;
+  const int gw = group_width(D);
+  p.hl_shift = share_token(T, heads, gw, static_cast<int64_t>(dev.sms) * 768 / gw);
+  const int64_t blocks = ((T << p.hl_shift) + 256 / gw - 1) / (256 / gw);
+  if (blocks > 0x7fffffffLL) return serve_fail(AQ_ERR_SHAPE, "%s: %lld tokens are too many for one call", who, (long long)T);
+  const To to = !cache ? kTensor : cache->type == AQ_KV_BF16 ? kCacheBf16 : kCacheE4m3;
+  const unsigned g = static_cast<unsigned>(blocks);
+  return serve_launched(rope && rope->layout == AQ_ROPE_HALF ? launch_head_norm<true>(p, g, gw, to, st) : launch_head_norm<false>(p, g, gw, to, st), who);
+}
+
 }  // namespace aq
 
 using namespace aq;
+
+extern "C" aq_status aq_qk_norm_rope(const aq_head_norm* q_norm, const aq_head_norm* k_norm, const aq_rope_spec* rope, const int32_t* pos,
+                                     int64_t T, int32_t head_dim, const aq_heads* q, const aq_heads* q_out, const aq_heads* k,
+                                     const aq_heads* k_out, void* stream) {
+  const char* who = "aq_qk_norm_rope";
+  if (T < 0) return serve_fail(AQ_ERR_SHAPE, "%s: T=%lld is negative", who, (long long)T);
+  if (head_dim < 16 || head_dim % 16 || head_dim > kServeMaxHeadDim)
+    return serve_fail(AQ_ERR_SHAPE, "%s: head_dim=%d must be a multiple of 16 up to %d", who, head_dim, kServeMaxHeadDim);
+  if (!q || !q_out) return serve_fail(AQ_ERR_INVALID_ARG, "%s: q and q_out must be non-NULL", who);
+  if (!k != !k_out) return serve_fail(AQ_ERR_INVALID_ARG, "%s: k and k_out go together", who);
+  if (k_norm && !k) return serve_fail(AQ_ERR_INVALID_ARG, "%s: k_norm needs k", who);
+  aq_status st;
+  if (rope && (st = check_rope_spec(rope, head_dim, who)) != AQ_OK) return st;
+  if ((st = check_head_norm(q_norm, "q_norm", who)) != AQ_OK || (st = check_head_norm(k_norm, "k_norm", who)) != AQ_OK) return st;
+  const aq_heads* const in[2] = {q, k};
+  const aq_heads* const out[2] = {q_out, k_out};
+  const int sets = k ? 2 : 1;
+  for (int i = 0; i < sets; ++i)
+    if (in[i]->heads < 1 || in[i]->heads != out[i]->heads)
+      return serve_fail(AQ_ERR_SHAPE, "%s: heads=%d and %d must be >= 1 and equal", who, in[i]->heads, out[i]->heads);
+  if (T == 0) return AQ_OK;
+  if (rope && !pos) return serve_fail(AQ_ERR_INVALID_ARG, "%s: rope needs pos", who);
+  const char* const names[2][2] = {{"q", "q_out"}, {"k", "k_out"}};
+  for (int i = 0; i < sets; ++i) {
+    if ((st = check_heads(in[i]->data, in[i]->tok, in[i]->head, in[i]->heads, head_dim, names[i][0], who)) != AQ_OK) return st;
+    if ((st = check_heads(out[i]->data, out[i]->tok, out[i]->head, out[i]->heads, head_dim, names[i][1], who)) != AQ_OK) return st;
+    if ((st = check_out_heads(out[i]->tok, out[i]->head, T, out[i]->heads, head_dim, names[i][1], who)) != AQ_OK) return st;
+  }
+  const ByteRows side[] = {ByteRows(rope ? pos : nullptr, 1, T * 4, T * 4), ByteRows(rope ? rope->freq : nullptr, 1, head_dim * 4, rope ? rope->rotary_dim * 4 : 0),
+                           ByteRows(q_norm ? q_norm->weight : nullptr, 1, head_dim * 2, head_dim * 2), ByteRows(k_norm ? k_norm->weight : nullptr, 1, head_dim * 2, head_dim * 2)};
+  for (int i = 0; i < sets; ++i) {
+    const ByteRows o = heads_rows(out[i], T, head_dim);
+    for (const ByteRows& s : side)
+      if (o.meets(s)) return serve_fail(AQ_ERR_OVERLAP, "%s: %s overlaps an input", who, names[i][1]);
+    for (int j = 0; j < sets; ++j) {
+      const bool same = i == j && in[i]->data == out[i]->data && (T == 1 || in[i]->tok == out[i]->tok) && (in[i]->heads == 1 || in[i]->head == out[i]->head);
+      if (!same && o.meets(heads_rows(in[j], T, head_dim)))
+        return serve_fail(AQ_ERR_OVERLAP, "%s: %s overlaps %s (in place needs the same pointer and strides)", who, names[i][1], names[j][0]);
+    }
+  }
+  if (sets == 2 && heads_rows(q_out, T, head_dim).meets(heads_rows(k_out, T, head_dim)))
+    return serve_fail(AQ_ERR_OVERLAP, "%s: q_out and k_out overlap", who);
+  return run_head_norm(q_norm, k_norm, rope, pos, T, head_dim, q, q_out, k, k_out, nullptr, nullptr, nullptr, static_cast<cudaStream_t>(stream), who);
+}
+
 
 extern "C" size_t aq_qk_norm_rope_backward_workspace_bytes(int64_t T, int32_t head_dim, int32_t q_heads, int32_t k_heads) {
   if (T < 0 || head_dim < 16 || head_dim % 16 || head_dim > kServeMaxHeadDim || q_heads < 1 || k_heads < 0) {
@@ -304,5 +656,5 @@ extern "C" aq_status aq_qk_norm_rope_backward(const aq_head_norm* q_norm, const 
   }
   j.D = D;
   j.tiles = (D + 31) / 32;
-  return serve_launched(launch_serve(aq_norm_join_kernel, j, dim3(static_cast<unsigned>(sets * j.tiles)), 256, 0, cs), who);
+  return serve_launched(launch_serve(aq_norm_join_kernel, j, dim3(static_cast<unsigned>(sets * j.tiles)), 1024, 0, cs), who);
 }

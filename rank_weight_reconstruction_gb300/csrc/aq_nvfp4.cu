@@ -5,14 +5,15 @@
 //
 // A code times its block scale has six significant bits between 2^-10 and 2688: exact in f16, so the weights are widened
 // to f16 in registers (one conversion for two codes, one packed product with the scale) and go to mma.sync as its 16-row
-// operand, the tokens as its 8 columns. x enters as f16 too, each token of a CTA's K slice scaled by the power of two that
+// operand, the tokens as its 8 columns. x enters as f16 too, each token's chunk of 256 K scaled by the power of two that
 // brings its largest element to at least 2^15: an element down to 2^-32 of the largest keeps all its bits. Sums are fp32.
 //
-// Bound by memory: 0.5625 bytes a weight are read once. A cluster of S CTAs takes groups of R row tiles of 16, each CTA a
-// K slice whose x it keeps in shared memory; its eight warps share out the group's tiles and the slice's chunks of 128, each
-// streaming its chunks through a ring of its own (cp.async: every lane copies what it will itself multiply, the scales
-// apart), so no barrier stands in the stream. Sums meet in shared memory once a group, in a fixed order, then over the
-// cluster, whose exchange of one group runs under the stream of the next.
+// Bound by memory: 0.5625 bytes a weight are read once. A cluster of S CTAs, one an SM, takes a stretch of row tiles of 16, each CTA
+// a K slice whose x it keeps in shared memory. Its sixteen warps share out the tiles' chunks of 256 K, and each streams its
+// own through a ring of its own (cp.async), so no barrier stands in the stream. Either a warp takes whole tiles, whose sums leave
+// from its registers, or, where the tiles are few, the chunks laid end to end are cut into equal runs, and a tile's sums from the
+// runs that cross it meet in shared memory, in the runs' order. The cluster's CTAs are added in their order, through distributed
+// shared memory.
 #include <algorithm>
 #include <atomic>
 
@@ -21,14 +22,11 @@
 namespace aq {
 namespace {
 
-constexpr int kQWarps = 8, kQThreads = 32 * kQWarps;
-constexpr int kQDepth = 6;                      // ring stages of a warp, one chunk each
-constexpr int kQChunk = 128;                    // K of a chunk: 64 bytes of codes a row
-constexpr int kQCodes = 1024;                   // bytes of a chunk's codes: 16 rows
-constexpr int kQStage = kQCodes + 16 * 12;      // and 12 bytes of scales a row: eight, and room for any alignment
-constexpr int kQPart = 20;                      // floats a token of a warp's partial sums: 16 rows, spread over the banks
-constexpr int kQMaxS = 8;
-constexpr int kQHead = 256;                     // bytes: per token the largest element, then the factor back
+constexpr int kQChunk = 256;                    // K of a chunk: 128 bytes of codes a row, 16 scales
+constexpr int kQCodes = 16 * 128;               // bytes of a chunk's codes
+constexpr int kQStage = kQCodes + 16 * 32;      // and up to 32 bytes of scales a row (two pieces of 16 hold 16 bytes at any alignment)
+constexpr int kQRow = 4 * 144;                  // bytes of a chunk of a token of x
+constexpr int kQPart = 20;                      // floats a token of a tile's partial sums: 16 rows, spread over the banks
 
 struct Nvfp4Seg {
   const uint8_t* q;
@@ -37,7 +35,7 @@ struct Nvfp4Seg {
   uint16_t* y;
   int64_t ldq, ldy;
   int32_t out;
-  int32_t begin;       // first group
+  int32_t begin;       // first tile
 };
 struct Nvfp4Params {
   Nvfp4Seg seg[AQ_MAX_FAMILIES];
@@ -45,11 +43,12 @@ struct Nvfp4Params {
   int64_t M, ldx;
   int32_t nseg, in;
   int32_t cols;        // in / 16
-  int32_t mode;        // scales: 0 linear, rows on 4 bytes; 1 linear; 2 128x4
   int32_t wide;        // codes move in 16-byte pieces (8 otherwise)
-  int32_t groups, clusters, S, R_shift;
+  int32_t tiles, clusters, S;
+  int32_t round;       // tiles of a round: the cluster's sums of a round meet together
+  int32_t whole;       // a warp takes whole tiles
+  int32_t tokens;      // of a launch row: up to 8 NT
   int32_t slice;       // chunks of a CTA's K slice
-  int32_t share;       // outputs of a group that one CTA of the cluster finishes
 };
 
 __device__ __forceinline__ void mma_f16(float (&d)[4], const uint32_t (&a)[4], uint32_t b0, uint32_t b1) {
@@ -58,19 +57,31 @@ __device__ __forceinline__ void mma_f16(float (&d)[4], const uint32_t (&a)[4], u
                : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3])
                : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
 }
-// Two E2M1 codes (byte i of w, the low nibble first) as halves.
-template <int I>
-__device__ __forceinline__ uint32_t f16x2_from_e2m1x2(uint32_t w) {
-  uint32_t r;
-  asm("{\n\t.reg .b8 b0, b1, b2, b3;\n\tmov.b32 {b0, b1, b2, b3}, %1;\n\tcvt.rn.f16x2.e2m1x2 %0, b0;\n\t}"
-      : "=r"(r)
-      : "r"(w >> (8 * I)));
-  return r;
+// The same onto nothing.
+__device__ __forceinline__ void mma_f16_first(float (&d)[4], const uint32_t (&a)[4], uint32_t b0, uint32_t b1) {
+  asm volatile("mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0, %1, %2, %3}, {%4, %5, %6, %7}, {%8, %9}, {%10, %10, %10, %10};"
+               : "=f"(d[0]), "=f"(d[1]), "=f"(d[2]), "=f"(d[3])
+               : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1), "f"(0.0f));
+}
+// Eight E2M1 codes, the low nibbles first, as four pairs of halves. All four bytes in one statement: each conversion then picks its
+// byte itself (3.2 clocks a warp and SM; with a shift for each 4.5, by masks and shifts 5.5).
+__device__ __forceinline__ void f16_from_e2m1x8(uint32_t w, uint32_t (&h)[4]) {
+  asm("{\n\t.reg .b8 b0, b1, b2, b3;\n\tmov.b32 {b0, b1, b2, b3}, %4;\n\tcvt.rn.f16x2.e2m1x2 %0, b0;\n\tcvt.rn.f16x2.e2m1x2 %1, b1;\n\t"
+      "cvt.rn.f16x2.e2m1x2 %2, b2;\n\tcvt.rn.f16x2.e2m1x2 %3, b3;\n\t}"
+      : "=r"(h[0]), "=r"(h[1]), "=r"(h[2]), "=r"(h[3])
+      : "r"(w));
 }
 __device__ __forceinline__ uint32_t hmul2(uint32_t a, uint32_t b) {
   uint32_t r;
   asm("mul.rn.f16x2 %0, %1, %2;" : "=r"(r) : "r"(a), "r"(b));
   return r;
+}
+__device__ __forceinline__ void cp_async_16(uint32_t dst, const void* src) {
+  asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(dst), "l"(src) : "memory");
+}
+template <int BYTES>
+__device__ __forceinline__ void cp_async_small(uint32_t dst, const void* src) {
+  asm volatile("cp.async.ca.shared.global [%0], [%1], %2;" ::"r"(dst), "l"(src), "n"(BYTES) : "memory");
 }
 template <int BYTES>
 __device__ __forceinline__ void cp_async_small(uint32_t dst, const void* src, int bytes) {
@@ -81,9 +92,14 @@ __device__ __forceinline__ uint4 lds128(uint32_t a) {
   asm volatile("ld.shared.v4.u32 {%0, %1, %2, %3}, [%4];" : "=r"(r.x), "=r"(r.y), "=r"(r.z), "=r"(r.w) : "r"(a));
   return r;
 }
-__device__ __forceinline__ uint32_t lds_u8(uint32_t a) {
+__device__ __forceinline__ uint32_t lds32(uint32_t a) {
   uint32_t r;
-  asm volatile("ld.shared.u8 %0, [%1];" : "=r"(r) : "r"(a));
+  asm volatile("ld.shared.u32 %0, [%1];" : "=r"(r) : "r"(a));
+  return r;
+}
+__device__ __forceinline__ float2 lds64f(uint32_t a) {
+  float2 r;
+  asm volatile("ld.shared.v2.f32 {%0, %1}, [%2];" : "=f"(r.x), "=f"(r.y) : "r"(a));
   return r;
 }
 template <int N>
@@ -91,282 +107,369 @@ __device__ __forceinline__ void cp_async_wait() {
   asm volatile("cp.async.wait_group %0;" ::"n"(N) : "memory");
 }
 
-// The segment and first row of a group of R row tiles.
-__device__ __forceinline__ int group_seg(const Nvfp4Params& p, int group) {
+__device__ __forceinline__ const Nvfp4Seg& tile_seg(const Nvfp4Params& p, int tile) {
   int s = 0;
-  if (p.nseg > 1 && group >= p.seg[1].begin) s = 1;
-  if (p.nseg > 2 && group >= p.seg[2].begin) s = 2;
-  return s;
+  if (p.nseg > 1 && tile >= p.seg[1].begin) s = 1;
+  if (p.nseg > 2 && tile >= p.seg[2].begin) s = 2;
+  return p.seg[s];
 }
 
-// Where a warp's next chunk comes from.
-struct Feed {
-  const uint8_t *qa, *qb;   // this lane's 16 bytes of rows g and g + 8, chunk 0
-  const uint8_t* q0;        // any readable byte of the codes
-  const uint8_t *s0, *s1;   // its word (or two) of the scales, chunk 0
-  const uint8_t* sb;        // any readable byte of the scales
-  int na, nb;               // code bytes of the rows from this lane's on (0: no such row)
-  int64_t left0, left1;     // bytes of scales from s0, s1 on that may be read
-};
-
-template <int NT>
-__global__ void __launch_bounds__(kQThreads, NT <= 2 ? 2 : 1) aq_nvfp4_kernel(const __grid_constant__ Nvfp4Params p) {
+// NW warps a CTA; DEPTH: ring stages of a warp, one chunk each; MODE of the scales: 0 linear, rows on 8 bytes; 1 linear, anywhere;
+// 2 128x4.
+template <int NT, int DEPTH, int NW, int MODE>
+__global__ void __launch_bounds__(32 * NW, 16 / NW) aq_nvfp4_kernel(const __grid_constant__ Nvfp4Params p) {
   extern __shared__ __align__(1024) uint8_t smem[];
-  const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5, g = lane >> 2, t = lane & 3;
+  const int tid = threadIdx.x, lane = tid & 31, warp = __shfl_sync(0xffffffffu, tid >> 5, 0), g = lane >> 2, t = lane & 3;
   const int S = p.S;
   const int rank = S > 1 ? static_cast<int>(cluster_ctarank()) : 0;
   const int cluster = static_cast<int>(blockIdx.x) / S;
   if (S > 1) asm volatile("barrier.cluster.arrive.relaxed.aligned;" ::: "memory");
-  const int R = 1 << p.R_shift, ksplit = kQWarps >> p.R_shift;
-  const int tile = warp & (R - 1), kpart = warp >> p.R_shift;
-  const int rounds = (p.groups - cluster + p.clusters - 1) / p.clusters;
-  const int c_first = rank * p.slice;
-  const int chunks = (p.in + kQChunk - 1) / kQChunk;
-  const int nc = max(0, min(p.slice, chunks - c_first));
-  const int64_t m0 = static_cast<int64_t>(blockIdx.y) * (8 * NT);
-  const int M = static_cast<int>(min(p.M - m0, static_cast<int64_t>(8 * NT)));
+  const int t_first = static_cast<int>(static_cast<int64_t>(p.tiles) * cluster / p.clusters);
+  const int t_last = static_cast<int>(static_cast<int64_t>(p.tiles) * (cluster + 1) / p.clusters);
+  const int rounds = (t_last - t_first + p.round - 1) / p.round;
+  const int c_first = rank * p.slice, c_whole = p.in / kQChunk;   // chunks before c_whole lie within K
+  const int nc = max(0, min(p.slice, (p.in + kQChunk - 1) / kQChunk - c_first));
+  const int64_t m0 = static_cast<int64_t>(blockIdx.y) * p.tokens;
+  const int M = static_cast<int>(min(p.M - m0, static_cast<int64_t>(p.tokens)));
 
-  uint32_t* top = reinterpret_cast<uint32_t*>(smem);
-  float* back = reinterpret_cast<float*>(smem + kQHead / 2);
-  float* part = reinterpret_cast<float*>(smem + kQHead);
-  constexpr int kPartWarp = 8 * NT * kQPart, kPartBuf = kQWarps * kPartWarp;
-  float* recv = part + 2 * kPartBuf;
-  const int recv_buf = S > 1 ? S * p.share : 0;
-  const uint32_t ring = smem_u32(recv + 2 * recv_buf) + warp * (kQDepth * kQStage);
-  const uint32_t xs = smem_u32(recv + 2 * recv_buf) + kQWarps * kQDepth * kQStage;
+  constexpr int kPart = 8 * NT * kQPart, kQThreads = 32 * NW;
+  float* part = reinterpret_cast<float*>(smem);                           // [round + NW][8 NT][kQPart], unless whole
+  const int recv_tiles = (p.round + S - 1) / S;                           // tiles that one CTA of the cluster finishes
+  const int recv_src = recv_tiles * 16 * p.tokens, recv_buf = S > 1 ? S * recv_src : 0;
+  float* recv = part + (p.whole ? 0 : (p.round + NW) * kPart);       // [2 or 1][S][recv_tiles][tokens][16]
+  float* back = recv + (p.clusters * p.round >= p.tiles ? 1 : 2) * recv_buf;   // [slice][8 NT]
+  const uint32_t ring = smem_u32(back + p.slice * 8 * NT) + warp * (DEPTH * kQStage);
+  const uint32_t xs = smem_u32(back + p.slice * 8 * NT) + NW * DEPTH * kQStage;
+
+  // A warp's run in a round, in chunks of the round's tiles laid end to end.
+  auto run = [&](int round, int& first, int& count) {
+    const int n = min(p.round, t_last - t_first - round * p.round);
+    const int lo = p.whole ? ((n * warp) / NW) * nc : (n * nc * warp) / NW;
+    first = lo;
+    count = (p.whole ? ((n * (warp + 1)) / NW) * nc : (n * nc * (warp + 1)) / NW) - lo;
+  };
 
   // ---- the weights' stream ----
-  Feed f;
-  int f_round = 0, f_c = 0;
-  auto enter = [&](int round) {   // the first chunk of a round
-    f_round = round;
-    f_c = ksplit > 1 ? (kpart + round) & (ksplit - 1) : 0;   // so that no part keeps the longer share
-    if (round >= rounds) return;
-    const int group = cluster + round * p.clusters;
-    const Nvfp4Seg& sg = p.seg[group_seg(p, group)];
-    const int row0 = ((group - sg.begin) * R + tile) * 16;
-    const int ra = row0 + g, rb = ra + 8;
-    f.q0 = sg.q;
-    f.na = ra < sg.out ? p.in / 2 - 16 * t : 0;
-    f.nb = rb < sg.out ? p.in / 2 - 16 * t : 0;
-    f.qa = sg.q + static_cast<int64_t>(min(ra, sg.out - 1)) * sg.ldq + 16 * t;
-    f.qb = sg.q + static_cast<int64_t>(min(rb, sg.out - 1)) * sg.ldq + 16 * t;
-    f.sb = sg.sf;
-    if (p.mode == 1) {
-      // three aligned words a row hold its eight scales: 48 words, the second of a lane for the first sixteen
-      const int64_t total = static_cast<int64_t>(sg.out) * p.cols;
-      auto word = [&](int i, const uint8_t*& s, int64_t& left) {
-        const int row = row0 + i / 3;
-        const int64_t at = ((static_cast<int64_t>(row) * p.cols) & ~3ll) + 4 * (i % 3);
-        s = sg.sf + at;
-        left = row < sg.out ? total - at : 0;
-      };
-      word(lane, f.s0, f.left0);
-      if (lane < 16) word(32 + lane, f.s1, f.left1);
-      else f.left1 = 0;
-    } else {
-      const int row = row0 + lane / 2, half = lane & 1;
-      const int r = min(row, sg.out - 1);
-      if (p.mode == 0) {
-        f.s0 = sg.sf + static_cast<int64_t>(r) * p.cols + 4 * half;
-        f.left0 = row < sg.out ? p.cols - 4 * half : 0;
+  int f_round = -1, f_left = 0, f_tile = 0, f_c = 0;
+  const uint8_t* f_q = nullptr;   // this lane's 16 bytes of row lane / 8 of the tile, chunk f_c; the others 4, 8 and 12 rows on
+  const uint8_t* f_s = nullptr;   // its scales there
+  int64_t f_row4 = 0;
+  bool f_full = false;            // all 16 rows there, and room behind their scales
+  const int s_step = MODE == 2 ? 2048 : 16;
+  auto aim = [&] {
+    const Nvfp4Seg& sg = tile_seg(p, f_tile);
+    const int row0 = (f_tile - sg.begin) * 16, rows = min(16, sg.out - row0);
+    f_full = rows == 16 && (MODE != 1 || static_cast<int64_t>(sg.out - row0 - 16) * p.cols >= 16);
+    f_row4 = 4 * sg.ldq;
+    f_q = sg.q + static_cast<int64_t>(row0 + min(lane / 8, rows - 1)) * sg.ldq + (lane & 7) * 16 + static_cast<int64_t>(f_c) * 128;
+    if (MODE <= 1) {   // row lane / 2: half of its 16 scales, or one of the two aligned pieces that hold them
+      const int64_t at = static_cast<int64_t>(row0 + min(lane / 2, rows - 1)) * p.cols;
+      f_s = sg.sf + f_c * 16 + (MODE == 0 ? at + (lane & 1) * 8 : (at & ~15ll) + (lane & 1) * 16);
+    } else {             // 128x4: word lane & 3 (four scales: a tile of 512 bytes each) of rows lane / 4 and 8 more
+      const int r = row0 + min(lane / 4, rows - 1);
+      f_s = sg.sf + (static_cast<int64_t>(r / 128) * ((p.cols + 3) / 4) + (lane & 3)) * 512 + 16 * (r % 32) + 4 * (r % 128 / 32) + static_cast<int64_t>(f_c) * 2048;
+    }
+  };
+  auto next_run = [&] {
+    while (f_left == 0 && f_round + 1 < rounds) {
+      int first;
+      run(++f_round, first, f_left);
+      if (f_left == 0) continue;
+      f_tile = t_first + f_round * p.round + first / nc;
+      f_c = c_first + first % nc;
+      aim();
+    }
+  };
+  // Rows or bytes that are not there: zeros.
+  auto copy_some = [&](uint32_t st, uint32_t dq) {
+    const Nvfp4Seg& sg = tile_seg(p, f_tile);
+    const int rows = min(16, sg.out - (f_tile - sg.begin) * 16);
+    const int held = max(0, min(16, p.in / 2 - f_c * 128 - (lane & 7) * 16));   // bytes of the rows in this piece
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      const int z = lane / 8 + 4 * i < rows ? held : 0;
+      const uint8_t* from = z ? f_q + i * f_row4 : sg.q;
+      if (p.wide) {
+        cp_async_16_zfill(dq + i * 512, from, z);
       } else {
-        const int ktiles = (p.cols + 3) / 4;
-        f.s0 = sg.sf + (static_cast<int64_t>(r / 128) * ktiles + half) * 512 + 16 * (r % 32) + 4 * (r % 128 / 32);
-        f.left0 = row < sg.out ? 4 * (ktiles - half) : 0;   // in scales of this row: a tile of four 512 bytes on
+        cp_async_small<8>(dq + i * 512, from, min(z, 8));
+        cp_async_small<8>(dq + i * 512 + 8, z > 8 ? from + 8 : sg.q, max(z - 8, 0));
+      }
+    }
+    const uint32_t ds = st + kQCodes;
+    const int col = f_c * 16;
+    if (MODE == 0) {
+      const int z = lane / 2 < rows && col + (lane & 1) * 8 < p.cols ? 8 : 0;
+      cp_async_small<8>(ds + lane * 8, z ? f_s : sg.sf, z);
+    } else if (MODE == 1) {
+      const int64_t left = static_cast<int64_t>(sg.out) * p.cols - (f_s - sg.sf);
+      const int z = lane / 2 < rows ? static_cast<int>(max(int64_t(0), min(int64_t(16), left))) : 0;
+      cp_async_16_zfill(ds + lane * 16, z ? f_s : sg.sf, z);
+    } else {
+#pragma unroll
+      for (int i = 0; i < 2; ++i) {
+        const int z = lane / 4 + 8 * i < rows && col + (lane & 3) * 4 < p.cols ? 4 : 0;
+        cp_async_small<4>(ds + lane * 4 + 128 * i, z ? f_s + 128 * i : sg.sf, z);
       }
     }
   };
-  // One chunk into stage `slot`, or an empty group where the stream is through.
-  auto feed = [&](int slot) {
-    while (f_round < rounds && f_c >= nc) enter(f_round + 1);
-    if (f_round < rounds) {
-      const int c = c_first + f_c;
-      const uint32_t dst = ring + slot * kQStage;
-      const int off = c * 64;
-      const int za = max(0, min(16, f.na - off)), zb = max(0, min(16, f.nb - off));
-      const uint8_t* sa = za ? f.qa + off : f.q0;
-      const uint8_t* sb = zb ? f.qb + off : f.q0;
-      if (p.wide) {
-        cp_async_16_zfill(dst + lane * 16, sa, za);
-        cp_async_16_zfill(dst + 512 + lane * 16, sb, zb);
-      } else {
-        cp_async_small<8>(dst + lane * 16, sa, min(za, 8));
-        cp_async_small<8>(dst + lane * 16 + 8, za > 8 ? sa + 8 : f.q0, max(za - 8, 0));
-        cp_async_small<8>(dst + 512 + lane * 16, sb, min(zb, 8));
-        cp_async_small<8>(dst + 512 + lane * 16 + 8, zb > 8 ? sb + 8 : f.q0, max(zb - 8, 0));
-      }
-      if (p.mode == 1) {
-        const int z0 = static_cast<int>(max(0ll, min(4ll, f.left0 - 8ll * c)));
-        cp_async_small<4>(dst + kQCodes + lane * 4, z0 ? f.s0 + 8 * static_cast<int64_t>(c) : f.sb, z0);
-        if (lane < 16) {
-          const int z1 = static_cast<int>(max(0ll, min(4ll, f.left1 - 8ll * c)));
-          cp_async_small<4>(dst + kQCodes + (32 + lane) * 4, z1 ? f.s1 + 8 * static_cast<int64_t>(c) : f.sb, z1);
+  const uint32_t to_q = (lane / 8) * 128 + (((lane & 7) ^ ((lane / 8) & 1)) * 16);   // rows 4 apart keep their parity
+  auto feed = [&](uint32_t st) {
+    if (f_left > 0) {
+      const uint32_t dq = st + to_q;
+      if (f_full && f_c < c_whole) {
+        if (p.wide) {
+          cp_async_16(dq, f_q);
+          cp_async_16(dq + 512, f_q + f_row4);
+          cp_async_16(dq + 1024, f_q + 2 * f_row4);
+          cp_async_16(dq + 1536, f_q + 3 * f_row4);
+        } else {
+#pragma unroll
+          for (int i = 0; i < 4; ++i) {
+            cp_async_small<8>(dq + i * 512, f_q + i * f_row4);
+            cp_async_small<8>(dq + i * 512 + 8, f_q + i * f_row4 + 8);
+          }
+        }
+        if (MODE == 0) {
+          cp_async_small<8>(st + kQCodes + lane * 8, f_s);
+        } else if (MODE == 1) {
+          cp_async_16(st + kQCodes + lane * 16, f_s);
+        } else {
+          cp_async_small<4>(st + kQCodes + lane * 4, f_s);
+          cp_async_small<4>(st + kQCodes + lane * 4 + 128, f_s + 128);
         }
       } else {
-        const bool in = f.left0 > 8 * c;
-        const int64_t at = p.mode == 0 ? 8 * static_cast<int64_t>(c) : 1024 * static_cast<int64_t>(c);
-        cp_async_small<4>(dst + kQCodes + (lane / 2) * 12 + (lane & 1) * 4, in ? f.s0 + at : f.sb, in ? 4 : 0);
+        copy_some(st, dq);
       }
-      f_c += ksplit;
+      f_q += 128;
+      f_s += s_step;
+      ++f_c;
+      if (--f_left == 0) {
+        next_run();
+      } else if (f_c == c_first + nc) {
+        f_c = c_first;
+        ++f_tile;
+        aim();
+      }
     }
     cp_async_commit();
   };
   // Weights are not written by a kernel that is still running, so the stream starts before the previous kernel ends.
-  enter(0);
-  for (int i = 0; i < kQDepth - 1; ++i) feed(i);
+  next_run();
+  for (int i = 0; i < DEPTH - 1; ++i) feed(ring + i * kQStage);
   pdl_wait_prior_grid();
   pdl_launch_dependents();
 
-  // ---- x of this slice: f16, in the order in which the lanes read it: [chunk][step pair][token][t][8] ----
-  if (tid < 8 * NT) top[tid] = 0;
-  __syncthreads();
+  // ---- x of this slice: f16, [chunk][token][t][word of codes][8], the lanes' rows of 128 bytes 144 apart, so that what eight lanes read
+  // together lies in eight places of the banks. A warp takes a chunk of a token at a time; the CTAs start at different ones, or all would ask the same
+  // part of L2 at once ----
+  const int items = nc * M;
+  const uint32_t x_chunk = static_cast<uint32_t>(M) * kQRow;
   {
-    const int vecs = nc * 16, k_first = c_first * kQChunk;   // vectors of eight elements a token
-    const int spans = (vecs + 31) / 32, items = spans * M;   // a warp takes 32 vectors of one token at a time
-    auto dst = [&](int v, int m) {   // chunk v / 16; in it t = v % 16 / 4, step pair v % 4
-      return xs + ((((v >> 4) * 4 + (v & 3)) * M + m) * 4 + ((v >> 2) & 3)) * 16;
-    };
-#pragma unroll 4
-    for (int it = warp; it < items; it += kQWarps) {
-      const int m = it / spans, v = (it - m * spans) * 32 + lane;
-      const int k = k_first + v * 8;
-      uint4 r = make_uint4(0, 0, 0, 0);
-      if (v < vecs && k < p.in) r = *reinterpret_cast<const uint4*>(p.x + (m0 + m) * p.ldx + k);
-      uint32_t most = 0;
-      const uint32_t w[4] = {r.x, r.y, r.z, r.w};
+    const uint32_t x_lane = xs + (lane >> 3) * 144 + (lane & 7) * 16;
+    const int turn = items ? static_cast<int>((blockIdx.x * 11u) % static_cast<uint32_t>(items)) : 0;
+    constexpr int kBatch = 8;   // loads in flight
+    for (int i0 = warp; i0 < items; i0 += kBatch * NW) {
+      uint4 r[kBatch];
+      int mc[kBatch];
 #pragma unroll
-      for (int i = 0; i < 4; ++i) {   // the largest finite magnitude
-        const uint32_t lo = w[i] & 0x7fffu, hi = (w[i] >> 16) & 0x7fffu;
-        most = max(most, max(lo < 0x7f80u ? lo : 0u, hi < 0x7f80u ? hi : 0u));
+      for (int j = 0; j < kBatch; ++j) {
+        const int i = i0 + j * NW;
+        int it = i + turn;
+        it = it >= items ? it - items : it;
+        const int m = it / nc, c = it - m * nc, k = (c_first + c) * kQChunk + lane * 8;
+        mc[j] = i < items ? (m << 16) | c : -1;
+        r[j] = make_uint4(0, 0, 0, 0);
+        if (i < items && k < p.in) r[j] = *reinterpret_cast<const uint4*>(p.x + (m0 + m) * p.ldx + k);
       }
-      most = __reduce_max_sync(0xffffffffu, most);
-      if (lane == 0) atomicMax(&top[m], most);
-      if (v < vecs) asm volatile("st.shared.v4.u32 [%0], {%1, %2, %3, %4};" ::"r"(dst(v, m)), "r"(r.x), "r"(r.y), "r"(r.z), "r"(r.w) : "memory");
-    }
-    __syncthreads();
-#pragma unroll 2
-    for (int it = warp; it < items; it += kQWarps) {
-      const int m = it / spans, v = (it - m * spans) * 32 + lane;
-      if (v >= vecs) continue;
-      const int e = static_cast<int>(top[m] >> 7) - 127;   // -127: zeros and numbers below the normal ones
-      const float up = __uint_as_float(static_cast<uint32_t>(min(15 - e, 120) + 127) << 23);
-      const uint4 r = lds128(dst(v, m));
-      const uint32_t w[4] = {r.x, r.y, r.z, r.w};
-      uint32_t h[4];
 #pragma unroll
-      for (int i = 0; i < 4; ++i) {
-        const float lo = __uint_as_float(w[i] << 16) * up, hi = __uint_as_float(w[i] & 0xffff0000u) * up;
-        asm("cvt.rn.f16x2.f32 %0, %1, %2;" : "=r"(h[i]) : "f"(hi), "f"(lo));
+      for (int j = 0; j < kBatch; ++j) {
+        if (mc[j] < 0) continue;
+        const int m = mc[j] >> 16, c = mc[j] & 0xffff;
+        const uint32_t w[4] = {r[j].x, r[j].y, r[j].z, r[j].w};
+        uint32_t most = 0;
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {   // the largest finite magnitude
+          const uint32_t lo = w[i] & 0x7fffu, hi = (w[i] >> 16) & 0x7fffu;
+          most = max(most, max(lo < 0x7f80u ? lo : 0u, hi < 0x7f80u ? hi : 0u));
+        }
+        const int e = static_cast<int>(__reduce_max_sync(0xffffffffu, most) >> 7) - 127;   // -127: zeros and numbers below the normal ones
+        const int lift = min(15 - e, 120);
+        const float up = __uint_as_float(static_cast<uint32_t>(lift + 127) << 23);
+        uint32_t h[4];
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+          const float lo = __uint_as_float(w[i] << 16) * up, hi = __uint_as_float(w[i] & 0xffff0000u) * up;
+          asm("cvt.rn.f16x2.f32 %0, %1, %2;" : "=r"(h[i]) : "f"(hi), "f"(lo));
+        }
+        asm volatile("st.shared.v4.u32 [%0], {%1, %2, %3, %4};" ::"r"(x_lane + c * x_chunk + m * kQRow), "r"(h[0]), "r"(h[1]), "r"(h[2]), "r"(h[3]) : "memory");
+        if (lane == 0) back[c * 8 * NT + m] = __uint_as_float(static_cast<uint32_t>(127 - lift) << 23);
       }
-      asm volatile("st.shared.v4.u32 [%0], {%1, %2, %3, %4};" ::"r"(dst(v, m)), "r"(h[0]), "r"(h[1]), "r"(h[2]), "r"(h[3]) : "memory");
-    }
-    if (tid < M) {
-      const int e = static_cast<int>(top[tid] >> 7) - 127;
-      back[tid] = __uint_as_float(static_cast<uint32_t>(127 - min(15 - e, 120)) << 23);
     }
     __syncthreads();
   }
 
   // ---- rounds ----
-  const int E = (16 << p.R_shift) * M;   // outputs of a group: token-major, its rows innermost
-  auto store = [&](int round, int e, float v) {
-    const int group = cluster + round * p.clusters;
-    const Nvfp4Seg& sg = p.seg[group_seg(p, group)];
-    const int m = e >> (4 + p.R_shift), row = (group - sg.begin) * (16 << p.R_shift) + (e & ((16 << p.R_shift) - 1));
+  auto put = [&](int tile, int m, int r, float v) {   // one output: row r of a tile
+    const Nvfp4Seg& sg = tile_seg(p, tile);
+    const int row = (tile - sg.begin) * 16 + r;
     if (row < sg.out) sg.y[(m0 + m) * sg.ldy + row] = f32_to_bf16_rn(v);
   };
-  auto finish = [&](int round) {   // the cluster's sums of a group: this CTA's share
+  // Tile i of a round is finished by CTA i % S of the cluster, as its tile i / S: the sums of all CTAs with a part of K in their order.
+  const int parts = (p.in + kQChunk * p.slice - 1) / (kQChunk * p.slice);
+  auto finish = [&](int round) {
     const float* from = recv + (round & 1) * recv_buf;
-    for (int i = tid; i < p.share; i += kQThreads) {
-      const int e = rank * p.share + i;
-      if (e >= E) break;
+    const int n = min(p.round, t_last - t_first - round * p.round), mine = (n - rank + S - 1) / S;
+    for (int e = tid; e < mine * 16 * M; e += kQThreads) {
+      const int i = e / (16 * M), in_tile = e - i * 16 * M;   // [token][row]
       float v = 0.0f;
-      for (int s = 0; s < S; ++s) v += from[s * p.share + i];
-      store(round, e, v);
+      for (int s = 0; s < parts; ++s) v += from[s * recv_src + i * 16 * p.tokens + in_tile];
+      put(t_first + round * p.round + i * S + rank, in_tile >> 4, in_tile & 15, v);
     }
   };
-  int slot = 0;
   uint32_t b_at[NT];
 #pragma unroll
-  for (int n = 0; n < NT; ++n) b_at[n] = xs + (min(n * 8 + g, M - 1) * 4 + t) * 16;   // columns past M repeat the last: unread
+  for (int n = 0; n < NT; ++n) b_at[n] = min(n * 8 + g, M - 1) * kQRow + t * 144;   // columns past M repeat the last: unread
+  const uint32_t at_a = g * 128 + (((2 * t) ^ (g & 1)) * 16), at_s = kQCodes + (MODE == 1 ? 32 : 16) * g + 4 * t;
+  const uint32_t back_at = smem_u32(back) + 8 * t;
+  if (S > 1) asm volatile("barrier.cluster.wait.acquire.aligned;" ::: "memory");   // the cluster's other CTAs run
+  uint32_t st = ring, st_feed = ring + (DEPTH - 1) * kQStage;
   for (int round = 0; round < rounds; ++round) {
-    const int group = cluster + round * p.clusters;
-    const Nvfp4Seg& sg = p.seg[group_seg(p, group)];
-    uint32_t sh_a = 12 * g + 2 * t, sh_b = sh_a + 96;   // this lane's two scales in a stage
-    if (p.mode == 1) {
-      const int64_t ra = static_cast<int64_t>((group - sg.begin) * R + tile) * 16 + g;
-      sh_a += static_cast<uint32_t>(ra * p.cols) & 3u;
-      sh_b += static_cast<uint32_t>((ra + 8) * p.cols) & 3u;
-    }
-    float acc[NT][4];
-#pragma unroll
-    for (int n = 0; n < NT; ++n) acc[n][0] = acc[n][1] = acc[n][2] = acc[n][3] = 0.0f;
-    for (int c = ksplit > 1 ? (kpart + round) & (ksplit - 1) : 0; c < nc; c += ksplit) {
-      cp_async_wait<kQDepth - 2>();
-      __syncwarp();
-      feed(slot == 0 ? kQDepth - 1 : slot - 1);
-      const uint32_t st = ring + slot * kQStage;
-      slot = slot == kQDepth - 1 ? 0 : slot + 1;
-      const uint4 wa = lds128(st + lane * 16), wb = lds128(st + 512 + lane * 16);
-      uint32_t ca = lds_u8(st + kQCodes + sh_a) | (lds_u8(st + kQCodes + sh_a + 1) << 8);
-      uint32_t cb = lds_u8(st + kQCodes + sh_b) | (lds_u8(st + kQCodes + sh_b + 1) << 8);
-      const int col = (c_first + c) * 8 + 2 * t;
-      if (col + 1 >= p.cols) {   // past the row's end stand the next row's scales
-        const uint32_t keep = col >= p.cols ? 0u : 0xffu;
-        ca &= keep;
-        cb &= keep;
+    const int tile0 = t_first + round * p.round;
+    int first, left;
+    run(round, first, left);
+    int tile = nc ? first / nc : 0, c = nc ? first - tile * nc : 0;
+    if (!p.whole && round > 0) __syncthreads();   // the sums of the round before have been taken
+    while (left > 0) {
+      const int here = min(left, nc - c);   // chunks of this tile
+      const Nvfp4Seg& sg = tile_seg(p, tile0 + tile);
+      const float scale = *sg.g;
+      uint32_t sa = 0, sb = 0;   // where the rows' scales stand in their pieces
+      if (MODE == 1) {
+        const uint32_t r = static_cast<uint32_t>((tile0 + tile - sg.begin) * 16 + g) * static_cast<uint32_t>(p.cols);
+        sa = r & 15u;
+        sb = (r + 8u * static_cast<uint32_t>(p.cols)) & 15u;
       }
-      const uint32_t fa = f16x2_from_e4m3x2(static_cast<uint16_t>(ca)), fb = f16x2_from_e4m3x2(static_cast<uint16_t>(cb));
-      const uint32_t pa[4] = {wa.x, wa.y, wa.z, wa.w}, pb[4] = {wb.x, wb.y, wb.z, wb.w};
-      const uint32_t xc = static_cast<uint32_t>(c * 4 * M) * 64;
+      float tot[NT][4];
 #pragma unroll
-      for (int j = 0; j < 4; ++j) {
-        const uint32_t s_a = __byte_perm(fa, fa, j < 2 ? 0x1010 : 0x3232), s_b = __byte_perm(fb, fb, j < 2 ? 0x1010 : 0x3232);
-        uint4 b[NT];
+      for (int n = 0; n < NT; ++n) tot[n][0] = tot[n][1] = tot[n][2] = tot[n][3] = 0.0f;
+      uint32_t xc = xs + c * x_chunk, bk = back_at + c * 32 * NT;
+      const int c_end = c_first + c + here;
+#pragma unroll 1
+      for (int ca = c_first + c; ca < c_end; ++ca) {
+        cp_async_wait<DEPTH - 2>();
+        __syncwarp();
+        feed(st_feed);
+        st_feed = st;
+        uint32_t sc_a, sc_b;   // four scales of rows g and g + 8
+        if (MODE == 1) {
+          const uint32_t wa = st + at_s + (sa & ~3u), wb = st + at_s + 256 + (sb & ~3u);
+          sc_a = __funnelshift_r(lds32(wa), lds32(wa + 4), (sa & 3u) * 8);
+          sc_b = __funnelshift_r(lds32(wb), lds32(wb + 4), (sb & 3u) * 8);
+        } else {
+          sc_a = lds32(st + at_s);
+          sc_b = lds32(st + at_s + 128);
+        }
+        if (ca >= c_whole) {   // past the row's end stand the next row's scales
+          const int over = ca * 16 + 4 * t + 4 - p.cols;
+          const uint32_t keep = over <= 0 ? 0xffffffffu : over >= 4 ? 0u : 0xffffffffu >> (8 * over);
+          sc_a &= keep;
+          sc_b &= keep;
+        }
+        const uint32_t fa[2] = {f16x2_from_e4m3x2(static_cast<uint16_t>(sc_a)), f16x2_from_e4m3x2(static_cast<uint16_t>(sc_a >> 16))};
+        const uint32_t fb[2] = {f16x2_from_e4m3x2(static_cast<uint16_t>(sc_b)), f16x2_from_e4m3x2(static_cast<uint16_t>(sc_b >> 16))};
+        uint32_t xb[NT];
 #pragma unroll
-        for (int n = 0; n < NT; ++n) b[n] = lds128(b_at[n] + xc + j * M * 64);
-        const uint32_t a0[4] = {hmul2(f16x2_from_e2m1x2<0>(pa[j]), s_a), hmul2(f16x2_from_e2m1x2<0>(pb[j]), s_b),
-                                hmul2(f16x2_from_e2m1x2<1>(pa[j]), s_a), hmul2(f16x2_from_e2m1x2<1>(pb[j]), s_b)};
-        const uint32_t a1[4] = {hmul2(f16x2_from_e2m1x2<2>(pa[j]), s_a), hmul2(f16x2_from_e2m1x2<2>(pb[j]), s_b),
-                                hmul2(f16x2_from_e2m1x2<3>(pa[j]), s_a), hmul2(f16x2_from_e2m1x2<3>(pb[j]), s_b)};
+        for (int n = 0; n < NT; ++n) xb[n] = xc + b_at[n];
+        float acc[NT][4], odd[4];   // one tile of tokens: two chains, so that a product does not wait for the one before
+#pragma unroll
+        for (int h = 0; h < 2; ++h) {   // sixteen bytes of codes a row: two blocks
+          const uint4 wa = lds128(st + (at_a ^ (h * 16))), wb = lds128(st + 1024 + (at_a ^ (h * 16)));
+          const uint32_t pa[4] = {wa.x, wa.y, wa.z, wa.w}, pb[4] = {wb.x, wb.y, wb.z, wb.w};
+#pragma unroll
+          for (int j = 0; j < 4; ++j) {
+            uint4 b[NT];
+#pragma unroll
+            for (int n = 0; n < NT; ++n) b[n] = lds128(xb[n] + (h * 4 + j) * 16);
+            const uint32_t s_a = __byte_perm(fa[h], 0, j < 2 ? 0x1010 : 0x3232), s_b = __byte_perm(fb[h], 0, j < 2 ? 0x1010 : 0x3232);
+            uint32_t ha[4], hb[4];
+            f16_from_e2m1x8(pa[j], ha);
+            f16_from_e2m1x8(pb[j], hb);
+            const uint32_t a0[4] = {hmul2(ha[0], s_a), hmul2(hb[0], s_b), hmul2(ha[1], s_a), hmul2(hb[1], s_b)};
+            const uint32_t a1[4] = {hmul2(ha[2], s_a), hmul2(hb[2], s_b), hmul2(ha[3], s_a), hmul2(hb[3], s_b)};
+#pragma unroll
+            for (int n = 0; n < NT; ++n) {
+              if (h == 0 && j == 0) mma_f16_first(acc[n], a0, b[n].x, b[n].y);
+              else mma_f16(acc[n], a0, b[n].x, b[n].y);
+            }
+            if (NT == 1) {
+              if (h == 0 && j == 0) mma_f16_first(odd, a1, b[0].z, b[0].w);
+              else mma_f16(odd, a1, b[0].z, b[0].w);
+            } else {
+#pragma unroll
+              for (int n = 0; n < NT; ++n) mma_f16(acc[n], a1, b[n].z, b[n].w);
+            }
+          }
+        }
 #pragma unroll
         for (int n = 0; n < NT; ++n) {
-          mma_f16(acc[n], a0, b[n].x, b[n].y);
-          mma_f16(acc[n], a1, b[n].z, b[n].w);
+          const float2 f = lds64f(bk + 32 * n);
+#pragma unroll
+          for (int i = 0; i < 4; ++i) tot[n][i] = fmaf((NT == 1 ? acc[n][i] + odd[i] : acc[n][i]) * scale, i & 1 ? f.y : f.x, tot[n][i]);
+        }
+        st = st == ring + (DEPTH - 1) * kQStage ? ring : st + kQStage;
+        xc += x_chunk;
+        bk += 32 * NT;
+      }
+      if (!p.whole) {   // the run's part of the tile: pieces of tiles and warps are told apart by their sum
+        float* mine = part + (tile + warp) * kPart;
+#pragma unroll
+        for (int n = 0; n < NT; ++n)
+#pragma unroll
+          for (int i = 0; i < 4; ++i) mine[(n * 8 + 2 * t + (i & 1)) * kQPart + g + (i >> 1) * 8] = tot[n][i];
+      } else {
+        const uint32_t to = S > 1 ? cluster_map(recv + (round & 1) * recv_buf + rank * recv_src + (tile / S) * 16 * p.tokens, tile % S) : 0;
+#pragma unroll
+        for (int n = 0; n < NT; ++n)
+#pragma unroll
+          for (int i = 0; i < 4; ++i) {
+            const int m = n * 8 + 2 * t + (i & 1), r = g + (i >> 1) * 8;
+            if (m >= M) continue;
+            if (S > 1) asm volatile("st.shared::cluster.f32 [%0], %1;" ::"r"(to + (m * 16 + r) * 4), "f"(tot[n][i]) : "memory");
+            else put(tile0 + tile, m, r, tot[n][i]);
+          }
+      }
+      left -= here;
+      c += here;
+      if (c == nc) {
+        c = 0;
+        ++tile;
+      }
+    }
+    if (!p.whole) {
+      __syncthreads();
+      const int n = min(p.round, t_last - tile0), units = n * nc;
+      for (int e = tid; e < n * 16 * M; e += kQThreads) {
+        const int m = e / (n * 16), r = e - m * (n * 16), i = r >> 4;   // token-major, the tiles' rows innermost
+        const int u0 = i * nc, u1 = u0 + nc;
+        const float* at = part + i * kPart + m * kQPart + (r & 15);
+        float v = 0.0f;
+        // from the first run that ends behind u0, on while runs begin before u1 (a run may be empty)
+        for (int w = units ? (NW * (u0 + 1) + units - 1) / units - 1 : NW; w < NW && (units * w) / NW < u1; ++w)
+          if ((units * w) / NW < (units * (w + 1)) / NW) v += at[w * kPart];
+        if (S > 1) {
+          asm volatile("st.shared::cluster.f32 [%0], %1;" ::"r"(cluster_map(recv + (round & 1) * recv_buf + rank * recv_src + (i / S) * 16 * p.tokens + m * 16 + (r & 15), i % S)), "f"(v) : "memory");
+        } else {
+          put(tile0 + i, m, r & 15, v);
         }
       }
     }
-    float* mine = part + (round & 1) * kPartBuf + warp * kPartWarp;
-#pragma unroll
-    for (int n = 0; n < NT; ++n)
-#pragma unroll
-      for (int i = 0; i < 4; ++i) mine[(n * 8 + 2 * t + (i & 1)) * kQPart + g + (i >> 1) * 8] = acc[n][i];
-    __syncthreads();
     if (S > 1) {
-      asm volatile("barrier.cluster.wait.acquire.aligned;" ::: "memory");   // every CTA runs, or the exchange of the round before is in
-      if (round > 0) finish(round - 1);
+      // Sums of a round are read behind its barrier; those of the next go to the other buffer, and the ones after that come behind
+      // the next barrier, which every CTA reaches with this reading done.
+      cluster_sync_all();
+      finish(round);
     }
-    const float scale = *sg.g;
-    const float* from = part + (round & 1) * kPartBuf;
-    for (int e = tid; e < E; e += kQThreads) {
-      const int m = e >> (4 + p.R_shift), rr = e & ((16 << p.R_shift) - 1);
-      const float* at = from + (rr >> 4) * kPartWarp + m * kQPart + (rr & 15);
-      float v = 0.0f;
-      for (int k = 0; k < ksplit; ++k) v += at[(k << p.R_shift) * kPartWarp];
-      v = (v * scale) * back[m];
-      if (S > 1) {
-        const int owner = e / p.share;
-        asm volatile("st.shared::cluster.f32 [%0], %1;" ::"r"(cluster_map(recv + (round & 1) * recv_buf + rank * p.share + (e - owner * p.share), owner)), "f"(v) : "memory");
-      } else {
-        store(round, e, v);
-      }
-    }
-    if (S > 1) asm volatile("barrier.cluster.arrive.release.aligned;" ::: "memory");
-  }
-  if (S > 1) {
-    asm volatile("barrier.cluster.wait.acquire.aligned;" ::: "memory");
-    finish(rounds - 1);
   }
 }
 
@@ -374,61 +477,106 @@ __global__ void __launch_bounds__(kQThreads, NT <= 2 ? 2 : 1) aq_nvfp4_kernel(co
 // host
 // ---------------------------------------------------------------------------------
 struct Nvfp4Plan {
-  int S = 0, R_shift = 0, groups = 0, clusters = 0, slice = 0, share = 0;
+  int S = 0, clusters = 0, slice = 0, round = 0, whole = 0, depth = 0, warps = 0;
   size_t smem = 0;
 };
 
-// The largest bytes of shared memory of a launch with NT token tiles, S CTAs a cluster and R row tiles a group.
-size_t nvfp4_smem(int NT, int M, int S, int R_shift, int slice, int* share) {
-  *share = ((16 << R_shift) * M + S - 1) / S;
-  const size_t part = 2ull * kQWarps * 8 * NT * kQPart * 4;
-  const size_t recv = S > 1 ? (2ull * S * *share * 4 + 15) / 16 * 16 : 0;
-  return kQHead + part + recv + static_cast<size_t>(kQWarps) * kQDepth * kQStage + static_cast<size_t>(slice) * kQChunk * 2 * M;
+// Shared memory of a launch, in the kernel's order.
+size_t nvfp4_smem(int NT, int M, int tok, int tiles, const Nvfp4Plan& c) {
+  const size_t part = c.whole ? 0 : static_cast<size_t>(c.round + c.warps) * 8 * NT * kQPart * 4;
+  const size_t recv = c.S > 1 ? static_cast<size_t>(c.S) * ((c.round + c.S - 1) / c.S) * 16 * tok * 4 * (c.clusters * c.round >= tiles ? 1 : 2) : 0;
+  return part + recv + static_cast<size_t>(c.slice) * 8 * NT * 4 + static_cast<size_t>(c.warps) * c.depth * kQStage +
+         static_cast<size_t>(c.slice) * kQRow * M;
 }
 
-// Cluster size and row tiles a group, by an estimate of the call's time in ns: the weights' stream, x into every CTA's shared
-// memory, and what each round and an exchange cost.
-bool plan_nvfp4(const int32_t* outs, int n, int in, int M, int NT, const ServeDev& dev, Nvfp4Plan* best) {
-  const int chunks = (in + kQChunk - 1) / kQChunk;
+// Cluster size, warps a CTA, tiles a round and how the warps share them, by an estimate of the call's time in ns: the chunks that the
+// busiest warp takes, x into every CTA's shared memory, and what a round and an exchange cost. CTAs of eight warps that leave half an SM
+// free may begin under the tail of the kernel before.
+bool plan_nvfp4(int tiles, int in, int M, int tok, const ServeDev& dev, const int (&fit)[4], Nvfp4Plan* best) {
+  const int NT = std::max(1, tok / 8), chunks = (in + kQChunk - 1) / kQChunk;
+  const size_t half = (dev.smem_optin + 1024) / 2 - 1024;
   double least = 0;
   bool found = false;
-  for (int S = 1; S <= kQMaxS && S <= chunks; S *= 2) {
-    const int slice = (chunks + S - 1) / S;
-    for (int r = 0; r <= 3; ++r) {
+  for (int i = 0, S = 1; i < 4 && S <= chunks; ++i, S *= 2)
+    for (int way = 0; way < 4; ++way) {
       Nvfp4Plan c;
       c.S = S;
-      c.R_shift = r;
-      c.slice = slice;
-      c.smem = nvfp4_smem(NT, M, S, r, slice, &c.share);
-      if (c.smem > dev.smem_optin) continue;
-      for (int i = 0; i < n; ++i) c.groups += (outs[i] + (16 << r) - 1) / (16 << r);
-      const int fit = NT <= 2 ? static_cast<int>(std::min<size_t>(2, (dev.smem_optin + 1024) / (c.smem + 1024))) : 1;
-      c.clusters = std::max(1, std::min(c.groups, dev.sms * fit / S));
-      const int rounds = (c.groups + c.clusters - 1) / c.clusters, ksplit = kQWarps >> r;
-      const int ctas = c.clusters * S, per_sm = (ctas + dev.sms - 1) / dev.sms, busy = std::min(ctas, dev.sms);
-      const double bytes = static_cast<double>(per_sm) * rounds * ((slice + ksplit - 1) / ksplit) * kQWarps * kQStage;
-      const double rate = std::min(90.0, 6600.0 / busy);   // bytes a ns of one SM
-      const double t = bytes / rate + per_sm * static_cast<double>(slice) * kQChunk * 2 * M / 40.0 + rounds * (S > 1 ? 250.0 : 120.0) + (S > 1 ? 700.0 : 0.0);
+      c.whole = way & 1;
+      c.warps = way & 2 ? 8 : 16;
+      const size_t room = c.warps == 8 ? half : dev.smem_optin;
+      c.slice = (chunks + S - 1) / S;
+      c.clusters = std::max(1, std::min(tiles, fit[i]));
+      const int each = (tiles + c.clusters - 1) / c.clusters;   // tiles of a cluster
+      int rounds = 1;
+      for (bool fits = false; !fits; ++rounds) {   // the fewest rounds and the deepest ring that fit
+        c.round = (each + rounds - 1) / rounds;
+        if (c.whole && rounds > 1) c.round = (c.round + c.warps - 1) / c.warps * c.warps;
+        for (c.depth = NT > 1 && c.warps == 8 ? 2 : 3; c.depth >= (NT > 1 ? 2 : 3) && !fits; --c.depth) fits = (c.smem = nvfp4_smem(NT, M, tok, tiles, c)) <= room;
+        ++c.depth;
+        if (fits || c.round <= (c.whole ? c.warps : 1)) break;
+      }
+      if (c.smem > room) continue;
+      rounds = (each + c.round - 1) / c.round;
+      const int ctas = c.clusters * S;
+      const double mine = c.whole ? (c.round + c.warps - 1) / c.warps * c.slice : (c.round * c.slice + c.warps - 1) / c.warps;   // chunks of a warp and round
+      const double chunk = std::max(2304.0 / std::min(60.0, 6600.0 / ctas), (NT == 1 ? 55.0 : NT == 2 ? 75.0 : 130.0) * (c.warps == 8 ? 1.3 : 1.0));
+      const double t = mine * rounds * c.warps * chunk + (c.warps == 8 ? 500.0 : 2000.0) + static_cast<double>(c.slice) * M * (c.warps == 8 ? 20.0 : 15.0) +
+                       (S > 1 ? 1000.0 * rounds + each * 64.0 * M / 20.0 : 0.0) + (c.whole ? 0.0 : 300.0 * rounds + each * 14.0 * M);
       if (!found || t < least) {
         least = t;
         *best = c;
         found = true;
       }
     }
-  }
   return found;
 }
 
-template <int NT>
+// Clusters of 1, 2, 4 and 8 CTAs, one an SM, that the device holds at once (groups of SMs that a cluster may span bound them).
+cudaError_t clusters_at_once(const ServeDev& dev, int (&fit)[4]) {
+  static std::atomic<int> known[64][4];
+  fit[0] = dev.sms;
+  for (int i = 1; i < 4; ++i) {
+    if (!(fit[i] = known[dev.index][i].load())) {
+      cudaError_t e = cudaFuncSetAttribute(aq_nvfp4_kernel<1, 3, 16, 0>, cudaFuncAttributeMaxDynamicSharedMemorySize, static_cast<int>(dev.smem_optin));
+      if (e != cudaSuccess) return e;
+      cudaLaunchConfig_t cfg = {};
+      cfg.gridDim = dim3(static_cast<unsigned>(dev.sms) & ~7u);
+      cfg.blockDim = dim3(512);
+      cfg.dynamicSmemBytes = dev.smem_optin;
+      cudaLaunchAttribute at[1] = {};
+      at[0].id = cudaLaunchAttributeClusterDimension;
+      at[0].val.clusterDim.x = 1u << i;
+      at[0].val.clusterDim.y = at[0].val.clusterDim.z = 1;
+      cfg.attrs = at;
+      cfg.numAttrs = 1;
+      int n = 0;
+      if ((e = cudaOccupancyMaxActiveClusters(&n, aq_nvfp4_kernel<1, 3, 16, 0>, &cfg)) != cudaSuccess) return e;
+      known[dev.index][i].store(fit[i] = std::max(1, n));
+    }
+  }
+  return cudaSuccess;
+}
+
+template <int NT, int DEPTH, int NW, int MODE>
 cudaError_t launch_nvfp4(const Nvfp4Params& p, dim3 grid, size_t smem, const ServeDev& dev, cudaStream_t st) {
   static std::atomic<uint64_t> ready{0};   // devices on which the kernel may use all of an SM's shared memory
   const uint64_t bit = 1ull << dev.index;
   if (!(ready.load() & bit)) {
-    const cudaError_t e = cudaFuncSetAttribute(aq_nvfp4_kernel<NT>, cudaFuncAttributeMaxDynamicSharedMemorySize, static_cast<int>(dev.smem_optin));
+    const cudaError_t e = cudaFuncSetAttribute(aq_nvfp4_kernel<NT, DEPTH, NW, MODE>, cudaFuncAttributeMaxDynamicSharedMemorySize, static_cast<int>(dev.smem_optin));
     if (e != cudaSuccess) return e;
     ready.fetch_or(bit);
   }
-  return launch_serve(aq_nvfp4_kernel<NT>, p, grid, kQThreads, smem, st, p.S);
+  return launch_serve(aq_nvfp4_kernel<NT, DEPTH, NW, MODE>, p, grid, 32 * NW, smem, st, p.S);
+}
+template <int MODE>
+cudaError_t launch_nvfp4(const Nvfp4Params& p, dim3 grid, const Nvfp4Plan& c, int tok, const ServeDev& dev, cudaStream_t st) {
+  if (tok <= 8) return c.warps == 8 ? launch_nvfp4<1, 3, 8, MODE>(p, grid, c.smem, dev, st) : launch_nvfp4<1, 3, 16, MODE>(p, grid, c.smem, dev, st);
+  if (tok == 16) {
+    if (c.warps == 8) return launch_nvfp4<2, 2, 8, MODE>(p, grid, c.smem, dev, st);
+    return c.depth == 3 ? launch_nvfp4<2, 3, 16, MODE>(p, grid, c.smem, dev, st) : launch_nvfp4<2, 2, 16, MODE>(p, grid, c.smem, dev, st);
+  }
+  if (c.warps == 8) return launch_nvfp4<4, 2, 8, MODE>(p, grid, c.smem, dev, st);
+  return c.depth == 3 ? launch_nvfp4<4, 3, 16, MODE>(p, grid, c.smem, dev, st) : launch_nvfp4<4, 2, 16, MODE>(p, grid, c.smem, dev, st);
 }
 
 }  // namespace
@@ -485,21 +633,24 @@ extern "C" aq_status aq_nvfp4_linear_multi(const aq_nvfp4_weight* w, int32_t n, 
   ServeDev dev;
   aq_status st = serve_device(&dev);
   if (st != AQ_OK) return st;
-  // Token tiles of 8, 16 or 32: the largest that the tokens fill and whose x a cluster's shared memory holds.
-  int32_t rows[AQ_MAX_FAMILIES];
-  for (int i = 0; i < n; ++i) rows[i] = w[i].out;
+  int64_t row_tiles = 0;
+  for (int i = 0; i < n; ++i) row_tiles += (w[i].out + 15) / 16;
+  if (row_tiles > 0x7fffffffLL / 16) return serve_fail(AQ_ERR_SHAPE, "%s: the weights have too many rows for one call", who);
+  int fit[4];
+  cudaError_t e = clusters_at_once(dev, fit);
+  if (e != cudaSuccess) return serve_launched(e, who);
   Nvfp4Plan plan;
-  int NT = M <= 8 ? 1 : M <= 16 ? 2 : 4;
-  for (; NT >= 1; NT /= 2)
-    if (plan_nvfp4(rows, n, in, static_cast<int>(std::min<int64_t>(M, 8 * NT)), NT, dev, &plan)) break;
-  if (NT < 1) return serve_fail(AQ_ERR_UNSUPPORTED, "%s: in=%d does not fit this device's shared memory", who, in);
-  const int64_t tiles = (M + 8 * NT - 1) / (8 * NT);
+  int tok = M <= 8 ? 8 : M <= 16 ? 16 : 32;   // tokens at once: what a cluster's shared memory holds of them
+  for (; tok >= 1; tok /= 2)
+    if (plan_nvfp4(static_cast<int>(row_tiles), in, static_cast<int>(std::min<int64_t>(M, tok)), tok, dev, fit, &plan)) break;
+  if (tok < 1) return serve_fail(AQ_ERR_UNSUPPORTED, "%s: in=%d does not fit this device's shared memory", who, in);
+  const int64_t tiles = (M + tok - 1) / tok;
   if (tiles > 65535) return serve_fail(AQ_ERR_SHAPE, "%s: M=%lld is too large", who, (long long)M);
   Nvfp4Params p = {};
   for (int i = 0, at = 0; i < n; ++i) {
     p.seg[i] = {static_cast<const uint8_t*>(w[i].q), static_cast<const uint8_t*>(w[i].sf), w[i].global_scale, static_cast<uint16_t*>(y[i]),
                 w[i].ldq, ldy[i], w[i].out, at};
-    at += (w[i].out + (16 << plan.R_shift) - 1) / (16 << plan.R_shift);
+    at += (w[i].out + 15) / 16;
   }
   p.x = static_cast<const uint16_t*>(x);
   p.M = M;
@@ -507,18 +658,18 @@ extern "C" aq_status aq_nvfp4_linear_multi(const aq_nvfp4_weight* w, int32_t n, 
   p.nseg = n;
   p.in = in;
   p.cols = static_cast<int32_t>(cols);
-  p.mode = w[0].sf_layout == AQ_SF_128X4 ? 2 : cols % 4 ? 1 : 0;
   p.wide = wide;
-  p.groups = plan.groups;
+  p.tiles = static_cast<int32_t>(row_tiles);
   p.clusters = plan.clusters;
   p.S = plan.S;
-  p.R_shift = plan.R_shift;
+  p.round = plan.round;
+  p.tokens = tok;
   p.slice = plan.slice;
-  p.share = plan.share;
+  p.whole = plan.whole;
   const dim3 grid(static_cast<unsigned>(plan.clusters) * plan.S, static_cast<unsigned>(tiles));
   const cudaStream_t cs = static_cast<cudaStream_t>(stream);
-  const cudaError_t e = NT == 1 ? launch_nvfp4<1>(p, grid, plan.smem, dev, cs) : NT == 2 ? launch_nvfp4<2>(p, grid, plan.smem, dev, cs)
-                                                                               : launch_nvfp4<4>(p, grid, plan.smem, dev, cs);
+  if (w[0].sf_layout == AQ_SF_128X4) e = launch_nvfp4<2>(p, grid, plan, tok, dev, cs);
+  else e = cols % 8 == 0 ? launch_nvfp4<0>(p, grid, plan, tok, dev, cs) : launch_nvfp4<1>(p, grid, plan, tok, dev, cs);
   return serve_launched(e, who);
 }
 

@@ -118,14 +118,12 @@ aq_status check_rope_spec(const aq_rope_spec* r, int32_t head_dim, const char* w
 namespace {
 
 // One call: up to three sets of heads over the same T tokens, walked as one list of heads:
-// [0, hq) rotated and written to qo, then hk keys rotated and stored (or written to ko), then hv values stored.
+// [0, hq) rotated and written to qo, then hk keys rotated and stored, then hk values stored.
 struct PosParams {
   const uint16_t* q;
   int64_t q_tok, q_head;
   uint16_t* qo;
   int64_t qo_tok, qo_head;
-  uint16_t* ko;           // NULL: keys and values go to the cache
-  int64_t ko_tok, ko_head;
   const uint16_t* k;
   int64_t k_tok, k_head;
   const uint16_t* v;
@@ -139,12 +137,9 @@ struct PosParams {
   float* vs;
   int64_t T;
   int64_t n_slots;
-  int32_t hq, hk, hv, D;
+  int32_t hq, hk, D;
   int32_t rot16;          // rotary_dim / 16
   float magnitude, sin_sign;
-  const uint16_t* norm_w[2];   // of q and k, before the rotation
-  float norm_eps[2], norm_offset[2];
-  int32_t norm[2];
   int32_t page_shift;
   int32_t hl_shift;       // log2 of the groups that share a token, each taking every hl-th head
 };
@@ -152,15 +147,15 @@ struct PosParams {
 // GW lanes per vector (a power of two, >= D / 16).
 // SPLIT: the groups of a warp are at one token. Four blocks an SM: a rotation of 8192 tokens takes 19.1 us, with three
 // blocks 21.7, with five 25.3; the next heads' loads under these heads' work 20.6 (three) and 23.1 (four).
-template <bool HALF, int GW, bool E4M3, bool SPLIT, bool NORM>
-__global__ void __launch_bounds__(256, NORM ? 3 : 4) aq_positions_kernel(const __grid_constant__ PosParams p) {
+template <bool HALF, int GW, bool E4M3, bool SPLIT>
+__global__ void __launch_bounds__(256, 4) aq_positions_kernel(const __grid_constant__ PosParams p) {
   pdl_wait_prior_grid();
   pdl_launch_dependents();
   const int u = threadIdx.x % GW;
   const int64_t item = static_cast<int64_t>(blockIdx.x) * (256 / GW) + threadIdx.x / GW;
   const int64_t t = item >> p.hl_shift;
   const int hl = 1 << p.hl_shift, h0 = static_cast<int>(item & (hl - 1));
-  const int heads = p.hq + p.hk + p.hv;
+  const int heads = p.hq + 2 * p.hk;
   const bool live = t < p.T && u * 16 < p.D;
   const int64_t tt = live ? t : 0;
   const Chunks<HALF> ch(u, p.rot16, p.D / 16);
@@ -169,7 +164,7 @@ __global__ void __launch_bounds__(256, NORM ? 3 : 4) aq_positions_kernel(const _
   const bool turn = p.freq != nullptr && (ch.turns0 || ch.turns1) && live && h0 < p.hq + p.hk;
   angles<HALF, GW, SPLIT>(ch, u, p.freq, p.freq && live ? p.pos[tt] : 0, p.magnitude, p.sin_sign, c, s);
   int64_t cell0 = -1;
-  if (p.hv > 0 && live) {
+  if (p.hk > 0 && live) {
     const int64_t slot = p.slots[tt];
     if (slot >= 0 && slot < p.n_slots)
       cell0 = (((slot >> p.page_shift) * p.hk) << p.page_shift) + (slot & ((1 << p.page_shift) - 1));
@@ -186,7 +181,7 @@ __global__ void __launch_bounds__(256, NORM ? 3 : 4) aq_positions_kernel(const _
   auto finish = [&](int h, const uint4& r0, const uint4& r1) {
     const bool is_v = h >= p.hq + p.hk;
     const bool turns = turn && !is_v;
-    if (!NORM && h < p.hq && !turns) {   // nothing rotates in this lane's part
+    if (h < p.hq && !turns) {   // nothing rotates in this lane's part
       uint16_t* dst = p.qo + tt * p.qo_tok + h * p.qo_head;
       if (live) *reinterpret_cast<uint4*>(dst + ch.c0 * 8) = r0;
       if (live) *reinterpret_cast<uint4*>(dst + ch.c1 * 8) = r1;
@@ -195,21 +190,9 @@ __global__ void __launch_bounds__(256, NORM ? 3 : 4) aq_positions_kernel(const _
     float a[8], b[8];
     unpack8(live ? r0 : make_uint4(0, 0, 0, 0), a);
     unpack8(live ? r1 : make_uint4(0, 0, 0, 0), b);
-    const int kind = h >= p.hq;
-    if (NORM && !is_v && p.norm[kind]) {
-      const float r = head_rstd<GW>(a, b, group, 1.0f / p.D, p.norm_eps[kind]);
-      float f0[8], f1[8];
-      norm_factor(p.norm_w[kind], k0, p.norm_offset[kind], f0);
-      norm_factor(p.norm_w[kind], k1, p.norm_offset[kind], f1);
-#pragma unroll
-      for (int i = 0; i < 8; ++i) {
-        a[i] = a[i] * r * f0[i];
-        b[i] = b[i] * r * f1[i];
-      }
-    }
     if (turns) rotate16<HALF>(a, b, c, s, ch.turns1);
-    if (h < p.hq || (NORM && p.ko)) {
-      uint16_t* dst = kind ? p.ko + tt * p.ko_tok + (h - p.hq) * p.ko_head : p.qo + tt * p.qo_tok + h * p.qo_head;
+    if (h < p.hq) {
+      uint16_t* dst = p.qo + tt * p.qo_tok + h * p.qo_head;
       if (live) *reinterpret_cast<uint4*>(dst + ch.c0 * 8) = pack8(a);
       if (live) *reinterpret_cast<uint4*>(dst + ch.c1 * 8) = pack8(b);
       return;
@@ -319,26 +302,21 @@ __global__ void __launch_bounds__(256) aq_kv_read_kernel(const __grid_constant__
   }
 }
 
-template <bool HALF, int GW, bool E4M3, bool NORM>
+template <bool HALF, int GW, bool E4M3>
 cudaError_t launch_positions(const PosParams& p, unsigned blocks, cudaStream_t st) {
   if (GW < 32 && (GW << p.hl_shift) >= 32)
-    return launch_serve(aq_positions_kernel<HALF, GW, E4M3, true, NORM>, p, blocks, 256, 0, st);
-  return launch_serve(aq_positions_kernel<HALF, GW, E4M3, false, NORM>, p, blocks, 256, 0, st);
+    return launch_serve(aq_positions_kernel<HALF, GW, E4M3, true>, p, blocks, 256, 0, st);
+  return launch_serve(aq_positions_kernel<HALF, GW, E4M3, false>, p, blocks, 256, 0, st);
 }
-template <bool HALF, bool E4M3, bool NORM>
+template <bool HALF, bool E4M3>
 cudaError_t launch_positions(const PosParams& p, unsigned blocks, int gw, cudaStream_t st) {
   switch (gw) {
-    case 1: return launch_positions<HALF, 1, E4M3, NORM>(p, blocks, st);
-    case 2: return launch_positions<HALF, 2, E4M3, NORM>(p, blocks, st);
-    case 4: return launch_positions<HALF, 4, E4M3, NORM>(p, blocks, st);
-    case 8: return launch_positions<HALF, 8, E4M3, NORM>(p, blocks, st);
-    default: return launch_positions<HALF, 16, E4M3, NORM>(p, blocks, st);
+    case 1: return launch_positions<HALF, 1, E4M3>(p, blocks, st);
+    case 2: return launch_positions<HALF, 2, E4M3>(p, blocks, st);
+    case 4: return launch_positions<HALF, 4, E4M3>(p, blocks, st);
+    case 8: return launch_positions<HALF, 8, E4M3>(p, blocks, st);
+    default: return launch_positions<HALF, 16, E4M3>(p, blocks, st);
   }
-}
-template <bool NORM>
-cudaError_t launch_positions(const PosParams& p, unsigned blocks, int gw, bool half, bool e4m3, cudaStream_t st) {
-  if (half) return e4m3 ? launch_positions<true, true, NORM>(p, blocks, gw, st) : launch_positions<true, false, NORM>(p, blocks, gw, st);
-  return e4m3 ? launch_positions<false, true, NORM>(p, blocks, gw, st) : launch_positions<false, false, NORM>(p, blocks, gw, st);
 }
 
 template <bool E4M3>
@@ -352,36 +330,21 @@ cudaError_t launch_read(const ReadParams& p, unsigned grid, int gw, cudaStream_t
   }
 }
 
-// Grid of a positions launch. The groups that share a token take neighbouring heads and each walks the rest of
-// them with its angles: as many as a warp holds, so that the angles are worked out once a warp (and 512 bytes to
-// 2 KB read in one stretch where heads are the inner dimension), more while the call does not fill half the GPU.
+// Grid of a positions launch.
 aq_status run_positions(PosParams& p, bool half, bool e4m3, cudaStream_t st, const char* who) {
   ServeDev dev;
   aq_status s = serve_device(&dev);
   if (s != AQ_OK) return s;
-  const int heads = p.hq + p.hk + p.hv;
+  const int heads = p.hq + 2 * p.hk;
   const int gw = group_width(p.D);
   const int64_t fill = static_cast<int64_t>(dev.sms) * 1024 / gw;
-  int most = 0;   // no more groups than heads, and a block's at most
-  while ((2 << most) <= heads && (2 << most) <= 256 / gw) ++most;
-  p.hl_shift = std::min(log2_of(32 / gw), most);
-  while (p.hl_shift < most && (p.T << p.hl_shift) < fill) ++p.hl_shift;
+  p.hl_shift = share_token(p.T, heads, gw, fill);
   const int64_t blocks = ((p.T << p.hl_shift) + 256 / gw - 1) / (256 / gw);
   if (blocks > 0x7fffffffLL) return serve_fail(AQ_ERR_SHAPE, "%s: %lld tokens are too many for one call", who, (long long)p.T);
   const unsigned g = static_cast<unsigned>(blocks);
-  const cudaError_t e = p.norm[0] || p.norm[1] || p.ko ? launch_positions<true>(p, g, gw, half, e4m3, st) : launch_positions<false>(p, g, gw, half, e4m3, st);
+  cudaError_t e = half ? (e4m3 ? launch_positions<true, true>(p, g, gw, st) : launch_positions<true, false>(p, g, gw, st))
+                       : (e4m3 ? launch_positions<false, true>(p, g, gw, st) : launch_positions<false, false>(p, g, gw, st));
   return serve_launched(e, who);
-}
-
-void set_norms(PosParams& p, const aq_head_norm* q, const aq_head_norm* k) {
-  const aq_head_norm* const n[2] = {q, k};
-  for (int i = 0; i < 2; ++i)
-    if (n[i]) {
-      p.norm[i] = 1;
-      p.norm_w[i] = static_cast<const uint16_t*>(n[i]->weight);
-      p.norm_eps[i] = n[i]->eps;
-      p.norm_offset[i] = n[i]->offset;
-    }
 }
 
 }  // namespace
@@ -474,77 +437,6 @@ extern "C" aq_status aq_rope(const aq_rope_spec* rope, const int32_t* pos, int64
   return run_positions(p, rope->layout == AQ_ROPE_HALF, false, static_cast<cudaStream_t>(stream), who);
 }
 
-extern "C" aq_status aq_qk_norm_rope(const aq_head_norm* q_norm, const aq_head_norm* k_norm, const aq_rope_spec* rope, const int32_t* pos,
-                                     int64_t T, int32_t head_dim, const aq_heads* q, const aq_heads* q_out, const aq_heads* k,
-                                     const aq_heads* k_out, void* stream) {
-  const char* who = "aq_qk_norm_rope";
-  if (T < 0) return serve_fail(AQ_ERR_SHAPE, "%s: T=%lld is negative", who, (long long)T);
-  if (head_dim < 16 || head_dim % 16 || head_dim > kServeMaxHeadDim)
-    return serve_fail(AQ_ERR_SHAPE, "%s: head_dim=%d must be a multiple of 16 up to %d", who, head_dim, kServeMaxHeadDim);
-  if (!q || !q_out) return serve_fail(AQ_ERR_INVALID_ARG, "%s: q and q_out must be non-NULL", who);
-  if (!k != !k_out) return serve_fail(AQ_ERR_INVALID_ARG, "%s: k and k_out go together", who);
-  if (k_norm && !k) return serve_fail(AQ_ERR_INVALID_ARG, "%s: k_norm needs k", who);
-  aq_status st;
-  if (rope && (st = check_rope_spec(rope, head_dim, who)) != AQ_OK) return st;
-  if ((st = check_head_norm(q_norm, "q_norm", who)) != AQ_OK || (st = check_head_norm(k_norm, "k_norm", who)) != AQ_OK) return st;
-  const aq_heads* const in[2] = {q, k};
-  const aq_heads* const out[2] = {q_out, k_out};
-  const int sets = k ? 2 : 1;
-  for (int i = 0; i < sets; ++i)
-    if (in[i]->heads < 1 || in[i]->heads != out[i]->heads)
-      return serve_fail(AQ_ERR_SHAPE, "%s: heads=%d and %d must be >= 1 and equal", who, in[i]->heads, out[i]->heads);
-  if (T == 0) return AQ_OK;
-  if (rope && !pos) return serve_fail(AQ_ERR_INVALID_ARG, "%s: rope needs pos", who);
-  const char* const names[2][2] = {{"q", "q_out"}, {"k", "k_out"}};
-  for (int i = 0; i < sets; ++i) {
-    if ((st = check_heads(in[i]->data, in[i]->tok, in[i]->head, in[i]->heads, head_dim, names[i][0], who)) != AQ_OK) return st;
-    if ((st = check_heads(out[i]->data, out[i]->tok, out[i]->head, out[i]->heads, head_dim, names[i][1], who)) != AQ_OK) return st;
-    if ((st = check_out_heads(out[i]->tok, out[i]->head, T, out[i]->heads, head_dim, names[i][1], who)) != AQ_OK) return st;
-  }
-  const ByteRows side[] = {ByteRows(rope ? pos : nullptr, 1, T * 4, T * 4), ByteRows(rope ? rope->freq : nullptr, 1, head_dim * 4, rope ? rope->rotary_dim * 4 : 0),
-                           ByteRows(q_norm ? q_norm->weight : nullptr, 1, head_dim * 2, head_dim * 2), ByteRows(k_norm ? k_norm->weight : nullptr, 1, head_dim * 2, head_dim * 2)};
-  for (int i = 0; i < sets; ++i) {
-    const ByteRows o = heads_rows(out[i], T, head_dim);
-    for (const ByteRows& s : side)
-      if (o.meets(s)) return serve_fail(AQ_ERR_OVERLAP, "%s: %s overlaps an input", who, names[i][1]);
-    for (int j = 0; j < sets; ++j) {
-      const bool same = i == j && in[i]->data == out[i]->data && (T == 1 || in[i]->tok == out[i]->tok) && (in[i]->heads == 1 || in[i]->head == out[i]->head);
-      if (!same && o.meets(heads_rows(in[j], T, head_dim)))
-        return serve_fail(AQ_ERR_OVERLAP, "%s: %s overlaps %s (in place needs the same pointer and strides)", who, names[i][1], names[j][0]);
-    }
-  }
-  if (sets == 2 && heads_rows(q_out, T, head_dim).meets(heads_rows(k_out, T, head_dim)))
-    return serve_fail(AQ_ERR_OVERLAP, "%s: q_out and k_out overlap", who);
-  PosParams p = {};
-  p.q = static_cast<const uint16_t*>(q->data);
-  p.q_tok = q->tok;
-  p.q_head = q->head;
-  p.qo = static_cast<uint16_t*>(q_out->data);
-  p.qo_tok = q_out->tok;
-  p.qo_head = q_out->head;
-  p.hq = q->heads;
-  if (k) {
-    p.k = static_cast<const uint16_t*>(k->data);
-    p.k_tok = k->tok;
-    p.k_head = k->head;
-    p.ko = static_cast<uint16_t*>(k_out->data);
-    p.ko_tok = k_out->tok;
-    p.ko_head = k_out->head;
-    p.hk = k->heads;
-  }
-  p.T = T;
-  p.D = head_dim;
-  set_norms(p, q_norm, k_norm);
-  if (rope) {
-    p.pos = pos;
-    p.freq = rope->freq;
-    p.rot16 = rope->rotary_dim / 16;
-    p.magnitude = rope->magnitude;
-    p.sin_sign = rope->magnitude;
-  }
-  return run_positions(p, rope && rope->layout == AQ_ROPE_HALF, false, static_cast<cudaStream_t>(stream), who);
-}
-
 extern "C" aq_status aq_kv_write(const aq_kv_cache* cache, const int64_t* slots, int64_t T, const void* k, int64_t k_tok,
                                  int64_t k_head, const void* v, int64_t v_tok, int64_t v_head, const aq_rope_spec* rope,
                                  const int32_t* pos, const void* q, int32_t q_heads, int64_t q_tok, int64_t q_head,
@@ -614,6 +506,11 @@ extern "C" aq_status aq_kv_write_norm(const aq_kv_cache* cache, const int64_t* s
     for (int j = 0; j < i; ++j)
       if (byte_overlap(outs[i], outs[j])) return serve_fail(AQ_ERR_OVERLAP, "%s: two outputs overlap", who);
   }
+  if (q_norm || k_norm) {
+    const aq_heads hq = {const_cast<void*>(q), q_tok, q_head, q ? q_heads : 0}, ho = {q_out, qo_tok, qo_head, q ? q_heads : 0},
+                   hk = {const_cast<void*>(k), k_tok, k_head, cache->kv_heads}, hv = {const_cast<void*>(v), v_tok, v_head, cache->kv_heads};
+    return run_head_norm(q_norm, k_norm, rope, pos, T, D, q ? &hq : nullptr, &ho, &hk, nullptr, &hv, cache, slots, static_cast<cudaStream_t>(stream), who);
+  }
   PosParams p = {};
   p.q = static_cast<const uint16_t*>(q);
   p.q_tok = q_tok;
@@ -636,10 +533,9 @@ extern "C" aq_status aq_kv_write_norm(const aq_kv_cache* cache, const int64_t* s
   p.T = T;
   p.n_slots = static_cast<int64_t>(cache->pages) * cache->page_size;
   p.hq = q ? q_heads : 0;
-  p.hk = p.hv = cache->kv_heads;
+  p.hk = cache->kv_heads;
   p.D = D;
   p.page_shift = log2_of(cache->page_size);
-  set_norms(p, q_norm, k_norm);
   if (rope) {
     p.freq = rope->freq;
     p.rot16 = rope->rotary_dim / 16;

@@ -105,39 +105,6 @@ __device__ __forceinline__ void angles(const Chunks<HALF>& ch, int u, const uint
   }
 }
 
-// 1 / sqrt(mean(x^2) + eps) of a head held by a group of GW lanes, 16 elements a lane (zeros past the head). Squares of numbers
-// past 2^60 could leave fp32: such a head is measured at 2^-70 of its size, where eps is nothing.
-template <int GW>
-__device__ __forceinline__ float head_rstd(const float (&a)[8], const float (&b)[8], uint32_t group, float inv_dim, float eps) {
-  auto squares = [&](float by) {
-    float s = 0.0f;
-#pragma unroll
-    for (int i = 0; i < 8; ++i) {
-      const float x = a[i] * by, y = b[i] * by;
-      s = fmaf(x, x, s);
-      s = fmaf(y, y, s);
-    }
-#pragma unroll
-    for (int o = GW / 2; o > 0; o >>= 1) s += __shfl_xor_sync(group, s, o);
-    return s;
-  };
-  const float s = squares(1.0f);
-  if (s < 0x1p120f) return rsqrtf(fmaf(s, inv_dim, eps));
-  return rsqrtf(squares(0x1p-70f) * inv_dim) * 0x1p-70f;
-}
-
-// offset + weight for a lane's chunk; ones without a weight.
-__device__ __forceinline__ void norm_factor(const uint16_t* w, int chunk, float offset, float (&f)[8]) {
-  if (w) {
-    unpack8(__ldg(reinterpret_cast<const uint4*>(w) + chunk), f);
-#pragma unroll
-    for (int i = 0; i < 8; ++i) f[i] += offset;
-  } else {
-#pragma unroll
-    for (int i = 0; i < 8; ++i) f[i] = 1.0f;
-  }
-}
-
 inline int group_width(int D) {
   int gw = 1;
   while (gw * 16 < D) gw *= 2;
@@ -146,6 +113,17 @@ inline int group_width(int D) {
 inline int log2_of(int v) {
   int s = 0;
   while ((1 << s) < v) ++s;
+  return s;
+}
+
+// log2 of the groups that share a token, taking neighbouring heads, each walking the rest of them with its angles: as many as a warp
+// holds, so that the angles are worked out once a warp (and 512 bytes to 2 KB read in one stretch where heads are the inner
+// dimension), more while the call has fewer than `fill` groups, and never more than heads or a block of 256 threads.
+inline int share_token(int64_t T, int heads, int gw, int64_t fill) {
+  int most = 0;
+  while ((2 << most) <= heads && (2 << most) <= 256 / gw) ++most;
+  int s = log2_of(32 / gw) < most ? log2_of(32 / gw) : most;
+  while (s < most && (T << s) < fill) ++s;
   return s;
 }
 
@@ -191,5 +169,10 @@ inline aq_status check_head_norm(const aq_head_norm* n, const char* name, const 
   if (!serve_aligned(n->weight, 16)) return serve_fail(AQ_ERR_ALIGNMENT, "%s: %s.weight must be 16-byte aligned", who, name);
   return AQ_OK;
 }
+
+// The head norms' launch (checked arguments): q into q_out, and k into k_out or, with the values, into the cache.
+aq_status run_head_norm(const aq_head_norm* q_norm, const aq_head_norm* k_norm, const aq_rope_spec* rope, const int32_t* pos, int64_t T,
+                        int32_t D, const aq_heads* q, const aq_heads* q_out, const aq_heads* k, const aq_heads* k_out, const aq_heads* v,
+                        const aq_kv_cache* cache, const int64_t* slots, cudaStream_t st, const char* who);
 
 }  // namespace aq

@@ -5,10 +5,13 @@
 // largest x so far, m, and s = sum 2^d, a = sum 2^d d with d = (x - m) scale log2(e): lse = m scale + ln s, H = ln s - ln2 a / s.
 // Threads, warps and the CTAs of a cluster are joined by the same rule in a fixed order.
 //
-// The most likely words: a warp keeps the best 32 of its words sorted, one a lane, as 64-bit keys (the value's order, then the
-// lower index), so equal values need no rule of their own and no order of arrival shows. A batch of words is looked at only where
-// a lane's largest beats the k-th of the list; where many do (the first batch, a rising row), the lanes' largest are sorted and
-// merged first, which raises the bar for the rest.
+// The most likely words cost the pass next to nothing: it leaves every thread's largest value, the batch of its words where that first
+// stood, and the largest of its other batches. Of each warp's 32 the j-th largest, and of the warps' the smallest, is a bar that
+// at least `top` words reach; those that do lie in the few threads whose largest does, in that batch alone unless another batch's
+// largest reaches the bar too. These words are read once more (from L2) and those that reach the bar collected as 64-bit
+// keys (the value's order, then the lower index), whose places are counted: equal values need no rule of their own, and no
+// order of arrival shows. Rows with more such words than places to collect them (one value everywhere, hardly a number above
+// -inf) go through the row again, each warp keeping the best 32 of its words sorted, one a lane.
 //
 // Bound by memory: the logits are read once (the gradient: read once, written once).
 #include <algorithm>
@@ -49,6 +52,12 @@ __device__ __forceinline__ float max_nan(float a, float b) {
   return r;
 }
 
+__device__ __forceinline__ void fadd2_rn(float& d0, float& d1, float a0, float a1, float b0, float b1) {
+  asm("{\n\t.reg .b64 ra, rb, rd;\n\tmov.b64 ra, {%2, %3};\n\tmov.b64 rb, {%4, %5};\n\tadd.rn.f32x2 rd, ra, rb;\n\tmov.b64 {%0, %1}, rd;\n\t}"
+      : "=f"(d0), "=f"(d1)
+      : "f"(a0), "f"(a1), "f"(b0), "f"(b1));
+}
+
 template <typename T>
 struct Words;   // 16 bytes of logits
 template <>
@@ -66,6 +75,14 @@ struct Words<float> {
   }
   static __device__ __forceinline__ float largest(const uint4& r) {
     return fmaxf(fmaxf(__uint_as_float(r.x), __uint_as_float(r.y)), fmaxf(__uint_as_float(r.z), __uint_as_float(r.w)));
+  }
+  static __device__ __forceinline__ float word(const uint4& r, int i) {
+    return __uint_as_float(i < 2 ? (i ? r.y : r.x) : (i == 2 ? r.z : r.w));
+  }
+  // Nothing below `to` (a NaN stays one).
+  static __device__ __forceinline__ uint4 raise(const uint4& r, float to) {
+    return make_uint4(__float_as_uint(max_nan(__uint_as_float(r.x), to)), __float_as_uint(max_nan(__uint_as_float(r.y), to)),
+                      __float_as_uint(max_nan(__uint_as_float(r.z), to)), __float_as_uint(max_nan(__uint_as_float(r.w), to)));
   }
   static __device__ __forceinline__ float one(const float* p) { return *p; }
   static __device__ __forceinline__ void put(float* p, float v) { *p = v; }
@@ -94,6 +111,19 @@ struct Words<uint16_t> {
     const uint32_t m = max2(max2(r.x, r.y), max2(r.z, r.w));
     return fmaxf(__uint_as_float(m << 16), __uint_as_float(m & 0xffff0000u));
   }
+  static __device__ __forceinline__ float word(const uint4& r, int i) {
+    const uint32_t w = i < 4 ? (i < 2 ? r.x : r.y) : (i < 6 ? r.z : r.w);
+    return __uint_as_float(i & 1 ? w & 0xffff0000u : w << 16);
+  }
+  static __device__ __forceinline__ uint4 raise(const uint4& r, float to) {
+    const uint32_t b = pack_bf16x2_cvt(to, to);
+    auto up = [&](uint32_t w) {
+      uint32_t o;
+      asm("max.NaN.bf16x2 %0, %1, %2;" : "=r"(o) : "r"(w), "r"(b));
+      return o;
+    };
+    return make_uint4(up(r.x), up(r.y), up(r.z), up(r.w));
+  }
   static __device__ __forceinline__ float one(const uint16_t* p) { return bf16_to_f32(*p); }
   static __device__ __forceinline__ void put(uint16_t* p, float v) { *p = f32_to_bf16_rn(v); }
 };
@@ -121,20 +151,35 @@ struct Row {
 
 // ---- sums ----
 struct Sums {
-  float m = -INFINITY, at = 0.0f, s = 0.0f, a = 0.0f;   // at: m, or 0 while m is -inf
+  float m = -INFINITY, at = 0.0f;   // at: m, or 0 while m is -inf
+  float s0 = 0.0f, s1 = 0.0f, a0 = 0.0f, a1 = 0.0f;
   // To a new largest value. Differences below -1000 are as good as -inf, whose product with 0 would be NaN; they are taken before
   // the scale, which could carry a mask of the type's lowest value past the range.
   __device__ __forceinline__ void rise(float to, float c) {
     at = to == -INFINITY ? 0.0f : to;
     const float d = fmaxf((m - at) * c, -1000.0f), f = ex2(d);
-    a = f * fmaf(s, d, a);
-    s *= f;
+    a0 = f * fmaf(s0, d, a0);
+    a1 = f * fmaf(s1, d, a1);
+    s0 *= f;
+    s1 *= f;
     m = to;
+  }
+  // Where words weigh nothing, and may be taken for larger ones that weigh nothing either: an infinite difference would make NaN of
+  // its weight of 0. 2^-7 of m is the least that a bf16 below m tells from it.
+  __device__ __forceinline__ float least(float c) const { return at - fmaxf(__fdividef(1000.0f, c), fabsf(at) * 0x1p-6f); }
+  // Two words, none below least().
+  __device__ __forceinline__ void add2(float x0, float x1, float c) {
+    float d0, d1;
+    fadd2_rn(d0, d1, x0, x1, -at, -at);
+    fmul2_rn(d0, d1, d0, d1, c, c);
+    const float e0 = ex2(d0), e1 = ex2(d1);
+    fadd2_rn(s0, s1, s0, s1, e0, e1);
+    ffma2_rn(a0, a1, e0, e1, d0, d1, a0, a1);
   }
   __device__ __forceinline__ void add(float x, float c) {
     const float d = max_nan((x - at) * c, -1000.0f), e = ex2(d);
-    s += e;
-    a = fmaf(e, d, a);
+    s0 += e;
+    a0 = fmaf(e, d, a0);
   }
 };
 
@@ -183,34 +228,39 @@ struct Best {
   }
 };
 
-// N words a lane, U times: x(u, i) at index at(u, i); `held(u)` whether the lane's words of that piece exist.
-template <int U, int N, typename X, typename At, typename Held>
-__device__ __forceinline__ void consider(Best& b, int k, float largest, X x, At at, Held held) {
-  const unsigned who = __ballot_sync(0xffffffffu, b.open || largest > b.bar);
+// U pieces of N words a lane, those of piece u at index at[u] and on (-1: none), `largest` of all: what reaches the bar `tau` (an order)
+// goes into the list. Later calls bring later words, so a word equal to the k-th of the list when the call begins is out.
+template <typename W, int U>
+__device__ __forceinline__ void consider(Best& b, int k, uint32_t tau, const uint4 (&raw)[U], const int (&at)[U], int words, float largest) {
+  constexpr int N = W::N;
+  const unsigned who = __ballot_sync(0xffffffffu, (b.open || largest > b.bar) && order_of(largest) >= tau);
   if (!who) return;
   Key used = 0;
-  if (__popc(who) >= 8) {
+  if (__popc(who) >= 8) {   // the lanes' best first: they raise the bar for the rest
 #pragma unroll
     for (int u = 0; u < U; ++u)
-      if (held(u))
-#pragma unroll
-        for (int i = 0; i < N; ++i) {
-          const Key y = key_of(x(u, i), at(u, i));
-          used = y > used ? y : used;
-        }
+      for (int i = 0; i < words; ++i) {
+        const Key y = at[u] < 0 ? 0 : key_of(W::word(raw[u], i), at[u] + i);
+        used = y > used ? y : used;
+      }
     b.merge(used);
     b.mark(k);
   }
 #pragma unroll
   for (int u = 0; u < U; ++u) {
-    bool any = false;
+    const float bar = b.bar;
+    const bool open = b.open;
+    uint32_t hits = 0;
 #pragma unroll
-    for (int i = 0; i < N; ++i) any = any || x(u, i) >= b.bar;
-    if (!__any_sync(0xffffffffu, held(u) && (b.open || any))) continue;
-#pragma unroll 1
     for (int i = 0; i < N; ++i) {
-      const Key y = key_of(x(u, i), at(u, i));
-      unsigned in = __ballot_sync(0xffffffffu, held(u) && y > b.kth && y != used);
+      const float x = W::word(raw[u], i);
+      hits |= (i < words && (open || x >= bar) && order_of(x) >= tau ? 1u : 0u) << i;
+    }
+    if (at[u] < 0) hits = 0;
+    for (uint32_t any = __reduce_or_sync(0xffffffffu, hits); any; any &= any - 1) {
+      const int i = __ffs(any) - 1;
+      const Key y = key_of(W::word(raw[u], i), at[u] + i);
+      unsigned in = __ballot_sync(0xffffffffu, (hits >> i & 1) && y > b.kth && y != used);
       while (in) {
         const Key z = __shfl_sync(0xffffffffu, y, __ffs(in) - 1);
         in &= in - 1;
@@ -223,24 +273,20 @@ __device__ __forceinline__ void consider(Best& b, int k, float largest, X x, At 
   }
 }
 
+constexpr int kScoreKeys = 512;   // keys of one CTA, or of the cluster's lists, that are ranked against each other
+static_assert(kScoreKeys >= kScoreMaxCluster * AQ_MAX_TOP, "the cluster's lists fit");
+
 struct ScoreShared {
+  Key keys[kScoreKeys];
+  int32_t n_keys;
   float m[kScoreMaxCluster * kScoreWarps], s[kScoreMaxCluster * kScoreWarps], a[kScoreMaxCluster * kScoreWarps];   // rank 0's
-  Key list[kScoreWarps][32];
   Key lists[kScoreMaxCluster][32];   // rank 0's
+  uint32_t bar[kScoreWarps];
   float ln_s, m_all;
 };
 
-// How many keys of a descending list of 32 are above x.
-__device__ __forceinline__ int above(const Key* list, Key x) {
-  int n = 0;
-#pragma unroll
-  for (int s = 16; s > 0; s /= 2)
-    if (list[n + s - 1] > x) n += s;
-  return n + (list[n] > x);
-}
-
 template <typename T, bool TOP>
-__global__ void __launch_bounds__(kScoreThreads, kScorePerSm) aq_scores_kernel(const __grid_constant__ ScoreParams p) {
+__global__ void __launch_bounds__(kScoreThreads, TOP ? kScorePerSm : kScorePerSm + 1) aq_scores_kernel(const __grid_constant__ ScoreParams p) {
   using W = Words<T>;
   constexpr int N = W::N, U = 4;
   __shared__ ScoreShared sh;
@@ -261,52 +307,164 @@ __global__ void __launch_bounds__(kScoreThreads, kScorePerSm) aq_scores_kernel(c
   }
 
   Sums q;
-  Best best;
-  // the words before the body, one a lane
-  if (rank == 0 && warp == 0 && w.head > 0) {
-    const bool in = lane < w.head;
-    const float x = in ? W::one(row + lane) : -INFINITY;
-    q.rise(fmaxf(x, -INFINITY), c);
-    if (in) q.add(x, c);
-    if (TOP) consider<1, 1>(best, p.top, x, [&](int, int) { return x; }, [&](int, int) { return lane; }, [&](int) { return in; });
+  // the words before and after the body, one a lane
+  const bool before = rank == 0 && warp == 0 && lane < w.head, after = rank == C - 1 && warp == 0 && lane < w.tail;
+  const int after_at = w.head + w.vecs * N + lane;
+  const float x_before = before ? W::one(row + lane) : -INFINITY, x_after = after ? W::one(row + after_at) : -INFINITY;
+  if (warp == 0) {
+    q.rise(fmaxf(x_before, fmaxf(x_after, -INFINITY)), c);
+    if (before) q.add(x_before, c);
+    if (after) q.add(x_after, c);
   }
   const T* body = row + w.head;
   const int v0 = static_cast<int>(static_cast<int64_t>(w.vecs) * rank / C), v1 = static_cast<int>(static_cast<int64_t>(w.vecs) * (rank + 1) / C);
-  for (int vw = v0 + warp * 32; vw < v1; vw += U * kScoreThreads) {   // a warp's words of a round are neighbours
+  const int vw = v0 + warp * 32;   // a warp's words of a round are neighbours
+  auto fetch = [&](uint4 (&raw)[U], int v) {
+#pragma unroll
+    for (int u = 0; u < U; ++u)
+      raw[u] = v + u * kScoreThreads < v1 ? ld_words(body + static_cast<int64_t>(v + u * kScoreThreads) * N) : make_uint4(W::kNone, W::kNone, W::kNone, W::kNone);
+  };
+  float second = -INFINITY;   // the largest of all batches but the one that holds the thread's largest
+  int best_v = -1;            // that batch's first piece
+  uint4 next[U];
+  fetch(next, vw + lane);
+#pragma unroll 1
+  for (int v = vw + lane; v - lane < v1; v += U * kScoreThreads) {   // the next words on their way under these
     uint4 raw[U];
 #pragma unroll
-    for (int u = 0; u < U; ++u) {
-      const int v = vw + lane + u * kScoreThreads;
-      raw[u] = v < v1 ? ld_words(body + static_cast<int64_t>(v) * N) : make_uint4(W::kNone, W::kNone, W::kNone, W::kNone);
-    }
+    for (int u = 0; u < U; ++u) raw[u] = next[u];
+    fetch(next, v + U * kScoreThreads);
     float top = W::largest(raw[0]);
 #pragma unroll
     for (int u = 1; u < U; ++u) top = fmaxf(top, W::largest(raw[u]));
-    q.rise(fmaxf(q.m, top), c);
-#pragma unroll
-    for (int u = 0; u < U; ++u) {
-      float x[N];
-      W::unpack(raw[u], x);
-#pragma unroll
-      for (int i = 0; i < N; ++i) q.add(x[i], c);
+    if (TOP) {
+      second = fmaxf(second, fminf(q.m, top));
+      best_v = top > q.m ? v : best_v;
     }
-    if (TOP)
-      consider<U, N>(
-          best, p.top, top,
-          [&](int u, int i) {
-            float x[N];
-            W::unpack(raw[u], x);
-            return x[i];
-          },
-          [&](int u, int i) { return w.head + (vw + lane + u * kScoreThreads) * N + i; }, [&](int u) { return vw + lane + u * kScoreThreads < v1; });
+    q.rise(fmaxf(q.m, top), c);
+    const float least = q.least(c);
+    if (least > -INFINITY) {
+#pragma unroll
+      for (int u = 0; u < U; ++u) {
+        float x[N];
+        W::unpack(W::raise(raw[u], least), x);
+#pragma unroll
+        for (int i = 0; i < N; i += 2) q.add2(x[i], x[i + 1], c);
+      }
+    } else {   // a largest word of plus infinity, or at the very bottom of the range
+#pragma unroll
+      for (int u = 0; u < U; ++u)
+#pragma unroll 1
+        for (int i = 0; i < N; ++i) q.add(W::word(raw[u], i), c);
+    }
   }
-  if (rank == C - 1 && warp == 0 && w.tail > 0) {
-    const bool in = lane < w.tail;
-    const int at = w.head + w.vecs * N + lane;
-    const float x = in ? W::one(row + at) : -INFINITY;
-    q.rise(fmaxf(q.m, x), c);
-    if (in) q.add(x, c);
-    if (TOP) consider<1, 1>(best, p.top, x, [&](int, int) { return x; }, [&](int, int) { return at; }, [&](int) { return in; });
+
+  // The CTA's list: its `top` best words, in rank 0's shared memory.
+  if (TOP) {
+    // the bar: of the warps whose lanes all have words, each has at least ceil(top / warps) threads with one that reaches it
+    const int full = min(kScoreWarps, (v1 - v0) / 32), share = full ? (p.top + full - 1) / full : 33;
+    uint32_t left = order_of(q.m), bar = 0;
+    for (int i = 0; i < share && share <= 32; ++i) {
+      bar = __reduce_max_sync(0xffffffffu, left);
+      if (lane == __ffs(__ballot_sync(0xffffffffu, left == bar)) - 1) left = 0;
+    }
+    if (lane == 0) sh.bar[warp] = warp < full ? bar : 0xffffffffu;
+    if (tid == 0) sh.n_keys = 0;
+    __syncthreads();
+    uint32_t tau = sh.bar[0];
+#pragma unroll
+    for (int i = 1; i < kScoreWarps; ++i) tau = min(tau, sh.bar[i]);
+    if (full == 0 || share > 32 || tau <= order_of(-INFINITY)) tau = 0;   // too few threads with a number above -inf
+    const int rounds = v1 > vw ? (v1 - vw + kScoreThreads - 1) / kScoreThreads : 0;   // pieces of a thread, at most
+    auto note = [&](float x, int at) {
+      if (order_of(x) < tau) return;
+      const int n = atomicAdd(&sh.n_keys, 1);
+      if (n < kScoreKeys) sh.keys[n] = key_of(x, at);
+    };
+    auto note_pieces = [&](const uint4 (&raw)[U], const int (&at)[U]) {
+#pragma unroll
+      for (int u = 0; u < U; ++u)
+        if (at[u] >= 0 && order_of(W::largest(raw[u])) >= tau)
+          for (int i = 0; i < N; ++i) note(W::word(raw[u], i), at[u] + i);
+    };
+    if (tau) {
+      if (before) note(x_before, lane);
+      if (after) note(x_after, after_at);
+      const bool all = order_of(second) >= tau, one = !all && best_v >= 0 && order_of(q.m) >= tau;
+      uint4 raw[U];
+      int at[U];
+      // a batch by its own thread
+      if (__any_sync(0xffffffffu, one)) {
+#pragma unroll
+        for (int u = 0; u < U; ++u) {
+          const int v = best_v + u * kScoreThreads;
+          at[u] = one && v < v1 ? w.head + v * N : -1;
+          raw[u] = at[u] >= 0 ? *reinterpret_cast<const uint4*>(body + static_cast<int64_t>(v) * N) : make_uint4(W::kNone, W::kNone, W::kNone, W::kNone);
+        }
+        note_pieces(raw, at);
+      }
+      // all of a thread's words by the warp
+      for (unsigned whole = __ballot_sync(0xffffffffu, all); whole; whole &= whole - 1) {
+        const int first = vw + __ffs(whole) - 1;
+        for (int i0 = 0; i0 < rounds; i0 += U * 32) {
+#pragma unroll
+          for (int u = 0; u < U; ++u) {
+            const int v = first + (i0 + u * 32 + lane) * kScoreThreads;
+            at[u] = i0 + u * 32 + lane < rounds && v < v1 ? w.head + v * N : -1;
+            raw[u] = at[u] >= 0 ? *reinterpret_cast<const uint4*>(body + static_cast<int64_t>(v) * N) : make_uint4(W::kNone, W::kNone, W::kNone, W::kNone);
+          }
+          note_pieces(raw, at);
+        }
+      }
+    }
+    __syncthreads();
+    int n = sh.n_keys;
+    if (!tau || n > kScoreKeys) {   // through the words again, in their order
+      Best best;
+      if (rank == 0 && warp == 0 && w.head > 0) {
+        const uint4 raw[1] = {make_uint4(sizeof(T) == 4 ? __float_as_uint(x_before) : __float_as_uint(x_before) >> 16, 0, 0, 0)};
+        const int at[1] = {before ? lane : -1};
+        consider<W, 1>(best, p.top, tau, raw, at, 1, x_before);
+      }
+      for (int v = vw + lane; v - lane < v1; v += U * kScoreThreads) {
+        uint4 raw[U];
+        int at[U];
+        fetch(raw, v);
+        float top = W::largest(raw[0]);
+#pragma unroll
+        for (int u = 0; u < U; ++u) {
+          at[u] = v + u * kScoreThreads < v1 ? w.head + (v + u * kScoreThreads) * N : -1;
+          top = fmaxf(top, W::largest(raw[u]));
+        }
+        consider<W, U>(best, p.top, tau, raw, at, N, top);
+      }
+      if (rank == C - 1 && warp == 0 && w.tail > 0) {
+        const uint4 raw[1] = {make_uint4(sizeof(T) == 4 ? __float_as_uint(x_after) : __float_as_uint(x_after) >> 16, 0, 0, 0)};
+        const int at[1] = {after ? after_at : -1};
+        consider<W, 1>(best, p.top, tau, raw, at, 1, x_after);
+      }
+      __syncthreads();
+      sh.keys[tid] = best.key;   // with zeros where a warp has fewer words
+      n = kScoreThreads;
+      __syncthreads();
+    }
+    // a key's place is the number of keys above it; the list's end is filled up with none
+    if (C > 1) asm volatile("barrier.cluster.wait.acquire.aligned;" ::: "memory");   // rank 0 runs
+    auto put = [&](int place, Key x) {
+      if (C > 1) asm volatile("st.shared::cluster.u64 [%0], %1;" ::"r"(cluster_map(&sh.lists[rank][place], 0)), "l"(x) : "memory");
+      else sh.lists[0][place] = x;
+    };
+    int held = 0;
+    for (int k = tid; k < n; k += kScoreThreads) {
+      const Key x = sh.keys[k];
+      int place = 0;
+      for (int i = 0; i < n; ++i) place += sh.keys[i] > x;
+      if (x && place < p.top) put(place, x);
+    }
+    if (n < p.top || n == kScoreThreads) {   // perhaps fewer words than places
+      for (int i = 0; i < n; ++i) held += sh.keys[i] != 0;
+      if (tid >= held && tid < p.top) put(tid, 0);
+    }
   }
 
   // the warp's sums
@@ -314,48 +472,27 @@ __global__ void __launch_bounds__(kScoreThreads, kScorePerSm) aq_scores_kernel(c
 #pragma unroll
   for (int o = 16; o > 0; o >>= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, o));
   q.rise(m, c);
+  float qs = q.s0 + q.s1, qa = q.a0 + q.a1;
 #pragma unroll
   for (int o = 16; o > 0; o >>= 1) {
-    q.s += __shfl_xor_sync(0xffffffffu, q.s, o);
-    q.a += __shfl_xor_sync(0xffffffffu, q.a, o);
+    qs += __shfl_xor_sync(0xffffffffu, qs, o);
+    qa += __shfl_xor_sync(0xffffffffu, qa, o);
   }
-  if (C > 1) asm volatile("barrier.cluster.wait.acquire.aligned;" ::: "memory");   // rank 0 runs
+  if (C > 1 && !TOP) asm volatile("barrier.cluster.wait.acquire.aligned;" ::: "memory");   // rank 0 runs
   if (lane == 0) {
     const int i = rank * kScoreWarps + warp;
     if (C > 1) {
       asm volatile("st.shared::cluster.f32 [%0], %1;" ::"r"(cluster_map(&sh.m[i], 0)), "f"(q.m) : "memory");
-      asm volatile("st.shared::cluster.f32 [%0], %1;" ::"r"(cluster_map(&sh.s[i], 0)), "f"(q.s) : "memory");
-      asm volatile("st.shared::cluster.f32 [%0], %1;" ::"r"(cluster_map(&sh.a[i], 0)), "f"(q.a) : "memory");
+      asm volatile("st.shared::cluster.f32 [%0], %1;" ::"r"(cluster_map(&sh.s[i], 0)), "f"(qs) : "memory");
+      asm volatile("st.shared::cluster.f32 [%0], %1;" ::"r"(cluster_map(&sh.a[i], 0)), "f"(qa) : "memory");
     } else {
       sh.m[i] = q.m;
-      sh.s[i] = q.s;
-      sh.a[i] = q.a;
-    }
-  }
-  if (TOP) {
-    sh.list[warp][lane] = best.key;
-    if (C == 1 && tid < 32) sh.lists[0][tid] = 0;
-  }
-  __syncthreads();
-  if (TOP) {
-    // the CTA's list: a key's place is its own in its warp's list and the number of keys above it in the others
-    int place = lane;
-#pragma unroll
-    for (int i = 0; i < kScoreWarps; ++i)
-      if (i != warp) place += above(sh.list[i], best.key);
-    if (C > 1) {
-      // its 32 places, empty ones (fewer words than places) as no word: those above the number of keys held
-      int held = 0;
-#pragma unroll
-      for (int i = 0; i < kScoreWarps; ++i) held += above(sh.list[i], 0);
-      if (best.key && place < 32) asm volatile("st.shared::cluster.u64 [%0], %1;" ::"r"(cluster_map(&sh.lists[rank][place], 0)), "l"(best.key) : "memory");
-      if (tid < 32 && tid >= held) asm volatile("st.shared::cluster.u64 [%0], %1;" ::"r"(cluster_map(&sh.lists[rank][tid], 0)), "l"(Key(0)) : "memory");
-    } else if (best.key && place < 32) {
-      sh.lists[0][place] = best.key;
+      sh.s[i] = qs;
+      sh.a[i] = qa;
     }
   }
   if (C > 1) cluster_sync_all();
-  else if (TOP) __syncthreads();
+  else __syncthreads();
   if (rank != 0) return;
   if (warp == 0) {
     // sums over the cluster, C * kScoreWarps of them
@@ -367,11 +504,11 @@ __global__ void __launch_bounds__(kScoreThreads, kScorePerSm) aq_scores_kernel(c
     for (int i = lane; i < C * kScoreWarps; i += 32) {
       Sums one;
       one.m = sh.m[i];
-      one.s = sh.s[i];
-      one.a = sh.a[i];
+      one.s0 = sh.s[i];
+      one.a0 = sh.a[i];
       one.rise(top, c);
-      s += one.s;
-      a += one.a;
+      s += one.s0;
+      a += one.a0;
     }
 #pragma unroll
     for (int o = 16; o > 0; o >>= 1) {
@@ -389,16 +526,33 @@ __global__ void __launch_bounds__(kScoreThreads, kScorePerSm) aq_scores_kernel(c
     }
   }
   if (TOP) {
+    // the row's list: of the CTAs' lists what reaches the largest of their last places (`top` words do)
+    Key floor = 0;
+    if (C > 1) {
+      if (lane < C) floor = sh.lists[lane][p.top - 1];
+#pragma unroll
+      for (int o = 8; o > 0; o >>= 1) {
+        const Key other = __shfl_xor_sync(0xffffffffu, floor, o);
+        floor = other > floor ? other : floor;
+      }
+      floor = __shfl_sync(0xffffffffu, floor, 0);
+      if (tid == 0) sh.n_keys = 0;
+      __syncthreads();
+      for (int i = tid; i < C * 32; i += kScoreThreads) {
+        const Key x = i % 32 < p.top ? sh.lists[i / 32][i % 32] : 0;
+        if (x && x >= floor) sh.keys[atomicAdd(&sh.n_keys, 1)] = x;
+      }
+    }
     __syncthreads();
     const float ln_s = sh.ln_s, m_all = sh.m_all;
     const bool none = m_all == -INFINITY && ln_s == -INFINITY;
-    for (int i = tid; i < C * 32; i += kScoreThreads) {
-      const Key x = sh.lists[i / 32][i % 32];
-      if (!x) continue;
-      int place = i % 32;
-      for (int l = 0; l < C && place < p.top; ++l)
-        if (l != i / 32) place += above(sh.lists[l], x);
-      if (place >= p.top) continue;
+    const int n = C > 1 ? sh.n_keys : p.top;
+    for (int k = tid; k < n; k += kScoreThreads) {
+      const Key x = C > 1 ? sh.keys[k] : sh.lists[0][k];
+      int place = C > 1 ? 0 : k;
+      if (C > 1)
+        for (int i = 0; i < n; ++i) place += sh.keys[i] > x;
+      if (!x || place >= p.top) continue;
       const float v = value_of(static_cast<uint32_t>(x >> 32));
       p.top_token[r * p.top + place] = static_cast<int32_t>(0xffffffffu - static_cast<uint32_t>(x));
       p.top_logprob[r * p.top + place] = none ? -INFINITY : fmaf(v - m_all, p.scale, -ln_s);
