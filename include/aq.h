@@ -599,7 +599,7 @@ aq_status aq_verify_drafts(int32_t batch, int32_t vocab, const int32_t* cu, cons
                            int32_t path_cap, int32_t* token, void* stream);
 
 /* Scores of words from rows of logits [rows, vocab] (row stride ld, aligned to their elements; type AQ_PROB_F32 or AQ_PROB_BF16,
- * vocab up to 2^30). With z = scale * logit:
+ * vocab up to 2^30). With z = scale * logit, scale between 1e-30 and 1e30:
  *   lse      [rows] log of the sum of e^z
  *   logprob  [rows] z[tokens[row]] - lse; 0 where tokens[row] (int32) lies outside the vocabulary (padding)
  *   entropy  [rows] of the distribution, in nats

@@ -16,6 +16,20 @@
 namespace aq {
 namespace {
 
+// Loads go through shared memory, each lane's own 16 bytes: they hold no registers, so many are in flight, over the ends of tokens too.
+__device__ __forceinline__ void cp_async_own(uint32_t dst, const void* src) {
+  asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(dst), "l"(src) : "memory");
+}
+template <int N>
+__device__ __forceinline__ void cp_async_wait() {
+  asm volatile("cp.async.wait_group %0;" ::"n"(N) : "memory");
+}
+__device__ __forceinline__ uint4 lds_own(uint32_t a) {
+  uint4 r;
+  asm volatile("ld.shared.v4.u32 {%0, %1, %2, %3}, [%4];" : "=r"(r.x), "=r"(r.y), "=r"(r.z), "=r"(r.w) : "r"(a) : "memory");
+  return r;
+}
+
 // Two chunks of a lane as pairs that turn against each other: (a[i], b[i]).
 template <bool HALF>
 __device__ __forceinline__ void unpack_pairs(const uint4& r0, const uint4& r1, float (&a)[8], float (&b)[8]) {
@@ -92,6 +106,9 @@ __device__ __forceinline__ float head_rstd(const float (&a)[8], const float (&b)
   return rsqrtf(group_sum<GW>(s0, group) * inv_dim) * 0x1p-70f;
 }
 
+// As share_token, but at least a warp's groups, heads or not: those without one work out their part of the angles too.
+int warp_token(int64_t T, int heads, int gw, int64_t fill) { return std::max(share_token(T, heads, gw, fill), log2_of(32 / gw)); }
+
 // offset + weight for a lane's pairs; ones without a weight.
 template <bool HALF>
 __device__ __forceinline__ void norm_factors(const uint16_t* w, int k0, int k1, float offset, float (&f)[8], float (&h)[8]) {
@@ -133,125 +150,160 @@ struct HeadNormParams {
 
 enum To { kTensor, kCacheBf16, kCacheE4m3 };
 
-template <bool HALF, int GW, To TO, bool SPLIT>
-__global__ void __launch_bounds__(256, 3) aq_head_norm_kernel(const __grid_constant__ HeadNormParams p) {
+constexpr int kHeadThreads = 256, kHeadPerSm = 2, kHeadDepth = 3;   // heads in flight of a group
+
+template <bool HALF, int GW, To TO>
+__global__ void __launch_bounds__(kHeadThreads, kHeadPerSm) aq_head_norm_kernel(const __grid_constant__ HeadNormParams p) {
+  __shared__ __align__(16) uint4 ring[kHeadDepth][2][kHeadThreads];
   pdl_wait_prior_grid();
   pdl_launch_dependents();
+  constexpr int kGroups = kHeadThreads / GW;
   const int u = threadIdx.x % GW, lane = threadIdx.x & 31;
-  const int64_t item = static_cast<int64_t>(blockIdx.x) * (256 / GW) + threadIdx.x / GW;
-  const int64_t t = item >> p.hl_shift;
-  const int hl = 1 << p.hl_shift, h0 = static_cast<int>(item & (hl - 1));
-  const bool live = t < p.T && u * 16 < p.D;
-  const int64_t tt = live ? t : 0;
   const Chunks<HALF> ch(u, p.rot16, p.D / 16);
-  float c[8], s[8];
-  angles<HALF, GW, SPLIT>(ch, u, p.freq, p.freq && live ? p.pos[tt] : 0, p.magnitude, p.magnitude, c, s);
-  const bool turn0 = p.freq && live && ch.turns0, turn1 = p.freq && live && ch.turns1;
-  int64_t cell0 = -1;
-  if (TO != kTensor && live) {
-    const int64_t slot = p.slots[tt];
-    if (slot >= 0 && slot < p.n_slots)
-      cell0 = (((slot >> p.page_shift) * p.set[1].heads) << p.page_shift) + (slot & ((1 << p.page_shift) - 1));
-  }
+  const bool mine = u * 16 < p.D;
   // groups of one warp may be at different heads, so each shuffles by itself
   const uint32_t group = (GW == 32 ? 0xffffffffu : (1u << GW) - 1) << (lane & ~(GW - 1));
-  // lanes without work load lane 0's chunks: a load under a condition would be waited for at once
-  const int k0 = live ? ch.c0 * 8 : 0, k1 = live ? ch.c1 * 8 : 0;
+  const int k0 = mine ? ch.c0 * 8 : 0, k1 = mine ? ch.c1 * 8 : 0;   // lanes without work load lane 0's chunks
   const float inv_dim = 1.0f / p.D;
+  const int hl = 1 << p.hl_shift;
+  // The groups of a token take its heads in turn, the sets' as one list; a warp's groups walk tokens together, so that angles can be
+  // passed round.
+  const int64_t items = p.T << p.hl_shift, step = static_cast<int64_t>(gridDim.x) * kGroups;
+  const int64_t start = static_cast<int64_t>(blockIdx.x) * kGroups + (threadIdx.x / 32) * (32 / GW);
+  const int h0 = static_cast<int>((start + lane / GW) & (hl - 1));   // step is a multiple of hl
+  const int n0 = p.set[0].heads, n1 = n0 + p.set[1].heads, n = n1 + (TO == kTensor ? 0 : p.set[2].heads);
 
-  auto walk = [&](const HeadSet& q, int which, int first) {
-    float f0[8], f1[8];
-    if (which < 2 && q.normed) norm_factors<HALF>(q.w, k0, k1, q.offset, f0, f1);
-    const uint16_t* x = q.x + tt * q.x_tok;
-    auto finish = [&](int h, const uint4& r0, const uint4& r1) {
-      uint4 o0 = r0, o1 = r1;
-      float a[8], b[8];
-      if (which < 2 || TO == kCacheE4m3) {
-        const uint4 none = make_uint4(0, 0, 0, 0);
-        unpack_pairs<HALF>(live ? r0 : none, live ? r1 : none, a, b);
+  int64_t f_item = h0 < n ? start + lane / GW : items;   // a group may have no head at all
+  int f_h = h0, f_slot = 0;
+  const uint32_t mine_at = smem_u32(&ring[0][0][threadIdx.x]);
+  constexpr uint32_t kSlot = 2 * kHeadThreads * 16;
+  auto fetch = [&] {
+    if (f_item < items) {
+      const int which = f_h < n0 ? 0 : TO == kTensor || f_h < n1 ? 1 : 2;
+      const HeadSet& q = p.set[which];
+      const uint16_t* x = q.x + (f_item >> p.hl_shift) * q.x_tok + (f_h - (which == 0 ? 0 : which == 1 ? n0 : n1)) * q.x_head;
+      const uint32_t to = mine_at + f_slot * kSlot;
+      cp_async_own(to, x + k0);
+      cp_async_own(to + kHeadThreads * 16, x + k1);
+      f_h += hl;
+      if (f_h >= n) {
+        f_h = h0;
+        f_item += step;
       }
-      if (which < 2) {
-        if (q.normed) {
+    }
+    f_slot = f_slot == kHeadDepth - 1 ? 0 : f_slot + 1;
+    cp_async_commit();
+  };
+#pragma unroll
+  for (int i = 0; i < kHeadDepth; ++i) fetch();
+
+  float f0[8], f1[8];   // the factors of one set
+  int held = -1;        // which
+  uint32_t at_slot = mine_at;
+  const uint32_t last_slot = mine_at + (kHeadDepth - 1) * kSlot;
+  int32_t next_pos = p.freq && start + lane / GW < items ? p.pos[(start + lane / GW) >> p.hl_shift] : 0;
+  int64_t next_slot = TO != kTensor && start + lane / GW < items ? p.slots[(start + lane / GW) >> p.hl_shift] : -1;
+  for (int64_t first = start; first < items; first += step) {
+    const int64_t item = first + lane / GW;
+    const bool there = item < items, live = there && mine;
+    const int64_t t = there ? item >> p.hl_shift : 0;
+    const int32_t pos = next_pos;
+    if (p.freq && item + step < items) next_pos = p.pos[(item + step) >> p.hl_shift];
+    float c[8], s[8];
+    angles<HALF, GW, true>(ch, u, p.freq, pos, p.magnitude, p.magnitude, c, s);
+    const bool turn0 = p.freq && live && ch.turns0, turn1 = p.freq && live && ch.turns1;
+    int64_t cell0 = -1;
+    if (TO != kTensor) {
+      const int64_t slot = next_slot;
+      if (item + step < items) next_slot = p.slots[(item + step) >> p.hl_shift];
+      if (live && slot >= 0 && slot < p.n_slots)
+        cell0 = (((slot >> p.page_shift) * p.set[1].heads) << p.page_shift) + (slot & ((1 << p.page_shift) - 1));
+    }
+    if (there) {
+#pragma unroll 1
+      for (int h = h0; h < n; h += hl) {
+        const int which = h < n0 ? 0 : TO == kTensor || h < n1 ? 1 : 2;
+        const HeadSet& q = p.set[which];
+        const int at = h - (which == 0 ? 0 : which == 1 ? n0 : n1);
+        const bool normed = which < 2 && q.normed;
+        if (normed && held != which) {
+          norm_factors<HALF>(q.w, k0, k1, q.offset, f0, f1);
+          held = which;
+        }
+        cp_async_wait<kHeadDepth - 1>();
+        float a[8], b[8];
+        {
+          const uint4 none = make_uint4(0, 0, 0, 0), r0 = lds_own(at_slot), r1 = lds_own(at_slot + kHeadThreads * 16);
+          unpack_pairs<HALF>(mine ? r0 : none, mine ? r1 : none, a, b);
+        }
+        at_slot = at_slot == last_slot ? mine_at : at_slot + kSlot;
+        fetch();   // over what has just been read
+        if (normed) {
           const float r = head_rstd<GW>(a, b, group, inv_dim, q.eps);
           scale8(a, r);
           scale8(b, r);
           scale8(a, f0);
           scale8(b, f1);
         }
-        if (turn0) turn4<0>(a, b, c, s);
-        if (turn1) turn4<4>(a, b, c, s);
-        if (TO != kCacheE4m3 || which == 0) pack_pairs<HALF>(a, b, o0, o1);
-      }
-      if (which == 0 || TO == kTensor) {
-        uint16_t* dst = q.y + tt * q.y_tok + h * q.y_head;
-        if (live) *reinterpret_cast<uint4*>(dst + k0) = o0;
-        if (live) *reinterpret_cast<uint4*>(dst + k1) = o1;
-        return;
-      }
-      const int64_t cell = cell0 + (static_cast<int64_t>(h) << p.page_shift);
-      if (TO == kCacheBf16) {
-        if (cell0 < 0) return;
-        uint16_t* dst = reinterpret_cast<uint16_t*>(p.c[which - 1]) + cell * p.D;
-        if (live) *reinterpret_cast<uint4*>(dst + k0) = o0;
-        if (live) *reinterpret_cast<uint4*>(dst + k1) = o1;
-        return;
-      }
-      // as the cache's write without norms: max|x| on the bit patterns, a NaN or infinity stays the largest
-      uint32_t top = 0;
+        if (which < 2) {
+          if (turn0) turn4<0>(a, b, c, s);
+          if (turn1) turn4<4>(a, b, c, s);
+        }
+        if (which == 0 || TO != kCacheE4m3) {
+          uint4 y0, y1;
+          pack_pairs<HALF>(a, b, y0, y1);
+          uint16_t* dst;
+          if (which == 0 || TO == kTensor) {
+            dst = q.y + t * q.y_tok + at * q.y_head;
+          } else {
+            if (cell0 < 0) continue;
+            dst = reinterpret_cast<uint16_t*>(p.c[which - 1]) + (cell0 + (static_cast<int64_t>(at) << p.page_shift)) * p.D;
+          }
+          if (live) *reinterpret_cast<uint4*>(dst + k0) = y0;
+          if (live) *reinterpret_cast<uint4*>(dst + k1) = y1;
+          continue;
+        }
+        // as the cache's write without norms: max|x| on the bit patterns, a NaN or infinity stays the largest
+        uint32_t top = 0;
 #pragma unroll
-      for (int i = 0; i < 8; ++i) top = max(top, max(__float_as_uint(a[i]) & 0x7fffffffu, __float_as_uint(b[i]) & 0x7fffffffu));
+        for (int i = 0; i < 8; ++i) top = max(top, max(__float_as_uint(a[i]) & 0x7fffffffu, __float_as_uint(b[i]) & 0x7fffffffu));
 #pragma unroll
-      for (int o = GW / 2; o > 0; o >>= 1) top = max(top, __shfl_xor_sync(group, top, o));
-      if (cell0 < 0) return;
-      const bool finite = top < 0x7f800000u;
-      const float scale = finite ? fmaxf(__uint_as_float(top) * (1.0f / kE4m3Max), kKvScaleFloor) : __uint_as_float(0x7fc00000u);
-      const float inv = finite ? __frcp_rn(scale) : 0.0f;
-      uint8_t* dst = p.c[which - 1] + cell * p.D;
-      scale8(a, inv);
-      scale8(b, inv);
-      auto two = [&](float lo, float hi) { return static_cast<uint32_t>(e4m3x2_from_f32(lo, hi)); };
-      uint2 d0, d1;
-      if (HALF) {
-        d0 = make_uint2(two(a[0], a[1]) | (two(a[2], a[3]) << 16), two(a[4], a[5]) | (two(a[6], a[7]) << 16));
-        d1 = make_uint2(two(b[0], b[1]) | (two(b[2], b[3]) << 16), two(b[4], b[5]) | (two(b[6], b[7]) << 16));
-      } else {
-        d0 = make_uint2(two(a[0], b[0]) | (two(a[1], b[1]) << 16), two(a[2], b[2]) | (two(a[3], b[3]) << 16));
-        d1 = make_uint2(two(a[4], b[4]) | (two(a[5], b[5]) << 16), two(a[6], b[6]) | (two(a[7], b[7]) << 16));
+        for (int o = GW / 2; o > 0; o >>= 1) top = max(top, __shfl_xor_sync(group, top, o));
+        if (cell0 < 0) continue;
+        const int64_t cell = cell0 + (static_cast<int64_t>(at) << p.page_shift);
+        const bool finite = top < 0x7f800000u;
+        const float scale = finite ? fmaxf(__uint_as_float(top) * (1.0f / kE4m3Max), kKvScaleFloor) : __uint_as_float(0x7fc00000u);
+        const float inv = finite ? __frcp_rn(scale) : 0.0f;
+        uint8_t* dst = p.c[which - 1] + cell * p.D;
+        scale8(a, inv);
+        scale8(b, inv);
+        auto two = [&](float lo, float hi) { return static_cast<uint32_t>(e4m3x2_from_f32(lo, hi)); };
+        uint2 d0, d1;
+        if (HALF) {
+          d0 = make_uint2(two(a[0], a[1]) | (two(a[2], a[3]) << 16), two(a[4], a[5]) | (two(a[6], a[7]) << 16));
+          d1 = make_uint2(two(b[0], b[1]) | (two(b[2], b[3]) << 16), two(b[4], b[5]) | (two(b[6], b[7]) << 16));
+        } else {
+          d0 = make_uint2(two(a[0], b[0]) | (two(a[1], b[1]) << 16), two(a[2], b[2]) | (two(a[3], b[3]) << 16));
+          d1 = make_uint2(two(a[4], b[4]) | (two(a[5], b[5]) << 16), two(a[6], b[6]) | (two(a[7], b[7]) << 16));
+        }
+        if (!finite) d0 = d1 = make_uint2(0, 0);
+        if (live) *reinterpret_cast<uint2*>(dst + k0) = d0;
+        if (live) *reinterpret_cast<uint2*>(dst + k1) = d1;
+        if (u == 0) p.sc[which - 1][cell] = scale;
       }
-      if (!finite) d0 = d1 = make_uint2(0, 0);
-      if (live) *reinterpret_cast<uint2*>(dst + k0) = d0;
-      if (live) *reinterpret_cast<uint2*>(dst + k1) = d1;
-      if (u == 0) p.sc[which - 1][cell] = scale;
-    };
-    // two heads' loads in flight
-    for (int h = first; h < q.heads; h += 2 * hl) {
-      const bool two = h + hl < q.heads;
-      const uint16_t* s0 = x + h * q.x_head;
-      const uint16_t* s1 = two ? s0 + hl * q.x_head : s0;
-      const uint4 r0 = ld_stream(s0 + k0), r1 = ld_stream(s0 + k1), r2 = ld_stream(s1 + k0), r3 = ld_stream(s1 + k1);
-      finish(h, r0, r1);
-      if (two) finish(h + hl, r2, r3);
     }
-  };
-  // the groups of a token take its heads in turn, all three sets as one list
-  walk(p.set[0], 0, h0);
-  walk(p.set[1], 1, (h0 - p.set[0].heads) & (hl - 1));
-  if (TO != kTensor) walk(p.set[2], 2, (h0 - p.set[0].heads - p.set[1].heads) & (hl - 1));
+    __syncwarp();
+  }
 }
 
-template <bool HALF, int GW, To TO>
-cudaError_t launch_head_norm(const HeadNormParams& p, unsigned blocks, cudaStream_t st) {
-  if (GW < 32 && (GW << p.hl_shift) >= 32) return launch_serve(aq_head_norm_kernel<HALF, GW, TO, true>, p, blocks, 256, 0, st);
-  return launch_serve(aq_head_norm_kernel<HALF, GW, TO, false>, p, blocks, 256, 0, st);
-}
 template <bool HALF, To TO>
 cudaError_t launch_head_norm(const HeadNormParams& p, unsigned blocks, int gw, cudaStream_t st) {
   switch (gw) {
-    case 1: return launch_head_norm<HALF, 1, TO>(p, blocks, st);
-    case 2: return launch_head_norm<HALF, 2, TO>(p, blocks, st);
-    case 4: return launch_head_norm<HALF, 4, TO>(p, blocks, st);
-    case 8: return launch_head_norm<HALF, 8, TO>(p, blocks, st);
-    default: return launch_head_norm<HALF, 16, TO>(p, blocks, st);
+    case 1: return launch_serve(aq_head_norm_kernel<HALF, 1, TO>, p, blocks, kHeadThreads, 0, st);
+    case 2: return launch_serve(aq_head_norm_kernel<HALF, 2, TO>, p, blocks, kHeadThreads, 0, st);
+    case 4: return launch_serve(aq_head_norm_kernel<HALF, 4, TO>, p, blocks, kHeadThreads, 0, st);
+    case 8: return launch_serve(aq_head_norm_kernel<HALF, 8, TO>, p, blocks, kHeadThreads, 0, st);
+    default: return launch_serve(aq_head_norm_kernel<HALF, 16, TO>, p, blocks, kHeadThreads, 0, st);
   }
 }
 template <bool HALF>
@@ -266,7 +318,7 @@ cudaError_t launch_head_norm(const HeadNormParams& p, unsigned blocks, int gw, T
 // ---------------------------------------------------------------------------------
 // gradient
 // ---------------------------------------------------------------------------------
-constexpr int kNormThreads = 256, kNormPerSm = 2;
+constexpr int kNormThreads = 256, kNormPerSm = 2, kNormDepth = 2;   // heads in flight of a group
 
 struct NormSet {
   const uint16_t* dy;
@@ -292,8 +344,9 @@ template <bool HALF, int GW>
 __global__ void __launch_bounds__(kNormThreads, kNormPerSm) aq_norm_grad_kernel(const __grid_constant__ NormGradParams p) {
   pdl_wait_prior_grid();
   pdl_launch_dependents();
-  constexpr int kGroups = kNormThreads / GW;
-  __shared__ float sums[kGroups][GW * 16 + 1];
+  constexpr int kGroups = kNormThreads / GW, kRow = GW * 16 + 1;
+  __shared__ __align__(16) uint4 ring[kNormDepth][4][kNormThreads];   // and the groups' sums in the end
+  static_assert(sizeof(ring) >= sizeof(float) * kGroups * kRow, "the sums fit");
   const int which = static_cast<int>(blockIdx.x) >= p.set[0].blocks;
   const NormSet& s = p.set[which];
   const int block = static_cast<int>(blockIdx.x) - (which ? p.set[0].blocks : 0);
@@ -309,57 +362,100 @@ __global__ void __launch_bounds__(kNormThreads, kNormPerSm) aq_norm_grad_kernel(
 #pragma unroll
   for (int i = 0; i < 8; ++i) w0[i] = w1[i] = 0.0f;
 
+  // A warp's groups walk tokens together, so that angles can be passed round.
   const int64_t items = p.T << s.hl_shift, step = static_cast<int64_t>(s.blocks) * kGroups;
-  for (int64_t item = static_cast<int64_t>(block) * kGroups + threadIdx.x / GW; item < items; item += step) {
-    const int64_t t = item >> s.hl_shift;
-    float c[8], sn[8];
-    angles<HALF, GW, false>(ch, u, p.freq, p.freq && mine ? p.pos[t] : 0, p.magnitude, -p.magnitude, c, sn);
-    const bool turn0 = p.freq && mine && ch.turns0, turn1 = p.freq && mine && ch.turns1;
-    const uint16_t* xs = s.x + t * s.x_tok;
-    const uint16_t* ys = s.dy + t * s.dy_tok;
-    uint16_t* ds = s.dx + t * s.dx_tok;
-    for (int h = static_cast<int>(item & (hl - 1)); h < s.heads; h += hl) {
-      const uint16_t* xh = xs + h * s.x_head;
-      const uint16_t* yh = ys + h * s.dy_head;
-      const uint4 r0 = ld_stream(xh + k0), r1 = ld_stream(xh + k1), r2 = ld_stream(yh + k0), r3 = ld_stream(yh + k1);
-      float a[8], b[8], ga[8], gb[8];
-      const uint4 none = make_uint4(0, 0, 0, 0);
-      unpack_pairs<HALF>(mine ? r0 : none, mine ? r1 : none, a, b);
-      unpack_pairs<HALF>(mine ? r2 : none, mine ? r3 : none, ga, gb);
-      if (turn0) turn4<0>(ga, gb, c, sn);
-      if (turn1) turn4<4>(ga, gb, c, sn);
-      const float r = head_rstd<GW>(a, b, group, inv_dim, s.eps);
-      scale8(a, r);
-      scale8(b, r);
-#pragma unroll
-      for (int i = 0; i < 8; i += 2) {
-        ffma2_rn(w0[i], w0[i + 1], ga[i], ga[i + 1], a[i], a[i + 1], w0[i], w0[i + 1]);
-        ffma2_rn(w1[i], w1[i + 1], gb[i], gb[i + 1], b[i], b[i + 1], w1[i], w1[i + 1]);
-      }
-      scale8(ga, f0);
-      scale8(gb, f1);
-      float d0 = 0.0f, d1 = 0.0f;
-      dot8(d0, d1, ga, a);
-      dot8(d0, d1, gb, b);
-      const float dot = -group_sum<GW>(d0 + d1, group) * inv_dim;
-#pragma unroll
-      for (int i = 0; i < 8; i += 2) {
-        ffma2_rn(a[i], a[i + 1], a[i], a[i + 1], dot, dot, ga[i], ga[i + 1]);
-        ffma2_rn(b[i], b[i + 1], b[i], b[i + 1], dot, dot, gb[i], gb[i + 1]);
-      }
-      scale8(a, r);
-      scale8(b, r);
-      if (mine) {
-        uint16_t* d = ds + h * s.dx_head;
-        uint4 o0, o1;
-        pack_pairs<HALF>(a, b, o0, o1);
-        *reinterpret_cast<uint4*>(d + k0) = o0;
-        *reinterpret_cast<uint4*>(d + k1) = o1;
+  const int64_t start = static_cast<int64_t>(block) * kGroups + (threadIdx.x / 32) * (32 / GW);
+  const int h0 = static_cast<int>((start + lane / GW) & (hl - 1));   // step is a multiple of hl
+  int64_t f_item = h0 < s.heads ? start + lane / GW : items;   // a group may have no head at all
+  int f_h = h0, f_slot = 0;
+  const uint32_t mine_at = smem_u32(&ring[0][0][threadIdx.x]);
+  constexpr uint32_t kPiece = kNormThreads * 16, kSlot = 4 * kPiece;
+  auto fetch = [&] {
+    if (f_item < items) {
+      const int64_t t = f_item >> s.hl_shift;
+      const uint16_t* xh = s.x + t * s.x_tok + f_h * s.x_head;
+      const uint16_t* yh = s.dy + t * s.dy_tok + f_h * s.dy_head;
+      const uint32_t to = mine_at + f_slot * kSlot;
+      cp_async_own(to, xh + k0);
+      cp_async_own(to + kPiece, xh + k1);
+      cp_async_own(to + 2 * kPiece, yh + k0);
+      cp_async_own(to + 3 * kPiece, yh + k1);
+      f_h += hl;
+      if (f_h >= s.heads) {
+        f_h = h0;
+        f_item += step;
       }
     }
+    f_slot = f_slot == kNormDepth - 1 ? 0 : f_slot + 1;
+    cp_async_commit();
+  };
+#pragma unroll
+  for (int i = 0; i < kNormDepth; ++i) fetch();
+  uint32_t at_slot = mine_at;
+  const uint32_t last_slot = mine_at + (kNormDepth - 1) * kSlot;
+  int32_t next_pos = p.freq && start + lane / GW < items ? p.pos[(start + lane / GW) >> s.hl_shift] : 0;
+  for (int64_t first = start; first < items; first += step) {
+    const int64_t item = first + lane / GW;
+    const bool there = item < items, live = there && mine;
+    const int64_t t = there ? item >> s.hl_shift : 0;
+    const int32_t pos = next_pos;
+    if (p.freq && item + step < items) next_pos = p.pos[(item + step) >> s.hl_shift];
+    float c[8], sn[8];
+    angles<HALF, GW, true>(ch, u, p.freq, pos, p.magnitude, -p.magnitude, c, sn);
+    const bool turn0 = p.freq && live && ch.turns0, turn1 = p.freq && live && ch.turns1;
+    uint16_t* ds = s.dx + t * s.dx_tok;
+    if (there) {
+#pragma unroll 1
+      for (int h = h0; h < s.heads; h += hl) {
+        float a[8], b[8], ga[8], gb[8];
+        cp_async_wait<kNormDepth - 1>();
+        {
+          const uint4 none = make_uint4(0, 0, 0, 0);
+          const uint4 r0 = lds_own(at_slot), r1 = lds_own(at_slot + kPiece), r2 = lds_own(at_slot + 2 * kPiece), r3 = lds_own(at_slot + 3 * kPiece);
+          unpack_pairs<HALF>(mine ? r0 : none, mine ? r1 : none, a, b);
+          unpack_pairs<HALF>(mine ? r2 : none, mine ? r3 : none, ga, gb);
+        }
+        at_slot = at_slot == last_slot ? mine_at : at_slot + kSlot;
+        fetch();   // over what has just been read
+        if (turn0) turn4<0>(ga, gb, c, sn);
+        if (turn1) turn4<4>(ga, gb, c, sn);
+        const float r = head_rstd<GW>(a, b, group, inv_dim, s.eps);
+        scale8(a, r);
+        scale8(b, r);
+#pragma unroll
+        for (int i = 0; i < 8; i += 2) {
+          ffma2_rn(w0[i], w0[i + 1], ga[i], ga[i + 1], a[i], a[i + 1], w0[i], w0[i + 1]);
+          ffma2_rn(w1[i], w1[i + 1], gb[i], gb[i + 1], b[i], b[i + 1], w1[i], w1[i + 1]);
+        }
+        scale8(ga, f0);
+        scale8(gb, f1);
+        float d0 = 0.0f, d1 = 0.0f;
+        dot8(d0, d1, ga, a);
+        dot8(d0, d1, gb, b);
+        const float dot = -group_sum<GW>(d0 + d1, group) * inv_dim;
+#pragma unroll
+        for (int i = 0; i < 8; i += 2) {
+          ffma2_rn(a[i], a[i + 1], a[i], a[i + 1], dot, dot, ga[i], ga[i + 1]);
+          ffma2_rn(b[i], b[i + 1], b[i], b[i + 1], dot, dot, gb[i], gb[i + 1]);
+        }
+        scale8(a, r);
+        scale8(b, r);
+        if (mine) {
+          uint16_t* d = ds + h * s.dx_head;
+          uint4 o0, o1;
+          pack_pairs<HALF>(a, b, o0, o1);
+          *reinterpret_cast<uint4*>(d + k0) = o0;
+          *reinterpret_cast<uint4*>(d + k1) = o1;
+        }
+      }
+    }
+    __syncwarp();
   }
   if (!s.part) return;
-  float* row = sums[threadIdx.x / GW];
+  cp_async_wait<0>();
+  __syncthreads();
+  float* sums = reinterpret_cast<float*>(ring);
+  float* row = sums + threadIdx.x / GW * kRow;
   if (mine) {
 #pragma unroll
     for (int i = 0; i < 8; ++i) {   // pair i: elements i of either chunk, or 2 i and 2 i + 1
@@ -370,7 +466,7 @@ __global__ void __launch_bounds__(kNormThreads, kNormPerSm) aq_norm_grad_kernel(
   __syncthreads();
   for (int d = threadIdx.x; d < p.D; d += kNormThreads) {
     float v = 0.0f;
-    for (int i = 0; i < kGroups; ++i) v += sums[i][d];
+    for (int i = 0; i < kGroups; ++i) v += sums[i * kRow + d];
     s.part[static_cast<int64_t>(block) * p.D + d] = v;
   }
 }
@@ -403,18 +499,23 @@ __global__ void __launch_bounds__(1024) aq_norm_join_kernel(const __grid_constan
   if ((threadIdx.x & 31) == 0 && at < p.D) p.dw[which][at] = v;
 }
 
-// Blocks of the two sets: what fills the GPU, shared out by their heads; no more than their groups of work.
+// Blocks of the two sets: what fills the GPU, shared out by their work (a token's angles weigh as much as a head, and every
+// group works them out); no more than their groups of work.
 void norm_blocks(int64_t T, int32_t D, int32_t hq, int32_t hk, int sms, int32_t* hl_shift, int32_t* blocks) {
   const int gw = group_width(D), groups = kNormThreads / gw, heads[2] = {hq, hk};
   const int fill = sms * kNormPerSm;
+  int64_t work[2] = {0, 0};
   for (int i = 0; i < 2; ++i) {
-    hl_shift[i] = 0;
-    blocks[i] = 0;
+    hl_shift[i] = blocks[i] = 0;
     if (!heads[i]) continue;
-    hl_shift[i] = share_token(T, heads[i], gw, static_cast<int64_t>(fill) * groups / 2);
+    hl_shift[i] = warp_token(T, heads[i], gw, static_cast<int64_t>(fill) * groups / 2);
+    const int hl = 1 << hl_shift[i];
+    work[i] = static_cast<int64_t>(hl) * (1 + (heads[i] + hl - 1) / hl);
+  }
+  for (int i = 0; i < 2; ++i) {
+    if (!heads[i]) continue;
     const int64_t need = ((T << hl_shift[i]) + groups - 1) / groups;
-    const int64_t share = std::max<int64_t>(1, static_cast<int64_t>(fill) * heads[i] / (hq + hk));
-    blocks[i] = static_cast<int32_t>(std::min(need, share));
+    blocks[i] = static_cast<int32_t>(std::min(need, std::max<int64_t>(1, fill * work[i] / (work[0] + work[1]))));
   }
 }
 constexpr int kNormSmsBound = 256;   // SMs that the workspace's size allows for
@@ -482,9 +583,9 @@ aq_status run_head_norm(const aq_head_norm* q_norm, const aq_head_norm* k_norm, 
   p.T = T;
   p.D = D;
   const int gw = group_width(D);
-  p.hl_shift = share_token(T, heads, gw, static_cast<int64_t>(dev.sms) * 768 / gw);
-  const int64_t blocks = ((T << p.hl_shift) + 256 / gw - 1) / (256 / gw);
-  if (blocks > 0x7fffffffLL) return serve_fail(AQ_ERR_SHAPE, "%s: %lld tokens are too many for one call", who, (long long)T);
+  p.hl_shift = warp_token(T, heads, gw, static_cast<int64_t>(dev.sms) * (kHeadPerSm * kHeadThreads) / gw);
+  // blocks that are resident at once, each walking over tokens
+  const int64_t blocks = std::min<int64_t>(((T << p.hl_shift) + kHeadThreads / gw - 1) / (kHeadThreads / gw), static_cast<int64_t>(dev.sms) * kHeadPerSm);
   const To to = !cache ? kTensor : cache->type == AQ_KV_BF16 ? kCacheBf16 : kCacheE4m3;
   const unsigned g = static_cast<unsigned>(blocks);
   return serve_launched(rope && rope->layout == AQ_ROPE_HALF ? launch_head_norm<true>(p, g, gw, to, st) : launch_head_norm<false>(p, g, gw, to, st), who);

@@ -15,6 +15,7 @@
 #include <ATen/core/LegacyTypeDispatch.h>
 #include <ATen/ops/empty.h>
 #include <ATen/ops/empty_like.h>
+#include <c10/core/TensorImpl.h>
 #include <c10/cuda/CUDACachingAllocator.h>
 #include <c10/cuda/CUDAFunctions.h>
 #include <c10/cuda/CUDAGuard.h>
@@ -331,9 +332,31 @@ bool on_gpu(const Device& dev) {
   return false;
 }
 
-at::Tensor like(const Tensor& x) { return at::empty_like(*x.t); }
+// A new tensor on the given one's device, from the current stream's memory: what at::empty does there, without the way through the
+// dispatcher (0.5 us where at::empty takes 1.4).
 at::Tensor fresh(at::IntArrayRef shape, at::ScalarType dtype, const Tensor& on) {
-  return at::empty(shape, at::TensorOptions().dtype(dtype).device(on.t->device()));
+  if (!on.t->is_cuda()) return at::empty(shape, at::TensorOptions().dtype(dtype).device(on.t->device()));
+  int64_t bytes = static_cast<int64_t>(c10::elementSize(dtype));
+  for (const int64_t n : shape) bytes *= n;
+  c10::Allocator* const memory = c10::cuda::CUDACachingAllocator::get();
+  at::Tensor t = at::detail::make_tensor<c10::TensorImpl>(
+      c10::Storage(c10::Storage::use_byte_size_t(), static_cast<size_t>(bytes), memory->allocate(static_cast<size_t>(bytes)), memory, true),
+      c10::DispatchKeySet(c10::DispatchKey::CUDA), c10::scalarTypeToTypeMeta(dtype));
+  t.unsafeGetTensorImpl()->set_sizes_contiguous(shape);
+  return t;
+}
+// A part of a contiguous tensor's storage, elements of the same size from `first` on.
+at::Tensor part(const at::Tensor& of, int64_t first, at::IntArrayRef shape, at::ScalarType dtype) {
+  at::Tensor t = at::detail::make_tensor<c10::TensorImpl>(c10::Storage(of.storage()), c10::DispatchKeySet(c10::DispatchKey::CUDA), c10::scalarTypeToTypeMeta(dtype));
+  t.unsafeGetTensorImpl()->set_storage_offset(first);
+  t.unsafeGetTensorImpl()->set_sizes_contiguous(shape);
+  return t;
+}
+// As at::empty_like: the same order of strides.
+at::Tensor like(const Tensor& x) {
+  bool falling = true;
+  for (int i = 1; i < x.nd; ++i) falling = falling && x.t->stride(i - 1) >= x.t->stride(i);
+  return falling && x.t->is_cuda() ? fresh(x.t->sizes(), x.t->scalar_type(), x) : at::empty_like(*x.t);
 }
 PyObject* given(PyObject* obj) {
   Py_INCREF(obj);
@@ -795,14 +818,15 @@ PyObject* py_scores(PyObject*, PyObject* const* a, Py_ssize_t n) {
   if (!on_gpu(dev)) return nullptr;
   at::AutoDispatchBelowADInplaceOrView plain;
   const int64_t rows = x.shape[0];
+  // one allocation: [rows] three times (twice without tokens), then [rows, top] twice
   at::Tensor made[5];
   const bool scored = a[1] != Py_None;
-  if (scored) made[0] = fresh({rows}, kF32, x);
-  made[1] = fresh({rows}, kF32, x);
-  made[2] = fresh({rows}, kF32, x);
-  if (top) {
-    made[3] = fresh({rows, top}, kF32, x);
-    made[4] = fresh({rows, top}, kI32, x);
+  const int64_t words = rows * ((scored ? 3 : 2) + 2 * static_cast<int64_t>(top));
+  const at::Tensor all = fresh({words}, kF32, x);
+  int64_t first = 0;
+  for (int i = scored ? 0 : 1; i < (top ? 5 : 3); ++i) {
+    made[i] = i < 3 ? part(all, first, {rows}, kF32) : part(all, first, {rows, top}, i == 3 ? kF32 : kI32);
+    first += i < 3 ? rows : rows * top;
   }
   auto f32 = [&](int i) { return made[i].defined() ? static_cast<float*>(made[i].data_ptr()) : nullptr; };
   if (!ok(f_scores(x.ptr, x.stride[0], rows, small(x.shape[1]), x.t->scalar_type() == kF32 ? AQ_PROB_F32 : AQ_PROB_BF16, static_cast<const int32_t*>(tokens.ptr), scale,

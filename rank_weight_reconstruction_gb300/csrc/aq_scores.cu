@@ -2,7 +2,7 @@
 // the log of the normaliser and the most likely words.
 //
 // With z = scale x over a row: lse = log sum e^z, log p(v) = z_v - lse, H = lse - sum p z. One pass holds, for each thread, the
-// largest x so far, m, and s = sum 2^d, a = sum 2^d d with d = (x - m) scale log2(e): lse = m scale + ln s, H = ln s - ln2 a / s.
+// largest x so far, m, and s = sum 2^d, a = sum 2^d d with d = (x - m) scale log2(e): log p(v) = ln2 d_v - ln s, H = ln s - ln2 a / s.
 // Threads, warps and the CTAs of a cluster are joined by the same rule in a fixed order.
 //
 // The most likely words cost the pass next to nothing: it leaves every thread's largest value, the batch of its words where that first
@@ -73,8 +73,13 @@ struct Words<float> {
   static __device__ __forceinline__ uint4 pack(const float (&x)[4]) {
     return make_uint4(__float_as_uint(x[0]), __float_as_uint(x[1]), __float_as_uint(x[2]), __float_as_uint(x[3]));
   }
-  static __device__ __forceinline__ float largest(const uint4& r) {
-    return fmaxf(fmaxf(__uint_as_float(r.x), __uint_as_float(r.y)), fmaxf(__uint_as_float(r.z), __uint_as_float(r.w)));
+  template <int U>
+  static __device__ __forceinline__ float largest(const uint4 (&r)[U]) {
+    float m = -INFINITY;
+#pragma unroll
+    for (int u = 0; u < U; ++u)
+      m = fmaxf(m, fmaxf(fmaxf(__uint_as_float(r[u].x), __uint_as_float(r[u].y)), fmaxf(__uint_as_float(r[u].z), __uint_as_float(r[u].w))));
+    return m;
   }
   static __device__ __forceinline__ float word(const uint4& r, int i) {
     return __uint_as_float(i < 2 ? (i ? r.y : r.x) : (i == 2 ? r.z : r.w));
@@ -107,9 +112,12 @@ struct Words<uint16_t> {
     asm("max.bf16x2 %0, %1, %2;" : "=r"(r) : "r"(a), "r"(b));
     return r;
   }
-  static __device__ __forceinline__ float largest(const uint4& r) {
-    const uint32_t m = max2(max2(r.x, r.y), max2(r.z, r.w));
-    return fmaxf(__uint_as_float(m << 16), __uint_as_float(m & 0xffff0000u));
+  template <int U>
+  static __device__ __forceinline__ float largest(const uint4 (&r)[U]) {
+    uint32_t m = max2(max2(r[0].x, r[0].y), max2(r[0].z, r[0].w));
+#pragma unroll
+    for (int u = 1; u < U; ++u) m = max2(m, max2(max2(r[u].x, r[u].y), max2(r[u].z, r[u].w)));
+    return fmaxf(fmaxf(__uint_as_float(m << 16), __uint_as_float(m & 0xffff0000u)), -INFINITY);   // NaN only where nothing else is
   }
   static __device__ __forceinline__ float word(const uint4& r, int i) {
     const uint32_t w = i < 4 ? (i < 2 ? r.x : r.y) : (i < 6 ? r.z : r.w);
@@ -150,37 +158,45 @@ struct Row {
 };
 
 // ---- sums ----
+// Weights are 2^(x c - ref), c = scale log2(e), with ref the rounded m c, so that a word costs one fused product and ref's rounding
+// cancels where log probabilities are taken. Where m c leaves the range (a row of nothing but a type's lowest value) they are
+// 2^((x - m) c).
 struct Sums {
-  float m = -INFINITY, at = 0.0f;   // at: m, or 0 while m is -inf
+  float m = -INFINITY, ref = 0.0f;   // ref: 0 while m is -inf
   float s0 = 0.0f, s1 = 0.0f, a0 = 0.0f, a1 = 0.0f;
-  // To a new largest value. Differences below -1000 are as good as -inf, whose product with 0 would be NaN; they are taken before
-  // the scale, which could carry a mask of the type's lowest value past the range.
+  __device__ __forceinline__ bool wild() const { return !(fabsf(ref) < 1e37f); }
+  // To a new largest value. Differences below -1000 are as good as -inf, whose product with 0 would be NaN.
   __device__ __forceinline__ void rise(float to, float c) {
-    at = to == -INFINITY ? 0.0f : to;
-    const float d = fmaxf((m - at) * c, -1000.0f), f = ex2(d);
+    const float was = m, from = ref;
+    m = to;
+    ref = to == -INFINITY ? 0.0f : to * c;
+    const float d = was == -INFINITY ? -1000.0f : fmaxf(wild() ? (was - to) * c : from - ref, -1000.0f), f = ex2(d);
     a0 = f * fmaf(s0, d, a0);
     a1 = f * fmaf(s1, d, a1);
     s0 *= f;
     s1 *= f;
-    m = to;
   }
   // Where words weigh nothing, and may be taken for larger ones that weigh nothing either: an infinite difference would make NaN of
   // its weight of 0. 2^-7 of m is the least that a bf16 below m tells from it.
-  __device__ __forceinline__ float least(float c) const { return at - fmaxf(__fdividef(1000.0f, c), fabsf(at) * 0x1p-6f); }
-  // Two words, none below least().
+  __device__ __forceinline__ float least(float c) const {
+    const float at = m == -INFINITY ? 0.0f : m;
+    return fmaxf(at - fmaxf(__fdividef(1000.0f, c), fabsf(at) * 0x1p-6f), -3.4028235e38f);
+  }
+  // Two words, none below least(), of a row that is not wild.
   __device__ __forceinline__ void add2(float x0, float x1, float c) {
     float d0, d1;
-    fadd2_rn(d0, d1, x0, x1, -at, -at);
-    fmul2_rn(d0, d1, d0, d1, c, c);
+    ffma2_rn(d0, d1, x0, x1, c, c, -ref, -ref);
     const float e0 = ex2(d0), e1 = ex2(d1);
     fadd2_rn(s0, s1, s0, s1, e0, e1);
     ffma2_rn(a0, a1, e0, e1, d0, d1, a0, a1);
   }
   __device__ __forceinline__ void add(float x, float c) {
-    const float d = max_nan((x - at) * c, -1000.0f), e = ex2(d);
+    const float d = max_nan(distance(x, c), -1000.0f), e = ex2(d);
     s0 += e;
     a0 = fmaf(e, d, a0);
   }
+  // log2 of a word's weight.
+  __device__ __forceinline__ float distance(float x, float c) const { return wild() ? (x - m) * c : fmaf(x, c, -ref); }
 };
 
 // ---- the most likely words ----
@@ -278,12 +294,35 @@ static_assert(kScoreKeys >= kScoreMaxCluster * AQ_MAX_TOP, "the cluster's lists 
 
 struct ScoreShared {
   Key keys[kScoreKeys];
-  int32_t n_keys;
-  float m[kScoreMaxCluster * kScoreWarps], s[kScoreMaxCluster * kScoreWarps], a[kScoreMaxCluster * kScoreWarps];   // rank 0's
   Key lists[kScoreMaxCluster][32];   // rank 0's
+  float cta_m[kScoreMaxCluster], cta_s[kScoreMaxCluster], cta_a[kScoreMaxCluster];   // rank 0's
+  float m[kScoreWarps], s[kScoreWarps], a[kScoreWarps];
   uint32_t bar[kScoreWarps];
-  float ln_s, m_all;
+  int32_t n_keys;
 };
+
+// The sums of n parts (n <= N, a power of two up to 32), every lane of a warp the same, in a fixed order: s0 and a0 of the result hold them.
+template <int N>
+__device__ __forceinline__ Sums join(const float* m, const float* s, const float* a, int n, float c) {
+  const int i = threadIdx.x & (N - 1);
+  Sums one;
+  if (i < n) {
+    one.m = m[i];
+    one.ref = one.m == -INFINITY ? 0.0f : one.m * c;
+    one.s0 = s[i];
+    one.a0 = a[i];
+  }
+  float top = one.m;
+#pragma unroll
+  for (int o = N / 2; o > 0; o >>= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, o));
+  one.rise(top, c);
+#pragma unroll
+  for (int o = N / 2; o > 0; o >>= 1) {
+    one.s0 += __shfl_xor_sync(0xffffffffu, one.s0, o);
+    one.a0 += __shfl_xor_sync(0xffffffffu, one.a0, o);
+  }
+  return one;
+}
 
 template <typename T, bool TOP>
 __global__ void __launch_bounds__(kScoreThreads, TOP ? kScorePerSm : kScorePerSm + 1) aq_scores_kernel(const __grid_constant__ ScoreParams p) {
@@ -319,31 +358,31 @@ __global__ void __launch_bounds__(kScoreThreads, TOP ? kScorePerSm : kScorePerSm
   const T* body = row + w.head;
   const int v0 = static_cast<int>(static_cast<int64_t>(w.vecs) * rank / C), v1 = static_cast<int>(static_cast<int64_t>(w.vecs) * (rank + 1) / C);
   const int vw = v0 + warp * 32;   // a warp's words of a round are neighbours
-  auto fetch = [&](uint4 (&raw)[U], int v) {
+  // A batch of the warp's words: U pieces of 16 bytes a lane, b batches from its first.
+  constexpr int kStep = U * kScoreThreads;
+  const int batches = v1 > vw ? (v1 - vw + kStep - 1) / kStep : 0;
+  auto fetch = [&](uint4 (&raw)[U], int b) {
+    const int v = vw + lane + b * kStep;
+    if (v - lane + 32 + (U - 1) * kScoreThreads <= v1) {
 #pragma unroll
-    for (int u = 0; u < U; ++u)
-      raw[u] = v + u * kScoreThreads < v1 ? ld_words(body + static_cast<int64_t>(v + u * kScoreThreads) * N) : make_uint4(W::kNone, W::kNone, W::kNone, W::kNone);
+      for (int u = 0; u < U; ++u) raw[u] = ld_words(body + static_cast<int64_t>(v + u * kScoreThreads) * N);
+    } else {
+#pragma unroll
+      for (int u = 0; u < U; ++u)
+        raw[u] = v + u * kScoreThreads < v1 ? ld_words(body + static_cast<int64_t>(v + u * kScoreThreads) * N) : make_uint4(W::kNone, W::kNone, W::kNone, W::kNone);
+    }
   };
   float second = -INFINITY;   // the largest of all batches but the one that holds the thread's largest
   int best_v = -1;            // that batch's first piece
-  uint4 next[U];
-  fetch(next, vw + lane);
-#pragma unroll 1
-  for (int v = vw + lane; v - lane < v1; v += U * kScoreThreads) {   // the next words on their way under these
-    uint4 raw[U];
-#pragma unroll
-    for (int u = 0; u < U; ++u) raw[u] = next[u];
-    fetch(next, v + U * kScoreThreads);
-    float top = W::largest(raw[0]);
-#pragma unroll
-    for (int u = 1; u < U; ++u) top = fmaxf(top, W::largest(raw[u]));
+  auto take = [&](const uint4 (&raw)[U], int v) {
+    const float top = W::largest(raw);
     if (TOP) {
       second = fmaxf(second, fminf(q.m, top));
       best_v = top > q.m ? v : best_v;
     }
     q.rise(fmaxf(q.m, top), c);
-    const float least = q.least(c);
-    if (least > -INFINITY) {
+    if (!q.wild()) {
+      const float least = q.least(c);
 #pragma unroll
       for (int u = 0; u < U; ++u) {
         float x[N];
@@ -351,123 +390,32 @@ __global__ void __launch_bounds__(kScoreThreads, TOP ? kScorePerSm : kScorePerSm
 #pragma unroll
         for (int i = 0; i < N; i += 2) q.add2(x[i], x[i + 1], c);
       }
-    } else {   // a largest word of plus infinity, or at the very bottom of the range
+    } else {   // a largest word of plus infinity, or at the very ends of the range
 #pragma unroll
       for (int u = 0; u < U; ++u)
 #pragma unroll 1
         for (int i = 0; i < N; ++i) q.add(W::word(raw[u], i), c);
     }
-  }
-
-  // The CTA's list: its `top` best words, in rank 0's shared memory.
-  if (TOP) {
-    // the bar: of the warps whose lanes all have words, each has at least ceil(top / warps) threads with one that reaches it
-    const int full = min(kScoreWarps, (v1 - v0) / 32), share = full ? (p.top + full - 1) / full : 33;
-    uint32_t left = order_of(q.m), bar = 0;
-    for (int i = 0; i < share && share <= 32; ++i) {
-      bar = __reduce_max_sync(0xffffffffu, left);
-      if (lane == __ffs(__ballot_sync(0xffffffffu, left == bar)) - 1) left = 0;
-    }
-    if (lane == 0) sh.bar[warp] = warp < full ? bar : 0xffffffffu;
-    if (tid == 0) sh.n_keys = 0;
-    __syncthreads();
-    uint32_t tau = sh.bar[0];
-#pragma unroll
-    for (int i = 1; i < kScoreWarps; ++i) tau = min(tau, sh.bar[i]);
-    if (full == 0 || share > 32 || tau <= order_of(-INFINITY)) tau = 0;   // too few threads with a number above -inf
-    const int rounds = v1 > vw ? (v1 - vw + kScoreThreads - 1) / kScoreThreads : 0;   // pieces of a thread, at most
-    auto note = [&](float x, int at) {
-      if (order_of(x) < tau) return;
-      const int n = atomicAdd(&sh.n_keys, 1);
-      if (n < kScoreKeys) sh.keys[n] = key_of(x, at);
-    };
-    auto note_pieces = [&](const uint4 (&raw)[U], const int (&at)[U]) {
-#pragma unroll
-      for (int u = 0; u < U; ++u)
-        if (at[u] >= 0 && order_of(W::largest(raw[u])) >= tau)
-          for (int i = 0; i < N; ++i) note(W::word(raw[u], i), at[u] + i);
-    };
-    if (tau) {
-      if (before) note(x_before, lane);
-      if (after) note(x_after, after_at);
-      const bool all = order_of(second) >= tau, one = !all && best_v >= 0 && order_of(q.m) >= tau;
-      uint4 raw[U];
-      int at[U];
-      // a batch by its own thread
-      if (__any_sync(0xffffffffu, one)) {
-#pragma unroll
-        for (int u = 0; u < U; ++u) {
-          const int v = best_v + u * kScoreThreads;
-          at[u] = one && v < v1 ? w.head + v * N : -1;
-          raw[u] = at[u] >= 0 ? *reinterpret_cast<const uint4*>(body + static_cast<int64_t>(v) * N) : make_uint4(W::kNone, W::kNone, W::kNone, W::kNone);
-        }
-        note_pieces(raw, at);
-      }
-      // all of a thread's words by the warp
-      for (unsigned whole = __ballot_sync(0xffffffffu, all); whole; whole &= whole - 1) {
-        const int first = vw + __ffs(whole) - 1;
-        for (int i0 = 0; i0 < rounds; i0 += U * 32) {
-#pragma unroll
-          for (int u = 0; u < U; ++u) {
-            const int v = first + (i0 + u * 32 + lane) * kScoreThreads;
-            at[u] = i0 + u * 32 + lane < rounds && v < v1 ? w.head + v * N : -1;
-            raw[u] = at[u] >= 0 ? *reinterpret_cast<const uint4*>(body + static_cast<int64_t>(v) * N) : make_uint4(W::kNone, W::kNone, W::kNone, W::kNone);
-          }
-          note_pieces(raw, at);
-        }
-      }
-    }
-    __syncthreads();
-    int n = sh.n_keys;
-    if (!tau || n > kScoreKeys) {   // through the words again, in their order
-      Best best;
-      if (rank == 0 && warp == 0 && w.head > 0) {
-        const uint4 raw[1] = {make_uint4(sizeof(T) == 4 ? __float_as_uint(x_before) : __float_as_uint(x_before) >> 16, 0, 0, 0)};
-        const int at[1] = {before ? lane : -1};
-        consider<W, 1>(best, p.top, tau, raw, at, 1, x_before);
-      }
-      for (int v = vw + lane; v - lane < v1; v += U * kScoreThreads) {
-        uint4 raw[U];
-        int at[U];
-        fetch(raw, v);
-        float top = W::largest(raw[0]);
-#pragma unroll
-        for (int u = 0; u < U; ++u) {
-          at[u] = v + u * kScoreThreads < v1 ? w.head + (v + u * kScoreThreads) * N : -1;
-          top = fmaxf(top, W::largest(raw[u]));
-        }
-        consider<W, U>(best, p.top, tau, raw, at, N, top);
-      }
-      if (rank == C - 1 && warp == 0 && w.tail > 0) {
-        const uint4 raw[1] = {make_uint4(sizeof(T) == 4 ? __float_as_uint(x_after) : __float_as_uint(x_after) >> 16, 0, 0, 0)};
-        const int at[1] = {after ? after_at : -1};
-        consider<W, 1>(best, p.top, tau, raw, at, 1, x_after);
-      }
-      __syncthreads();
-      sh.keys[tid] = best.key;   // with zeros where a warp has fewer words
-      n = kScoreThreads;
-      __syncthreads();
-    }
-    // a key's place is the number of keys above it; the list's end is filled up with none
-    if (C > 1) asm volatile("barrier.cluster.wait.acquire.aligned;" ::: "memory");   // rank 0 runs
-    auto put = [&](int place, Key x) {
-      if (C > 1) asm volatile("st.shared::cluster.u64 [%0], %1;" ::"r"(cluster_map(&sh.lists[rank][place], 0)), "l"(x) : "memory");
-      else sh.lists[0][place] = x;
-    };
-    int held = 0;
-    for (int k = tid; k < n; k += kScoreThreads) {
-      const Key x = sh.keys[k];
-      int place = 0;
-      for (int i = 0; i < n; ++i) place += sh.keys[i] > x;
-      if (x && place < p.top) put(place, x);
-    }
-    if (n < p.top || n == kScoreThreads) {   // perhaps fewer words than places
-      for (int i = 0; i < n; ++i) held += sh.keys[i] != 0;
-      if (tid >= held && tid < p.top) put(tid, 0);
+  };
+  {
+    uint4 even[U], odd[U];   // the next batch is on its way under each
+    if (batches > 0) fetch(even, 0);
+#pragma unroll 1
+    for (int b = 0; b < batches; b += 2) {
+      if (b + 1 < batches) fetch(odd, b + 1);
+      take(even, vw + lane + b * kStep);
+      if (b + 1 >= batches) break;
+      if (b + 2 < batches) fetch(even, b + 2);
+      take(odd, vw + lane + (b + 1) * kStep);
     }
   }
 
-  // the warp's sums
+  // the warp's sums, and its bar: of the warps whose lanes all have words, each has at least ceil(top / warps) threads with a word that
+  // reaches it
+  uint32_t left = order_of(q.m);   // of this thread's largest, before it becomes the warp's
+  const bool mine = best_v >= 0;
+  const int full = min(kScoreWarps, (v1 - v0) / 32), share = full ? (p.top + full - 1) / full : 33;
+  const uint32_t largest = left;
   float m = q.m;
 #pragma unroll
   for (int o = 16; o > 0; o >>= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, o));
@@ -478,58 +426,146 @@ __global__ void __launch_bounds__(kScoreThreads, TOP ? kScorePerSm : kScorePerSm
     qs += __shfl_xor_sync(0xffffffffu, qs, o);
     qa += __shfl_xor_sync(0xffffffffu, qa, o);
   }
-  if (C > 1 && !TOP) asm volatile("barrier.cluster.wait.acquire.aligned;" ::: "memory");   // rank 0 runs
-  if (lane == 0) {
-    const int i = rank * kScoreWarps + warp;
-    if (C > 1) {
-      asm volatile("st.shared::cluster.f32 [%0], %1;" ::"r"(cluster_map(&sh.m[i], 0)), "f"(q.m) : "memory");
-      asm volatile("st.shared::cluster.f32 [%0], %1;" ::"r"(cluster_map(&sh.s[i], 0)), "f"(qs) : "memory");
-      asm volatile("st.shared::cluster.f32 [%0], %1;" ::"r"(cluster_map(&sh.a[i], 0)), "f"(qa) : "memory");
-    } else {
-      sh.m[i] = q.m;
-      sh.s[i] = qs;
-      sh.a[i] = qa;
-    }
-  }
-  if (C > 1) cluster_sync_all();
-  else __syncthreads();
-  if (rank != 0) return;
-  if (warp == 0) {
-    // sums over the cluster, C * kScoreWarps of them
-    float top = -INFINITY;
-    for (int i = lane; i < C * kScoreWarps; i += 32) top = fmaxf(top, sh.m[i]);
-#pragma unroll
-    for (int o = 16; o > 0; o >>= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, o));
-    float s = 0.0f, a = 0.0f;
-    for (int i = lane; i < C * kScoreWarps; i += 32) {
-      Sums one;
-      one.m = sh.m[i];
-      one.s0 = sh.s[i];
-      one.a0 = sh.a[i];
-      one.rise(top, c);
-      s += one.s0;
-      a += one.a0;
-    }
-#pragma unroll
-    for (int o = 16; o > 0; o >>= 1) {
-      s += __shfl_xor_sync(0xffffffffu, s, o);
-      a += __shfl_xor_sync(0xffffffffu, a, o);
-    }
-    if (lane == 0) {
-      const bool none = top == -INFINITY && s == 0.0f;   // no word has any mass
-      const float ln_s = logf(s);
-      sh.ln_s = ln_s;
-      sh.m_all = top;
-      if (p.lse) p.lse[r] = none ? -INFINITY : (top == -INFINITY ? s : fmaf(top, p.scale, ln_s));
-      if (p.entropy) p.entropy[r] = none ? 0.0f : ln_s - kLn2 * (a / s);
-      if (p.logprob) p.logprob[r] = token < 0 || token >= p.vocab ? 0.0f : none ? -INFINITY : fmaf(given - top, p.scale, -ln_s);
-    }
-  }
   if (TOP) {
-    // the row's list: of the CTAs' lists what reaches the largest of their last places (`top` words do)
-    Key floor = 0;
-    if (C > 1) {
-      if (lane < C) floor = sh.lists[lane][p.top - 1];
+    uint32_t bar = 0;
+    for (int i = 0; i < share && share <= 32; ++i) {
+      bar = __reduce_max_sync(0xffffffffu, left);
+      if (lane == __ffs(__ballot_sync(0xffffffffu, left == bar)) - 1) left = 0;
+    }
+    if (lane == 0) sh.bar[warp] = warp < full ? bar : 0xffffffffu;
+    if (tid == 0) sh.n_keys = 0;
+  }
+  if (lane == 0) {
+    sh.m[warp] = q.m;
+    sh.s[warp] = qs;
+    sh.a[warp] = qa;
+  }
+  __syncthreads();
+
+  // What reaches the bar, on its way; every warp adds up the CTA's sums meanwhile.
+  uint32_t tau = 0;
+  float bar = 0.0f;
+  bool all = false;
+  uint4 raw[U];
+  int at[U];
+  if (TOP) {
+    tau = sh.bar[0];
+#pragma unroll
+    for (int i = 1; i < kScoreWarps; ++i) tau = min(tau, sh.bar[i]);
+    if (full == 0 || share > 32 || tau <= order_of(-INFINITY)) tau = 0;   // too few threads with a number above -inf
+    bar = value_of(tau);
+    all = tau && order_of(second) >= tau;
+    const bool one = tau && !all && mine && largest >= tau;   // in one batch alone
+#pragma unroll
+    for (int u = 0; u < U; ++u) {
+      const int v = best_v + u * kScoreThreads;
+      at[u] = w.head + v * N;
+      raw[u] = one && v < v1 ? *reinterpret_cast<const uint4*>(body + static_cast<int64_t>(v) * N) : make_uint4(W::kNone, W::kNone, W::kNone, W::kNone);
+    }
+  }
+  Sums sum = join<kScoreWarps>(sh.m, sh.s, sh.a, kScoreWarps, c);
+
+  int n = 0;
+  if (TOP) {
+    auto note_pieces = [&] {
+#pragma unroll
+      for (int u = 0; u < U; ++u) {
+        uint32_t hits = 0;
+#pragma unroll
+        for (int i = 0; i < N; ++i) hits |= (W::word(raw[u], i) >= bar ? 1u : 0u) << i;
+        if (!hits) continue;
+        for (int k = atomicAdd(&sh.n_keys, __popc(hits)); hits; hits &= hits - 1, ++k) {
+          const int i = __ffs(hits) - 1;
+          if (k < kScoreKeys) sh.keys[k] = key_of(W::word(raw[u], i), at[u] + i);
+        }
+      }
+    };
+    if (tau) {
+      note_pieces();
+      auto note = [&](float x, int where) {
+        if (!(x >= bar)) return;
+        const int k = atomicAdd(&sh.n_keys, 1);
+        if (k < kScoreKeys) sh.keys[k] = key_of(x, where);
+      };
+      if (before) note(x_before, lane);
+      if (after) note(x_after, after_at);
+      // threads with several such batches: all of their words, by the warp
+      const int rounds = v1 > vw ? (v1 - vw + kScoreThreads - 1) / kScoreThreads : 0;   // pieces of a thread, at most
+      for (unsigned whole = __ballot_sync(0xffffffffu, all); whole; whole &= whole - 1) {
+        const int first = vw + __ffs(whole) - 1;
+        for (int i0 = lane; i0 - lane < rounds; i0 += U * 32) {
+#pragma unroll
+          for (int u = 0; u < U; ++u) {
+            const int v = first + (i0 + u * 32) * kScoreThreads;
+            at[u] = w.head + v * N;
+            raw[u] = i0 + u * 32 < rounds && v < v1 ? *reinterpret_cast<const uint4*>(body + static_cast<int64_t>(v) * N) : make_uint4(W::kNone, W::kNone, W::kNone, W::kNone);
+          }
+          note_pieces();
+        }
+      }
+    }
+    __syncthreads();
+    n = sh.n_keys;
+    if (!tau || n > kScoreKeys) {   // through the words again, in their order
+      Best best;
+      if (rank == 0 && warp == 0 && w.head > 0) {
+        const uint4 one[1] = {make_uint4(sizeof(T) == 4 ? __float_as_uint(x_before) : __float_as_uint(x_before) >> 16, 0, 0, 0)};
+        const int where[1] = {before ? lane : -1};
+        consider<W, 1>(best, p.top, tau, one, where, 1, x_before);
+      }
+#pragma unroll 1
+      for (int b = 0; b < batches; ++b) {
+        const int v = vw + lane + b * kStep;
+        fetch(raw, b);
+#pragma unroll
+        for (int u = 0; u < U; ++u) at[u] = v + u * kScoreThreads < v1 ? w.head + (v + u * kScoreThreads) * N : -1;
+        consider<W, U>(best, p.top, tau, raw, at, N, W::largest(raw));
+      }
+      if (rank == C - 1 && warp == 0 && w.tail > 0) {
+        const uint4 one[1] = {make_uint4(sizeof(T) == 4 ? __float_as_uint(x_after) : __float_as_uint(x_after) >> 16, 0, 0, 0)};
+        const int where[1] = {after ? after_at : -1};
+        consider<W, 1>(best, p.top, tau, one, where, 1, x_after);
+      }
+      __syncthreads();
+      sh.keys[tid] = best.key;   // none where a warp has fewer words
+      n = kScoreThreads;
+      __syncthreads();
+    }
+  }
+  // The number of keys above one is its place.
+  auto place_of = [&](Key x) {
+    int place = 0;
+#pragma unroll 8
+    for (int i = 0; i < n; ++i) place += sh.keys[i] > x;
+    return place;
+  };
+
+  if (C > 1) {
+    asm volatile("barrier.cluster.wait.acquire.aligned;" ::: "memory");   // rank 0 runs
+    if (tid == 0) {
+      asm volatile("st.shared::cluster.f32 [%0], %1;" ::"r"(cluster_map(&sh.cta_m[rank], 0)), "f"(sum.m) : "memory");
+      asm volatile("st.shared::cluster.f32 [%0], %1;" ::"r"(cluster_map(&sh.cta_s[rank], 0)), "f"(sum.s0) : "memory");
+      asm volatile("st.shared::cluster.f32 [%0], %1;" ::"r"(cluster_map(&sh.cta_a[rank], 0)), "f"(sum.a0) : "memory");
+    }
+    if (TOP) {   // this CTA's list; its end is filled up with none where it has fewer words than places
+      auto put = [&](int place, Key x) { asm volatile("st.shared::cluster.u64 [%0], %1;" ::"r"(cluster_map(&sh.lists[rank][place], 0)), "l"(x) : "memory"); };
+      for (int k = tid; k < n; k += kScoreThreads) {
+        const Key x = sh.keys[k];
+        if (!x) continue;
+        const int place = place_of(x);
+        if (place < p.top) put(place, x);
+      }
+      if (n < p.top || n == kScoreThreads) {
+        const int held = place_of(0);
+        if (tid >= held && tid < p.top) put(tid, 0);
+      }
+    }
+    cluster_sync_all();
+    if (rank != 0) return;
+    sum = join<kScoreMaxCluster>(sh.cta_m, sh.cta_s, sh.cta_a, C, c);
+    if (TOP) {
+      // of the CTAs' lists what reaches the largest of their last places (`top` words do)
+      Key floor = lane < C ? sh.lists[lane][p.top - 1] : 0;
 #pragma unroll
       for (int o = 8; o > 0; o >>= 1) {
         const Key other = __shfl_xor_sync(0xffffffffu, floor, o);
@@ -542,20 +578,30 @@ __global__ void __launch_bounds__(kScoreThreads, TOP ? kScorePerSm : kScorePerSm
         const Key x = i % 32 < p.top ? sh.lists[i / 32][i % 32] : 0;
         if (x && x >= floor) sh.keys[atomicAdd(&sh.n_keys, 1)] = x;
       }
+      __syncthreads();
+      n = sh.n_keys;
     }
-    __syncthreads();
-    const float ln_s = sh.ln_s, m_all = sh.m_all;
-    const bool none = m_all == -INFINITY && ln_s == -INFINITY;
-    const int n = C > 1 ? sh.n_keys : p.top;
+  }
+  const bool none = sum.m == -INFINITY && sum.s0 == 0.0f;   // no word has any mass
+  const float ln_s = logf(sum.s0);
+  auto logp = [&](float x) {
+    const float d = sum.distance(x, c) * kLn2;   // past the range, where log2(e) takes it, the difference itself
+    return none ? -INFINITY : (fabsf(d) < 1e37f ? d : (x - sum.m) * p.scale) - ln_s;
+  };
+  if (tid == 0) {
+    if (p.lse) p.lse[r] = none ? -INFINITY : sum.m == -INFINITY ? sum.s0 : sum.wild() ? fmaf(sum.m, p.scale, ln_s) : fmaf(sum.ref, kLn2, ln_s);
+    if (p.entropy) p.entropy[r] = none ? 0.0f : ln_s - kLn2 * (sum.a0 / sum.s0);
+    if (p.logprob) p.logprob[r] = token < 0 || token >= p.vocab ? 0.0f : logp(given);
+  }
+  if (TOP) {
     for (int k = tid; k < n; k += kScoreThreads) {
-      const Key x = C > 1 ? sh.keys[k] : sh.lists[0][k];
-      int place = C > 1 ? 0 : k;
-      if (C > 1)
-        for (int i = 0; i < n; ++i) place += sh.keys[i] > x;
-      if (!x || place >= p.top) continue;
+      const Key x = sh.keys[k];
+      if (!x) continue;
+      const int place = place_of(x);
+      if (place >= p.top) continue;
       const float v = value_of(static_cast<uint32_t>(x >> 32));
       p.top_token[r * p.top + place] = static_cast<int32_t>(0xffffffffu - static_cast<uint32_t>(x));
-      p.top_logprob[r * p.top + place] = none ? -INFINITY : fmaf(v - m_all, p.scale, -ln_s);
+      p.top_logprob[r * p.top + place] = logp(v);
     }
   }
 }
@@ -652,18 +698,26 @@ aq_status check_logits(const void* logits, int64_t ld, int64_t rows, int32_t voc
   if (rows < 0) return serve_fail(AQ_ERR_SHAPE, "%s: rows=%lld is negative", who, (long long)rows);
   if (vocab < 1 || vocab > (1 << 30)) return serve_fail(AQ_ERR_SHAPE, "%s: vocab=%d outside [1, 2^30]", who, vocab);
   if (type != AQ_PROB_F32 && type != AQ_PROB_BF16) return serve_fail(AQ_ERR_INVALID_ARG, "%s: unknown element type %d", who, type);
-  if (!(scale > 0.0f) || !(scale < 1e30f)) return serve_fail(AQ_ERR_INVALID_ARG, "%s: scale must be positive and finite", who);
+  if (!(scale >= 1e-30f) || !(scale <= 1e30f)) return serve_fail(AQ_ERR_INVALID_ARG, "%s: scale must lie between 1e-30 and 1e30", who);
   if (rows > 0 && !logits) return serve_fail(AQ_ERR_INVALID_ARG, "%s: logits must be non-NULL", who);
   if (ld < vocab && rows > 1) return serve_fail(AQ_ERR_SHAPE, "%s: ld=%lld < vocab=%d", who, (long long)ld, vocab);
   if (!serve_aligned(logits, type == AQ_PROB_F32 ? 4 : 2)) return serve_fail(AQ_ERR_ALIGNMENT, "%s: logits must be aligned to their elements", who);
   return AQ_OK;
 }
 
-// CTAs that share a row: enough of them to fill the GPU several times over (so that the last wave weighs little), with at least
-// one round of loads a thread and more.
-int score_parts(int64_t rows, int32_t vocab, int sms, int most) {
+// CTAs that share a row. Three CTAs an SM is what fills the GPU once; a row's part is no smaller than 8192 words, as what comes after
+// its words weighs as much as 4000 of them (333 rows of 50257 words with 20 alternatives, us: one CTA a row 22, two 29, four 40; 100
+// rows of 262144: one 36, two 25, four 23, eight 32).
+int score_cluster(int64_t rows, int32_t vocab, int sms) {
   int c = 1;
-  while (c < most && rows * c < 6ll * sms && vocab / (2 * c) >= 8192) c *= 2;
+  while (c < kScoreMaxCluster && 2 * rows * c <= 3ll * sms && vocab / (2 * c) >= 8192) c *= 2;
+  return c;
+}
+// Blocks that share a row of the gradient: pieces of 48 KB and more, smaller ones while they would not fill the GPU (1024 rows of
+// 262144 words in bf16, us: 166 in one piece, 159 in eight; one row 21 and 2.3 in 64).
+int score_parts(int64_t rows, int32_t vocab, int size, int sms) {
+  int c = 1;
+  while (c < 64 && (static_cast<int64_t>(vocab) * size / (2 * c) >= 48 * 1024 || (2 * rows * c <= 2ll * sms && vocab / (2 * c) >= 4096))) c *= 2;
   return c;
 }
 
@@ -713,7 +767,7 @@ extern "C" aq_status aq_token_logprobs(const void* logits, int64_t ld, int64_t r
   p.vocab = vocab;
   p.top = top;
   p.device = dev.index;
-  p.cluster = score_parts(rows, vocab, dev.sms, kScoreMaxCluster);
+  p.cluster = score_cluster(rows, vocab, dev.sms);
   if (rows * p.cluster > 0x7fffffffLL) return serve_fail(AQ_ERR_SHAPE, "%s: rows=%lld is too large", who, (long long)rows);
   const unsigned grid = static_cast<unsigned>(rows * p.cluster);
   const cudaStream_t cs = static_cast<cudaStream_t>(stream);
@@ -763,7 +817,7 @@ extern "C" aq_status aq_token_logprobs_backward(const void* logits, int64_t ld, 
   p.dlse = dlse;
   p.scale = scale;
   p.vocab = vocab;
-  p.parts = score_parts(rows, vocab, dev.sms, 64);
+  p.parts = score_parts(rows, vocab, static_cast<int>(size), dev.sms);
   if (rows * p.parts > 0x7fffffffLL) return serve_fail(AQ_ERR_SHAPE, "%s: rows=%lld is too large", who, (long long)rows);
   const unsigned grid = static_cast<unsigned>(rows * p.parts);
   const cudaStream_t cs = static_cast<cudaStream_t>(stream);
