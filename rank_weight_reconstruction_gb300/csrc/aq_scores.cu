@@ -25,6 +25,7 @@ namespace {
 
 constexpr int kScoreThreads = 256, kScoreWarps = kScoreThreads / 32, kScorePerSm = 3;
 constexpr int kScoreMaxCluster = 16;
+constexpr int kScoreSmall = 2;   // warps of a CTA for many rows of few words
 constexpr float kLog2e = 1.4426950408889634f, kLn2 = 0.6931471805599453f;
 
 struct ScoreParams {
@@ -292,12 +293,13 @@ __device__ __forceinline__ void consider(Best& b, int k, uint32_t tau, const uin
 constexpr int kScoreKeys = 512;   // keys of one CTA, or of the cluster's lists, that are ranked against each other
 static_assert(kScoreKeys >= kScoreMaxCluster * AQ_MAX_TOP, "the cluster's lists fit");
 
+template <int WARPS>
 struct ScoreShared {
   Key keys[kScoreKeys];
-  Key lists[kScoreMaxCluster][32];   // rank 0's
+  Key lists[WARPS < kScoreWarps ? 1 : kScoreMaxCluster][32];   // rank 0's
   float cta_m[kScoreMaxCluster], cta_s[kScoreMaxCluster], cta_a[kScoreMaxCluster];   // rank 0's
-  float m[kScoreWarps], s[kScoreWarps], a[kScoreWarps];
-  uint32_t bar[kScoreWarps];
+  float m[WARPS], s[WARPS], a[WARPS];
+  uint32_t bar[WARPS];
   int32_t n_keys;
 };
 
@@ -324,11 +326,12 @@ __device__ __forceinline__ Sums join(const float* m, const float* s, const float
   return one;
 }
 
-template <typename T, bool TOP>
-__global__ void __launch_bounds__(kScoreThreads, TOP ? kScorePerSm : kScorePerSm + 1) aq_scores_kernel(const __grid_constant__ ScoreParams p) {
+// WARPS: eight, or two for many rows of few words (a cluster of one).
+template <typename T, bool TOP, int WARPS>
+__global__ void __launch_bounds__(32 * WARPS, (TOP ? kScorePerSm : kScorePerSm + 1) * kScoreWarps / WARPS) aq_scores_kernel(const __grid_constant__ ScoreParams p) {
   using W = Words<T>;
-  constexpr int N = W::N, U = 4;
-  __shared__ ScoreShared sh;
+  constexpr int N = W::N, U = 4, kThreads = 32 * WARPS;
+  __shared__ ScoreShared<WARPS> sh;
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
   const int C = p.cluster, rank = C > 1 ? static_cast<int>(cluster_ctarank()) : 0;
   const int64_t r = blockIdx.x / C;
@@ -359,17 +362,17 @@ __global__ void __launch_bounds__(kScoreThreads, TOP ? kScorePerSm : kScorePerSm
   const int v0 = static_cast<int>(static_cast<int64_t>(w.vecs) * rank / C), v1 = static_cast<int>(static_cast<int64_t>(w.vecs) * (rank + 1) / C);
   const int vw = v0 + warp * 32;   // a warp's words of a round are neighbours
   // A batch of the warp's words: U pieces of 16 bytes a lane, b batches from its first.
-  constexpr int kStep = U * kScoreThreads;
+  constexpr int kStep = U * kThreads;
   const int batches = v1 > vw ? (v1 - vw + kStep - 1) / kStep : 0;
   auto fetch = [&](uint4 (&raw)[U], int b) {
     const int v = vw + lane + b * kStep;
-    if (v - lane + 32 + (U - 1) * kScoreThreads <= v1) {
+    if (v - lane + 32 + (U - 1) * kThreads <= v1) {
 #pragma unroll
-      for (int u = 0; u < U; ++u) raw[u] = ld_words(body + static_cast<int64_t>(v + u * kScoreThreads) * N);
+      for (int u = 0; u < U; ++u) raw[u] = ld_words(body + static_cast<int64_t>(v + u * kThreads) * N);
     } else {
 #pragma unroll
       for (int u = 0; u < U; ++u)
-        raw[u] = v + u * kScoreThreads < v1 ? ld_words(body + static_cast<int64_t>(v + u * kScoreThreads) * N) : make_uint4(W::kNone, W::kNone, W::kNone, W::kNone);
+        raw[u] = v + u * kThreads < v1 ? ld_words(body + static_cast<int64_t>(v + u * kThreads) * N) : make_uint4(W::kNone, W::kNone, W::kNone, W::kNone);
     }
   };
   float second = -INFINITY;   // the largest of all batches but the one that holds the thread's largest
@@ -414,7 +417,7 @@ __global__ void __launch_bounds__(kScoreThreads, TOP ? kScorePerSm : kScorePerSm
   // reaches it
   uint32_t left = order_of(q.m);   // of this thread's largest, before it becomes the warp's
   const bool mine = best_v >= 0;
-  const int full = min(kScoreWarps, (v1 - v0) / 32), share = full ? (p.top + full - 1) / full : 33;
+  const int full = min(WARPS, (v1 - v0) / 32), share = full ? (p.top + full - 1) / full : 33;
   const uint32_t largest = left;
   float m = q.m;
 #pragma unroll
@@ -451,19 +454,19 @@ __global__ void __launch_bounds__(kScoreThreads, TOP ? kScorePerSm : kScorePerSm
   if (TOP) {
     tau = sh.bar[0];
 #pragma unroll
-    for (int i = 1; i < kScoreWarps; ++i) tau = min(tau, sh.bar[i]);
+    for (int i = 1; i < WARPS; ++i) tau = min(tau, sh.bar[i]);
     if (full == 0 || share > 32 || tau <= order_of(-INFINITY)) tau = 0;   // too few threads with a number above -inf
     bar = value_of(tau);
     all = tau && order_of(second) >= tau;
     const bool one = tau && !all && mine && largest >= tau;   // in one batch alone
 #pragma unroll
     for (int u = 0; u < U; ++u) {
-      const int v = best_v + u * kScoreThreads;
+      const int v = best_v + u * kThreads;
       at[u] = w.head + v * N;
       raw[u] = one && v < v1 ? *reinterpret_cast<const uint4*>(body + static_cast<int64_t>(v) * N) : make_uint4(W::kNone, W::kNone, W::kNone, W::kNone);
     }
   }
-  Sums sum = join<kScoreWarps>(sh.m, sh.s, sh.a, kScoreWarps, c);
+  Sums sum = join<WARPS>(sh.m, sh.s, sh.a, WARPS, c);
 
   int n = 0;
   if (TOP) {
@@ -490,13 +493,13 @@ __global__ void __launch_bounds__(kScoreThreads, TOP ? kScorePerSm : kScorePerSm
       if (before) note(x_before, lane);
       if (after) note(x_after, after_at);
       // threads with several such batches: all of their words, by the warp
-      const int rounds = v1 > vw ? (v1 - vw + kScoreThreads - 1) / kScoreThreads : 0;   // pieces of a thread, at most
+      const int rounds = v1 > vw ? (v1 - vw + kThreads - 1) / kThreads : 0;   // pieces of a thread, at most
       for (unsigned whole = __ballot_sync(0xffffffffu, all); whole; whole &= whole - 1) {
         const int first = vw + __ffs(whole) - 1;
         for (int i0 = lane; i0 - lane < rounds; i0 += U * 32) {
 #pragma unroll
           for (int u = 0; u < U; ++u) {
-            const int v = first + (i0 + u * 32) * kScoreThreads;
+            const int v = first + (i0 + u * 32) * kThreads;
             at[u] = w.head + v * N;
             raw[u] = i0 + u * 32 < rounds && v < v1 ? *reinterpret_cast<const uint4*>(body + static_cast<int64_t>(v) * N) : make_uint4(W::kNone, W::kNone, W::kNone, W::kNone);
           }
@@ -518,7 +521,7 @@ __global__ void __launch_bounds__(kScoreThreads, TOP ? kScorePerSm : kScorePerSm
         const int v = vw + lane + b * kStep;
         fetch(raw, b);
 #pragma unroll
-        for (int u = 0; u < U; ++u) at[u] = v + u * kScoreThreads < v1 ? w.head + (v + u * kScoreThreads) * N : -1;
+        for (int u = 0; u < U; ++u) at[u] = v + u * kThreads < v1 ? w.head + (v + u * kThreads) * N : -1;
         consider<W, U>(best, p.top, tau, raw, at, N, W::largest(raw));
       }
       if (rank == C - 1 && warp == 0 && w.tail > 0) {
@@ -528,7 +531,7 @@ __global__ void __launch_bounds__(kScoreThreads, TOP ? kScorePerSm : kScorePerSm
       }
       __syncthreads();
       sh.keys[tid] = best.key;   // none where a warp has fewer words
-      n = kScoreThreads;
+      n = kThreads;
       __syncthreads();
     }
   }
@@ -549,13 +552,13 @@ __global__ void __launch_bounds__(kScoreThreads, TOP ? kScorePerSm : kScorePerSm
     }
     if (TOP) {   // this CTA's list; its end is filled up with none where it has fewer words than places
       auto put = [&](int place, Key x) { asm volatile("st.shared::cluster.u64 [%0], %1;" ::"r"(cluster_map(&sh.lists[rank][place], 0)), "l"(x) : "memory"); };
-      for (int k = tid; k < n; k += kScoreThreads) {
+      for (int k = tid; k < n; k += kThreads) {
         const Key x = sh.keys[k];
         if (!x) continue;
         const int place = place_of(x);
         if (place < p.top) put(place, x);
       }
-      if (n < p.top || n == kScoreThreads) {
+      if (n < p.top || n == kThreads) {
         const int held = place_of(0);
         if (tid >= held && tid < p.top) put(tid, 0);
       }
@@ -574,7 +577,7 @@ __global__ void __launch_bounds__(kScoreThreads, TOP ? kScorePerSm : kScorePerSm
       floor = __shfl_sync(0xffffffffu, floor, 0);
       if (tid == 0) sh.n_keys = 0;
       __syncthreads();
-      for (int i = tid; i < C * 32; i += kScoreThreads) {
+      for (int i = tid; i < C * 32; i += kThreads) {
         const Key x = i % 32 < p.top ? sh.lists[i / 32][i % 32] : 0;
         if (x && x >= floor) sh.keys[atomicAdd(&sh.n_keys, 1)] = x;
       }
@@ -594,7 +597,7 @@ __global__ void __launch_bounds__(kScoreThreads, TOP ? kScorePerSm : kScorePerSm
     if (p.logprob) p.logprob[r] = token < 0 || token >= p.vocab ? 0.0f : logp(given);
   }
   if (TOP) {
-    for (int k = tid; k < n; k += kScoreThreads) {
+    for (int k = tid; k < n; k += kThreads) {
       const Key x = sh.keys[k];
       if (!x) continue;
       const int place = place_of(x);
@@ -684,14 +687,15 @@ __global__ void __launch_bounds__(kScoreThreads, 4) aq_scores_grad_kernel(const 
 }
 
 template <typename T, bool TOP>
-cudaError_t launch_scores(const ScoreParams& p, unsigned grid, cudaStream_t st) {
+cudaError_t launch_scores(const ScoreParams& p, unsigned grid, int warps, cudaStream_t st) {
+  if (warps == kScoreSmall) return launch_serve(aq_scores_kernel<T, TOP, kScoreSmall>, p, grid, 32 * kScoreSmall, 0, st);
   static std::atomic<uint64_t> ready{0};   // devices on which the kernel may use clusters of 16
   if (p.cluster > 8 && !(ready.load() >> p.device & 1)) {
-    const cudaError_t e = cudaFuncSetAttribute(aq_scores_kernel<T, TOP>, cudaFuncAttributeNonPortableClusterSizeAllowed, 1);
+    const cudaError_t e = cudaFuncSetAttribute(aq_scores_kernel<T, TOP, kScoreWarps>, cudaFuncAttributeNonPortableClusterSizeAllowed, 1);
     if (e != cudaSuccess) return e;
     ready.fetch_or(1ull << p.device);
   }
-  return launch_serve(aq_scores_kernel<T, TOP>, p, grid, kScoreThreads, 0, st, p.cluster);
+  return launch_serve(aq_scores_kernel<T, TOP, kScoreWarps>, p, grid, kScoreThreads, 0, st, p.cluster);
 }
 
 aq_status check_logits(const void* logits, int64_t ld, int64_t rows, int32_t vocab, int32_t type, float scale, const char* who) {
@@ -712,6 +716,13 @@ int score_cluster(int64_t rows, int32_t vocab, int sms) {
   int c = 1;
   while (c < kScoreMaxCluster && 2 * rows * c <= 3ll * sms && vocab / (2 * c) >= 8192) c *= 2;
   return c;
+}
+// Warps of a CTA: two where there are rows enough and a row's words are few, so that what comes before and after the words (the row's
+// sums joined, its best words placed) goes on in four times as many rows at once. Two warps against eight, us: 4096 rows of 1000 words
+// 6.9 and 18.7, with 5 alternatives 13.0 and 36.3, with 32 17 and 42; 1000 rows of 3000 3.9 and 5.6, with 5 7.8 and 11.9, but with 32
+// 15.0 and 13.7; 4096 rows of 8000 24 and 30, with 32 56 and 67; 2048 rows of 100000 with 5 163 and 138.
+int score_warps(int64_t rows, int32_t vocab, int32_t top, int cluster, int sms) {
+  return cluster == 1 && rows > 3ll * sms && vocab <= 16384 && (top <= 16 || rows > 16ll * sms) ? kScoreSmall : kScoreWarps;
 }
 // Blocks that share a row of the gradient: pieces of 48 KB and more, smaller ones while they would not fill the GPU (1024 rows of
 // 262144 words in bf16, us: 166 in one piece, 159 in eight; one row 21 and 2.3 in 64).
@@ -772,8 +783,9 @@ extern "C" aq_status aq_token_logprobs(const void* logits, int64_t ld, int64_t r
   const unsigned grid = static_cast<unsigned>(rows * p.cluster);
   const cudaStream_t cs = static_cast<cudaStream_t>(stream);
   cudaError_t e;
-  if (type == AQ_PROB_F32) e = top ? launch_scores<float, true>(p, grid, cs) : launch_scores<float, false>(p, grid, cs);
-  else e = top ? launch_scores<uint16_t, true>(p, grid, cs) : launch_scores<uint16_t, false>(p, grid, cs);
+  const int warps = score_warps(rows, vocab, top, p.cluster, dev.sms);
+  if (type == AQ_PROB_F32) e = top ? launch_scores<float, true>(p, grid, warps, cs) : launch_scores<float, false>(p, grid, warps, cs);
+  else e = top ? launch_scores<uint16_t, true>(p, grid, warps, cs) : launch_scores<uint16_t, false>(p, grid, warps, cs);
   return serve_launched(e, who);
 }
 
