@@ -16,6 +16,7 @@
 // shared memory.
 #include <algorithm>
 #include <atomic>
+#include <type_traits>
 
 #include "aq_serve.h"
 
@@ -97,6 +98,11 @@ __device__ __forceinline__ uint32_t lds32(uint32_t a) {
   asm volatile("ld.shared.u32 %0, [%1];" : "=r"(r) : "r"(a));
   return r;
 }
+__device__ __forceinline__ uint16_t lds16(uint32_t a) {
+  uint16_t r;
+  asm volatile("ld.shared.u16 %0, [%1];" : "=h"(r) : "r"(a));
+  return r;
+}
 __device__ __forceinline__ float2 lds64f(uint32_t a) {
   float2 r;
   asm volatile("ld.shared.v2.f32 {%0, %1}, [%2];" : "=f"(r.x), "=f"(r.y) : "r"(a));
@@ -127,12 +133,15 @@ __global__ void __launch_bounds__(32 * NW, 16 / NW) aq_nvfp4_kernel(const __grid
   const int t_first = static_cast<int>(static_cast<int64_t>(p.tiles) * cluster / p.clusters);
   const int t_last = static_cast<int>(static_cast<int64_t>(p.tiles) * (cluster + 1) / p.clusters);
   const int rounds = (t_last - t_first + p.round - 1) / p.round;
+  // Of a chunk of a row lane t of four takes two pieces of 16 bytes: side by side, or, where its scales' bytes can be read in twos, one of
+  // either half, so that a last chunk of half a row's chunk is half the work.
+  constexpr bool kHalves = MODE != 1;
   const int c_first = rank * p.slice, c_whole = p.in / kQChunk;   // chunks before c_whole lie within K
   const int nc = max(0, min(p.slice, (p.in + kQChunk - 1) / kQChunk - c_first));
   const int64_t m0 = static_cast<int64_t>(blockIdx.y) * p.tokens;
   const int M = static_cast<int>(min(p.M - m0, static_cast<int64_t>(p.tokens)));
 
-  constexpr int kPart = 8 * NT * kQPart, kQThreads = 32 * NW;
+  constexpr int kPart = 8 * NT * kQPart;
   float* part = reinterpret_cast<float*>(smem);                           // [round + NW][8 NT][kQPart], unless whole
   const int recv_tiles = (p.round + S - 1) / S;                           // tiles that one CTA of the cluster finishes
   const int recv_src = recv_tiles * 16 * p.tokens, recv_buf = S > 1 ? S * recv_src : 0;
@@ -154,12 +163,14 @@ __global__ void __launch_bounds__(32 * NW, 16 / NW) aq_nvfp4_kernel(const __grid
   const uint8_t* f_q = nullptr;   // this lane's 16 bytes of row lane / 8 of the tile, chunk f_c; the others 4, 8 and 12 rows on
   const uint8_t* f_s = nullptr;   // its scales there
   int64_t f_row4 = 0;
-  bool f_full = false;            // all 16 rows there, and room behind their scales
+  int f_safe = 0;                 // tiles of this segment before f_safe have all 16 rows, and room behind their scales
+  int64_t f_skip = 0;             // from a tile's chunk behind the slice to the next tile's first
   const int s_step = MODE == 2 ? 2048 : 16;
   auto aim = [&] {
     const Nvfp4Seg& sg = tile_seg(p, f_tile);
     const int row0 = (f_tile - sg.begin) * 16, rows = min(16, sg.out - row0);
-    f_full = rows == 16 && (MODE != 1 || static_cast<int64_t>(sg.out - row0 - 16) * p.cols >= 16);
+    f_safe = sg.begin + (sg.out - (MODE == 1 ? (31 + p.cols) / p.cols : 0)) / 16;
+    f_skip = 16 * sg.ldq - nc * 128;
     f_row4 = 4 * sg.ldq;
     f_q = sg.q + static_cast<int64_t>(row0 + min(lane / 8, rows - 1)) * sg.ldq + (lane & 7) * 16 + static_cast<int64_t>(f_c) * 128;
     if (MODE <= 1) {   // row lane / 2: half of its 16 scales, or one of the two aligned pieces that hold them
@@ -178,6 +189,17 @@ __global__ void __launch_bounds__(32 * NW, 16 / NW) aq_nvfp4_kernel(const __grid
       f_tile = t_first + f_round * p.round + first / nc;
       f_c = c_first + first % nc;
       aim();
+    }
+  };
+  auto next_tile = [&] {   // the slice's first chunk, a tile on
+    f_c = c_first;
+    if (++f_tile >= f_safe) return aim();
+    f_q += f_skip;
+    if (MODE <= 1) {
+      f_s += 16 * (p.cols - nc);
+    } else {
+      const int i = f_tile - tile_seg(p, f_tile).begin;   // rows 16 apart stand 256 bytes apart, or 4 on in the 16 bytes of the row 32 before
+      f_s += (i & 1 ? 256 : i & 7 ? -252 : (p.cols + 3) / 4 * 512 - 268) - nc * 2048ll;
     }
   };
   // Rows or bytes that are not there: zeros.
@@ -213,11 +235,11 @@ __global__ void __launch_bounds__(32 * NW, 16 / NW) aq_nvfp4_kernel(const __grid
       }
     }
   };
-  const uint32_t to_q = (lane / 8) * 128 + (((lane & 7) ^ ((lane / 8) & 1)) * 16);   // rows 4 apart keep their parity
+  const uint32_t to_q = (lane / 8) * 128 + (((lane & 7) ^ (((lane / 8) & 1) * (kHalves ? 4 : 1))) * 16);   // rows 4 apart keep their parity
   auto feed = [&](uint32_t st) {
     if (f_left > 0) {
       const uint32_t dq = st + to_q;
-      if (f_full && f_c < c_whole) {
+      if (f_tile < f_safe && f_c < c_whole) {
         if (p.wide) {
           cp_async_16(dq, f_q);
           cp_async_16(dq + 512, f_q + f_row4);
@@ -238,6 +260,22 @@ __global__ void __launch_bounds__(32 * NW, 16 / NW) aq_nvfp4_kernel(const __grid
           cp_async_small<4>(st + kQCodes + lane * 4, f_s);
           cp_async_small<4>(st + kQCodes + lane * 4 + 128, f_s + 128);
         }
+      } else if (f_tile < f_safe && p.wide) {   // a row's last bytes: a piece with none of them reads at the chunk's first
+        const int held = max(0, min(16, p.in / 2 - f_c * 128 - (lane & 7) * 16));
+        const uint8_t* from = f_q - (held ? 0 : (lane & 7) * 16);
+#pragma unroll
+        for (int i = 0; i < 4; ++i) cp_async_16_zfill(dq + i * 512, from + i * f_row4, held);
+        if (MODE == 0) {
+          const bool is = f_c * 16 + (lane & 1) * 8 < p.cols;
+          cp_async_small<8>(st + kQCodes + lane * 8, f_s - (is ? 0 : (lane & 1) * 8), is ? 8 : 0);
+        } else if (MODE == 1) {
+          cp_async_16(st + kQCodes + lane * 16, f_s);
+        } else {
+          const bool is = f_c * 16 + (lane & 3) * 4 < p.cols;
+          const uint8_t* at = f_s - (is ? 0 : (lane & 3) * 512);
+          cp_async_small<4>(st + kQCodes + lane * 4, at, is ? 4 : 0);
+          cp_async_small<4>(st + kQCodes + lane * 4 + 128, at + 128, is ? 4 : 0);
+        }
       } else {
         copy_some(st, dq);
       }
@@ -247,9 +285,7 @@ __global__ void __launch_bounds__(32 * NW, 16 / NW) aq_nvfp4_kernel(const __grid
       if (--f_left == 0) {
         next_run();
       } else if (f_c == c_first + nc) {
-        f_c = c_first;
-        ++f_tile;
-        aim();
+        next_tile();
       }
     }
     cp_async_commit();
@@ -266,7 +302,7 @@ __global__ void __launch_bounds__(32 * NW, 16 / NW) aq_nvfp4_kernel(const __grid
   const int items = nc * M;
   const uint32_t x_chunk = static_cast<uint32_t>(M) * kQRow;
   {
-    const uint32_t x_lane = xs + (lane >> 3) * 144 + (lane & 7) * 16;
+    const uint32_t x_lane = xs + (kHalves ? ((lane >> 2) & 3) * 144 + (lane >> 4) * 64 + (lane & 3) * 16 : (lane >> 3) * 144 + (lane & 7) * 16);
     const int turn = items ? static_cast<int>((blockIdx.x * 11u) % static_cast<uint32_t>(items)) : 0;
     constexpr int kBatch = 8;   // loads in flight
     for (int i0 = warp; i0 < items; i0 += kBatch * NW) {
@@ -320,20 +356,29 @@ __global__ void __launch_bounds__(32 * NW, 16 / NW) aq_nvfp4_kernel(const __grid
   auto finish = [&](int round) {
     const float* from = recv + (round & 1) * recv_buf;
     const int n = min(p.round, t_last - t_first - round * p.round), mine = (n - rank + S - 1) / S;
-    for (int e = tid; e < mine * 16 * M; e += kQThreads) {
-      const int i = e / (16 * M), in_tile = e - i * 16 * M;   // [token][row]
+    const int pairs = (M + 1) / 2;   // a warp: two tokens of a tile
+    for (int e = warp; e < mine * pairs; e += NW) {
+      const int i = e / pairs, m = 2 * (e - i * pairs) + (lane >> 4);
+      if (m >= M) continue;
+      const float* at = from + i * 16 * p.tokens + m * 16 + (lane & 15);
       float v = 0.0f;
-      for (int s = 0; s < parts; ++s) v += from[s * recv_src + i * 16 * p.tokens + in_tile];
-      put(t_first + round * p.round + i * S + rank, in_tile >> 4, in_tile & 15, v);
+      for (int s = 0; s < parts; ++s) v += at[s * recv_src];
+      put(t_first + round * p.round + i * S + rank, m, lane & 15, v);
     }
   };
   uint32_t b_at[NT];
 #pragma unroll
   for (int n = 0; n < NT; ++n) b_at[n] = min(n * 8 + g, M - 1) * kQRow + t * 144;   // columns past M repeat the last: unread
-  const uint32_t at_a = g * 128 + (((2 * t) ^ (g & 1)) * 16), at_s = kQCodes + (MODE == 1 ? 32 : 16) * g + 4 * t;
+  const uint32_t at_a = g * 128 + (kHalves ? (t ^ ((g & 1) * 4)) : ((2 * t) ^ (g & 1))) * 16, at_s = kQCodes + (kHalves ? 16 * g + 2 * t : 32 * g + 4 * t);
   const uint32_t back_at = smem_u32(back) + 8 * t;
   if (S > 1) asm volatile("barrier.cluster.wait.acquire.aligned;" ::: "memory");   // the cluster's other CTAs run
+  const int last_left = p.in - c_whole * kQChunk;   // K of a chunk that is not whole
   uint32_t st = ring, st_feed = ring + (DEPTH - 1) * kQStage;
+  int seg_end = 0;              // first tile behind the segment of:
+  float scale = 0.0f;
+  uint16_t* y_lane = nullptr;   // row g of its first tile, token 2 t
+  int64_t ldy = 0;
+  int seg_begin = 0, seg_out = 0;
   for (int round = 0; round < rounds; ++round) {
     const int tile0 = t_first + round * p.round;
     int first, left;
@@ -342,11 +387,18 @@ __global__ void __launch_bounds__(32 * NW, 16 / NW) aq_nvfp4_kernel(const __grid
     if (!p.whole && round > 0) __syncthreads();   // the sums of the round before have been taken
     while (left > 0) {
       const int here = min(left, nc - c);   // chunks of this tile
-      const Nvfp4Seg& sg = tile_seg(p, tile0 + tile);
-      const float scale = *sg.g;
+      if (tile0 + tile >= seg_end) {
+        const Nvfp4Seg& sg = tile_seg(p, tile0 + tile);
+        scale = *sg.g;
+        seg_begin = sg.begin;
+        seg_out = sg.out;
+        seg_end = sg.begin + (sg.out + 15) / 16;
+        ldy = sg.ldy;
+        y_lane = sg.y + (m0 + 2 * t) * ldy + g;
+      }
       uint32_t sa = 0, sb = 0;   // where the rows' scales stand in their pieces
       if (MODE == 1) {
-        const uint32_t r = static_cast<uint32_t>((tile0 + tile - sg.begin) * 16 + g) * static_cast<uint32_t>(p.cols);
+        const uint32_t r = static_cast<uint32_t>((tile0 + tile - seg_begin) * 16 + g) * static_cast<uint32_t>(p.cols);
         sa = r & 15u;
         sb = (r + 8u * static_cast<uint32_t>(p.cols)) & 15u;
       }
@@ -361,56 +413,71 @@ __global__ void __launch_bounds__(32 * NW, 16 / NW) aq_nvfp4_kernel(const __grid
         __syncwarp();
         feed(st_feed);
         st_feed = st;
-        uint32_t sc_a, sc_b;   // four scales of rows g and g + 8
+        uint32_t sc[2][2];   // [row g, g + 8][half]: two scales
         if (MODE == 1) {
           const uint32_t wa = st + at_s + (sa & ~3u), wb = st + at_s + 256 + (sb & ~3u);
-          sc_a = __funnelshift_r(lds32(wa), lds32(wa + 4), (sa & 3u) * 8);
-          sc_b = __funnelshift_r(lds32(wb), lds32(wb + 4), (sb & 3u) * 8);
+          const uint32_t a = __funnelshift_r(lds32(wa), lds32(wa + 4), (sa & 3u) * 8), b = __funnelshift_r(lds32(wb), lds32(wb + 4), (sb & 3u) * 8);
+          sc[0][0] = a, sc[0][1] = a >> 16, sc[1][0] = b, sc[1][1] = b >> 16;
         } else {
-          sc_a = lds32(st + at_s);
-          sc_b = lds32(st + at_s + 128);
+#pragma unroll
+          for (int i = 0; i < 4; ++i) sc[i >> 1][i & 1] = lds16(st + at_s + (i >> 1) * 128 + (i & 1) * 8);
         }
-        if (ca >= c_whole) {   // past the row's end stand the next row's scales
-          const int over = ca * 16 + 4 * t + 4 - p.cols;
-          const uint32_t keep = over <= 0 ? 0xffffffffu : over >= 4 ? 0u : 0xffffffffu >> (8 * over);
-          sc_a &= keep;
-          sc_b &= keep;
+        if (ca >= c_whole) {   // behind a row's scales stand the next row's, or what the layout is filled up with
+#pragma unroll
+          for (int h = 0; h < 2; ++h) {
+            const int over = ca * 16 + (kHalves ? 8 * h + 2 * t : 4 * t + 2 * h) + 2 - p.cols;
+            const uint32_t keep = over <= 0 ? 0xffffu : over == 1 ? 0xffu : 0u;
+            sc[0][h] &= keep;
+            sc[1][h] &= keep;
+          }
         }
-        const uint32_t fa[2] = {f16x2_from_e4m3x2(static_cast<uint16_t>(sc_a)), f16x2_from_e4m3x2(static_cast<uint16_t>(sc_a >> 16))};
-        const uint32_t fb[2] = {f16x2_from_e4m3x2(static_cast<uint16_t>(sc_b)), f16x2_from_e4m3x2(static_cast<uint16_t>(sc_b >> 16))};
         uint32_t xb[NT];
 #pragma unroll
         for (int n = 0; n < NT; ++n) xb[n] = xc + b_at[n];
         float acc[NT][4], odd[4];   // one tile of tokens: two chains, so that a product does not wait for the one before
+        // Up to two tiles of tokens the products of a word of codes stand behind the next word's widening, and the two run side by side
+        // (the loop by itself: 3.9 clocks a word, warp and SM, 4.5 with the products first). With four the products take longest.
+        constexpr bool kBehind = NT <= 2;
+        uint32_t a0[4], a1[4];
+        uint4 b[NT];
+        auto products = [&](bool first) {
 #pragma unroll
-        for (int h = 0; h < 2; ++h) {   // sixteen bytes of codes a row: two blocks
-          const uint4 wa = lds128(st + (at_a ^ (h * 16))), wb = lds128(st + 1024 + (at_a ^ (h * 16)));
+          for (int n = 0; n < NT; ++n) {
+            if (first) mma_f16_first(acc[n], a0, b[n].x, b[n].y);
+            else mma_f16(acc[n], a0, b[n].x, b[n].y);
+          }
+          if (NT == 1) {
+            if (first) mma_f16_first(odd, a1, b[0].z, b[0].w);
+            else mma_f16(odd, a1, b[0].z, b[0].w);
+          } else {
+#pragma unroll
+            for (int n = 0; n < NT; ++n) mma_f16(acc[n], a1, b[n].z, b[n].w);
+          }
+        };
+        auto half = [&](auto which) {   // sixteen bytes of codes a row: two blocks
+          constexpr int h = decltype(which)::value;
+          const uint4 wa = lds128(st + (at_a ^ (h * (kHalves ? 64 : 16)))), wb = lds128(st + 1024 + (at_a ^ (h * (kHalves ? 64 : 16))));
           const uint32_t pa[4] = {wa.x, wa.y, wa.z, wa.w}, pb[4] = {wb.x, wb.y, wb.z, wb.w};
+          const uint32_t fa = f16x2_from_e4m3x2(static_cast<uint16_t>(sc[0][h])), fb = f16x2_from_e4m3x2(static_cast<uint16_t>(sc[1][h]));
 #pragma unroll
           for (int j = 0; j < 4; ++j) {
-            uint4 b[NT];
-#pragma unroll
-            for (int n = 0; n < NT; ++n) b[n] = lds128(xb[n] + (h * 4 + j) * 16);
-            const uint32_t s_a = __byte_perm(fa[h], 0, j < 2 ? 0x1010 : 0x3232), s_b = __byte_perm(fb[h], 0, j < 2 ? 0x1010 : 0x3232);
+            const uint32_t s_a = __byte_perm(fa, 0, j < 2 ? 0x1010 : 0x3232), s_b = __byte_perm(fb, 0, j < 2 ? 0x1010 : 0x3232);
             uint32_t ha[4], hb[4];
             f16_from_e2m1x8(pa[j], ha);
             f16_from_e2m1x8(pb[j], hb);
-            const uint32_t a0[4] = {hmul2(ha[0], s_a), hmul2(hb[0], s_b), hmul2(ha[1], s_a), hmul2(hb[1], s_b)};
-            const uint32_t a1[4] = {hmul2(ha[2], s_a), hmul2(hb[2], s_b), hmul2(ha[3], s_a), hmul2(hb[3], s_b)};
+            const uint32_t n0[4] = {hmul2(ha[0], s_a), hmul2(hb[0], s_b), hmul2(ha[1], s_a), hmul2(hb[1], s_b)};
+            const uint32_t n1[4] = {hmul2(ha[2], s_a), hmul2(hb[2], s_b), hmul2(ha[3], s_a), hmul2(hb[3], s_b)};
+            if (kBehind && h + j) products(h == 0 && j == 1);
 #pragma unroll
-            for (int n = 0; n < NT; ++n) {
-              if (h == 0 && j == 0) mma_f16_first(acc[n], a0, b[n].x, b[n].y);
-              else mma_f16(acc[n], a0, b[n].x, b[n].y);
-            }
-            if (NT == 1) {
-              if (h == 0 && j == 0) mma_f16_first(odd, a1, b[0].z, b[0].w);
-              else mma_f16(odd, a1, b[0].z, b[0].w);
-            } else {
+            for (int i = 0; i < 4; ++i) a0[i] = n0[i], a1[i] = n1[i];
 #pragma unroll
-              for (int n = 0; n < NT; ++n) mma_f16(acc[n], a1, b[n].z, b[n].w);
-            }
+            for (int n = 0; n < NT; ++n) b[n] = lds128(xb[n] + (h * 4 + j) * 16);
+            if (!kBehind) products(h == 0 && j == 0);
           }
-        }
+        };
+        half(std::integral_constant<int, 0>());
+        if (!kHalves || ca < c_whole || last_left > kQChunk / 2) half(std::integral_constant<int, 1>());
+        if (kBehind) products(false);
 #pragma unroll
         for (int n = 0; n < NT; ++n) {
           const float2 f = lds64f(bk + 32 * n);
@@ -429,6 +496,7 @@ __global__ void __launch_bounds__(32 * NW, 16 / NW) aq_nvfp4_kernel(const __grid
           for (int i = 0; i < 4; ++i) mine[(n * 8 + 2 * t + (i & 1)) * kQPart + g + (i >> 1) * 8] = tot[n][i];
       } else {
         const uint32_t to = S > 1 ? cluster_map(recv + (round & 1) * recv_buf + rank * recv_src + (tile / S) * 16 * p.tokens, tile % S) : 0;
+        const int row0 = (tile0 + tile - seg_begin) * 16, rows = seg_out - row0 - g;   // from row g on
 #pragma unroll
         for (int n = 0; n < NT; ++n)
 #pragma unroll
@@ -436,7 +504,7 @@ __global__ void __launch_bounds__(32 * NW, 16 / NW) aq_nvfp4_kernel(const __grid
             const int m = n * 8 + 2 * t + (i & 1), r = g + (i >> 1) * 8;
             if (m >= M) continue;
             if (S > 1) asm volatile("st.shared::cluster.f32 [%0], %1;" ::"r"(to + (m * 16 + r) * 4), "f"(tot[n][i]) : "memory");
-            else put(tile0 + tile, m, r, tot[n][i]);
+            else if ((i >> 1) * 8 < rows) y_lane[(n * 8 + (i & 1)) * ldy + row0 + (i >> 1) * 8] = f32_to_bf16_rn(tot[n][i]);
           }
       }
       left -= here;
@@ -448,19 +516,22 @@ __global__ void __launch_bounds__(32 * NW, 16 / NW) aq_nvfp4_kernel(const __grid
     }
     if (!p.whole) {
       __syncthreads();
-      const int n = min(p.round, t_last - tile0), units = n * nc;
-      for (int e = tid; e < n * 16 * M; e += kQThreads) {
-        const int m = e / (n * 16), r = e - m * (n * 16), i = r >> 4;   // token-major, the tiles' rows innermost
-        const int u0 = i * nc, u1 = u0 + nc;
-        const float* at = part + i * kPart + m * kQPart + (r & 15);
-        float v = 0.0f;
+      const int n = min(p.round, t_last - tile0), units = n * nc, pairs = (M + 1) / 2;
+      const float inverse = units ? 1.0f / static_cast<float>(units) : 0.0f;
+      for (int e = warp; e < n * pairs; e += NW) {   // a warp: two tokens of a tile
+        const int i = e / pairs, m = 2 * (e - i * pairs) + (lane >> 4), u0 = i * nc, u1 = u0 + nc;
         // from the first run that ends behind u0, on while runs begin before u1 (a run may be empty)
-        for (int w = units ? (NW * (u0 + 1) + units - 1) / units - 1 : NW; w < NW && (units * w) / NW < u1; ++w)
-          if ((units * w) / NW < (units * (w + 1)) / NW) v += at[w * kPart];
+        int w = units ? max(0, static_cast<int>(static_cast<float>(NW * u0) * inverse) - 1) : NW;
+        while (w < NW && (units * (w + 1)) / NW <= u0) ++w;
+        const float* at = part + (i + w) * kPart + m * kQPart + (lane & 15);
+        float v = 0.0f;
+        for (; w < NW && (units * w) / NW < u1; ++w, at += kPart)
+          if (m < M && (units * w) / NW < (units * (w + 1)) / NW) v += *at;
+        if (m >= M) continue;
         if (S > 1) {
-          asm volatile("st.shared::cluster.f32 [%0], %1;" ::"r"(cluster_map(recv + (round & 1) * recv_buf + rank * recv_src + (i / S) * 16 * p.tokens + m * 16 + (r & 15), i % S)), "f"(v) : "memory");
+          asm volatile("st.shared::cluster.f32 [%0], %1;" ::"r"(cluster_map(recv + (round & 1) * recv_buf + rank * recv_src + (i / S) * 16 * p.tokens + m * 16 + (lane & 15), i % S)), "f"(v) : "memory");
         } else {
-          put(tile0 + i, m, r & 15, v);
+          put(tile0 + i, m, lane & 15, v);
         }
       }
     }
@@ -490,8 +561,12 @@ size_t nvfp4_smem(int NT, int M, int tok, int tiles, const Nvfp4Plan& c) {
 }
 
 // Cluster size, warps a CTA, tiles a round and how the warps share them, by an estimate of the call's time in ns: the chunks that the
-// busiest warp takes, x into every CTA's shared memory, and what a round and an exchange cost. CTAs of eight warps that leave half an SM
-// free may begin under the tail of the kernel before.
+// busiest warp takes, x into every CTA's shared memory, and what a round and an exchange cost. Its figures are fitted to 28 products
+// timed under every plan (M 1 to 32, K 1024 to 21504, rows 1152 to 262144); what it picks is within 1 % of the fastest of them on
+// average. CTAs of eight warps that leave half an SM free may begin under the tail of the kernel before. Some of them, us (S, runs or
+// whole tiles, warps): 21504 rows of 5376, M=8: (1, runs, 16) 19.5, (1, whole, 16) 22.5, (4, whole, 16) 19.7, (1, runs, 8) 48; 262144
+// rows of 1152, M=5: (1, whole, 16) 34.9, (1, whole, 8) 44; 1536 rows of 1152, M=1: (1, runs, 8) 3.8, (1, runs, 16) 4.5, (2, runs, 8)
+// 4.6; 5376 rows of 21504, M=8: (8, whole, 16) 21.0, (4, runs, 16) 22.8, (1, whole, 16) 176.
 bool plan_nvfp4(int tiles, int in, int M, int tok, const ServeDev& dev, const int (&fit)[4], Nvfp4Plan* best) {
   const int NT = std::max(1, tok / 8), chunks = (in + kQChunk - 1) / kQChunk;
   const size_t half = (dev.smem_optin + 1024) / 2 - 1024;
@@ -511,7 +586,7 @@ bool plan_nvfp4(int tiles, int in, int M, int tok, const ServeDev& dev, const in
       for (bool fits = false; !fits; ++rounds) {   // the fewest rounds and the deepest ring that fit
         c.round = (each + rounds - 1) / rounds;
         if (c.whole && rounds > 1) c.round = (c.round + c.warps - 1) / c.warps * c.warps;
-        for (c.depth = NT > 1 && c.warps == 8 ? 2 : 3; c.depth >= (NT > 1 ? 2 : 3) && !fits; --c.depth) fits = (c.smem = nvfp4_smem(NT, M, tok, tiles, c)) <= room;
+        for (c.depth = NT > 1 && c.warps == 8 ? 2 : 3; c.depth >= (NT > 1 || c.warps == 16 ? 2 : 3) && !fits; --c.depth) fits = (c.smem = nvfp4_smem(NT, M, tok, tiles, c)) <= room;
         ++c.depth;
         if (fits || c.round <= (c.whole ? c.warps : 1)) break;
       }
@@ -519,9 +594,9 @@ bool plan_nvfp4(int tiles, int in, int M, int tok, const ServeDev& dev, const in
       rounds = (each + c.round - 1) / c.round;
       const int ctas = c.clusters * S;
       const double mine = c.whole ? (c.round + c.warps - 1) / c.warps * c.slice : (c.round * c.slice + c.warps - 1) / c.warps;   // chunks of a warp and round
-      const double chunk = std::max(2304.0 / std::min(60.0, 6600.0 / ctas), (NT == 1 ? 55.0 : NT == 2 ? 75.0 : 130.0) * (c.warps == 8 ? 1.3 : 1.0));
-      const double t = mine * rounds * c.warps * chunk + (c.warps == 8 ? 500.0 : 2000.0) + static_cast<double>(c.slice) * M * (c.warps == 8 ? 20.0 : 15.0) +
-                       (S > 1 ? 1000.0 * rounds + each * 64.0 * M / 20.0 : 0.0) + (c.whole ? 0.0 : 300.0 * rounds + each * 14.0 * M);
+      const double chunk = std::max(2304.0 / std::min(47.0, 6300.0 / ctas), (NT == 1 ? 51.0 : NT == 2 ? 73.0 : 94.0) * (c.warps == 8 ? 1.34 : 1.0));
+      const double t = mine * rounds * c.warps * chunk + (c.warps == 8 ? 1050.0 : 1500.0) + static_cast<double>(c.slice) * M * (c.warps == 8 ? 15.0 : 12.5) +
+                       (S > 1 ? 790.0 * rounds + each * 6.9 * M : 0.0) + (c.whole ? 0.0 : 550.0 * rounds + each * 27.5 * M);
       if (!found || t < least) {
         least = t;
         *best = c;
@@ -570,7 +645,10 @@ cudaError_t launch_nvfp4(const Nvfp4Params& p, dim3 grid, size_t smem, const Ser
 }
 template <int MODE>
 cudaError_t launch_nvfp4(const Nvfp4Params& p, dim3 grid, const Nvfp4Plan& c, int tok, const ServeDev& dev, cudaStream_t st) {
-  if (tok <= 8) return c.warps == 8 ? launch_nvfp4<1, 3, 8, MODE>(p, grid, c.smem, dev, st) : launch_nvfp4<1, 3, 16, MODE>(p, grid, c.smem, dev, st);
+  if (tok <= 8) {
+    if (c.warps == 8) return launch_nvfp4<1, 3, 8, MODE>(p, grid, c.smem, dev, st);
+    return c.depth == 3 ? launch_nvfp4<1, 3, 16, MODE>(p, grid, c.smem, dev, st) : launch_nvfp4<1, 2, 16, MODE>(p, grid, c.smem, dev, st);
+  }
   if (tok == 16) {
     if (c.warps == 8) return launch_nvfp4<2, 2, 8, MODE>(p, grid, c.smem, dev, st);
     return c.depth == 3 ? launch_nvfp4<2, 3, 16, MODE>(p, grid, c.smem, dev, st) : launch_nvfp4<2, 2, 16, MODE>(p, grid, c.smem, dev, st);
