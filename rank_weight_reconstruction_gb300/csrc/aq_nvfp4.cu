@@ -346,24 +346,37 @@ __global__ void __launch_bounds__(32 * NW, 16 / NW) aq_nvfp4_kernel(const __grid
   }
 
   // ---- rounds ----
-  auto put = [&](int tile, int m, int r, float v) {   // one output: row r of a tile
+  auto put = [&](int tile, int m, int r, const float4& v) {   // four outputs: rows r.. of a tile
     const Nvfp4Seg& sg = tile_seg(p, tile);
     const int row = (tile - sg.begin) * 16 + r;
-    if (row < sg.out) sg.y[(m0 + m) * sg.ldy + row] = f32_to_bf16_rn(v);
+    uint16_t* to = sg.y + (m0 + m) * sg.ldy + row;
+    const uint16_t h[4] = {f32_to_bf16_rn(v.x), f32_to_bf16_rn(v.y), f32_to_bf16_rn(v.z), f32_to_bf16_rn(v.w)};
+    if (row + 4 <= sg.out && (reinterpret_cast<uintptr_t>(to) & 7) == 0) {
+      *reinterpret_cast<uint2*>(to) = make_uint2(h[0] | static_cast<uint32_t>(h[1]) << 16, h[2] | static_cast<uint32_t>(h[3]) << 16);
+    } else {
+#pragma unroll
+      for (int i = 0; i < 4; ++i)
+        if (row + i < sg.out) to[i] = h[i];
+    }
   };
+  auto add = [](float4& v, const float* at) {
+    const float4 x = *reinterpret_cast<const float4*>(at);
+    v.x += x.x, v.y += x.y, v.z += x.z, v.w += x.w;
+  };
+  const int eights = (M + 7) / 8;   // the sums that warps share go by eight tokens of a tile, four rows a lane
+  const int l_m = lane >> 2, l_r = 4 * (lane & 3);
   // Tile i of a round is finished by CTA i % S of the cluster, as its tile i / S: the sums of all CTAs with a part of K in their order.
   const int parts = (p.in + kQChunk * p.slice - 1) / (kQChunk * p.slice);
   auto finish = [&](int round) {
     const float* from = recv + (round & 1) * recv_buf;
     const int n = min(p.round, t_last - t_first - round * p.round), mine = (n - rank + S - 1) / S;
-    const int pairs = (M + 1) / 2;   // a warp: two tokens of a tile
-    for (int e = warp; e < mine * pairs; e += NW) {
-      const int i = e / pairs, m = 2 * (e - i * pairs) + (lane >> 4);
+    for (int e = warp; e < mine * eights; e += NW) {
+      const int i = e / eights, m = 8 * (e - i * eights) + l_m;
       if (m >= M) continue;
-      const float* at = from + i * 16 * p.tokens + m * 16 + (lane & 15);
-      float v = 0.0f;
-      for (int s = 0; s < parts; ++s) v += at[s * recv_src];
-      put(t_first + round * p.round + i * S + rank, m, lane & 15, v);
+      const float* at = from + i * 16 * p.tokens + m * 16 + l_r;
+      float4 v = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+      for (int s = 0; s < parts; ++s) add(v, at + s * recv_src);
+      put(t_first + round * p.round + i * S + rank, m, l_r, v);
     }
   };
   uint32_t b_at[NT];
@@ -516,22 +529,23 @@ __global__ void __launch_bounds__(32 * NW, 16 / NW) aq_nvfp4_kernel(const __grid
     }
     if (!p.whole) {
       __syncthreads();
-      const int n = min(p.round, t_last - tile0), units = n * nc, pairs = (M + 1) / 2;
+      const int n = min(p.round, t_last - tile0), units = n * nc;
       const float inverse = units ? 1.0f / static_cast<float>(units) : 0.0f;
-      for (int e = warp; e < n * pairs; e += NW) {   // a warp: two tokens of a tile
-        const int i = e / pairs, m = 2 * (e - i * pairs) + (lane >> 4), u0 = i * nc, u1 = u0 + nc;
+      for (int e = warp; e < n * eights; e += NW) {
+        const int i = e / eights, m = 8 * (e - i * eights) + l_m, u0 = i * nc, u1 = u0 + nc;
         // from the first run that ends behind u0, on while runs begin before u1 (a run may be empty)
         int w = units ? max(0, static_cast<int>(static_cast<float>(NW * u0) * inverse) - 1) : NW;
         while (w < NW && (units * (w + 1)) / NW <= u0) ++w;
-        const float* at = part + (i + w) * kPart + m * kQPart + (lane & 15);
-        float v = 0.0f;
+        const float* at = part + (i + w) * kPart + m * kQPart + l_r;
+        float4 v = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
         for (; w < NW && (units * w) / NW < u1; ++w, at += kPart)
-          if (m < M && (units * w) / NW < (units * (w + 1)) / NW) v += *at;
+          if (m < M && (units * w) / NW < (units * (w + 1)) / NW) add(v, at);
         if (m >= M) continue;
         if (S > 1) {
-          asm volatile("st.shared::cluster.f32 [%0], %1;" ::"r"(cluster_map(recv + (round & 1) * recv_buf + rank * recv_src + (i / S) * 16 * p.tokens + m * 16 + (lane & 15), i % S)), "f"(v) : "memory");
+          asm volatile("st.shared::cluster.v4.f32 [%0], {%1, %2, %3, %4};" ::"r"(cluster_map(recv + (round & 1) * recv_buf + rank * recv_src + (i / S) * 16 * p.tokens + m * 16 + l_r, i % S)),
+                       "f"(v.x), "f"(v.y), "f"(v.z), "f"(v.w) : "memory");
         } else {
-          put(tile0 + i, m, lane & 15, v);
+          put(tile0 + i, m, l_r, v);
         }
       }
     }
@@ -564,9 +578,9 @@ size_t nvfp4_smem(int NT, int M, int tok, int tiles, const Nvfp4Plan& c) {
 // busiest warp takes, x into every CTA's shared memory, and what a round and an exchange cost. Its figures are fitted to 28 products
 // timed under every plan (M 1 to 32, K 1024 to 21504, rows 1152 to 262144); what it picks is within 1 % of the fastest of them on
 // average. CTAs of eight warps that leave half an SM free may begin under the tail of the kernel before. Some of them, us (S, runs or
-// whole tiles, warps): 21504 rows of 5376, M=8: (1, runs, 16) 19.5, (1, whole, 16) 22.5, (4, whole, 16) 19.7, (1, runs, 8) 48; 262144
+// whole tiles, warps): 21504 rows of 5376, M=8: (1, runs, 16) 18.5, (1, whole, 16) 22.5, (4, whole, 16) 19.7, (1, runs, 8) 48; 262144
 // rows of 1152, M=5: (1, whole, 16) 34.9, (1, whole, 8) 44; 1536 rows of 1152, M=1: (1, runs, 8) 3.8, (1, runs, 16) 4.5, (2, runs, 8)
-// 4.6; 5376 rows of 21504, M=8: (8, whole, 16) 21.0, (4, runs, 16) 22.8, (1, whole, 16) 176.
+// 4.6; 5376 rows of 21504, M=8: (8, whole, 16) 20.9, (4, runs, 16) 22.0, (1, whole, 16) 176.
 bool plan_nvfp4(int tiles, int in, int M, int tok, const ServeDev& dev, const int (&fit)[4], Nvfp4Plan* best) {
   const int NT = std::max(1, tok / 8), chunks = (in + kQChunk - 1) / kQChunk;
   const size_t half = (dev.smem_optin + 1024) / 2 - 1024;
@@ -594,9 +608,9 @@ bool plan_nvfp4(int tiles, int in, int M, int tok, const ServeDev& dev, const in
       rounds = (each + c.round - 1) / c.round;
       const int ctas = c.clusters * S;
       const double mine = c.whole ? (c.round + c.warps - 1) / c.warps * c.slice : (c.round * c.slice + c.warps - 1) / c.warps;   // chunks of a warp and round
-      const double chunk = std::max(2304.0 / std::min(47.0, 6300.0 / ctas), (NT == 1 ? 51.0 : NT == 2 ? 73.0 : 94.0) * (c.warps == 8 ? 1.34 : 1.0));
-      const double t = mine * rounds * c.warps * chunk + (c.warps == 8 ? 1050.0 : 1500.0) + static_cast<double>(c.slice) * M * (c.warps == 8 ? 15.0 : 12.5) +
-                       (S > 1 ? 790.0 * rounds + each * 6.9 * M : 0.0) + (c.whole ? 0.0 : 550.0 * rounds + each * 27.5 * M);
+      const double chunk = std::max(2304.0 / std::min(47.0, 6300.0 / ctas), (NT == 1 ? 49.0 : NT == 2 ? 65.0 : 82.0) * (c.warps == 8 ? 1.34 : 1.0));
+      const double t = mine * rounds * c.warps * chunk + (c.warps == 8 ? 1050.0 : 1650.0) + static_cast<double>(c.slice) * M * (c.warps == 8 ? 20.0 : 18.0) +
+                       (S > 1 ? 900.0 * rounds + each * 5.6 * M : 0.0) + (c.whole ? 0.0 : 650.0 * rounds + each * 11.0 * M);
       if (!found || t < least) {
         least = t;
         *best = c;
