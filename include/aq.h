@@ -256,7 +256,7 @@ aq_status aq_precompute_nvfp4(const aq_theta* th, void* q, int64_t ldq, void* sf
  *   y[m, o] = RN_bf16( g * sum over k of E2M1(q[o, k]) * E4M3(sf[o, k / 16]) * x[m, k] )
  * q, ldq, sf, sf_layout and global_scale as there; in a multiple of 16 up to AQ_NVFP4_MAX_IN. Code times block scale is exact;
  * x enters as f16 scaled by a power of two for each token and a part of K, so that elements below 2^-32 of the largest there lose
- * bits; sums are fp32, in an order that the sizes fix; one rounding at the end. A block scale that is NaN makes its row NaN, an
+ * bits; sums are fp32, in an order that the sizes and the device fix; one rounding at the end. A block scale that is NaN makes its row NaN, an
  * infinity or NaN in x its token alone.
  * x [M, in] bf16, 16-byte aligned, ldx a multiple of 8. y[i] [M, out] bf16 with any row stride (aligned to its elements),
  * apart from every input. M == 0 is a no-op. Any M is served; the weights are read once for every 32 tokens (fewer where
@@ -615,8 +615,9 @@ aq_status aq_token_logprobs(const void* logits, int64_t ld, int64_t rows, int32_
 
 /* Gradient of the above with respect to the logits, from what it returned and the gradients of logprob (with its tokens), entropy
  * and lse, fp32 [rows] each, NULL where there is none:
- *   dlogits = scale * ( dlogprob ([v = token] - p) - dentropy p (log p + entropy) + dlse p ),  p = e^(z - lse)
- * in the logits' type, rounded once. A token outside the vocabulary has no gradient of its logprob; a row with lse -inf gives zeros.
+ *   dlogits = scale * ( dlogprob ([v = token] - p) - dentropy p (log p + entropy) + dlse p ),  p = e^(z - lse), at most 1
+ * in the logits' type, rounded once. lse is fp32: p is off by 2^-24 |lse| of itself besides. A token outside the vocabulary has no
+ * gradient of its logprob; a row with lse -inf gives zeros.
  * dlogits may be logits (same pointer and stride); otherwise it lies apart from every input. */
 aq_status aq_token_logprobs_backward(const void* logits, int64_t ld, int64_t rows, int32_t vocab, int32_t type, const int32_t* tokens,
                                      float scale, const float* lse, const float* entropy, const float* dlogprob, const float* dentropy,

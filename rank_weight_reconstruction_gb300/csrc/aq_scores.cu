@@ -52,6 +52,11 @@ __device__ __forceinline__ float max_nan(float a, float b) {
   asm("max.NaN.f32 %0, %1, %2;" : "=f"(r) : "f"(a), "f"(b));
   return r;
 }
+__device__ __forceinline__ float min_nan(float a, float b) {
+  float r;
+  asm("min.NaN.f32 %0, %1, %2;" : "=f"(r) : "f"(a), "f"(b));
+  return r;
+}
 
 __device__ __forceinline__ void fadd2_rn(float& d0, float& d1, float a0, float a1, float b0, float b1) {
   asm("{\n\t.reg .b64 ra, rb, rd;\n\tmov.b64 ra, {%2, %3};\n\tmov.b64 rb, {%4, %5};\n\tadd.rn.f32x2 rd, ra, rb;\n\tmov.b64 {%0, %1}, rd;\n\t}"
@@ -160,18 +165,24 @@ struct Row {
 
 // ---- sums ----
 // Weights are 2^(x c - ref), c = scale log2(e), with ref the rounded m c, so that a word costs one fused product and ref's rounding
-// cancels where log probabilities are taken. Where m c leaves the range (a row of nothing but a type's lowest value) they are
-// 2^((x - m) c).
+// cancels where log probabilities are taken. Beyond 2^26 that rounding passes 2, and soon 2^128 of a weight: there (a row of nothing but
+// a type's lowest value, scales far from one) they are 2^((x - m) c).
 struct Sums {
   float m = -INFINITY, ref = 0.0f;   // ref: 0 while m is -inf
   float s0 = 0.0f, s1 = 0.0f, a0 = 0.0f, a1 = 0.0f;
-  __device__ __forceinline__ bool wild() const { return !(fabsf(ref) < 1e37f); }
+  static __device__ __forceinline__ bool beyond(float r) { return !(fabsf(r) < 0x1p26f); }
+  // Not one product with the differences below: to the same largest value they are 0.
+  static __device__ __forceinline__ float ref_of(float m, float c) { return m == -INFINITY ? 0.0f : __fmul_rn(m, c); }
+  __device__ __forceinline__ bool wild() const { return beyond(ref); }
   // To a new largest value. Differences below -1000 are as good as -inf, whose product with 0 would be NaN.
   __device__ __forceinline__ void rise(float to, float c) {
     const float was = m, from = ref;
     m = to;
-    ref = to == -INFINITY ? 0.0f : to * c;
-    const float d = was == -INFINITY ? -1000.0f : fmaxf(wild() ? (was - to) * c : from - ref, -1000.0f), f = ex2(d);
+    ref = ref_of(to, c);
+    float d = from - ref;
+    if (beyond(from) || wild()) d = !wild() ? fmaf(was, c, -ref) : beyond(from) ? (was - to) * c : fmaf(-to, c, from);
+    d = was == -INFINITY ? -1000.0f : fmaxf(d, -1000.0f);
+    const float f = ex2(d);
     a0 = f * fmaf(s0, d, a0);
     a1 = f * fmaf(s1, d, a1);
     s0 *= f;
@@ -310,7 +321,7 @@ __device__ __forceinline__ Sums join(const float* m, const float* s, const float
   Sums one;
   if (i < n) {
     one.m = m[i];
-    one.ref = one.m == -INFINITY ? 0.0f : one.m * c;
+    one.ref = Sums::ref_of(one.m, c);
     one.s0 = s[i];
     one.a0 = a[i];
   }
@@ -643,7 +654,7 @@ __global__ void __launch_bounds__(kScoreThreads, 4) aq_scores_grad_kernel(const 
   // dx = p (A + B d) + [v = token] g scale, with d = log2 p
   const float A = p.scale * (gl - g - (p.dentropy ? gh * p.entropy[r] : 0.0f)), B = -p.scale * gh * kLn2, hit = g * p.scale;
   auto grad = [&](float x) {
-    const float d = max_nan(fmaf(x, p.scale, -lse) * kLog2e, -1000.0f);
+    const float d = min_nan(max_nan(fmaf(x, p.scale, -lse) * kLog2e, -1000.0f), 0.0f);   // lse is rounded: no p above one
     return none ? 0.0f : ex2(d) * fmaf(B, d, A);
   };
   const bool whole = ((reinterpret_cast<uintptr_t>(row) ^ reinterpret_cast<uintptr_t>(out)) & 15) == 0;

@@ -134,7 +134,7 @@ def call_scores(lib, x=A, ld=100, rows=3, vocab=100, type=0, tokens=0x1000, scal
 LOGITS = [
     (dict(rows=-1), b.AQ_ERR_SHAPE), (dict(vocab=0), b.AQ_ERR_SHAPE), (dict(vocab=(1 << 30) + 1), b.AQ_ERR_SHAPE), (dict(type=2), b.AQ_ERR_INVALID_ARG),
     (dict(scale=0.0), b.AQ_ERR_INVALID_ARG), (dict(scale=-1.0), b.AQ_ERR_INVALID_ARG), (dict(scale=float("nan")), b.AQ_ERR_INVALID_ARG),
-    (dict(scale=float("inf")), b.AQ_ERR_INVALID_ARG), (dict(x=0), b.AQ_ERR_INVALID_ARG), (dict(ld=99), b.AQ_ERR_SHAPE), (dict(x=A + 2), b.AQ_ERR_ALIGNMENT),
+    (dict(scale=float("inf")), b.AQ_ERR_INVALID_ARG), (dict(scale=9e-31), b.AQ_ERR_INVALID_ARG), (dict(scale=1.1e30), b.AQ_ERR_INVALID_ARG), (dict(x=0), b.AQ_ERR_INVALID_ARG), (dict(ld=99), b.AQ_ERR_SHAPE), (dict(x=A + 2), b.AQ_ERR_ALIGNMENT),
     (dict(x=A + 1, type=1), b.AQ_ERR_ALIGNMENT),
 ]
 
