@@ -72,6 +72,11 @@ __device__ __forceinline__ void f16_from_e2m1x8(uint32_t w, uint32_t (&h)[4]) {
       : "=r"(h[0]), "=r"(h[1]), "=r"(h[2]), "=r"(h[3])
       : "r"(w));
 }
+__device__ __forceinline__ uint32_t max_u16x2(uint32_t a, uint32_t b) {
+  uint32_t r;
+  asm("max.u16x2 %0, %1, %2;" : "=r"(r) : "r"(a), "r"(b));
+  return r;
+}
 __device__ __forceinline__ uint32_t hmul2(uint32_t a, uint32_t b) {
   uint32_t r;
   asm("mul.rn.f16x2 %0, %1, %2;" : "=r"(r) : "r"(a), "r"(b));
@@ -293,49 +298,61 @@ __global__ void __launch_bounds__(32 * NW, 16 / NW) aq_nvfp4_kernel(const __grid
   // Weights are not written by a kernel that is still running, so the stream starts before the previous kernel ends.
   next_run();
   for (int i = 0; i < DEPTH - 1; ++i) feed(ring + i * kQStage);
+  // A warp's first piece of x, [token][chunk] from a place of the CTA's own on, and the way from one to its next.
+  const int items = nc * M;
+  int m = 0, c = 0, by_m = 0, by_c = 0;
+  if (items) {
+    const int at = static_cast<int>(__umulhi(blockIdx.x * 0x9e3779b9u, static_cast<uint32_t>(items))) + warp;
+    m = at / nc;
+    c = at - m * nc;
+    by_m = NW / nc;
+    by_c = NW - by_m * nc;
+    while (m >= M) m -= M;
+  }
   pdl_wait_prior_grid();
   pdl_launch_dependents();
 
   // ---- x of this slice: f16, [chunk][token][t][word of codes][8], the lanes' rows of 128 bytes 144 apart, so that what eight lanes read
   // together lies in eight places of the banks. A warp takes a chunk of a token at a time; the CTAs start at different ones, or all would ask the same
   // part of L2 at once ----
-  const int items = nc * M;
   const uint32_t x_chunk = static_cast<uint32_t>(M) * kQRow;
   {
     const uint32_t x_lane = xs + (kHalves ? ((lane >> 2) & 3) * 144 + (lane >> 4) * 64 + (lane & 3) * 16 : (lane >> 3) * 144 + (lane & 7) * 16);
-    const int turn = items ? static_cast<int>((blockIdx.x * 11u) % static_cast<uint32_t>(items)) : 0;
     constexpr int kBatch = 8;   // loads in flight
     for (int i0 = warp; i0 < items; i0 += kBatch * NW) {
       uint4 r[kBatch];
       int mc[kBatch];
 #pragma unroll
       for (int j = 0; j < kBatch; ++j) {
-        const int i = i0 + j * NW;
-        int it = i + turn;
-        it = it >= items ? it - items : it;
-        const int m = it / nc, c = it - m * nc, k = (c_first + c) * kQChunk + lane * 8;
-        mc[j] = i < items ? (m << 16) | c : -1;
+        const int k = (c_first + c) * kQChunk + lane * 8;
+        const bool there = i0 + j * NW < items;
+        mc[j] = there ? (m << 16) | c : -1;
         r[j] = make_uint4(0, 0, 0, 0);
-        if (i < items && k < p.in) r[j] = *reinterpret_cast<const uint4*>(p.x + (m0 + m) * p.ldx + k);
+        if (there && k < p.in) r[j] = *reinterpret_cast<const uint4*>(p.x + (m0 + m) * p.ldx + k);
+        m += by_m;
+        c += by_c;
+        if (c >= nc) {
+          c -= nc;
+          ++m;
+        }
+        while (m >= M) m -= M;   // by_m may pass M: a slice of few chunks of few tokens
       }
 #pragma unroll
       for (int j = 0; j < kBatch; ++j) {
         if (mc[j] < 0) continue;
         const int m = mc[j] >> 16, c = mc[j] & 0xffff;
         const uint32_t w[4] = {r[j].x, r[j].y, r[j].z, r[j].w};
-        uint32_t most = 0;
-#pragma unroll
-        for (int i = 0; i < 4; ++i) {   // the largest finite magnitude
-          const uint32_t lo = w[i] & 0x7fffu, hi = (w[i] >> 16) & 0x7fffu;
-          most = max(most, max(lo < 0x7f80u ? lo : 0u, hi < 0x7f80u ? hi : 0u));
-        }
+        // The largest magnitude. A token with an infinity or a NaN has no finite output, so what becomes of its numbers is all one.
+        uint32_t most = max_u16x2(max_u16x2(w[0] & 0x7fff7fffu, w[1] & 0x7fff7fffu), max_u16x2(w[2] & 0x7fff7fffu, w[3] & 0x7fff7fffu));
+        most = max(most & 0xffffu, most >> 16);
         const int e = static_cast<int>(__reduce_max_sync(0xffffffffu, most) >> 7) - 127;   // -127: zeros and numbers below the normal ones
         const int lift = min(15 - e, 120);
         const float up = __uint_as_float(static_cast<uint32_t>(lift + 127) << 23);
         uint32_t h[4];
 #pragma unroll
         for (int i = 0; i < 4; ++i) {
-          const float lo = __uint_as_float(w[i] << 16) * up, hi = __uint_as_float(w[i] & 0xffff0000u) * up;
+          float lo, hi;
+          fmul2_rn(lo, hi, __uint_as_float(w[i] << 16), __uint_as_float(w[i] & 0xffff0000u), up, up);
           asm("cvt.rn.f16x2.f32 %0, %1, %2;" : "=r"(h[i]) : "f"(hi), "f"(lo));
         }
         asm volatile("st.shared.v4.u32 [%0], {%1, %2, %3, %4};" ::"r"(x_lane + c * x_chunk + m * kQRow), "r"(h[0]), "r"(h[1]), "r"(h[2]), "r"(h[3]) : "memory");
@@ -578,8 +595,8 @@ size_t nvfp4_smem(int NT, int M, int tok, int tiles, const Nvfp4Plan& c) {
 // busiest warp takes, x into every CTA's shared memory, and what a round and an exchange cost. Its figures are fitted to 28 products
 // timed under every plan (M 1 to 32, K 1024 to 21504, rows 1152 to 262144); what it picks is within 1 % of the fastest of them on
 // average. CTAs of eight warps that leave half an SM free may begin under the tail of the kernel before. Some of them, us (S, runs or
-// whole tiles, warps): 21504 rows of 5376, M=8: (1, runs, 16) 18.5, (1, whole, 16) 22.5, (4, whole, 16) 19.7, (1, runs, 8) 48; 262144
-// rows of 1152, M=5: (1, whole, 16) 34.9, (1, whole, 8) 44; 1536 rows of 1152, M=1: (1, runs, 8) 3.8, (1, runs, 16) 4.5, (2, runs, 8)
+// whole tiles, warps): 21504 rows of 5376, M=8: (1, runs, 16) 17.5, (1, whole, 16) 22, (4, whole, 16) 20, (1, runs, 8) 48; 262144
+// rows of 1152, M=5: (1, whole, 16) 34.7, (1, whole, 8) 44; 1536 rows of 1152, M=1: (1, runs, 8) 3.8, (1, runs, 16) 4.5, (2, runs, 8)
 // 4.6; 5376 rows of 21504, M=8: (8, whole, 16) 20.9, (4, runs, 16) 22.0, (1, whole, 16) 176.
 bool plan_nvfp4(int tiles, int in, int M, int tok, const ServeDev& dev, const int (&fit)[4], Nvfp4Plan* best) {
   const int NT = std::max(1, tok / 8), chunks = (in + kQChunk - 1) / kQChunk;
