@@ -8,12 +8,18 @@
 // operand, the tokens as its 8 columns. x enters as f16 too, each token's chunk of 256 K scaled by the power of two that
 // brings its largest element to at least 2^15: an element down to 2^-32 of the largest keeps all its bits. Sums are fp32.
 //
-// Bound by memory: 0.5625 bytes a weight are read once. A cluster of S CTAs, one an SM, takes a stretch of row tiles of 16, each CTA
-// a K slice whose x it keeps in shared memory. Its sixteen warps share out the tiles' chunks of 256 K, and each streams its
-// own through a ring of its own (cp.async), so no barrier stands in the stream. Either a warp takes whole tiles, whose sums leave
-// from its registers, or, where the tiles are few, the chunks laid end to end are cut into equal runs, and a tile's sums from the
-// runs that cross it meet in shared memory, in the runs' order. The cluster's CTAs are added in their order, through distributed
-// shared memory.
+// Bound by memory (0.5625 bytes a weight are read once) and, near it, by instructions: a chunk of 16 rows and 256 K is 2304 bytes, about
+// 300 instructions of a warp, of which 64 conversions (half an ALU clock of the SM each), 64 products by the scale and 16 mma.sync (2.5
+// clocks each): the SM's share of the copy rate allows 100 clocks a chunk, and 110 to 125 are taken. Scales behind the product instead
+// of before it would need each instruction's 16 K within one block, and so codes in pieces of two bytes; the matrix instructions
+// that take both operands' block scales want x in 4 bits as well. 262144 rows of 1152, five tokens: 34.7 us (4890 GB/s); 21504 rows of
+// 5376, one token 14.6 us (4460 GB/s), eight 17.5, 16 25.4, 32 50.
+//
+// A cluster of S CTAs, one an SM, takes a stretch of row tiles of 16, each CTA a K slice whose x it keeps in shared memory. Its sixteen
+// warps share out the tiles' chunks, and each streams its own through a ring of its own (cp.async), so no barrier stands in the stream.
+// Either a warp takes whole tiles, whose sums leave from its registers, or, where the tiles are few, the chunks laid end to end are cut
+// into equal runs, and a tile's sums from the runs that cross it meet in shared memory, in the runs' order. The cluster's CTAs are
+// added in their order, through distributed shared memory.
 #include <algorithm>
 #include <atomic>
 #include <type_traits>

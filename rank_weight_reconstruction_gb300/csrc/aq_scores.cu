@@ -13,7 +13,9 @@
 // order of arrival shows. Rows with more such words than places to collect them (one value everywhere, hardly a number above
 // -inf) go through the row again, each warp keeping the best 32 of its words sorted, one a lane.
 //
-// Bound by memory: the logits are read once (the gradient: read once, written once).
+// Bound by memory: the logits are read once (the gradient: read once, written once). 1024 rows of 262144 words in bf16: 86 us (6250
+// GB/s), their gradient 159 us (6750 GB/s). Five such rows with five alternatives, a cluster of 16 CTAs each: 6.9 us, latency. 333 rows of
+// 50257 in fp32 with 20 alternatives: 19 us (3520 GB/s): two or three CTAs an SM, whose first loads and last choices stand alone.
 #include <algorithm>
 #include <atomic>
 #include <type_traits>
@@ -578,19 +580,16 @@ __global__ void __launch_bounds__(32 * WARPS, (TOP ? kScorePerSm : kScorePerSm +
     if (rank != 0) return;
     sum = join<kScoreMaxCluster>(sh.cta_m, sh.cta_s, sh.cta_a, C, c);
     if (TOP) {
-      // of the CTAs' lists what reaches the largest of their last places (`top` words do)
-      Key floor = lane < C ? sh.lists[lane][p.top - 1] : 0;
-#pragma unroll
-      for (int o = 8; o > 0; o >>= 1) {
-        const Key other = __shfl_xor_sync(0xffffffffu, floor, o);
-        floor = other > floor ? other : floor;
-      }
-      floor = __shfl_sync(0xffffffffu, floor, 0);
+      // Of the CTAs' lists what reaches the larger of two bars, each of which `top` words do: the largest of their last places, and the
+      // smallest of the places that make up `top` together (16 lists of 32: hundreds of words reach the first, some 70 the second).
+      const uint32_t last = lane < C ? static_cast<uint32_t>(sh.lists[lane][p.top - 1] >> 32) : 0u;
+      const uint32_t shared = lane < C ? static_cast<uint32_t>(sh.lists[lane][(p.top + C - 1) / C - 1] >> 32) : 0xffffffffu;
+      const uint32_t floor = max(__reduce_max_sync(0xffffffffu, last), __reduce_min_sync(0xffffffffu, shared));
       if (tid == 0) sh.n_keys = 0;
       __syncthreads();
       for (int i = tid; i < C * 32; i += kThreads) {
         const Key x = i % 32 < p.top ? sh.lists[i / 32][i % 32] : 0;
-        if (x && x >= floor) sh.keys[atomicAdd(&sh.n_keys, 1)] = x;
+        if (x && static_cast<uint32_t>(x >> 32) >= floor) sh.keys[atomicAdd(&sh.n_keys, 1)] = x;
       }
       __syncthreads();
       n = sh.n_keys;
@@ -728,12 +727,16 @@ int score_cluster(int64_t rows, int32_t vocab, int sms) {
   while (c < kScoreMaxCluster && 2 * rows * c <= 3ll * sms && vocab / (2 * c) >= 8192) c *= 2;
   return c;
 }
-// Warps of a CTA: two where there are rows enough and a row's words are few, so that what comes before and after the words (the row's
-// sums joined, its best words placed) goes on in four times as many rows at once. Two warps against eight, us: 4096 rows of 1000 words
-// 6.9 and 18.7, with 5 alternatives 13.0 and 36.3, with 32 17 and 42; 1000 rows of 3000 3.9 and 5.6, with 5 7.8 and 11.9, but with 32
-// 15.0 and 13.7; 4096 rows of 8000 24 and 30, with 32 56 and 67; 2048 rows of 100000 with 5 163 and 138.
-int score_warps(int64_t rows, int32_t vocab, int32_t top, int cluster, int sms) {
-  return cluster == 1 && rows > 3ll * sms && vocab <= 16384 && (top <= 16 || rows > 16ll * sms) ? kScoreSmall : kScoreWarps;
+// Warps of a CTA: two where there are rows enough and a row's bytes are few, so that what comes before and after the words (the row's
+// sums joined, its best words placed) goes on in four times as many rows at once; alternatives make more of that, but of the warps' work
+// too. Two warps against eight, us, fp32: 4096 rows of 1000 words 6.9 and 18.7, with 5 alternatives 13.0 and 36.3, with 32 17 and 42;
+// 1000 rows of 3000 3.9 and 5.6, with 5 7.8 and 11.9, but with 32 15.0 and 13.7; 4096 rows of 8000 24 and 30, with 32 56 and 67; bf16:
+// 500 rows of 30000 12.2 and 9.3; 1000 of 24000 12.6 and 13.3, with 5 18.4 and 20.4, with 16 22.5 and 21.8; 1750 of 32000 with 5 24.7
+// and 35, with 16 31 and 39, with 20 42.6 and 42.7; fp32, 2048 of 100000 with 5 163 and 138.
+int score_warps(int64_t rows, int64_t bytes, int32_t top, int cluster, int sms) {
+  const bool few = bytes <= 32 * 1024;
+  const int most = rows > 16ll * sms ? AQ_MAX_TOP : rows > 8ll * sms || few ? 16 : 8;
+  return cluster == 1 && bytes <= 64 * 1024 && rows > (few ? 3ll : 6ll) * sms && top <= most ? kScoreSmall : kScoreWarps;
 }
 // Blocks that share a row of the gradient: pieces of 48 KB and more, smaller ones while they would not fill the GPU (1024 rows of
 // 262144 words in bf16, us: 166 in one piece, 159 in eight; one row 21 and 2.3 in 64).
@@ -794,7 +797,7 @@ extern "C" aq_status aq_token_logprobs(const void* logits, int64_t ld, int64_t r
   const unsigned grid = static_cast<unsigned>(rows * p.cluster);
   const cudaStream_t cs = static_cast<cudaStream_t>(stream);
   cudaError_t e;
-  const int warps = score_warps(rows, vocab, top, p.cluster, dev.sms);
+  const int warps = score_warps(rows, static_cast<int64_t>(vocab) * (type == AQ_PROB_F32 ? 4 : 2), top, p.cluster, dev.sms);
   if (type == AQ_PROB_F32) e = top ? launch_scores<float, true>(p, grid, warps, cs) : launch_scores<float, false>(p, grid, warps, cs);
   else e = top ? launch_scores<uint16_t, true>(p, grid, warps, cs) : launch_scores<uint16_t, false>(p, grid, warps, cs);
   return serve_launched(e, who);

@@ -108,7 +108,7 @@ def test_heads_past_32_bits():
 # ---- scores ----
 @pytest.mark.parametrize("dtype", ["f32", "bf16"])
 @pytest.mark.parametrize("rows,vocab,top", [(600, 1, 1), (600, 257, 0), (1000, 3000, 5), (900, 8191, 16), (900, 8193, 17), (2500, 1000, 32), (2500, 16384, 20),
-                                            (600, 16385, 3), (457, 65, 2)])
+                                            (600, 16385, 3), (457, 65, 2), (950, 16385, 8), (1300, 32768, 16), (1300, 32769, 9)])
 def test_many_rows_of_few_words(rows, vocab, top, dtype):
     r = np.random.RandomState(rows + vocab)
     x = scores.logits(r, rows, vocab, dtype)
