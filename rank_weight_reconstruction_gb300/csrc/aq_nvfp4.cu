@@ -18,7 +18,7 @@
 // A cluster of S CTAs, one an SM, takes a stretch of row tiles of 16, each CTA a K slice whose x it keeps in shared memory. Its sixteen
 // warps share out the tiles' chunks, and each streams its own through a ring of its own (cp.async), so no barrier stands in the stream.
 // Either a warp takes whole tiles, whose sums leave from its registers, or, where the tiles are few, the chunks laid end to end are cut
-// into equal runs, and a tile's sums from the runs that cross it meet in shared memory, in the runs' order. The cluster's CTAs are
+// into equal runs, and the warp whose run begins a tile adds the sums of the runs that go on with it, in their order. The cluster's CTAs are
 // added in their order, through distributed shared memory.
 #include <algorithm>
 #include <atomic>
@@ -33,7 +33,6 @@ constexpr int kQChunk = 256;                    // K of a chunk: 128 bytes of co
 constexpr int kQCodes = 16 * 128;               // bytes of a chunk's codes
 constexpr int kQStage = kQCodes + 16 * 32;      // and up to 32 bytes of scales a row (two pieces of 16 hold 16 bytes at any alignment)
 constexpr int kQRow = 4 * 144;                  // bytes of a chunk of a token of x
-constexpr int kQPart = 20;                      // floats a token of a tile's partial sums: 16 rows, spread over the banks
 
 struct Nvfp4Seg {
   const uint8_t* q;
@@ -152,11 +151,10 @@ __global__ void __launch_bounds__(32 * NW, 16 / NW) aq_nvfp4_kernel(const __grid
   const int64_t m0 = static_cast<int64_t>(blockIdx.y) * p.tokens;
   const int M = static_cast<int>(min(p.M - m0, static_cast<int64_t>(p.tokens)));
 
-  constexpr int kPart = 8 * NT * kQPart;
-  float* part = reinterpret_cast<float*>(smem);                           // [round + NW][8 NT][kQPart], unless whole
+  const uint32_t part = smem_u32(smem) + (tid & 31) * 16;                  // [NW][NT][lane] four sums, unless whole
   const int recv_tiles = (p.round + S - 1) / S;                           // tiles that one CTA of the cluster finishes
   const int recv_src = recv_tiles * 16 * p.tokens, recv_buf = S > 1 ? S * recv_src : 0;
-  float* recv = part + (p.whole ? 0 : (p.round + NW) * kPart);       // [2 or 1][S][recv_tiles][tokens][16]
+  float* recv = reinterpret_cast<float*>(smem) + (p.whole ? 0 : NW * NT * 128);   // [2 or 1][S][recv_tiles][tokens][16]
   float* back = recv + (p.clusters * p.round >= p.tiles ? 1 : 2) * recv_buf;   // [slice][8 NT]
   const uint32_t ring = smem_u32(back + p.slice * 8 * NT) + warp * (DEPTH * kQStage);
   const uint32_t xs = smem_u32(back + p.slice * 8 * NT) + NW * DEPTH * kQStage;
@@ -421,6 +419,23 @@ __global__ void __launch_bounds__(32 * NW, 16 / NW) aq_nvfp4_kernel(const __grid
     run(round, first, left);
     int tile = nc ? first / nc : 0, c = nc ? first - tile * nc : 0;
     if (!p.whole && round > 0) __syncthreads();   // the sums of the round before have been taken
+    const int units = min(p.round, t_last - tile0) * nc;
+    float tot[NT][4];
+    // A tile's sums on their way out of this CTA: over the cluster to the one that adds them up, or rounded.
+    auto leave = [&](int tile) {
+      const uint32_t to = S > 1 ? cluster_map(recv + (round & 1) * recv_buf + rank * recv_src + (tile / S) * 16 * p.tokens, tile % S) : 0;
+      const int row0 = (tile0 + tile - seg_begin) * 16, rows = seg_out - row0 - g;   // from row g on
+#pragma unroll
+      for (int n = 0; n < NT; ++n)
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+          const int m = n * 8 + 2 * t + (i & 1), r = g + (i >> 1) * 8;
+          if (m >= M) continue;
+          if (S > 1) asm volatile("st.shared::cluster.f32 [%0], %1;" ::"r"(to + (m * 16 + r) * 4), "f"(tot[n][i]) : "memory");
+          else if ((i >> 1) * 8 < rows) y_lane[(n * 8 + (i & 1)) * ldy + row0 + (i >> 1) * 8] = f32_to_bf16_rn(tot[n][i]);
+        }
+    };
+    int kept = -1;   // tile that this warp's run begins and does not end, its last
     while (left > 0) {
       const int here = min(left, nc - c);   // chunks of this tile
       if (tile0 + tile >= seg_end) {
@@ -438,7 +453,6 @@ __global__ void __launch_bounds__(32 * NW, 16 / NW) aq_nvfp4_kernel(const __grid
         sa = r & 15u;
         sb = (r + 8u * static_cast<uint32_t>(p.cols)) & 15u;
       }
-      float tot[NT][4];
 #pragma unroll
       for (int n = 0; n < NT; ++n) tot[n][0] = tot[n][1] = tot[n][2] = tot[n][3] = 0.0f;
       uint32_t xc = xs + c * x_chunk, bk = back_at + c * 32 * NT;
@@ -524,24 +538,14 @@ __global__ void __launch_bounds__(32 * NW, 16 / NW) aq_nvfp4_kernel(const __grid
         xc += x_chunk;
         bk += 32 * NT;
       }
-      if (!p.whole) {   // the run's part of the tile: pieces of tiles and warps are told apart by their sum
-        float* mine = part + (tile + warp) * kPart;
+      if (here == nc) {
+        leave(tile);
+      } else if (c == 0) {
+        kept = tile;
+      } else {   // a part of a tile that an earlier warp's run begins: the first of this run
 #pragma unroll
         for (int n = 0; n < NT; ++n)
-#pragma unroll
-          for (int i = 0; i < 4; ++i) mine[(n * 8 + 2 * t + (i & 1)) * kQPart + g + (i >> 1) * 8] = tot[n][i];
-      } else {
-        const uint32_t to = S > 1 ? cluster_map(recv + (round & 1) * recv_buf + rank * recv_src + (tile / S) * 16 * p.tokens, tile % S) : 0;
-        const int row0 = (tile0 + tile - seg_begin) * 16, rows = seg_out - row0 - g;   // from row g on
-#pragma unroll
-        for (int n = 0; n < NT; ++n)
-#pragma unroll
-          for (int i = 0; i < 4; ++i) {
-            const int m = n * 8 + 2 * t + (i & 1), r = g + (i >> 1) * 8;
-            if (m >= M) continue;
-            if (S > 1) asm volatile("st.shared::cluster.f32 [%0], %1;" ::"r"(to + (m * 16 + r) * 4), "f"(tot[n][i]) : "memory");
-            else if ((i >> 1) * 8 < rows) y_lane[(n * 8 + (i & 1)) * ldy + row0 + (i >> 1) * 8] = f32_to_bf16_rn(tot[n][i]);
-          }
+          asm volatile("st.shared.v4.f32 [%0], {%1, %2, %3, %4};" ::"r"(part + (warp * NT + n) * 512), "f"(tot[n][0]), "f"(tot[n][1]), "f"(tot[n][2]), "f"(tot[n][3]) : "memory");
       }
       left -= here;
       c += here;
@@ -552,24 +556,19 @@ __global__ void __launch_bounds__(32 * NW, 16 / NW) aq_nvfp4_kernel(const __grid
     }
     if (!p.whole) {
       __syncthreads();
-      const int n = min(p.round, t_last - tile0), units = n * nc;
-      const float inverse = units ? 1.0f / static_cast<float>(units) : 0.0f;
-      for (int e = warp; e < n * eights; e += NW) {
-        const int i = e / eights, m = 8 * (e - i * eights) + l_m, u0 = i * nc, u1 = u0 + nc;
-        // from the first run that ends behind u0, on while runs begin before u1 (a run may be empty)
-        int w = units ? max(0, static_cast<int>(static_cast<float>(NW * u0) * inverse) - 1) : NW;
-        while (w < NW && (units * (w + 1)) / NW <= u0) ++w;
-        const float* at = part + (i + w) * kPart + m * kQPart + l_r;
-        float4 v = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
-        for (; w < NW && (units * w) / NW < u1; ++w, at += kPart)
-          if (m < M && (units * w) / NW < (units * (w + 1)) / NW) add(v, at);
-        if (m >= M) continue;
-        if (S > 1) {
-          asm volatile("st.shared::cluster.v4.f32 [%0], {%1, %2, %3, %4};" ::"r"(cluster_map(recv + (round & 1) * recv_buf + rank * recv_src + (i / S) * 16 * p.tokens + m * 16 + l_r, i % S)),
-                       "f"(v.x), "f"(v.y), "f"(v.z), "f"(v.w) : "memory");
-        } else {
-          put(tile0 + i, m, l_r, v);
+      if (kept >= 0) {   // the runs that begin within the tile, in their order (one may be empty)
+        for (int w = warp + 1; w < NW && (units * w) / NW < (kept + 1) * nc; ++w) {
+          if ((units * w) / NW == (units * (w + 1)) / NW) continue;
+#pragma unroll
+          for (int n = 0; n < NT; ++n) {
+            const uint4 x = lds128(part + (w * NT + n) * 512);
+            tot[n][0] += __uint_as_float(x.x);
+            tot[n][1] += __uint_as_float(x.y);
+            tot[n][2] += __uint_as_float(x.z);
+            tot[n][3] += __uint_as_float(x.w);
+          }
         }
+        leave(kept);
       }
     }
     if (S > 1) {
@@ -584,30 +583,34 @@ __global__ void __launch_bounds__(32 * NW, 16 / NW) aq_nvfp4_kernel(const __grid
 // ---------------------------------------------------------------------------------
 // host
 // ---------------------------------------------------------------------------------
+// What a ring of three chunks leaves of an SM's shared memory: x comes through L1, which has what is left (21504 rows of 5376, us, K in one
+// slice: 18.6 with three chunks in 228 KB, 17.4 with two in 187; 16 tokens, four slices 26.1 and 24.3).
+constexpr size_t kQFree = 20 * 1024;
 struct Nvfp4Plan {
   int S = 0, clusters = 0, slice = 0, round = 0, whole = 0, depth = 0, warps = 0;
   size_t smem = 0;
+  double ns = 0;   // estimated
 };
 
 // Shared memory of a launch, in the kernel's order.
 size_t nvfp4_smem(int NT, int M, int tok, int tiles, const Nvfp4Plan& c) {
-  const size_t part = c.whole ? 0 : static_cast<size_t>(c.round + c.warps) * 8 * NT * kQPart * 4;
+  const size_t part = c.whole ? 0 : static_cast<size_t>(c.warps) * NT * 512;
   const size_t recv = c.S > 1 ? static_cast<size_t>(c.S) * ((c.round + c.S - 1) / c.S) * 16 * tok * 4 * (c.clusters * c.round >= tiles ? 1 : 2) : 0;
   return part + recv + static_cast<size_t>(c.slice) * 8 * NT * 4 + static_cast<size_t>(c.warps) * c.depth * kQStage +
          static_cast<size_t>(c.slice) * kQRow * M;
 }
 
 // Cluster size, warps a CTA, tiles a round and how the warps share them, by an estimate of the call's time in ns: the chunks that the
-// busiest warp takes, x into every CTA's shared memory, and what a round and an exchange cost. Its figures are fitted to 28 products
-// timed under every plan (M 1 to 32, K 1024 to 21504, rows 1152 to 262144); what it picks is within 1 % of the fastest of them on
-// average. CTAs of eight warps that leave half an SM free may begin under the tail of the kernel before. Some of them, us (S, runs or
-// whole tiles, warps): 21504 rows of 5376, M=8: (1, runs, 16) 17.5, (1, whole, 16) 22, (4, whole, 16) 20, (1, runs, 8) 48; 262144
-// rows of 1152, M=5: (1, whole, 16) 34.7, (1, whole, 8) 44; 1536 rows of 1152, M=1: (1, runs, 8) 3.8, (1, runs, 16) 4.5, (2, runs, 8)
-// 4.6; 5376 rows of 21504, M=8: (8, whole, 16) 20.9, (4, runs, 16) 22.0, (1, whole, 16) 176.
-bool plan_nvfp4(int tiles, int in, int M, int tok, const ServeDev& dev, const int (&fit)[4], Nvfp4Plan* best) {
+// busiest warp takes, x into every CTA's shared memory, what a round and an exchange cost, and the tokens' launch rows after one another
+// (of CTAs of eight warps two run beside each other). Its figures are fitted to 39 products timed under every plan (M 1 to 32, K 80 to
+// 21504, rows 100 to 262144); what it picks is within 1 % of the fastest of them on average. CTAs of eight warps that leave half an SM
+// free may begin under the tail of the kernel before. Some of them, us (S, runs or whole tiles, warps): 21504 rows of 5376, M=8: (2,
+// runs, 16) 16.4, (1, runs, 16) 17.3, (4, whole, 16) 18.6, (1, whole, 16) 21.9, (1, runs, 8) 25.6; 262144 rows of 1152, M=5: (1, runs,
+// 16) 33.7, (1, whole, 16) 34.2, (1, runs, 8) 42.6; 1536 rows of 1152, M=1: (1, runs, 8) 3.6, (1, runs, 16) 4.5, (2, runs, 8) 4.6; 5376
+// rows of 21504, M=8: (4, runs, 16) 19.1, (8, whole, 16) 20.3, (1, runs, 16) 76.
+bool plan_nvfp4(int tiles, int in, int M, int tok, int64_t rows_of_tokens, const ServeDev& dev, const int (&fit)[4], Nvfp4Plan* best) {
   const int NT = std::max(1, tok / 8), chunks = (in + kQChunk - 1) / kQChunk;
   const size_t half = (dev.smem_optin + 1024) / 2 - 1024;
-  double least = 0;
   bool found = false;
   for (int i = 0, S = 1; i < 4 && S <= chunks; ++i, S *= 2)
     for (int way = 0; way < 4; ++way) {
@@ -623,22 +626,21 @@ bool plan_nvfp4(int tiles, int in, int M, int tok, const ServeDev& dev, const in
       for (bool fits = false; !fits; ++rounds) {   // the fewest rounds and the deepest ring that fit
         c.round = (each + rounds - 1) / rounds;
         if (c.whole && rounds > 1) c.round = (c.round + c.warps - 1) / c.warps * c.warps;
-        for (c.depth = NT > 1 && c.warps == 8 ? 2 : 3; c.depth >= (NT > 1 || c.warps == 16 ? 2 : 3) && !fits; --c.depth) fits = (c.smem = nvfp4_smem(NT, M, tok, tiles, c)) <= room;
+        for (c.depth = NT > 1 && c.warps == 8 ? 2 : 3; c.depth >= (NT > 1 || c.warps == 16 ? 2 : 3) && !fits; --c.depth)
+          fits = (c.smem = nvfp4_smem(NT, M, tok, tiles, c)) <= (c.depth == 3 && c.warps == 16 ? room - kQFree : room);
         ++c.depth;
         if (fits || c.round <= (c.whole ? c.warps : 1)) break;
       }
       if (c.smem > room) continue;
       rounds = (each + c.round - 1) / c.round;
-      const int ctas = c.clusters * S;
       const double mine = c.whole ? (c.round + c.warps - 1) / c.warps * c.slice : (c.round * c.slice + c.warps - 1) / c.warps;   // chunks of a warp and round
-      const double chunk = std::max(2304.0 / std::min(47.0, 6300.0 / ctas), (NT == 1 ? 49.0 : NT == 2 ? 65.0 : 82.0) * (c.warps == 8 ? 1.34 : 1.0));
-      const double t = mine * rounds * c.warps * chunk + (c.warps == 8 ? 1050.0 : 1650.0) + static_cast<double>(c.slice) * M * (c.warps == 8 ? 20.0 : 18.0) +
-                       (S > 1 ? 900.0 * rounds + each * 5.6 * M : 0.0) + (c.whole ? 0.0 : 650.0 * rounds + each * 11.0 * M);
-      if (!found || t < least) {
-        least = t;
-        *best = c;
-        found = true;
-      }
+      const bool eight = c.warps == 8;
+      const double chunk = (NT == 1 ? 49.0 : NT == 2 ? 65.0 : 88.0) * (eight ? 1.5 : c.depth == 2 ? 1.18 : 1.0);
+      c.ns = mine * rounds * c.warps * chunk + (eight ? 1130.0 : 2070.0) + static_cast<double>(c.slice) * M * (eight ? 9.2 : 12.2) +
+             (S > 1 ? 980.0 * rounds + each * 5.0 * M : 0.0) + (c.whole ? 0.0 : 460.0 * rounds + each * 3.1 * M);
+      c.ns *= 1.0 + (rows_of_tokens - 1) * (eight ? 0.44 : 1.0);
+      if (!found || c.ns < best->ns) *best = c;
+      found = true;
     }
   return found;
 }
@@ -754,11 +756,18 @@ extern "C" aq_status aq_nvfp4_linear_multi(const aq_nvfp4_weight* w, int32_t n, 
   int fit[4];
   cudaError_t e = clusters_at_once(dev, fit);
   if (e != cudaSuccess) return serve_launched(e, who);
+  // Tokens of a launch row: 32, 16 or 8 by the estimate (21504 rows of 5376, 32 tokens, us: 49.8 at once, 44.4 in two rows; 1152 of 6912
+  // 10.6 and 8.7; 49567 of 5264, 20 tokens: 97 and 134), or fewer where a cluster's shared memory does not hold so many.
   Nvfp4Plan plan;
-  int tok = M <= 8 ? 8 : M <= 16 ? 16 : 32;   // tokens at once: what a cluster's shared memory holds of them
-  for (; tok >= 1; tok /= 2)
-    if (plan_nvfp4(static_cast<int>(row_tiles), in, static_cast<int>(std::min<int64_t>(M, tok)), tok, dev, fit, &plan)) break;
-  if (tok < 1) return serve_fail(AQ_ERR_UNSUPPORTED, "%s: in=%d does not fit this device's shared memory", who, in);
+  int tok = 0;
+  for (int t = M <= 8 ? 8 : M <= 16 ? 16 : 32; t >= 1 && (t >= 8 || !tok); t /= 2) {
+    Nvfp4Plan c;
+    if (!plan_nvfp4(static_cast<int>(row_tiles), in, static_cast<int>(std::min<int64_t>(M, t)), t, (M + t - 1) / t, dev, fit, &c)) continue;
+    if (!tok || c.ns < plan.ns) {
+      tok = t;
+      plan = c;
+    }
+  }
   const int64_t tiles = (M + tok - 1) / tok;
   if (tiles > 65535) return serve_fail(AQ_ERR_SHAPE, "%s: M=%lld is too large", who, (long long)M);
   Nvfp4Params p = {};
