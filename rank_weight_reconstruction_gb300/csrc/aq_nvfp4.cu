@@ -635,9 +635,10 @@ bool plan_nvfp4(int tiles, int in, int M, int tok, int64_t rows_of_tokens, const
       rounds = (each + c.round - 1) / c.round;
       const double mine = c.whole ? (c.round + c.warps - 1) / c.warps * c.slice : (c.round * c.slice + c.warps - 1) / c.warps;   // chunks of a warp and round
       const bool eight = c.warps == 8;
-      const double chunk = (NT == 1 ? 49.0 : NT == 2 ? 65.0 : 88.0) * (eight ? 1.5 : c.depth == 2 ? 1.18 : 1.0);
-      c.ns = mine * rounds * c.warps * chunk + (eight ? 1130.0 : 2070.0) + static_cast<double>(c.slice) * M * (eight ? 9.2 : 12.2) +
-             (S > 1 ? 980.0 * rounds + each * 5.0 * M : 0.0) + (c.whole ? 0.0 : 460.0 * rounds + each * 3.1 * M);
+      const double chunk = (NT == 1 ? 49.0 : NT == 2 ? 66.0 : 91.0) * (eight ? 1.56 : c.depth == 2 ? 1.16 : 1.0);
+      const int pieces = c.slice * M, turns = (pieces + 8 * c.warps - 1) / (8 * c.warps);   // of x; a warp has eight on their way at once
+      c.ns = mine * rounds * c.warps * chunk + (eight ? 1170.0 : 2210.0) + pieces * (eight ? 6.7 : 10.9) + 380.0 * (turns - 1) +
+             (S > 1 ? 930.0 * rounds + each * 4.8 * M : 0.0) + (c.whole ? 0.0 : 460.0 * rounds + each * 3.2 * M);
       c.ns *= 1.0 + (rows_of_tokens - 1) * (eight ? 0.44 : 1.0);
       if (!found || c.ns < best->ns) *best = c;
       found = true;
