@@ -405,7 +405,8 @@ __global__ void __launch_bounds__(kNormThreads, kNormPerSm) aq_norm_grad_kernel(
     const int32_t pos = next_pos;
     if (p.freq && item + step < items) next_pos = p.pos[(item + step) >> s.hl_shift];
     float c[8], sn[8];
-    angles<HALF, GW, true>(ch, u, p.freq, pos, p.magnitude, -p.magnitude, c, sn);
+    if (hl < 32 / GW) angles<HALF, GW, false>(ch, u, p.freq, pos, p.magnitude, -p.magnitude, c, sn);   // its groups have a token each
+    else angles<HALF, GW, true>(ch, u, p.freq, pos, p.magnitude, -p.magnitude, c, sn);
     const bool turn0 = p.freq && live && ch.turns0, turn1 = p.freq && live && ch.turns1;
     uint16_t* ds = s.dx + t * s.dx_tok;
     if (there) {
@@ -504,7 +505,7 @@ __global__ void __launch_bounds__(1024) aq_norm_join_kernel(const __grid_constan
 }
 
 // Blocks of the two sets: what fills the GPU, shared out by their work (a token's angles weigh as much as a head, and every
-// group works them out); no more than their groups of work.
+// group works them out; to itself, twice as much); no more than their groups of work.
 void norm_blocks(int64_t T, int32_t D, int32_t hq, int32_t hk, int sms, int32_t* hl_shift, int32_t* blocks) {
   const int gw = group_width(D), groups = kNormThreads / gw, heads[2] = {hq, hk};
   const int fill = sms * kNormPerSm;
@@ -512,9 +513,15 @@ void norm_blocks(int64_t T, int32_t D, int32_t hq, int32_t hk, int sms, int32_t*
   for (int i = 0; i < 2; ++i) {
     hl_shift[i] = blocks[i] = 0;
     if (!heads[i]) continue;
-    hl_shift[i] = warp_token(T, heads[i], gw, static_cast<int64_t>(fill) * groups / 2);
+    // A block has one set's heads, often one: where half of a warp's groups or more would have none, and the tokens are enough without, each
+    // group has a token and its angles to itself. Shared and apart, us: 16000 tokens of 1 + 1 heads of 64 22.4 and 8.5, 4000 9.3 and 5.6;
+    // 2000 of 2 + 2 6.7 and 5.4; 16000 of 4 + 1 of 128 25.7 and 21.1. (Without the gradient q, k and v make one list, and it costs more
+    // than it gives: 16385 tokens of 16 + 4 heads 29.6 and 30.0 for having both.)
+    const int64_t fit = static_cast<int64_t>(fill) * groups;
+    const int own = share_token(T, heads[i], gw, fit / 2);
+    hl_shift[i] = 2 * heads[i] <= 32 / gw && (T << own) >= fit / 8 ? own : warp_token(T, heads[i], gw, fit / 2);
     const int hl = 1 << hl_shift[i];
-    work[i] = static_cast<int64_t>(hl) * (1 + (heads[i] + hl - 1) / hl);
+    work[i] = static_cast<int64_t>(hl) * ((hl < 32 / gw ? 2 : 1) + (heads[i] + hl - 1) / hl);
   }
   for (int i = 0; i < 2; ++i) {
     if (!heads[i]) continue;

@@ -73,7 +73,8 @@ def test_products_past_32_bits():
 
 
 # ---- head norms ----
-@pytest.mark.parametrize("T,hq,hk,D", [(9001, 1, 1, 16), (6003, 3, 1, 48), (5001, 2, 2, 80), (2500, 5, 2, 256), (20011, 1, 1, 128)])
+@pytest.mark.parametrize("T,hq,hk,D", [(9001, 1, 1, 16), (6003, 3, 1, 48), (5001, 2, 2, 80), (2500, 5, 2, 256), (20011, 1, 1, 128), (12001, 1, 1, 64),
+                                       (9999, 2, 1, 64), (8001, 4, 1, 32), (7003, 1, 1, 256), (15001, 3, 1, 80)])
 def test_more_tokens_than_the_grid_holds_in_place(T, hq, hk, D):
     r = np.random.RandomState(T)
     q, k, dq, dk = norms.randn(r, T, hq, D), norms.randn(r, T, hk, D), norms.randn(r, T, hq, D), norms.randn(r, T, hk, D)
@@ -86,6 +87,14 @@ def test_more_tokens_than_the_grid_holds_in_place(T, hq, hk, D):
     assert mine[0] is dq and mine[1] is dk and all(torch.equal(a, b) for a, b in zip(mine, grads))
     got = aq.aq_qk_norm_rope(q, k, n, n, rope, pos, q_out=q, k_out=k)
     assert got[0] is q and got[1] is k and all(torch.equal(a, b) for a, b in zip(got, want))
+
+
+@pytest.mark.parametrize("T,hq,hk,D,rot,layout", [
+    (12001, 1, 1, 64, 64, "half"), (9999, 4, 1, 128, 64, "interleaved"), (8001, 3, 2, 32, 16, "half"), (7003, 1, 1, 256, 256, "interleaved"),
+    (15001, 2, 1, 80, 80, "half"), (5001, 1, 1, 16, None, "half"), (2003, 5, 3, 48, 48, "interleaved"),
+])
+def test_gradient_of_few_heads_of_many_tokens(T, hq, hk, D, rot, layout):
+    norms.test_backward(T, hq, hk, D, rot, layout)
 
 
 def test_heads_past_32_bits():
