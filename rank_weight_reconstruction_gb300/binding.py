@@ -787,7 +787,8 @@ def aq_nvfp4_linear_multi(weights, x, ys=None, stream=None):
 
 
 class TokenScores(NamedTuple):
-    """What aq_token_logprobs returns: fp32 [rows] (logprob None without tokens) and [rows, top] (None with top=0)."""
+    """What aq_token_logprobs returns: fp32 [rows] (logprob None without tokens) and [rows, top] (None with top=0), parts of
+    one allocation."""
     logprob: object
     lse: object
     entropy: object

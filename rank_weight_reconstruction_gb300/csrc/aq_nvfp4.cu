@@ -12,14 +12,14 @@
 // 300 instructions of a warp, of which 64 conversions (half an ALU clock of the SM each), 64 products by the scale and 16 mma.sync (2.5
 // clocks each): the SM's share of the copy rate allows 100 clocks a chunk, and 110 to 125 are taken. Scales behind the product instead
 // of before it would need each instruction's 16 K within one block, and so codes in pieces of two bytes; the matrix instructions
-// that take both operands' block scales want x in 4 bits as well. 262144 rows of 1152, five tokens: 34.7 us (4890 GB/s); 21504 rows of
-// 5376, one token 14.6 us (4460 GB/s), eight 17.5, 16 25.4, 32 50.
+// that take both operands' block scales want x in 4 bits as well. 262144 rows of 1152, five tokens: 34.2 us (4970 GB/s); 21504 rows of
+// 5376, one token 14.2 us (4580 GB/s), eight 16.2, 16 22.9, 32 44.
 //
 // A cluster of S CTAs, one an SM, takes a stretch of row tiles of 16, each CTA a K slice whose x it keeps in shared memory. Its sixteen
 // warps share out the tiles' chunks, and each streams its own through a ring of its own (cp.async), so no barrier stands in the stream.
-// Either a warp takes whole tiles, whose sums leave from its registers, or, where the tiles are few, the chunks laid end to end are cut
-// into equal runs, and the warp whose run begins a tile adds the sums of the runs that go on with it, in their order. The cluster's CTAs are
-// added in their order, through distributed shared memory.
+// Either a warp takes whole tiles, or the chunks laid end to end are cut into equal runs. A tile's sums leave from the registers of the
+// warp whose run begins it, which adds those of the runs that go on with it, in their order. The cluster's CTAs are added in their
+// order, through distributed shared memory.
 #include <algorithm>
 #include <atomic>
 #include <type_traits>

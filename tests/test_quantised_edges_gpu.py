@@ -234,3 +234,42 @@ def test_scores_far_from_zero(dtype):
         assert np.array_equal(s.top_token.cpu().numpy(), tt)
         d = aq.aq_token_logprobs_backward(t, tokens, s.lse, None, torch.ones(8, device="cuda"), scale=scale)
         assert torch.isfinite(d).all() and d.abs().max() <= 1
+
+
+FIRST = """
+import sys
+sys.path[:0] = [{root!r}, {root!r} + "/tests"]
+import torch
+import rank_weight_reconstruction_gb300 as aq
+r = torch.Generator(device="cuda").manual_seed(1)
+byte = lambda *s: torch.randint(0, 0x70, s, generator=r, device="cuda", dtype=torch.uint8)
+randn = lambda *s: torch.randn(*s, generator=r, device="cuda").to(torch.bfloat16)
+w = aq.Nvfp4Weight(byte(200, 2048), byte(200, 256), torch.ones(1, device="cuda"))
+x, h, dh, z, n = randn(9, 4096), randn(30, 2, 64), randn(30, 2, 64), randn(5, 70000), aq.HeadNorm(randn(64))
+tok, one = torch.zeros(5, dtype=torch.int32, device="cuda"), torch.ones(5, device="cuda")
+
+def run():
+    s = aq.aq_token_logprobs(z, tok, top=3)
+    return [aq.aq_nvfp4_linear(w, x), aq.aq_qk_norm_rope(h, q_norm=n)[0], *aq.aq_qk_norm_rope_backward(dh, None, h, None, n, None)[::2], *s,
+            aq.aq_token_logprobs_backward(z, tok, s.lse, None, one)]
+
+torch.cuda.synchronize()
+graph = torch.cuda.CUDAGraph()
+with torch.cuda.graph(graph):
+    out = run()
+graph.replay()
+torch.cuda.synchronize()
+assert all(torch.equal(a, b) for a, b in zip(out, run()))
+print("captured")
+"""
+
+
+def test_first_calls_of_a_process_captured():
+    """No call of these needs to have run before it is captured."""
+    import pathlib
+    import subprocess
+    import sys
+
+    root = str(pathlib.Path(__file__).resolve().parents[1])
+    r = subprocess.run([sys.executable, "-c", FIRST.format(root=root)], capture_output=True, text=True, timeout=300)
+    assert r.returncode == 0 and "captured" in r.stdout, r.stderr[-2000:]
