@@ -8,8 +8,8 @@
 // rotation, 16 elements a lane, kept as the eight pairs that turn against each other in either order, so that squares, scales and
 // turns are packed products of two; a head's sums are a few shuffles. The factors f stay in registers while a group walks the heads
 // of q, then those of k. In the gradient the weight's sums stay in 16 registers a lane over all the heads that the lane sees,
-// so a block is given heads of q alone or of k alone; the groups' sums meet in shared memory, the blocks' in the workspace, and a
-// second launch adds those up, all in an order fixed by the sizes and the device's SM count.
+// so a block is given heads of q alone or of k alone; the groups' sums meet in shared memory, the blocks' in their cluster's where
+// they are few, otherwise in the workspace, where a second launch adds them up, all in an order fixed by the sizes and the device's SM count.
 #include <algorithm>
 
 #include "aq_positions.cuh"
@@ -330,6 +330,7 @@ struct NormSet {
   uint16_t* dx;
   const uint16_t* w;
   float* part;         // [blocks][D], or NULL
+  float* dw;           // with a cluster: where the sums go, or NULL
   int64_t dy_tok, dy_head, x_tok, x_head, dx_tok, dx_head;
   int32_t heads, hl_shift;   // log2 of the groups that share a token
   int32_t blocks;
@@ -341,8 +342,10 @@ struct NormGradParams {
   const uint64_t* freq;   // NULL: no rotation
   int64_t T;
   int32_t D, rot16;
+  int32_t cluster;        // blocks of a set, which are a cluster and join their sums themselves; 0: a second launch does
   float magnitude;
 };
+constexpr int kNormCluster = 8;
 
 template <bool HALF, int GW>
 __global__ void __launch_bounds__(kNormThreads, kNormPerSm) aq_norm_grad_kernel(const __grid_constant__ NormGradParams p) {
@@ -353,6 +356,7 @@ __global__ void __launch_bounds__(kNormThreads, kNormPerSm) aq_norm_grad_kernel(
   static_assert(sizeof(ring) >= sizeof(float) * kGroups * kRow, "the sums fit");
   const int which = static_cast<int>(blockIdx.x) >= p.set[0].blocks;
   const NormSet& s = p.set[which];
+  if (p.cluster > 1 && s.dw) asm volatile("barrier.cluster.arrive.relaxed.aligned;" ::: "memory");
   const int block = static_cast<int>(blockIdx.x) - (which ? p.set[0].blocks : 0);
   const int lane = threadIdx.x & 31, u = threadIdx.x % GW;
   const Chunks<HALF> ch(u, p.rot16, p.D / 16);
@@ -456,7 +460,7 @@ __global__ void __launch_bounds__(kNormThreads, kNormPerSm) aq_norm_grad_kernel(
     }
     __syncwarp();
   }
-  if (!s.part) return;
+  if (!s.part && !s.dw) return;
   cp_async_wait<0>();
   __syncthreads();
   float* sums = reinterpret_cast<float*>(ring);
@@ -468,11 +472,23 @@ __global__ void __launch_bounds__(kNormThreads, kNormPerSm) aq_norm_grad_kernel(
       row[HALF ? k1 + i : (i < 4 ? k0 : k1) + 2 * (i & 3) + 1] = w1[i];
     }
   }
+  __shared__ float met[kNormCluster][kServeMaxHeadDim];   // the first block's: every block's sums
+  if (p.cluster > 1) asm volatile("barrier.cluster.wait.acquire.aligned;" ::: "memory");   // it runs
   __syncthreads();
   for (int d = threadIdx.x; d < p.D; d += kNormThreads) {
     float v = 0.0f;
     for (int i = 0; i < kGroups; ++i) v += sums[i * kRow + d];
-    s.part[static_cast<int64_t>(block) * p.D + d] = v;
+    if (p.cluster == 0) s.part[static_cast<int64_t>(block) * p.D + d] = v;
+    else if (p.cluster == 1) s.dw[d] = v;
+    else asm volatile("st.shared::cluster.f32 [%0], %1;" ::"r"(cluster_map(&met[block][d], 0)), "f"(v) : "memory");
+  }
+  if (p.cluster <= 1) return;
+  cluster_sync_all();
+  if (block != 0) return;
+  for (int d = threadIdx.x; d < p.D; d += kNormThreads) {
+    float v = 0.0f;
+    for (int i = 0; i < p.cluster; ++i) v += met[i][d];
+    s.dw[d] = v;
   }
 }
 
@@ -529,17 +545,30 @@ void norm_blocks(int64_t T, int32_t D, int32_t hq, int32_t hk, int sms, int32_t*
     blocks[i] = static_cast<int32_t>(std::min(need, std::max<int64_t>(1, fill * work[i] / (work[0] + work[1]))));
   }
 }
+// Blocks of a set where each group has one token and they are few enough to be a cluster, which joins their sums itself, or 0. One launch
+// against two, us: one token of 32 + 8 heads of 128 3.2 and 4.4, eight 3.8 and 4.6, 60 of 4 + 1 3.8 and 4.6; with two tokens a group no less.
+int norm_cluster(int64_t T, int32_t D, int32_t hq, int32_t hk, int32_t* hl_shift, int32_t* blocks) {
+  const int gw = group_width(D), groups = kNormThreads / gw, heads[2] = {hq, hk};
+  int cluster = 1;
+  for (int i = 0; i < 2; ++i) {
+    hl_shift[i] = heads[i] ? warp_token(T, heads[i], gw, INT64_MAX) : 0;
+    if (T > static_cast<int64_t>(kNormCluster) * groups >> hl_shift[i]) return 0;
+    while (heads[i] && static_cast<int64_t>(cluster) * groups < T << hl_shift[i]) cluster *= 2;
+  }
+  for (int i = 0; i < 2; ++i) blocks[i] = heads[i] ? cluster : 0;
+  return cluster;
+}
 constexpr int kNormSmsBound = 256;   // SMs that the workspace's size allows for
 
 template <bool HALF>
 cudaError_t launch_norm_grad(const NormGradParams& p, int gw, cudaStream_t st) {
   const unsigned grid = static_cast<unsigned>(p.set[0].blocks + p.set[1].blocks);
   switch (gw) {
-    case 1: return launch_serve(aq_norm_grad_kernel<HALF, 1>, p, grid, kNormThreads, 0, st);
-    case 2: return launch_serve(aq_norm_grad_kernel<HALF, 2>, p, grid, kNormThreads, 0, st);
-    case 4: return launch_serve(aq_norm_grad_kernel<HALF, 4>, p, grid, kNormThreads, 0, st);
-    case 8: return launch_serve(aq_norm_grad_kernel<HALF, 8>, p, grid, kNormThreads, 0, st);
-    default: return launch_serve(aq_norm_grad_kernel<HALF, 16>, p, grid, kNormThreads, 0, st);
+    case 1: return launch_serve(aq_norm_grad_kernel<HALF, 1>, p, grid, kNormThreads, 0, st, p.cluster);
+    case 2: return launch_serve(aq_norm_grad_kernel<HALF, 2>, p, grid, kNormThreads, 0, st, p.cluster);
+    case 4: return launch_serve(aq_norm_grad_kernel<HALF, 4>, p, grid, kNormThreads, 0, st, p.cluster);
+    case 8: return launch_serve(aq_norm_grad_kernel<HALF, 8>, p, grid, kNormThreads, 0, st, p.cluster);
+    default: return launch_serve(aq_norm_grad_kernel<HALF, 16>, p, grid, kNormThreads, 0, st, p.cluster);
   }
 }
 
@@ -729,7 +758,8 @@ extern "C" aq_status aq_qk_norm_rope_backward(const aq_head_norm* q_norm, const 
   if ((st = serve_device(&dev)) != AQ_OK) return st;
   NormGradParams p = {};
   int32_t hl[2], blocks[2];
-  norm_blocks(T, D, q->heads, k ? k->heads : 0, std::min(dev.sms, kNormSmsBound), hl, blocks);
+  p.cluster = sums ? norm_cluster(T, D, q->heads, k ? k->heads : 0, hl, blocks) : 0;
+  if (!p.cluster) norm_blocks(T, D, q->heads, k ? k->heads : 0, std::min(dev.sms, kNormSmsBound), hl, blocks);
   float* part = static_cast<float*>(workspace);
   for (int i = 0; i < sets; ++i) {
     NormSet& s = p.set[i];
@@ -748,7 +778,8 @@ extern "C" aq_status aq_qk_norm_rope_backward(const aq_head_norm* q_norm, const 
     s.blocks = blocks[i];
     s.eps = norm[i]->eps;
     s.offset = norm[i]->offset;
-    if (dw[i]) s.part = part + (i ? static_cast<int64_t>(blocks[0]) * D : 0);
+    if (p.cluster) s.dw = dw[i];
+    else if (dw[i]) s.part = part + (i ? static_cast<int64_t>(blocks[0]) * D : 0);
   }
   p.T = T;
   p.D = D;
@@ -759,7 +790,7 @@ extern "C" aq_status aq_qk_norm_rope_backward(const aq_head_norm* q_norm, const 
     p.magnitude = rope->magnitude;
   }
   const cudaError_t e = rope && rope->layout == AQ_ROPE_HALF ? launch_norm_grad<true>(p, group_width(D), cs) : launch_norm_grad<false>(p, group_width(D), cs);
-  if (e != cudaSuccess || !sums) return serve_launched(e, who);
+  if (e != cudaSuccess || !sums || p.cluster) return serve_launched(e, who);
   NormJoinParams j = {};
   for (int i = 0; i < sets; ++i) {
     j.part[i] = p.set[i].part;

@@ -92,8 +92,10 @@ def test_more_tokens_than_the_grid_holds_in_place(T, hq, hk, D):
 @pytest.mark.parametrize("T,hq,hk,D,rot,layout", [
     (12001, 1, 1, 64, 64, "half"), (9999, 4, 1, 128, 64, "interleaved"), (8001, 3, 2, 32, 16, "half"), (7003, 1, 1, 256, 256, "interleaved"),
     (15001, 2, 1, 80, 80, "half"), (5001, 1, 1, 16, None, "half"), (2003, 5, 3, 48, 48, "interleaved"),
+    (8, 32, 8, 128, 128, "half"), (64, 4, 1, 128, 64, "half"), (65, 4, 1, 128, 128, "interleaved"), (16, 40, 8, 256, 256, "half"), (40, 3, 1, 80, 80, "interleaved"),
+    (127, 1, 1, 64, 64, "half"), (512, 1, 1, 16, 16, "half"), (2, 1, 64, 32, 32, "half"),
 ])
-def test_gradient_of_few_heads_of_many_tokens(T, hq, hk, D, rot, layout):
+def test_gradient_of_few_heads_or_few_tokens(T, hq, hk, D, rot, layout):
     norms.test_backward(T, hq, hk, D, rot, layout)
 
 
