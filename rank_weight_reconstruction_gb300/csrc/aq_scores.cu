@@ -27,7 +27,6 @@ namespace {
 
 constexpr int kScoreThreads = 256, kScoreWarps = kScoreThreads / 32, kScorePerSm = 3;
 constexpr int kScoreMaxCluster = 16;
-constexpr int kScoreSmall = 2;   // warps of a CTA for many rows of few words
 constexpr float kLog2e = 1.4426950408889634f, kLn2 = 0.6931471805599453f;
 
 struct ScoreParams {
@@ -339,7 +338,7 @@ __device__ __forceinline__ Sums join(const float* m, const float* s, const float
   return one;
 }
 
-// WARPS: eight, or two for many rows of few words (a cluster of one).
+// WARPS: eight, or two or four for many rows of few words (a cluster of one).
 template <typename T, bool TOP, int WARPS>
 __global__ void __launch_bounds__(32 * WARPS, (TOP ? kScorePerSm : kScorePerSm + 1) * kScoreWarps / WARPS) aq_scores_kernel(const __grid_constant__ ScoreParams p) {
   using W = Words<T>;
@@ -698,7 +697,8 @@ __global__ void __launch_bounds__(kScoreThreads, 4) aq_scores_grad_kernel(const 
 
 template <typename T, bool TOP>
 cudaError_t launch_scores(const ScoreParams& p, unsigned grid, int warps, cudaStream_t st) {
-  if (warps == kScoreSmall) return launch_serve(aq_scores_kernel<T, TOP, kScoreSmall>, p, grid, 32 * kScoreSmall, 0, st);
+  if (warps == 2) return launch_serve(aq_scores_kernel<T, TOP, 2>, p, grid, 64, 0, st);
+  if (warps == 4) return launch_serve(aq_scores_kernel<T, TOP, 4>, p, grid, 128, 0, st);
   static std::atomic<uint64_t> ready{0};   // devices on which the kernel may use clusters of 16
   if (p.cluster > 8 && !(ready.load() >> p.device & 1)) {
     const cudaError_t e = cudaFuncSetAttribute(aq_scores_kernel<T, TOP, kScoreWarps>, cudaFuncAttributeNonPortableClusterSizeAllowed, 1);
@@ -727,16 +727,18 @@ int score_cluster(int64_t rows, int32_t vocab, int sms) {
   while (c < kScoreMaxCluster && 2 * rows * c <= 3ll * sms && vocab / (2 * c) >= 8192) c *= 2;
   return c;
 }
-// Warps of a CTA: two where there are rows enough and a row's bytes are few, so that what comes before and after the words (the row's
-// sums joined, its best words placed) goes on in four times as many rows at once; alternatives make more of that, but of the warps' work
-// too. Two warps against eight, us, fp32: 4096 rows of 1000 words 6.9 and 18.7, with 5 alternatives 13.0 and 36.3, with 32 17 and 42;
-// 1000 rows of 3000 3.9 and 5.6, with 5 7.8 and 11.9, but with 32 15.0 and 13.7; 4096 rows of 8000 24 and 30, with 32 56 and 67; bf16:
-// 500 rows of 30000 12.2 and 9.3; 1000 of 24000 12.6 and 13.3, with 5 18.4 and 20.4, with 16 22.5 and 21.8; 1750 of 32000 with 5 24.7
-// and 35, with 16 31 and 39, with 20 42.6 and 42.7; fp32, 2048 of 100000 with 5 163 and 138.
+// Warps of a CTA: two or four where there are rows enough and a row's bytes are few, so that what comes before and after the words (the
+// row's sums joined, its best words placed) goes on in four or two times as many rows at once; alternatives make more of that, but of
+// the warps' work too. Eight, four and two warps, us: 4096 rows of 1000 words, fp32, 18.7, -, 6.9; 1000 of 8000 10.4, 7.9, 8.5, with 5
+// alternatives 16.3, 13.7, 11.9, with 20 18.0, 15.0, 15.8; bf16, 500 of 16000 5.7, 5.7, 7.4, with 5 10.9, 9.8, 9.6; 1750 of 32000
+// with 5 35, 27.9, 25.1, with 20 42, 33, 34; 1000 of 50257 23.2, 21.2, 23.3, with 20 35.6, 33.4, 38, with 32 38.6, 40, 47; fp32, 500 of
+// 50257 19.4, 21.1, 30, with 5 28.2, 25.2, 34; 2500 with 20 108, 102, 129; bf16, 1000 of 151936 with 5 64, 71, 81.
 int score_warps(int64_t rows, int64_t bytes, int32_t top, int cluster, int sms) {
-  const bool few = bytes <= 32 * 1024;
-  const int most = rows > 16ll * sms ? AQ_MAX_TOP : rows > 8ll * sms || few ? 16 : 8;
-  return cluster == 1 && bytes <= 64 * 1024 && rows > (few ? 3ll : 6ll) * sms && top <= most ? kScoreSmall : kScoreWarps;
+  const int64_t fills = rows / sms;   // rows an SM
+  if (cluster > 1 || fills < 3 || bytes > 208 * 1024 || (top == 0 && fills < 6 && bytes > 32 * 1024)) return kScoreWarps;
+  if (bytes <= 32 * 1024 && (top ? top <= 8 || fills >= 16 : fills >= 6)) return 2;
+  if (bytes <= 64 * 1024 && fills >= 8 && top >= 1 && top <= 8) return 2;
+  return bytes > 64 * 1024 && top > 20 && fills < 8 ? kScoreWarps : 4;
 }
 // Blocks that share a row of the gradient: pieces of 48 KB and more, smaller ones while they would not fill the GPU (1024 rows of
 // 262144 words in bf16, us: 166 in one piece, 159 in eight; one row 21 and 2.3 in 64).
