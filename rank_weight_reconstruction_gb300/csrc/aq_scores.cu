@@ -719,12 +719,13 @@ aq_status check_logits(const void* logits, int64_t ld, int64_t rows, int32_t voc
   return AQ_OK;
 }
 
-// CTAs that share a row. Three CTAs an SM is what fills the GPU once; a row's part is no smaller than 8192 words, as what comes after
-// its words weighs as much as 4000 of them (333 rows of 50257 words with 20 alternatives, us: one CTA a row 22, two 29, four 40; 100
-// rows of 262144: one 36, two 25, four 23, eight 32).
-int score_cluster(int64_t rows, int32_t vocab, int sms) {
+// CTAs that share a row. Three CTAs an SM are what fills the GPU once (four without alternatives); a row's part is no smaller than 8192
+// words, as what comes after its words weighs as much as 4000 of them. One CTA a row, two and four, us: fp32, 300 rows of 151936 words 32.0,
+// 29.8, 36.9, with 20 alternatives 40.8, 47.0, 50.6; 120 rows 23.8, 17.3, 15.4, with 20 31.4, 23.4, 27.2; 246 rows of 50257 12.7, 12.0,
+// 14.4, with 20 17.8, 22.1, 26.1.
+int score_cluster(int64_t rows, int32_t vocab, int32_t top, int sms) {
   int c = 1;
-  while (c < kScoreMaxCluster && 2 * rows * c <= 3ll * sms && vocab / (2 * c) >= 8192) c *= 2;
+  while (c < kScoreMaxCluster && 2 * rows * c <= (top ? 3ll : 4ll) * sms && vocab / (2 * c) >= 8192) c *= 2;
   return c;
 }
 // Warps of a CTA: two or four where there are rows enough and a row's bytes are few, so that what comes before and after the words (the
@@ -794,7 +795,7 @@ extern "C" aq_status aq_token_logprobs(const void* logits, int64_t ld, int64_t r
   p.vocab = vocab;
   p.top = top;
   p.device = dev.index;
-  p.cluster = score_cluster(rows, vocab, dev.sms);
+  p.cluster = score_cluster(rows, vocab, top, dev.sms);
   if (rows * p.cluster > 0x7fffffffLL) return serve_fail(AQ_ERR_SHAPE, "%s: rows=%lld is too large", who, (long long)rows);
   const unsigned grid = static_cast<unsigned>(rows * p.cluster);
   const cudaStream_t cs = static_cast<cudaStream_t>(stream);

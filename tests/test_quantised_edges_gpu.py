@@ -120,7 +120,7 @@ def test_heads_past_32_bits():
 @pytest.mark.parametrize("dtype", ["f32", "bf16"])
 @pytest.mark.parametrize("rows,vocab,top", [(600, 1, 1), (600, 257, 0), (1000, 3000, 5), (900, 8191, 16), (900, 8193, 17), (2500, 1000, 32), (2500, 16384, 20),
                                             (600, 16385, 3), (457, 65, 2), (950, 16385, 8), (1300, 32768, 16), (1300, 32769, 9), (1220, 20000, 8),
-                                               (470, 9001, 32), (480, 50257, 5), (470, 65000, 21)])
+                                               (470, 9001, 32), (480, 50257, 5), (470, 65000, 21), (290, 20000, 0), (150, 33000, 0)])
 def test_many_rows_of_few_words(rows, vocab, top, dtype):
     r = np.random.RandomState(rows + vocab)
     x = scores.logits(r, rows, vocab, dtype)
