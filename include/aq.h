@@ -259,7 +259,8 @@ aq_status aq_precompute_nvfp4(const aq_theta* th, void* q, int64_t ldq, void* sf
  * bits; sums are fp32, in an order that the sizes and the device fix; one rounding at the end. A block scale that is NaN makes its row NaN, an
  * infinity or NaN in x its token alone.
  * x [M, in] bf16, 16-byte aligned, ldx a multiple of 8. y[i] [M, out] bf16 with any row stride (aligned to its elements),
- * apart from every input. M == 0 is a no-op. M up to 65535 is served; the weights are read once for every 8 to 32 tokens (fewer where
+ * apart from every input. M == 0 is a no-op. M up to 65535 is served, and weights of 2^31 - 16 rows together (each rounded up to 16);
+ * the weights are read once for every 8 to 32 tokens (fewer where
  * in * M passes what a cluster's shared memory holds), so for many tokens the bf16 product on W_eff is the faster one.
  * aq_nvfp4_linear_multi: one to three weights (AQ_MAX_FAMILIES) of one `in` and one layout over one x, in one launch.
  * No workspace; these calls leave aq_last_launch_count() and aq_last_path() alone. Weights may be read before the previous

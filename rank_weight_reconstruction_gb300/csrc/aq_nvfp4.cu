@@ -712,6 +712,7 @@ extern "C" aq_status aq_nvfp4_linear_multi(const aq_nvfp4_weight* w, int32_t n, 
   if (in < 16 || in % 16 || in > AQ_NVFP4_MAX_IN)
     return serve_fail(in > AQ_NVFP4_MAX_IN ? AQ_ERR_UNSUPPORTED : AQ_ERR_SHAPE, "%s: in=%d must be a multiple of 16 up to %d", who, in, AQ_NVFP4_MAX_IN);
   bool wide = true;
+  int64_t row_tiles = 0;
   ByteRows outs[AQ_MAX_FAMILIES], ins[1 + 3 * AQ_MAX_FAMILIES];
   for (int i = 0; i < n; ++i) {
     const aq_nvfp4_weight& a = w[i];
@@ -724,7 +725,9 @@ extern "C" aq_status aq_nvfp4_linear_multi(const aq_nvfp4_weight* w, int32_t n, 
     if (a.ldq % 8 || !serve_aligned(a.q, 8) || !serve_aligned(a.sf, 16) || !serve_aligned(a.global_scale, 4))
       return serve_fail(AQ_ERR_ALIGNMENT, "%s: q and ldq must be 8-byte aligned, sf 16-byte, global_scale 4-byte", who);
     wide = wide && a.ldq % 16 == 0 && serve_aligned(a.q, 16);
+    row_tiles += (a.out + 15ll) / 16;
   }
+  if (row_tiles > 0x7fffffffLL / 16) return serve_fail(AQ_ERR_SHAPE, "%s: the weights have too many rows for one call", who);   // rows of a tile count in 32 bits
   if (M == 0) return AQ_OK;
   if (!x) return serve_fail(AQ_ERR_INVALID_ARG, "%s: x must be non-NULL", who);
   if (!serve_aligned(x, 16) || (M > 1 && ldx % 8)) return serve_fail(AQ_ERR_ALIGNMENT, "%s: x must be 16-byte aligned and ldx a multiple of 8", who);
@@ -751,9 +754,6 @@ extern "C" aq_status aq_nvfp4_linear_multi(const aq_nvfp4_weight* w, int32_t n, 
   ServeDev dev;
   aq_status st = serve_device(&dev);
   if (st != AQ_OK) return st;
-  int64_t row_tiles = 0;
-  for (int i = 0; i < n; ++i) row_tiles += (w[i].out + 15) / 16;
-  if (row_tiles > 0x7fffffffLL / 16) return serve_fail(AQ_ERR_SHAPE, "%s: the weights have too many rows for one call", who);
   int fit[4];
   cudaError_t e = clusters_at_once(dev, fit);
   if (e != cudaSuccess) return serve_launched(e, who);
