@@ -103,6 +103,12 @@ bool contiguous(const Tensor& x) {
   return true;
 }
 
+// A dimension as the ABI takes it; more than 32 bits hold is an error (of the calls' own handling), not fewer of them.
+int32_t dim32(int64_t v, const char* name) {
+  TORCH_CHECK_VALUE(v <= INT32_MAX, name, ": ", v, " are more than 32 bits hold");
+  return static_cast<int32_t>(v);
+}
+
 // A contiguous 1-D tensor of n elements (n < 0: any number).
 bool read_flat(Device& dev, PyObject* obj, const char* name, at::ScalarType dtype, int64_t n, Tensor* x) {
   if (!read(dev, obj, name, dtype, dtype, 1, x)) return false;
@@ -135,6 +141,7 @@ bool read_heads(Device& dev, PyObject* obj, const char* name, int64_t tokens, in
                  static_cast<long long>(x->shape[0]), static_cast<long long>(x->shape[1]), static_cast<long long>(x->shape[2]));
     return false;
   }
+  dim32(x->shape[1], name), dim32(x->shape[2], name);
   return head_strides(name, x);
 }
 
@@ -220,8 +227,6 @@ struct Norm {
   }
 };
 
-int32_t small(int64_t v) { return v > INT32_MAX ? INT32_MAX : static_cast<int32_t>(v); }
-
 struct Cache {
   PyObject* part[4] = {};
   aq_kv_cache c = {};
@@ -255,10 +260,10 @@ struct Cache {
     c.v = t[1].ptr;
     c.k_scale = static_cast<float*>(t[2].ptr);
     c.v_scale = static_cast<float*>(t[3].ptr);
-    c.pages = small(t[0].shape[0]);
-    c.kv_heads = small(t[0].shape[1]);
-    c.page_size = small(t[0].shape[2]);
-    c.head_dim = small(t[0].shape[3]);
+    c.pages = dim32(t[0].shape[0], "KvCache pages");
+    c.kv_heads = dim32(t[0].shape[1], "KvCache kv_heads");
+    c.page_size = dim32(t[0].shape[2], "KvCache page_size");
+    c.head_dim = dim32(t[0].shape[3], "KvCache head_dim");
     c.type = scaled ? AQ_KV_E4M3 : AQ_KV_BF16;
     return true;
   }
@@ -393,7 +398,7 @@ PyObject* py_rope(PyObject*, PyObject* const* a, Py_ssize_t n) {
     take(made, &y);
     if (!head_strides("y", &y)) return nullptr;
   }
-  if (!on_gpu(dev) || !ok(f_rope(&r.spec, static_cast<const int32_t*>(pos.ptr), x.shape[0], small(x.shape[1]), small(x.shape[2]), x.ptr, x.stride[0], x.stride[1],
+  if (!on_gpu(dev) || !ok(f_rope(&r.spec, static_cast<const int32_t*>(pos.ptr), x.shape[0], dim32(x.shape[1], "heads"), dim32(x.shape[2], "head_dim"), x.ptr, x.stride[0], x.stride[1],
                  y.ptr, y.stride[0], y.stride[1], inverse, st.handle)))
     return nullptr;
   return made.defined() ? st.hand_out(std::move(made)) : given(a[3]);
@@ -425,7 +430,7 @@ PyObject* py_kv_write(PyObject*, PyObject* const* a, Py_ssize_t n) {
     if (!head_strides("q_out", &o)) return nullptr;
   }
   if (!on_gpu(dev) || !ok(f_kv_write_norm(&c.c, static_cast<const int64_t*>(slots.ptr), T, k.ptr, k.stride[0], k.stride[1], v.ptr, v.stride[0], v.stride[1],
-                     turned ? &r.spec : nullptr, static_cast<const int32_t*>(pos.ptr), q.ptr, small(q.shape[1]), q.stride[0], q.stride[1], o.ptr,
+                     turned ? &r.spec : nullptr, static_cast<const int32_t*>(pos.ptr), q.ptr, dim32(q.shape[1], "q heads"), q.stride[0], q.stride[1], o.ptr,
                      o.stride[0], o.stride[1], qn.c(), kn.c(), st.handle)))
     return nullptr;
   return made.defined() ? st.hand_out(std::move(made)) : given(a[7]);
@@ -509,12 +514,12 @@ PyObject* py_attention(PyObject*, PyObject* const* a, Py_ssize_t n) {
     }
   }
   if ((a[13] != Py_None && !read_flat(dev, a[13], "workspace", kU8, -1, &ws)) || !st.read_from(a[14], q)) return nullptr;
-  d.batch = small(table.shape[0]);
+  d.batch = dim32(table.shape[0], "batch");
   d.total_q = total;
   d.cu_q = static_cast<const int32_t*>(cu.ptr);
   d.ctx = static_cast<const int32_t*>(ctx.ptr);
   d.page_table = static_cast<const int32_t*>(table.ptr);
-  d.pages_per_seq = small(table.shape[1]);
+  d.pages_per_seq = dim32(table.shape[1], "pages of a sequence");
   d.ld_table = table.stride[0];
   d.mask = static_cast<const uint64_t*>(mask.ptr);
   d.ld_mask = mask.stride[0];
@@ -531,7 +536,7 @@ PyObject* py_attention(PyObject*, PyObject* const* a, Py_ssize_t n) {
     take(made_lse, &lse);
   }
   if (a[13] == Py_None) {
-    const size_t need = f_attention_bytes(&c.c, &d, small(heads));
+    const size_t need = f_attention_bytes(&c.c, &d, dim32(heads, "q heads"));
     if (need == static_cast<size_t>(-1)) {
       ok(AQ_ERR_INVALID_ARG);
       return nullptr;
@@ -541,7 +546,7 @@ PyObject* py_attention(PyObject*, PyObject* const* a, Py_ssize_t n) {
       take(made_ws, &ws);
     }
   }
-  if (!on_gpu(dev) || !ok(f_attention(&c.c, &d, q.ptr, small(heads), q.stride[0], q.stride[1], static_cast<float>(scale), out.ptr, out.stride[0], out.stride[1],
+  if (!on_gpu(dev) || !ok(f_attention(&c.c, &d, q.ptr, dim32(heads, "q heads"), q.stride[0], q.stride[1], static_cast<float>(scale), out.ptr, out.stride[0], out.stride[1],
                       static_cast<float*>(lse.ptr), ws.ptr, static_cast<size_t>(ws.shape[0]), st.handle)))
     return nullptr;
   PyObject* o = made_out.defined() ? st.hand_out(std::move(made_out)) : given(a[10]);
@@ -586,7 +591,7 @@ PyObject* py_verify(PyObject*, PyObject* const* a, Py_ssize_t n) {
   take(made[0], &count);
   take(made[1], &path);
   take(made[2], &token);
-  if (!on_gpu(dev) || !ok(f_verify(small(batch), small(vocab), static_cast<const int32_t*>(cu.ptr), static_cast<const int32_t*>(tokens.ptr),
+  if (!on_gpu(dev) || !ok(f_verify(dim32(batch, "batch"), dim32(vocab, "vocab"), static_cast<const int32_t*>(cu.ptr), static_cast<const int32_t*>(tokens.ptr),
                    static_cast<const int32_t*>(parent.ptr), nodes, most, p.ptr, p.stride[0], q.ptr, q.stride[0], p.shape[0],
                    dtype == kF32 ? AQ_PROB_F32 : AQ_PROB_BF16, static_cast<const float*>(u.ptr), static_cast<const float*>(noise.ptr), noise.stride[0],
                    static_cast<int32_t*>(count.ptr), static_cast<int32_t*>(path.ptr), cap, cap, static_cast<int32_t*>(token.ptr), st.handle)))
@@ -595,7 +600,7 @@ PyObject* py_verify(PyObject*, PyObject* const* a, Py_ssize_t n) {
   END_HANDLE_TH_ERRORS
 }
 
-aq_heads heads_of(const Tensor& x) { return {x.ptr, x.stride[0], x.stride[1], small(x.shape[1])}; }
+aq_heads heads_of(const Tensor& x) { return {x.ptr, x.stride[0], x.stride[1], dim32(x.shape[1], "heads")}; }
 
 // qk_norm_rope(q, k, q_norm, k_norm, rope, pos, q_out, k_out, stream) -> (q_out, k_out)
 PyObject* py_qk_norm_rope(PyObject*, PyObject* const* a, Py_ssize_t n) {
@@ -625,7 +630,7 @@ PyObject* py_qk_norm_rope(PyObject*, PyObject* const* a, Py_ssize_t n) {
       if (!head_strides(name[i], &y[i])) return nullptr;
     }
   const aq_heads q = heads_of(x[0]), k = heads_of(x[1]), qo = heads_of(y[0]), ko = heads_of(y[1]);
-  if (!on_gpu(dev) || !ok(f_norm(norm[0].c(), norm[1].c(), turned ? &r.spec : nullptr, static_cast<const int32_t*>(pos.ptr), T, small(D), &q, &qo,
+  if (!on_gpu(dev) || !ok(f_norm(norm[0].c(), norm[1].c(), turned ? &r.spec : nullptr, static_cast<const int32_t*>(pos.ptr), T, dim32(D, "head_dim"), &q, &qo,
                                  sets == 2 ? &k : nullptr, sets == 2 ? &ko : nullptr, st.handle)))
     return nullptr;
   PyObject* out[2];
@@ -674,7 +679,7 @@ PyObject* py_qk_norm_rope_backward(PyObject*, PyObject* const* a, Py_ssize_t n) 
     }
   }
   if (a[10] == Py_None && (dw[0] || dw[1])) {
-    const size_t need = f_norm_bytes(T, small(D), small(x[0].shape[1]), sets == 2 ? small(x[1].shape[1]) : 0);
+    const size_t need = f_norm_bytes(T, dim32(D, "head_dim"), dim32(x[0].shape[1], "q heads"), sets == 2 ? dim32(x[1].shape[1], "k heads") : 0);
     if (need == static_cast<size_t>(-1)) {
       ok(AQ_ERR_INVALID_ARG);
       return nullptr;
@@ -689,7 +694,7 @@ PyObject* py_qk_norm_rope_backward(PyObject*, PyObject* const* a, Py_ssize_t n) 
     h[i][2] = heads_of(dx[i]);
   }
   const bool two = sets == 2;
-  if (!on_gpu(dev) || !ok(f_norm_backward(norm[0].c(), norm[1].c(), turned ? &r.spec : nullptr, static_cast<const int32_t*>(pos.ptr), T, small(D), &h[0][0],
+  if (!on_gpu(dev) || !ok(f_norm_backward(norm[0].c(), norm[1].c(), turned ? &r.spec : nullptr, static_cast<const int32_t*>(pos.ptr), T, dim32(D, "head_dim"), &h[0][0],
                                           &h[0][1], &h[0][2], dw[0], two ? &h[1][0] : nullptr, two ? &h[1][1] : nullptr, two ? &h[1][2] : nullptr, dw[1], ws.ptr,
                                           static_cast<size_t>(ws.shape[0]), st.handle)))
     return nullptr;
@@ -726,8 +731,8 @@ struct Weight4 {
     }
     w.q = t.ptr;
     w.ldq = t.stride[0];
-    w.out = small(t.shape[0]);
-    w.in = small(2 * t.shape[1]);
+    w.out = dim32(t.shape[0], "Nvfp4Weight.q rows");
+    w.in = dim32(2 * t.shape[1], "Nvfp4Weight.q columns");
     w.global_scale = static_cast<const float*>(one.ptr);
     const int64_t cols = t.shape[1] / 8;
     const int64_t need = w.sf_layout == AQ_SF_128X4 ? (t.shape[0] + 127) / 128 * 128 * ((cols + 3) / 4 * 4) : t.shape[0] * cols;
@@ -829,7 +834,7 @@ PyObject* py_scores(PyObject*, PyObject* const* a, Py_ssize_t n) {
     first += i < 3 ? rows : rows * top;
   }
   auto f32 = [&](int i) { return made[i].defined() ? static_cast<float*>(made[i].data_ptr()) : nullptr; };
-  if (!ok(f_scores(x.ptr, x.stride[0], rows, small(x.shape[1]), x.t->scalar_type() == kF32 ? AQ_PROB_F32 : AQ_PROB_BF16, static_cast<const int32_t*>(tokens.ptr), scale,
+  if (!ok(f_scores(x.ptr, x.stride[0], rows, dim32(x.shape[1], "vocab"), x.t->scalar_type() == kF32 ? AQ_PROB_F32 : AQ_PROB_BF16, static_cast<const int32_t*>(tokens.ptr), scale,
                    f32(0), f32(1), f32(2), top, f32(3), top ? static_cast<int32_t*>(made[4].data_ptr()) : nullptr, st.handle)))
     return nullptr;
   PyObject* out[5];
@@ -867,7 +872,7 @@ PyObject* py_scores_backward(PyObject*, PyObject* const* a, Py_ssize_t n) {
   }
   auto f32 = [&](int i) { return static_cast<const float*>(side[i].ptr); };
   // tokens matter to the gradient of logprob alone
-  if (!ok(f_scores_backward(x.ptr, x.stride[0], rows, small(x.shape[1]), dtype == kF32 ? AQ_PROB_F32 : AQ_PROB_BF16,
+  if (!ok(f_scores_backward(x.ptr, x.stride[0], rows, dim32(x.shape[1], "vocab"), dtype == kF32 ? AQ_PROB_F32 : AQ_PROB_BF16,
                             side[2].ptr ? static_cast<const int32_t*>(tokens.ptr) : nullptr, scale, f32(0), f32(1), f32(2), f32(3), f32(4), out.ptr, out.stride[0], st.handle)))
     return nullptr;
   return made.defined() ? st.hand_out(std::move(made)) : given(a[8]);
