@@ -453,7 +453,8 @@ aq_status aq_rope(const aq_rope_spec* rope, const int32_t* pos, int64_t T, int32
                   const void* x, int64_t x_tok, int64_t x_head, void* y, int64_t y_tok, int64_t y_head,
                   int32_t inverse, void* stream);
 
-/* T tokens' heads, [T, heads, head_dim] bf16 with a stride from token to token and one from head to head. */
+/* T tokens' heads, [T, heads, head_dim] bf16 with a stride from token to token and one from head to head. A token has up to 2^30
+ * heads in all of a call's inputs together (rotation and cache writes too). */
 typedef struct aq_heads {
   void* data;
   int64_t tok, head;

@@ -654,6 +654,7 @@ extern "C" aq_status aq_qk_norm_rope(const aq_head_norm* q_norm, const aq_head_n
   for (int i = 0; i < sets; ++i)
     if (in[i]->heads < 1 || in[i]->heads != out[i]->heads)
       return serve_fail(AQ_ERR_SHAPE, "%s: heads=%d and %d must be >= 1 and equal", who, in[i]->heads, out[i]->heads);
+  if ((st = check_head_count(static_cast<int64_t>(q->heads) + (k ? k->heads : 0), who)) != AQ_OK) return st;
   if (T == 0) return AQ_OK;
   if (rope && !pos) return serve_fail(AQ_ERR_INVALID_ARG, "%s: rope needs pos", who);
   const char* const names[2][2] = {{"q", "q_out"}, {"k", "k_out"}};
@@ -716,6 +717,7 @@ extern "C" aq_status aq_qk_norm_rope_backward(const aq_head_norm* q_norm, const 
       if (set[i][j]->heads < 1 || set[i][j]->heads != set[i][0]->heads)
         return serve_fail(AQ_ERR_SHAPE, "%s: heads of %s, %s and %s must be >= 1 and equal", who, names[i][0], names[i][1], names[i][2]);
   }
+  if ((st = check_head_count(static_cast<int64_t>(q->heads) + (k ? k->heads : 0), who)) != AQ_OK) return st;
   const cudaStream_t cs = static_cast<cudaStream_t>(stream);
   if (T == 0) {
     for (int i = 0; i < sets; ++i)

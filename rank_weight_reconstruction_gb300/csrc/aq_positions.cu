@@ -407,7 +407,7 @@ extern "C" aq_status aq_rope(const aq_rope_spec* rope, const int32_t* pos, int64
   if (head_dim < 16 || head_dim % 16 || head_dim > kServeMaxHeadDim)
     return serve_fail(AQ_ERR_SHAPE, "%s: head_dim=%d must be a multiple of 16 up to %d", who, head_dim, kServeMaxHeadDim);
   aq_status st = check_rope_spec(rope, head_dim, who);
-  if (st != AQ_OK) return st;
+  if (st != AQ_OK || (st = check_head_count(heads, who)) != AQ_OK) return st;
   if (T == 0) return AQ_OK;
   if (!pos) return serve_fail(AQ_ERR_INVALID_ARG, "%s: pos must be non-NULL", who);
   if ((st = check_heads(x, x_tok, x_head, heads, head_dim, "x", who)) != AQ_OK) return st;
@@ -461,6 +461,7 @@ extern "C" aq_status aq_kv_write_norm(const aq_kv_cache* cache, const int64_t* s
   if (q_norm && !q) return serve_fail(AQ_ERR_INVALID_ARG, "%s: q_norm needs q", who);
   if ((st = check_head_norm(q_norm, "q_norm", who)) != AQ_OK || (st = check_head_norm(k_norm, "k_norm", who)) != AQ_OK) return st;
   if (q && q_heads < 1) return serve_fail(AQ_ERR_SHAPE, "%s: q_heads=%d must be >= 1", who, q_heads);
+  if ((st = check_head_count(2ll * cache->kv_heads + (q ? q_heads : 0), who)) != AQ_OK) return st;
   if (T == 0) return AQ_OK;
   if (!slots) return serve_fail(AQ_ERR_INVALID_ARG, "%s: slots must be non-NULL", who);
   if (rope && !pos) return serve_fail(AQ_ERR_INVALID_ARG, "%s: rope needs pos", who);

@@ -127,6 +127,11 @@ inline int share_token(int64_t T, int heads, int gw, int64_t fill) {
   return s;
 }
 
+// Heads of all of a call's tensors together: the kernels walk them as one list, a block's groups at a time.
+inline aq_status check_head_count(int64_t heads, const char* who) {
+  if (heads > (1 << 30)) return serve_fail(AQ_ERR_SHAPE, "%s: %lld heads of a token are more than 2^30", who, (long long)heads);
+  return AQ_OK;
+}
 // x [T, heads, D] with the given strides: shape, alignment.
 inline aq_status check_heads(const void* x, int64_t tok, int64_t head, int32_t heads, int32_t D, const char* name,
                       const char* who) {

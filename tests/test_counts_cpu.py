@@ -50,3 +50,23 @@ def test_dimensions_past_32_bits_are_refused(lib):
     ):
         with pytest.raises(ValueError, match="2147483648 are more than 32 bits hold"):
             call()
+
+
+@pytest.mark.parametrize("hq,hk", [((1 << 30) + 1, 0), (MOST, 0), (MOST, 1), (1 << 30, 1 << 30), (1, MOST)])
+def test_heads_past_what_a_list_holds_are_refused(lib, hq, hk):
+    """The heads of a token are walked as one list, counted in 32 bits: q's and k's, and in the cache's write the values' too."""
+    rope, norm = b.c_rope(FAR, 16, 0, 1.0), b.c_head_norm(2 * FAR, 1e-6, 0.0)
+    heads = lambda i, n: ctypes.byref(b.c_heads(i * FAR, 16 * n, 16, n)) if n else None  # noqa: E731
+    p = ctypes.byref
+    calls = {
+        "aq_qk_norm_rope": lambda: lib.aq_qk_norm_rope(p(norm), p(norm) if hk else None, p(rope), 3 * FAR, 1, 16, heads(4, hq), heads(5, hq), heads(6, hk), heads(7, hk), None),
+        "aq_qk_norm_rope_backward": lambda: lib.aq_qk_norm_rope_backward(
+            p(norm), p(norm) if hk else None, p(rope), 3 * FAR, 1, 16, heads(4, hq), heads(5, hq), heads(6, hq), None, heads(7, hk), heads(8, hk), heads(9, hk), None, None, 0, None),
+    }
+    if not hk:
+        calls["aq_rope"] = lambda: lib.aq_rope(p(rope), 3 * FAR, 1, hq, 16, 4 * FAR, 16, 16, 5 * FAR, 16, 16, 0, None)
+    cache = b.c_kv_cache(k=10 * FAR, v=12 * FAR, k_scale=0, v_scale=0, pages=1, page_size=16, kv_heads=hk or 1, head_dim=16, type=b.AQ_KV_BF16)
+    calls["aq_kv_write"] = lambda: lib.aq_kv_write(p(cache), 2 * FAR, 1, 14 * FAR, 16, 16, 16 * FAR, 16, 16, p(rope), 3 * FAR, 4 * FAR, hq, 16, 16, 5 * FAR, 16, 16, None)
+    for who, call in calls.items():
+        st, said = call(), b.aq_last_error()
+        assert st == b.AQ_ERR_SHAPE and said.startswith(who + ":") and "more than 2^30" in said, (st, said)
