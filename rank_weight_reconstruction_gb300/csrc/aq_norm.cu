@@ -89,7 +89,7 @@ __device__ __forceinline__ float group_sum(float s, uint32_t group) {
 }
 
 // 1 / sqrt(mean(x^2) + eps) of a head held by a group of GW lanes, 16 elements a lane (zeros past the head). Squares of numbers
-// past 2^60 could leave fp32: such a head is measured at 2^-70 of its size, where eps is nothing.
+// past 2^60 could leave fp32: such a head is measured at 2^-70 of its size, and eps with it.
 template <int GW>
 __device__ __forceinline__ float head_rstd(const float (&a)[8], const float (&b)[8], uint32_t group, float inv_dim, float eps) {
   float s0 = 0.0f, s1 = 0.0f;
@@ -104,7 +104,7 @@ __device__ __forceinline__ float head_rstd(const float (&a)[8], const float (&b)
     s0 = fmaf(x, x, s0);
     s0 = fmaf(y, y, s0);
   }
-  return rsqrtf(group_sum<GW>(s0, group) * inv_dim) * 0x1p-70f;
+  return rsqrtf(fmaf(group_sum<GW>(s0, group), inv_dim, eps * 0x1p-140f)) * 0x1p-70f;
 }
 
 // As share_token, but at least a warp's groups, heads or not: those without one work out their part of the angles too.
