@@ -70,3 +70,16 @@ def test_heads_past_what_a_list_holds_are_refused(lib, hq, hk):
     for who, call in calls.items():
         st, said = call(), b.aq_last_error()
         assert st == b.AQ_ERR_SHAPE and said.startswith(who + ":") and "more than 2^30" in said, (st, said)
+
+
+def test_the_single_weight_entry_refuses(lib):
+    """aq_nvfp4_linear of the C ABI checks as the call for several weights does."""
+    def call(w, x=20 * FAR, M=3, ldx=16, y=21 * FAR, ldy=40):
+        return lib.aq_nvfp4_linear(w, x, M, ldx, y, ldy, None)
+
+    weight = lambda out=40, inp=16, g=3 * FAR: ctypes.byref(b.c_nvfp4_weight(FAR, 8, 2 * FAR, g, b.AQ_SF_LINEAR, out, inp))  # noqa: E731
+    for st, want in ((call(None), b.AQ_ERR_INVALID_ARG), (call(weight(g=0)), b.AQ_ERR_INVALID_ARG), (call(weight(out=0)), b.AQ_ERR_SHAPE),
+                     (call(weight(inp=24)), b.AQ_ERR_SHAPE), (call(weight(), ldx=8), b.AQ_ERR_SHAPE), (call(weight(), ldx=18), b.AQ_ERR_ALIGNMENT),
+                     (call(weight(), x=0), b.AQ_ERR_INVALID_ARG), (call(weight(), y=0), b.AQ_ERR_INVALID_ARG), (call(weight(), ldy=39), b.AQ_ERR_SHAPE),
+                     (call(weight(), y=20 * FAR + 64), b.AQ_ERR_OVERLAP), (call(weight(out=MOST), ldy=MOST, M=1), b.AQ_ERR_SHAPE), (call(weight(), M=0), b.AQ_OK)):
+        assert st == want, (st, want, b.aq_last_error())
