@@ -618,9 +618,10 @@ aq_status aq_token_logprobs(const void* logits, int64_t ld, int64_t rows, int32_
 /* Gradient of the above with respect to the logits, from what it returned and the gradients of logprob (with its tokens), entropy
  * and lse, fp32 [rows] each, NULL where there is none:
  *   dlogits = scale * ( dlogprob ([v = token] - p) - dentropy p (log p + entropy) + dlse p ),  p = e^(z - lse), at most 1
- * in the logits' type, rounded once. lse is fp32: p is off by 2^-24 |lse| of itself besides. A token outside the vocabulary has no
+ * in the logits' type, rounded once. lse is fp32: p is off by 2^-24 |lse| of itself besides; below 2^-126 it is 0. A token outside the vocabulary has no
  * gradient of its logprob; a row with lse -inf gives zeros.
- * dlogits may be logits (same pointer and stride); otherwise it lies apart from every input. */
+ * dlogits may be logits (same pointer and stride); otherwise it lies apart from every input. Rows of both that start at the same place of
+ * 16 bytes move in such pieces, others word by word (two to four times the time). */
 aq_status aq_token_logprobs_backward(const void* logits, int64_t ld, int64_t rows, int32_t vocab, int32_t type, const int32_t* tokens,
                                      float scale, const float* lse, const float* entropy, const float* dlogprob, const float* dentropy,
                                      const float* dlse, void* dlogits, int64_t ld_out, void* stream);

@@ -777,12 +777,13 @@ class Nvfp4Weight:
 
 
 def aq_nvfp4_linear(weight: Nvfp4Weight, x, y=None, stream=None):
-    """y [M, out] = x [M, in] times an NVFP4 weight, both bf16: decode's product on the weights of aq_precompute_nvfp4."""
+    """y [M, out] = x [M, in] times an NVFP4 weight, both bf16: decode's product on the weights of aq_precompute_nvfp4. Records no
+    history."""
     return _serve().nvfp4_linear((weight,), x, None if y is None else (y,), _raw_stream(stream))[0]
 
 
 def aq_nvfp4_linear_multi(weights, x, ys=None, stream=None):
-    """One to three NVFP4 weights (of one layout) over one x in one launch; returns the outputs."""
+    """One to three NVFP4 weights (of one layout) over one x in one launch; returns the outputs. Records no history."""
     return _serve().nvfp4_linear(weights, x, ys, _raw_stream(stream))
 
 
@@ -799,12 +800,14 @@ class TokenScores(NamedTuple):
 def aq_token_logprobs(logits, tokens=None, scale: float = 1.0, top: int = 0, stream=None) -> TokenScores:
     """Scores from logits [rows, vocab] (fp32 or bf16) times ``scale``: log probabilities of ``tokens`` (int32 [rows]; 0 where a
     token lies outside the vocabulary), the log of the normaliser, the entropy, and the ``top`` (up to 32) most likely
-    words with their log probabilities."""
+    words with their log probabilities. Records no history: aq_token_logprobs_backward is the gradient."""
     return TokenScores(*_serve().scores(logits, tokens, scale, top, _raw_stream(stream)))
 
 
 def aq_token_logprobs_backward(logits, tokens, lse, entropy=None, dlogprob=None, dentropy=None, dlse=None, scale: float = 1.0,
                                dlogits=None, stream=None):
     """Gradient with respect to the logits, in their type, from what aq_token_logprobs returned (lse, and entropy where dentropy
-    is given) and the gradients of logprob, entropy and lse (fp32 [rows], None for none). dlogits may be logits."""
+    is given) and the gradients of logprob, entropy and lse (fp32 [rows], None for none). dlogits may be logits; where the logits
+    are columns of a wider buffer, dlogits with their row stride is written two to four times as fast as the contiguous one
+    that is made otherwise."""
     return _serve().scores_backward(logits, tokens, lse, entropy, dlogprob, dentropy, dlse, scale, dlogits, _raw_stream(stream))

@@ -321,7 +321,7 @@ cudaError_t launch_head_norm(const HeadNormParams& p, unsigned blocks, int gw, T
 // ---------------------------------------------------------------------------------
 // gradient
 // ---------------------------------------------------------------------------------
-// As above, us for the gradient at the top: 1 and 2 53, 2 and 2 44.9, 2 and 3 46.1, 2 and 4 46.8, 3 and 2 65, 4 and 2 83.
+// As above, us for the gradient at the top: 1 and 2 53.2, 2 and 2 44.7, 2 and 3 46.2, 3 and 2 63.6, 4 and 2 86.5.
 constexpr int kNormThreads = 256, kNormPerSm = 2, kNormDepth = 2;
 
 struct NormSet {

@@ -131,7 +131,7 @@ __device__ __forceinline__ const Nvfp4Seg& tile_seg(const Nvfp4Params& p, int ti
 }
 
 // NW warps a CTA; DEPTH: ring stages of a warp, one chunk each; MODE of the scales: 0 linear, rows on 8 bytes; 1 linear, anywhere;
-// 2 128x4.
+// 2 128x4. (Four tiles of tokens, two stages and mode 1 together pass 128 registers by four: 16 bytes a thread are spilled.)
 template <int NT, int DEPTH, int NW, int MODE>
 __global__ void __launch_bounds__(32 * NW, 16 / NW) aq_nvfp4_kernel(const __grid_constant__ Nvfp4Params p) {
   extern __shared__ __align__(1024) uint8_t smem[];
@@ -603,7 +603,8 @@ size_t nvfp4_smem(int NT, int M, int tok, int tiles, const Nvfp4Plan& c) {
 // Cluster size, warps a CTA, tiles a round and how the warps share them, by an estimate of the call's time in ns: the chunks that the
 // busiest warp takes, x into every CTA's shared memory, what a round and an exchange cost, and the tokens' launch rows after one another
 // (of CTAs of eight warps two run beside each other). Its figures are fitted to 39 products timed under every plan (M 1 to 32, K 80 to
-// 21504, rows 100 to 262144); what it picks is within 1 % of the fastest of them on average. CTAs of eight warps that leave half an SM
+// 21504, rows 100 to 262144); what it picks for these is within 1 % of the fastest on average, 14 % at worst (19451 + 181 + 25353 rows of
+// 1936, M=15). It ranks plans: its times themselves are up to a third too low. CTAs of eight warps that leave half an SM
 // free may begin under the tail of the kernel before. Some of them, us (S, runs or whole tiles, warps): 21504 rows of 5376, M=8: (2,
 // runs, 16) 16.4, (1, runs, 16) 17.3, (4, whole, 16) 18.6, (1, whole, 16) 21.9, (1, runs, 8) 25.6; 262144 rows of 1152, M=5: (1, runs,
 // 16) 33.7, (1, whole, 16) 34.2, (1, runs, 8) 42.6; 1536 rows of 1152, M=1: (1, runs, 8) 3.6, (1, runs, 16) 4.5, (2, runs, 8) 4.6; 5376

@@ -50,7 +50,8 @@ inline aq_status serve_launched(cudaError_t e, const char* what) {
 inline bool serve_aligned(const void* p, uintptr_t n) { return (reinterpret_cast<uintptr_t>(p) & (n - 1)) == 0; }
 
 // One launch whose prologue may overlap the tail of the previous kernel in the stream; every
-// kernel launched this way calls pdl_wait_prior_grid() before it touches memory.
+// kernel launched this way calls pdl_wait_prior_grid() before it touches memory, but for the codes and scales
+// of NVFP4 weights, which the products read ahead of it (what may write them: aq.h, at the top).
 template <typename P>
 cudaError_t launch_serve(void (*kernel)(P), const P& p, dim3 grid, int threads, size_t smem, cudaStream_t st,
                          int cluster = 1) {
